@@ -11,6 +11,7 @@
 
 #include "exattn.h"
 #include "kernels.cuh"
+#include "paged.cuh"
 #include "ptx.cuh"
 
 namespace exattn {
@@ -190,6 +191,19 @@ int check_strides(const exattn_strides& s, int B, int H, int N) {
 }
 
 }  // namespace
+
+int setup_device(int* dev, unsigned** err) { return device_setup(dev, err); }
+
+bool encode_map(CUtensorMap* m, int dtype, int rank, const void* base, const cuuint64_t* dims,
+                const cuuint64_t* strides, const cuuint32_t* box) {
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  const CUtensorMapDataType ty = dtype == kF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const CUresult r = g_encode(m, ty, static_cast<cuuint32_t>(rank), const_cast<void*>(base), dims, strides, box, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) note_failure("cuTensorMapEncodeTiled", static_cast<int>(r), true);
+  return r == CUDA_SUCCESS;
+}
 
 void note_failure(const char* call, int code, bool driver) {
   t_fail_call = call;
@@ -766,12 +780,14 @@ extern "C" const char* exattn_status_string(int status) {
     case EXATTN_ERR_NULL: return "a required pointer is NULL";
     case EXATTN_ERR_SHAPE: return "B, H or N out of range";
     case EXATTN_ERR_ALIGN: return "a pointer is misaligned (bf16 tensors and workspace need 16 bytes, lse 4)";
-    case EXATTN_ERR_UNSUPPORTED: return "head dimension d must be 64 or 128";
+    case EXATTN_ERR_UNSUPPORTED: return "unsupported type, head dimension (64 or 128), page size or rotary size";
     case EXATTN_ERR_ARCH: return "the current device is not sm_103 (GB300)";
     case EXATTN_ERR_WORKSPACE: return "workspace is NULL or smaller than attn_bwd_workspace_size()";
     case EXATTN_ERR_CUDA: return "a CUDA call or kernel launch failed";
     case EXATTN_ERR_TIMEOUT: return "a kernel's bounded internal wait gave up; outputs are invalid";
-    case EXATTN_ERR_VALUE: return "scale must be finite and positive";
+    case EXATTN_ERR_VALUE:
+      return "a value is out of range (scale and factor: finite and positive; window; page numbers, distinct and "
+             "inside the pool)";
     default: return "unknown exattn status";
   }
 }

@@ -1,0 +1,72 @@
+// paged.cuh -- launch interfaces of the operators around a paged key/value
+// cache (rotary.cu, pages.cu, paged.cu) and the set-up that paged_api.cu
+// shares with api.cu.
+#pragma once
+#include "kernels.cuh"
+
+namespace exattn {
+
+// api.cu: the current device's set-up (architecture check, watchdog word) and
+// the driver's tensor-map encoder.
+int setup_device(int* dev, unsigned** err);
+bool encode_map(CUtensorMap* m, int dtype, int rank, const void* base, const cuuint64_t* dims,
+                const cuuint64_t* strides, const cuuint32_t* box);
+
+// Pages of a cache: K and V are [num_pages, Hkv, page_size, d] views (Strides:
+// b = page, h = head, n = row), and row b of the table lists the pages of
+// sequence b in order.
+struct PageView {
+  const int* table;        // device [B, max_pages], row stride table_stride
+  long long table_stride;
+  int max_pages;
+  int num_pages;
+  int page_size;           // a power of two
+  int page_shift;          // log2(page_size)
+};
+
+// Which rows of a packed tensor are the new tokens of sequence b: rows
+// [cu_seqlens[b], cu_seqlens[b + 1]), or, without a table, `each` rows a
+// sequence.  seqlens[b] is the sequence's length with its new tokens.
+struct NewTokens {
+  const int* cu_seqlens;
+  const int* seqlens;
+  int B, total, each;
+};
+
+struct RotaryArgs {
+  const void* q;  // [B, Hq, N, d] (append: [total, Hq, d], n = token) or nullptr
+  Strides sq;
+  void* q_out;
+  Strides sqo;
+  const void* k;
+  Strides sk;
+  void* k_out;    // append: the K cache
+  Strides sko;
+  const void* v;  // append only
+  Strides sv;
+  void* v_out;    // append: the V cache
+  Strides svo;
+  int Hq, Hk;
+  int B, N, d, dtype;
+  const int* positions;    // [B, N], row stride pos_stride; append: unused
+  long long pos_stride;
+  const double* inv_freq;  // [rot / 2] radians a token, or nullptr (append: no rotation)
+  int rot, interleaved, inverse;
+  float factor;
+  bool append;
+  NewTokens nt;
+  PageView pv;
+};
+cudaError_t launch_rotary(const RotaryArgs& a, cudaStream_t stream);
+
+struct CopyArgs {
+  char* pool;
+  long long slab_stride, page_stride, page_bytes;  // bytes
+  int slabs;
+  const int* src;  // host
+  const int* dst;  // host
+  int n;
+};
+cudaError_t launch_page_copy(const CopyArgs& a, cudaStream_t stream);
+
+}  // namespace exattn

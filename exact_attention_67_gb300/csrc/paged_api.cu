@@ -1,0 +1,210 @@
+// paged_api.cu -- the C ABI of the operators around a paged key/value cache
+// (declared in include/exattn.h): argument validation and launches.  No device
+// memory is allocated and nothing synchronises.
+#include <cmath>
+#include <cstdint>
+#include <cstdlib>
+
+#include "exattn.h"
+#include "paged.cuh"
+
+using namespace exattn;
+
+namespace {
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+Strides to_strides(const exattn_strides& s) { return Strides{s.b_stride, s.h_stride, s.n_stride}; }
+
+// As for the attention calls: non-negative multiples of 8 elements below
+// 2^36, positive along every axis of extent > 1.
+int check_strides(const exattn_strides& s, long long B, long long H, long long N) {
+  const long long v[3] = {s.b_stride, s.h_stride, s.n_stride}, ext[3] = {B, H, N};
+  for (int i = 0; i < 3; ++i) {
+    if (v[i] < 0 || v[i] >= (1ll << 36) || (v[i] & 7) != 0) return EXATTN_ERR_ALIGN;
+    if (ext[i] > 1 && v[i] == 0) return EXATTN_ERR_SHAPE;
+  }
+  return EXATTN_OK;
+}
+
+bool known_dtype(int dtype) { return dtype == EXATTN_DTYPE_BF16 || dtype == EXATTN_DTYPE_F16; }
+
+// The turned part of a head: even, within it, with finite positive factor.
+int check_rotary(const double* inv_freq, int rot_dim, int d, float factor) {
+  if (rot_dim < 2 || rot_dim > d || (rot_dim & 1)) return EXATTN_ERR_UNSUPPORTED;
+  if (!aligned(inv_freq, 8)) return EXATTN_ERR_ALIGN;
+  if (!std::isfinite(factor) || !(factor > 0.f)) return EXATTN_ERR_VALUE;
+  return EXATTN_OK;
+}
+
+// Shared checks of a cache and its page table; fills the view.
+int check_pages(PageView* pv, const int* page_table, long long table_stride, int max_pages, int num_pages,
+                int page_size, int B, int Hkv, const exattn_strides& sk, const exattn_strides& sv) {
+  if (!aligned(page_table, 4)) return EXATTN_ERR_ALIGN;
+  if (num_pages < 1 || max_pages < 1 || Hkv < 1 || B < 1) return EXATTN_ERR_SHAPE;
+  if (table_stride < 0 || (B > 1 && table_stride < max_pages)) return EXATTN_ERR_SHAPE;
+  if (page_size < 8 || page_size > 1024 || (page_size & (page_size - 1))) return EXATTN_ERR_UNSUPPORTED;
+  if (static_cast<long long>(max_pages) * page_size >= (1ll << 31)) return EXATTN_ERR_SHAPE;
+  int rc;
+  if ((rc = check_strides(sk, num_pages, Hkv, page_size)) != EXATTN_OK ||
+      (rc = check_strides(sv, num_pages, Hkv, page_size)) != EXATTN_OK)
+    return rc;
+  pv->table = page_table;
+  pv->table_stride = table_stride;
+  pv->max_pages = max_pages;
+  pv->num_pages = num_pages;
+  pv->page_size = page_size;
+  pv->page_shift = 0;
+  while ((1 << pv->page_shift) < page_size) ++pv->page_shift;
+  return EXATTN_OK;
+}
+
+// The new tokens of B sequences in `total` packed rows.
+int check_tokens(NewTokens* nt, const int* cu_seqlens, const int* seqlens, int B, int total) {
+  if (B < 1 || total < 1) return EXATTN_ERR_SHAPE;
+  if (!aligned(seqlens, 4) || !aligned(cu_seqlens, 4)) return EXATTN_ERR_ALIGN;
+  if (!cu_seqlens && total % B != 0) return EXATTN_ERR_SHAPE;
+  *nt = NewTokens{cu_seqlens, seqlens, B, total, cu_seqlens ? 0 : total / B};
+  return EXATTN_OK;
+}
+
+}  // namespace
+
+extern "C" int attn_rotary(int dtype, const void* q, exattn_strides sq, void* q_out, exattn_strides sqo, int Hq,
+                           const void* k, exattn_strides sk, void* k_out, exattn_strides sko, int Hk,
+                           const int* positions, long long pos_stride, const double* inv_freq, int rot_dim,
+                           int interleaved, int inverse, float factor, int B, int N, int d, void* stream) {
+  if (!q || !q_out || !positions || !inv_freq || (Hk > 0 && (!k || !k_out))) return EXATTN_ERR_NULL;
+  if (!known_dtype(dtype) || (d != 64 && d != 128)) return EXATTN_ERR_UNSUPPORTED;
+  if (B < 1 || N < 1 || Hq < 1 || Hk < 0 || Hq > 65536 || Hk > 65536) return EXATTN_ERR_SHAPE;
+  if (static_cast<long long>(B) * N >= (1ll << 31) || pos_stride < 0) return EXATTN_ERR_SHAPE;
+  int rc = check_rotary(inv_freq, rot_dim, d, factor);
+  if (rc != EXATTN_OK) return rc;
+  if (!aligned(q, 16) || !aligned(q_out, 16) || !aligned(k, 16) || !aligned(k_out, 16) || !aligned(positions, 4))
+    return EXATTN_ERR_ALIGN;
+  if ((rc = check_strides(sq, B, Hq, N)) != EXATTN_OK || (rc = check_strides(sqo, B, Hq, N)) != EXATTN_OK) return rc;
+  if (Hk > 0 &&
+      ((rc = check_strides(sk, B, Hk, N)) != EXATTN_OK || (rc = check_strides(sko, B, Hk, N)) != EXATTN_OK))
+    return rc;
+  int dev = 0;
+  unsigned* err = nullptr;
+  if ((rc = setup_device(&dev, &err)) != EXATTN_OK) return rc;
+  RotaryArgs a{};
+  a.q = q;
+  a.sq = to_strides(sq);
+  a.q_out = q_out;
+  a.sqo = to_strides(sqo);
+  a.k = k;
+  a.sk = to_strides(sk);
+  a.k_out = k_out;
+  a.sko = to_strides(sko);
+  a.Hq = Hq;
+  a.Hk = Hk;
+  a.B = B;
+  a.N = N;
+  a.d = d;
+  a.dtype = dtype == EXATTN_DTYPE_F16 ? kF16 : kBF16;
+  a.positions = positions;
+  a.pos_stride = pos_stride;
+  a.inv_freq = inv_freq;
+  a.rot = rot_dim;
+  a.interleaved = interleaved ? 1 : 0;
+  a.inverse = inverse ? 1 : 0;
+  a.factor = factor;
+  return launch_rotary(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? EXATTN_OK : EXATTN_ERR_CUDA;
+}
+
+extern "C" int attn_cache_append(int dtype, const void* q, exattn_strides sq, void* q_out, exattn_strides sqo, int Hq,
+                                 const void* k, exattn_strides sk, const void* v, exattn_strides sv, void* k_cache,
+                                 exattn_strides skc, void* v_cache, exattn_strides svc, int Hkv, int num_pages,
+                                 int page_size, const int* page_table, long long table_stride, int max_pages,
+                                 const int* seqlens, const int* cu_seqlens, int B, int total, int d,
+                                 const double* inv_freq, int rot_dim, int interleaved, float factor, void* stream) {
+  if (!k || !v || !k_cache || !v_cache || !page_table || !seqlens) return EXATTN_ERR_NULL;
+  if (Hq > 0 && (!q || !q_out || !inv_freq)) return EXATTN_ERR_NULL;
+  if (!known_dtype(dtype) || (d != 64 && d != 128)) return EXATTN_ERR_UNSUPPORTED;
+  if (Hq < 0 || Hq > 65536 || Hkv < 1 || Hkv > 65536) return EXATTN_ERR_SHAPE;
+  RotaryArgs a{};
+  int rc = check_tokens(&a.nt, cu_seqlens, seqlens, B, total);
+  if (rc != EXATTN_OK) return rc;
+  if ((rc = check_pages(&a.pv, page_table, table_stride, max_pages, num_pages, page_size, B, Hkv, skc, svc)) !=
+      EXATTN_OK)
+    return rc;
+  if (inv_freq && (rc = check_rotary(inv_freq, rot_dim, d, factor)) != EXATTN_OK) return rc;
+  if (!aligned(q, 16) || !aligned(q_out, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(k_cache, 16) ||
+      !aligned(v_cache, 16))
+    return EXATTN_ERR_ALIGN;
+  if (Hq > 0 && ((rc = check_strides(sq, 1, Hq, total)) != EXATTN_OK ||
+                 (rc = check_strides(sqo, 1, Hq, total)) != EXATTN_OK))
+    return rc;
+  if ((rc = check_strides(sk, 1, Hkv, total)) != EXATTN_OK || (rc = check_strides(sv, 1, Hkv, total)) != EXATTN_OK)
+    return rc;
+  int dev = 0;
+  unsigned* err = nullptr;
+  if ((rc = setup_device(&dev, &err)) != EXATTN_OK) return rc;
+  a.q = q;
+  a.sq = to_strides(sq);
+  a.q_out = q_out;
+  a.sqo = to_strides(sqo);
+  a.k = k;
+  a.sk = to_strides(sk);
+  a.k_out = k_cache;
+  a.sko = to_strides(skc);
+  a.v = v;
+  a.sv = to_strides(sv);
+  a.v_out = v_cache;
+  a.svo = to_strides(svc);
+  a.Hq = Hq;
+  a.Hk = Hkv;
+  a.d = d;
+  a.dtype = dtype == EXATTN_DTYPE_F16 ? kF16 : kBF16;
+  a.inv_freq = inv_freq;
+  a.rot = rot_dim;
+  a.interleaved = interleaved ? 1 : 0;
+  a.factor = factor;
+  a.append = true;
+  return launch_rotary(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? EXATTN_OK : EXATTN_ERR_CUDA;
+}
+
+extern "C" int attn_cache_copy(void* pool, long long slab_stride, long long page_stride, long long page_bytes,
+                               int slabs, int num_pages, const int* src, const int* dst, int n, void* stream) {
+  if (n < 0) return EXATTN_ERR_SHAPE;
+  if (!pool || (n > 0 && (!src || !dst))) return EXATTN_ERR_NULL;
+  if (slabs < 1 || slabs > 65535 || num_pages < 1 || page_bytes < 16 || page_bytes > (1ll << 30))
+    return EXATTN_ERR_SHAPE;
+  if (!aligned(pool, 16) || ((slab_stride | page_stride | page_bytes) & 15)) return EXATTN_ERR_ALIGN;
+  // Pages of a slab, and slabs, must not overlap (either may be the outer one).
+  if ((num_pages > 1 && page_stride < page_bytes) || (slabs > 1 && slab_stride < page_bytes)) return EXATTN_ERR_SHAPE;
+  if (page_stride >= (1ll << 40) || slab_stride >= (1ll << 44)) return EXATTN_ERR_SHAPE;
+  if (num_pages > 1 && slabs > 1 && slab_stride < page_stride * (num_pages - 1) + page_bytes &&
+      page_stride < slab_stride * (slabs - 1) + page_bytes)
+    return EXATTN_ERR_SHAPE;
+  if (n == 0) return EXATTN_OK;
+  // One bit a page for the destinations, so that every pair is independent:
+  // none named twice, none read.
+  for (int i = 0; i < n; ++i)
+    if (src[i] < 0 || src[i] >= num_pages || dst[i] < 0 || dst[i] >= num_pages) return EXATTN_ERR_VALUE;
+  bool clash = false;
+  if (n <= 32) {
+    for (int i = 0; i < n; ++i)
+      for (int j = 0; j < n; ++j) clash |= dst[i] == src[j] || (i < j && dst[i] == dst[j]);
+  } else {
+    uint64_t* written = static_cast<uint64_t*>(std::calloc((static_cast<size_t>(num_pages) + 63) / 64, 8));
+    if (!written) return EXATTN_ERR_WORKSPACE;
+    for (int i = 0; i < n; ++i) {
+      uint64_t& w = written[dst[i] >> 6];
+      const uint64_t bit = 1ull << (dst[i] & 63);
+      clash |= (w & bit) != 0;
+      w |= bit;
+    }
+    for (int i = 0; i < n; ++i) clash |= (written[src[i] >> 6] >> (src[i] & 63)) & 1;
+    std::free(written);
+  }
+  if (clash) return EXATTN_ERR_VALUE;
+  int dev = 0;
+  unsigned* err = nullptr;
+  const int rc = setup_device(&dev, &err);
+  if (rc != EXATTN_OK) return rc;
+  const CopyArgs a{static_cast<char*>(pool), slab_stride, page_stride, page_bytes, slabs, src, dst, n};
+  return launch_page_copy(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? EXATTN_OK : EXATTN_ERR_CUDA;
+}

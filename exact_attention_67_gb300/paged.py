@@ -1,0 +1,254 @@
+"""Operators around a paged key/value cache: ctypes binding of the C ABI's
+rotary, cache and paged-attention calls (include/exattn.h; the same names,
+argument marshalling only), and the helpers on top of them.
+
+A cache is a pair of [num_pages, Hkv, page_size, d] views (d contiguous; a
+token-major [num_pages, page_size, Hkv, d] tensor passes as
+``x.transpose(1, 2)``), a page table int32 [B, max_pages] and lengths int32 [B]
+on the device.  New tokens are packed [total, H, d] tensors with offsets
+``cu_seqlens`` int32 [B + 1], or ``cu_seqlens=None`` when every sequence has
+total / B of them.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+
+import torch
+
+from ._lib import _DTYPES, _check, _device_of, _packed3, _ptr, _stream, _view4, Strides, load
+
+_NO_STRIDES = Strides(0, 0, 0)
+
+
+def _call(name: str, dev, stream, *args) -> None:
+    """One C call on ``dev``, which is made current if it is not, with the
+    stream last."""
+    if dev.index == torch.cuda.current_device():
+        _check(getattr(load(), name)(*args, _stream(stream, dev)))
+        return
+    with torch.cuda.device(dev):
+        _check(getattr(load(), name)(*args, _stream(stream, dev)))
+
+
+def _int32(t, name: str, shape=None):
+    if t.dtype != torch.int32:
+        raise TypeError(f"{name} must be int32, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {tuple(t.shape)}")
+    if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last axis must be contiguous")
+    return t
+
+
+def _frequencies(inv_freq):
+    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise ValueError("inv_freq must be a contiguous float64 tensor [rot_dim / 2] (rotary_frequencies)")
+    return 2 * inv_freq.numel()
+
+
+# ---------------------------------------------------------------- rotary positions
+def rotary_frequencies(rot_dim: int, base: float = 10000.0, *, linear: float = 1.0, yarn: float = 1.0,
+                       trained_length: int = 8192, slow_turns: float = 1.0, fast_turns: float = 32.0, device="cuda"):
+    """Frequencies float64 [rot_dim / 2] (radians a token) and the factor of cos
+    and sin, for ``rotary``: f_i = base^(-2 i / rot_dim), and for contexts
+    beyond the trained length
+      * ``linear`` = s > 1: positions divided by s (every f_i / s);
+      * ``yarn`` = s > 1: pairs that make fewer than ``slow_turns`` turns over
+        ``trained_length`` tokens are divided by s, those that make more than
+        ``fast_turns`` are kept, those between are blended linearly in their
+        turns; the factor is 0.1 ln s + 1.
+    A changed ``base`` is the remaining common scaling."""
+    if rot_dim < 2 or rot_dim % 2:
+        raise ValueError(f"rot_dim must be even and at least 2, got {rot_dim}")
+    if not (base > 0 and linear > 0 and yarn > 0) or (linear != 1.0 and yarn != 1.0):
+        raise ValueError("base, linear and yarn must be positive, and only one of linear and yarn given")
+    if not fast_turns > slow_turns:
+        raise ValueError("fast_turns must exceed slow_turns")
+    f = torch.tensor(float(base), dtype=torch.float64) ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64) / rot_dim)
+    factor = 1.0
+    if linear != 1.0:
+        f = f / linear
+    if yarn != 1.0:
+        turns = trained_length * f / (2 * math.pi)
+        keep = ((turns - slow_turns) / (fast_turns - slow_turns)).clamp(0, 1)
+        f = f / yarn * (1 - keep) + f * keep
+        factor = 0.1 * math.log(yarn) + 1.0 if yarn > 1.0 else 1.0
+    return f.to(device), factor
+
+
+def attn_rotary(q, q_out, k, k_out, positions, inv_freq, interleaved: bool = False, inverse: bool = False,
+                factor: float = 1.0, stream=None) -> None:
+    """C ``attn_rotary``: q, q_out [B, Hq, N, d] and k, k_out [B, Hk, N, d] views of
+    one 16-bit type (k, k_out may be None); positions int32 [N] or [B, N];
+    inv_freq float64 [rot_dim / 2].  An output may be its own input."""
+    (B, Hq, N, d), dt, sq = _view4(q, "q")
+    so, sk, sko, Hk = _view4(q_out, "q_out"), _NO_STRIDES, _NO_STRIDES, 0
+    if so[0] != (B, Hq, N, d) or so[1] != dt:
+        raise ValueError("q_out shape/dtype differs from q")
+    if (k is None) != (k_out is None):
+        raise ValueError("k and k_out go together")
+    if k is not None:
+        (Bk, Hk, Nk, dk), dtk, sk = _view4(k, "k")
+        vo = _view4(k_out, "k_out")
+        if (Bk, Nk, dk) != (B, N, d) or dtk != dt or vo[:2] != ((B, Hk, N, d), dt):
+            raise ValueError("k, k_out must be [B, Hk, N, d] like q, of one dtype")
+        sko = vo[2]
+    if positions.dim() == 1:
+        _int32(positions, "positions", (N,))
+        ps = 0
+    else:
+        _int32(positions, "positions", (B, N))
+        ps = positions.stride(0) if B > 1 else 0
+    rot = _frequencies(inv_freq)
+    dev = _device_of(q, q_out, k, k_out, positions, inv_freq)
+    _call("attn_rotary", dev, stream, dt, _ptr(q), sq, _ptr(q_out), so[2], Hq, _ptr(k), sk, _ptr(k_out), sko, Hk,
+          _ptr(positions), ps, _ptr(inv_freq), rot, int(bool(interleaved)), int(bool(inverse)), float(factor), B, N, d)
+
+
+def _rotary(q, k, positions, inv_freq, interleaved, inverse, factor, stream):
+    def four(x):  # packed [total, H, d] as one batch
+        return x.transpose(0, 1).unsqueeze(0) if x is not None and x.dim() == 3 else x
+
+    if k is not None and k.dim() != q.dim():
+        raise ValueError("q and k must both be [B, H, N, d], or both packed [total, H, d]")
+    qo, ko = torch.empty_like(q), None if k is None else torch.empty_like(k)
+    if q.numel():
+        if positions is None:
+            positions = torch.arange(q.shape[2] if q.dim() == 4 else q.shape[0], dtype=torch.int32, device=q.device)
+        attn_rotary(four(q), four(qo), four(k), four(ko), positions, inv_freq, interleaved, inverse, factor, stream)
+    return qo if k is None else (qo, ko)
+
+
+class _Rotary(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, positions, inv_freq, interleaved, factor):
+        ctx.save_for_backward(positions, inv_freq)
+        ctx.how = (interleaved, factor)
+        return _rotary(q, k, positions, inv_freq, interleaved, False, factor, None)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dq, dk=None):
+        positions, inv_freq = ctx.saved_tensors
+        # As for attention: gradients the library cannot read in place (expanded,
+        # oddly strided, misaligned) are made contiguous first.
+        dq, dk = (g if g is None or _readable(g) else g.contiguous() for g in (dq, dk))
+        got = _rotary(dq, dk, positions, inv_freq, ctx.how[0], True, ctx.how[1], None)
+        dq, dk = (got, None) if dk is None else got
+        return dq, dk, None, None, None, None
+
+
+def _readable(g) -> bool:
+    return g.stride(-1) == 1 and all(s and s % 8 == 0 for s in g.stride()[:-1]) and g.data_ptr() % 16 == 0
+
+
+def rotary(q, k=None, positions=None, inv_freq=None, interleaved: bool = False, factor: float = 1.0, stream=None):
+    """Q and K (or Q alone) with rotary positions applied, differentiable in
+    both: q [B, Hq, N, d] and k [B, Hk, N, d] bf16/f16 views (any layout with d
+    contiguous), or both packed [total, H, d].  ``positions``: int32 [N] or
+    [B, N] ([total] when packed), by default 0..N-1; ``inv_freq`` and ``factor``
+    from ``rotary_frequencies`` (its defaults if not given).  The first
+    2 * len(inv_freq) elements of a head are turned, the others copied."""
+    if inv_freq is None:
+        inv_freq, _ = rotary_frequencies(q.shape[-1], device=q.device)
+    if torch.is_grad_enabled() and (q.requires_grad or (k is not None and k.requires_grad)):
+        if stream is not None:
+            raise ValueError("rotary under autograd runs on the current stream: use torch.cuda.stream(...)")
+        return _Rotary.apply(q, k, positions, inv_freq, bool(interleaved), float(factor))
+    return _rotary(q, k, positions, inv_freq, interleaved, False, factor, stream)
+
+
+def rotary_backward(dq, dk=None, positions=None, inv_freq=None, interleaved: bool = False, factor: float = 1.0,
+                    stream=None):
+    """The gradient of ``rotary`` with the same arguments: from the gradients of
+    its outputs those of q and k."""
+    if inv_freq is None:
+        inv_freq, _ = rotary_frequencies(dq.shape[-1], device=dq.device)
+    return _rotary(dq, dk, positions, inv_freq, interleaved, True, factor, stream)
+
+
+# ---------------------------------------------------------------- the cache
+def _cache(k_cache, v_cache, dt, d):
+    (P, H, ps, dc), dtk, sk = _view4(k_cache, "k_cache")
+    (Pv, Hv, psv, dv), dtv, sv = _view4(v_cache, "v_cache")
+    if (P, H, ps, dc) != (Pv, Hv, psv, dv) or dtk != dt or dtv != dt or dc != d:
+        raise ValueError("k_cache and v_cache must be [num_pages, Hkv, page_size, d] of the tokens' type and d")
+    return P, H, ps, sk, sv
+
+
+def _tables(page_table, seqlens, cu_seqlens, total):
+    if page_table.dim() != 2:
+        raise ValueError(f"page_table must be [B, max_pages], got {tuple(page_table.shape)}")
+    B = _int32(page_table, "page_table").shape[0]
+    _int32(seqlens, "seqlens", (B,))
+    if cu_seqlens is not None:
+        _int32(cu_seqlens, "cu_seqlens", (B + 1,))
+    elif B == 0 or total % B:
+        raise ValueError(f"without cu_seqlens the {total} new tokens must divide evenly over {B} sequences")
+    return B
+
+
+def attn_cache_append(k, v, k_cache, v_cache, page_table, seqlens, cu_seqlens=None, q=None, q_out=None, inv_freq=None,
+                      interleaved: bool = False, factor: float = 1.0, stream=None) -> None:
+    """C ``attn_cache_append``: k, v packed [total, Hkv, d] into the pages of their
+    sequences; with ``inv_freq`` K is turned to its position, and q into q_out
+    ([total, Hq, d], which may be q) if given."""
+    (total, Hk, d), dt, sk = _packed3(k, "k")
+    (tv, Hv, dv), dtv, sv = _packed3(v, "v")
+    P, Hc, ps, skc, svc = _cache(k_cache, v_cache, dt, d)
+    if (tv, Hv, dv, dtv) != (total, Hk, d, dt) or Hc != Hk:
+        raise ValueError("k and v must be [total, Hkv, d] of one type, Hkv as in the cache")
+    B = _tables(page_table, seqlens, cu_seqlens, total)
+    Hq, sq, sqo, rot = 0, _NO_STRIDES, _NO_STRIDES, 0
+    if (q is None) != (q_out is None) or (q is not None and inv_freq is None):
+        raise ValueError("q, q_out and inv_freq go together")
+    if q is not None:
+        (tq, Hq, dq), dtq, sq = _packed3(q, "q")
+        qo = _packed3(q_out, "q_out")
+        if (tq, dq, dtq) != (total, d, dt) or qo[:2] != ((total, Hq, d), dt):
+            raise ValueError("q and q_out must be [total, Hq, d] of k's type")
+        sqo = qo[2]
+    if inv_freq is not None:
+        rot = _frequencies(inv_freq)
+    dev = _device_of(k, v, k_cache, v_cache, page_table, seqlens, cu_seqlens, q, q_out, inv_freq)
+    if total == 0:
+        return
+    _call("attn_cache_append", dev, stream, dt, _ptr(q), sq, _ptr(q_out), sqo, Hq, _ptr(k), sk, _ptr(v), sv, _ptr(k_cache),
+          skc, _ptr(v_cache), svc, Hk, P, ps, _ptr(page_table), page_table.stride(0) if B > 1 else page_table.shape[1],
+          page_table.shape[1], _ptr(seqlens), _ptr(cu_seqlens), B, total, d, _ptr(inv_freq), rot, int(bool(interleaved)),
+          float(factor))
+
+
+def _pages(x, name: str):
+    """Host int32 page numbers, contiguous."""
+    if not isinstance(x, torch.Tensor):
+        x = torch.tensor(list(x), dtype=torch.int32)
+    if x.is_cuda:
+        raise ValueError(f"{name}: page numbers are host data (page tables are kept on the host)")
+    if x.dim() != 1 or x.dtype != torch.int32:
+        raise ValueError(f"{name} must be 1-D int32 page numbers")
+    return x.contiguous()
+
+
+def attn_cache_copy(pool, src, dst, stream=None) -> None:
+    """C ``attn_cache_copy``: pool [slabs, num_pages, ...] (each page dense; slabs are
+    layers' K and V; a single cache passes as ``x.unsqueeze(0)``), src and dst
+    host page numbers (int32 tensors or sequences): page dst[i] of every slab
+    becomes a copy of page src[i]."""
+    if pool.dim() < 3 or not pool.is_cuda:
+        raise ValueError("pool must be a CUDA tensor [slabs, num_pages, ...]")
+    inner = sorted(((s, n) for s, n in zip(pool.stride()[2:], pool.shape[2:]) if n > 1))
+    each = 1
+    for s, n in inner:
+        if s != each:
+            raise ValueError("each page of the pool must be one dense block")
+        each *= n
+    src, dst = _pages(src, "src"), _pages(dst, "dst")
+    if src.numel() != dst.numel():
+        raise ValueError("src and dst must be of one length")
+    if src.numel() == 0:
+        return
+    size = pool.element_size()
+    _call("attn_cache_copy", pool.device, stream, _ptr(pool), pool.stride(0) * size, pool.stride(1) * size, each * size,
+          pool.shape[0], pool.shape[1], src.data_ptr(), dst.data_ptr(), src.numel())

@@ -51,12 +51,12 @@ typedef enum {
   EXATTN_ERR_NULL = 1,        /* a required pointer is NULL */
   EXATTN_ERR_SHAPE = 2,       /* B, H or N out of range */
   EXATTN_ERR_ALIGN = 3,       /* a pointer is not aligned as stated above */
-  EXATTN_ERR_UNSUPPORTED = 4, /* d not in {64, 128} */
+  EXATTN_ERR_UNSUPPORTED = 4, /* d not in {64, 128}; a type, page size or rotary size out of range */
   EXATTN_ERR_ARCH = 5,        /* current device is not sm_103 */
   EXATTN_ERR_WORKSPACE = 6,   /* workspace NULL or smaller than required */
   EXATTN_ERR_CUDA = 7,        /* a CUDA runtime/driver call or a launch failed */
   EXATTN_ERR_TIMEOUT = 8,     /* a kernel's bounded internal wait gave up */
-  EXATTN_ERR_VALUE = 9        /* scale not finite or not positive */
+  EXATTN_ERR_VALUE = 9        /* scale or factor not finite and positive; a window or page number out of range */
 } exattn_status;
 
 /*
@@ -344,6 +344,91 @@ int attn_fwd_bwd_host(int dtype, const void* q, const void* k, const void* v, co
                       void* dq, void* dk, void* dv, int B, int H, int N, int d, int causal, float scale,
                       void* workspace, size_t workspace_bytes, int groups, void* stream, void* copy_in_stream,
                       void* copy_out_stream, void* stream2);
+
+/*
+ * Rotary positions.  Each pair (x1, x2) of the first rot_dim elements of a
+ * head turns by the angle a = p f_i, position p and frequency f_i of pair i:
+ *     y1 = factor (x1 cos a - x2 sin a),  y2 = factor (x2 cos a + x1 sin a);
+ * the other elements are copied.  Pair i is elements (i, i + rot_dim / 2), or
+ * with `interleaved` (2 i, 2 i + 1).  `inverse` turns by -a: the gradient of
+ * the call with the same arguments (the map is factor times an orthogonal
+ * one).  The operands of attention that the flash_attn_func example of
+ * "提示词再优也救不了的性能黑洞…", 第一章, takes as given.
+ *   q, q_out : [B, Hq, N, d] views (exattn_strides) of one 16-bit type;
+ *     k, k_out : [B, Hk, N, d], or NULL with Hk = 0.  An output may be its
+ *     own input (same address and strides); otherwise no output may overlap
+ *     an input or the other output.
+ *   positions : device int32, position of row n of batch b at
+ *     positions[b * pos_stride + n] (pos_stride 0: the same for every batch);
+ *     any int32, negative ones included.
+ *   inv_freq  : device fp64 [rot_dim / 2], radians a token.  Angles are
+ *     reduced exactly in fixed point, so far positions lose nothing.
+ *   rot_dim   : even, 2..d; factor finite and positive.
+ * Products in fp32, rounded once to the output's type.  B N < 2^31, 1 <= Hq,
+ * Hk <= 65536; a rot_dim out of range returns EXATTN_ERR_UNSUPPORTED, a
+ * factor EXATTN_ERR_VALUE; otherwise errors as attn_fwd_ex.
+ */
+int attn_rotary(int dtype, const void* q, exattn_strides q_strides, void* q_out, exattn_strides qo_strides, int Hq,
+                const void* k, exattn_strides k_strides, void* k_out, exattn_strides ko_strides, int Hk,
+                const int* positions, long long pos_stride, const double* inv_freq, int rot_dim, int interleaved,
+                int inverse, float factor, int B, int N, int d, void* stream);
+
+/*
+ * A paged key/value cache.  K and V live in pages of page_size rows, so that
+ * sequences grow without being moved and share the pages of a common prefix.
+ *   k_cache, v_cache : [num_pages, Hkv, page_size, d] views, described by
+ *     exattn_strides with b_stride the page stride, h_stride and n_stride
+ *     (the row stride).  page_size is a power of two, 8..1024 (else
+ *     EXATTN_ERR_UNSUPPORTED).
+ *   page_table : device int32 [B, max_pages], row stride table_stride >=
+ *     max_pages: row r of sequence b is row r % page_size of page
+ *     page_table[b][r / page_size].
+ *   seqlens    : device int32 [B], rows of each sequence, its new tokens
+ *     included.
+ *   cu_seqlens : device int32 [B + 1]: the new tokens of sequence b are rows
+ *     [cu_seqlens[b], cu_seqlens[b + 1]) of the packed tensors, its last
+ *     positions; NULL: every sequence has total / B of them (total a
+ *     multiple of B, else EXATTN_ERR_SHAPE).
+ * The tables are read on the device and every access is checked against the
+ * sizes given here, so a wrong table gives wrong results but never an access
+ * out of bounds.  Rows of the packed tensors that belong to no sequence
+ * (at or past cu_seqlens[B]) are neither read nor written.
+ *
+ * attn_cache_append -- writes the new tokens' K and V into their pages, K
+ *   turned as by attn_rotary at each token's position (seqlens[b] minus the
+ *   new tokens of b, and on), and Q likewise into q_out, in one launch.
+ *   k, v : [total, Hkv, d] packed (b_stride unused); q, q_out : [total, Hq, d],
+ *     or NULL with Hq = 0.  inv_freq NULL (then Hq = 0): nothing is turned.
+ *   A token whose position is negative, past max_pages * page_size, or on a
+ *   page number outside the pool is not stored (its q_out is written).  Two
+ *   tokens that share a row of a page (a page in two sequences' tables) race:
+ *   give each sequence its own copy of a page before it is written to
+ *   (attn_cache_copy).
+ */
+int attn_cache_append(int dtype, const void* q, exattn_strides q_strides, void* q_out, exattn_strides qo_strides,
+                      int Hq, const void* k, exattn_strides k_strides, const void* v, exattn_strides v_strides,
+                      void* k_cache, exattn_strides kc_strides, void* v_cache, exattn_strides vc_strides, int Hkv,
+                      int num_pages, int page_size, const int* page_table, long long table_stride, int max_pages,
+                      const int* seqlens, const int* cu_seqlens, int B, int total, int d, const double* inv_freq,
+                      int rot_dim, int interleaved, float factor, void* stream);
+
+/*
+ * attn_cache_copy -- page dst[i] of every slab becomes a copy of page src[i],
+ *   for i in [0, n): the partly filled last page of a forked sequence, or the
+ *   moves that compact a fragmented pool.
+ *   pool : `slabs` slabs (a layer's K or V) of num_pages pages; page p of slab
+ *     s is the page_bytes bytes at pool + s * slab_stride + p * page_stride
+ *     (strides in bytes).  Pages must not overlap; pool, strides and page_bytes
+ *     are multiples of 16 (EXATTN_ERR_ALIGN).
+ *   src, dst : HOST int32 [n] (page tables are kept on the host; the numbers
+ *     travel with the launches, and a captured graph keeps those of its
+ *     capture).  They may be freed once the call returns.
+ *   Every number lies in [0, num_pages), no destination occurs twice and none
+ *   is a source, else EXATTN_ERR_VALUE and nothing is copied.  n = 0 does
+ *   nothing.  1 <= slabs <= 65535.
+ */
+int attn_cache_copy(void* pool, long long slab_stride, long long page_stride, long long page_bytes, int slabs,
+                    int num_pages, const int* src, const int* dst, int n, void* stream);
 
 /* Human-readable text of an exattn_status (static storage, never NULL). */
 const char* exattn_status_string(int status);

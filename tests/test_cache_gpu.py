@@ -1,0 +1,156 @@
+"""Appending tokens to a paged cache and copying its pages: values against the
+definition in 64 bits with the bound of test_rotary_gpu.py, and everything that
+a call must not touch, bit for bit."""
+import numpy as np
+import pytest
+import torch
+
+from tests.test_rotary_gpu import check, f64, turned
+
+pytestmark = pytest.mark.gpu
+
+DEV = torch.device("cuda:0")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from exact_attention_67_gb300 import build
+    build.build()
+
+
+def randn(*shape, seed, dtype):
+    return torch.randn(*shape, generator=torch.Generator().manual_seed(seed)).to(dtype).to(DEV)
+
+
+CASES = [
+    # (new tokens, lengths, Hq, Hk, d, page size, rot (0: none), interleaved, dtype, token-major cache)
+    ([1], [1], 1, 1, 64, 16, 64, False, torch.bfloat16, False),
+    ([1] * 9, [1, 16, 17, 300, 5, 64, 128, 33, 2], 8, 2, 128, 16, 128, False, torch.bfloat16, False),
+    ([7, 0, 130, 1, 64], [7, 40, 200, 9, 64], 3, 3, 64, 32, 32, True, torch.float16, True),
+    ([5, 3], [2, 3], 2, 1, 128, 8, 6, False, torch.bfloat16, False),   # more new tokens than length: positions below 0
+    ([600, 500], [70000, 500], 4, 4, 128, 128, 20, True, torch.bfloat16, False),
+    ([40, 40], [41, 99], 0, 2, 64, 64, 0, False, torch.float16, True),
+]
+
+
+@pytest.mark.parametrize("new,lens,Hq,Hk,d,ps,rot,interleaved,dtype,token_major", CASES, ids=lambda x: str(x)[:40])
+def test_append(new, lens, Hq, Hk, d, ps, rot, interleaved, dtype, token_major):
+    import exact_attention_67_gb300 as ex
+    B, pad = len(new), 3
+    total = sum(new) + pad  # rows behind the last sequence stay as they are
+    need = [-(-n // ps) for n in lens]
+    pages = sum(need) + 2
+    order = torch.randperm(pages, generator=torch.Generator().manual_seed(4)).tolist()
+    table = torch.full((B, max(need) + 1), -1, dtype=torch.int32)
+    for b in range(B):
+        for i in range(need[b]):
+            table[b, i] = order.pop()
+    if token_major:
+        kc, vc = (randn(pages, ps, Hk, d, seed=s, dtype=dtype).transpose(1, 2) for s in (1, 2))
+    else:
+        kc, vc = (randn(pages, Hk, ps, d, seed=s, dtype=dtype) for s in (1, 2))
+    kc0, vc0 = f64(kc), f64(vc)
+    k, v = randn(total, Hk, d, seed=5, dtype=dtype), randn(total, Hk, d, seed=6, dtype=dtype)
+    q = randn(total, Hq, d, seed=7, dtype=dtype) if Hq else None
+    qo = torch.full_like(q, 7.0) if Hq else None
+    freq, factor = ex.rotary_frequencies(rot, yarn=4.0) if rot else (None, 1.0)
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(new)]), dtype=torch.int32, device=DEV)
+    seq = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    ex.attn_cache_append(k, v, kc, vc, table.to(DEV), seq, cu, q, qo, freq, interleaved, factor)
+    torch.cuda.synchronize()
+    pos = np.concatenate([lens[b] - new[b] + np.arange(new[b]) for b in range(B)])
+    fr = freq.cpu().numpy() if rot else np.zeros(0)
+
+    def turn(x):  # [tokens, H, d]
+        y, s = turned(f64(x)[: total - pad].transpose(1, 0, 2), pos, fr, factor, interleaved)
+        return y.transpose(1, 0, 2), s.transpose(1, 0, 2)
+
+    if Hq:
+        check(qo[: total - pad], *turn(q), dtype)
+        assert torch.all(qo[total - pad:] == 7.0)
+    ky, ks = turn(k)
+    size = np.zeros_like(kc0)
+    t = 0
+    for b in range(B):
+        for i in range(new[b]):
+            p = pos[t]
+            if p >= 0:
+                page, row = int(table[b, p // ps]), p % ps
+                kc0[page, :, row], size[page, :, row] = ky[t], ks[t]
+                vc0[page, :, row] = f64(v[t])
+            t += 1
+    touched = size.sum((1, 3)) > 0
+    check(kc, kc0, size, dtype)
+    got = f64(kc)
+    keep = ~np.broadcast_to(touched[:, None, :, None], got.shape)
+    assert np.array_equal(got[keep], kc0[keep]) and np.array_equal(f64(vc), vc0)
+
+
+def test_append_without_offsets_and_bad_tables():
+    """The same tokens with and without cu_seqlens; page numbers outside the
+    pool, positions past the table and offsets past the tensors store nothing."""
+    import exact_attention_67_gb300 as ex
+    B, ps, H, d, pages = 3, 16, 2, 64, 6
+    k, v = randn(B * 2, H, d, seed=1, dtype=torch.bfloat16), randn(B * 2, H, d, seed=2, dtype=torch.bfloat16)
+    table = torch.tensor([[0, 1], [2, 3], [4, 5]], dtype=torch.int32, device=DEV)
+    lens = torch.tensor([17, 2, 32], dtype=torch.int32, device=DEV)
+    caches = [[torch.zeros(pages, H, ps, d, dtype=torch.bfloat16, device=DEV) for _ in range(2)] for _ in range(3)]
+    ex.attn_cache_append(k, v, *caches[0], table, lens)
+    ex.attn_cache_append(k, v, *caches[1], table, lens, torch.tensor([0, 2, 4, 6], dtype=torch.int32, device=DEV))
+    assert torch.equal(caches[0][0], caches[1][0]) and torch.equal(caches[0][1], caches[1][1])
+    assert caches[0][0].any()
+    bad = torch.tensor([[6, -1], [1 << 30, -(1 << 30)], [-5, 99]], dtype=torch.int32, device=DEV)
+    ex.attn_cache_append(k, v, *caches[2], bad, lens)
+    ex.attn_cache_append(k, v, *caches[2], table, lens + 40)       # past the table
+    ex.attn_cache_append(k, v, *caches[2], table, lens - (1 << 30))
+    ex.attn_cache_append(k, v, *caches[2], table, lens, torch.tensor([6, 9, 12, 90], dtype=torch.int32, device=DEV))
+    torch.cuda.synchronize()
+    assert not caches[2][0].any() and not caches[2][1].any()
+    ex.attn_cache_append(k[:0], v[:0], *caches[2], table, lens)
+    assert not caches[2][0].any()
+
+
+@pytest.mark.parametrize("slabs,pages,block,n,dtype", [
+    (1, 4, (1, 8, 64), 1, torch.bfloat16), (6, 70, (2, 16, 64), 33, torch.float16), (2, 5000, (1, 8, 64), 2300, torch.bfloat16),
+    (3, 9, (5, 64, 128), 4, torch.bfloat16), (1, 3, (17, 256, 128), 1, torch.float16), (2, 6, (8,), 2, torch.float32),
+])
+def test_copy(slabs, pages, block, n, dtype):
+    import exact_attention_67_gb300 as ex
+    pool = randn(slabs, pages, *block, seed=n, dtype=dtype)
+    order = torch.randperm(pages, generator=torch.Generator().manual_seed(n)).to(torch.int32)
+    src, dst = order[:n], order[n: 2 * n]
+    want = pool.clone()
+    want[:, dst.long().to(DEV)] = pool[:, src.long().to(DEV)]
+    ex.attn_cache_copy(pool, src, dst.tolist())
+    assert torch.equal(pool, want)
+
+
+def test_copy_of_layouts_and_refusals():
+    import exact_attention_67_gb300 as ex
+    # Page-major storage: a page's slabs side by side; and a pool inside a wider tensor.
+    store = randn(10, 3, 2, 16, 64, seed=1, dtype=torch.bfloat16)
+    pool, want = store.transpose(0, 1), store.clone()
+    ex.attn_cache_copy(pool, [1, 2, 9], [0, 5, 3])
+    want[[0, 5, 3]] = want[[1, 2, 9]]
+    assert torch.equal(store, want)
+    wide = randn(2, 10, 4, 16, 64, seed=2, dtype=torch.bfloat16)
+    want = wide.clone()
+    ex.attn_cache_copy(wide[:, :, 1:3], [4], [7])
+    want[:, 7, 1:3] = want[:, 4, 1:3]
+    assert torch.equal(wide, want)
+    for src, dst in (([0], [10]), ([-1], [2]), ([0, 1], [5, 5]), ([0, 1], [1, 2]), ([3], [3]),
+                     (list(range(40)), list(range(40, 79)) + [40])):
+        big = torch.zeros(1, 10 if len(src) < 5 else 200, 1, 8, 64, dtype=torch.bfloat16, device=DEV)
+        with pytest.raises(ex.ExattnError):
+            ex.attn_cache_copy(big, src, dst)
+    with pytest.raises(ValueError):
+        ex.attn_cache_copy(pool, [1], [2, 3])
+    with pytest.raises(ValueError):
+        ex.attn_cache_copy(pool, torch.tensor([1], dtype=torch.int32, device=DEV), [2])
+    with pytest.raises(ValueError):
+        ex.attn_cache_copy(wide[:, :, :, ::2], [1], [2])  # a page with holes
+    with pytest.raises(ex.ExattnError):
+        ex.attn_cache_copy(wide[:1].expand(2, -1, -1, -1, -1), [1], [2])  # slabs on top of each other
+    ex.attn_cache_copy(pool, [], [])
