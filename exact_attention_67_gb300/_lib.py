@@ -28,7 +28,7 @@ EXPORTS = ("attn_fwd", "attn_bwd", "attn_bwd_workspace_size", "attn_bwd_preproce
            "attn_bwd_varlen",
            "attn_fwd_decode_workspace_size", "attn_fwd_decode", "attn_bwd_noalloc",
            "attn_fwd_bwd_host_workspace_size", "attn_fwd_bwd_host",
-           "attn_rotary", "attn_cache_append", "attn_cache_copy",
+           "attn_rotary", "attn_cache_append", "attn_cache_copy", "attn_fwd_paged_workspace_size", "attn_fwd_paged",
            "exattn_status_string", "exattn_last_cuda_error",
            "exattn_device_error", "exattn_device_error_poll", "exattn_watchdog_selftest", "exattn_version")
 
@@ -118,6 +118,11 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
         lib.attn_cache_append.restype = i
         lib.attn_cache_copy.argtypes = [vp, ll, ll, ll, i, i, vp, vp, i, vp]
         lib.attn_cache_copy.restype = i
+        lib.attn_fwd_paged_workspace_size.argtypes = [i, i, i, i, i, i, i]
+        lib.attn_fwd_paged_workspace_size.restype = sz
+        lib.attn_fwd_paged.argtypes = [i, vp, S, vp, S, vp, S, vp, S, vp, i, i, vp, ll, i, vp, vp, i, i, i, i, i, i, i, i, i, f,
+                                       vp, sz, vp]
+        lib.attn_fwd_paged.restype = i
         lib.exattn_status_string.argtypes = [i]
         lib.exattn_status_string.restype = ctypes.c_char_p
         lib.exattn_last_cuda_error.argtypes = []

@@ -59,6 +59,38 @@ struct RotaryArgs {
 };
 cudaError_t launch_rotary(const RotaryArgs& a, cudaStream_t stream);
 
+// Attention of new tokens over a paged cache.  The query heads of a key head
+// (G of them) and consecutive new tokens share the rows (forward kernel) or
+// columns (decode kernel) of a unit: unit row r is token r / G, head r % G.
+struct PagedArgs {
+  const CUtensorMap* tm_q;  // (d, G, Hkv, total), box 64 x G x 1 x tokens of a query tile
+  const CUtensorMap* tm_k;  // (d, page_size, Hkv, num_pages), box 64 x min(page_size, 128) x 1 x 1
+  const CUtensorMap* tm_v;
+  void* o;                  // [total, Hq, d], strides h and n
+  Strides so;
+  float* lse;               // fp32 [Hq, total]
+  NewTokens nt;
+  PageView pv;
+  int Hkv, G, d, dtype;
+  int max_q, max_k;         // bounds of the new tokens and lengths of a sequence
+  int causal, window;
+  float scale_log2;
+  int tile_tokens;          // tokens of a query tile: 128 / G (forward), 16 / G (decode)
+  int ctas;                 // grid; the work's split follows from it (paged_sched.cuh)
+  int unit_cost, min_chunk;
+  float* part_o;            // [ctas][2][rows][d]
+  float* part_lse;          // [ctas][2][rows]
+  int* plan;                // [ctas][8]
+  unsigned* err;
+  int device;
+};
+constexpr int kPagedDecodeCols = 16;  // unit rows of the decode kernel
+constexpr int kPagedRows = 256;       // unit rows of the forward kernel: two query tiles
+cudaError_t launch_paged_decode(const PagedArgs& a, cudaStream_t stream);
+cudaError_t launch_paged_fwd(const PagedArgs& a, cudaStream_t stream);
+// Joins the pieces of the units that ended up on several CTAs (rows: a unit's).
+cudaError_t launch_paged_merge(const PagedArgs& a, int rows, cudaStream_t stream);
+
 struct CopyArgs {
   char* pool;
   long long slab_stride, page_stride, page_bytes;  // bytes

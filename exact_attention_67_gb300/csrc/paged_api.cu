@@ -1,6 +1,7 @@
 // paged_api.cu -- the C ABI of the operators around a paged key/value cache
 // (declared in include/exattn.h): argument validation and launches.  No device
 // memory is allocated and nothing synchronises.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstdlib>
@@ -207,4 +208,131 @@ extern "C" int attn_cache_copy(void* pool, long long slab_stride, long long page
   if (rc != EXATTN_OK) return rc;
   const CopyArgs a{static_cast<char*>(pool), slab_stride, page_stride, page_bytes, slabs, src, dst, n};
   return launch_page_copy(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? EXATTN_OK : EXATTN_ERR_CUDA;
+}
+
+namespace {
+
+constexpr int kSMs = 152;
+
+// How a paged attention is laid out on the GPU, from sizes alone.
+struct PagedPlan {
+  bool decode;
+  int tile_tokens, ctas, rows, unit_cost, min_chunk;
+  size_t plan_bytes, lse_bytes, total_bytes;
+};
+
+PagedPlan paged_plan(int B, int Hq, int Hkv, int total, int max_q, int max_k, int d) {
+  PagedPlan p{};
+  const int G = Hq / Hkv;
+  max_q = std::min(max_q, total);
+  p.decode = static_cast<long long>(max_q) * G <= kPagedDecodeCols;
+  p.rows = p.decode ? kPagedDecodeCols : kPagedRows;
+  p.tile_tokens = (p.decode ? kPagedDecodeCols : 128) / G;
+  p.unit_cost = 2;
+  p.min_chunk = 6;
+  const int ut = p.decode ? p.tile_tokens : 2 * p.tile_tokens;
+  // At most so many weights (paged_sched.cuh): units of full length.
+  const double units = static_cast<double>(Hkv) * std::min<double>(static_cast<double>(B) * ((max_q + ut - 1) / ut),
+                                                                   static_cast<double>(total) / ut + B);
+  const double weights = units * ((static_cast<double>(max_k) + 127) / 128 + p.unit_cost);
+  p.ctas = static_cast<int>(std::min<double>(kSMs, std::max(1.0, std::ceil(weights / p.min_chunk))));
+  auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+  const size_t slots = static_cast<size_t>(p.ctas) * 2 * p.rows;
+  p.plan_bytes = up(static_cast<size_t>(p.ctas) * 8 * sizeof(int));
+  p.lse_bytes = up(slots * sizeof(float));
+  p.total_bytes = p.plan_bytes + p.lse_bytes + up(slots * d * sizeof(float));
+  return p;
+}
+
+int check_paged(int B, int Hq, int Hkv, int total, int max_q, int max_k, int d) {
+  if (B < 1 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || total < 1 || max_q < 1 || max_k < 1) return EXATTN_ERR_SHAPE;
+  if (Hq > 65536 || static_cast<long long>(Hq) * total >= (1ll << 31) || total >= (1 << 30) || max_k >= (1 << 30) ||
+      B >= (1 << 24))
+    return EXATTN_ERR_SHAPE;
+  if ((d != 64 && d != 128) || Hq / Hkv > 128) return EXATTN_ERR_UNSUPPORTED;
+  return EXATTN_OK;
+}
+
+}  // namespace
+
+extern "C" size_t attn_fwd_paged_workspace_size(int B, int Hq, int Hkv, int total, int max_seqlen_q, int max_seqlen_k,
+                                                int d) {
+  if (check_paged(B, Hq, Hkv, total, max_seqlen_q, max_seqlen_k, d) != EXATTN_OK) return 0;
+  return paged_plan(B, Hq, Hkv, total, max_seqlen_q, max_seqlen_k, d).total_bytes;
+}
+
+extern "C" int attn_fwd_paged(int dtype, const void* q, exattn_strides sq, const void* k_cache, exattn_strides skc,
+                              const void* v_cache, exattn_strides svc, void* o, exattn_strides so, float* lse,
+                              int num_pages, int page_size, const int* page_table, long long table_stride,
+                              int max_pages, const int* seqlens, const int* cu_seqlens, int B, int Hq, int Hkv,
+                              int total, int max_seqlen_q, int max_seqlen_k, int d, int causal, int window,
+                              float scale, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!q || !k_cache || !v_cache || !o || !lse || !page_table || !seqlens) return EXATTN_ERR_NULL;
+  if (!known_dtype(dtype)) return EXATTN_ERR_UNSUPPORTED;
+  int rc = check_paged(B, Hq, Hkv, total, max_seqlen_q, max_seqlen_k, d);
+  if (rc != EXATTN_OK) return rc;
+  PagedArgs a{};
+  if ((rc = check_tokens(&a.nt, cu_seqlens, seqlens, B, total)) != EXATTN_OK) return rc;
+  if ((rc = check_pages(&a.pv, page_table, table_stride, max_pages, num_pages, page_size, B, Hkv, skc, svc)) !=
+      EXATTN_OK)
+    return rc;
+  if (window < 0 || !std::isfinite(scale) || !(scale > 0.f)) return EXATTN_ERR_VALUE;
+  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(o, 16) || !aligned(lse, 4))
+    return EXATTN_ERR_ALIGN;
+  if ((rc = check_strides(sq, 1, Hq, total)) != EXATTN_OK || (rc = check_strides(so, 1, Hq, total)) != EXATTN_OK)
+    return rc;
+  const PagedPlan plan = paged_plan(B, Hq, Hkv, total, max_seqlen_q, max_seqlen_k, d);
+  if (!workspace || workspace_bytes < plan.total_bytes) return EXATTN_ERR_WORKSPACE;
+  if (!aligned(workspace, 16)) return EXATTN_ERR_ALIGN;
+  int dev = 0;
+  unsigned* err = nullptr;
+  if ((rc = setup_device(&dev, &err)) != EXATTN_OK) return rc;
+
+  const int dt = dtype == EXATTN_DTYPE_F16 ? kF16 : kBF16, G = Hq / Hkv;
+  CUtensorMap mq, mk, mv;
+  // A stride along an axis of extent 1 is never used; the encoder gets a legal one.
+  auto bytes = [&](int extent, long long stride) { return static_cast<cuuint64_t>(extent > 1 ? stride : d) * 2; };
+  {
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(G), static_cast<cuuint64_t>(Hkv),
+                                static_cast<cuuint64_t>(total)};
+    const cuuint64_t str[3] = {bytes(G, sq.h_stride), bytes(Hkv, G * sq.h_stride), bytes(total, sq.n_stride)};
+    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(G), 1, static_cast<cuuint32_t>(plan.tile_tokens)};
+    if (!encode_map(&mq, dt, 4, q, dims, str, box)) return EXATTN_ERR_CUDA;
+  }
+  for (int i = 0; i < 2; ++i) {
+    const exattn_strides& s = i == 0 ? skc : svc;
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(page_size),
+                                static_cast<cuuint64_t>(Hkv), static_cast<cuuint64_t>(num_pages)};
+    const cuuint64_t str[3] = {bytes(page_size, s.n_stride), bytes(Hkv, s.h_stride), bytes(num_pages, s.b_stride)};
+    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(std::min(page_size, 128)), 1, 1};
+    if (!encode_map(i == 0 ? &mk : &mv, dt, 4, i == 0 ? k_cache : v_cache, dims, str, box)) return EXATTN_ERR_CUDA;
+  }
+  a.tm_q = &mq;
+  a.tm_k = &mk;
+  a.tm_v = &mv;
+  a.o = o;
+  a.so = to_strides(so);
+  a.lse = lse;
+  a.Hkv = Hkv;
+  a.G = G;
+  a.d = d;
+  a.dtype = dt;
+  a.max_q = max_seqlen_q;
+  a.max_k = static_cast<int>(std::min<long long>(max_seqlen_k, static_cast<long long>(max_pages) * page_size));
+  a.causal = causal ? 1 : 0;
+  a.window = std::min(window, 1 << 30);
+  a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  a.tile_tokens = plan.tile_tokens;
+  a.ctas = plan.ctas;
+  a.unit_cost = plan.unit_cost;
+  a.min_chunk = plan.min_chunk;
+  char* ws = static_cast<char*>(workspace);
+  a.plan = reinterpret_cast<int*>(ws);
+  a.part_lse = reinterpret_cast<float*>(ws + plan.plan_bytes);
+  a.part_o = reinterpret_cast<float*>(ws + plan.plan_bytes + plan.lse_bytes);
+  a.err = err;
+  a.device = dev;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if ((plan.decode ? launch_paged_decode(a, st) : launch_paged_fwd(a, st)) != cudaSuccess) return EXATTN_ERR_CUDA;
+  return launch_paged_merge(a, plan.rows, st) == cudaSuccess ? EXATTN_OK : EXATTN_ERR_CUDA;
 }

@@ -1,0 +1,543 @@
+// paged_fwd.cu -- attention of chunks of new tokens over a paged cache, for
+// sm_103a.
+//
+// The products, the softmax and the warps' roles are those of the dense forward
+// (fwd.cu): two 128-row query tiles share a stream of 128-key tiles, S_t = Q_t
+// K_j^T and O_t += P_t V_j accumulate in TMEM, a softmax warpgroup works on one
+// tile while the tensor core works on the other, P and V enter the second
+// product in f16.  What differs:
+//   * a tile's rows are the query heads of one key head times consecutive tokens
+//     (row r: token r / G, head r % G; 128 / G tokens, the rows left over idle),
+//     loaded by one TMA box, so K and V are streamed once for a whole group;
+//   * one CTA an SM runs through its chunk of the batch's keys (paged_sched.cuh),
+//     piece after piece;
+//   * a key tile is gathered page by page: one box a page, issued by one lane
+//     each, page numbers read one tile ahead;
+//   * stored rows behind the last visible key may hold anything: their scores are
+//     replaced by -inf, their V rows zeroed in shared memory by the converting
+//     warps (which run for f16 inputs too, to that end);
+//   * the logsumexp is formed from the unrounded weights.  So is bf16's O: the
+//     f16 rounding of P (2^-12 of a weight at most) is far below the output's.
+//     f16's O is normalised by the sum of the rounded weights.
+#include "paged.cuh"
+#include "paged_sched.cuh"
+#include "ptx.cuh"
+
+namespace exattn {
+
+namespace {
+
+template <int D>
+struct PfCfg {
+  static constexpr int BN = kKeyTile;
+  static constexpr int NCHUNK = D / 64;
+  static constexpr int CHUNK_BYTES = 128 * 128;
+  static constexpr int TILE_BYTES = NCHUNK * CHUNK_BYTES;
+  static constexpr int STAGES = D == 64 ? 4 : 2;
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_K = OFF_Q + 2 * TILE_BYTES;
+  static constexpr int OFF_V = OFF_K + STAGES * TILE_BYTES;
+  static constexpr int OFF_BAR = OFF_V + STAGES * TILE_BYTES;
+  static constexpr int SMEM_BYTES = OFF_BAR + 512 + 1024;
+  static_assert(SMEM_BYTES > 120 * 1024, "one CTA per SM: it holds all 512 TMEM columns");
+  static constexpr int THREADS = 384;
+  // TMEM as in fwd.cu: at d = 64 P has columns of its own, so that the next S_t
+  // can be computed while the softmax still works on this one.
+  static constexpr bool EARLY_S = D == 64;
+  static constexpr uint32_t TM_COLS = 512;
+  __host__ __device__ static constexpr uint32_t tm_s(int t) { return 128u * t; }
+  __host__ __device__ static constexpr uint32_t tm_p(int t) { return EARLY_S ? 256u + 64u * t : 128u * t; }
+  __host__ __device__ static constexpr uint32_t tm_o(int t) { return EARLY_S ? 384u + 64u * t : 256u + 128u * t; }
+};
+
+template <int STAGES>
+struct PfBars {
+  uint64_t q_full, q_empty;
+  uint64_t k_full[STAGES], k_empty[STAGES];
+  uint64_t v_full[STAGES], v_empty[STAGES], v_ready[STAGES];
+  uint64_t s_full[2], s_free[2], p_full[2], pv_done[2];
+  uint64_t o_full[2], o_free[2];
+  uint64_t mma_done;
+  PagedCursor start;
+  uint32_t tmem_base;
+  int abort;
+};
+
+constexpr float kPfRescale = 8.0f;
+
+__device__ __forceinline__ uint32_t pf_bf16x2_to_f16x2(uint32_t w) {
+  return pack_f16x2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
+// Key tiles of piece p that query tile t (tokens [tok0 + t TT, ...)) takes part
+// in, counted from p.t_lo.
+__device__ __forceinline__ int tiles_of(const PagedArgs& a, const PagedPiece& p, int t) {
+  const int t0 = p.tok0 + t * a.tile_tokens, t1 = min(p.tok0 + p.ntok, t0 + a.tile_tokens);
+  if (t0 >= t1) return 0;
+  int lo, hi;
+  paged_keys(a, p.s, t0, t1, &lo, &hi);
+  if (hi <= lo) return 0;
+  return max(0, min((hi + kKeyTile - 1) / kKeyTile, p.t_hi) - p.t_lo);
+}
+
+}  // namespace
+
+template <typename T, int D>
+__global__ void __launch_bounds__(384, 1)
+    paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PagedArgs a) {
+  using C = PfCfg<D>;
+  using E = Elem<T>;
+  using PE = Elem<__half>;
+  using Bars = PfBars<C::STAGES>;
+  constexpr bool kConvertV = E::kFmt != PE::kFmt;
+  static_assert(sizeof(Bars) <= 512, "barrier block too large");
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Bars* bars = reinterpret_cast<Bars*>(smem + C::OFF_BAR);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int TT = a.tile_tokens, UT = 2 * TT, G = a.G;
+
+  if (warp == 0) {
+    long long chunk;
+    const PagedCursor c = paged_start(a, UT, static_cast<int>(blockIdx.x), lane, &chunk);
+    if (lane == 0) {
+      bars->start = c;
+      paged_note(a, c, chunk, static_cast<int>(blockIdx.x));
+    }
+  }
+  if (threadIdx.x == 32) {
+    mbar_init(&bars->q_full, 1);
+    mbar_init(&bars->q_empty, 1);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&bars->s_full[t], 1);
+      mbar_init(&bars->s_free[t], 4);
+      mbar_init(&bars->p_full[t], 4);
+      mbar_init(&bars->pv_done[t], 1);
+      mbar_init(&bars->o_full[t], 1);
+      mbar_init(&bars->o_free[t], 4);
+    }
+    mbar_init(&bars->mma_done, 1);
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(&bars->k_full[s], 1);
+      mbar_init(&bars->k_empty[s], 1);
+      mbar_init(&bars->v_full[s], 1);
+      mbar_init(&bars->v_empty[s], 1);
+      mbar_init(&bars->v_ready[s], 2);
+    }
+    bars->abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(&bars->tmem_base, C::TM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const uint32_t tmem = bars->tmem_base;
+  const WaitCtl wc{&bars->abort, a.err};
+  PagedCursor cur = bars->start;
+  PagedSeq seq = cur.left > 0 ? paged_seq(a, cur.b) : PagedSeq{};
+  PagedPiece pc;
+
+  if (warp == 8) {
+    // ------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      tma_prefetch_desc(&tm_q);
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+    }
+    const uint64_t pol_kv = l2_policy_evict_last();  // re-read by every unit of the (sequence, key head)
+    const uint64_t pol_q = l2_policy_evict_first();
+    const int ps = a.pv.page_size, shift = a.pv.page_shift;
+    const int box = min(ps, C::BN), per_tile = C::BN / box;
+    const uint32_t q_bytes = static_cast<uint32_t>(TT * G) * 128 * C::NCHUNK;
+    int kt = 0, vt = 0, seg = 0;  // key tiles and Qs issued
+    bool ok = true;
+    while (ok && cur.next(a, UT, seq, &pc)) {
+      const int n0 = tiles_of(a, pc, 0), n1 = tiles_of(a, pc, 1), n = max(n0, n1);
+      if (n == 0) continue;
+      if (seg >= 1 && !(ok = mbar_wait_warp(&bars->q_empty, (seg - 1) & 1, wc))) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&bars->q_full, q_bytes * ((n0 > 0) + (n1 > 0)));
+        for (int t = 0; t < 2; ++t)
+          if ((t == 0 ? n0 : n1) > 0)
+            for (int c = 0; c < C::NCHUNK; ++c)
+              tma_load_4d(&tm_q, &bars->q_full, smem + C::OFF_Q + t * C::TILE_BYTES + c * C::CHUNK_BYTES, c * 64, 0, pc.h,
+                          pc.s.row0 + pc.tok0 + t * TT, pol_q);
+      }
+      ++seg;
+      const int* row = a.pv.table + pc.b * a.pv.table_stride;
+      auto boxes = [&](int t) { return min(per_tile, (pc.key_hi - t * C::BN + box - 1) / box); };
+      auto page_of = [&](int t) { return lane < boxes(t) ? row[(t * C::BN >> shift) + lane] : 0; };
+      int page = page_of(pc.t_lo);
+      for (int t = pc.t_lo; t < pc.t_lo + n; ++t) {
+        const int s = kt % C::STAGES;
+        const uint32_t ph = ((kt / C::STAGES) & 1) ^ 1;
+        const int next_page = t + 1 < pc.t_lo + n ? page_of(t + 1) : 0;
+        const int nb = boxes(t), off = t * C::BN & (ps - 1);
+        const uint32_t bytes = static_cast<uint32_t>(nb * box) * 128 * C::NCHUNK;
+        const int at = s * C::TILE_BYTES + lane * box * 128;
+        if (!(ok = mbar_wait_warp(&bars->k_empty[s], ph, wc))) break;
+        if (lane == 0) mbar_arrive_expect_tx(&bars->k_full[s], bytes);
+        __syncwarp();
+        if (lane < nb)
+          for (int c = 0; c < C::NCHUNK; ++c)
+            tma_load_4d(&tm_k, &bars->k_full[s], smem + C::OFF_K + at + c * C::CHUNK_BYTES, c * 64, off, pc.h, page, pol_kv);
+        __syncwarp();
+        ++kt;
+        if (!(ok = mbar_wait_warp(&bars->v_empty[s], ph, wc))) break;
+        if (lane == 0) mbar_arrive_expect_tx(&bars->v_full[s], bytes);
+        __syncwarp();
+        if (lane < nb)
+          for (int c = 0; c < C::NCHUNK; ++c)
+            tma_load_4d(&tm_v, &bars->v_full[s], smem + C::OFF_V + at + c * C::CHUNK_BYTES, c * 64, off, pc.h, page, pol_kv);
+        __syncwarp();
+        ++vt;
+        page = next_page;
+      }
+    }
+    __syncwarp();
+    if (lane == 0 && *reinterpret_cast<volatile int*>(&bars->abort)) {
+      // Never leave a copy in flight into shared memory this CTA is about to release.
+      if (seg > 0) mbar_wait_drain(&bars->q_full, (seg - 1) & 1, a.err);
+      for (int j = max(0, kt - C::STAGES); j < kt; ++j)
+        mbar_wait_drain(&bars->k_full[j % C::STAGES], (j / C::STAGES) & 1, a.err);
+      for (int j = max(0, vt - C::STAGES); j < vt; ++j)
+        mbar_wait_drain(&bars->v_full[j % C::STAGES], (j / C::STAGES) & 1, a.err);
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ MMA issuer
+    constexpr uint32_t idesc_s = idesc_f16kind(E::kFmt, 128, C::BN, 0, 0);
+    constexpr uint32_t idesc_o = idesc_f16kind(PE::kFmt, 128, D, 0, 1);
+    const uint64_t q_desc = sdesc_sw128(smem_u32(smem + C::OFF_Q), 16, 1024);
+    const uint64_t k_desc = sdesc_sw128(smem_u32(smem + C::OFF_K), 16, 1024);
+    const uint64_t v_desc = sdesc_sw128(smem_u32(smem + C::OFF_V), C::CHUNK_BYTES, 1024);
+    constexpr uint32_t kTileDesc = C::TILE_BYTES >> 4;
+    auto issue_s = [&](int t, int stage) {
+      const uint64_t qa = q_desc + t * kTileDesc, kb = k_desc + stage * kTileDesc;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = ((kk >> 2) * C::CHUNK_BYTES + (kk & 3) * 32) >> 4;
+        mma_ss(tmem + C::tm_s(t), qa + off, kb + off, idesc_s, kk > 0);
+      }
+    };
+    auto issue_pv = [&](int t, int stage, bool acc) {
+      const uint64_t vb = v_desc + stage * kTileDesc;
+#pragma unroll
+      for (int kk = 0; kk < C::BN / 16; ++kk)
+        mma_ts(tmem + C::tm_o(t), tmem + C::tm_p(t) + kk * 8, vb + ((kk * 16 * 128) >> 4), idesc_o, (acc || kk > 0) ? 1u : 0u);
+    };
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_warp(bar, parity, wc); };
+    int kt = 0, seg = 0;
+    int cs[2] = {0, 0};  // S_t issued
+    int cp[2] = {0, 0};  // P_t consumed
+    int co[2] = {0, 0};  // pieces that tile t took part in
+    bool ok = true;
+    // S_t of the next step of tile t from K stage s.
+    auto next_s = [&](int t, int s) {
+      if (C::EARLY_S && cs[t] >= 1 && !(ok = wait(&bars->s_free[t], (cs[t] - 1) & 1))) return;
+      tc_fence_after();
+      if (elect_one()) {
+        issue_s(t, s);
+        mma_commit(&bars->s_full[t]);
+      }
+      __syncwarp();
+      ++cs[t];
+    };
+    while (ok && cur.next(a, UT, seq, &pc)) {
+      const int nt[2] = {tiles_of(a, pc, 0), tiles_of(a, pc, 1)};
+      const int n = max(nt[0], nt[1]);
+      if (n == 0) continue;
+      if (!(ok = wait(&bars->q_full, seg & 1))) break;
+      if (!(ok = wait(&bars->k_full[kt % C::STAGES], (kt / C::STAGES) & 1))) break;
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        if (ok && nt[t] > 0) next_s(t, kt % C::STAGES);
+      if (!ok) break;
+      if (elect_one()) {
+        mma_commit(&bars->k_empty[kt % C::STAGES]);
+        if (n == 1) mma_commit(&bars->q_empty);
+      }
+      __syncwarp();
+      for (int j = 0; ok && j < n; ++j) {
+        const int s = (kt + j) % C::STAGES, s1 = (kt + j + 1) % C::STAGES;
+        const uint32_t ph = ((kt + j) / C::STAGES) & 1, ph1 = ((kt + j + 1) / C::STAGES) & 1;
+        bool k_ready = false, v_ready = false;
+        auto want_k = [&]() {
+          if (!k_ready) k_ready = ok = wait(&bars->k_full[s1], ph1);
+          return k_ready;
+        };
+        if constexpr (C::EARLY_S) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+            if (ok && j + 1 < nt[t] && want_k()) next_s(t, s1);
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (!ok || j >= nt[t]) continue;
+          if (!(ok = wait(&bars->p_full[t], cp[t] & 1))) continue;
+          ++cp[t];
+          if (!v_ready && !(v_ready = ok = wait(&bars->v_ready[s], ph))) continue;
+          // The piece before has been read out of O_t.
+          if (j == 0 && co[t] >= 1 && !(ok = wait(&bars->o_free[t], (co[t] - 1) & 1))) continue;
+          tc_fence_after();
+          if (elect_one()) {
+            issue_pv(t, s, j > 0);
+            if (C::EARLY_S) mma_commit(&bars->pv_done[t]);
+            if (t == 1 || nt[1] <= j) mma_commit(&bars->v_empty[s]);
+            if (j + 1 == nt[t]) mma_commit(&bars->o_full[t]);
+          }
+          __syncwarp();
+          if (!C::EARLY_S && j + 1 < nt[t] && want_k()) next_s(t, s1);
+        }
+        if (ok && k_ready) {
+          if (elect_one()) {
+            mma_commit(&bars->k_empty[s1]);
+            if (j + 2 == n) mma_commit(&bars->q_empty);
+          }
+          __syncwarp();
+        }
+      }
+      kt += n;
+      ++seg;
+      co[0] += nt[0] > 0;
+      co[1] += nt[1] > 0;
+    }
+    // Nothing may still read shared memory or write TMEM once the CTA tears down.
+    if (elect_one()) mma_commit(&bars->mma_done);
+    __syncwarp();
+    if (lane == 0) mbar_wait_drain(&bars->mma_done, 0, a.err);
+    __syncwarp();
+  } else if (warp >= 10) {
+    // ------------------------------------------------------------ V made ready
+    constexpr int PER = C::TILE_BYTES / 16 / 64, BATCH = 8;
+    static_assert(PER % BATCH == 0, "conversion batches must divide the tile");
+    const int ct = (warp - 10) * 32 + lane;
+    int vt = 0;
+    bool ok = true;
+    while (ok && cur.next(a, UT, seq, &pc)) {
+      const int n = max(tiles_of(a, pc, 0), tiles_of(a, pc, 1));
+      for (int j = 0; j < n; ++j, ++vt) {
+        const int s = vt % C::STAGES, rows = pc.key_hi - (pc.t_lo + j) * C::BN;
+        if (!(ok = mbar_wait_warp(&bars->v_full[s], (vt / C::STAGES) & 1, wc))) break;
+        uint4* tile = reinterpret_cast<uint4*>(smem + C::OFF_V + s * C::TILE_BYTES);
+        if (kConvertV || rows < C::BN) {
+#pragma unroll 1
+          for (int b0 = 0; b0 < PER; b0 += BATCH) {
+            uint4 x[BATCH];
+#pragma unroll
+            for (int u = 0; u < BATCH; ++u) x[u] = tile[(b0 + u) * 64 + ct];
+#pragma unroll
+            for (int u = 0; u < BATCH; ++u) {
+              if constexpr (kConvertV)
+                x[u] = make_uint4(pf_bf16x2_to_f16x2(x[u].x), pf_bf16x2_to_f16x2(x[u].y), pf_bf16x2_to_f16x2(x[u].z),
+                                  pf_bf16x2_to_f16x2(x[u].w));
+              if ((((b0 + u) * 64 + ct) >> 3 & (C::BN - 1)) >= rows) x[u] = make_uint4(0, 0, 0, 0);
+              tile[(b0 + u) * 64 + ct] = x[u];
+            }
+          }
+          fence_proxy_async_smem();
+        }
+        mbar_arrive_warp(&bars->v_ready[s]);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int t = warp >> 2, wq = warp & 3;
+    const int row = wq * 32 + lane;  // row of the query tile == TMEM lane
+    const int row_tok = row / G, row_head = row % G;
+    const uint32_t lane_bits = static_cast<uint32_t>(wq * 32) << 16;
+    const uint32_t tS = tmem + lane_bits + C::tm_s(t);
+    const uint32_t tP = tmem + lane_bits + C::tm_p(t);
+    const uint32_t tO = tmem + lane_bits + C::tm_o(t);
+    int cs = 0, co = 0;
+    bool ok = true;
+    while (ok && cur.next(a, UT, seq, &pc)) {
+      const int n = tiles_of(a, pc, t);
+      const int tok0 = pc.tok0 + t * TT;
+      const int first = pc.s.off + tok0, last = first + TT - 1;  // positions of the tile's rows
+      const int pos = first + row_tok;
+      float m_ref = -INFINITY;  // reference maximum, log2 units
+      float le = 0.f, lb = 0.f; // sums of the unrounded and (f16) the rounded weights
+      for (int j = 0; j < n; ++j, ++cs) {
+        if (!(ok = mbar_wait_warp(&bars->s_full[t], cs & 1, wc))) break;
+        tc_fence_after();
+        uint32_t sr[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, sr[c]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_reg_fence(sr[c]);
+        if constexpr (C::EARLY_S) {
+          tc_fence_before();
+          mbar_arrive_warp(&bars->s_free[t]);
+        }
+        const int kv0 = (pc.t_lo + j) * C::BN;
+        const bool need_mask = kv0 + C::BN > pc.key_hi || (a.causal && kv0 + C::BN - 1 > first) ||
+                               (a.window > 0 && (kv0 < last - a.window + 1 || (!a.causal && kv0 + C::BN - 1 > first + a.window - 1)));
+        if (need_mask) {
+          int lim = pc.key_hi - kv0;  // visible columns c: lo <= c < lim
+          if (a.causal) lim = min(lim, pos - kv0 + 1);
+          else if (a.window > 0) lim = min(lim, pos + a.window - kv0);
+          const int lo = a.window > 0 ? pos - a.window + 1 - kv0 : 0;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (c * 32 + e >= lim || c * 32 + e < lo) sr[c][e] = __float_as_uint(-INFINITY);
+        }
+        float mx;
+        {
+          auto x = [&](int f) { return __uint_as_float(sr[f >> 5][f & 31]); };
+          float pm[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) pm[k] = fmaxf(x(k), x(k + 8));
+#pragma unroll
+          for (int f = 16; f < 128; f += 16)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) pm[k] = fmax3(pm[k], x(f + k), x(f + 8 + k));
+          mx = fmax3(fmax3(pm[0], pm[1], pm[2]), fmax3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7]));
+        }
+        const float m_new = fmaxf(m_ref, mx * a.scale_log2);
+        float alpha = 1.f;
+        bool rescale_warp = false;
+        if (j == 0) {
+          m_ref = m_new;
+        } else {
+          const bool need = m_new > m_ref + kPfRescale;
+          rescale_warp = __any_sync(0xffffffffu, need);
+          if (need) {
+            alpha = ex2(m_ref - m_new);
+            m_ref = m_new;
+          }
+        }
+        const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;
+        const float2 sc2 = make_float2(a.scale_log2, a.scale_log2), nm2 = make_float2(neg_m, neg_m);
+        uint32_t pk[4][16];
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float2 y = ffma2(make_float2(__uint_as_float(sr[c][2 * e]), __uint_as_float(sr[c][2 * e + 1])), sc2, nm2);
+            const float2 p = make_float2(ex2(y.x), ex2(y.y));
+            pk[c][e] = PE::pack(p.x, p.y);
+            sum[e & 1] = fadd2(sum[e & 1], p);
+          }
+          if constexpr (!C::EARLY_S) tmem_st16(tP + c * 16, pk[c]);
+        }
+        if constexpr (C::EARLY_S) {
+          // P_t V of the step before must be done before its P_t and O_t change.
+          if (j > 0 && !(ok = mbar_wait_warp(&bars->pv_done[t], (cs - 1) & 1, wc))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_st16(tP + c * 16, pk[c]);
+        }
+        if (rescale_warp) {
+          // d = 128: S_t of this step was issued after P_t V of the last one.
+#pragma unroll(D == 128 ? 1 : D / 32)
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o_r[32];
+            tmem_ld32(tO + c * 32, o_r);
+            tmem_wait_ld();
+            tmem_reg_fence(o_r);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o_r[e] = __float_as_uint(__uint_as_float(o_r[e]) * alpha);
+            tmem_st32(tO + c * 32, o_r);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive_warp(&bars->p_full[t]);
+        const float2 s2 = fadd2(sum[0], sum[1]);
+        le = le * alpha + (s2.x + s2.y);
+        if constexpr (!kConvertV) {
+          float2 rb[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) rb[e & 1] = PE::add_pair(pk[c][e], rb[e & 1]);
+          const float2 rbs = fadd2(rb[0], rb[1]);
+          lb = lb * alpha + (rbs.x + rbs.y);
+        }
+      }
+      // ---------------------------------------------------------- the piece's end
+      if (ok && n > 0) ok = mbar_wait_warp(&bars->o_full[t], co & 1, wc);
+      if (!ok) break;
+      if (n > 0) {
+        ++co;
+        tc_fence_after();
+      }
+      const float l = kConvertV ? le : lb;
+      // No visible key: 0 and -inf.  A NaN among the scores makes the sum NaN.
+      const float inv_l = l == 0.f ? 0.f : 1.f / l;
+      const float L = le == 0.f ? -INFINITY : (m_ref + log2f(le)) * 0.6931471805599453f;
+      const bool live = row_tok < TT && tok0 + row_tok < pc.tok0 + pc.ntok;
+      const bool whole = pc.whole();
+      const long long prow = (static_cast<long long>(blockIdx.x) * 2 + pc.slot()) * kPagedRows + t * 128 + row;
+      const int grow = pc.s.row0 + tok0 + row_tok, head = pc.h * G + row_head;
+      T* orow = static_cast<T*>(a.o) + grow * a.so.n + head * a.so.h;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o_r[32];
+        if (n > 0) {
+          tmem_ld32(tO + c * 32, o_r);
+          tmem_wait_ld();
+          tmem_reg_fence(o_r);
+        }
+        float v[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] = l == 0.f || n == 0 ? 0.f : __uint_as_float(o_r[e]) * inv_l;
+        if (live && whole) {
+          uint4* dst = reinterpret_cast<uint4*>(orow + c * 32);
+#pragma unroll
+          for (int v4 = 0; v4 < 4; ++v4)
+            dst[v4] = make_uint4(E::pack(v[8 * v4], v[8 * v4 + 1]), E::pack(v[8 * v4 + 2], v[8 * v4 + 3]),
+                                 E::pack(v[8 * v4 + 4], v[8 * v4 + 5]), E::pack(v[8 * v4 + 6], v[8 * v4 + 7]));
+        } else if (live && n > 0) {
+          float4* dst = reinterpret_cast<float4*>(a.part_o + prow * D + c * 32);
+#pragma unroll
+          for (int v4 = 0; v4 < 8; ++v4) dst[v4] = make_float4(v[4 * v4], v[4 * v4 + 1], v[4 * v4 + 2], v[4 * v4 + 3]);
+        }
+      }
+      if (n > 0) {
+        tc_fence_before();
+        mbar_arrive_warp(&bars->o_free[t]);
+      }
+      if (live) {
+        if (whole) a.lse[static_cast<long long>(head) * a.nt.total + grow] = L;
+        else a.part_lse[prow] = L;
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 9) tmem_dealloc(tmem, C::TM_COLS);
+}
+
+namespace {
+
+template <typename T, int D>
+cudaError_t launch_t(const PagedArgs& a, cudaStream_t stream) {
+  using C = PfCfg<D>;
+  auto kern = paged_fwd_kernel<T, D>;
+  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), C::SMEM_BYTES, a.device);
+  if (e != cudaSuccess) return e;
+  kern<<<a.ctas, C::THREADS, C::SMEM_BYTES, stream>>>(*a.tm_q, *a.tm_k, *a.tm_v, a);
+  return note_cuda(cudaGetLastError(), "paged forward kernel launch");
+}
+
+}  // namespace
+
+cudaError_t launch_paged_fwd(const PagedArgs& a, cudaStream_t stream) {
+  if (a.dtype == kF16) return a.d == 64 ? launch_t<__half, 64>(a, stream) : launch_t<__half, 128>(a, stream);
+  return a.d == 64 ? launch_t<__nv_bfloat16, 64>(a, stream) : launch_t<__nv_bfloat16, 128>(a, stream);
+}
+
+}  // namespace exattn

@@ -16,7 +16,7 @@ import math
 
 import torch
 
-from ._lib import _DTYPES, _check, _device_of, _packed3, _ptr, _stream, _view4, Strides, load
+from ._lib import _DTYPES, _check, _device_of, _packed3, _ptr, _stream, _view4, Strides, load, watchdog_check, watchdog_poll
 
 _NO_STRIDES = Strides(0, 0, 0)
 
@@ -218,6 +218,59 @@ def attn_cache_append(k, v, k_cache, v_cache, page_table, seqlens, cu_seqlens=No
           skc, _ptr(v_cache), svc, Hk, P, ps, _ptr(page_table), page_table.stride(0) if B > 1 else page_table.shape[1],
           page_table.shape[1], _ptr(seqlens), _ptr(cu_seqlens), B, total, d, _ptr(inv_freq), rot, int(bool(interleaved)),
           float(factor))
+
+
+def attn_fwd_paged_workspace_size(B: int, Hq: int, Hkv: int, total: int, max_seqlen_q: int, max_seqlen_k: int,
+                                  d: int) -> int:
+    """C ``attn_fwd_paged_workspace_size`` (bytes; 0 for invalid sizes)."""
+    return int(load().attn_fwd_paged_workspace_size(B, Hq, Hkv, total, max_seqlen_q, max_seqlen_k, d))
+
+
+def attn_fwd_paged(q, k_cache, v_cache, o, lse, page_table, seqlens, cu_seqlens, max_seqlen_q: int, max_seqlen_k: int,
+                   causal: bool, scale: float, workspace, stream=None, window: int = 0) -> None:
+    """C ``attn_fwd_paged``: q, o packed [total, Hq, d], lse fp32 [Hq, total]; the new
+    tokens are the last positions of their sequences in the cache."""
+    (total, Hq, d), dt, sq = _packed3(q, "q")
+    P, Hkv, ps, skc, svc = _cache(k_cache, v_cache, dt, d)
+    vo = _packed3(o, "o")
+    if vo[:2] != ((total, Hq, d), dt):
+        raise ValueError("o shape/dtype differs from q")
+    if lse.dtype != torch.float32 or tuple(lse.shape) != (Hq, total) or not lse.is_contiguous():
+        raise ValueError("lse must be contiguous float32 [Hq, total]")
+    B = _tables(page_table, seqlens, cu_seqlens, total)
+    dev = _device_of(q, k_cache, v_cache, o, lse, page_table, seqlens, cu_seqlens, workspace)
+    if total == 0:
+        return
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _call("attn_fwd_paged", dev, stream, dt, _ptr(q), sq, _ptr(k_cache), skc, _ptr(v_cache), svc, _ptr(o), vo[2], _ptr(lse), P,
+          ps, _ptr(page_table), page_table.stride(0) if B > 1 else page_table.shape[1], page_table.shape[1], _ptr(seqlens),
+          _ptr(cu_seqlens), B, Hq, Hkv, total, int(max_seqlen_q), int(max_seqlen_k), d, int(bool(causal)), int(window),
+          float(scale), _ptr(workspace), ws_bytes)
+
+
+def forward_paged(q, k_cache, v_cache, page_table, seqlens, cu_seqlens=None, max_seqlen_q: int | None = None,
+                  max_seqlen_k: int | None = None, causal: bool = True, scale: float | None = None, stream=None,
+                  window: int = 0):
+    """Attention of new tokens over a paged cache: q packed [total, Hq, d], the
+    cache and tables as in the module's head; returns O (like q) and lse fp32
+    [Hq, total].  ``max_seqlen_q`` defaults to total / B without ``cu_seqlens`` and
+    to total with them, ``max_seqlen_k`` to the table's capacity: give them where
+    they are known, they size the work's split."""
+    total, Hq, d = q.shape
+    B = page_table.shape[0]
+    if max_seqlen_q is None:
+        max_seqlen_q = total if cu_seqlens is not None else total // max(B, 1)
+    if max_seqlen_k is None:
+        max_seqlen_k = page_table.shape[1] * k_cache.shape[2]
+    watchdog_check(q.device)
+    o = torch.empty_like(q)
+    lse = torch.empty((Hq, total), dtype=torch.float32, device=q.device)
+    nbytes = attn_fwd_paged_workspace_size(B, Hq, k_cache.shape[1], total, max_seqlen_q, max_seqlen_k, d)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    attn_fwd_paged(q, k_cache, v_cache, o, lse, page_table, seqlens, cu_seqlens, max_seqlen_q, max_seqlen_k, causal,
+                   d ** -0.5 if scale is None else scale, ws, stream, window)
+    watchdog_poll(q.device, stream)
+    return o, lse
 
 
 def _pages(x, name: str):

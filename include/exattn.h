@@ -413,6 +413,41 @@ int attn_cache_append(int dtype, const void* q, exattn_strides q_strides, void* 
                       int rot_dim, int interleaved, float factor, void* stream);
 
 /*
+ * attn_fwd_paged -- attention of new tokens over a paged cache: O = softmax(
+ *   scale Q K^T + masks) V and its logsumexp, K and V the cache's rows of
+ *   each sequence, the new tokens being its last positions (bottom-right
+ *   alignment, as attn_fwd_decode): chunks of prompts, single next tokens, or
+ *   both in one call.
+ *   q, o  : [total, Hq, d] packed (b_stride unused).  Query heads
+ *     h G .. h G + G - 1 share key head h, G = Hq / Hkv (Hq a multiple of
+ *     Hkv, else EXATTN_ERR_SHAPE; G <= 128, else EXATTN_ERR_UNSUPPORTED).
+ *   lse   : fp32 [Hq, total].
+ *   causal, window : as for the _ex calls, counted from a token's position
+ *     seqlens[b] minus the new tokens of b, and on.  A query that sees no key
+ *     (an empty sequence, a position below 0) gets O = 0 and lse = -inf.
+ *   max_seqlen_q, max_seqlen_k : at least the largest count of new tokens and the
+ *     largest length; a sequence beyond them is cut off (its further rows are
+ *     not written, its further keys not seen).
+ *   Whatever is stored behind a sequence's last row -- NaN included -- does not
+ *   reach its output; a row on a page number outside the pool reads as zeros.
+ *   The keys of the whole batch are shared evenly between the SMs, whatever
+ *   its lengths, and the sequences that fall on several of them are joined by
+ *   a second kernel from the workspace (attn_fwd_paged_workspace_size bytes,
+ *   16-byte aligned; 0 for invalid sizes; its contents need not be kept, and
+ *   calls that may run at the same time need one each).  Results do not vary
+ *   from run to run.  Arithmetic as attn_fwd (V entries beyond +-65504 are not
+ *   supported); lse is formed from the unrounded weights.
+ *   H total and the other sizes below 2^31, lengths below 2^30.
+ */
+size_t attn_fwd_paged_workspace_size(int B, int Hq, int Hkv, int total, int max_seqlen_q, int max_seqlen_k, int d);
+int attn_fwd_paged(int dtype, const void* q, exattn_strides q_strides, const void* k_cache, exattn_strides kc_strides,
+                   const void* v_cache, exattn_strides vc_strides, void* o, exattn_strides o_strides, float* lse,
+                   int num_pages, int page_size, const int* page_table, long long table_stride, int max_pages,
+                   const int* seqlens, const int* cu_seqlens, int B, int Hq, int Hkv, int total, int max_seqlen_q,
+                   int max_seqlen_k, int d, int causal, int window, float scale, void* workspace,
+                   size_t workspace_bytes, void* stream);
+
+/*
  * attn_cache_copy -- page dst[i] of every slab becomes a copy of page src[i],
  *   for i in [0, n): the partly filled last page of a forked sequence, or the
  *   moves that compact a fragmented pool.
