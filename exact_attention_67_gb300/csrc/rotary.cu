@@ -17,9 +17,10 @@
 // The turned values are rounded once, to the output's type.
 //
 // A block takes a few consecutive tokens: it forms cos and sin of their
-// rot / 2 angles once, in shared memory, for all heads of Q and K; then
-// each thread turns items of 2 V elements (two 16-byte vectors at V = 8), four
-// items in flight.  Bound by memory traffic: every element is read once and
+// rot / 2 angles once, in shared memory, for all heads of Q and K; a thread
+// turns one item of 2 V elements (two 16-byte vectors at V = 8), whose cos and sin
+// it keeps, of every few heads, two items in flight, the first of them while the
+// angles are formed.  Bound by memory traffic: every element is read once and
 // written once.  V is the widest vector that divides rot / 2 (interleaved: half
 // of an item's run), so rot a multiple of 16 moves 16-byte vectors.
 #include "paged.cuh"
@@ -31,6 +32,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxTok = 8;  // tokens a block at most
+constexpr int kBatch = 2;   // items a thread has in flight
+static_assert(kMaxTok <= kThreads / 32, "a warp looks up each token");
 
 template <int V>
 struct Vec;
@@ -43,25 +46,21 @@ struct Vec<2> { using type = uint32_t; };
 template <>
 struct Vec<1> { using type = uint16_t; };
 
-template <typename T>
-__device__ __forceinline__ float to_f(T x);
-template <>
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
-template <>
-__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
-template <typename T>
-__device__ __forceinline__ T from_f(float x);
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f(float x) { return __float2bfloat16_rn(x); }
-template <>
-__device__ __forceinline__ __half from_f(float x) { return __float2half_rn(x); }
+// One item: two vectors of V elements, as 32-bit words of two (V = 1: one
+// element in a word's low half).
+template <int V>
+struct Item {
+  static constexpr int W = V > 1 ? V / 2 : 1;
+  union Half {
+    typename Vec<V>::type v;
+    uint32_t w[W];
+    __device__ Half() : w{} {}
+  } p1, p2;
+};
 
-// V elements of one type in registers.
-template <typename T, int V>
-union Pack {
-  typename Vec<V>::type v;
-  T e[V];
-  __device__ Pack() {}
+template <int Q>
+struct alignas(4 * Q) Angles {
+  float a[Q];
 };
 
 // What a block knows of each of its tokens.
@@ -83,10 +82,11 @@ __device__ __forceinline__ int sequence_of(const int* cu, int B, int t, int lane
 }
 
 template <typename T, int D, int V, bool IL, bool APPEND>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryArgs a, int tok_per_block,
-                                                          long long tokens, unsigned head_magic) {
+__global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_constant__ RotaryArgs a, int tok_per_block,
+                                                          long long tokens) {
   constexpr int S = D / (2 * V);  // items a head
-  __shared__ float2 cs[kMaxTok * (D / 2)];
+  constexpr int Q = V < 4 ? V : 4;  // angles a vector load
+  __shared__ alignas(16) float cos_s[kMaxTok * (D / 2)], sin_s[kMaxTok * (D / 2)];
   __shared__ Token tk[kMaxTok];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const long long t0 = static_cast<long long>(blockIdx.x) * tok_per_block;
@@ -142,101 +142,112 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
     if (lane == 0) tk[warp] = k;
   }
   __syncthreads();
+
+  // This thread: item `slot` of the heads hl, hl + HL, ... of one token.
+  using VT = typename Vec<V>::type;
+  using I = Item<V>;
   const int half = a.inv_freq ? a.rot >> 1 : 0;
-  for (int x = tid; x < nt * half; x += kThreads) {
-    const int t = x / half, f = x - t * half;
+  const int heads = a.Hq + a.Hk + (APPEND ? a.Hk : 0);
+  const int slot = tid % S, t = tid / S & (tok_per_block - 1), hl = tid / S / tok_per_block;
+  const int HL = kThreads / S / tok_per_block;
+  const bool live = t < nt;
+  const Token k = live ? tk[t] : Token{};
+  const int pairs0 = slot * V;
+  const bool turned = pairs0 < half;
+  // The item's two vectors: its pairs' halves, or (interleaved, and past the
+  // turned part) 2 V consecutive elements.  V is copied whole: the same places.
+  const int e1 = !IL && turned ? pairs0 : 2 * pairs0;
+  const int e2 = !IL && turned ? pairs0 + half : 2 * pairs0 + V;
+  I x[kBatch];
+  T* dst[kBatch];
+  auto load = [&](int h, I& x, T*& dst) {
+    dst = nullptr;
+    if (!live || h >= heads) return;
+    const T* src;
+    if (h < a.Hq) {
+      if (!(k.flags & 1)) return;
+      src = static_cast<const T*>(a.q) + (k.q + h * a.sq.h);
+      dst = static_cast<T*>(a.q_out) + (k.qo + h * a.sqo.h);
+    } else {
+      if (!(k.flags & 2)) return;
+      const int g = h - a.Hq;
+      if (!APPEND || g < a.Hk) {
+        src = static_cast<const T*>(a.k) + (k.k + g * a.sk.h);
+        dst = static_cast<T*>(a.k_out) + (k.ko + g * a.sko.h);
+      } else {
+        src = static_cast<const T*>(a.v) + (k.v + (g - a.Hk) * a.sv.h);
+        dst = static_cast<T*>(a.v_out) + (k.vo + (g - a.Hk) * a.svo.h);
+      }
+    }
+    x.p1.v = *reinterpret_cast<const VT*>(src + e1);
+    x.p2.v = *reinterpret_cast<const VT*>(src + e2);
+  };
+  // The first items are on their way while the angles are formed.
+#pragma unroll
+  for (int u = 0; u < kBatch; ++u) load(hl + u * HL, x[u], dst[u]);
+  for (int i = tid; i < nt * half; i += kThreads) {
+    const int tt = i / half, f = i - tt * half;
     double turns = a.inv_freq[f] * 0.15915494309189535;  // 1 / 2 pi
     turns -= floor(turns);
     const unsigned long long F = __double2ull_rn(turns * 18446744073709551616.0);
-    const unsigned long long angle = static_cast<unsigned long long>(static_cast<long long>(tk[t].pos)) * F;
+    const unsigned long long angle = static_cast<unsigned long long>(static_cast<long long>(tk[tt].pos)) * F;
     float s, c;
     sincospif(static_cast<float>(static_cast<int>(angle >> 32)) * 4.656612873077393e-10f, &s, &c);  // 2^-31: half turns
-    cs[t * (D / 2) + f] = make_float2(c * a.factor, (a.inverse ? -s : s) * a.factor);
+    // Runs of Q angles of neighbouring items side by side: the items' vector
+    // loads below then meet no bank twice.
+    const int at = tt * (D / 2) + f % V / Q * (S * Q) + f / V * Q + f % Q;
+    cos_s[at] = c * a.factor;
+    sin_s[at] = (a.inverse ? -s : s) * a.factor;
   }
   __syncthreads();
-
-  using VT = typename Vec<V>::type;
-  const int heads = a.Hq + a.Hk + (APPEND ? a.Hk : 0);
-  const int items = nt * heads * S;
-  constexpr int U = 4;
-  for (int x0 = tid; x0 < items; x0 += U * kThreads) {
-    Pack<T, V> p1[U], p2[U];
-    T* dst[U];
-    int e1[U], e2[U], tok[U];
-    bool turn[U];
+  float c[V] = {}, s[V] = {};
+  if (turned) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int x = x0 + u * kThreads;
-      dst[u] = nullptr;
-      if (x >= items) continue;
-      const int slot = x % S, row = x / S;
-      const int t = static_cast<int>(__umulhi(static_cast<unsigned>(row), head_magic));
-      int h = row - t * heads;
-      const Token& k = tk[t];
-      const T* src;
-      turn[u] = true;
-      if (h < a.Hq) {
-        if (!(k.flags & 1)) continue;
-        src = static_cast<const T*>(a.q) + k.q + h * a.sq.h;
-        dst[u] = static_cast<T*>(a.q_out) + k.qo + h * a.sqo.h;
-      } else {
-        if (!(k.flags & 2)) continue;
-        h -= a.Hq;
-        if (!APPEND || h < a.Hk) {
-          src = static_cast<const T*>(a.k) + k.k + h * a.sk.h;
-          dst[u] = static_cast<T*>(a.k_out) + k.ko + h * a.sko.h;
-        } else {
-          h -= a.Hk;
-          src = static_cast<const T*>(a.v) + k.v + h * a.sv.h;
-          dst[u] = static_cast<T*>(a.v_out) + k.vo + h * a.svo.h;
-          turn[u] = false;
-        }
+    for (int i = 0; i < V / Q; ++i) {
+      const int at = t * (D / 2) + i * (S * Q) + slot * Q;
+      const Angles<Q> cc = *reinterpret_cast<const Angles<Q>*>(&cos_s[at]);
+      const Angles<Q> ss = *reinterpret_cast<const Angles<Q>*>(&sin_s[at]);
+#pragma unroll
+      for (int j = 0; j < Q; ++j) {
+        c[i * Q + j] = cc.a[j];
+        s[i * Q + j] = ss.a[j];
       }
-      // The item's two vectors: a pair's halves, or (interleaved, and past the
-      // turned part) 2 V consecutive elements.
-      const int pairs0 = slot * V;
-      turn[u] = turn[u] && pairs0 < half;
-      e1[u] = !IL && turn[u] ? pairs0 : 2 * pairs0;
-      e2[u] = !IL && turn[u] ? pairs0 + half : 2 * pairs0 + V;
-      tok[u] = t * (D / 2) + pairs0;
-      p1[u].v = *reinterpret_cast<const VT*>(src + e1[u]);
-      p2[u].v = *reinterpret_cast<const VT*>(src + e2[u]);
     }
+  }
+  using E = Elem<T>;
+  for (int h = hl; h < heads; h += kBatch * HL) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
+    for (int u = 0; u < kBatch; ++u) {
       if (dst[u] == nullptr) continue;
-      if (turn[u]) {
-        if constexpr (!IL) {
+      I& y = x[u];
+      const bool turn = turned && (!APPEND || h + u * HL < a.Hq + a.Hk);
+      if (turn) {
+        if constexpr (V == 1) {
+          const float x1 = E::unpack(y.p1.w[0]).x, x2 = E::unpack(y.p2.w[0]).x;
+          y.p1.w[0] = E::pack(x1 * c[0] - x2 * s[0], 0.f);
+          y.p2.w[0] = E::pack(x2 * c[0] + x1 * s[0], 0.f);
+        } else if constexpr (!IL) {
 #pragma unroll
-          for (int e = 0; e < V; ++e) {
-            const float2 w = cs[tok[u] + e];
-            const float x1 = to_f<T>(p1[u].e[e]), x2 = to_f<T>(p2[u].e[e]);
-            p1[u].e[e] = from_f<T>(x1 * w.x - x2 * w.y);
-            p2[u].e[e] = from_f<T>(x2 * w.x + x1 * w.y);
+          for (int i = 0; i < I::W; ++i) {
+            const float2 x1 = E::unpack(y.p1.w[i]), x2 = E::unpack(y.p2.w[i]);
+            const float2 cc = make_float2(c[2 * i], c[2 * i + 1]), ss = make_float2(s[2 * i], s[2 * i + 1]);
+            const float2 y1 = ffma2(x2, make_float2(-ss.x, -ss.y), fmul2(x1, cc)), y2 = ffma2(x1, ss, fmul2(x2, cc));
+            y.p1.w[i] = E::pack(y1.x, y1.y);
+            y.p2.w[i] = E::pack(y2.x, y2.y);
           }
         } else {
-          T e[2 * V];
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            e[i] = p1[u].e[i];
-            e[V + i] = p2[u].e[i];
-          }
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            const float2 w = cs[tok[u] + i];
-            const float x1 = to_f<T>(e[2 * i]), x2 = to_f<T>(e[2 * i + 1]);
-            e[2 * i] = from_f<T>(x1 * w.x - x2 * w.y);
-            e[2 * i + 1] = from_f<T>(x2 * w.x + x1 * w.y);
-          }
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            p1[u].e[i] = e[i];
-            p2[u].e[i] = e[V + i];
+          for (int i = 0; i < V; ++i) {  // pair i is one word
+            uint32_t& w = i < I::W ? y.p1.w[i] : y.p2.w[i - I::W];
+            const float2 z = E::unpack(w);
+            const float2 r = ffma2(make_float2(z.y, z.x), make_float2(-s[i], s[i]), fmul2(z, make_float2(c[i], c[i])));
+            w = E::pack(r.x, r.y);
           }
         }
       }
-      *reinterpret_cast<VT*>(dst[u] + e1[u]) = p1[u].v;
-      *reinterpret_cast<VT*>(dst[u] + e2[u]) = p2[u].v;
+      *reinterpret_cast<VT*>(dst[u] + e1) = y.p1.v;
+      *reinterpret_cast<VT*>(dst[u] + e2) = y.p2.v;
+      load(h + (kBatch + u) * HL, y, dst[u]);  // its successor, while the other item is turned
     }
   }
 }
@@ -244,14 +255,14 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
 template <typename T, int D, int V, bool IL>
 cudaError_t launch_t(const RotaryArgs& a, cudaStream_t stream) {
   const long long tokens = a.append ? a.nt.total : static_cast<long long>(a.B) * a.N;
-  const int heads = a.Hq + a.Hk + (a.append ? a.Hk : 0);
-  // Several tokens a block once that still leaves eight blocks an SM.
+  // Several tokens a block (a power of two, at most a block's rows of items)
+  // once that still leaves sixteen blocks an SM.
+  constexpr int kRows = kThreads / (D / (2 * V));
   int tok = 1;
-  while (tok < kMaxTok && tokens / (2 * tok) >= 152 * 8) tok *= 2;
+  while (tok < kMaxTok && tok < kRows && tokens / (2 * tok) >= 152 * 16) tok *= 2;
   const long long grid = (tokens + tok - 1) / tok;
-  const unsigned magic = static_cast<unsigned>(((1ull << 32) + heads - 1) / heads);
   auto kern = a.append ? rotary_kernel<T, D, V, IL, true> : rotary_kernel<T, D, V, IL, false>;
-  kern<<<static_cast<unsigned>(grid), kThreads, 0, stream>>>(a, tok, tokens, magic);
+  kern<<<static_cast<unsigned>(grid), kThreads, 0, stream>>>(a, tok, tokens);
   return note_cuda(cudaGetLastError(), "rotary kernel launch");
 }
 
