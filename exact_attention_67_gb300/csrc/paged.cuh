@@ -75,7 +75,9 @@ struct PagedArgs {
   int max_q, max_k;         // bounds of the new tokens and lengths of a sequence
   int causal, window;
   float scale_log2;
-  int tile_tokens;          // tokens of a query tile: 128 / G (forward), 16 / G (decode)
+  int tile_tokens;          // tokens of a query tile: 128 / G (forward), cols / G (decode)
+  int cols;                 // decode kernel: query columns, 4, 8, 16 or 32
+  int rows;                 // rows of a piece's partial results
   int ctas;                 // grid; the work's split follows from it (paged_sched.cuh)
   int unit_cost, min_chunk;
   float* part_o;            // [ctas][2][rows][d]
@@ -84,12 +86,12 @@ struct PagedArgs {
   unsigned* err;
   int device;
 };
-constexpr int kPagedDecodeCols = 16;  // unit rows of the decode kernel
+constexpr int kPagedDecodeCols = 32;  // query columns of the decode kernel at most
 constexpr int kPagedRows = 256;       // unit rows of the forward kernel: two query tiles
 cudaError_t launch_paged_decode(const PagedArgs& a, cudaStream_t stream);
 cudaError_t launch_paged_fwd(const PagedArgs& a, cudaStream_t stream);
-// Joins the pieces of the units that ended up on several CTAs (rows: a unit's).
-cudaError_t launch_paged_merge(const PagedArgs& a, int rows, cudaStream_t stream);
+// Joins the pieces of the units that ended up on several CTAs.
+cudaError_t launch_paged_merge(const PagedArgs& a, cudaStream_t stream);
 
 struct CopyArgs {
   char* pool;

@@ -216,7 +216,7 @@ constexpr int kSMs = 152;
 
 // How a paged attention is laid out on the GPU, from sizes alone.
 struct PagedPlan {
-  bool decode;
+  int cols;  // of the decode kernel, 0: the forward kernel
   int tile_tokens, ctas, rows, unit_cost, min_chunk;
   size_t plan_bytes, lse_bytes, total_bytes;
 };
@@ -225,12 +225,13 @@ PagedPlan paged_plan(int B, int Hq, int Hkv, int total, int max_q, int max_k, in
   PagedPlan p{};
   const int G = Hq / Hkv;
   max_q = std::min(max_q, total);
-  p.decode = static_cast<long long>(max_q) * G <= kPagedDecodeCols;
-  p.rows = p.decode ? kPagedDecodeCols : kPagedRows;
-  p.tile_tokens = (p.decode ? kPagedDecodeCols : 128) / G;
+  const long long need = static_cast<long long>(max_q) * G;
+  p.cols = need <= 4 ? 4 : need <= 8 ? 8 : need <= 16 ? 16 : need <= kPagedDecodeCols ? 32 : 0;
+  p.rows = p.cols ? std::max(p.cols, 16) : kPagedRows;
+  p.tile_tokens = (p.cols ? p.cols : 128) / G;
   p.unit_cost = 2;
   p.min_chunk = 6;
-  const int ut = p.decode ? p.tile_tokens : 2 * p.tile_tokens;
+  const int ut = p.cols ? p.tile_tokens : 2 * p.tile_tokens;
   // At most so many weights (paged_sched.cuh): units of full length.
   const double units = static_cast<double>(Hkv) * std::min<double>(static_cast<double>(B) * ((max_q + ut - 1) / ut),
                                                                    static_cast<double>(total) / ut + B);
@@ -323,6 +324,8 @@ extern "C" int attn_fwd_paged(int dtype, const void* q, exattn_strides sq, const
   a.window = std::min(window, 1 << 30);
   a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   a.tile_tokens = plan.tile_tokens;
+  a.cols = plan.cols;
+  a.rows = plan.rows;
   a.ctas = plan.ctas;
   a.unit_cost = plan.unit_cost;
   a.min_chunk = plan.min_chunk;
@@ -333,6 +336,6 @@ extern "C" int attn_fwd_paged(int dtype, const void* q, exattn_strides sq, const
   a.err = err;
   a.device = dev;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if ((plan.decode ? launch_paged_decode(a, st) : launch_paged_fwd(a, st)) != cudaSuccess) return EXATTN_ERR_CUDA;
-  return launch_paged_merge(a, plan.rows, st) == cudaSuccess ? EXATTN_OK : EXATTN_ERR_CUDA;
+  if ((plan.cols ? launch_paged_decode(a, st) : launch_paged_fwd(a, st)) != cudaSuccess) return EXATTN_ERR_CUDA;
+  return launch_paged_merge(a, st) == cudaSuccess ? EXATTN_OK : EXATTN_ERR_CUDA;
 }

@@ -1,22 +1,29 @@
-// paged_decode.cu -- attention of few query rows (at most 16 a key head) over a
+// paged_decode.cu -- attention of few query rows (at most 32 a key head) over a
 // paged cache, for sm_103a.
 //
 // The products run as in the dense decode kernel (decode.cu): keys on the MMA's
-// M side, S^T = K_j Q^T with 16 query columns, the online softmax down each
+// M side, S^T = K_j Q^T with 16 or 32 query columns, the online softmax down each
 // column, O^T += V_j^T P^T.  The columns are the query heads that share the key
 // head, times the new tokens (column c is token c / G, head c % G), so K and V
 // are read once for all of them.  What differs:
 //   * one CTA an SM runs through its chunk of the batch's keys (paged_sched.cuh),
 //     unit after unit, with the loads of the next unit in flight while the
 //     last one ends: Q and O^T have two buffers;
+//   * two elementwise warpgroups take key tiles in turn, each with its own
+//     references, sums and O^T accumulator, joined at the unit's end.  One tile's
+//     work is a chain of latencies (TMEM load, barrier, exponentials, store) of
+//     over a microsecond at 8 columns; with one warpgroup it was the bound
+//     (B48 Hq32 Hk4 ctx to 16384: 160 us; B16 x 5 tokens Hq24 Hk8 d64: 58);
+//   * the columns' count, rounded up, is a template argument: straight-line code;
 //   * a 128-key tile is gathered page by page: one TMA box a page, issued by one
 //     lane each, the page numbers read one tile ahead.  Pages past the last visible
 //     key are not read, whatever the table says there;
 //   * the stored rows behind a sequence's end may hold anything: scores there are
 //     replaced (not added to) by -inf, and V rows are zeroed in shared memory
 //     by the converting warps, so that 0 * NaN never meets an accumulator;
-//   * the logsumexp comes from a sum of the unrounded weights; O is
-//     normalised by the sum of the rounded ones that the product used.
+//   * the logsumexp comes from a sum of the unrounded weights, and so does
+//     bf16's O (P's f16 rounding, 2^-11 of a weight, is far below the output's);
+//     f16's O is normalised by the sum of the rounded weights.
 // d = 64: V^T has 64 rows and the MMA takes 128, so the second half reads the
 // shared memory behind the tile; those accumulator rows are never read.
 #include "paged.cuh"
@@ -27,15 +34,16 @@ namespace exattn {
 
 namespace {
 
-template <int D>
+template <int D, int NC>
 struct PdCfg {
   static constexpr int BN = kKeyTile;
-  static constexpr int NQ = kPagedDecodeCols;
+  static constexpr int NQ = NC < 16 ? 16 : NC;  // the MMA's N
   static constexpr int NCHUNK = D / 64;
   static constexpr int KV_CHUNK = BN * 128;
   static constexpr int KV_TILE = NCHUNK * KV_CHUNK;
   static constexpr int Q_CHUNK = NQ * 128;
   static constexpr int Q_TILE = NCHUNK * Q_CHUNK;
+  static constexpr int QBUF = NC == 32 ? 1 : 2;  // Q tiles in shared memory
   static constexpr int P_CHUNK = NQ * 128;
   static constexpr int P_TILE = 2 * P_CHUNK;
   static constexpr int STAGES = D == 128 ? 3 : 6;  // 192 KB of K and V
@@ -43,14 +51,20 @@ struct PdCfg {
   static constexpr int OFF_V = 0;
   static constexpr int OFF_K = OFF_V + STAGES * KV_TILE;
   static constexpr int OFF_Q = OFF_K + STAGES * KV_TILE;
-  static constexpr int OFF_P = OFF_Q + 2 * Q_TILE;
-  static constexpr int OFF_RED = OFF_P + 2 * P_TILE;  // maxima [2][4][16], sums [2][4][16], bits [2][4]
-  static constexpr int OFF_BAR = OFF_RED + 4 * 4 * NQ * 4 + 2 * 4 * 4;
+  static constexpr int OFF_P = OFF_Q + QBUF * Q_TILE;
+  // Per warpgroup maxima [2][4][NC]; by the unit's parity: references
+  // [2][2][NC], sums of unrounded and rounded weights [2][2][2][4][NC].
+  static constexpr int OFF_RED = OFF_P + 2 * P_TILE;
+  static constexpr int OFF_BAR = OFF_RED + (8 + 4 + 32) * NC * 4;
   static constexpr int SMEM_BYTES = OFF_BAR + 512 + 1024;
   static_assert(SMEM_BYTES <= 232448, "over the 227 KB shared-memory limit");
-  static constexpr int PRODUCER_WARP = 4, MMA_WARP = 5;
-  static constexpr int THREADS = 256;
-  static constexpr uint32_t TM_S = 0, TM_O = 2 * NQ, TM_COLS = 64;  // two S^T and two O^T buffers
+  static constexpr int PRODUCER_WARP = 8, MMA_WARP = 9, READY_WARP = 10;
+  // Warps that make V ready: two leave the threads 168 registers, which the wider
+  // forms need.
+  static constexpr int READY_WARPS = NC <= 8 ? 4 : 2;
+  static constexpr int THREADS = 32 * (READY_WARP + READY_WARPS);
+  // Two S^T buffers, and O^T by warpgroup and by the unit's parity.
+  static constexpr uint32_t TM_S = 0, TM_O = 2 * NQ, TM_COLS = NQ == 16 ? 128 : 256;
 };
 
 template <int STAGES>
@@ -59,7 +73,7 @@ struct PdBars {
   uint64_t kv_full[STAGES], kv_empty[STAGES], v_ready[STAGES];
   uint64_t s_full[2], s_free[2], p_full[2], p_free[2];
   uint64_t o_full[2], o_free[2];
-  uint64_t pv_done, mma_done;
+  uint64_t mma_done;
   PagedCursor start;
   uint32_t tmem_base;
   int abort;
@@ -71,23 +85,79 @@ __device__ __forceinline__ uint32_t pd_bf16x2_to_f16x2(uint32_t w) {
   return pack_f16x2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
-__device__ __forceinline__ void pd_reg_fence16(uint32_t (&r)[16]) {
-  asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
-               "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),
-               "+r"(r[14]), "+r"(r[15]));
+// N columns of TMEM for this lane, loaded and waited for (the empty statement
+// keeps every use of them behind the wait, as tmem_reg_fence).
+template <int N>
+__device__ __forceinline__ void tmem_read(uint32_t at, uint32_t (&r)[N]) {
+  if constexpr (N == 2) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(at));
+  } else if constexpr (N == 4) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(at));
+  } else if constexpr (N == 8) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(at));
+  } else if constexpr (N == 16) {
+    tmem_ld16(at, r);
+  } else {
+    tmem_ld32(at, r);
+  }
+  tmem_wait_ld();
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_write(uint32_t at, const uint32_t (&r)[N]) {
+  if constexpr (N == 4) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+                 "r"(r[3])
+                 : "memory");
+  } else if constexpr (N == 8) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+  } else if constexpr (N == 16) {
+    tmem_st16(at, r);
+  } else {
+    tmem_st32(at, r);
+  }
+  tmem_wait_st();
+}
+
+// Barrier `id` of `threads` threads that also tells whether any of them said yes.
+__device__ __forceinline__ bool bar_any(int id, int threads, bool yes) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(static_cast<uint32_t>(yes)), "r"(id), "r"(threads)
+      : "memory");
+  return any != 0;
+}
+
+// Maximum over a warp (NaN only if all are).
+__device__ __forceinline__ float warp_max(float x) {
+  float m;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x));
+  return m;
 }
 
 }  // namespace
 
-template <typename T, int D>
-__global__ void __launch_bounds__(256, 1)
+template <typename T, int D, int NC>
+__global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PagedArgs a) {
-  using C = PdCfg<D>;
+  using C = PdCfg<D, NC>;
   using E = Elem<T>;
   using PE = Elem<__half>;
   using Bars = PdBars<C::STAGES>;
   constexpr bool kConvertV = E::kFmt != PE::kFmt;
+  constexpr bool kRounded = !kConvertV;  // O normalised by the rounded weights' sum
   constexpr int NQ = C::NQ, BN = C::BN;
   static_assert(sizeof(Bars) <= 512, "barrier block too large");
   extern __shared__ uint8_t smem_raw[];
@@ -114,14 +184,13 @@ __global__ void __launch_bounds__(256, 1)
       mbar_init(&bars->p_full[b], 4);
       mbar_init(&bars->p_free[b], 1);
       mbar_init(&bars->o_full[b], 1);
-      mbar_init(&bars->o_free[b], 4);
+      mbar_init(&bars->o_free[b], 8);
     }
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(&bars->kv_full[s], 1);
       mbar_init(&bars->kv_empty[s], 1);
-      mbar_init(&bars->v_ready[s], 2);
+      mbar_init(&bars->v_ready[s], C::READY_WARPS);
     }
-    mbar_init(&bars->pv_done, 1);
     mbar_init(&bars->mma_done, 1);
     bars->abort = 0;
     fence_barrier_init();
@@ -130,6 +199,11 @@ __global__ void __launch_bounds__(256, 1)
     tmem_alloc(&bars->tmem_base, C::TM_COLS);
     tmem_relinquish();
   }
+  // Rows of Q past the unit's box are never loaded: zero, so that their columns'
+  // scores are.
+  for (int i = threadIdx.x; i < C::QBUF * C::Q_TILE / 16; i += C::THREADS)
+    reinterpret_cast<uint4*>(smem + C::OFF_Q)[i] = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -155,8 +229,8 @@ __global__ void __launch_bounds__(256, 1)
     bool ok = true;
     while (ok && cur.next(a, UT, seq, &pc)) {
       if (pc.t_hi == pc.t_lo) continue;
-      const int qb = seg & 1;
-      if (seg >= 2 && !(ok = mbar_wait_warp(&bars->q_empty[qb], ((seg >> 1) - 1) & 1, wc))) break;
+      const int qb = seg % C::QBUF;
+      if (seg >= C::QBUF && !(ok = mbar_wait_warp(&bars->q_empty[qb], (seg / C::QBUF - 1) & 1, wc))) break;
       if (lane == 0) {
         mbar_arrive_expect_tx(&bars->q_full[qb], q_bytes);
         for (int c = 0; c < C::NCHUNK; ++c)
@@ -191,7 +265,8 @@ __global__ void __launch_bounds__(256, 1)
     __syncwarp();
     if (lane == 0 && *reinterpret_cast<volatile int*>(&bars->abort)) {
       // Never leave a copy in flight into shared memory this CTA is about to release.
-      for (int i = max(0, seg - 2); i < seg; ++i) mbar_wait_drain(&bars->q_full[i & 1], (i >> 1) & 1, a.err);
+      for (int i = max(0, seg - C::QBUF); i < seg; ++i)
+        mbar_wait_drain(&bars->q_full[i % C::QBUF], (i / C::QBUF) & 1, a.err);
       for (int j = max(0, st - C::STAGES); j < st; ++j)
         mbar_wait_drain(&bars->kv_full[j % C::STAGES], (j / C::STAGES) & 1, a.err);
     }
@@ -207,8 +282,8 @@ __global__ void __launch_bounds__(256, 1)
     const uint64_t v_desc = sdesc_sw128(smem_u32(smem + C::OFF_V), C::KV_CHUNK, 1024);
     auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_warp(bar, parity, wc); };
     int st = 0, seg = -1, j = 0, n = 0;
-    bool ok = true, prev = false, prev_first = false, prev_last = false;
-    int prev_seg = 0;
+    bool ok = true, prev = false, prev_last = false;
+    int prev_seg = 0, prev_j = 0;
     for (;;) {
       bool have = j < n;
       while (!have && cur.next(a, UT, seq, &pc)) {
@@ -217,7 +292,7 @@ __global__ void __launch_bounds__(256, 1)
         j = 0;
         ++seg;
         have = true;
-        if (!(ok = wait(&bars->q_full[seg & 1], (seg >> 1) & 1))) break;
+        if (!(ok = wait(&bars->q_full[seg % C::QBUF], (seg / C::QBUF) & 1))) break;
       }
       if (!ok) break;
       if (have) {
@@ -226,7 +301,7 @@ __global__ void __launch_bounds__(256, 1)
         if (st >= 2 && !(ok = wait(&bars->s_free[b], ((st - 2) >> 1) & 1))) break;
         tc_fence_after();
         if (elect_one()) {
-          const uint64_t qd = q_desc + (((seg & 1) * C::Q_TILE) >> 4);
+          const uint64_t qd = q_desc + (((seg % C::QBUF) * C::Q_TILE) >> 4);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t ko = ((kk >> 2) * C::KV_CHUNK + (kk & 3) * 32) >> 4;
@@ -234,7 +309,7 @@ __global__ void __launch_bounds__(256, 1)
             mma_ss(tmem + C::TM_S + b * NQ, k_desc + ((s * C::KV_TILE) >> 4) + ko, qd + qo, idesc_s, kk > 0);
           }
           mma_commit(&bars->s_full[b]);
-          if (j == n - 1) mma_commit(&bars->q_empty[seg & 1]);
+          if (j == n - 1) mma_commit(&bars->q_empty[seg % C::QBUF]);
         }
         __syncwarp();
       }
@@ -242,18 +317,17 @@ __global__ void __launch_bounds__(256, 1)
         const int sp = st - 1, ss = sp % C::STAGES, bp = sp & 1, ob = prev_seg & 1;
         if (!(ok = wait(&bars->p_full[bp], (sp >> 1) & 1))) break;
         if (!(ok = wait(&bars->v_ready[ss], (sp / C::STAGES) & 1))) break;
-        // The unit two before has been read out of this accumulator.
-        if (prev_first && prev_seg >= 2 && !(ok = wait(&bars->o_free[ob], ((prev_seg >> 1) - 1) & 1))) break;
+        // The unit two before has been read out of these accumulators.
+        if (prev_j == 0 && prev_seg >= 2 && !(ok = wait(&bars->o_free[ob], ((prev_seg >> 1) - 1) & 1))) break;
         tc_fence_after();
         if (elect_one()) {
           const uint64_t vd = v_desc + ((ss * C::KV_TILE) >> 4);
 #pragma unroll
           for (int kk = 0; kk < BN / 16; ++kk) {
             const uint32_t po = ((kk >> 2) * C::P_CHUNK + (kk & 3) * 32) >> 4;
-            mma_ss(tmem + C::TM_O + ob * NQ, vd + ((kk * 16 * 128) >> 4), p_desc + ((bp * C::P_TILE) >> 4) + po, idesc_o,
-                   (!prev_first || kk > 0) ? 1u : 0u);
+            mma_ss(tmem + C::TM_O + (ob * 2 + bp) * NQ, vd + ((kk * 16 * 128) >> 4), p_desc + ((bp * C::P_TILE) >> 4) + po,
+                   idesc_o, (prev_j >= 2 || kk > 0) ? 1u : 0u);
           }
-          mma_commit(&bars->pv_done);
           mma_commit(&bars->kv_empty[ss]);
           mma_commit(&bars->p_free[bp]);
           if (prev_last) mma_commit(&bars->o_full[ob]);
@@ -262,7 +336,7 @@ __global__ void __launch_bounds__(256, 1)
       }
       if (!have) break;
       prev = true;
-      prev_first = j == 0;
+      prev_j = j;
       prev_last = j == n - 1;
       prev_seg = seg;
       ++j;
@@ -273,10 +347,11 @@ __global__ void __launch_bounds__(256, 1)
     __syncwarp();
     if (lane == 0) mbar_wait_drain(&bars->mma_done, 0, a.err);
     __syncwarp();
-  } else if (warp >= 6) {
+  } else if (warp >= C::READY_WARP) {
     // ------------------------------------------------------------ V made ready
     // bf16 tiles to f16 in place; rows at or past the last visible key to zero.
-    const int ct = (warp - 6) * 32 + lane;
+    constexpr int RT = 32 * C::READY_WARPS;
+    const int ct = threadIdx.x - 32 * C::READY_WARP;
     int st = 0;
     bool ok = true;
     while (ok && cur.next(a, UT, seq, &pc)) {
@@ -286,13 +361,13 @@ __global__ void __launch_bounds__(256, 1)
         uint4* tile = reinterpret_cast<uint4*>(smem + C::OFF_V + s * C::KV_TILE);
         if (kConvertV || rows < BN) {
 #pragma unroll 8
-          for (int i = 0; i < C::KV_TILE / 16 / 64; ++i) {
-            uint4 x = tile[i * 64 + ct];
+          for (int i = 0; i < C::KV_TILE / 16 / RT; ++i) {
+            uint4 x = tile[i * RT + ct];
             if constexpr (kConvertV)
               x = make_uint4(pd_bf16x2_to_f16x2(x.x), pd_bf16x2_to_f16x2(x.y), pd_bf16x2_to_f16x2(x.z),
                              pd_bf16x2_to_f16x2(x.w));
-            if (((i * 64 + ct) >> 3 & (BN - 1)) >= rows) x = make_uint4(0, 0, 0, 0);
-            tile[i * 64 + ct] = x;
+            if (((i * RT + ct) >> 3 & (BN - 1)) >= rows) x = make_uint4(0, 0, 0, 0);
+            tile[i * RT + ct] = x;
           }
           fence_proxy_async_smem();
         }
@@ -301,172 +376,167 @@ __global__ void __launch_bounds__(256, 1)
     }
   } else {
     // ------------------------------------------------------------ elementwise (thread = key row / d row)
-    const int tid = threadIdx.x;
-    const uint32_t lane_bits = static_cast<uint32_t>(warp * 32) << 16;
-    // The warps' maxima and bits have two buffers, by the step's parity: one is
-    // written again two steps on, when every warp has met the next step's
-    // barrier and so has read it.
-    float* rs = red + 8 * NQ;                                     // [2][4][NQ]: rounded and unrounded sums
-    uint32_t* bits = reinterpret_cast<uint32_t*>(red + 16 * NQ);  // [2][4]
-    const uint32_t gm = 65536u / G + 1;                         // q / G == q * gm >> 16 for q < 16
-    int st = 0, seg = 0;
+    // Warpgroup w takes the steps of its parity: S^T, P^T buffer w.
+    const int w = warp >> 2, wl = warp & 3, tid = threadIdx.x & 127;
+    const uint32_t lane_bits = static_cast<uint32_t>(wl * 32) << 16;
+    float* mx = red + w * 4 * NC;                                // [4][NC]
+    const uint32_t gm = 65536u / G + 1;                          // q / G == q * gm >> 16 for q < 32, G <= 32
+    int st = 0, seg = 0, pieces = 0;
     bool ok = true;
-    // Every warp runs every step and meets the step's named barrier (id 1),
+    // Every warp of the group runs every step and meets its barriers (id 1 + w),
     // also after a bounded wait has given up: then without the work.
-    while (cur.next(a, UT, seq, &pc)) {
-      const int cols = pc.ntok * G, n = pc.t_hi - pc.t_lo;
+    for (; cur.next(a, UT, seq, &pc); ++pieces) {
+      const int cols = pc.ntok * G, n = pc.t_hi - pc.t_lo, ob = seg & 1;
       const int p0 = pc.s.off + pc.tok0, p1 = p0 + pc.ntok - 1;  // first and last position
-      float m_ref[NQ], lsum[NQ], lexact[NQ];
+      const uint32_t tO = tmem + lane_bits + C::TM_O + (ob * 2 + w) * NQ;
+      const uint32_t all = cols < 32 ? (1u << cols) - 1 : ~0u;
+      uint32_t none = all;  // columns that have seen no key: their reference is 0 so far
+      float m[NC], l[NC], lr[kRounded ? NC : 1];
 #pragma unroll
-      for (int q = 0; q < NQ; ++q) {
-        m_ref[q] = -INFINITY;
-        lsum[q] = lexact[q] = 0.f;
-      }
-      for (int j = 0; j < n; ++j, ++st) {
-        const int b = st & 1;
-        float* mx = red + b * 4 * NQ;  // [4][NQ]
-        float x[NQ];
-        uint32_t need = 0;
-        if (ok) ok = mbar_wait_warp(&bars->s_full[b], (st >> 1) & 1, wc);
+      for (int q = 0; q < NC; ++q) m[q] = l[q] = 0.f;
+#pragma unroll
+      for (int q = 0; q < (kRounded ? NC : 1); ++q) lr[q] = 0.f;
+      for (int j = (st ^ w) & 1; j < n; j += 2) {
+        const int s = st + j;
+        float y[NC];  // scores above the column's reference, log2 units
+        bool need = none != 0;
+        if (ok) ok = mbar_wait_warp(&bars->s_full[w], (s >> 1) & 1, wc);
         if (ok) {
           tc_fence_after();
-          uint32_t sv[NQ];
-          tmem_ld16(tmem + lane_bits + C::TM_S + b * NQ, sv);
-          tmem_wait_ld();
-          pd_reg_fence16(sv);
+          uint32_t sv[NC];
+          tmem_read<NC>(tmem + lane_bits + C::TM_S + w * NQ, sv);
           tc_fence_before();
-          mbar_arrive_warp(&bars->s_free[b]);
+          mbar_arrive_warp(&bars->s_free[w]);
+#pragma unroll
+          for (int q = 0; q < NC; ++q) y[q] = fmaf(__uint_as_float(sv[q]), a.scale_log2, -m[q]);
           const int kj0 = (pc.t_lo + j) * BN, kj = kj0 + tid;
-          const bool need_mask = kj0 + BN > pc.key_hi || (a.causal && kj0 + BN - 1 > p0) ||
-                                 (a.window > 0 && (p1 - kj0 >= a.window || (!a.causal && kj0 + BN - 1 - p0 >= a.window)));
+          if (kj0 + BN > pc.key_hi || (a.causal && kj0 + BN - 1 > p0) ||
+              (a.window > 0 && (p1 - kj0 >= a.window || (!a.causal && kj0 + BN - 1 - p0 >= a.window)))) {
 #pragma unroll
-          for (int q = 0; q < NQ; ++q) {
-            if (4 * (q >> 2) >= cols) break;
-            bool vis = q < cols;
-            if (need_mask) {
+            for (int q = 0; q < NC; ++q) {
               const int pos = p0 + static_cast<int>(q * gm >> 16);
-              vis = vis && kj < pc.key_hi && (!a.causal || kj <= pos) &&
-                    (a.window == 0 || (pos - kj < a.window && (a.causal || kj - pos < a.window)));
+              const bool vis = kj < pc.key_hi && (!a.causal || kj <= pos) &&
+                               (a.window == 0 || (pos - kj < a.window && (a.causal || kj - pos < a.window)));
+              if (!vis) y[q] = -INFINITY;
             }
-            x[q] = vis ? __uint_as_float(sv[q]) * a.scale_log2 : -INFINITY;
-            if (x[q] > m_ref[q] + kPdRescale || (m_ref[q] == -INFINITY && x[q] != -INFINITY)) need |= 1u << q;
           }
-          need = __reduce_or_sync(0xffffffffu, need);
+#pragma unroll
+          for (int q = 0; q < NC; ++q) need |= y[q] > kPdRescale;
+        } else {
+          need = false;
         }
-        if (lane == 0) bits[b * 4 + warp] = need;
-        named_bar_sync(1, 128);
-        const uint32_t need_all = bits[b * 4] | bits[b * 4 + 1] | bits[b * 4 + 2] | bits[b * 4 + 3];
-        float alpha[NQ];
-#pragma unroll
-        for (int q = 0; q < NQ; ++q) alpha[q] = 1.f;
-        bool rescale = false;
-        if (need_all != 0) {
+        // The product before last, of this buffer's parity: done with P^T and O^T.
+        auto product_done = [&]() { return s < 2 || mbar_wait_warp(&bars->p_free[w], ((s - 2) >> 1) & 1, wc); };
+        bool done = false;
+        if (bar_any(1 + w, 128, need)) {
+          // Some column outgrew its reference, or has none: the maxima over the
+          // tile's 128 keys, warps first.
           if (ok) {
 #pragma unroll
-            for (int g = 0; g < NQ / 4; ++g) {
-              if (4 * g >= cols) break;
-              float v[4];
-#pragma unroll
-              for (int u = 0; u < 4; ++u) v[u] = x[4 * g + u];
-#pragma unroll
-              for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-                for (int u = 0; u < 4; ++u) v[u] = fmaxf(v[u], __shfl_xor_sync(0xffffffffu, v[u], o));
-              if (lane == 0) {
-#pragma unroll
-                for (int u = 0; u < 4; ++u) mx[warp * NQ + 4 * g + u] = v[u];
-              }
+            for (int q = 0; q < NC; ++q) {
+              const float v = warp_max(y[q]);
+              if (lane == 0) mx[wl * NC + q] = v;
             }
           }
-          named_bar_sync(1, 128);
+          named_bar_sync(1 + w, 128);
+          if (ok) ok = done = product_done();
           if (ok) {
+            float alpha[NC];
+            bool rescale = false;
 #pragma unroll
-            for (int q = 0; q < NQ; ++q) {
-              if (4 * (q >> 2) >= cols) break;
-              if (!((need_all >> q) & 1u)) continue;
-              const float mstep = fmaxf(fmaxf(mx[q], mx[NQ + q]), fmaxf(mx[2 * NQ + q], mx[3 * NQ + q]));
-              if (m_ref[q] != -INFINITY) {
-                alpha[q] = ex2(m_ref[q] - mstep);
-                rescale = true;
+            for (int q = 0; q < NC; ++q) {
+              const float up = fmaxf(fmaxf(mx[q], mx[NC + q]), fmaxf(mx[2 * NC + q], mx[3 * NC + q]));
+              const bool first = (none >> q) & 1u;
+              const bool move = first ? up != -INFINITY : up > kPdRescale;
+              alpha[q] = 1.f;
+              if (move) {
+                if (!first) {
+                  alpha[q] = ex2(-up);
+                  l[q] *= alpha[q];
+                  if constexpr (kRounded) lr[q] *= alpha[q];
+                  rescale = true;
+                }
+                m[q] += up;
+                y[q] -= up;
+                none &= ~(1u << q);
               }
-              m_ref[q] = mstep;
+            }
+            if (rescale && j >= 2) {
+              tc_fence_after();
+              uint32_t o[NC];
+              tmem_read<NC>(tO, o);
+#pragma unroll
+              for (int q = 0; q < NC; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * alpha[q]);
+              tmem_write<NC>(tO, o);
             }
           }
         }
         if (!ok) continue;
-        __half ph[NQ];
+        __half ph[NC];
 #pragma unroll
-        for (int q = 0; q < NQ; ++q) {
-          if (4 * (q >> 2) >= cols) break;
-          // Hidden: 0 (also while the reference is -inf); a NaN score stays one.
-          const float p = x[q] == -INFINITY ? 0.f : ex2(x[q] - m_ref[q]);
+        for (int q = 0; q < NC; ++q) {
+          const float p = ex2(y[q]);
           ph[q] = __float2half_rn(p);
-          lsum[q] = lsum[q] * alpha[q] + __half2float(ph[q]);
-          lexact[q] = lexact[q] * alpha[q] + p;
+          l[q] += p;
+          if constexpr (kRounded) lr[q] += __half2float(ph[q]);
         }
-        // P^T into buffer b, K-major with 128-byte swizzle (as decode.cu).  Rows
-        // past `cols` are left as they are: they feed columns never read.
-        if (st >= 2 && !(ok = mbar_wait_warp(&bars->p_free[b], ((st - 2) >> 1) & 1, wc))) continue;
+        // P^T into buffer w, K-major with 128-byte swizzle (as decode.cu).
+        if (!done && !(ok = product_done())) continue;
         {
-          uint8_t* pb = smem + C::OFF_P + b * C::P_TILE + (tid >> 6) * C::P_CHUNK;
+          uint8_t* pb = smem + C::OFF_P + w * C::P_TILE + (tid >> 6) * C::P_CHUNK;
           const int kc = tid & 63, g = kc >> 3, wb = (kc & 7) * 2;
 #pragma unroll
-          for (int q = 0; q < NQ; ++q) {
-            if (4 * (q >> 2) >= cols) break;
-            *reinterpret_cast<__half*>(pb + q * 128 + ((g ^ (q & 7)) << 4) + wb) = ph[q];
-          }
-        }
-        if (rescale) {
-          // Not in a unit's first step: its reference is -inf until then.
-          if (!(ok = mbar_wait_warp(&bars->pv_done, (st - 1) & 1, wc))) continue;
-          tc_fence_after();
-          uint32_t o[NQ];
-          tmem_ld16(tmem + lane_bits + C::TM_O + (seg & 1) * NQ, o);
-          tmem_wait_ld();
-          pd_reg_fence16(o);
-#pragma unroll
-          for (int q = 0; q < NQ; ++q)
-            if (4 * (q >> 2) < cols) o[q] = __float_as_uint(__uint_as_float(o[q]) * alpha[q]);
-          tmem_st16(tmem + lane_bits + C::TM_O + (seg & 1) * NQ, o);
-          tmem_wait_st();
+          for (int q = 0; q < NC; ++q) *reinterpret_cast<__half*>(pb + q * 128 + ((g ^ (q & 7)) << 4) + wb) = ph[q];
         }
         fence_proxy_async_smem();
         tc_fence_before();
-        mbar_arrive_warp(&bars->p_full[b]);
+        mbar_arrive_warp(&bars->p_full[w]);
       }
+      st += n;
       // ---------------------------------------------------------- the unit's end
-      // Column sums over the 128 threads, in a fixed order.
+      // Column sums over the group's 128 threads, in a fixed order, and the
+      // references, by the piece's parity: a buffer is written again two pieces
+      // on, behind the next piece's barrier.
+      float* ms = red + 8 * NC + (pieces & 1) * 2 * NC;    // [2][NC]
+      float* rs = red + 12 * NC + (pieces & 1) * 16 * NC;  // [unrounded, rounded][2][4][NC]
 #pragma unroll
-      for (int g = 0; g < NQ / 4; ++g) {
-        if (4 * g >= cols) break;
-        float v[8];
+      for (int q0 = 0; q0 < NC; q0 += 4) {
+        float v[4], vr[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          v[u] = lsum[4 * g + u];
-          v[4 + u] = lexact[4 * g + u];
+          v[u] = l[q0 + u];
+          if constexpr (kRounded) vr[u] = lr[q0 + u];
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
-          for (int u = 0; u < 8; ++u) v[u] += __shfl_xor_sync(0xffffffffu, v[u], o);
+          for (int u = 0; u < 4; ++u) {
+            v[u] += __shfl_xor_sync(0xffffffffu, v[u], o);
+            if constexpr (kRounded) vr[u] += __shfl_xor_sync(0xffffffffu, vr[u], o);
+          }
         if (lane == 0) {
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            rs[warp * NQ + 4 * g + u] = v[u];
-            rs[(4 + warp) * NQ + 4 * g + u] = v[4 + u];
+            rs[(w * 4 + wl) * NC + q0 + u] = v[u];
+            if constexpr (kRounded) rs[(8 + w * 4 + wl) * NC + q0 + u] = vr[u];
           }
         }
       }
-      named_bar_sync(1, 128);
-      const int ob = seg & 1;
+      if (tid == 0) {
+#pragma unroll
+        for (int q = 0; q < NC; ++q) ms[w * NC + q] = m[q];
+      }
+      named_bar_sync(3, 256);
       if (ok && n > 0) ok = mbar_wait_warp(&bars->o_full[ob], (seg >> 1) & 1, wc);
       if (ok) {
-        uint32_t o[NQ];
+        // Each group joins half of the columns from both accumulators.
+        constexpr int H = NC / 2;
+        uint32_t o0[H], o1[H];
         if (n > 0) {
           tc_fence_after();
-          tmem_ld16(tmem + lane_bits + C::TM_O + ob * NQ, o);
-          tmem_wait_ld();
-          pd_reg_fence16(o);
+          const uint32_t at = tmem + lane_bits + C::TM_O + ob * 2 * NQ + w * H;
+          tmem_read<H>(at, o0);
+          tmem_read<H>(at + NQ, o1);
           tc_fence_before();
           mbar_arrive_warp(&bars->o_free[ob]);
         }
@@ -474,14 +544,21 @@ __global__ void __launch_bounds__(256, 1)
         const bool whole = pc.whole();
         const long long part0 = (static_cast<long long>(blockIdx.x) * 2 + pc.slot()) * NQ;
 #pragma unroll
-        for (int q = 0; q < NQ; ++q) {
+        for (int i = 0; i < H; ++i) {
+          const int q = w * H + i;
           if (q >= cols) break;
-          const float l = (rs[q] + rs[NQ + q]) + (rs[2 * NQ + q] + rs[3 * NQ + q]);
-          const float le = (rs[4 * NQ + q] + rs[5 * NQ + q]) + (rs[6 * NQ + q] + rs[7 * NQ + q]);
-          // A NaN among the scores makes the sum NaN, and O with it.
-          const float inv_l = l == 0.f ? 0.f : 1.f / l;
-          const float val = l == 0.f ? 0.f : __uint_as_float(o[q]) * inv_l;
-          const float L = le == 0.f ? -INFINITY : (m_ref[q] + log2f(le)) * kLn2;
+          auto sum = [&](int g) { return (rs[g * NC + q] + rs[(g + 1) * NC + q]) + (rs[(g + 2) * NC + q] + rs[(g + 3) * NC + q]); };
+          const float l0 = sum(0), l1 = sum(4), m0 = ms[q], m1 = ms[NC + q];
+          // A group without a visible key has the sum 0 and no part; a NaN among
+          // the scores makes a sum NaN, and O and lse with it.
+          const float top = l0 == 0.f ? m1 : l1 == 0.f ? m0 : fmaxf(m0, m1);
+          const float c0 = l0 == 0.f ? 0.f : ex2(m0 - top), c1 = l1 == 0.f ? 0.f : ex2(m1 - top);
+          const float le = l0 * c0 + l1 * c1;
+          float lo = le;
+          if constexpr (kRounded) lo = sum(8) * c0 + sum(12) * c1;
+          const float inv = lo == 0.f ? 0.f : 1.f / lo;
+          const float val = ((l0 == 0.f ? 0.f : __uint_as_float(o0[i]) * c0) + (l1 == 0.f ? 0.f : __uint_as_float(o1[i]) * c1)) * inv;
+          const float L = le == 0.f ? -INFINITY : (top + log2f(le)) * kLn2;
           if (!whole) {
             if (tid < D) a.part_o[(part0 + q) * D + tid] = val;
             if (tid == 0) a.part_lse[part0 + q] = L;
@@ -497,7 +574,6 @@ __global__ void __launch_bounds__(256, 1)
         }
       }
       if (n > 0) ++seg;
-      named_bar_sync(1, 128);  // the sums have been read: the next unit may write its own
     }
   }
 
@@ -509,14 +585,25 @@ __global__ void __launch_bounds__(256, 1)
 
 namespace {
 
-template <typename T, int D>
-cudaError_t launch_t(const PagedArgs& a, cudaStream_t stream) {
-  using C = PdCfg<D>;
-  auto kern = paged_decode_kernel<T, D>;
+template <typename T, int D, int NC>
+cudaError_t launch_n(const PagedArgs& a, cudaStream_t stream) {
+  using C = PdCfg<D, NC>;
+  auto kern = paged_decode_kernel<T, D, NC>;
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), C::SMEM_BYTES, a.device);
   if (e != cudaSuccess) return e;
   kern<<<a.ctas, C::THREADS, C::SMEM_BYTES, stream>>>(*a.tm_q, *a.tm_k, *a.tm_v, a);
   return note_cuda(cudaGetLastError(), "paged decode kernel launch");
+}
+
+template <typename T, int D>
+cudaError_t launch_t(const PagedArgs& a, cudaStream_t stream) {
+  switch (a.cols) {
+    case 4: return launch_n<T, D, 4>(a, stream);
+    case 8: return launch_n<T, D, 8>(a, stream);
+    case 16: return launch_n<T, D, 16>(a, stream);
+    case 32: return launch_n<T, D, 32>(a, stream);
+    default: return note_cuda(cudaErrorInvalidValue, "paged decode kernel (columns)");
+  }
 }
 
 }  // namespace

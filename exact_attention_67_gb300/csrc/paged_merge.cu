@@ -116,14 +116,15 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant_
 }
 
 template <typename T, int D>
-cudaError_t launch_t(const PagedArgs& a, int rows, cudaStream_t stream) {
-  const bool few = rows == kPagedDecodeCols;
+cudaError_t launch_t(const PagedArgs& a, cudaStream_t stream) {
+  const int rows = a.rows;
+  const bool few = a.cols > 0;
   const int UT = few ? a.tile_tokens : 2 * a.tile_tokens;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.ctas - 1, few ? rows : rows / 8);
+  cfg.gridDim = dim3(a.ctas - 1, few ? a.cols : rows / 8);
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cfg.attrs = attr;
@@ -136,10 +137,10 @@ cudaError_t launch_t(const PagedArgs& a, int rows, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_paged_merge(const PagedArgs& a, int rows, cudaStream_t stream) {
+cudaError_t launch_paged_merge(const PagedArgs& a, cudaStream_t stream) {
   if (a.ctas < 2) return cudaSuccess;
-  if (a.dtype == kF16) return a.d == 64 ? launch_t<__half, 64>(a, rows, stream) : launch_t<__half, 128>(a, rows, stream);
-  return a.d == 64 ? launch_t<__nv_bfloat16, 64>(a, rows, stream) : launch_t<__nv_bfloat16, 128>(a, rows, stream);
+  if (a.dtype == kF16) return a.d == 64 ? launch_t<__half, 64>(a, stream) : launch_t<__half, 128>(a, stream);
+  return a.d == 64 ? launch_t<__nv_bfloat16, 64>(a, stream) : launch_t<__nv_bfloat16, 128>(a, stream);
 }
 
 }  // namespace exattn

@@ -121,6 +121,11 @@ CASES = [
     ([5, 3], [2, 900], 3, 1, 64, 32, torch.float16, True, 0),     # positions below 0 see nothing
     ([3], [600], 5, 1, 128, 64, torch.bfloat16, False, 70),
     ([1], [70000], 2, 1, 128, 64, torch.bfloat16, True, 0),
+    ([4, 1, 3], [900, 1, 4000], 16, 2, 128, 16, torch.bfloat16, True, 0),   # up to 32 rows
+    ([1] * 6, [50, 1200, 128, 3, 900, 4000], 32, 1, 64, 32, torch.float16, True, 0),
+    ([1, 1], [300, 5000], 20, 1, 128, 64, torch.float16, True, 0),
+    ([2, 2, 0], [256, 1025, 7], 30, 2, 64, 128, torch.bfloat16, True, 200),
+    ([7, 2], [5, 1500], 4, 1, 128, 8, torch.bfloat16, True, 0),
     # More rows: the forward kernel.
     ([17], [17], 1, 1, 64, 16, torch.bfloat16, True, 0),
     ([130, 1, 40], [400, 33, 40], 4, 1, 128, 16, torch.bfloat16, True, 0),
