@@ -22,6 +22,8 @@ struct PageView {
   int num_pages;
   int page_size;           // a power of two
   int page_shift;          // log2(page_size)
+  // Attention: steps of a page and a key head in the places of the tensor maps.
+  int k_page_step, k_head_step, v_page_step, v_head_step;
 };
 
 // Which rows of a packed tensor are the new tokens of sequence b: rows
@@ -64,7 +66,7 @@ cudaError_t launch_rotary(const RotaryArgs& a, cudaStream_t stream);
 // columns (decode kernel) of a unit: unit row r is token r / G, head r % G.
 struct PagedArgs {
   const CUtensorMap* tm_q;  // (d, G, Hkv, total), box 64 x G x 1 x tokens of a query tile
-  const CUtensorMap* tm_k;  // (d, page_size, Hkv, num_pages), box 64 x min(page_size, 128) x 1 x 1
+  const CUtensorMap* tm_k;  // (64, 8, d / 64, page_size / 8, places): load_page in paged_sched.cuh
   const CUtensorMap* tm_v;
   void* o;                  // [total, Hq, d], strides h and n
   Strides so;
@@ -82,7 +84,7 @@ struct PagedArgs {
   int unit_cost, min_chunk;
   float* part_o;            // [ctas][2][rows][d]
   float* part_lse;          // [ctas][2][rows]
-  int* plan;                // [ctas][8]
+  struct PagedPlan* plan;   // [ctas]
   unsigned* err;
   int device;
 };

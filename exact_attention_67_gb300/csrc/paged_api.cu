@@ -5,6 +5,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstdlib>
+#include <numeric>
 
 #include "exattn.h"
 #include "paged.cuh"
@@ -215,14 +216,15 @@ namespace {
 constexpr int kSMs = 152;
 
 // How a paged attention is laid out on the GPU, from sizes alone.
-struct PagedPlan {
+struct AttendPlan {
   int cols;  // of the decode kernel, 0: the forward kernel
   int tile_tokens, ctas, rows, unit_cost, min_chunk;
   size_t plan_bytes, lse_bytes, total_bytes;
+  double weights;  // of the line, at most
 };
 
-PagedPlan paged_plan(int B, int Hq, int Hkv, int total, int max_q, int max_k, int d) {
-  PagedPlan p{};
+AttendPlan paged_plan(int B, int Hq, int Hkv, int total, int max_q, int max_k, int d) {
+  AttendPlan p{};
   const int G = Hq / Hkv;
   max_q = std::min(max_q, total);
   const long long need = static_cast<long long>(max_q) * G;
@@ -235,11 +237,11 @@ PagedPlan paged_plan(int B, int Hq, int Hkv, int total, int max_q, int max_k, in
   // At most so many weights (paged_sched.cuh): units of full length.
   const double units = static_cast<double>(Hkv) * std::min<double>(static_cast<double>(B) * ((max_q + ut - 1) / ut),
                                                                    static_cast<double>(total) / ut + B);
-  const double weights = units * ((static_cast<double>(max_k) + 127) / 128 + p.unit_cost);
-  p.ctas = static_cast<int>(std::min<double>(kSMs, std::max(1.0, std::ceil(weights / p.min_chunk))));
+  p.weights = units * ((static_cast<double>(max_k) + 127) / 128 + p.unit_cost);
+  p.ctas = static_cast<int>(std::min<double>(kSMs, std::max(1.0, std::ceil(p.weights / p.min_chunk))));
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
   const size_t slots = static_cast<size_t>(p.ctas) * 2 * p.rows;
-  p.plan_bytes = up(static_cast<size_t>(p.ctas) * 8 * sizeof(int));
+  p.plan_bytes = up(static_cast<size_t>(p.ctas) * 32);  // a PagedPlan each
   p.lse_bytes = up(slots * sizeof(float));
   p.total_bytes = p.plan_bytes + p.lse_bytes + up(slots * d * sizeof(float));
   return p;
@@ -259,7 +261,8 @@ int check_paged(int B, int Hq, int Hkv, int total, int max_q, int max_k, int d) 
 extern "C" size_t attn_fwd_paged_workspace_size(int B, int Hq, int Hkv, int total, int max_seqlen_q, int max_seqlen_k,
                                                 int d) {
   if (check_paged(B, Hq, Hkv, total, max_seqlen_q, max_seqlen_k, d) != EXATTN_OK) return 0;
-  return paged_plan(B, Hq, Hkv, total, max_seqlen_q, max_seqlen_k, d).total_bytes;
+  const AttendPlan p = paged_plan(B, Hq, Hkv, total, max_seqlen_q, max_seqlen_k, d);
+  return p.weights < 2e9 ? p.total_bytes : 0;
 }
 
 extern "C" int attn_fwd_paged(int dtype, const void* q, exattn_strides sq, const void* k_cache, exattn_strides skc,
@@ -282,7 +285,8 @@ extern "C" int attn_fwd_paged(int dtype, const void* q, exattn_strides sq, const
     return EXATTN_ERR_ALIGN;
   if ((rc = check_strides(sq, 1, Hq, total)) != EXATTN_OK || (rc = check_strides(so, 1, Hq, total)) != EXATTN_OK)
     return rc;
-  const PagedPlan plan = paged_plan(B, Hq, Hkv, total, max_seqlen_q, max_seqlen_k, d);
+  const AttendPlan plan = paged_plan(B, Hq, Hkv, total, max_seqlen_q, max_seqlen_k, d);
+  if (plan.weights >= 2e9) return EXATTN_ERR_SHAPE;
   if (!workspace || workspace_bytes < plan.total_bytes) return EXATTN_ERR_WORKSPACE;
   if (!aligned(workspace, 16)) return EXATTN_ERR_ALIGN;
   int dev = 0;
@@ -301,12 +305,21 @@ extern "C" int attn_fwd_paged(int dtype, const void* q, exattn_strides sq, const
     if (!encode_map(&mq, dt, 4, q, dims, str, box)) return EXATTN_ERR_CUDA;
   }
   for (int i = 0; i < 2; ++i) {
+    // Pages and heads as one axis: places a common divisor of both strides apart.
     const exattn_strides& s = i == 0 ? skc : svc;
-    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(page_size),
-                                static_cast<cuuint64_t>(Hkv), static_cast<cuuint64_t>(num_pages)};
-    const cuuint64_t str[3] = {bytes(page_size, s.n_stride), bytes(Hkv, s.h_stride), bytes(num_pages, s.b_stride)};
-    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(std::min(page_size, 128)), 1, 1};
-    if (!encode_map(i == 0 ? &mk : &mv, dt, 4, i == 0 ? k_cache : v_cache, dims, str, box)) return EXATTN_ERR_CUDA;
+    const long long sb = num_pages > 1 ? s.b_stride : 0, sh = Hkv > 1 ? s.h_stride : 0;
+    const long long step = std::max(std::gcd(sb, sh), 8ll);
+    const long long places = (num_pages - 1) * (sb / step) + (Hkv - 1) * (sh / step) + 1;
+    if (places >= (1ll << 31)) return EXATTN_ERR_SHAPE;
+    (i == 0 ? a.pv.k_page_step : a.pv.v_page_step) = static_cast<int>(sb / step);
+    (i == 0 ? a.pv.k_head_step : a.pv.v_head_step) = static_cast<int>(sh / step);
+    const cuuint64_t dims[5] = {64, 8, static_cast<cuuint64_t>(d / 64), static_cast<cuuint64_t>(page_size / 8),
+                                static_cast<cuuint64_t>(places)};
+    const cuuint64_t str[4] = {static_cast<cuuint64_t>(s.n_stride) * 2, 128, static_cast<cuuint64_t>(s.n_stride) * 16,
+                               static_cast<cuuint64_t>(step) * 2};
+    const cuuint32_t box[5] = {64, 8, static_cast<cuuint32_t>(d / 64),
+                               static_cast<cuuint32_t>(std::min(page_size, 128) / 8), 1};
+    if (!encode_map(i == 0 ? &mk : &mv, dt, 5, i == 0 ? k_cache : v_cache, dims, str, box)) return EXATTN_ERR_CUDA;
   }
   a.tm_q = &mq;
   a.tm_k = &mk;
@@ -330,7 +343,7 @@ extern "C" int attn_fwd_paged(int dtype, const void* q, exattn_strides sq, const
   a.unit_cost = plan.unit_cost;
   a.min_chunk = plan.min_chunk;
   char* ws = static_cast<char*>(workspace);
-  a.plan = reinterpret_cast<int*>(ws);
+  a.plan = reinterpret_cast<exattn::PagedPlan*>(ws);
   a.part_lse = reinterpret_cast<float*>(ws + plan.plan_bytes);
   a.part_o = reinterpret_cast<float*>(ws + plan.plan_bytes + plan.lse_bytes);
   a.err = err;

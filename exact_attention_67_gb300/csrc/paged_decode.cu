@@ -10,14 +10,18 @@
 //     unit after unit, with the loads of the next unit in flight while the
 //     last one ends: Q and O^T have two buffers;
 //   * two elementwise warpgroups take key tiles in turn, each with its own
-//     references, sums and O^T accumulator, joined at the unit's end.  One tile's
-//     work is a chain of latencies (TMEM load, barrier, exponentials, store) of
-//     over a microsecond at 8 columns; with one warpgroup it was the bound
-//     (B48 Hq32 Hk4 ctx to 16384: 160 us; B16 x 5 tokens Hq24 Hk8 d64: 58);
+//     references, sums, two S^T buffers and O^T accumulator, joined at the unit's
+//     end.  One tile's work is a chain of latencies (TMEM load, barrier,
+//     exponentials, store, hand-offs) of some 1,500 clocks, as long as d = 64's
+//     tile takes to arrive; so S^T runs up to four tiles ahead, and a warp each
+//     issues K Q^T and V P^T, whose waits would add up in one;
 //   * the columns' count, rounded up, is a template argument: straight-line code;
-//   * a 128-key tile is gathered page by page: one TMA box a page, issued by one
-//     lane each, the page numbers read one tile ahead.  Pages past the last visible
-//     key are not read, whatever the table says there;
+//   * a 128-key tile is gathered page by page: one TMA box a page for K and one
+//     for V, by two producer warps, issued by one lane each, the page numbers read
+//     one tile ahead (a box takes some 75 clocks to issue: at 16 rows a page and
+//     two boxes of 64 columns, one warp took 2,400 a tile, more than the tile's
+//     own time).  Pages past the last visible key are not read, whatever the
+//     table says there;
 //   * the stored rows behind a sequence's end may hold anything: scores there are
 //     replaced (not added to) by -inf, and V rows are zeroed in shared memory
 //     by the converting warps, so that 0 * NaN never meets an accumulator;
@@ -39,8 +43,9 @@ struct PdCfg {
   static constexpr int BN = kKeyTile;
   static constexpr int NQ = NC < 16 ? 16 : NC;  // the MMA's N
   static constexpr int NCHUNK = D / 64;
-  static constexpr int KV_CHUNK = BN * 128;
-  static constexpr int KV_TILE = NCHUNK * KV_CHUNK;
+  // A K or V tile: 16 groups of 8 rows, each NCHUNK swizzled atoms of 8 x 128 bytes.
+  static constexpr int GROUP = NCHUNK * 1024;
+  static constexpr int KV_TILE = 16 * GROUP;
   static constexpr int Q_CHUNK = NQ * 128;
   static constexpr int Q_TILE = NCHUNK * Q_CHUNK;
   static constexpr int QBUF = NC == 32 ? 1 : 2;  // Q tiles in shared memory
@@ -52,31 +57,41 @@ struct PdCfg {
   static constexpr int OFF_K = OFF_V + STAGES * KV_TILE;
   static constexpr int OFF_Q = OFF_K + STAGES * KV_TILE;
   static constexpr int OFF_P = OFF_Q + QBUF * Q_TILE;
-  // Per warpgroup maxima [2][4][NC]; by the unit's parity: references
-  // [2][2][NC], sums of unrounded and rounded weights [2][2][2][4][NC].
+  // Floats: maxima [2 groups][NC][4]; by the piece's parity the references
+  // [2][2][NC] and the sums of unrounded and rounded weights [2][2][2][NC][4];
+  // coefficients and output offsets [2 parities][NC] of 16 bytes.
   static constexpr int OFF_RED = OFF_P + 2 * P_TILE;
-  static constexpr int OFF_BAR = OFF_RED + (8 + 4 + 32) * NC * 4;
+  static constexpr int RED_REF = 8 * NC, RED_SUM = RED_REF + 4 * NC, RED_COEF = RED_SUM + 32 * NC;
+  static constexpr int OFF_BAR = OFF_RED + (RED_COEF + 8 * NC) * 4;
   static constexpr int SMEM_BYTES = OFF_BAR + 512 + 1024;
   static_assert(SMEM_BYTES <= 232448, "over the 227 KB shared-memory limit");
-  static constexpr int PRODUCER_WARP = 8, MMA_WARP = 9, READY_WARP = 10;
-  // Warps that make V ready: two leave the threads 168 registers, which the wider
-  // forms need.
-  static constexpr int READY_WARPS = NC <= 8 ? 4 : 2;
-  static constexpr int THREADS = 32 * (READY_WARP + READY_WARPS);
-  // Two S^T buffers, and O^T by warpgroup and by the unit's parity.
-  static constexpr uint32_t TM_S = 0, TM_O = 2 * NQ, TM_COLS = NQ == 16 ? 128 : 256;
+  static constexpr int K_WARP = 8, V_WARP = 9, S_WARP = 10, O_WARP = 11, READY_WARP = 12, THREADS = 512;
+  // Registers: 128 a thread at launch; with 32 columns the elementwise warpgroups
+  // take over most of the others' (2 x 184 + 2 x 72 = 4 x 128).
+  static constexpr bool SPLIT_REGS = false;
+  // Four S^T buffers, and O^T by warpgroup and by the unit's parity.
+  static constexpr uint32_t TM_S = 0, TM_O = 4 * NQ, TM_COLS = 8 * NQ;
 };
 
 template <int STAGES>
 struct PdBars {
   uint64_t q_full[2], q_empty[2];
-  uint64_t kv_full[STAGES], kv_empty[STAGES], v_ready[STAGES];
-  uint64_t s_full[2], s_free[2], p_full[2], p_free[2];
+  uint64_t k_full[STAGES], k_empty[STAGES];
+  uint64_t v_full[STAGES], v_empty[STAGES], v_ready[STAGES];
+  uint64_t s_full[4], s_free[4], p_full[2], p_free[2];
   uint64_t o_full[2], o_free[2];
-  uint64_t mma_done;
+  uint64_t done[2];  // teardown: all of the issuing warp's products
   PagedCursor start;
+  PagedSeq seq;
   uint32_t tmem_base;
   int abort;
+};
+
+// What the epilogue needs of a column: the two accumulators' factors, and its row
+// in the output, or in the partial results.
+struct alignas(16) Column {
+  float c0, c1;
+  long long row;  // element offset
 };
 
 constexpr float kPdRescale = 8.0f;  // log2 units a column's maximum may outgrow its reference
@@ -139,11 +154,26 @@ __device__ __forceinline__ bool bar_any(int id, int threads, bool yes) {
   return any != 0;
 }
 
-// Maximum over a warp (NaN only if all are).
-__device__ __forceinline__ float warp_max(float x) {
-  float m;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x));
-  return m;
+// The warp's reductions of NC columns, scattered: lane l gets column
+// l >> (5 - log2 NC), by halving the columns with every exchange.
+template <int NC, typename Op>
+__device__ __forceinline__ float warp_columns(const float (&in)[NC], int lane, Op op) {
+  float v[NC];
+#pragma unroll
+  for (int i = 0; i < NC; ++i) v[i] = in[i];
+  int o = 16;
+#pragma unroll
+  for (int width = NC; width > 1; width /= 2, o >>= 1) {
+    const bool upper = lane & o;
+#pragma unroll
+    for (int i = 0; i < width / 2; ++i) {
+      const float send = upper ? v[i] : v[i + width / 2], keep = upper ? v[i + width / 2] : v[i];
+      v[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, o));
+    }
+  }
+#pragma unroll
+  for (int k = 32 / NC; k > 1; k /= 2, o >>= 1) v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
+  return v[0];
 }
 
 }  // namespace
@@ -168,36 +198,45 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
   const int UT = a.tile_tokens, G = a.G;
 
   if (warp == 0) {
-    long long chunk;
-    const PagedCursor c = paged_start(a, UT, static_cast<int>(blockIdx.x), lane, &chunk);
+    PagedSeq s;
+    const PagedCursor c = paged_start(a, UT, lane, &s);
     if (lane == 0) {
       bars->start = c;
-      paged_note(a, c, chunk, static_cast<int>(blockIdx.x));
+      bars->seq = s;
     }
   }
   if (threadIdx.x == 32) {
     for (int b = 0; b < 2; ++b) {
       mbar_init(&bars->q_full[b], 1);
       mbar_init(&bars->q_empty[b], 1);
-      mbar_init(&bars->s_full[b], 1);
-      mbar_init(&bars->s_free[b], 4);
       mbar_init(&bars->p_full[b], 4);
       mbar_init(&bars->p_free[b], 1);
       mbar_init(&bars->o_full[b], 1);
       mbar_init(&bars->o_free[b], 8);
+      mbar_init(&bars->done[b], 1);
+    }
+    for (int b = 0; b < 4; ++b) {
+      mbar_init(&bars->s_full[b], 1);
+      mbar_init(&bars->s_free[b], 4);
     }
     for (int s = 0; s < C::STAGES; ++s) {
-      mbar_init(&bars->kv_full[s], 1);
-      mbar_init(&bars->kv_empty[s], 1);
-      mbar_init(&bars->v_ready[s], C::READY_WARPS);
+      mbar_init(&bars->k_full[s], 1);
+      mbar_init(&bars->k_empty[s], 1);
+      mbar_init(&bars->v_full[s], 1);
+      mbar_init(&bars->v_empty[s], 1);
+      mbar_init(&bars->v_ready[s], 4);
     }
-    mbar_init(&bars->mma_done, 1);
     bars->abort = 0;
     fence_barrier_init();
   }
-  if (warp == C::MMA_WARP) {
+  if (warp == C::S_WARP) {
     tmem_alloc(&bars->tmem_base, C::TM_COLS);
     tmem_relinquish();
+  }
+  if (warp == C::K_WARP && lane == 0) {
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
   }
   // Rows of Q past the unit's box are never loaded: zero, so that their columns'
   // scores are.
@@ -211,53 +250,53 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
   const uint32_t tmem = bars->tmem_base;
   const WaitCtl wc{&bars->abort, a.err};
   PagedCursor cur = bars->start;
-  PagedSeq seq = cur.left > 0 ? paged_seq(a, cur.b) : PagedSeq{};
+  PagedSeq seq = bars->seq;
   PagedPiece pc;
 
-  if (warp == C::PRODUCER_WARP) {
-    // ------------------------------------------------------------ TMA producer
-    if (lane == 0) {
-      tma_prefetch_desc(&tm_q);
-      tma_prefetch_desc(&tm_k);
-      tma_prefetch_desc(&tm_v);
-    }
+  if constexpr (C::SPLIT_REGS) {
+    if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+  }
+  if (warp == C::K_WARP || warp == C::V_WARP) {
+    // ------------------------------------------------------------ TMA producers
+    const bool is_k = warp == C::K_WARP;
+    const CUtensorMap* tm = is_k ? &tm_k : &tm_v;
+    uint64_t* full = is_k ? bars->k_full : bars->v_full;
+    uint64_t* empty = is_k ? bars->k_empty : bars->v_empty;
+    uint8_t* tiles = smem + (is_k ? C::OFF_K : C::OFF_V);
     const uint64_t pol = l2_policy_evict_first();
-    const int ps = a.pv.page_size, shift = a.pv.page_shift;
-    const int box = min(ps, BN), per_tile = BN / box;
+    const int shift = a.pv.page_shift, box = min(a.pv.page_size, BN), per_tile = BN / box;
     const uint32_t q_bytes = static_cast<uint32_t>(UT * G) * 128 * C::NCHUNK;
     int st = 0, seg = 0;
     bool ok = true;
     while (ok && cur.next(a, UT, seq, &pc)) {
       if (pc.t_hi == pc.t_lo) continue;
-      const int qb = seg % C::QBUF;
-      if (seg >= C::QBUF && !(ok = mbar_wait_warp(&bars->q_empty[qb], (seg / C::QBUF - 1) & 1, wc))) break;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&bars->q_full[qb], q_bytes);
-        for (int c = 0; c < C::NCHUNK; ++c)
-          tma_load_4d(&tm_q, &bars->q_full[qb], smem + C::OFF_Q + qb * C::Q_TILE + c * C::Q_CHUNK, c * 64, 0, pc.h,
-                      pc.s.row0 + pc.tok0, pol);
-      }
-      ++seg;
       const int* row = a.pv.table + pc.b * a.pv.table_stride;
       // Boxes of a tile that hold a visible key, and this lane's page of it.
       auto boxes = [&](int t) { return min(per_tile, (pc.key_hi - t * BN + box - 1) / box); };
       auto page_of = [&](int t) { return lane < boxes(t) ? row[(t * BN >> shift) + lane] : 0; };
       int page = page_of(pc.t_lo);
+      if (is_k) {
+        const int qb = seg % C::QBUF;
+        if (seg >= C::QBUF && !(ok = mbar_wait_warp(&bars->q_empty[qb], (seg / C::QBUF - 1) & 1, wc))) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&bars->q_full[qb], q_bytes);
+          for (int c = 0; c < C::NCHUNK; ++c)
+            tma_load_4d(&tm_q, &bars->q_full[qb], smem + C::OFF_Q + qb * C::Q_TILE + c * C::Q_CHUNK, c * 64, 0, pc.h,
+                        pc.s.row0 + pc.tok0, pol);
+        }
+      }
+      ++seg;
       for (int t = pc.t_lo; t < pc.t_hi; ++t, ++st) {
         const int s = st % C::STAGES;
         const int next_page = t + 1 < pc.t_hi ? page_of(t + 1) : 0;
-        if (!(ok = mbar_wait_warp(&bars->kv_empty[s], ((st / C::STAGES) & 1) ^ 1, wc))) break;
+        if (!(ok = mbar_wait_warp(&empty[s], ((st / C::STAGES) & 1) ^ 1, wc))) break;
         const int nb = boxes(t);
-        if (lane == 0) mbar_arrive_expect_tx(&bars->kv_full[s], static_cast<uint32_t>(nb * box) * 256 * C::NCHUNK);
+        if (lane == 0) mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(nb * box) * 128 * C::NCHUNK);
         __syncwarp();
-        if (lane < nb) {
-          const int off = t * BN & (ps - 1);  // of the tile's start in its page (pages longer than a tile)
-          for (int c = 0; c < C::NCHUNK; ++c) {
-            const int at = s * C::KV_TILE + c * C::KV_CHUNK + lane * box * 128;
-            tma_load_4d(&tm_k, &bars->kv_full[s], smem + C::OFF_K + at, c * 64, off, pc.h, page, pol);
-            tma_load_4d(&tm_v, &bars->kv_full[s], smem + C::OFF_V + at, c * 64, off, pc.h, page, pol);
-          }
-        }
+        if (lane < nb)
+          load_page(tm, &full[s], tiles + s * C::KV_TILE + lane * box * 128 * C::NCHUNK, a.pv,
+                    (t * BN & (a.pv.page_size - 1)) >> 3, page, pc.h, is_k, pol);
         __syncwarp();
         page = next_page;
       }
@@ -265,109 +304,114 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
     __syncwarp();
     if (lane == 0 && *reinterpret_cast<volatile int*>(&bars->abort)) {
       // Never leave a copy in flight into shared memory this CTA is about to release.
-      for (int i = max(0, seg - C::QBUF); i < seg; ++i)
+      for (int i = max(0, seg - C::QBUF); is_k && i < seg; ++i)
         mbar_wait_drain(&bars->q_full[i % C::QBUF], (i / C::QBUF) & 1, a.err);
       for (int j = max(0, st - C::STAGES); j < st; ++j)
-        mbar_wait_drain(&bars->kv_full[j % C::STAGES], (j / C::STAGES) & 1, a.err);
+        mbar_wait_drain(&full[j % C::STAGES], (j / C::STAGES) & 1, a.err);
     }
     __syncwarp();
-  } else if (warp == C::MMA_WARP) {
-    // ------------------------------------------------------------ MMA issuer
-    // Steps run on across units: S^T of step st, then P^T V of step st - 1.
-    constexpr uint32_t idesc_s = idesc_f16kind(E::kFmt, 128, NQ, 0, 0);
-    constexpr uint32_t idesc_o = idesc_f16kind(PE::kFmt, 128, NQ, 1, 0);
+  } else if (warp == C::S_WARP) {
+    // ------------------------------------------------------------ S^T = K Q^T
+    constexpr uint32_t idesc = idesc_f16kind(E::kFmt, 128, NQ, 0, 0);
     const uint64_t q_desc = sdesc_sw128(smem_u32(smem + C::OFF_Q), 16, 1024);
-    const uint64_t k_desc = sdesc_sw128(smem_u32(smem + C::OFF_K), 16, 1024);
-    const uint64_t p_desc = sdesc_sw128(smem_u32(smem + C::OFF_P), 16, 1024);
-    const uint64_t v_desc = sdesc_sw128(smem_u32(smem + C::OFF_V), C::KV_CHUNK, 1024);
+    const uint64_t k_desc = sdesc_sw128(smem_u32(smem + C::OFF_K), 16, C::GROUP);
     auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_warp(bar, parity, wc); };
-    int st = 0, seg = -1, j = 0, n = 0;
-    bool ok = true, prev = false, prev_last = false;
-    int prev_seg = 0, prev_j = 0;
-    for (;;) {
-      bool have = j < n;
-      while (!have && cur.next(a, UT, seq, &pc)) {
-        if (pc.t_hi == pc.t_lo) continue;
-        n = pc.t_hi - pc.t_lo;
-        j = 0;
-        ++seg;
-        have = true;
-        if (!(ok = wait(&bars->q_full[seg % C::QBUF], (seg / C::QBUF) & 1))) break;
-      }
-      if (!ok) break;
-      if (have) {
-        const int s = st % C::STAGES, b = st & 1;
-        if (!(ok = wait(&bars->kv_full[s], (st / C::STAGES) & 1))) break;
-        if (st >= 2 && !(ok = wait(&bars->s_free[b], ((st - 2) >> 1) & 1))) break;
+    int st = 0, seg = 0;
+    bool ok = true;
+    while (ok && cur.next(a, UT, seq, &pc)) {
+      if (pc.t_hi == pc.t_lo) continue;
+      const int qb = seg % C::QBUF;
+      if (!(ok = wait(&bars->q_full[qb], (seg / C::QBUF) & 1))) break;
+      const uint64_t qd = q_desc + ((qb * C::Q_TILE) >> 4);
+      for (int t = pc.t_lo; t < pc.t_hi; ++t, ++st) {
+        const int s = st % C::STAGES, b = st & 3;
+        if (!(ok = wait(&bars->k_full[s], (st / C::STAGES) & 1))) break;
+        if (st >= 4 && !(ok = wait(&bars->s_free[b], ((st >> 2) - 1) & 1))) break;
         tc_fence_after();
         if (elect_one()) {
-          const uint64_t qd = q_desc + (((seg % C::QBUF) * C::Q_TILE) >> 4);
+          const uint64_t kd = k_desc + ((s * C::KV_TILE) >> 4);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t ko = ((kk >> 2) * C::KV_CHUNK + (kk & 3) * 32) >> 4;
-            const uint32_t qo = ((kk >> 2) * C::Q_CHUNK + (kk & 3) * 32) >> 4;
-            mma_ss(tmem + C::TM_S + b * NQ, k_desc + ((s * C::KV_TILE) >> 4) + ko, qd + qo, idesc_s, kk > 0);
-          }
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_ss(tmem + C::TM_S + b * NQ, kd + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4),
+                   qd + (((kk >> 2) * C::Q_CHUNK + (kk & 3) * 32) >> 4), idesc, kk > 0);
           mma_commit(&bars->s_full[b]);
-          if (j == n - 1) mma_commit(&bars->q_empty[seg % C::QBUF]);
+          mma_commit(&bars->k_empty[s]);
+          if (t == pc.t_hi - 1) mma_commit(&bars->q_empty[qb]);
         }
         __syncwarp();
       }
-      if (prev) {
-        const int sp = st - 1, ss = sp % C::STAGES, bp = sp & 1, ob = prev_seg & 1;
-        if (!(ok = wait(&bars->p_full[bp], (sp >> 1) & 1))) break;
-        if (!(ok = wait(&bars->v_ready[ss], (sp / C::STAGES) & 1))) break;
-        // The unit two before has been read out of these accumulators.
-        if (prev_j == 0 && prev_seg >= 2 && !(ok = wait(&bars->o_free[ob], ((prev_seg >> 1) - 1) & 1))) break;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint64_t vd = v_desc + ((ss * C::KV_TILE) >> 4);
-#pragma unroll
-          for (int kk = 0; kk < BN / 16; ++kk) {
-            const uint32_t po = ((kk >> 2) * C::P_CHUNK + (kk & 3) * 32) >> 4;
-            mma_ss(tmem + C::TM_O + (ob * 2 + bp) * NQ, vd + ((kk * 16 * 128) >> 4), p_desc + ((bp * C::P_TILE) >> 4) + po,
-                   idesc_o, (prev_j >= 2 || kk > 0) ? 1u : 0u);
-          }
-          mma_commit(&bars->kv_empty[ss]);
-          mma_commit(&bars->p_free[bp]);
-          if (prev_last) mma_commit(&bars->o_full[ob]);
-        }
-        __syncwarp();
-      }
-      if (!have) break;
-      prev = true;
-      prev_j = j;
-      prev_last = j == n - 1;
-      prev_seg = seg;
-      ++j;
-      ++st;
+      ++seg;
     }
     // Nothing may still read shared memory or write TMEM once the CTA tears down.
-    if (elect_one()) mma_commit(&bars->mma_done);
+    if (elect_one()) mma_commit(&bars->done[0]);
     __syncwarp();
-    if (lane == 0) mbar_wait_drain(&bars->mma_done, 0, a.err);
+    if (lane == 0) mbar_wait_drain(&bars->done[0], 0, a.err);
+    __syncwarp();
+  } else if (warp == C::O_WARP) {
+    // ------------------------------------------------------------ O^T += V^T P^T
+    constexpr uint32_t idesc = idesc_f16kind(PE::kFmt, 128, NQ, 1, 0);
+    const uint64_t p_desc = sdesc_sw128(smem_u32(smem + C::OFF_P), 16, 1024);
+    // Its two runs of 64 rows (d) are a group's two atoms; at d = 64 the second
+    // run is the next group's.
+    const uint64_t v_desc = sdesc_sw128(smem_u32(smem + C::OFF_V), 1024, C::GROUP);
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_warp(bar, parity, wc); };
+    int st = 0, seg = 0;
+    bool ok = true;
+    while (ok && cur.next(a, UT, seq, &pc)) {
+      const int n = pc.t_hi - pc.t_lo, ob = seg & 1;
+      if (n == 0) continue;
+      for (int j = 0; j < n; ++j, ++st) {
+        const int s = st % C::STAGES, w = st & 1;
+        if (!(ok = wait(&bars->v_ready[s], (st / C::STAGES) & 1))) break;
+        // The unit two before has been read out of these accumulators.
+        if (j == 0 && seg >= 2 && !(ok = wait(&bars->o_free[ob], ((seg >> 1) - 1) & 1))) break;
+        if (!(ok = wait(&bars->p_full[w], (st >> 1) & 1))) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t vd = v_desc + ((s * C::KV_TILE) >> 4), pd = p_desc + ((w * C::P_TILE) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < BN / 16; ++kk)
+            mma_ss(tmem + C::TM_O + (ob * 2 + w) * NQ, vd + ((kk * 2 * C::GROUP) >> 4),
+                   pd + (((kk >> 2) * C::P_CHUNK + (kk & 3) * 32) >> 4), idesc, (j >= 2 || kk > 0) ? 1u : 0u);
+          mma_commit(&bars->p_free[w]);
+          mma_commit(&bars->v_empty[s]);
+          if (j == n - 1) mma_commit(&bars->o_full[ob]);
+        }
+        __syncwarp();
+      }
+      ++seg;
+    }
+    if (elect_one()) mma_commit(&bars->done[1]);
+    __syncwarp();
+    if (lane == 0) mbar_wait_drain(&bars->done[1], 0, a.err);
     __syncwarp();
   } else if (warp >= C::READY_WARP) {
     // ------------------------------------------------------------ V made ready
     // bf16 tiles to f16 in place; rows at or past the last visible key to zero.
-    constexpr int RT = 32 * C::READY_WARPS;
     const int ct = threadIdx.x - 32 * C::READY_WARP;
     int st = 0;
     bool ok = true;
     while (ok && cur.next(a, UT, seq, &pc)) {
       for (int t = pc.t_lo; t < pc.t_hi; ++t, ++st) {
         const int s = st % C::STAGES, rows = pc.key_hi - t * BN;
-        if (!(ok = mbar_wait_warp(&bars->kv_full[s], (st / C::STAGES) & 1, wc))) break;
+        if (!(ok = mbar_wait_warp(&bars->v_full[s], (st / C::STAGES) & 1, wc))) break;
         uint4* tile = reinterpret_cast<uint4*>(smem + C::OFF_V + s * C::KV_TILE);
         if (kConvertV || rows < BN) {
-#pragma unroll 8
-          for (int i = 0; i < C::KV_TILE / 16 / RT; ++i) {
-            uint4 x = tile[i * RT + ct];
-            if constexpr (kConvertV)
-              x = make_uint4(pd_bf16x2_to_f16x2(x.x), pd_bf16x2_to_f16x2(x.y), pd_bf16x2_to_f16x2(x.z),
-                             pd_bf16x2_to_f16x2(x.w));
-            if (((i * RT + ct) >> 3 & (BN - 1)) >= rows) x = make_uint4(0, 0, 0, 0);
-            tile[i * RT + ct] = x;
+#pragma unroll
+          for (int i0 = 0; i0 < C::KV_TILE / 16 / 128; i0 += 8) {
+            uint4 x[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) x[u] = tile[(i0 + u) * 128 + ct];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              if constexpr (kConvertV)
+                x[u] = make_uint4(pd_bf16x2_to_f16x2(x[u].x), pd_bf16x2_to_f16x2(x[u].y), pd_bf16x2_to_f16x2(x[u].z),
+                                  pd_bf16x2_to_f16x2(x[u].w));
+              // 64 vectors an atom of 8 rows, 8 a row.
+              const int i = (i0 + u) * 128 + ct;
+              if (i / (64 * C::NCHUNK) * 8 + (i >> 3 & 7) >= rows) x[u] = make_uint4(0, 0, 0, 0);
+              tile[i] = x[u];
+            }
           }
           fence_proxy_async_smem();
         }
@@ -376,10 +420,13 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
     }
   } else {
     // ------------------------------------------------------------ elementwise (thread = key row / d row)
-    // Warpgroup w takes the steps of its parity: S^T, P^T buffer w.
+    // Warpgroup w takes the steps of its parity: S^T buffers w and w + 2, P^T buffer w.
     const int w = warp >> 2, wl = warp & 3, tid = threadIdx.x & 127;
+    constexpr int CB = NC == 4 ? 2 : NC == 8 ? 3 : NC == 16 ? 4 : 5;  // log2 NC
+    const int my_col = lane >> (5 - CB);                              // of warp_columns
+    const bool writer = (lane & ((1 << (5 - CB)) - 1)) == 0;
     const uint32_t lane_bits = static_cast<uint32_t>(wl * 32) << 16;
-    float* mx = red + w * 4 * NC;                                // [4][NC]
+    float4* mx = reinterpret_cast<float4*>(red) + w * NC;        // [NC], a warp each
     const uint32_t gm = 65536u / G + 1;                          // q / G == q * gm >> 16 for q < 32, G <= 32
     int st = 0, seg = 0, pieces = 0;
     bool ok = true;
@@ -400,25 +447,31 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
         const int s = st + j;
         float y[NC];  // scores above the column's reference, log2 units
         bool need = none != 0;
-        if (ok) ok = mbar_wait_warp(&bars->s_full[w], (s >> 1) & 1, wc);
+        if (ok) ok = mbar_wait_warp(&bars->s_full[s & 3], (s >> 2) & 1, wc);
         if (ok) {
           tc_fence_after();
           uint32_t sv[NC];
-          tmem_read<NC>(tmem + lane_bits + C::TM_S + w * NQ, sv);
+          tmem_read<NC>(tmem + lane_bits + C::TM_S + (s & 3) * NQ, sv);
           tc_fence_before();
-          mbar_arrive_warp(&bars->s_free[w]);
+          mbar_arrive_warp(&bars->s_free[s & 3]);
 #pragma unroll
           for (int q = 0; q < NC; ++q) y[q] = fmaf(__uint_as_float(sv[q]), a.scale_log2, -m[q]);
-          const int kj0 = (pc.t_lo + j) * BN, kj = kj0 + tid;
+          const int kj0 = (pc.t_lo + j) * BN;
           if (kj0 + BN > pc.key_hi || (a.causal && kj0 + BN - 1 > p0) ||
               (a.window > 0 && (p1 - kj0 >= a.window || (!a.causal && kj0 + BN - 1 - p0 >= a.window)))) {
-#pragma unroll
-            for (int q = 0; q < NC; ++q) {
-              const int pos = p0 + static_cast<int>(q * gm >> 16);
-              const bool vis = kj < pc.key_hi && (!a.causal || kj <= pos) &&
-                               (a.window == 0 || (pos - kj < a.window && (a.causal || kj - pos < a.window)));
-              if (!vis) y[q] = -INFINITY;
+            // This key's visible columns [lo, hi): tokens are G columns each, and
+            // a token sees a key by its distance only.
+            const int dist = kj0 + tid - p0;  // from token 0's position
+            auto column = [&](int token) { return min(max(token, 0), NC) * G; };
+            int lo = 0, hi = kj0 + tid < pc.key_hi ? NC : 0;
+            if (a.causal) lo = column(dist);
+            if (a.window > 0) {
+              hi = min(hi, column(dist + a.window));
+              if (!a.causal) lo = column(dist - a.window + 1);
             }
+#pragma unroll
+            for (int q = 0; q < NC; ++q)
+              if (q < lo || q >= hi) y[q] = -INFINITY;
           }
 #pragma unroll
           for (int q = 0; q < NC; ++q) need |= y[q] > kPdRescale;
@@ -432,11 +485,8 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
           // Some column outgrew its reference, or has none: the maxima over the
           // tile's 128 keys, warps first.
           if (ok) {
-#pragma unroll
-            for (int q = 0; q < NC; ++q) {
-              const float v = warp_max(y[q]);
-              if (lane == 0) mx[wl * NC + q] = v;
-            }
+            const float v = warp_columns(y, lane, [](float x, float z) { return fmaxf(x, z); });
+            if (writer) reinterpret_cast<float*>(mx + my_col)[wl] = v;
           }
           named_bar_sync(1 + w, 128);
           if (ok) ok = done = product_done();
@@ -445,7 +495,8 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
             bool rescale = false;
 #pragma unroll
             for (int q = 0; q < NC; ++q) {
-              const float up = fmaxf(fmaxf(mx[q], mx[NC + q]), fmaxf(mx[2 * NC + q], mx[3 * NC + q]));
+              const float4 v = mx[q];
+              const float up = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
               const bool first = (none >> q) & 1u;
               const bool move = first ? up != -INFINITY : up > kPdRescale;
               alpha[q] = 1.f;
@@ -472,13 +523,18 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
           }
         }
         if (!ok) continue;
-        __half ph[NC];
+        uint32_t ph[NC / 2];  // weights, as f16 pairs
 #pragma unroll
-        for (int q = 0; q < NC; ++q) {
-          const float p = ex2(y[q]);
-          ph[q] = __float2half_rn(p);
-          l[q] += p;
-          if constexpr (kRounded) lr[q] += __half2float(ph[q]);
+        for (int q = 0; q < NC; q += 2) {
+          const float pa = ex2(y[q]), pb = ex2(y[q + 1]);
+          ph[q / 2] = PE::pack(pa, pb);
+          l[q] += pa;
+          l[q + 1] += pb;
+          if constexpr (kRounded) {
+            const float2 r = PE::add_pair(ph[q / 2], make_float2(lr[q], lr[q + 1]));
+            lr[q] = r.x;
+            lr[q + 1] = r.y;
+          }
         }
         // P^T into buffer w, K-major with 128-byte swizzle (as decode.cu).
         if (!done && !(ok = product_done())) continue;
@@ -486,7 +542,9 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
           uint8_t* pb = smem + C::OFF_P + w * C::P_TILE + (tid >> 6) * C::P_CHUNK;
           const int kc = tid & 63, g = kc >> 3, wb = (kc & 7) * 2;
 #pragma unroll
-          for (int q = 0; q < NC; ++q) *reinterpret_cast<__half*>(pb + q * 128 + ((g ^ (q & 7)) << 4) + wb) = ph[q];
+          for (int q = 0; q < NC; ++q)
+            *reinterpret_cast<uint16_t*>(pb + q * 128 + ((g ^ (q & 7)) << 4) + wb) =
+                static_cast<uint16_t>(q & 1 ? ph[q / 2] >> 16 : ph[q / 2] & 0xffffu);
         }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -497,40 +555,55 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
       // Column sums over the group's 128 threads, in a fixed order, and the
       // references, by the piece's parity: a buffer is written again two pieces
       // on, behind the next piece's barrier.
-      float* ms = red + 8 * NC + (pieces & 1) * 2 * NC;    // [2][NC]
-      float* rs = red + 12 * NC + (pieces & 1) * 16 * NC;  // [unrounded, rounded][2][4][NC]
-#pragma unroll
-      for (int q0 = 0; q0 < NC; q0 += 4) {
-        float v[4], vr[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          v[u] = l[q0 + u];
-          if constexpr (kRounded) vr[u] = lr[q0 + u];
+      const int par = pieces & 1;
+      float* ref = red + C::RED_REF + par * 2 * NC;                                        // [2][NC]
+      float4* sums = reinterpret_cast<float4*>(red + C::RED_SUM) + par * 4 * NC;  // [unrounded, rounded][2][NC]
+      Column* coef = reinterpret_cast<Column*>(red + C::RED_COEF) + par * NC;     // [NC]
+      {
+        auto add = [](float x, float z) { return x + z; };
+        const float v = warp_columns(l, lane, add);
+        if (writer) reinterpret_cast<float*>(sums + w * NC + my_col)[wl] = v;
+        if constexpr (kRounded) {
+          const float vr = warp_columns(lr, lane, add);
+          if (writer) reinterpret_cast<float*>(sums + (2 + w) * NC + my_col)[wl] = vr;
         }
+        if (tid == 0) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            v[u] += __shfl_xor_sync(0xffffffffu, v[u], o);
-            if constexpr (kRounded) vr[u] += __shfl_xor_sync(0xffffffffu, vr[u], o);
-          }
-        if (lane == 0) {
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            rs[(w * 4 + wl) * NC + q0 + u] = v[u];
-            if constexpr (kRounded) rs[(8 + w * 4 + wl) * NC + q0 + u] = vr[u];
-          }
+          for (int q = 0; q < NC; ++q) ref[w * NC + q] = m[q];
         }
-      }
-      if (tid == 0) {
-#pragma unroll
-        for (int q = 0; q < NC; ++q) ms[w * NC + q] = m[q];
       }
       named_bar_sync(3, 256);
+      // Each group joins half of the columns from both accumulators.  Their
+      // coefficients, a lane each:
+      constexpr int H = NC / 2;
+      const bool whole = pc.whole();
+      if (wl == 0 && lane < H) {
+        const int q = w * H + lane;
+        auto sum = [&](int g) {
+          const float4 v = sums[g * NC + q];
+          return (v.x + v.y) + (v.z + v.w);
+        };
+        const float l0 = sum(0), l1 = sum(1), m0 = ref[q], m1 = ref[NC + q];
+        // A group without a visible key has the sum 0 and no part; a NaN among the
+        // scores makes a sum NaN, and O and lse with it.
+        const float top = l0 == 0.f ? m1 : l1 == 0.f ? m0 : fmaxf(m0, m1);
+        const float c0 = l0 == 0.f ? 0.f : ex2(m0 - top), c1 = l1 == 0.f ? 0.f : ex2(m1 - top);
+        const float le = l0 * c0 + l1 * c1;
+        float lo = le;
+        if constexpr (kRounded) lo = sum(2) * c0 + sum(3) * c1;
+        const float inv = lo == 0.f ? 0.f : 1.f / lo;
+        const float L = le == 0.f ? -INFINITY : (top + log2f(le)) * 0.6931471805599453f;
+        const int t = static_cast<int>(q * gm >> 16), head = pc.h * G + q - t * G, prow = pc.s.row0 + pc.tok0 + t;
+        const long long part = (static_cast<long long>(blockIdx.x) * 2 + pc.slot()) * NQ + q;
+        coef[q] = Column{c0 * inv, c1 * inv, whole ? prow * a.so.n + head * a.so.h : part * D};
+        if (ok && q < cols) {
+          if (whole) a.lse[static_cast<long long>(head) * a.nt.total + prow] = L;
+          else a.part_lse[part] = L;
+        }
+      }
+      named_bar_sync(1 + w, 128);
       if (ok && n > 0) ok = mbar_wait_warp(&bars->o_full[ob], (seg >> 1) & 1, wc);
       if (ok) {
-        // Each group joins half of the columns from both accumulators.
-        constexpr int H = NC / 2;
         uint32_t o0[H], o1[H];
         if (n > 0) {
           tc_fence_after();
@@ -540,36 +613,16 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
           tc_fence_before();
           mbar_arrive_warp(&bars->o_free[ob]);
         }
-        constexpr float kLn2 = 0.6931471805599453f;
-        const bool whole = pc.whole();
-        const long long part0 = (static_cast<long long>(blockIdx.x) * 2 + pc.slot()) * NQ;
 #pragma unroll
         for (int i = 0; i < H; ++i) {
           const int q = w * H + i;
           if (q >= cols) break;
-          auto sum = [&](int g) { return (rs[g * NC + q] + rs[(g + 1) * NC + q]) + (rs[(g + 2) * NC + q] + rs[(g + 3) * NC + q]); };
-          const float l0 = sum(0), l1 = sum(4), m0 = ms[q], m1 = ms[NC + q];
-          // A group without a visible key has the sum 0 and no part; a NaN among
-          // the scores makes a sum NaN, and O and lse with it.
-          const float top = l0 == 0.f ? m1 : l1 == 0.f ? m0 : fmaxf(m0, m1);
-          const float c0 = l0 == 0.f ? 0.f : ex2(m0 - top), c1 = l1 == 0.f ? 0.f : ex2(m1 - top);
-          const float le = l0 * c0 + l1 * c1;
-          float lo = le;
-          if constexpr (kRounded) lo = sum(8) * c0 + sum(12) * c1;
-          const float inv = lo == 0.f ? 0.f : 1.f / lo;
-          const float val = ((l0 == 0.f ? 0.f : __uint_as_float(o0[i]) * c0) + (l1 == 0.f ? 0.f : __uint_as_float(o1[i]) * c1)) * inv;
-          const float L = le == 0.f ? -INFINITY : (top + log2f(le)) * kLn2;
-          if (!whole) {
-            if (tid < D) a.part_o[(part0 + q) * D + tid] = val;
-            if (tid == 0) a.part_lse[part0 + q] = L;
-          } else {
-            const int t = static_cast<int>(q * gm >> 16), head = pc.h * G + q - t * G, prow = pc.s.row0 + pc.tok0 + t;
-            T* orow = static_cast<T*>(a.o) + prow * a.so.n + head * a.so.h;
-            if (tid < D) {
-              if constexpr (E::kFmt == 1) orow[tid] = __float2bfloat16_rn(val);
-              else orow[tid] = __float2half_rn(val);
-            }
-            if (tid == 0) a.lse[static_cast<long long>(head) * a.nt.total + prow] = L;
+          const Column c = coef[q];
+          const float val = (c.c0 != 0.f ? __uint_as_float(o0[i]) * c.c0 : 0.f) + (c.c1 != 0.f ? __uint_as_float(o1[i]) * c.c1 : 0.f);
+          if (tid < D) {
+            if (!whole) a.part_o[c.row + tid] = val;
+            else if constexpr (E::kFmt == 1) static_cast<T*>(a.o)[c.row + tid] = __float2bfloat16_rn(val);
+            else static_cast<T*>(a.o)[c.row + tid] = __float2half_rn(val);
           }
         }
       }
@@ -580,7 +633,7 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == C::MMA_WARP) tmem_dealloc(tmem, C::TM_COLS);
+  if (warp == C::S_WARP) tmem_dealloc(tmem, C::TM_COLS);
 }
 
 namespace {

@@ -32,6 +32,8 @@ struct PfCfg {
   static constexpr int BN = kKeyTile;
   static constexpr int NCHUNK = D / 64;
   static constexpr int CHUNK_BYTES = 128 * 128;
+  // A K or V tile: 16 groups of 8 rows, each NCHUNK swizzled atoms of 8 x 128 bytes.
+  static constexpr int GROUP = NCHUNK * 1024;
   static constexpr int TILE_BYTES = NCHUNK * CHUNK_BYTES;
   static constexpr int STAGES = D == 64 ? 4 : 2;
   static constexpr int OFF_Q = 0;
@@ -59,6 +61,7 @@ struct PfBars {
   uint64_t o_full[2], o_free[2];
   uint64_t mma_done;
   PagedCursor start;
+  PagedSeq seq;
   uint32_t tmem_base;
   int abort;
 };
@@ -99,11 +102,11 @@ __global__ void __launch_bounds__(384, 1)
   const int TT = a.tile_tokens, UT = 2 * TT, G = a.G;
 
   if (warp == 0) {
-    long long chunk;
-    const PagedCursor c = paged_start(a, UT, static_cast<int>(blockIdx.x), lane, &chunk);
+    PagedSeq s;
+    const PagedCursor c = paged_start(a, UT, lane, &s);
     if (lane == 0) {
       bars->start = c;
-      paged_note(a, c, chunk, static_cast<int>(blockIdx.x));
+      bars->seq = s;
     }
   }
   if (threadIdx.x == 32) {
@@ -139,7 +142,7 @@ __global__ void __launch_bounds__(384, 1)
   const uint32_t tmem = bars->tmem_base;
   const WaitCtl wc{&bars->abort, a.err};
   PagedCursor cur = bars->start;
-  PagedSeq seq = cur.left > 0 ? paged_seq(a, cur.b) : PagedSeq{};
+  PagedSeq seq = bars->seq;
   PagedPiece pc;
 
   if (warp == 8) {
@@ -177,23 +180,19 @@ __global__ void __launch_bounds__(384, 1)
         const int s = kt % C::STAGES;
         const uint32_t ph = ((kt / C::STAGES) & 1) ^ 1;
         const int next_page = t + 1 < pc.t_lo + n ? page_of(t + 1) : 0;
-        const int nb = boxes(t), off = t * C::BN & (ps - 1);
+        const int nb = boxes(t), group = (t * C::BN & (ps - 1)) >> 3;
         const uint32_t bytes = static_cast<uint32_t>(nb * box) * 128 * C::NCHUNK;
-        const int at = s * C::TILE_BYTES + lane * box * 128;
+        const int at = s * C::TILE_BYTES + lane * box * 128 * C::NCHUNK;
         if (!(ok = mbar_wait_warp(&bars->k_empty[s], ph, wc))) break;
         if (lane == 0) mbar_arrive_expect_tx(&bars->k_full[s], bytes);
         __syncwarp();
-        if (lane < nb)
-          for (int c = 0; c < C::NCHUNK; ++c)
-            tma_load_4d(&tm_k, &bars->k_full[s], smem + C::OFF_K + at + c * C::CHUNK_BYTES, c * 64, off, pc.h, page, pol_kv);
+        if (lane < nb) load_page(&tm_k, &bars->k_full[s], smem + C::OFF_K + at, a.pv, group, page, pc.h, true, pol_kv);
         __syncwarp();
         ++kt;
         if (!(ok = mbar_wait_warp(&bars->v_empty[s], ph, wc))) break;
         if (lane == 0) mbar_arrive_expect_tx(&bars->v_full[s], bytes);
         __syncwarp();
-        if (lane < nb)
-          for (int c = 0; c < C::NCHUNK; ++c)
-            tma_load_4d(&tm_v, &bars->v_full[s], smem + C::OFF_V + at + c * C::CHUNK_BYTES, c * 64, off, pc.h, page, pol_kv);
+        if (lane < nb) load_page(&tm_v, &bars->v_full[s], smem + C::OFF_V + at, a.pv, group, page, pc.h, false, pol_kv);
         __syncwarp();
         ++vt;
         page = next_page;
@@ -214,22 +213,23 @@ __global__ void __launch_bounds__(384, 1)
     constexpr uint32_t idesc_s = idesc_f16kind(E::kFmt, 128, C::BN, 0, 0);
     constexpr uint32_t idesc_o = idesc_f16kind(PE::kFmt, 128, D, 0, 1);
     const uint64_t q_desc = sdesc_sw128(smem_u32(smem + C::OFF_Q), 16, 1024);
-    const uint64_t k_desc = sdesc_sw128(smem_u32(smem + C::OFF_K), 16, 1024);
-    const uint64_t v_desc = sdesc_sw128(smem_u32(smem + C::OFF_V), C::CHUNK_BYTES, 1024);
+    const uint64_t k_desc = sdesc_sw128(smem_u32(smem + C::OFF_K), 16, C::GROUP);
+    const uint64_t v_desc = sdesc_sw128(smem_u32(smem + C::OFF_V), 1024, C::GROUP);
     constexpr uint32_t kTileDesc = C::TILE_BYTES >> 4;
     auto issue_s = [&](int t, int stage) {
       const uint64_t qa = q_desc + t * kTileDesc, kb = k_desc + stage * kTileDesc;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t off = ((kk >> 2) * C::CHUNK_BYTES + (kk & 3) * 32) >> 4;
-        mma_ss(tmem + C::tm_s(t), qa + off, kb + off, idesc_s, kk > 0);
+        mma_ss(tmem + C::tm_s(t), qa + (((kk >> 2) * C::CHUNK_BYTES + (kk & 3) * 32) >> 4),
+               kb + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), idesc_s, kk > 0);
       }
     };
     auto issue_pv = [&](int t, int stage, bool acc) {
       const uint64_t vb = v_desc + stage * kTileDesc;
 #pragma unroll
       for (int kk = 0; kk < C::BN / 16; ++kk)
-        mma_ts(tmem + C::tm_o(t), tmem + C::tm_p(t) + kk * 8, vb + ((kk * 16 * 128) >> 4), idesc_o, (acc || kk > 0) ? 1u : 0u);
+        mma_ts(tmem + C::tm_o(t), tmem + C::tm_p(t) + kk * 8, vb + ((kk * 2 * C::GROUP) >> 4), idesc_o,
+               (acc || kk > 0) ? 1u : 0u);
     };
     auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_warp(bar, parity, wc); };
     int kt = 0, seg = 0;
@@ -336,7 +336,9 @@ __global__ void __launch_bounds__(384, 1)
               if constexpr (kConvertV)
                 x[u] = make_uint4(pf_bf16x2_to_f16x2(x[u].x), pf_bf16x2_to_f16x2(x[u].y), pf_bf16x2_to_f16x2(x[u].z),
                                   pf_bf16x2_to_f16x2(x[u].w));
-              if ((((b0 + u) * 64 + ct) >> 3 & (C::BN - 1)) >= rows) x[u] = make_uint4(0, 0, 0, 0);
+              // 64 vectors an atom of 8 rows, 8 a row.
+              const int i = (b0 + u) * 64 + ct;
+              if (i / (64 * C::NCHUNK) * 8 + (i >> 3 & 7) >= rows) x[u] = make_uint4(0, 0, 0, 0);
               tile[(b0 + u) * 64 + ct] = x[u];
             }
           }

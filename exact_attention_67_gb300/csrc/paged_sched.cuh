@@ -65,8 +65,8 @@ struct PagedPiece {
 // A place in the line and the way through it.  UT: tokens a unit.
 struct PagedCursor {
   int b, h, t;
-  int pos;          // weights of unit t already passed
-  long long left;   // weights left of this CTA's chunk
+  int pos;    // weights of unit t already passed
+  int left;   // weights left of this CTA's chunk
 
   // The next piece with anything to do (an empty unit has its zeros to
   // write); false at the chunk's end.
@@ -88,7 +88,7 @@ struct PagedCursor {
       paged_keys(a, s, t0, t1, &lo, &hi);
       const int k0 = lo / kKeyTile, k1 = hi > lo ? (hi + kKeyTile - 1) / kKeyTile : k0;
       const int w = k1 - k0 + a.unit_cost;
-      const int take = static_cast<int>(min(left, static_cast<long long>(w - pos)));
+      const int take = min(left, w - pos);
       p->s = s;
       p->b = b;
       p->h = h;
@@ -112,89 +112,102 @@ struct PagedCursor {
   }
 };
 
-// Weight of sequence b's units with one key head.
-__device__ __forceinline__ long long paged_weight(const PagedArgs& a, const PagedSeq& s, int UT) {
-  long long w = 0;
-  for (int t0 = 0; t0 < s.n; t0 += UT) {
-    int lo, hi;
-    paged_keys(a, s, t0, min(s.n, t0 + UT), &lo, &hi);
-    const int k0 = lo / kKeyTile, k1 = hi > lo ? (hi + kKeyTile - 1) / kKeyTile : k0;
-    w += k1 - k0 + a.unit_cost;
-  }
+// Key tiles of the unit of tokens [t0, t0 + UT).
+__device__ __forceinline__ int paged_tiles(const PagedArgs& a, const PagedSeq& s, int t0, int UT) {
+  int lo, hi;
+  paged_keys(a, s, t0, min(s.n, t0 + UT), &lo, &hi);
+  return hi > lo ? (hi + kKeyTile - 1) / kKeyTile - lo / kKeyTile : 0;
+}
+
+// Weight of a sequence's units with one key head.
+__device__ __forceinline__ int paged_weight(const PagedArgs& a, const PagedSeq& s, int UT) {
+  int w = 0;
+  for (int t0 = 0; t0 < s.n; t0 += UT) w += paged_tiles(a, s, t0, UT) + a.unit_cost;
   return w;
 }
 
-// Start of CTA `cta`'s chunk, found by one warp; the same in every lane.  W and
-// chunk come back for the merge.
-__device__ __forceinline__ PagedCursor paged_start(const PagedArgs& a, int UT, int cta, int lane, long long* chunk_out) {
-  const int B = a.nt.B;
-  auto weight = [&](int b) {
-    return b < B ? paged_weight(a, paged_seq(a, b), UT) * a.Hkv : 0ll;
-  };
-  auto warp_sum = [](long long x) {
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    return x;
-  };
-  const long long w0 = weight(lane);  // kept: most batches have at most 32 sequences
-  long long W = warp_sum(w0);
-  for (int b0 = 32; b0 < B; b0 += 32) W += warp_sum(weight(b0 + lane));
-  long long chunk = (W + a.ctas - 1) / a.ctas;
-  if (chunk < a.min_chunk) chunk = a.min_chunk;
-  *chunk_out = chunk;
-  PagedCursor c;
-  const long long lo = cta * chunk;
-  c.left = min(chunk, W - lo);
-  c.b = c.h = c.t = c.pos = 0;
-  if (c.left <= 0) {
-    c.left = 0;
-    return c;
-  }
-  long long before = 0;
-  for (int b0 = 0; b0 < B; b0 += 32) {
-    const long long w = b0 == 0 ? w0 : weight(b0 + lane);
-    long long inc = w;  // inclusive prefix over the lanes
+// What the merge needs of the boundary before a CTA's chunk.
+struct PagedPlan {
+  int pos;           // weights of the unit before the boundary (0: it starts there)
+  int chunk;
+  int tiles;         // key tiles of the unit
+  int row, ntok, h;  // its first packed row, tokens, key head
+  int unused[2];
+};
+
+// Start of this CTA's chunk, found by one warp; the same in every lane.  Leaves
+// the merge its PagedPlan.  The line's weights fit 31 bits (checked on the host
+// against the largest that the sizes allow).
+__device__ __forceinline__ PagedCursor paged_start(const PagedArgs& a, int UT, int lane, PagedSeq* seq) {
+  const int B = a.nt.B, cta = static_cast<int>(blockIdx.x);
+  auto read = [&](int b) { return b < B ? paged_seq(a, b) : PagedSeq{0, 0, 0, 0}; };
+  const PagedSeq s0 = read(lane);
+  const int w0 = paged_weight(a, s0, UT) * a.Hkv;  // kept: most batches have at most 32 sequences
+  int W = __reduce_add_sync(0xffffffffu, w0);
+  for (int b0 = 32; b0 < B; b0 += 32) W += __reduce_add_sync(0xffffffffu, paged_weight(a, read(b0 + lane), UT) * a.Hkv);
+  const int chunk = max((W + a.ctas - 1) / a.ctas, a.min_chunk);
+  const long long lo64 = static_cast<long long>(cta) * chunk;
+  PagedCursor c{0, 0, 0, 0, 0};
+  PagedPlan plan{0, chunk, 0, 0, 0, 0, {0, 0}};
+  *seq = PagedSeq{0, 0, 0, 0};
+  int before = 0;
+  for (int b0 = 0; b0 < B && lo64 < W; b0 += 32) {
+    const int lo = static_cast<int>(lo64);
+    const PagedSeq sl = b0 == 0 ? s0 : read(b0 + lane);
+    const int w = b0 == 0 ? w0 : paged_weight(a, sl, UT) * a.Hkv;
+    int inc = w;  // inclusive prefix over the lanes
+#pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+      const int y = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += y;
     }
     const unsigned past = __ballot_sync(0xffffffffu, before + inc > lo);
     if (past) {
       const int l = __ffs(past) - 1;
+      PagedSeq s;
+      s.row0 = __shfl_sync(0xffffffffu, sl.row0, l);
+      s.n = __shfl_sync(0xffffffffu, sl.n, l);
+      s.len = __shfl_sync(0xffffffffu, sl.len, l);
+      s.off = __shfl_sync(0xffffffffu, sl.off, l);
+      const int per_head = __shfl_sync(0xffffffffu, w, l) / a.Hkv;
+      int r = lo - before - __shfl_sync(0xffffffffu, inc - w, l);
+      c.left = min(chunk, W - lo);
       c.b = b0 + l;
-      const long long start = before + __shfl_sync(0xffffffffu, inc - w, l);
-      const long long per_head = __shfl_sync(0xffffffffu, w, l) / a.Hkv;
-      long long r = lo - start;
-      c.h = static_cast<int>(r / per_head);
+      c.h = r / per_head;
       r -= c.h * per_head;
-      const PagedSeq s = paged_seq(a, c.b);
+      int tiles;
       for (;;) {
-        int klo, khi;
-        paged_keys(a, s, c.t * UT, min(s.n, (c.t + 1) * UT), &klo, &khi);
-        const int k0 = klo / kKeyTile, k1 = khi > klo ? (khi + kKeyTile - 1) / kKeyTile : k0;
-        const int u = k1 - k0 + a.unit_cost;
-        if (r < u) break;
-        r -= u;
+        tiles = paged_tiles(a, s, c.t * UT, UT);
+        if (r < tiles + a.unit_cost) break;
+        r -= tiles + a.unit_cost;
         ++c.t;
       }
-      c.pos = static_cast<int>(r);
-      return c;
+      c.pos = r;
+      *seq = s;
+      plan = PagedPlan{r, chunk, tiles, s.row0 + c.t * UT, min(UT, s.n - c.t * UT), c.h, {0, 0}};
+      break;
     }
     before += __shfl_sync(0xffffffffu, inc, 31);
   }
-  c.left = 0;
+  if (lane == 0) a.plan[cta] = plan;
   return c;
 }
 
-// What CTA `cta` found, for the merge.
-__device__ __forceinline__ void paged_note(const PagedArgs& a, const PagedCursor& c, long long chunk, int cta) {
-  int* p = a.plan + cta * 8;
-  p[0] = c.left > 0 ? 1 : 0;
-  p[1] = c.b;
-  p[2] = c.h;
-  p[3] = c.t;
-  p[4] = c.pos;
-  p[5] = static_cast<int>(chunk & 0x7fffffff);
-  p[6] = static_cast<int>(chunk >> 31);
+// One page's (at most 128) rows of a K or V tile: a box of the 5-D map
+// (64 elements, 8 rows, d / 64, groups of 8 rows, places), which lands as groups
+// of 8 rows, each with its 64-element atoms side by side.  A place is a (page,
+// key head), so K and V of any strides take one box a page whatever d is.  A
+// page outside the pool loads zeros (a place before the map's first).
+__device__ __forceinline__ void load_page(const CUtensorMap* m, uint64_t* bar, void* dst, const PageView& pv, int group,
+                                          int page, int head, bool is_k, uint64_t cache_hint) {
+  const int place = page >= 0 && page < pv.num_pages
+                        ? page * (is_k ? pv.k_page_step : pv.v_page_step) + head * (is_k ? pv.k_head_step : pv.v_head_step)
+                        : -1;
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %3, %3, %4, %5}], [%2], %6;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(0), "r"(group), "r"(place), "l"(cache_hint)
+      : "memory");
 }
 
 }  // namespace exattn
