@@ -63,7 +63,7 @@ struct PdCfg {
   static constexpr int OFF_RED = OFF_P + 2 * P_TILE;
   static constexpr int RED_REF = 8 * NC, RED_SUM = RED_REF + 4 * NC, RED_COEF = RED_SUM + 32 * NC;
   static constexpr int OFF_BAR = OFF_RED + (RED_COEF + 8 * NC) * 4;
-  static constexpr int SMEM_BYTES = OFF_BAR + 512 + 1024;
+  static constexpr int SMEM_BYTES = OFF_BAR + 1024 + 1024;
   static_assert(SMEM_BYTES <= 232448, "over the 227 KB shared-memory limit");
   static constexpr int K_WARP = 8, V_WARP = 9, S_WARP = 10, O_WARP = 11, READY_WARP = 12, THREADS = 512;
   // Registers: 128 a thread at launch; with 32 columns the elementwise warpgroups
@@ -81,8 +81,7 @@ struct PdBars {
   uint64_t s_full[4], s_free[4], p_full[2], p_free[2];
   uint64_t o_full[2], o_free[2];
   uint64_t done[2];  // teardown: all of the issuing warp's products
-  PagedCursor start;
-  PagedSeq seq;
+  PagedRing ring;
   uint32_t tmem_base;
   int abort;
 };
@@ -189,7 +188,7 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
   constexpr bool kConvertV = E::kFmt != PE::kFmt;
   constexpr bool kRounded = !kConvertV;  // O normalised by the rounded weights' sum
   constexpr int NQ = C::NQ, BN = C::BN;
-  static_assert(sizeof(Bars) <= 512, "barrier block too large");
+  static_assert(sizeof(Bars) <= 1024, "barrier block too large");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Bars* bars = reinterpret_cast<Bars*>(smem + C::OFF_BAR);
@@ -197,14 +196,10 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int UT = a.tile_tokens, G = a.G;
 
-  if (warp == 0) {
-    PagedSeq s;
-    const PagedCursor c = paged_start(a, UT, lane, &s);
-    if (lane == 0) {
-      bars->start = c;
-      bars->seq = s;
-    }
-  }
+  // The walking warp finds its place while the others set up.
+  PagedCursor cur{};
+  PagedSeq seq{};
+  if (warp == C::K_WARP) cur = paged_start(a, UT, lane, &seq);
   if (threadIdx.x == 32) {
     for (int b = 0; b < 2; ++b) {
       mbar_init(&bars->q_full[b], 1);
@@ -226,6 +221,7 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
       mbar_init(&bars->v_empty[s], 1);
       mbar_init(&bars->v_ready[s], 4);
     }
+    bars->ring.init(15);  // all but the walking warp
     bars->abort = 0;
     fence_barrier_init();
   }
@@ -233,7 +229,7 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
     tmem_alloc(&bars->tmem_base, C::TM_COLS);
     tmem_relinquish();
   }
-  if (warp == C::K_WARP && lane == 0) {
+  if (warp == C::V_WARP && lane == 0) {
     tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
@@ -249,9 +245,7 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tmem = bars->tmem_base;
   const WaitCtl wc{&bars->abort, a.err};
-  PagedCursor cur = bars->start;
-  PagedSeq seq = bars->seq;
-  PagedPiece pc;
+  PagedRing& ring = bars->ring;
 
   if constexpr (C::SPLIT_REGS) {
     if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
@@ -269,7 +263,17 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
     const uint32_t q_bytes = static_cast<uint32_t>(UT * G) * 128 * C::NCHUNK;
     int st = 0, seg = 0;
     bool ok = true;
-    while (ok && cur.next(a, UT, seq, &pc)) {
+    for (int i = 0; ok; ++i) {
+      PagedPiece pc;
+      if (is_k) {
+        const bool more = cur.next(a, UT, seq, &pc);
+        if (!(ok = ring.put(i, more ? &pc : nullptr, lane, wc)) || !more) break;
+      } else {
+        const PagedPiece* p = ring.get(i, wc);
+        if (!p) break;
+        pc = *p;
+        ring.release(i);
+      }
       if (pc.t_hi == pc.t_lo) continue;
       const int* row = a.pv.table + pc.b * a.pv.table_stride;
       // Boxes of a tile that hold a visible key, and this lane's page of it.
@@ -318,12 +322,16 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
     auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_warp(bar, parity, wc); };
     int st = 0, seg = 0;
     bool ok = true;
-    while (ok && cur.next(a, UT, seq, &pc)) {
-      if (pc.t_hi == pc.t_lo) continue;
+    for (int i = 0; ok; ++i) {
+      const PagedPiece* pc = ring.get(i, wc);
+      if (!pc) break;
+      const int n = pc->t_hi - pc->t_lo;
+      ring.release(i);
+      if (n == 0) continue;
       const int qb = seg % C::QBUF;
       if (!(ok = wait(&bars->q_full[qb], (seg / C::QBUF) & 1))) break;
       const uint64_t qd = q_desc + ((qb * C::Q_TILE) >> 4);
-      for (int t = pc.t_lo; t < pc.t_hi; ++t, ++st) {
+      for (int j = 0; j < n; ++j, ++st) {
         const int s = st % C::STAGES, b = st & 3;
         if (!(ok = wait(&bars->k_full[s], (st / C::STAGES) & 1))) break;
         if (st >= 4 && !(ok = wait(&bars->s_free[b], ((st >> 2) - 1) & 1))) break;
@@ -336,7 +344,7 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
                    qd + (((kk >> 2) * C::Q_CHUNK + (kk & 3) * 32) >> 4), idesc, kk > 0);
           mma_commit(&bars->s_full[b]);
           mma_commit(&bars->k_empty[s]);
-          if (t == pc.t_hi - 1) mma_commit(&bars->q_empty[qb]);
+          if (j == n - 1) mma_commit(&bars->q_empty[qb]);
         }
         __syncwarp();
       }
@@ -357,8 +365,11 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
     auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_warp(bar, parity, wc); };
     int st = 0, seg = 0;
     bool ok = true;
-    while (ok && cur.next(a, UT, seq, &pc)) {
-      const int n = pc.t_hi - pc.t_lo, ob = seg & 1;
+    for (int i = 0; ok; ++i) {
+      const PagedPiece* pc = ring.get(i, wc);
+      if (!pc) break;
+      const int n = pc->t_hi - pc->t_lo, ob = seg & 1;
+      ring.release(i);
       if (n == 0) continue;
       for (int j = 0; j < n; ++j, ++st) {
         const int s = st % C::STAGES, w = st & 1;
@@ -391,9 +402,13 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
     const int ct = threadIdx.x - 32 * C::READY_WARP;
     int st = 0;
     bool ok = true;
-    while (ok && cur.next(a, UT, seq, &pc)) {
-      for (int t = pc.t_lo; t < pc.t_hi; ++t, ++st) {
-        const int s = st % C::STAGES, rows = pc.key_hi - t * BN;
+    for (int k = 0; ok; ++k) {
+      const PagedPiece* pc = ring.get(k, wc);
+      if (!pc) break;
+      const int t_lo = pc->t_lo, t_hi = pc->t_hi, key_hi = pc->key_hi;
+      ring.release(k);
+      for (int t = t_lo; t < t_hi; ++t, ++st) {
+        const int s = st % C::STAGES, rows = key_hi - t * BN;
         if (!(ok = mbar_wait_warp(&bars->v_full[s], (st / C::STAGES) & 1, wc))) break;
         uint4* tile = reinterpret_cast<uint4*>(smem + C::OFF_V + s * C::KV_TILE);
         if (kConvertV || rows < BN) {
@@ -430,11 +445,14 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
     const uint32_t gm = 65536u / G + 1;                          // q / G == q * gm >> 16 for q < 32, G <= 32
     int st = 0, seg = 0, pieces = 0;
     bool ok = true;
-    // Every warp of the group runs every step and meets its barriers (id 1 + w),
-    // also after a bounded wait has given up: then without the work.
-    for (; cur.next(a, UT, seq, &pc); ++pieces) {
-      const int cols = pc.ntok * G, n = pc.t_hi - pc.t_lo, ob = seg & 1;
-      const int p0 = pc.s.off + pc.tok0, p1 = p0 + pc.ntok - 1;  // first and last position
+    // Every warp of the group runs every step of a piece and meets its barriers
+    // (id 1 + w), also after a bounded wait has given up: then without the work.
+    for (;; ++pieces) {
+      // The eight warps go on or stop as one: the joint barriers count them all.
+      const PagedPiece* pc = ok ? ring.get(pieces, wc) : nullptr;
+      if (bar_any(3, 256, pc == nullptr)) break;
+      const int cols = pc->ntok * G, n = pc->t_hi - pc->t_lo, ob = seg & 1, t_lo = pc->t_lo, key_hi = pc->key_hi;
+      const int p0 = pc->s.off + pc->tok0, p1 = p0 + pc->ntok - 1;  // first and last position
       const uint32_t tO = tmem + lane_bits + C::TM_O + (ob * 2 + w) * NQ;
       const uint32_t all = cols < 32 ? (1u << cols) - 1 : ~0u;
       uint32_t none = all;  // columns that have seen no key: their reference is 0 so far
@@ -456,14 +474,14 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
           mbar_arrive_warp(&bars->s_free[s & 3]);
 #pragma unroll
           for (int q = 0; q < NC; ++q) y[q] = fmaf(__uint_as_float(sv[q]), a.scale_log2, -m[q]);
-          const int kj0 = (pc.t_lo + j) * BN;
-          if (kj0 + BN > pc.key_hi || (a.causal && kj0 + BN - 1 > p0) ||
+          const int kj0 = (t_lo + j) * BN;
+          if (kj0 + BN > key_hi || (a.causal && kj0 + BN - 1 > p0) ||
               (a.window > 0 && (p1 - kj0 >= a.window || (!a.causal && kj0 + BN - 1 - p0 >= a.window)))) {
             // This key's visible columns [lo, hi): tokens are G columns each, and
             // a token sees a key by its distance only.
             const int dist = kj0 + tid - p0;  // from token 0's position
             auto column = [&](int token) { return min(max(token, 0), NC) * G; };
-            int lo = 0, hi = kj0 + tid < pc.key_hi ? NC : 0;
+            int lo = 0, hi = kj0 + tid < key_hi ? NC : 0;
             if (a.causal) lo = column(dist);
             if (a.window > 0) {
               hi = min(hi, column(dist + a.window));
@@ -576,7 +594,7 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
       // Each group joins half of the columns from both accumulators.  Their
       // coefficients, a lane each:
       constexpr int H = NC / 2;
-      const bool whole = pc.whole();
+      const bool whole = pc->whole();
       if (wl == 0 && lane < H) {
         const int q = w * H + lane;
         auto sum = [&](int g) {
@@ -593,8 +611,8 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
         if constexpr (kRounded) lo = sum(2) * c0 + sum(3) * c1;
         const float inv = lo == 0.f ? 0.f : 1.f / lo;
         const float L = le == 0.f ? -INFINITY : (top + log2f(le)) * 0.6931471805599453f;
-        const int t = static_cast<int>(q * gm >> 16), head = pc.h * G + q - t * G, prow = pc.s.row0 + pc.tok0 + t;
-        const long long part = (static_cast<long long>(blockIdx.x) * 2 + pc.slot()) * NQ + q;
+        const int t = static_cast<int>(q * gm >> 16), head = pc->h * G + q - t * G, prow = pc->s.row0 + pc->tok0 + t;
+        const long long part = (static_cast<long long>(blockIdx.x) * 2 + pc->slot()) * NQ + q;
         coef[q] = Column{c0 * inv, c1 * inv, whole ? prow * a.so.n + head * a.so.h : part * D};
         if (ok && q < cols) {
           if (whole) a.lse[static_cast<long long>(head) * a.nt.total + prow] = L;
@@ -626,6 +644,7 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
           }
         }
       }
+      ring.release(pieces);
       if (n > 0) ++seg;
     }
   }

@@ -40,7 +40,7 @@ struct PfCfg {
   static constexpr int OFF_K = OFF_Q + 2 * TILE_BYTES;
   static constexpr int OFF_V = OFF_K + STAGES * TILE_BYTES;
   static constexpr int OFF_BAR = OFF_V + STAGES * TILE_BYTES;
-  static constexpr int SMEM_BYTES = OFF_BAR + 512 + 1024;
+  static constexpr int SMEM_BYTES = OFF_BAR + 1024 + 1024;
   static_assert(SMEM_BYTES > 120 * 1024, "one CTA per SM: it holds all 512 TMEM columns");
   static constexpr int THREADS = 384;
   // TMEM as in fwd.cu: at d = 64 P has columns of its own, so that the next S_t
@@ -60,8 +60,7 @@ struct PfBars {
   uint64_t s_full[2], s_free[2], p_full[2], pv_done[2];
   uint64_t o_full[2], o_free[2];
   uint64_t mma_done;
-  PagedCursor start;
-  PagedSeq seq;
+  PagedRing ring;
   uint32_t tmem_base;
   int abort;
 };
@@ -94,21 +93,17 @@ __global__ void __launch_bounds__(384, 1)
   using PE = Elem<__half>;
   using Bars = PfBars<C::STAGES>;
   constexpr bool kConvertV = E::kFmt != PE::kFmt;
-  static_assert(sizeof(Bars) <= 512, "barrier block too large");
+  static_assert(sizeof(Bars) <= 1024, "barrier block too large");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Bars* bars = reinterpret_cast<Bars*>(smem + C::OFF_BAR);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int TT = a.tile_tokens, UT = 2 * TT, G = a.G;
 
-  if (warp == 0) {
-    PagedSeq s;
-    const PagedCursor c = paged_start(a, UT, lane, &s);
-    if (lane == 0) {
-      bars->start = c;
-      bars->seq = s;
-    }
-  }
+  // The walking warp finds its place while the others set up.
+  PagedCursor cur{};
+  PagedSeq seq{};
+  if (warp == 8) cur = paged_start(a, UT, lane, &seq);
   if (threadIdx.x == 32) {
     mbar_init(&bars->q_full, 1);
     mbar_init(&bars->q_empty, 1);
@@ -128,6 +123,7 @@ __global__ void __launch_bounds__(384, 1)
       mbar_init(&bars->v_empty[s], 1);
       mbar_init(&bars->v_ready[s], 2);
     }
+    bars->ring.init(11);  // all but the walking warp
     bars->abort = 0;
     fence_barrier_init();
   }
@@ -141,9 +137,7 @@ __global__ void __launch_bounds__(384, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tmem = bars->tmem_base;
   const WaitCtl wc{&bars->abort, a.err};
-  PagedCursor cur = bars->start;
-  PagedSeq seq = bars->seq;
-  PagedPiece pc;
+  PagedRing& ring = bars->ring;
 
   if (warp == 8) {
     // ------------------------------------------------------------ TMA producer
@@ -159,7 +153,10 @@ __global__ void __launch_bounds__(384, 1)
     const uint32_t q_bytes = static_cast<uint32_t>(TT * G) * 128 * C::NCHUNK;
     int kt = 0, vt = 0, seg = 0;  // key tiles and Qs issued
     bool ok = true;
-    while (ok && cur.next(a, UT, seq, &pc)) {
+    for (int i = 0; ok; ++i) {
+      PagedPiece pc;
+      const bool more = cur.next(a, UT, seq, &pc);
+      if (!(ok = ring.put(i, more ? &pc : nullptr, lane, wc)) || !more) break;
       const int n0 = tiles_of(a, pc, 0), n1 = tiles_of(a, pc, 1), n = max(n0, n1);
       if (n == 0) continue;
       if (seg >= 1 && !(ok = mbar_wait_warp(&bars->q_empty, (seg - 1) & 1, wc))) break;
@@ -248,8 +245,11 @@ __global__ void __launch_bounds__(384, 1)
       __syncwarp();
       ++cs[t];
     };
-    while (ok && cur.next(a, UT, seq, &pc)) {
-      const int nt[2] = {tiles_of(a, pc, 0), tiles_of(a, pc, 1)};
+    for (int i = 0; ok; ++i) {
+      const PagedPiece* pc = ring.get(i, wc);
+      if (!pc) break;
+      const int nt[2] = {tiles_of(a, *pc, 0), tiles_of(a, *pc, 1)};
+      ring.release(i);
       const int n = max(nt[0], nt[1]);
       if (n == 0) continue;
       if (!(ok = wait(&bars->q_full, seg & 1))) break;
@@ -319,10 +319,13 @@ __global__ void __launch_bounds__(384, 1)
     const int ct = (warp - 10) * 32 + lane;
     int vt = 0;
     bool ok = true;
-    while (ok && cur.next(a, UT, seq, &pc)) {
-      const int n = max(tiles_of(a, pc, 0), tiles_of(a, pc, 1));
+    for (int i = 0; ok; ++i) {
+      const PagedPiece* pc = ring.get(i, wc);
+      if (!pc) break;
+      const int n = max(tiles_of(a, *pc, 0), tiles_of(a, *pc, 1)), keys = pc->key_hi - pc->t_lo * C::BN;
+      ring.release(i);
       for (int j = 0; j < n; ++j, ++vt) {
-        const int s = vt % C::STAGES, rows = pc.key_hi - (pc.t_lo + j) * C::BN;
+        const int s = vt % C::STAGES, rows = keys - j * C::BN;
         if (!(ok = mbar_wait_warp(&bars->v_full[s], (vt / C::STAGES) & 1, wc))) break;
         uint4* tile = reinterpret_cast<uint4*>(smem + C::OFF_V + s * C::TILE_BYTES);
         if (kConvertV || rows < C::BN) {
@@ -351,18 +354,28 @@ __global__ void __launch_bounds__(384, 1)
     // ------------------------------------------------------------ softmax
     const int t = warp >> 2, wq = warp & 3;
     const int row = wq * 32 + lane;  // row of the query tile == TMEM lane
-    const int row_tok = row / G, row_head = row % G;
     const uint32_t lane_bits = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t tS = tmem + lane_bits + C::tm_s(t);
     const uint32_t tP = tmem + lane_bits + C::tm_p(t);
     const uint32_t tO = tmem + lane_bits + C::tm_o(t);
     int cs = 0, co = 0;
     bool ok = true;
-    while (ok && cur.next(a, UT, seq, &pc)) {
-      const int n = tiles_of(a, pc, t);
-      const int tok0 = pc.tok0 + t * TT;
-      const int first = pc.s.off + tok0, last = first + TT - 1;  // positions of the tile's rows
-      const int pos = first + row_tok;
+    for (int i = 0; ok; ++i) {
+      const PagedPiece* pc = ring.get(i, wc);
+      if (!pc) break;
+      // The steps before `low` have some row with hidden keys below its window,
+      // those from `high` on some row with hidden keys above.
+      const int n = tiles_of(a, *pc, t);
+      int low = 0, high = (pc->key_hi - pc->t_lo * C::BN) / C::BN;
+      {
+        const int first = pc->s.off + pc->tok0 + t * TT - pc->t_lo * C::BN;  // first position, from the first key
+        // Division rounds towards 0: what it should put below 0 is masked from 0 on.
+        if (a.causal) high = min(high, (first + 1) / C::BN);
+        else if (a.window > 0) high = min(high, (first + a.window) / C::BN);
+        if (a.window > 0) low = (first + TT - a.window + C::BN - 1) / C::BN;
+      }
+      // This row's position, from the first key of step j's tile.
+      auto pos_from = [&](int j) { return pc->s.off + pc->tok0 + t * TT + row / G - (pc->t_lo + j) * C::BN; };
       float m_ref = -INFINITY;  // reference maximum, log2 units
       float le = 0.f, lb = 0.f; // sums of the unrounded and (f16) the rounded weights
       for (int j = 0; j < n; ++j, ++cs) {
@@ -378,19 +391,23 @@ __global__ void __launch_bounds__(384, 1)
           tc_fence_before();
           mbar_arrive_warp(&bars->s_free[t]);
         }
-        const int kv0 = (pc.t_lo + j) * C::BN;
-        const bool need_mask = kv0 + C::BN > pc.key_hi || (a.causal && kv0 + C::BN - 1 > first) ||
-                               (a.window > 0 && (kv0 < last - a.window + 1 || (!a.causal && kv0 + C::BN - 1 > first + a.window - 1)));
-        if (need_mask) {
-          int lim = pc.key_hi - kv0;  // visible columns c: lo <= c < lim
-          if (a.causal) lim = min(lim, pos - kv0 + 1);
-          else if (a.window > 0) lim = min(lim, pos + a.window - kv0);
-          const int lo = a.window > 0 ? pos - a.window + 1 - kv0 : 0;
+        if (j >= high) {
+          int x = pc->key_hi - (pc->t_lo + j) * C::BN;  // visible: columns below x
+          if (a.causal) x = min(x, pos_from(j) + 1);
+          else if (a.window > 0) x = min(x, pos_from(j) + a.window);
 #pragma unroll
           for (int c = 0; c < 4; ++c)
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              if (c * 32 + e >= lim || c * 32 + e < lo) sr[c][e] = __float_as_uint(-INFINITY);
+              if (c * 32 + e >= x) sr[c][e] = __float_as_uint(-INFINITY);
+        }
+        if (j < low) {
+          const int x = pos_from(j) - a.window + 1;  // visible: columns from x on
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (c * 32 + e < x) sr[c][e] = __float_as_uint(-INFINITY);
         }
         float mx;
         {
@@ -441,7 +458,7 @@ __global__ void __launch_bounds__(384, 1)
         }
         if (rescale_warp) {
           // d = 128: S_t of this step was issued after P_t V of the last one.
-#pragma unroll(D == 128 ? 1 : D / 32)
+#pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t o_r[32];
             tmem_ld32(tO + c * 32, o_r);
@@ -478,41 +495,46 @@ __global__ void __launch_bounds__(384, 1)
       // No visible key: 0 and -inf.  A NaN among the scores makes the sum NaN.
       const float inv_l = l == 0.f ? 0.f : 1.f / l;
       const float L = le == 0.f ? -INFINITY : (m_ref + log2f(le)) * 0.6931471805599453f;
-      const bool live = row_tok < TT && tok0 + row_tok < pc.tok0 + pc.ntok;
-      const bool whole = pc.whole();
-      const long long prow = (static_cast<long long>(blockIdx.x) * 2 + pc.slot()) * kPagedRows + t * 128 + row;
-      const int grow = pc.s.row0 + tok0 + row_tok, head = pc.h * G + row_head;
-      T* orow = static_cast<T*>(a.o) + grow * a.so.n + head * a.so.h;
-#pragma unroll
+      const int row_tok = row / G, tok = t * TT + row_tok, prow = pc->s.row0 + pc->tok0 + tok, head = pc->h * G + row % G;
+      const bool live = row_tok < TT && tok < pc->ntok, whole = pc->whole();
+      // Partial results lie [d / 4][row][4]: a warp's rows side by side.
+      const long long part = (static_cast<long long>(blockIdx.x) * 2 + pc->slot()) * 2 + t;
+      float4* po = reinterpret_cast<float4*>(a.part_o + part * 128 * D) + row;
+      T* orow = static_cast<T*>(a.o) + prow * a.so.n + head * a.so.h;
+      ring.release(i);
+#pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o_r[32];
+        float v[32];
         if (n > 0) {
           tmem_ld32(tO + c * 32, o_r);
           tmem_wait_ld();
           tmem_reg_fence(o_r);
         }
-        float v[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) v[e] = l == 0.f || n == 0 ? 0.f : __uint_as_float(o_r[e]) * inv_l;
-        if (live && whole) {
+        if (whole) {
           uint4* dst = reinterpret_cast<uint4*>(orow + c * 32);
+          if (live) {
 #pragma unroll
-          for (int v4 = 0; v4 < 4; ++v4)
-            dst[v4] = make_uint4(E::pack(v[8 * v4], v[8 * v4 + 1]), E::pack(v[8 * v4 + 2], v[8 * v4 + 3]),
-                                 E::pack(v[8 * v4 + 4], v[8 * v4 + 5]), E::pack(v[8 * v4 + 6], v[8 * v4 + 7]));
-        } else if (live && n > 0) {
-          float4* dst = reinterpret_cast<float4*>(a.part_o + prow * D + c * 32);
+            for (int v4 = 0; v4 < 4; ++v4)
+              dst[v4] = make_uint4(E::pack(v[8 * v4], v[8 * v4 + 1]), E::pack(v[8 * v4 + 2], v[8 * v4 + 3]),
+                                   E::pack(v[8 * v4 + 4], v[8 * v4 + 5]), E::pack(v[8 * v4 + 6], v[8 * v4 + 7]));
+          }
+        } else if (n > 0) {
 #pragma unroll
-          for (int v4 = 0; v4 < 8; ++v4) dst[v4] = make_float4(v[4 * v4], v[4 * v4 + 1], v[4 * v4 + 2], v[4 * v4 + 3]);
+          for (int v4 = 0; v4 < 8; ++v4)
+            po[(c * 8 + v4) * 128] = make_float4(v[4 * v4], v[4 * v4 + 1], v[4 * v4 + 2], v[4 * v4 + 3]);
         }
       }
       if (n > 0) {
         tc_fence_before();
         mbar_arrive_warp(&bars->o_free[t]);
       }
-      if (live) {
-        if (whole) a.lse[static_cast<long long>(head) * a.nt.total + grow] = L;
-        else a.part_lse[prow] = L;
+      if (whole) {
+        if (live) a.lse[static_cast<long long>(head) * a.nt.total + prow] = L;
+      } else {
+        a.part_lse[part * 128 + row] = L;
       }
     }
   }

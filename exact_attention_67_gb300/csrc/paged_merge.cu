@@ -14,9 +14,9 @@ namespace exattn {
 
 namespace {
 
-// Two rows a block, WPR warps each: two where a unit has few pieces, or all of
-// them many rows; eight for the decode kernel's rows when they are so few that
-// each chain of loads over the pieces, as many as there are CTAs, is the kernel.
+// The decode kernel's rows: two a block, WPR warps each.  Eight where there are
+// so few rows that a row's chain of loads over the pieces, as many as there are
+// CTAs, would be the kernel; else two.
 template <typename T, int D, int WPR>
 __global__ void __launch_bounds__(64 * WPR) paged_merge_kernel(const __grid_constant__ PagedArgs a) {
   constexpr int V = D / 32;      // columns a lane
@@ -30,10 +30,8 @@ __global__ void __launch_bounds__(64 * WPR) paged_merge_kernel(const __grid_cons
   if (p.pos == 0 || p.pos > p.chunk) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = static_cast<int>(blockIdx.y) * 2 + warp / WPR, part = warp % WPR;
-  // Row r of a unit lies in query tile r / 128 at the forward kernel (tiles of
-  // tile_tokens G rows), in the only one at the decode kernel.
-  const int tr = row % 128, tok = row / 128 * a.tile_tokens + tr / a.G;
-  const bool live = tr < a.tile_tokens * a.G && tok < p.ntok;
+  const int tok = row / a.G;
+  const bool live = tok < p.ntok;
   // Pieces: CTA g - 1 + i has the weights [i chunk - lead, (i + 1) chunk - lead)
   // of the unit, lead those of its chunk that lie before it.
   const int w = p.tiles + a.unit_cost, lead = p.chunk - p.pos;
@@ -103,7 +101,7 @@ __global__ void __launch_bounds__(64 * WPR) paged_merge_kernel(const __grid_cons
     for (int c = 0; c < V; ++c) acc[c] += acc_s[warp + i][lane * V + c];
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const int head = p.h * a.G + tr % a.G, prow = p.row + tok;
+  const int head = p.h * a.G + row % a.G, prow = p.row + tok;
   T* out = static_cast<T*>(a.o) + prow * a.so.n + head * a.so.h + lane * V;
 #pragma unroll
   for (int c = 0; c < V; c += 2)
@@ -111,21 +109,74 @@ __global__ void __launch_bounds__(64 * WPR) paged_merge_kernel(const __grid_cons
   if (lane == 0) a.lse[static_cast<long long>(head) * a.nt.total + prow] = sum == 0.f ? -INFINITY : m + logf(sum);
 }
 
+// The forward kernel's rows: a block takes 32 of a query tile, a lane each (their
+// partial results lie side by side), a warp a quarter of the columns.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) paged_merge_rows_kernel(const __grid_constant__ PagedArgs a) {
+  constexpr int C4 = D / 16;  // 4-column vectors a warp
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int g = static_cast<int>(blockIdx.x) + 1;
+  const PagedPlan p = a.plan[g];
+  if (p.pos == 0 || p.pos > p.chunk) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int t = static_cast<int>(blockIdx.y) >> 2, row = (static_cast<int>(blockIdx.y) & 3) * 32 + lane;
+  const int row_tok = row / a.G, tok = t * a.tile_tokens + row_tok;
+  const int w = p.tiles + a.unit_cost, lead = p.chunk - p.pos;
+  const int pieces = (w + lead + p.chunk - 1) / p.chunk;
+  auto tiles_before = [&](int x) { return max(0, min(w, x) - a.unit_cost); };
+  auto from = [&](int i) { return tiles_before(i * p.chunk - lead); };
+  int used = 0;
+  for (int i = 0; i < pieces && used < 2; ++i) used += from(i + 1) > from(i);
+  if (used < 2) return;
+  auto part = [&](int i) { return (static_cast<long long>(g - 1 + i) * 2 + (from(i) == 0)) * 2 + t; };
+  const bool live = row_tok < a.tile_tokens && tok < p.ntok;
+  float m = -INFINITY;
+  for (int i = 0; i < pieces; ++i)
+    if (live && from(i + 1) > from(i)) m = fmaxf(m, a.part_lse[part(i) * 128 + row]);
+  float4 acc[C4];
+#pragma unroll
+  for (int c = 0; c < C4; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+  float sum = 0.f;
+  for (int i = 0; i < pieces; ++i) {
+    if (!live || from(i + 1) <= from(i)) continue;
+    const float l = a.part_lse[part(i) * 128 + row];
+    if (l == -INFINITY) continue;  // a piece that this row saw no key of: its O may not be written
+    const float e = expf(l - m);
+    sum += e;
+    const float4* po = reinterpret_cast<const float4*>(a.part_o + part(i) * 128 * D) + warp * C4 * 128 + row;
+#pragma unroll
+    for (int c = 0; c < C4; ++c) {
+      const float4 x = po[c * 128];
+      acc[c] = make_float4(fmaf(e, x.x, acc[c].x), fmaf(e, x.y, acc[c].y), fmaf(e, x.z, acc[c].z), fmaf(e, x.w, acc[c].w));
+    }
+  }
+  if (!live) return;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const int head = p.h * a.G + row % a.G, prow = p.row + tok;
+  uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(a.o) + prow * a.so.n + head * a.so.h + warp * C4 * 4);
+#pragma unroll
+  for (int c = 0; c < C4; c += 2)
+    out[c / 2] = make_uint4(Elem<T>::pack(acc[c].x * inv, acc[c].y * inv), Elem<T>::pack(acc[c].z * inv, acc[c].w * inv),
+                            Elem<T>::pack(acc[c + 1].x * inv, acc[c + 1].y * inv),
+                            Elem<T>::pack(acc[c + 1].z * inv, acc[c + 1].w * inv));
+  if (warp == 0) a.lse[static_cast<long long>(head) * a.nt.total + prow] = sum == 0.f ? -INFINITY : m + logf(sum);
+}
+
 template <typename T, int D>
 cudaError_t launch_t(const PagedArgs& a, cudaStream_t stream) {
-  const int rows = a.cols > 0 ? a.cols : a.rows;
-  const bool deep = a.cols > 0 && rows <= 8;
+  const bool few = a.cols > 0, deep = few && a.cols <= 8;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.ctas - 1, rows / 2);
+  cfg.gridDim = dim3(a.ctas - 1, few ? a.cols / 2 : 8);
   cfg.blockDim = dim3(deep ? 512 : 128);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = deep ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<T, D, 8>, a)
-                             : cudaLaunchKernelEx(&cfg, paged_merge_kernel<T, D, 2>, a);
+  const cudaError_t e = deep  ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<T, D, 8>, a)
+                        : few ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<T, D, 2>, a)
+                              : cudaLaunchKernelEx(&cfg, paged_merge_rows_kernel<T, D>, a);
   const cudaError_t last = cudaGetLastError();
   return note_cuda(e != cudaSuccess ? e : last, "paged merge kernel launch");
 }

@@ -62,6 +62,41 @@ struct PagedPiece {
   __device__ int slot() const { return t_lo == k_lo ? 1 : 0; }
 };
 
+// The pieces of a CTA's chunk in order, from the warp that walks the line to the
+// other warps: they keep no state of the walk, and hold a slot as long as they
+// read it.  A piece with ntok = 0 ends the chunk.
+constexpr int kRing = 4;
+struct PagedRing {
+  uint64_t full[kRing], empty[kRing];
+  PagedPiece piece[kRing];
+
+  __device__ void init(int readers) {  // reading warps
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], readers);
+    }
+  }
+  // By one warp: piece i, or with p = nullptr the end.
+  __device__ bool put(int i, const PagedPiece* p, int lane, const WaitCtl& wc) {
+    const int s = i % kRing;
+    if (i >= kRing && !mbar_wait_warp(&empty[s], (i / kRing - 1) & 1, wc)) return false;
+    if (lane == 0) {
+      if (p) piece[s] = *p;
+      else piece[s].ntok = 0;
+      mbar_arrive(&full[s]);
+    }
+    __syncwarp();
+    return true;
+  }
+  // By each reading warp: piece i, or nullptr at the end (and when a wait gave up).
+  __device__ const PagedPiece* get(int i, const WaitCtl& wc) {
+    const int s = i % kRing;
+    if (!mbar_wait_warp(&full[s], (i / kRing) & 1, wc)) return nullptr;
+    return piece[s].ntok > 0 ? &piece[s] : nullptr;
+  }
+  __device__ void release(int i) { mbar_arrive_warp(&empty[i % kRing]); }
+};
+
 // A place in the line and the way through it.  UT: tokens a unit.
 struct PagedCursor {
   int b, h, t;
