@@ -68,7 +68,7 @@ struct PdCfg {
   static constexpr int K_WARP = 8, V_WARP = 9, S_WARP = 10, O_WARP = 11, READY_WARP = 12, THREADS = 512;
   // Registers: 128 a thread at launch; with 32 columns the elementwise warpgroups
   // take over most of the others' (2 x 184 + 2 x 72 = 4 x 128).
-  static constexpr bool SPLIT_REGS = false;
+  static constexpr bool SPLIT_REGS = NC == 32;
   // Four S^T buffers, and O^T by warpgroup and by the unit's parity.
   static constexpr uint32_t TM_S = 0, TM_O = 4 * NQ, TM_COLS = 8 * NQ;
 };
@@ -247,193 +247,9 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
   const WaitCtl wc{&bars->abort, a.err};
   PagedRing& ring = bars->ring;
 
-  if constexpr (C::SPLIT_REGS) {
-    if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
-    else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-  }
-  if (warp == C::K_WARP || warp == C::V_WARP) {
-    // ------------------------------------------------------------ TMA producers
-    const bool is_k = warp == C::K_WARP;
-    const CUtensorMap* tm = is_k ? &tm_k : &tm_v;
-    uint64_t* full = is_k ? bars->k_full : bars->v_full;
-    uint64_t* empty = is_k ? bars->k_empty : bars->v_empty;
-    uint8_t* tiles = smem + (is_k ? C::OFF_K : C::OFF_V);
-    const uint64_t pol = l2_policy_evict_first();
-    const int shift = a.pv.page_shift, box = min(a.pv.page_size, BN), per_tile = BN / box;
-    const uint32_t q_bytes = static_cast<uint32_t>(UT * G) * 128 * C::NCHUNK;
-    int st = 0, seg = 0;
-    bool ok = true;
-    for (int i = 0; ok; ++i) {
-      PagedPiece pc;
-      if (is_k) {
-        const bool more = cur.next(a, UT, seq, &pc);
-        if (!(ok = ring.put(i, more ? &pc : nullptr, lane, wc)) || !more) break;
-      } else {
-        const PagedPiece* p = ring.get(i, wc);
-        if (!p) break;
-        pc = *p;
-        ring.release(i);
-      }
-      if (pc.t_hi == pc.t_lo) continue;
-      const int* row = a.pv.table + pc.b * a.pv.table_stride;
-      // Boxes of a tile that hold a visible key, and this lane's page of it.
-      auto boxes = [&](int t) { return min(per_tile, (pc.key_hi - t * BN + box - 1) / box); };
-      auto page_of = [&](int t) { return lane < boxes(t) ? row[(t * BN >> shift) + lane] : 0; };
-      int page = page_of(pc.t_lo);
-      if (is_k) {
-        const int qb = seg % C::QBUF;
-        if (seg >= C::QBUF && !(ok = mbar_wait_warp(&bars->q_empty[qb], (seg / C::QBUF - 1) & 1, wc))) break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&bars->q_full[qb], q_bytes);
-          for (int c = 0; c < C::NCHUNK; ++c)
-            tma_load_4d(&tm_q, &bars->q_full[qb], smem + C::OFF_Q + qb * C::Q_TILE + c * C::Q_CHUNK, c * 64, 0, pc.h,
-                        pc.s.row0 + pc.tok0, pol);
-        }
-      }
-      ++seg;
-      for (int t = pc.t_lo; t < pc.t_hi; ++t, ++st) {
-        const int s = st % C::STAGES;
-        const int next_page = t + 1 < pc.t_hi ? page_of(t + 1) : 0;
-        if (!(ok = mbar_wait_warp(&empty[s], ((st / C::STAGES) & 1) ^ 1, wc))) break;
-        const int nb = boxes(t);
-        if (lane == 0) mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(nb * box) * 128 * C::NCHUNK);
-        __syncwarp();
-        if (lane < nb)
-          load_page(tm, &full[s], tiles + s * C::KV_TILE + lane * box * 128 * C::NCHUNK, a.pv,
-                    (t * BN & (a.pv.page_size - 1)) >> 3, page, pc.h, is_k, pol);
-        __syncwarp();
-        page = next_page;
-      }
-    }
-    __syncwarp();
-    if (lane == 0 && *reinterpret_cast<volatile int*>(&bars->abort)) {
-      // Never leave a copy in flight into shared memory this CTA is about to release.
-      for (int i = max(0, seg - C::QBUF); is_k && i < seg; ++i)
-        mbar_wait_drain(&bars->q_full[i % C::QBUF], (i / C::QBUF) & 1, a.err);
-      for (int j = max(0, st - C::STAGES); j < st; ++j)
-        mbar_wait_drain(&full[j % C::STAGES], (j / C::STAGES) & 1, a.err);
-    }
-    __syncwarp();
-  } else if (warp == C::S_WARP) {
-    // ------------------------------------------------------------ S^T = K Q^T
-    constexpr uint32_t idesc = idesc_f16kind(E::kFmt, 128, NQ, 0, 0);
-    const uint64_t q_desc = sdesc_sw128(smem_u32(smem + C::OFF_Q), 16, 1024);
-    const uint64_t k_desc = sdesc_sw128(smem_u32(smem + C::OFF_K), 16, C::GROUP);
-    auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_warp(bar, parity, wc); };
-    int st = 0, seg = 0;
-    bool ok = true;
-    for (int i = 0; ok; ++i) {
-      const PagedPiece* pc = ring.get(i, wc);
-      if (!pc) break;
-      const int n = pc->t_hi - pc->t_lo;
-      ring.release(i);
-      if (n == 0) continue;
-      const int qb = seg % C::QBUF;
-      if (!(ok = wait(&bars->q_full[qb], (seg / C::QBUF) & 1))) break;
-      const uint64_t qd = q_desc + ((qb * C::Q_TILE) >> 4);
-      for (int j = 0; j < n; ++j, ++st) {
-        const int s = st % C::STAGES, b = st & 3;
-        if (!(ok = wait(&bars->k_full[s], (st / C::STAGES) & 1))) break;
-        if (st >= 4 && !(ok = wait(&bars->s_free[b], ((st >> 2) - 1) & 1))) break;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint64_t kd = k_desc + ((s * C::KV_TILE) >> 4);
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_ss(tmem + C::TM_S + b * NQ, kd + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4),
-                   qd + (((kk >> 2) * C::Q_CHUNK + (kk & 3) * 32) >> 4), idesc, kk > 0);
-          mma_commit(&bars->s_full[b]);
-          mma_commit(&bars->k_empty[s]);
-          if (j == n - 1) mma_commit(&bars->q_empty[qb]);
-        }
-        __syncwarp();
-      }
-      ++seg;
-    }
-    // Nothing may still read shared memory or write TMEM once the CTA tears down.
-    if (elect_one()) mma_commit(&bars->done[0]);
-    __syncwarp();
-    if (lane == 0) mbar_wait_drain(&bars->done[0], 0, a.err);
-    __syncwarp();
-  } else if (warp == C::O_WARP) {
-    // ------------------------------------------------------------ O^T += V^T P^T
-    constexpr uint32_t idesc = idesc_f16kind(PE::kFmt, 128, NQ, 1, 0);
-    const uint64_t p_desc = sdesc_sw128(smem_u32(smem + C::OFF_P), 16, 1024);
-    // Its two runs of 64 rows (d) are a group's two atoms; at d = 64 the second
-    // run is the next group's.
-    const uint64_t v_desc = sdesc_sw128(smem_u32(smem + C::OFF_V), 1024, C::GROUP);
-    auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_warp(bar, parity, wc); };
-    int st = 0, seg = 0;
-    bool ok = true;
-    for (int i = 0; ok; ++i) {
-      const PagedPiece* pc = ring.get(i, wc);
-      if (!pc) break;
-      const int n = pc->t_hi - pc->t_lo, ob = seg & 1;
-      ring.release(i);
-      if (n == 0) continue;
-      for (int j = 0; j < n; ++j, ++st) {
-        const int s = st % C::STAGES, w = st & 1;
-        if (!(ok = wait(&bars->v_ready[s], (st / C::STAGES) & 1))) break;
-        // The unit two before has been read out of these accumulators.
-        if (j == 0 && seg >= 2 && !(ok = wait(&bars->o_free[ob], ((seg >> 1) - 1) & 1))) break;
-        if (!(ok = wait(&bars->p_full[w], (st >> 1) & 1))) break;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint64_t vd = v_desc + ((s * C::KV_TILE) >> 4), pd = p_desc + ((w * C::P_TILE) >> 4);
-#pragma unroll
-          for (int kk = 0; kk < BN / 16; ++kk)
-            mma_ss(tmem + C::TM_O + (ob * 2 + w) * NQ, vd + ((kk * 2 * C::GROUP) >> 4),
-                   pd + (((kk >> 2) * C::P_CHUNK + (kk & 3) * 32) >> 4), idesc, (j >= 2 || kk > 0) ? 1u : 0u);
-          mma_commit(&bars->p_free[w]);
-          mma_commit(&bars->v_empty[s]);
-          if (j == n - 1) mma_commit(&bars->o_full[ob]);
-        }
-        __syncwarp();
-      }
-      ++seg;
-    }
-    if (elect_one()) mma_commit(&bars->done[1]);
-    __syncwarp();
-    if (lane == 0) mbar_wait_drain(&bars->done[1], 0, a.err);
-    __syncwarp();
-  } else if (warp >= C::READY_WARP) {
-    // ------------------------------------------------------------ V made ready
-    // bf16 tiles to f16 in place; rows at or past the last visible key to zero.
-    const int ct = threadIdx.x - 32 * C::READY_WARP;
-    int st = 0;
-    bool ok = true;
-    for (int k = 0; ok; ++k) {
-      const PagedPiece* pc = ring.get(k, wc);
-      if (!pc) break;
-      const int t_lo = pc->t_lo, t_hi = pc->t_hi, key_hi = pc->key_hi;
-      ring.release(k);
-      for (int t = t_lo; t < t_hi; ++t, ++st) {
-        const int s = st % C::STAGES, rows = key_hi - t * BN;
-        if (!(ok = mbar_wait_warp(&bars->v_full[s], (st / C::STAGES) & 1, wc))) break;
-        uint4* tile = reinterpret_cast<uint4*>(smem + C::OFF_V + s * C::KV_TILE);
-        if (kConvertV || rows < BN) {
-#pragma unroll
-          for (int i0 = 0; i0 < C::KV_TILE / 16 / 128; i0 += 8) {
-            uint4 x[8];
-#pragma unroll
-            for (int u = 0; u < 8; ++u) x[u] = tile[(i0 + u) * 128 + ct];
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-              if constexpr (kConvertV)
-                x[u] = make_uint4(pd_bf16x2_to_f16x2(x[u].x), pd_bf16x2_to_f16x2(x[u].y), pd_bf16x2_to_f16x2(x[u].z),
-                                  pd_bf16x2_to_f16x2(x[u].w));
-              // 64 vectors an atom of 8 rows, 8 a row.
-              const int i = (i0 + u) * 128 + ct;
-              if (i / (64 * C::NCHUNK) * 8 + (i >> 3 & 7) >= rows) x[u] = make_uint4(0, 0, 0, 0);
-              tile[i] = x[u];
-            }
-          }
-          fence_proxy_async_smem();
-        }
-        mbar_arrive_warp(&bars->v_ready[s]);
-      }
-    }
-  } else {
+  // (setmaxnreg is a warpgroup's: each branch here takes whole ones.)
+  if (warp < 8) {
+    if constexpr (C::SPLIT_REGS) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
     // ------------------------------------------------------------ elementwise (thread = key row / d row)
     // Warpgroup w takes the steps of its parity: S^T buffers w and w + 2, P^T buffer w.
     const int w = warp >> 2, wl = warp & 3, tid = threadIdx.x & 127;
@@ -646,6 +462,192 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
       }
       ring.release(pieces);
       if (n > 0) ++seg;
+    }
+  } else if (warp >= C::READY_WARP) {
+    if constexpr (C::SPLIT_REGS) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    // ------------------------------------------------------------ V made ready
+    // bf16 tiles to f16 in place; rows at or past the last visible key to zero.
+    const int ct = threadIdx.x - 32 * C::READY_WARP;
+    int st = 0;
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      const PagedPiece* pc = ring.get(k, wc);
+      if (!pc) break;
+      const int t_lo = pc->t_lo, t_hi = pc->t_hi, key_hi = pc->key_hi;
+      ring.release(k);
+      for (int t = t_lo; t < t_hi; ++t, ++st) {
+        const int s = st % C::STAGES, rows = key_hi - t * BN;
+        if (!(ok = mbar_wait_warp(&bars->v_full[s], (st / C::STAGES) & 1, wc))) break;
+        uint4* tile = reinterpret_cast<uint4*>(smem + C::OFF_V + s * C::KV_TILE);
+        if constexpr (kConvertV) {
+#pragma unroll
+          for (int i0 = 0; i0 < C::KV_TILE / 16 / 128; i0 += 8) {
+            uint4 x[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) x[u] = tile[(i0 + u) * 128 + ct];
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+              tile[(i0 + u) * 128 + ct] = make_uint4(pd_bf16x2_to_f16x2(x[u].x), pd_bf16x2_to_f16x2(x[u].y),
+                                                     pd_bf16x2_to_f16x2(x[u].z), pd_bf16x2_to_f16x2(x[u].w));
+          }
+        }
+        if (rows < BN) {
+          // Each thread zeroes vectors that it has itself written above.
+#pragma unroll 1
+          for (int i = ct; i < C::KV_TILE / 16; i += 128)  // 64 vectors an atom of 8 rows, 8 a row
+            if (i / (64 * C::NCHUNK) * 8 + (i >> 3 & 7) >= rows) tile[i] = make_uint4(0, 0, 0, 0);
+        }
+        if (kConvertV || rows < BN) fence_proxy_async_smem();
+        mbar_arrive_warp(&bars->v_ready[s]);
+      }
+    }
+  } else {
+    if constexpr (C::SPLIT_REGS) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == C::S_WARP) {
+    // ------------------------------------------------------------ S^T = K Q^T
+    constexpr uint32_t idesc = idesc_f16kind(E::kFmt, 128, NQ, 0, 0);
+    const uint64_t q_desc = sdesc_sw128(smem_u32(smem + C::OFF_Q), 16, 1024);
+    const uint64_t k_desc = sdesc_sw128(smem_u32(smem + C::OFF_K), 16, C::GROUP);
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_warp(bar, parity, wc); };
+    int st = 0, seg = 0;
+    bool ok = true;
+    for (int i = 0; ok; ++i) {
+      const PagedPiece* pc = ring.get(i, wc);
+      if (!pc) break;
+      const int n = pc->t_hi - pc->t_lo;
+      ring.release(i);
+      if (n == 0) continue;
+      const int qb = seg % C::QBUF;
+      if (!(ok = wait(&bars->q_full[qb], (seg / C::QBUF) & 1))) break;
+      const uint64_t qd = q_desc + ((qb * C::Q_TILE) >> 4);
+      for (int j = 0; j < n; ++j, ++st) {
+        const int s = st % C::STAGES, b = st & 3;
+        if (!(ok = wait(&bars->k_full[s], (st / C::STAGES) & 1))) break;
+        if (st >= 4 && !(ok = wait(&bars->s_free[b], ((st >> 2) - 1) & 1))) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t kd = k_desc + ((s * C::KV_TILE) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_ss(tmem + C::TM_S + b * NQ, kd + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4),
+                   qd + (((kk >> 2) * C::Q_CHUNK + (kk & 3) * 32) >> 4), idesc, kk > 0);
+          mma_commit(&bars->s_full[b]);
+          mma_commit(&bars->k_empty[s]);
+          if (j == n - 1) mma_commit(&bars->q_empty[qb]);
+        }
+        __syncwarp();
+      }
+      ++seg;
+    }
+    // Nothing may still read shared memory or write TMEM once the CTA tears down.
+    if (elect_one()) mma_commit(&bars->done[0]);
+    __syncwarp();
+    if (lane == 0) mbar_wait_drain(&bars->done[0], 0, a.err);
+    __syncwarp();
+    } else if (warp == C::O_WARP) {
+    // ------------------------------------------------------------ O^T += V^T P^T
+    constexpr uint32_t idesc = idesc_f16kind(PE::kFmt, 128, NQ, 1, 0);
+    const uint64_t p_desc = sdesc_sw128(smem_u32(smem + C::OFF_P), 16, 1024);
+    // Its two runs of 64 rows (d) are a group's two atoms; at d = 64 the second
+    // run is the next group's.
+    const uint64_t v_desc = sdesc_sw128(smem_u32(smem + C::OFF_V), 1024, C::GROUP);
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_warp(bar, parity, wc); };
+    int st = 0, seg = 0;
+    bool ok = true;
+    for (int i = 0; ok; ++i) {
+      const PagedPiece* pc = ring.get(i, wc);
+      if (!pc) break;
+      const int n = pc->t_hi - pc->t_lo, ob = seg & 1;
+      ring.release(i);
+      if (n == 0) continue;
+      for (int j = 0; j < n; ++j, ++st) {
+        const int s = st % C::STAGES, w = st & 1;
+        if (!(ok = wait(&bars->v_ready[s], (st / C::STAGES) & 1))) break;
+        // The unit two before has been read out of these accumulators.
+        if (j == 0 && seg >= 2 && !(ok = wait(&bars->o_free[ob], ((seg >> 1) - 1) & 1))) break;
+        if (!(ok = wait(&bars->p_full[w], (st >> 1) & 1))) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t vd = v_desc + ((s * C::KV_TILE) >> 4), pd = p_desc + ((w * C::P_TILE) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < BN / 16; ++kk)
+            mma_ss(tmem + C::TM_O + (ob * 2 + w) * NQ, vd + ((kk * 2 * C::GROUP) >> 4),
+                   pd + (((kk >> 2) * C::P_CHUNK + (kk & 3) * 32) >> 4), idesc, (j >= 2 || kk > 0) ? 1u : 0u);
+          mma_commit(&bars->p_free[w]);
+          mma_commit(&bars->v_empty[s]);
+          if (j == n - 1) mma_commit(&bars->o_full[ob]);
+        }
+        __syncwarp();
+      }
+      ++seg;
+    }
+    if (elect_one()) mma_commit(&bars->done[1]);
+    __syncwarp();
+    if (lane == 0) mbar_wait_drain(&bars->done[1], 0, a.err);
+    __syncwarp();
+    } else {
+    // ------------------------------------------------------------ TMA producers
+    const bool is_k = warp == C::K_WARP;
+    const CUtensorMap* tm = is_k ? &tm_k : &tm_v;
+    uint64_t* full = is_k ? bars->k_full : bars->v_full;
+    uint64_t* empty = is_k ? bars->k_empty : bars->v_empty;
+    uint8_t* tiles = smem + (is_k ? C::OFF_K : C::OFF_V);
+    const uint64_t pol = l2_policy_evict_first();
+    const int shift = a.pv.page_shift, box = min(a.pv.page_size, BN), per_tile = BN / box;
+    const uint32_t q_bytes = static_cast<uint32_t>(UT * G) * 128 * C::NCHUNK;
+    int st = 0, seg = 0;
+    bool ok = true;
+    for (int i = 0; ok; ++i) {
+      PagedPiece pc;
+      if (is_k) {
+        const bool more = cur.next(a, UT, seq, &pc);
+        if (!(ok = ring.put(i, more ? &pc : nullptr, lane, wc)) || !more) break;
+      } else {
+        const PagedPiece* p = ring.get(i, wc);
+        if (!p) break;
+        pc = *p;
+        ring.release(i);
+      }
+      if (pc.t_hi == pc.t_lo) continue;
+      const int* row = a.pv.table + pc.b * a.pv.table_stride;
+      // Boxes of a tile that hold a visible key, and this lane's page of it.
+      auto boxes = [&](int t) { return min(per_tile, (pc.key_hi - t * BN + box - 1) / box); };
+      auto page_of = [&](int t) { return lane < boxes(t) ? row[(t * BN >> shift) + lane] : 0; };
+      int page = page_of(pc.t_lo);
+      if (is_k) {
+        const int qb = seg % C::QBUF;
+        if (seg >= C::QBUF && !(ok = mbar_wait_warp(&bars->q_empty[qb], (seg / C::QBUF - 1) & 1, wc))) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&bars->q_full[qb], q_bytes);
+          for (int c = 0; c < C::NCHUNK; ++c)
+            tma_load_4d(&tm_q, &bars->q_full[qb], smem + C::OFF_Q + qb * C::Q_TILE + c * C::Q_CHUNK, c * 64, 0, pc.h,
+                        pc.s.row0 + pc.tok0, pol);
+        }
+      }
+      ++seg;
+      for (int t = pc.t_lo; t < pc.t_hi; ++t, ++st) {
+        const int s = st % C::STAGES;
+        const int next_page = t + 1 < pc.t_hi ? page_of(t + 1) : 0;
+        if (!(ok = mbar_wait_warp(&empty[s], ((st / C::STAGES) & 1) ^ 1, wc))) break;
+        const int nb = boxes(t);
+        if (lane == 0) mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(nb * box) * 128 * C::NCHUNK);
+        __syncwarp();
+        if (lane < nb)
+          load_page(tm, &full[s], tiles + s * C::KV_TILE + lane * box * 128 * C::NCHUNK, a.pv,
+                    (t * BN & (a.pv.page_size - 1)) >> 3, page, pc.h, is_k, pol);
+        __syncwarp();
+        page = next_page;
+      }
+    }
+    __syncwarp();
+    if (lane == 0 && *reinterpret_cast<volatile int*>(&bars->abort)) {
+      // Never leave a copy in flight into shared memory this CTA is about to release.
+      for (int i = max(0, seg - C::QBUF); is_k && i < seg; ++i)
+        mbar_wait_drain(&bars->q_full[i % C::QBUF], (i / C::QBUF) & 1, a.err);
+      for (int j = max(0, st - C::STAGES); j < st; ++j)
+        mbar_wait_drain(&full[j % C::STAGES], (j / C::STAGES) & 1, a.err);
+    }
+    __syncwarp();
     }
   }
 

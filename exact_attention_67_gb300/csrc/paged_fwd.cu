@@ -42,7 +42,12 @@ struct PfCfg {
   static constexpr int OFF_BAR = OFF_V + STAGES * TILE_BYTES;
   static constexpr int SMEM_BYTES = OFF_BAR + 1024 + 1024;
   static_assert(SMEM_BYTES > 120 * 1024, "one CTA per SM: it holds all 512 TMEM columns");
-  static constexpr int THREADS = 384;
+  // Warps: 0-7 softmax, 8 the walk of the line, Q and K, 9 the products, 10 V, 11 none,
+  // 12-15 make V ready (one an SM quarter: two of them left the softmax warps that
+  // shared their quarters behind the others).  Registers: 128 a thread at launch, of
+  // which the softmax takes over 48 a thread of the other warpgroups
+  // (2 x 176 + 2 x 80 = 4 x 128).
+  static constexpr int THREADS = 512, K_WARP = 8, MMA_WARP = 9, READY_WARP = 12;
   // TMEM as in fwd.cu: at d = 64 P has columns of its own, so that the next S_t
   // can be computed while the softmax still works on this one.
   static constexpr bool EARLY_S = D == 64;
@@ -85,7 +90,7 @@ __device__ __forceinline__ int tiles_of(const PagedArgs& a, const PagedPiece& p,
 }  // namespace
 
 template <typename T, int D>
-__global__ void __launch_bounds__(384, 1)
+__global__ void __launch_bounds__(512, 1)
     paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PagedArgs a) {
   using C = PfCfg<D>;
@@ -103,7 +108,7 @@ __global__ void __launch_bounds__(384, 1)
   // The walking warp finds its place while the others set up.
   PagedCursor cur{};
   PagedSeq seq{};
-  if (warp == 8) cur = paged_start(a, UT, lane, &seq);
+  if (warp == C::K_WARP) cur = paged_start(a, UT, lane, &seq);
   if (threadIdx.x == 32) {
     mbar_init(&bars->q_full, 1);
     mbar_init(&bars->q_empty, 1);
@@ -121,13 +126,13 @@ __global__ void __launch_bounds__(384, 1)
       mbar_init(&bars->k_empty[s], 1);
       mbar_init(&bars->v_full[s], 1);
       mbar_init(&bars->v_empty[s], 1);
-      mbar_init(&bars->v_ready[s], 2);
+      mbar_init(&bars->v_ready[s], 4);
     }
-    bars->ring.init(11);  // all but the walking warp
+    bars->ring.init(14);  // the eight softmax warps, the four of READY_WARP, products, V
     bars->abort = 0;
     fence_barrier_init();
   }
-  if (warp == 9) {
+  if (warp == C::MMA_WARP) {
     tmem_alloc(&bars->tmem_base, C::TM_COLS);
     tmem_relinquish();
   }
@@ -139,218 +144,9 @@ __global__ void __launch_bounds__(384, 1)
   const WaitCtl wc{&bars->abort, a.err};
   PagedRing& ring = bars->ring;
 
-  if (warp == 8) {
-    // ------------------------------------------------------------ TMA producer
-    if (lane == 0) {
-      tma_prefetch_desc(&tm_q);
-      tma_prefetch_desc(&tm_k);
-      tma_prefetch_desc(&tm_v);
-    }
-    const uint64_t pol_kv = l2_policy_evict_last();  // re-read by every unit of the (sequence, key head)
-    const uint64_t pol_q = l2_policy_evict_first();
-    const int ps = a.pv.page_size, shift = a.pv.page_shift;
-    const int box = min(ps, C::BN), per_tile = C::BN / box;
-    const uint32_t q_bytes = static_cast<uint32_t>(TT * G) * 128 * C::NCHUNK;
-    int kt = 0, vt = 0, seg = 0;  // key tiles and Qs issued
-    bool ok = true;
-    for (int i = 0; ok; ++i) {
-      PagedPiece pc;
-      const bool more = cur.next(a, UT, seq, &pc);
-      if (!(ok = ring.put(i, more ? &pc : nullptr, lane, wc)) || !more) break;
-      const int n0 = tiles_of(a, pc, 0), n1 = tiles_of(a, pc, 1), n = max(n0, n1);
-      if (n == 0) continue;
-      if (seg >= 1 && !(ok = mbar_wait_warp(&bars->q_empty, (seg - 1) & 1, wc))) break;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&bars->q_full, q_bytes * ((n0 > 0) + (n1 > 0)));
-        for (int t = 0; t < 2; ++t)
-          if ((t == 0 ? n0 : n1) > 0)
-            for (int c = 0; c < C::NCHUNK; ++c)
-              tma_load_4d(&tm_q, &bars->q_full, smem + C::OFF_Q + t * C::TILE_BYTES + c * C::CHUNK_BYTES, c * 64, 0, pc.h,
-                          pc.s.row0 + pc.tok0 + t * TT, pol_q);
-      }
-      ++seg;
-      const int* row = a.pv.table + pc.b * a.pv.table_stride;
-      auto boxes = [&](int t) { return min(per_tile, (pc.key_hi - t * C::BN + box - 1) / box); };
-      auto page_of = [&](int t) { return lane < boxes(t) ? row[(t * C::BN >> shift) + lane] : 0; };
-      int page = page_of(pc.t_lo);
-      for (int t = pc.t_lo; t < pc.t_lo + n; ++t) {
-        const int s = kt % C::STAGES;
-        const uint32_t ph = ((kt / C::STAGES) & 1) ^ 1;
-        const int next_page = t + 1 < pc.t_lo + n ? page_of(t + 1) : 0;
-        const int nb = boxes(t), group = (t * C::BN & (ps - 1)) >> 3;
-        const uint32_t bytes = static_cast<uint32_t>(nb * box) * 128 * C::NCHUNK;
-        const int at = s * C::TILE_BYTES + lane * box * 128 * C::NCHUNK;
-        if (!(ok = mbar_wait_warp(&bars->k_empty[s], ph, wc))) break;
-        if (lane == 0) mbar_arrive_expect_tx(&bars->k_full[s], bytes);
-        __syncwarp();
-        if (lane < nb) load_page(&tm_k, &bars->k_full[s], smem + C::OFF_K + at, a.pv, group, page, pc.h, true, pol_kv);
-        __syncwarp();
-        ++kt;
-        if (!(ok = mbar_wait_warp(&bars->v_empty[s], ph, wc))) break;
-        if (lane == 0) mbar_arrive_expect_tx(&bars->v_full[s], bytes);
-        __syncwarp();
-        if (lane < nb) load_page(&tm_v, &bars->v_full[s], smem + C::OFF_V + at, a.pv, group, page, pc.h, false, pol_kv);
-        __syncwarp();
-        ++vt;
-        page = next_page;
-      }
-    }
-    __syncwarp();
-    if (lane == 0 && *reinterpret_cast<volatile int*>(&bars->abort)) {
-      // Never leave a copy in flight into shared memory this CTA is about to release.
-      if (seg > 0) mbar_wait_drain(&bars->q_full, (seg - 1) & 1, a.err);
-      for (int j = max(0, kt - C::STAGES); j < kt; ++j)
-        mbar_wait_drain(&bars->k_full[j % C::STAGES], (j / C::STAGES) & 1, a.err);
-      for (int j = max(0, vt - C::STAGES); j < vt; ++j)
-        mbar_wait_drain(&bars->v_full[j % C::STAGES], (j / C::STAGES) & 1, a.err);
-    }
-    __syncwarp();
-  } else if (warp == 9) {
-    // ------------------------------------------------------------ MMA issuer
-    constexpr uint32_t idesc_s = idesc_f16kind(E::kFmt, 128, C::BN, 0, 0);
-    constexpr uint32_t idesc_o = idesc_f16kind(PE::kFmt, 128, D, 0, 1);
-    const uint64_t q_desc = sdesc_sw128(smem_u32(smem + C::OFF_Q), 16, 1024);
-    const uint64_t k_desc = sdesc_sw128(smem_u32(smem + C::OFF_K), 16, C::GROUP);
-    const uint64_t v_desc = sdesc_sw128(smem_u32(smem + C::OFF_V), 1024, C::GROUP);
-    constexpr uint32_t kTileDesc = C::TILE_BYTES >> 4;
-    auto issue_s = [&](int t, int stage) {
-      const uint64_t qa = q_desc + t * kTileDesc, kb = k_desc + stage * kTileDesc;
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        mma_ss(tmem + C::tm_s(t), qa + (((kk >> 2) * C::CHUNK_BYTES + (kk & 3) * 32) >> 4),
-               kb + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), idesc_s, kk > 0);
-      }
-    };
-    auto issue_pv = [&](int t, int stage, bool acc) {
-      const uint64_t vb = v_desc + stage * kTileDesc;
-#pragma unroll
-      for (int kk = 0; kk < C::BN / 16; ++kk)
-        mma_ts(tmem + C::tm_o(t), tmem + C::tm_p(t) + kk * 8, vb + ((kk * 2 * C::GROUP) >> 4), idesc_o,
-               (acc || kk > 0) ? 1u : 0u);
-    };
-    auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_warp(bar, parity, wc); };
-    int kt = 0, seg = 0;
-    int cs[2] = {0, 0};  // S_t issued
-    int cp[2] = {0, 0};  // P_t consumed
-    int co[2] = {0, 0};  // pieces that tile t took part in
-    bool ok = true;
-    // S_t of the next step of tile t from K stage s.
-    auto next_s = [&](int t, int s) {
-      if (C::EARLY_S && cs[t] >= 1 && !(ok = wait(&bars->s_free[t], (cs[t] - 1) & 1))) return;
-      tc_fence_after();
-      if (elect_one()) {
-        issue_s(t, s);
-        mma_commit(&bars->s_full[t]);
-      }
-      __syncwarp();
-      ++cs[t];
-    };
-    for (int i = 0; ok; ++i) {
-      const PagedPiece* pc = ring.get(i, wc);
-      if (!pc) break;
-      const int nt[2] = {tiles_of(a, *pc, 0), tiles_of(a, *pc, 1)};
-      ring.release(i);
-      const int n = max(nt[0], nt[1]);
-      if (n == 0) continue;
-      if (!(ok = wait(&bars->q_full, seg & 1))) break;
-      if (!(ok = wait(&bars->k_full[kt % C::STAGES], (kt / C::STAGES) & 1))) break;
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-        if (ok && nt[t] > 0) next_s(t, kt % C::STAGES);
-      if (!ok) break;
-      if (elect_one()) {
-        mma_commit(&bars->k_empty[kt % C::STAGES]);
-        if (n == 1) mma_commit(&bars->q_empty);
-      }
-      __syncwarp();
-      for (int j = 0; ok && j < n; ++j) {
-        const int s = (kt + j) % C::STAGES, s1 = (kt + j + 1) % C::STAGES;
-        const uint32_t ph = ((kt + j) / C::STAGES) & 1, ph1 = ((kt + j + 1) / C::STAGES) & 1;
-        bool k_ready = false, v_ready = false;
-        auto want_k = [&]() {
-          if (!k_ready) k_ready = ok = wait(&bars->k_full[s1], ph1);
-          return k_ready;
-        };
-        if constexpr (C::EARLY_S) {
-#pragma unroll
-          for (int t = 0; t < 2; ++t)
-            if (ok && j + 1 < nt[t] && want_k()) next_s(t, s1);
-        }
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (!ok || j >= nt[t]) continue;
-          if (!(ok = wait(&bars->p_full[t], cp[t] & 1))) continue;
-          ++cp[t];
-          if (!v_ready && !(v_ready = ok = wait(&bars->v_ready[s], ph))) continue;
-          // The piece before has been read out of O_t.
-          if (j == 0 && co[t] >= 1 && !(ok = wait(&bars->o_free[t], (co[t] - 1) & 1))) continue;
-          tc_fence_after();
-          if (elect_one()) {
-            issue_pv(t, s, j > 0);
-            if (C::EARLY_S) mma_commit(&bars->pv_done[t]);
-            if (t == 1 || nt[1] <= j) mma_commit(&bars->v_empty[s]);
-            if (j + 1 == nt[t]) mma_commit(&bars->o_full[t]);
-          }
-          __syncwarp();
-          if (!C::EARLY_S && j + 1 < nt[t] && want_k()) next_s(t, s1);
-        }
-        if (ok && k_ready) {
-          if (elect_one()) {
-            mma_commit(&bars->k_empty[s1]);
-            if (j + 2 == n) mma_commit(&bars->q_empty);
-          }
-          __syncwarp();
-        }
-      }
-      kt += n;
-      ++seg;
-      co[0] += nt[0] > 0;
-      co[1] += nt[1] > 0;
-    }
-    // Nothing may still read shared memory or write TMEM once the CTA tears down.
-    if (elect_one()) mma_commit(&bars->mma_done);
-    __syncwarp();
-    if (lane == 0) mbar_wait_drain(&bars->mma_done, 0, a.err);
-    __syncwarp();
-  } else if (warp >= 10) {
-    // ------------------------------------------------------------ V made ready
-    constexpr int PER = C::TILE_BYTES / 16 / 64, BATCH = 8;
-    static_assert(PER % BATCH == 0, "conversion batches must divide the tile");
-    const int ct = (warp - 10) * 32 + lane;
-    int vt = 0;
-    bool ok = true;
-    for (int i = 0; ok; ++i) {
-      const PagedPiece* pc = ring.get(i, wc);
-      if (!pc) break;
-      const int n = max(tiles_of(a, *pc, 0), tiles_of(a, *pc, 1)), keys = pc->key_hi - pc->t_lo * C::BN;
-      ring.release(i);
-      for (int j = 0; j < n; ++j, ++vt) {
-        const int s = vt % C::STAGES, rows = keys - j * C::BN;
-        if (!(ok = mbar_wait_warp(&bars->v_full[s], (vt / C::STAGES) & 1, wc))) break;
-        uint4* tile = reinterpret_cast<uint4*>(smem + C::OFF_V + s * C::TILE_BYTES);
-        if (kConvertV || rows < C::BN) {
-#pragma unroll 1
-          for (int b0 = 0; b0 < PER; b0 += BATCH) {
-            uint4 x[BATCH];
-#pragma unroll
-            for (int u = 0; u < BATCH; ++u) x[u] = tile[(b0 + u) * 64 + ct];
-#pragma unroll
-            for (int u = 0; u < BATCH; ++u) {
-              if constexpr (kConvertV)
-                x[u] = make_uint4(pf_bf16x2_to_f16x2(x[u].x), pf_bf16x2_to_f16x2(x[u].y), pf_bf16x2_to_f16x2(x[u].z),
-                                  pf_bf16x2_to_f16x2(x[u].w));
-              // 64 vectors an atom of 8 rows, 8 a row.
-              const int i = (b0 + u) * 64 + ct;
-              if (i / (64 * C::NCHUNK) * 8 + (i >> 3 & 7) >= rows) x[u] = make_uint4(0, 0, 0, 0);
-              tile[(b0 + u) * 64 + ct] = x[u];
-            }
-          }
-          fence_proxy_async_smem();
-        }
-        mbar_arrive_warp(&bars->v_ready[s]);
-      }
-    }
-  } else {
+  // (setmaxnreg is a warpgroup's: each branch here takes whole ones.)
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
     // ------------------------------------------------------------ softmax
     const int t = warp >> 2, wq = warp & 3;
     const int row = wq * 32 + lane;  // row of the query tile == TMEM lane
@@ -365,7 +161,7 @@ __global__ void __launch_bounds__(384, 1)
       if (!pc) break;
       // The steps before `low` have some row with hidden keys below its window,
       // those from `high` on some row with hidden keys above.
-      const int n = tiles_of(a, *pc, t);
+      const int n = pc->n[t];
       int low = 0, high = (pc->key_hi - pc->t_lo * C::BN) / C::BN;
       {
         const int first = pc->s.off + pc->tok0 + t * TT - pc->t_lo * C::BN;  // first position, from the first key
@@ -374,13 +170,34 @@ __global__ void __launch_bounds__(384, 1)
         else if (a.window > 0) high = min(high, (first + a.window) / C::BN);
         if (a.window > 0) low = (first + TT - a.window + C::BN - 1) / C::BN;
       }
-      // This row's position, from the first key of step j's tile.
-      auto pos_from = [&](int j) { return pc->s.off + pc->tok0 + t * TT + row / G - (pc->t_lo + j) * C::BN; };
       float m_ref = -INFINITY;  // reference maximum, log2 units
       float le = 0.f, lb = 0.f; // sums of the unrounded and (f16) the rounded weights
       for (int j = 0; j < n; ++j, ++cs) {
         if (!(ok = mbar_wait_warp(&bars->s_full[t], cs & 1, wc))) break;
         tc_fence_after();
+        if (j >= high || j < low) {
+          // Hidden columns to -inf, in place and in a rolled loop: unrolled over the
+          // 128 registers, this code, that a chunk meets a few times, took some 4,000
+          // clocks to fetch.
+          int hi = pc->key_hi - (pc->t_lo + j) * C::BN, lo = 0;  // visible: columns [lo, hi)
+          const int pos = pc->s.off + pc->tok0 + t * TT + row / G - (pc->t_lo + j) * C::BN;
+          if (a.causal) hi = min(hi, pos + 1);
+          else if (a.window > 0) hi = min(hi, pos + a.window);
+          if (a.window > 0) lo = pos - a.window + 1;
+#pragma unroll 1
+          for (int c = 0; c < C::BN; c += 16) {
+            uint32_t x[16];
+            tmem_ld16(tS + c, x);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              asm volatile("" : "+r"(x[e]));
+              if (c + e >= hi || c + e < lo) x[e] = __float_as_uint(-INFINITY);
+            }
+            tmem_st16(tS + c, x);
+          }
+          tmem_wait_st();
+        }
         uint32_t sr[4][32];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, sr[c]);
@@ -390,24 +207,6 @@ __global__ void __launch_bounds__(384, 1)
         if constexpr (C::EARLY_S) {
           tc_fence_before();
           mbar_arrive_warp(&bars->s_free[t]);
-        }
-        if (j >= high) {
-          int x = pc->key_hi - (pc->t_lo + j) * C::BN;  // visible: columns below x
-          if (a.causal) x = min(x, pos_from(j) + 1);
-          else if (a.window > 0) x = min(x, pos_from(j) + a.window);
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (c * 32 + e >= x) sr[c][e] = __float_as_uint(-INFINITY);
-        }
-        if (j < low) {
-          const int x = pos_from(j) - a.window + 1;  // visible: columns from x on
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (c * 32 + e < x) sr[c][e] = __float_as_uint(-INFINITY);
         }
         float mx;
         {
@@ -503,29 +302,32 @@ __global__ void __launch_bounds__(384, 1)
       T* orow = static_cast<T*>(a.o) + prow * a.so.n + head * a.so.h;
       ring.release(i);
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t o_r[32];
-        float v[32];
+      for (int c = 0; c < D; c += 16) {
+        uint32_t o_r[16];
+        float v[16];
         if (n > 0) {
-          tmem_ld32(tO + c * 32, o_r);
+          tmem_ld16(tO + c, o_r);
           tmem_wait_ld();
-          tmem_reg_fence(o_r);
         }
 #pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] = l == 0.f || n == 0 ? 0.f : __uint_as_float(o_r[e]) * inv_l;
-        if (whole) {
-          uint4* dst = reinterpret_cast<uint4*>(orow + c * 32);
-          if (live) {
+        for (int e = 0; e < 16; ++e) {
+          asm volatile("" : "+r"(o_r[e]));
+          v[e] = l == 0.f || n == 0 ? 0.f : __uint_as_float(o_r[e]) * inv_l;
+        }
+        if (!whole) {
+          if (n > 0) {
 #pragma unroll
             for (int v4 = 0; v4 < 4; ++v4)
-              dst[v4] = make_uint4(E::pack(v[8 * v4], v[8 * v4 + 1]), E::pack(v[8 * v4 + 2], v[8 * v4 + 3]),
-                                   E::pack(v[8 * v4 + 4], v[8 * v4 + 5]), E::pack(v[8 * v4 + 6], v[8 * v4 + 7]));
+              po[(c / 4 + v4) * 128] = make_float4(v[4 * v4], v[4 * v4 + 1], v[4 * v4 + 2], v[4 * v4 + 3]);
           }
-        } else if (n > 0) {
+        } else if (live) {
+          uint4* dst = reinterpret_cast<uint4*>(orow + c);
 #pragma unroll
-          for (int v4 = 0; v4 < 8; ++v4)
-            po[(c * 8 + v4) * 128] = make_float4(v[4 * v4], v[4 * v4 + 1], v[4 * v4 + 2], v[4 * v4 + 3]);
+          for (int v4 = 0; v4 < 2; ++v4)
+            dst[v4] = make_uint4(E::pack(v[8 * v4], v[8 * v4 + 1]), E::pack(v[8 * v4 + 2], v[8 * v4 + 3]),
+                                 E::pack(v[8 * v4 + 4], v[8 * v4 + 5]), E::pack(v[8 * v4 + 6], v[8 * v4 + 7]));
         }
+        __syncwarp();
       }
       if (n > 0) {
         tc_fence_before();
@@ -537,12 +339,227 @@ __global__ void __launch_bounds__(384, 1)
         a.part_lse[part * 128 + row] = L;
       }
     }
+  } else if (warp >= C::READY_WARP) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    // ------------------------------------------------------------ V made ready
+    constexpr int PER = C::TILE_BYTES / 16 / 128, BATCH = 8;
+    static_assert(PER % BATCH == 0, "conversion batches must divide the tile");
+    const int ct = threadIdx.x - 32 * C::READY_WARP;
+    int vt = 0;
+    bool ok = true;
+    for (int i = 0; ok; ++i) {
+      const PagedPiece* pc = ring.get(i, wc);
+      if (!pc) break;
+      const int n = max(pc->n[0], pc->n[1]), keys = pc->key_hi - pc->t_lo * C::BN;
+      ring.release(i);
+      for (int j = 0; j < n; ++j, ++vt) {
+        const int s = vt % C::STAGES, rows = keys - j * C::BN;
+        if (!(ok = mbar_wait_warp(&bars->v_full[s], (vt / C::STAGES) & 1, wc))) break;
+        uint4* tile = reinterpret_cast<uint4*>(smem + C::OFF_V + s * C::TILE_BYTES);
+        if constexpr (kConvertV) {
+#pragma unroll 1
+          for (int b0 = 0; b0 < PER; b0 += BATCH) {
+            uint4 x[BATCH];
+#pragma unroll
+            for (int u = 0; u < BATCH; ++u) x[u] = tile[(b0 + u) * 128 + ct];
+#pragma unroll
+            for (int u = 0; u < BATCH; ++u)
+              tile[(b0 + u) * 128 + ct] = make_uint4(pf_bf16x2_to_f16x2(x[u].x), pf_bf16x2_to_f16x2(x[u].y),
+                                                     pf_bf16x2_to_f16x2(x[u].z), pf_bf16x2_to_f16x2(x[u].w));
+          }
+        }
+        if (rows < C::BN) {
+          // Each thread zeroes vectors that it has itself written above.
+#pragma unroll 1
+          for (int i = ct; i < C::TILE_BYTES / 16; i += 128)  // 64 vectors an atom of 8 rows, 8 a row
+            if (i / (64 * C::NCHUNK) * 8 + (i >> 3 & 7) >= rows) tile[i] = make_uint4(0, 0, 0, 0);
+        }
+        if (kConvertV || rows < C::BN) fence_proxy_async_smem();
+        mbar_arrive_warp(&bars->v_ready[s]);
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (warp == C::MMA_WARP) {
+    // ------------------------------------------------------------ MMA issuer
+    constexpr uint32_t idesc_s = idesc_f16kind(E::kFmt, 128, C::BN, 0, 0);
+    constexpr uint32_t idesc_o = idesc_f16kind(PE::kFmt, 128, D, 0, 1);
+    const uint64_t q_desc = sdesc_sw128(smem_u32(smem + C::OFF_Q), 16, 1024);
+    const uint64_t k_desc = sdesc_sw128(smem_u32(smem + C::OFF_K), 16, C::GROUP);
+    const uint64_t v_desc = sdesc_sw128(smem_u32(smem + C::OFF_V), 1024, C::GROUP);
+    constexpr uint32_t kTileDesc = C::TILE_BYTES >> 4;
+    auto issue_s = [&](int t, int stage) {
+      const uint64_t qa = q_desc + t * kTileDesc, kb = k_desc + stage * kTileDesc;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        mma_ss(tmem + C::tm_s(t), qa + (((kk >> 2) * C::CHUNK_BYTES + (kk & 3) * 32) >> 4),
+               kb + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), idesc_s, kk > 0);
+      }
+    };
+    auto issue_pv = [&](int t, int stage, bool acc) {
+      const uint64_t vb = v_desc + stage * kTileDesc;
+#pragma unroll
+      for (int kk = 0; kk < C::BN / 16; ++kk)
+        mma_ts(tmem + C::tm_o(t), tmem + C::tm_p(t) + kk * 8, vb + ((kk * 2 * C::GROUP) >> 4), idesc_o,
+               (acc || kk > 0) ? 1u : 0u);
+    };
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_warp(bar, parity, wc); };
+    int kt = 0, seg = 0;
+    int cs[2] = {0, 0};  // S_t issued
+    int cp[2] = {0, 0};  // P_t consumed
+    int co[2] = {0, 0};  // pieces that tile t took part in
+    bool ok = true;
+    // S_t of the next step of tile t from K stage s.
+    auto next_s = [&](int t, int s) {
+      if (C::EARLY_S && cs[t] >= 1 && !(ok = wait(&bars->s_free[t], (cs[t] - 1) & 1))) return;
+      tc_fence_after();
+      if (elect_one()) {
+        issue_s(t, s);
+        mma_commit(&bars->s_full[t]);
+      }
+      __syncwarp();
+      ++cs[t];
+    };
+    for (int i = 0; ok; ++i) {
+      const PagedPiece* pc = ring.get(i, wc);
+      if (!pc) break;
+      const int nt[2] = {pc->n[0], pc->n[1]};
+      ring.release(i);
+      const int n = max(nt[0], nt[1]);
+      if (n == 0) continue;
+      if (!(ok = wait(&bars->q_full, seg & 1))) break;
+      if (!(ok = wait(&bars->k_full[kt % C::STAGES], (kt / C::STAGES) & 1))) break;
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        if (ok && nt[t] > 0) next_s(t, kt % C::STAGES);
+      if (!ok) break;
+      if (elect_one()) {
+        mma_commit(&bars->k_empty[kt % C::STAGES]);
+        if (n == 1) mma_commit(&bars->q_empty);
+      }
+      __syncwarp();
+      for (int j = 0; ok && j < n; ++j) {
+        const int s = (kt + j) % C::STAGES, s1 = (kt + j + 1) % C::STAGES;
+        const uint32_t ph = ((kt + j) / C::STAGES) & 1, ph1 = ((kt + j + 1) / C::STAGES) & 1;
+        bool k_ready = false, v_ready = false;
+        auto want_k = [&]() {
+          if (!k_ready) k_ready = ok = wait(&bars->k_full[s1], ph1);
+          return k_ready;
+        };
+        if constexpr (C::EARLY_S) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+            if (ok && j + 1 < nt[t] && want_k()) next_s(t, s1);
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (!ok || j >= nt[t]) continue;
+          if (!(ok = wait(&bars->p_full[t], cp[t] & 1))) continue;
+          ++cp[t];
+          if (!v_ready && !(v_ready = ok = wait(&bars->v_ready[s], ph))) continue;
+          // The piece before has been read out of O_t.
+          if (j == 0 && co[t] >= 1 && !(ok = wait(&bars->o_free[t], (co[t] - 1) & 1))) continue;
+          tc_fence_after();
+          if (elect_one()) {
+            issue_pv(t, s, j > 0);
+            if (C::EARLY_S) mma_commit(&bars->pv_done[t]);
+            if (t == 1 || nt[1] <= j) mma_commit(&bars->v_empty[s]);
+            if (j + 1 == nt[t]) mma_commit(&bars->o_full[t]);
+          }
+          __syncwarp();
+          if (!C::EARLY_S && j + 1 < nt[t] && want_k()) next_s(t, s1);
+        }
+        if (ok && k_ready) {
+          if (elect_one()) {
+            mma_commit(&bars->k_empty[s1]);
+            if (j + 2 == n) mma_commit(&bars->q_empty);
+          }
+          __syncwarp();
+        }
+      }
+      kt += n;
+      ++seg;
+      co[0] += nt[0] > 0;
+      co[1] += nt[1] > 0;
+    }
+    // Nothing may still read shared memory or write TMEM once the CTA tears down.
+    if (elect_one()) mma_commit(&bars->mma_done);
+    __syncwarp();
+    if (lane == 0) mbar_wait_drain(&bars->mma_done, 0, a.err);
+    __syncwarp();
+    } else if (warp != 11) {
+    // ------------------------------------------------------------ TMA producers
+    const bool is_k = warp == C::K_WARP;
+    const CUtensorMap* tm = is_k ? &tm_k : &tm_v;
+    uint64_t* full = is_k ? bars->k_full : bars->v_full;
+    uint64_t* empty = is_k ? bars->k_empty : bars->v_empty;
+    uint8_t* tiles = smem + (is_k ? C::OFF_K : C::OFF_V);
+    const uint64_t pol_kv = l2_policy_evict_last();  // re-read by every unit of the (sequence, key head)
+    const uint64_t pol_q = l2_policy_evict_first();
+    const int shift = a.pv.page_shift, box = min(a.pv.page_size, C::BN), per_tile = C::BN / box;
+    const uint32_t q_bytes = static_cast<uint32_t>(TT * G) * 128 * C::NCHUNK;
+    int kt = 0, seg = 0;  // key tiles and Qs issued
+    bool ok = true;
+    for (int i = 0; ok; ++i) {
+      PagedPiece pc;
+      if (is_k) {
+        const bool more = cur.next(a, UT, seq, &pc);
+        for (int t = 0; t < 2; ++t) pc.n[t] = more ? tiles_of(a, pc, t) : 0;
+        if (!(ok = ring.put(i, more ? &pc : nullptr, lane, wc)) || !more) break;
+      } else {
+        const PagedPiece* p = ring.get(i, wc);
+        if (!p) break;
+        pc = *p;
+        ring.release(i);
+      }
+      const int n0 = pc.n[0], n1 = pc.n[1], n = max(n0, n1);
+      if (n == 0) continue;
+      const int* row = a.pv.table + pc.b * a.pv.table_stride;
+      // Boxes of a tile that hold a visible key, and this lane's page of it.
+      auto boxes = [&](int t) { return min(per_tile, (pc.key_hi - t * C::BN + box - 1) / box); };
+      auto page_of = [&](int t) { return lane < boxes(t) ? row[(t * C::BN >> shift) + lane] : 0; };
+      int page = page_of(pc.t_lo);
+      if (is_k) {
+        if (seg >= 1 && !(ok = mbar_wait_warp(&bars->q_empty, (seg - 1) & 1, wc))) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&bars->q_full, q_bytes * ((n0 > 0) + (n1 > 0)));
+          for (int t = 0; t < 2; ++t)
+            if ((t == 0 ? n0 : n1) > 0)
+              for (int c = 0; c < C::NCHUNK; ++c)
+                tma_load_4d(&tm_q, &bars->q_full, smem + C::OFF_Q + t * C::TILE_BYTES + c * C::CHUNK_BYTES, c * 64, 0, pc.h,
+                            pc.s.row0 + pc.tok0 + t * TT, pol_q);
+        }
+      }
+      ++seg;
+      for (int t = pc.t_lo; t < pc.t_lo + n; ++t, ++kt) {
+        const int s = kt % C::STAGES;
+        const int next_page = t + 1 < pc.t_lo + n ? page_of(t + 1) : 0;
+        if (!(ok = mbar_wait_warp(&empty[s], ((kt / C::STAGES) & 1) ^ 1, wc))) break;
+        const int nb = boxes(t);
+        if (lane == 0) mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(nb * box) * 128 * C::NCHUNK);
+        __syncwarp();
+        if (lane < nb)
+          load_page(tm, &full[s], tiles + s * C::TILE_BYTES + lane * box * 128 * C::NCHUNK, a.pv,
+                    (t * C::BN & (a.pv.page_size - 1)) >> 3, page, pc.h, is_k, pol_kv);
+        __syncwarp();
+        page = next_page;
+      }
+    }
+    __syncwarp();
+    if (lane == 0 && *reinterpret_cast<volatile int*>(&bars->abort)) {
+      // Never leave a copy in flight into shared memory this CTA is about to release.
+      if (is_k && seg > 0) mbar_wait_drain(&bars->q_full, (seg - 1) & 1, a.err);
+      for (int j = max(0, kt - C::STAGES); j < kt; ++j)
+        mbar_wait_drain(&full[j % C::STAGES], (j / C::STAGES) & 1, a.err);
+    }
+    __syncwarp();
+    }
   }
 
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 9) tmem_dealloc(tmem, C::TM_COLS);
+  if (warp == C::MMA_WARP) tmem_dealloc(tmem, C::TM_COLS);
 }
 
 namespace {

@@ -58,6 +58,7 @@ struct PagedPiece {
   int tok0, ntok;   // tokens of the unit
   int key_hi;       // keys end
   int t_lo, t_hi, k_lo, k_hi;
+  int n[2];         // forward kernel: key tiles from t_lo on that each query tile takes part in
   __device__ bool whole() const { return t_lo == k_lo && t_hi == k_hi; }
   __device__ int slot() const { return t_lo == k_lo ? 1 : 0; }
 };
