@@ -42,15 +42,21 @@ struct PfCfg {
   static constexpr int OFF_BAR = OFF_V + STAGES * TILE_BYTES;
   static constexpr int SMEM_BYTES = OFF_BAR + 1024 + 1024;
   static_assert(SMEM_BYTES > 120 * 1024, "one CTA per SM: it holds all 512 TMEM columns");
-  // Warps: 0-7 softmax, 8 the walk of the line, Q and K, 9 the products, 10 V, 11 none,
-  // 12-15 make V ready (one an SM quarter: two of them left the softmax warps that
-  // shared their quarters behind the others).  Registers: 128 a thread at launch, of
-  // which the softmax takes over 48 a thread of the other warpgroups
-  // (2 x 176 + 2 x 80 = 4 x 128).
-  static constexpr int THREADS = 512, K_WARP = 8, MMA_WARP = 9, READY_WARP = 12;
+  // Warps: 0-7 softmax; 8 the walk of the line, Q and K; 9 the products, and at d =
+  // 64 those of tile 0 only, 11 then tile 1's (ISSUERS below); 10 V; 12-15 make V
+  // ready (one an SM quarter: two of them left the softmax warps that shared their
+  // quarters behind the others).  Registers: 128 a thread at launch, of which the
+  // softmax takes over 48 a thread of the other warpgroups (2 x 176 + 2 x 80 =
+  // 4 x 128).
+  static constexpr int THREADS = 512, K_WARP = 8, MMA_WARP = 9, V_WARP = 10, READY_WARP = 12;
   // TMEM as in fwd.cu: at d = 64 P has columns of its own, so that the next S_t
   // can be computed while the softmax still works on this one.
   static constexpr bool EARLY_S = D == 64;
+  // A warp takes some 650 clocks to issue a product and wait for its operands:
+  // both tiles' four a step were the bound at d = 64 (690 TFLOP/s on long chunks;
+  // 826 with a warp a tile).  At d = 128 the products themselves take that long,
+  // and two warps' run into one another (1,199 TFLOP/s; 1,306 from one warp).
+  static constexpr int ISSUERS = D == 64 ? 2 : 1;
   static constexpr uint32_t TM_COLS = 512;
   __host__ __device__ static constexpr uint32_t tm_s(int t) { return 128u * t; }
   __host__ __device__ static constexpr uint32_t tm_p(int t) { return EARLY_S ? 256u + 64u * t : 128u * t; }
@@ -111,7 +117,7 @@ __global__ void __launch_bounds__(512, 1)
   if (warp == C::K_WARP) cur = paged_start(a, UT, lane, &seq);
   if (threadIdx.x == 32) {
     mbar_init(&bars->q_full, 1);
-    mbar_init(&bars->q_empty, 1);
+    mbar_init(&bars->q_empty, C::ISSUERS);
     for (int t = 0; t < 2; ++t) {
       mbar_init(&bars->s_full[t], 1);
       mbar_init(&bars->s_free[t], 4);
@@ -120,15 +126,15 @@ __global__ void __launch_bounds__(512, 1)
       mbar_init(&bars->o_full[t], 1);
       mbar_init(&bars->o_free[t], 4);
     }
-    mbar_init(&bars->mma_done, 1);
+    mbar_init(&bars->mma_done, C::ISSUERS);
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(&bars->k_full[s], 1);
-      mbar_init(&bars->k_empty[s], 1);
+      mbar_init(&bars->k_empty[s], C::ISSUERS);
       mbar_init(&bars->v_full[s], 1);
-      mbar_init(&bars->v_empty[s], 1);
+      mbar_init(&bars->v_empty[s], C::ISSUERS);
       mbar_init(&bars->v_ready[s], 4);
     }
-    bars->ring.init(14);  // the eight softmax warps, the four of READY_WARP, products, V
+    bars->ring.init(13 + C::ISSUERS);  // softmax, V's warps, the products
     bars->abort = 0;
     fence_barrier_init();
   }
@@ -380,114 +386,7 @@ __global__ void __launch_bounds__(512, 1)
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-    if (warp == C::MMA_WARP) {
-    // ------------------------------------------------------------ MMA issuer
-    constexpr uint32_t idesc_s = idesc_f16kind(E::kFmt, 128, C::BN, 0, 0);
-    constexpr uint32_t idesc_o = idesc_f16kind(PE::kFmt, 128, D, 0, 1);
-    const uint64_t q_desc = sdesc_sw128(smem_u32(smem + C::OFF_Q), 16, 1024);
-    const uint64_t k_desc = sdesc_sw128(smem_u32(smem + C::OFF_K), 16, C::GROUP);
-    const uint64_t v_desc = sdesc_sw128(smem_u32(smem + C::OFF_V), 1024, C::GROUP);
-    constexpr uint32_t kTileDesc = C::TILE_BYTES >> 4;
-    auto issue_s = [&](int t, int stage) {
-      const uint64_t qa = q_desc + t * kTileDesc, kb = k_desc + stage * kTileDesc;
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        mma_ss(tmem + C::tm_s(t), qa + (((kk >> 2) * C::CHUNK_BYTES + (kk & 3) * 32) >> 4),
-               kb + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), idesc_s, kk > 0);
-      }
-    };
-    auto issue_pv = [&](int t, int stage, bool acc) {
-      const uint64_t vb = v_desc + stage * kTileDesc;
-#pragma unroll
-      for (int kk = 0; kk < C::BN / 16; ++kk)
-        mma_ts(tmem + C::tm_o(t), tmem + C::tm_p(t) + kk * 8, vb + ((kk * 2 * C::GROUP) >> 4), idesc_o,
-               (acc || kk > 0) ? 1u : 0u);
-    };
-    auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_warp(bar, parity, wc); };
-    int kt = 0, seg = 0;
-    int cs[2] = {0, 0};  // S_t issued
-    int cp[2] = {0, 0};  // P_t consumed
-    int co[2] = {0, 0};  // pieces that tile t took part in
-    bool ok = true;
-    // S_t of the next step of tile t from K stage s.
-    auto next_s = [&](int t, int s) {
-      if (C::EARLY_S && cs[t] >= 1 && !(ok = wait(&bars->s_free[t], (cs[t] - 1) & 1))) return;
-      tc_fence_after();
-      if (elect_one()) {
-        issue_s(t, s);
-        mma_commit(&bars->s_full[t]);
-      }
-      __syncwarp();
-      ++cs[t];
-    };
-    for (int i = 0; ok; ++i) {
-      const PagedPiece* pc = ring.get(i, wc);
-      if (!pc) break;
-      const int nt[2] = {pc->n[0], pc->n[1]};
-      ring.release(i);
-      const int n = max(nt[0], nt[1]);
-      if (n == 0) continue;
-      if (!(ok = wait(&bars->q_full, seg & 1))) break;
-      if (!(ok = wait(&bars->k_full[kt % C::STAGES], (kt / C::STAGES) & 1))) break;
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-        if (ok && nt[t] > 0) next_s(t, kt % C::STAGES);
-      if (!ok) break;
-      if (elect_one()) {
-        mma_commit(&bars->k_empty[kt % C::STAGES]);
-        if (n == 1) mma_commit(&bars->q_empty);
-      }
-      __syncwarp();
-      for (int j = 0; ok && j < n; ++j) {
-        const int s = (kt + j) % C::STAGES, s1 = (kt + j + 1) % C::STAGES;
-        const uint32_t ph = ((kt + j) / C::STAGES) & 1, ph1 = ((kt + j + 1) / C::STAGES) & 1;
-        bool k_ready = false, v_ready = false;
-        auto want_k = [&]() {
-          if (!k_ready) k_ready = ok = wait(&bars->k_full[s1], ph1);
-          return k_ready;
-        };
-        if constexpr (C::EARLY_S) {
-#pragma unroll
-          for (int t = 0; t < 2; ++t)
-            if (ok && j + 1 < nt[t] && want_k()) next_s(t, s1);
-        }
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (!ok || j >= nt[t]) continue;
-          if (!(ok = wait(&bars->p_full[t], cp[t] & 1))) continue;
-          ++cp[t];
-          if (!v_ready && !(v_ready = ok = wait(&bars->v_ready[s], ph))) continue;
-          // The piece before has been read out of O_t.
-          if (j == 0 && co[t] >= 1 && !(ok = wait(&bars->o_free[t], (co[t] - 1) & 1))) continue;
-          tc_fence_after();
-          if (elect_one()) {
-            issue_pv(t, s, j > 0);
-            if (C::EARLY_S) mma_commit(&bars->pv_done[t]);
-            if (t == 1 || nt[1] <= j) mma_commit(&bars->v_empty[s]);
-            if (j + 1 == nt[t]) mma_commit(&bars->o_full[t]);
-          }
-          __syncwarp();
-          if (!C::EARLY_S && j + 1 < nt[t] && want_k()) next_s(t, s1);
-        }
-        if (ok && k_ready) {
-          if (elect_one()) {
-            mma_commit(&bars->k_empty[s1]);
-            if (j + 2 == n) mma_commit(&bars->q_empty);
-          }
-          __syncwarp();
-        }
-      }
-      kt += n;
-      ++seg;
-      co[0] += nt[0] > 0;
-      co[1] += nt[1] > 0;
-    }
-    // Nothing may still read shared memory or write TMEM once the CTA tears down.
-    if (elect_one()) mma_commit(&bars->mma_done);
-    __syncwarp();
-    if (lane == 0) mbar_wait_drain(&bars->mma_done, 0, a.err);
-    __syncwarp();
-    } else if (warp != 11) {
+    if (warp == C::K_WARP || warp == C::V_WARP) {
     // ------------------------------------------------------------ TMA producers
     const bool is_k = warp == C::K_WARP;
     const CUtensorMap* tm = is_k ? &tm_k : &tm_v;
@@ -552,6 +451,105 @@ __global__ void __launch_bounds__(512, 1)
       for (int j = max(0, kt - C::STAGES); j < kt; ++j)
         mbar_wait_drain(&full[j % C::STAGES], (j / C::STAGES) & 1, a.err);
     }
+    __syncwarp();
+    } else if (warp == C::MMA_WARP || C::ISSUERS == 2) {
+    // ------------------------------------------------------------ MMA issuers
+    constexpr int NT = 2 / C::ISSUERS;  // query tiles of this warp, from t0 on
+    const int t0 = warp == C::MMA_WARP ? 0 : 1;
+    constexpr uint32_t idesc_s = idesc_f16kind(E::kFmt, 128, C::BN, 0, 0);
+    constexpr uint32_t idesc_o = idesc_f16kind(PE::kFmt, 128, D, 0, 1);
+    const uint64_t q_desc = sdesc_sw128(smem_u32(smem + C::OFF_Q + t0 * C::TILE_BYTES), 16, 1024);
+    const uint64_t k_desc = sdesc_sw128(smem_u32(smem + C::OFF_K), 16, C::GROUP);
+    const uint64_t v_desc = sdesc_sw128(smem_u32(smem + C::OFF_V), 1024, C::GROUP);
+    constexpr uint32_t kTileDesc = C::TILE_BYTES >> 4;
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_warp(bar, parity, wc); };
+    int kt = 0, seg = 0;
+    int cs[NT] = {}, cp[NT] = {}, co[NT] = {};  // S issued, P consumed, pieces that the tile took part in
+    int nt[NT], n = 0;
+    bool ok = true;
+    auto issue_s = [&](int u, int j) {
+      if (C::EARLY_S && cs[u] >= 1 && !(ok = wait(&bars->s_free[t0 + u], (cs[u] - 1) & 1))) return;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t kd = k_desc + (kt + j) % C::STAGES * kTileDesc;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_ss(tmem + C::tm_s(t0 + u), q_desc + u * kTileDesc + (((kk >> 2) * C::CHUNK_BYTES + (kk & 3) * 32) >> 4),
+                 kd + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), idesc_s, kk > 0);
+        mma_commit(&bars->s_full[t0 + u]);
+      }
+      __syncwarp();
+      ++cs[u];
+    };
+    auto want_k = [&](int j) { return ok = wait(&bars->k_full[(kt + j) % C::STAGES], ((kt + j) / C::STAGES) & 1); };
+    // This warp is done with the K tile of step j (and Q after the last).
+    auto release_k = [&](int j) {
+      if (elect_one()) {
+        mma_commit(&bars->k_empty[(kt + j) % C::STAGES]);
+        if (j == n - 1) mma_commit(&bars->q_empty);
+      }
+      __syncwarp();
+    };
+    auto all_s = [&](int j) {
+      if (!want_k(j)) return;
+#pragma unroll
+      for (int u = 0; u < NT; ++u)
+        if (ok && j < nt[u]) issue_s(u, j);
+      if (ok) release_k(j);
+    };
+    for (int i = 0; ok; ++i) {
+      const PagedPiece* pc = ring.get(i, wc);
+      if (!pc) break;
+      n = max(pc->n[0], pc->n[1]);
+#pragma unroll
+      for (int u = 0; u < NT; ++u) nt[u] = pc->n[t0 + u];
+      ring.release(i);
+      if (n == 0) continue;
+      if (!(ok = wait(&bars->q_full, seg & 1))) break;
+      all_s(0);
+      for (int j = 0; ok && j < n; ++j) {
+        const int s = (kt + j) % C::STAGES;
+        if (C::EARLY_S && j + 1 < n) all_s(j + 1);
+        if (!ok || !(ok = wait(&bars->v_ready[s], ((kt + j) / C::STAGES) & 1))) break;
+        bool k_ready = false, v_released = false;
+#pragma unroll
+        for (int u = 0; u < NT; ++u) {
+          const int t = t0 + u;
+          if (!ok || j >= nt[u]) continue;
+          // The piece before has been read out of O.
+          if (j == 0 && co[u] >= 1 && !(ok = wait(&bars->o_free[t], (co[u] - 1) & 1))) continue;
+          if (!(ok = wait(&bars->p_full[t], cp[u] & 1))) continue;
+          ++cp[u];
+          const bool last = u + 1 == NT || j >= nt[NT - 1];
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < C::BN / 16; ++kk)
+              mma_ts(tmem + C::tm_o(t), tmem + C::tm_p(t) + kk * 8, v_desc + s * kTileDesc + ((kk * 2 * C::GROUP) >> 4),
+                     idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
+            if (C::EARLY_S) mma_commit(&bars->pv_done[t]);
+            if (last) mma_commit(&bars->v_empty[s]);
+            if (j + 1 == nt[u]) mma_commit(&bars->o_full[t]);
+          }
+          __syncwarp();
+          v_released = last;
+          if (!C::EARLY_S && j + 1 < nt[u] && (k_ready || (k_ready = want_k(j + 1)))) issue_s(u, j + 1);
+        }
+        if (ok && !v_released) {  // none of this warp's tiles takes part any more
+          if (elect_one()) mma_commit(&bars->v_empty[s]);
+          __syncwarp();
+        }
+        if (!C::EARLY_S && ok && j + 1 < n) release_k(j + 1);
+      }
+      kt += n;
+      ++seg;
+#pragma unroll
+      for (int u = 0; u < NT; ++u) co[u] += nt[u] > 0;
+    }
+    // Nothing may still read shared memory or write TMEM once the CTA tears down.
+    if (elect_one()) mma_commit(&bars->mma_done);
+    __syncwarp();
+    if (lane == 0) mbar_wait_drain(&bars->mma_done, 0, a.err);
     __syncwarp();
     }
   }
