@@ -3,7 +3,9 @@
     python -m exact_attention_67_gb300.build [--force]
 
 Each .cu file is compiled in parallel to an object file, then linked into
-exact_attention_67_gb300/_build/libexattn.so.  No CMake, one -gencode.
+exact_attention_67_gb300/_build/libexattn.so; binding.cpp, the Python side of
+the paged-cache calls, is compiled by g++ against PyTorch's headers and linked
+to it as _build/_exattn_binding.so.  No CMake, one -gencode.
 """
 from __future__ import annotations
 
@@ -20,6 +22,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libexattn.so")
+BINDING = os.path.join(OUT_DIR, "_exattn_binding.so")
 SOURCES = ["api.cu", "fwd.cu", "merge.cu", "bwd.cu", "dq.cu", "decode.cu", "noalloc.cu", "host.cu",
            "paged_api.cu", "rotary.cu", "pages.cu", "paged_decode.cu", "paged_fwd.cu", "paged_merge.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -41,7 +44,23 @@ def _deps_mtime() -> float:
 
 
 def up_to_date() -> bool:
-    return os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime()
+    return all(os.path.exists(f) and os.path.getmtime(f) >= _deps_mtime() for f in (LIB, BINDING))
+
+
+def _binding_flags():
+    """Compiler and linker flags of binding.cpp: PyTorch's headers and libraries
+    (loaded before the module is), Python's headers."""
+    import sysconfig
+
+    import torch
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    includes = [os.path.join(base, "include"), sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    compile_flags = ["-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                     "-I", INCLUDE, *[x for i in includes for x in ("-isystem", i)]]
+    link_flags = ["-shared", "-L", OUT_DIR, "-lexattn", "-Wl,-rpath,$ORIGIN", "-L", os.path.join(base, "lib"),
+                  "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    return compile_flags, link_flags
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
@@ -62,14 +81,31 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             print(r.stdout + r.stderr, flush=True)
         return obj
 
-    with cf.ThreadPoolExecutor(len(SOURCES)) as ex:
+    cxx = os.environ.get("CXX", "g++")
+    binding_obj = os.path.join(OUT_DIR, "binding.o")
+    compile_flags, link_flags = _binding_flags()
+
+    def compile_binding():
+        cmd = [cxx, *compile_flags, "-c", os.path.join(CSRC, "binding.cpp"), "-o", binding_obj]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"{cxx} failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
+
+    with cf.ThreadPoolExecutor(len(SOURCES) + 1) as ex:
+        bound = ex.submit(compile_binding)
         objs = list(ex.map(compile_one, SOURCES))
+        bound.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    tmp = BINDING + f".tmp{os.getpid()}"
+    r = subprocess.run([cxx, binding_obj, "-o", tmp, *link_flags], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of the binding failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
     return LIB
 
 
