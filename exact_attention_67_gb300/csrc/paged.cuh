@@ -12,6 +12,28 @@ int setup_device(int* dev, unsigned** err);
 bool encode_map(CUtensorMap* m, int dtype, int rank, const void* base, const cuuint64_t* dims,
                 const cuuint64_t* strides, const cuuint32_t* box);
 
+// Launches a kernel that may start before the stream's last kernel has ended (a
+// programmatic dependent launch): it sets itself up meanwhile and executes
+// griddepcontrol.wait before it reads or writes global memory, which holds it
+// until everything before it in the stream is done and visible.
+template <typename... Args, typename... Given>
+cudaError_t launch_dependent(const char* what, void (*kern)(Args...), dim3 grid, dim3 block, int smem,
+                             cudaStream_t stream, const Given&... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+  const cudaError_t last = cudaGetLastError();  // also clears a launch error e reported
+  return note_cuda(e != cudaSuccess ? e : last, what);
+}
+
 // Pages of a cache: K and V are [num_pages, Hkv, page_size, d] views (Strides:
 // b = page, h = head, n = row), and row b of the table lists the pages of
 // sequence b in order.

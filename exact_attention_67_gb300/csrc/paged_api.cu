@@ -232,13 +232,13 @@ AttendPlan paged_plan(int B, int Hq, int Hkv, int total, int max_q, int max_k, i
   p.rows = p.cols ? std::max(p.cols, 16) : kPagedRows;
   p.tile_tokens = (p.cols ? p.cols : 128) / G;
   p.unit_cost = 2;
-  p.min_chunk = 6;
+  p.min_chunk = 3;
   const int ut = p.cols ? p.tile_tokens : 2 * p.tile_tokens;
   // At most so many weights (paged_sched.cuh): units of full length.
   const double units = static_cast<double>(Hkv) * std::min<double>(static_cast<double>(B) * ((max_q + ut - 1) / ut),
                                                                    static_cast<double>(total) / ut + B);
   p.weights = units * ((static_cast<double>(max_k) + 127) / 128 + p.unit_cost);
-  p.ctas = static_cast<int>(std::min<double>(kSMs, std::max(1.0, std::ceil(p.weights / p.min_chunk))));
+  p.ctas = static_cast<int>(std::min<double>(kSMs, std::max(1.0, std::ceil(p.weights / 2))));
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
   const size_t slots = static_cast<size_t>(p.ctas) * 2 * p.rows;
   p.plan_bytes = up(static_cast<size_t>(p.ctas) * 32);  // a PagedPlan each

@@ -196,10 +196,9 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int UT = a.tile_tokens, G = a.G;
 
-  // The walking warp finds its place while the others set up.
   PagedCursor cur{};
   PagedSeq seq{};
-  if (warp == C::K_WARP) cur = paged_start(a, UT, lane, &seq);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 32) {
     for (int b = 0; b < 2; ++b) {
       mbar_init(&bars->q_full[b], 1);
@@ -239,10 +238,13 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
   for (int i = threadIdx.x; i < C::QBUF * C::Q_TILE / 16; i += C::THREADS)
     reinterpret_cast<uint4*>(smem + C::OFF_Q)[i] = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
+  // Up to here this CTA may run beside the stream's last kernel.  The walking warp
+  // finds its place in the line.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (warp == C::K_WARP) cur = paged_start(a, UT, lane, &seq);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tmem = bars->tmem_base;
   const WaitCtl wc{&bars->abort, a.err};
   PagedRing& ring = bars->ring;
@@ -665,8 +667,8 @@ cudaError_t launch_n(const PagedArgs& a, cudaStream_t stream) {
   auto kern = paged_decode_kernel<T, D, NC>;
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), C::SMEM_BYTES, a.device);
   if (e != cudaSuccess) return e;
-  kern<<<a.ctas, C::THREADS, C::SMEM_BYTES, stream>>>(*a.tm_q, *a.tm_k, *a.tm_v, a);
-  return note_cuda(cudaGetLastError(), "paged decode kernel launch");
+  return launch_dependent("paged decode kernel launch", kern, a.ctas, C::THREADS, C::SMEM_BYTES, stream, *a.tm_q, *a.tm_k,
+                          *a.tm_v, a);
 }
 
 template <typename T, int D>

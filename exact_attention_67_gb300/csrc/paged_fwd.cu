@@ -111,10 +111,9 @@ __global__ void __launch_bounds__(512, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int TT = a.tile_tokens, UT = 2 * TT, G = a.G;
 
-  // The walking warp finds its place while the others set up.
   PagedCursor cur{};
   PagedSeq seq{};
-  if (warp == C::K_WARP) cur = paged_start(a, UT, lane, &seq);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 32) {
     mbar_init(&bars->q_full, 1);
     mbar_init(&bars->q_empty, C::ISSUERS);
@@ -142,10 +141,13 @@ __global__ void __launch_bounds__(512, 1)
     tmem_alloc(&bars->tmem_base, C::TM_COLS);
     tmem_relinquish();
   }
+  // Up to here this CTA may run beside the stream's last kernel.  The walking warp
+  // finds its place in the line.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (warp == C::K_WARP) cur = paged_start(a, UT, lane, &seq);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tmem = bars->tmem_base;
   const WaitCtl wc{&bars->abort, a.err};
   PagedRing& ring = bars->ring;
@@ -568,8 +570,8 @@ cudaError_t launch_t(const PagedArgs& a, cudaStream_t stream) {
   auto kern = paged_fwd_kernel<T, D>;
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), C::SMEM_BYTES, a.device);
   if (e != cudaSuccess) return e;
-  kern<<<a.ctas, C::THREADS, C::SMEM_BYTES, stream>>>(*a.tm_q, *a.tm_k, *a.tm_v, a);
-  return note_cuda(cudaGetLastError(), "paged forward kernel launch");
+  return launch_dependent("paged forward kernel launch", kern, a.ctas, C::THREADS, C::SMEM_BYTES, stream, *a.tm_q, *a.tm_k,
+                          *a.tm_v, a);
 }
 
 }  // namespace

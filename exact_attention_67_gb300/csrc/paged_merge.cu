@@ -23,6 +23,8 @@ __global__ void __launch_bounds__(64 * WPR) paged_merge_kernel(const __grid_cons
   constexpr int BATCH = 4;       // pieces a warp loads at once
   __shared__ float red[2 * WPR];
   __shared__ float acc_s[2 * WPR][D];
+  // The next kernel of the stream may set itself up; this one waits for the pieces.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int g = static_cast<int>(blockIdx.x) + 1;  // boundary between CTAs g - 1 and g
   const PagedPlan p = a.plan[g];
@@ -34,9 +36,9 @@ __global__ void __launch_bounds__(64 * WPR) paged_merge_kernel(const __grid_cons
   const bool live = tok < p.ntok;
   // Pieces: CTA g - 1 + i has the weights [i chunk - lead, (i + 1) chunk - lead)
   // of the unit, lead those of its chunk that lie before it.
-  const int w = p.tiles + a.unit_cost, lead = p.chunk - p.pos;
+  const int w = p.tiles + p.cost, lead = p.chunk - p.pos;
   const int pieces = (w + lead + p.chunk - 1) / p.chunk;
-  auto tiles_before = [&](int x) { return max(0, min(w, x) - a.unit_cost); };  // in the unit's first x weights
+  auto tiles_before = [&](int x) { return max(0, min(w, x) - p.cost); };  // in the unit's first x weights
   auto from = [&](int i) { return tiles_before(i * p.chunk - lead); };
   // All its key tiles on one CTA: that CTA has written the rows itself.
   int used = 0;
@@ -114,6 +116,8 @@ __global__ void __launch_bounds__(64 * WPR) paged_merge_kernel(const __grid_cons
 template <typename T, int D>
 __global__ void __launch_bounds__(128) paged_merge_rows_kernel(const __grid_constant__ PagedArgs a) {
   constexpr int C4 = D / 16;  // 4-column vectors a warp
+  // The next kernel of the stream may set itself up; this one waits for the pieces.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int g = static_cast<int>(blockIdx.x) + 1;
   const PagedPlan p = a.plan[g];
@@ -121,9 +125,9 @@ __global__ void __launch_bounds__(128) paged_merge_rows_kernel(const __grid_cons
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t = static_cast<int>(blockIdx.y) >> 2, row = (static_cast<int>(blockIdx.y) & 3) * 32 + lane;
   const int row_tok = row / a.G, tok = t * a.tile_tokens + row_tok;
-  const int w = p.tiles + a.unit_cost, lead = p.chunk - p.pos;
+  const int w = p.tiles + p.cost, lead = p.chunk - p.pos;
   const int pieces = (w + lead + p.chunk - 1) / p.chunk;
-  auto tiles_before = [&](int x) { return max(0, min(w, x) - a.unit_cost); };
+  auto tiles_before = [&](int x) { return max(0, min(w, x) - p.cost); };
   auto from = [&](int i) { return tiles_before(i * p.chunk - lead); };
   int used = 0;
   for (int i = 0; i < pieces && used < 2; ++i) used += from(i + 1) > from(i);
@@ -165,20 +169,11 @@ __global__ void __launch_bounds__(128) paged_merge_rows_kernel(const __grid_cons
 template <typename T, int D>
 cudaError_t launch_t(const PagedArgs& a, cudaStream_t stream) {
   const bool few = a.cols > 0, deep = few && a.cols <= 8;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.ctas - 1, few ? a.cols / 2 : 8);
-  cfg.blockDim = dim3(deep ? 512 : 128);
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = deep  ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<T, D, 8>, a)
-                        : few ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<T, D, 2>, a)
-                              : cudaLaunchKernelEx(&cfg, paged_merge_rows_kernel<T, D>, a);
-  const cudaError_t last = cudaGetLastError();
-  return note_cuda(e != cudaSuccess ? e : last, "paged merge kernel launch");
+  const dim3 grid(a.ctas - 1, few ? a.cols / 2 : 8), block(deep ? 512 : 128);
+  const char* what = "paged merge kernel launch";
+  return deep  ? launch_dependent(what, paged_merge_kernel<T, D, 8>, grid, block, 0, stream, a)
+         : few ? launch_dependent(what, paged_merge_kernel<T, D, 2>, grid, block, 0, stream, a)
+               : launch_dependent(what, paged_merge_rows_kernel<T, D>, grid, block, 0, stream, a);
 }
 
 }  // namespace

@@ -14,6 +14,8 @@
 #include "paged.cuh"
 #include "ptx.cuh"
 
+#include <limits.h>
+
 namespace exattn {
 
 constexpr int kKeyTile = 128;
@@ -102,6 +104,7 @@ struct PagedRing {
 struct PagedCursor {
   int b, h, t;
   int pos;    // weights of unit t already passed
+  int cost;   // fixed weight of a unit
   int left;   // weights left of this CTA's chunk
 
   // The next piece with anything to do (an empty unit has its zeros to
@@ -123,7 +126,7 @@ struct PagedCursor {
       int lo, hi;
       paged_keys(a, s, t0, t1, &lo, &hi);
       const int k0 = lo / kKeyTile, k1 = hi > lo ? (hi + kKeyTile - 1) / kKeyTile : k0;
-      const int w = k1 - k0 + a.unit_cost;
+      const int w = k1 - k0 + cost;
       const int take = min(left, w - pos);
       p->s = s;
       p->b = b;
@@ -133,8 +136,8 @@ struct PagedCursor {
       p->key_hi = hi;
       p->k_lo = k0;
       p->k_hi = k1;
-      p->t_lo = k0 + max(0, pos - a.unit_cost);
-      p->t_hi = k0 + max(0, pos + take - a.unit_cost);
+      p->t_lo = k0 + max(0, pos - cost);
+      p->t_hi = k0 + max(0, pos + take - cost);
       const bool first = pos == 0;
       left -= take;
       pos += take;
@@ -167,8 +170,9 @@ struct PagedPlan {
   int pos;           // weights of the unit before the boundary (0: it starts there)
   int chunk;
   int tiles;         // key tiles of the unit
+  int cost;          // its fixed weight
   int row, ntok, h;  // its first packed row, tokens, key head
-  int unused[2];
+  int unused;
 };
 
 // Start of this CTA's chunk, found by one warp; the same in every lane.  Leaves
@@ -181,16 +185,44 @@ __device__ __forceinline__ PagedCursor paged_start(const PagedArgs& a, int UT, i
   const int w0 = paged_weight(a, s0, UT) * a.Hkv;  // kept: most batches have at most 32 sequences
   int W = __reduce_add_sync(0xffffffffu, w0);
   for (int b0 = 32; b0 < B; b0 += 32) W += __reduce_add_sync(0xffffffffu, paged_weight(a, read(b0 + lane), UT) * a.Hkv);
-  const int chunk = max((W + a.ctas - 1) / a.ctas, a.min_chunk);
+  int chunk = max((W + a.ctas - 1) / a.ctas, a.min_chunk), cost = a.unit_cost;
+  if (a.cols > 0) {
+    // The decode kernel: a unit is a (sequence, key head).  Do all that exist weigh
+    // the same, with `tiles` key tiles each?
+    int most = w0, least = w0 > 0 ? w0 : INT_MAX, count = w0 > 0;
+    for (int b0 = 32; b0 < B; b0 += 32) {
+      const int w = paged_weight(a, read(b0 + lane), UT) * a.Hkv;
+      most = max(most, w);
+      least = min(least, w > 0 ? w : INT_MAX);
+      count += w > 0;
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
+    least = __reduce_min_sync(0xffffffffu, least);
+    const int units = __reduce_add_sync(0xffffffffu, count) * a.Hkv, tiles = most / a.Hkv - a.unit_cost;
+    if (most == least && tiles > 0 && units <= a.ctas) {
+      // As many pieces a unit as CTAs, of two tiles at least; none of four or fewer
+      // (joining pieces takes some 2 us, a tile 0.6).  Unless this leaves over a
+      // quarter of the SMs out of long work.
+      const int each = tiles <= 4 ? tiles : max((tiles + a.ctas / units - 1) / (a.ctas / units), 2);
+      const int k = (tiles + each - 1) / each;
+      if (4 * units * k >= 3 * a.ctas || each <= 4) {
+        chunk = each;
+        cost = k * chunk - tiles;  // less than a chunk: the first piece's tiles are fewer by it
+        W = units * k * chunk;
+      }
+    }
+  }
   const long long lo64 = static_cast<long long>(cta) * chunk;
-  PagedCursor c{0, 0, 0, 0, 0};
-  PagedPlan plan{0, chunk, 0, 0, 0, 0, {0, 0}};
+  const int pad = cost - a.unit_cost;  // of every unit's weight
+  PagedCursor c{0, 0, 0, 0, cost, 0};
+  PagedPlan plan{0, chunk, 0, cost, 0, 0, 0, 0};
   *seq = PagedSeq{0, 0, 0, 0};
   int before = 0;
   for (int b0 = 0; b0 < B && lo64 < W; b0 += 32) {
     const int lo = static_cast<int>(lo64);
     const PagedSeq sl = b0 == 0 ? s0 : read(b0 + lane);
-    const int w = b0 == 0 ? w0 : paged_weight(a, sl, UT) * a.Hkv;
+    int w = b0 == 0 ? w0 : paged_weight(a, sl, UT) * a.Hkv;
+    if (w > 0 && pad != 0) w += pad * a.Hkv;  // only where a sequence has one unit a key head
     int inc = w;  // inclusive prefix over the lanes
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -214,13 +246,13 @@ __device__ __forceinline__ PagedCursor paged_start(const PagedArgs& a, int UT, i
       int tiles;
       for (;;) {
         tiles = paged_tiles(a, s, c.t * UT, UT);
-        if (r < tiles + a.unit_cost) break;
-        r -= tiles + a.unit_cost;
+        if (r < tiles + cost) break;
+        r -= tiles + cost;
         ++c.t;
       }
       c.pos = r;
       *seq = s;
-      plan = PagedPlan{r, chunk, tiles, s.row0 + c.t * UT, min(UT, s.n - c.t * UT), c.h, {0, 0}};
+      plan = PagedPlan{r, chunk, tiles, cost, s.row0 + c.t * UT, min(UT, s.n - c.t * UT), c.h, 0};
       break;
     }
     before += __shfl_sync(0xffffffffu, inc, 31);

@@ -24,6 +24,8 @@ template <int N>
 __global__ void __launch_bounds__(kThreads) page_copy_kernel(const __grid_constant__ Pairs<N> p, char* pool,
                                                              long long slab_stride, long long page_stride,
                                                              long long page_bytes, int pieces) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int pair = static_cast<int>(blockIdx.x) / pieces, piece = static_cast<int>(blockIdx.x) % pieces;
   char* slab = pool + blockIdx.y * slab_stride;
   const char* src = slab + p.src[pair] * page_stride;
@@ -51,8 +53,8 @@ cudaError_t launch_n(const CopyArgs& a, int at, int n, cudaStream_t stream) {
   }
   const int pieces = static_cast<int>((a.page_bytes + kPiece - 1) / kPiece);
   const dim3 grid(static_cast<unsigned>(n) * pieces, a.slabs);
-  page_copy_kernel<N><<<grid, kThreads, 0, stream>>>(p, a.pool, a.slab_stride, a.page_stride, a.page_bytes, pieces);
-  return note_cuda(cudaGetLastError(), "page copy kernel launch");
+  return launch_dependent("page copy kernel launch", page_copy_kernel<N>, grid, kThreads, 0, stream, p, a.pool,
+                          a.slab_stride, a.page_stride, a.page_bytes, pieces);
 }
 
 }  // namespace

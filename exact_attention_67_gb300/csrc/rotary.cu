@@ -89,6 +89,8 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_consta
   __shared__ alignas(16) float cos_s[kMaxTok * (D / 2)], sin_s[kMaxTok * (D / 2)];
   __shared__ Token tk[kMaxTok];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const long long t0 = static_cast<long long>(blockIdx.x) * tok_per_block;
   const int nt = static_cast<int>(min(static_cast<long long>(tok_per_block), tokens - t0));
 
@@ -262,8 +264,7 @@ cudaError_t launch_t(const RotaryArgs& a, cudaStream_t stream) {
   while (tok < kMaxTok && tok < kRows && tokens / (2 * tok) >= 152 * 16) tok *= 2;
   const long long grid = (tokens + tok - 1) / tok;
   auto kern = a.append ? rotary_kernel<T, D, V, IL, true> : rotary_kernel<T, D, V, IL, false>;
-  kern<<<static_cast<unsigned>(grid), kThreads, 0, stream>>>(a, tok, tokens);
-  return note_cuda(cudaGetLastError(), "rotary kernel launch");
+  return launch_dependent("rotary kernel launch", kern, static_cast<unsigned>(grid), kThreads, 0, stream, a, tok, tokens);
 }
 
 template <typename T, int D>
