@@ -51,11 +51,13 @@ struct PdCfg {
   static constexpr int QBUF = NC == 32 ? 1 : 2;  // Q tiles in shared memory
   static constexpr int P_CHUNK = NQ * 128;
   static constexpr int P_TILE = 2 * P_CHUNK;
-  static constexpr int STAGES = D == 128 ? 3 : 6;  // 192 KB of K and V
+  // 192 KB of K and V.  A V tile is held longer (converted, and until its weights
+  // are there): some 3,500 clocks from its load against 1,800.
+  static constexpr int K_STAGES = D == 128 ? 2 : 4, V_STAGES = 2 * K_STAGES;
   // V before K: the 128-row read of a 64-wide V tile stays inside the buffers.
   static constexpr int OFF_V = 0;
-  static constexpr int OFF_K = OFF_V + STAGES * KV_TILE;
-  static constexpr int OFF_Q = OFF_K + STAGES * KV_TILE;
+  static constexpr int OFF_K = OFF_V + V_STAGES * KV_TILE;
+  static constexpr int OFF_Q = OFF_K + K_STAGES * KV_TILE;
   static constexpr int OFF_P = OFF_Q + QBUF * Q_TILE;
   // Floats: maxima [2 groups][NC][4]; by the piece's parity the references
   // [2][2][NC] and the sums of unrounded and rounded weights [2][2][2][NC][4];
@@ -73,11 +75,11 @@ struct PdCfg {
   static constexpr uint32_t TM_S = 0, TM_O = 4 * NQ, TM_COLS = 8 * NQ;
 };
 
-template <int STAGES>
+template <int KS, int VS>
 struct PdBars {
   uint64_t q_full[2], q_empty[2];
-  uint64_t k_full[STAGES], k_empty[STAGES];
-  uint64_t v_full[STAGES], v_empty[STAGES], v_ready[STAGES];
+  uint64_t k_full[KS], k_empty[KS];
+  uint64_t v_full[VS], v_empty[VS], v_ready[VS];
   uint64_t s_full[4], s_free[4], p_full[2], p_free[2];
   uint64_t o_full[2], o_free[2];
   uint64_t done[2];  // teardown: all of the issuing warp's products
@@ -184,7 +186,7 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
   using C = PdCfg<D, NC>;
   using E = Elem<T>;
   using PE = Elem<__half>;
-  using Bars = PdBars<C::STAGES>;
+  using Bars = PdBars<C::K_STAGES, C::V_STAGES>;
   constexpr bool kConvertV = E::kFmt != PE::kFmt;
   constexpr bool kRounded = !kConvertV;  // O normalised by the rounded weights' sum
   constexpr int NQ = C::NQ, BN = C::BN;
@@ -213,9 +215,11 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
       mbar_init(&bars->s_full[b], 1);
       mbar_init(&bars->s_free[b], 4);
     }
-    for (int s = 0; s < C::STAGES; ++s) {
+    for (int s = 0; s < C::K_STAGES; ++s) {
       mbar_init(&bars->k_full[s], 1);
       mbar_init(&bars->k_empty[s], 1);
+    }
+    for (int s = 0; s < C::V_STAGES; ++s) {
       mbar_init(&bars->v_full[s], 1);
       mbar_init(&bars->v_empty[s], 1);
       mbar_init(&bars->v_ready[s], 4);
@@ -478,8 +482,8 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
       const int t_lo = pc->t_lo, t_hi = pc->t_hi, key_hi = pc->key_hi;
       ring.release(k);
       for (int t = t_lo; t < t_hi; ++t, ++st) {
-        const int s = st % C::STAGES, rows = key_hi - t * BN;
-        if (!(ok = mbar_wait_warp(&bars->v_full[s], (st / C::STAGES) & 1, wc))) break;
+        const int s = st % C::V_STAGES, rows = key_hi - t * BN;
+        if (!(ok = mbar_wait_warp(&bars->v_full[s], (st / C::V_STAGES) & 1, wc))) break;
         uint4* tile = reinterpret_cast<uint4*>(smem + C::OFF_V + s * C::KV_TILE);
         if constexpr (kConvertV) {
 #pragma unroll
@@ -523,8 +527,8 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
       if (!(ok = wait(&bars->q_full[qb], (seg / C::QBUF) & 1))) break;
       const uint64_t qd = q_desc + ((qb * C::Q_TILE) >> 4);
       for (int j = 0; j < n; ++j, ++st) {
-        const int s = st % C::STAGES, b = st & 3;
-        if (!(ok = wait(&bars->k_full[s], (st / C::STAGES) & 1))) break;
+        const int s = st % C::K_STAGES, b = st & 3;
+        if (!(ok = wait(&bars->k_full[s], (st / C::K_STAGES) & 1))) break;
         if (st >= 4 && !(ok = wait(&bars->s_free[b], ((st >> 2) - 1) & 1))) break;
         tc_fence_after();
         if (elect_one()) {
@@ -563,8 +567,8 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
       ring.release(i);
       if (n == 0) continue;
       for (int j = 0; j < n; ++j, ++st) {
-        const int s = st % C::STAGES, w = st & 1;
-        if (!(ok = wait(&bars->v_ready[s], (st / C::STAGES) & 1))) break;
+        const int s = st % C::V_STAGES, w = st & 1;
+        if (!(ok = wait(&bars->v_ready[s], (st / C::V_STAGES) & 1))) break;
         // The unit two before has been read out of these accumulators.
         if (j == 0 && seg >= 2 && !(ok = wait(&bars->o_free[ob], ((seg >> 1) - 1) & 1))) break;
         if (!(ok = wait(&bars->p_full[w], (st >> 1) & 1))) break;
@@ -594,6 +598,7 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
     uint64_t* full = is_k ? bars->k_full : bars->v_full;
     uint64_t* empty = is_k ? bars->k_empty : bars->v_empty;
     uint8_t* tiles = smem + (is_k ? C::OFF_K : C::OFF_V);
+    const int stages = is_k ? C::K_STAGES : C::V_STAGES;  // a power of two
     const uint64_t pol = l2_policy_evict_first();
     const int shift = a.pv.page_shift, box = min(a.pv.page_size, BN), per_tile = BN / box;
     const uint32_t q_bytes = static_cast<uint32_t>(UT * G) * 128 * C::NCHUNK;
@@ -628,9 +633,9 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
       }
       ++seg;
       for (int t = pc.t_lo; t < pc.t_hi; ++t, ++st) {
-        const int s = st % C::STAGES;
+        const int s = st & (stages - 1);
         const int next_page = t + 1 < pc.t_hi ? page_of(t + 1) : 0;
-        if (!(ok = mbar_wait_warp(&empty[s], ((st / C::STAGES) & 1) ^ 1, wc))) break;
+        if (!(ok = mbar_wait_warp(&empty[s], (st & stages) ? 0 : 1, wc))) break;
         const int nb = boxes(t);
         if (lane == 0) mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(nb * box) * 128 * C::NCHUNK);
         __syncwarp();
@@ -646,8 +651,8 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
       // Never leave a copy in flight into shared memory this CTA is about to release.
       for (int i = max(0, seg - C::QBUF); is_k && i < seg; ++i)
         mbar_wait_drain(&bars->q_full[i % C::QBUF], (i / C::QBUF) & 1, a.err);
-      for (int j = max(0, st - C::STAGES); j < st; ++j)
-        mbar_wait_drain(&full[j % C::STAGES], (j / C::STAGES) & 1, a.err);
+      for (int j = max(0, st - stages); j < st; ++j)
+        mbar_wait_drain(&full[j & (stages - 1)], (j & stages) ? 1 : 0, a.err);
     }
     __syncwarp();
     }
