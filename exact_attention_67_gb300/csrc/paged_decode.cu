@@ -244,6 +244,7 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
   fence_proxy_async_smem();
   // Up to here this CTA may run beside the stream's last kernel.  The walking warp
   // finds its place in the line.
+  if (warp == C::K_WARP) paged_touch(a);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (warp == C::K_WARP) cur = paged_start(a, UT, lane, &seq);
   tc_fence_before();
@@ -604,23 +605,27 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
     const uint32_t q_bytes = static_cast<uint32_t>(UT * G) * 128 * C::NCHUNK;
     int st = 0, seg = 0;
     bool ok = true;
+    // Boxes of a tile that hold a visible key, and this lane's page of it.
+    auto boxes = [&](const PagedPiece& pc, int t) { return min(per_tile, (pc.key_hi - t * BN + box - 1) / box); };
+    auto page_of = [&](const PagedPiece& pc, int t) {
+      return lane < boxes(pc, t) ? a.pv.table[pc.b * a.pv.table_stride + (t * BN >> shift) + lane] : 0;
+    };
     for (int i = 0; ok; ++i) {
       PagedPiece pc;
+      int first_page = 0;
       if (is_k) {
         const bool more = cur.next(a, UT, seq, &pc);
+        if (more && pc.t_hi > pc.t_lo) first_page = page_of(pc, pc.t_lo);
         if (!(ok = ring.put(i, more ? &pc : nullptr, lane, wc)) || !more) break;
       } else {
         const PagedPiece* p = ring.get(i, wc);
         if (!p) break;
         pc = *p;
         ring.release(i);
+        if (pc.t_hi > pc.t_lo) first_page = page_of(pc, pc.t_lo);
       }
       if (pc.t_hi == pc.t_lo) continue;
-      const int* row = a.pv.table + pc.b * a.pv.table_stride;
-      // Boxes of a tile that hold a visible key, and this lane's page of it.
-      auto boxes = [&](int t) { return min(per_tile, (pc.key_hi - t * BN + box - 1) / box); };
-      auto page_of = [&](int t) { return lane < boxes(t) ? row[(t * BN >> shift) + lane] : 0; };
-      int page = page_of(pc.t_lo);
+      int page = first_page;
       if (is_k) {
         const int qb = seg % C::QBUF;
         if (seg >= C::QBUF && !(ok = mbar_wait_warp(&bars->q_empty[qb], (seg / C::QBUF - 1) & 1, wc))) break;
@@ -634,9 +639,9 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
       ++seg;
       for (int t = pc.t_lo; t < pc.t_hi; ++t, ++st) {
         const int s = st & (stages - 1);
-        const int next_page = t + 1 < pc.t_hi ? page_of(t + 1) : 0;
+        const int next_page = t + 1 < pc.t_hi ? page_of(pc, t + 1) : 0;
         if (!(ok = mbar_wait_warp(&empty[s], (st & stages) ? 0 : 1, wc))) break;
-        const int nb = boxes(t);
+        const int nb = boxes(pc, t);
         if (lane == 0) mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(nb * box) * 128 * C::NCHUNK);
         __syncwarp();
         if (lane < nb)

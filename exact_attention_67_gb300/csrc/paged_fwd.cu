@@ -143,6 +143,7 @@ __global__ void __launch_bounds__(512, 1)
   }
   // Up to here this CTA may run beside the stream's last kernel.  The walking warp
   // finds its place in the line.
+  if (warp == C::K_WARP) paged_touch(a);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (warp == C::K_WARP) cur = paged_start(a, UT, lane, &seq);
   tc_fence_before();
@@ -401,10 +402,17 @@ __global__ void __launch_bounds__(512, 1)
     const uint32_t q_bytes = static_cast<uint32_t>(TT * G) * 128 * C::NCHUNK;
     int kt = 0, seg = 0;  // key tiles and Qs issued
     bool ok = true;
+    // Boxes of a tile that hold a visible key, and this lane's page of it.
+    auto boxes = [&](const PagedPiece& pc, int t) { return min(per_tile, (pc.key_hi - t * C::BN + box - 1) / box); };
+    auto page_of = [&](const PagedPiece& pc, int t) {
+      return lane < boxes(pc, t) ? a.pv.table[pc.b * a.pv.table_stride + (t * C::BN >> shift) + lane] : 0;
+    };
     for (int i = 0; ok; ++i) {
       PagedPiece pc;
+      int first_page = 0;
       if (is_k) {
         const bool more = cur.next(a, UT, seq, &pc);
+        if (more && pc.t_hi > pc.t_lo) first_page = page_of(pc, pc.t_lo);
         for (int t = 0; t < 2; ++t) pc.n[t] = more ? tiles_of(a, pc, t) : 0;
         if (!(ok = ring.put(i, more ? &pc : nullptr, lane, wc)) || !more) break;
       } else {
@@ -412,14 +420,11 @@ __global__ void __launch_bounds__(512, 1)
         if (!p) break;
         pc = *p;
         ring.release(i);
+        if (pc.t_hi > pc.t_lo) first_page = page_of(pc, pc.t_lo);
       }
       const int n0 = pc.n[0], n1 = pc.n[1], n = max(n0, n1);
       if (n == 0) continue;
-      const int* row = a.pv.table + pc.b * a.pv.table_stride;
-      // Boxes of a tile that hold a visible key, and this lane's page of it.
-      auto boxes = [&](int t) { return min(per_tile, (pc.key_hi - t * C::BN + box - 1) / box); };
-      auto page_of = [&](int t) { return lane < boxes(t) ? row[(t * C::BN >> shift) + lane] : 0; };
-      int page = page_of(pc.t_lo);
+      int page = first_page;
       if (is_k) {
         if (seg >= 1 && !(ok = mbar_wait_warp(&bars->q_empty, (seg - 1) & 1, wc))) break;
         if (lane == 0) {
@@ -434,9 +439,9 @@ __global__ void __launch_bounds__(512, 1)
       ++seg;
       for (int t = pc.t_lo; t < pc.t_lo + n; ++t, ++kt) {
         const int s = kt % C::STAGES;
-        const int next_page = t + 1 < pc.t_lo + n ? page_of(t + 1) : 0;
+        const int next_page = t + 1 < pc.t_lo + n ? page_of(pc, t + 1) : 0;
         if (!(ok = mbar_wait_warp(&empty[s], ((kt / C::STAGES) & 1) ^ 1, wc))) break;
-        const int nb = boxes(t);
+        const int nb = boxes(pc, t);
         if (lane == 0) mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(nb * box) * 128 * C::NCHUNK);
         __syncwarp();
         if (lane < nb)

@@ -54,7 +54,7 @@ __device__ __forceinline__ void paged_keys(const PagedArgs& a, const PagedSeq& s
 }
 
 // One piece of a unit: its key tiles [t_lo, t_hi) of the unit's [k_lo, k_hi).
-struct PagedPiece {
+struct alignas(16) PagedPiece {  // 64 bytes
   PagedSeq s;
   int b, h;
   int tok0, ntok;   // tokens of the unit
@@ -175,6 +175,23 @@ struct PagedPlan {
   int unused;
 };
 
+// x / y for x >= 0, y > 0, without the division's subroutine: it and the loads are
+// the start of every call.
+__device__ __forceinline__ int paged_div(int x, int y) {
+  int q = static_cast<int>(__fdividef(static_cast<float>(x), static_cast<float>(y)));
+  while (static_cast<long long>(q) * y > x) --q;
+  while ((q + 1ll) * y <= x) ++q;
+  return q;
+}
+
+// Reads the call's constants before griddepcontrol.wait: they need not wait for
+// anything, and the first read of each line of them takes a few hundred clocks.
+__device__ __forceinline__ void paged_touch(const PagedArgs& a) {
+  asm volatile("" ::"l"(a.nt.cu_seqlens), "l"(a.nt.seqlens), "r"(a.nt.B), "r"(a.nt.total), "l"(a.pv.table),
+               "r"(a.pv.page_size), "r"(a.pv.k_page_step), "r"(a.Hkv), "r"(a.max_q), "r"(a.window), "r"(a.ctas),
+               "l"(a.plan), "l"(a.err));
+}
+
 // Start of this CTA's chunk, found by one warp; the same in every lane.  Leaves
 // the merge its PagedPlan.  The line's weights fit 31 bits (checked on the host
 // against the largest that the sizes allow).
@@ -182,34 +199,33 @@ __device__ __forceinline__ PagedCursor paged_start(const PagedArgs& a, int UT, i
   const int B = a.nt.B, cta = static_cast<int>(blockIdx.x);
   auto read = [&](int b) { return b < B ? paged_seq(a, b) : PagedSeq{0, 0, 0, 0}; };
   const PagedSeq s0 = read(lane);
-  const int w0 = paged_weight(a, s0, UT) * a.Hkv;  // kept: most batches have at most 32 sequences
-  int W = __reduce_add_sync(0xffffffffu, w0);
-  for (int b0 = 32; b0 < B; b0 += 32) W += __reduce_add_sync(0xffffffffu, paged_weight(a, read(b0 + lane), UT) * a.Hkv);
-  int chunk = max((W + a.ctas - 1) / a.ctas, a.min_chunk), cost = a.unit_cost;
-  if (a.cols > 0) {
-    // The decode kernel: a unit is a (sequence, key head).  Do all that exist weigh
-    // the same, with `tiles` key tiles each?
-    int most = w0, least = w0 > 0 ? w0 : INT_MAX, count = w0 > 0;
-    for (int b0 = 32; b0 < B; b0 += 32) {
-      const int w = paged_weight(a, read(b0 + lane), UT) * a.Hkv;
-      most = max(most, w);
-      least = min(least, w > 0 ? w : INT_MAX);
-      count += w > 0;
-    }
-    most = __reduce_max_sync(0xffffffffu, most);
-    least = __reduce_min_sync(0xffffffffu, least);
-    const int units = __reduce_add_sync(0xffffffffu, count) * a.Hkv, tiles = most / a.Hkv - a.unit_cost;
-    if (most == least && tiles > 0 && units <= a.ctas) {
-      // As many pieces a unit as CTAs, of two tiles at least; none of four or fewer
-      // (joining pieces takes some 2 us, a tile 0.6).  Unless this leaves over a
-      // quarter of the SMs out of long work.
-      const int each = tiles <= 4 ? tiles : max((tiles + a.ctas / units - 1) / (a.ctas / units), 2);
-      const int k = (tiles + each - 1) / each;
-      if (4 * units * k >= 3 * a.ctas || each <= 4) {
-        chunk = each;
-        cost = k * chunk - tiles;  // less than a chunk: the first piece's tiles are fewer by it
-        W = units * k * chunk;
-      }
+  const int w0 = paged_weight(a, s0, UT);  // kept: most batches have at most 32 sequences
+  int sum = w0, most = w0, least = w0 > 0 ? w0 : INT_MAX, count = w0 > 0;
+  for (int b = 32 + lane; b < B; b += 32) {
+    const int w = paged_weight(a, paged_seq(a, b), UT);
+    sum += w;
+    most = max(most, w);
+    least = min(least, w > 0 ? w : INT_MAX);
+    count += w > 0;
+  }
+  sum = __reduce_add_sync(0xffffffffu, sum);
+  most = __reduce_max_sync(0xffffffffu, most);
+  least = __reduce_min_sync(0xffffffffu, least);
+  const int units = __reduce_add_sync(0xffffffffu, count) * a.Hkv, tiles_each = most - a.unit_cost;
+  int W = sum * a.Hkv, cost = a.unit_cost;
+  int chunk = max(paged_div(W + a.ctas - 1, a.ctas), a.min_chunk);
+  // The decode kernel, where a unit is a (sequence, key head), and all weigh the same.
+  if (a.cols > 0 && most == least && tiles_each > 0 && units <= a.ctas) {
+    // As many pieces a unit as CTAs, of two tiles at least; none of four or fewer
+    // (joining pieces takes some 2 us, a tile 0.6).  Unless this leaves over a
+    // quarter of the SMs out of long work.
+    const int most_pieces = paged_div(a.ctas, units);
+    const int each = tiles_each <= 4 ? tiles_each : max(paged_div(tiles_each + most_pieces - 1, most_pieces), 2);
+    const int k = paged_div(tiles_each + each - 1, each);
+    if (4 * units * k >= 3 * a.ctas || each <= 4) {
+      chunk = each;
+      cost = k * chunk - tiles_each;  // less than a chunk: the first piece's tiles are fewer by it
+      W = units * k * chunk;
     }
   }
   const long long lo64 = static_cast<long long>(cta) * chunk;
@@ -221,8 +237,10 @@ __device__ __forceinline__ PagedCursor paged_start(const PagedArgs& a, int UT, i
   for (int b0 = 0; b0 < B && lo64 < W; b0 += 32) {
     const int lo = static_cast<int>(lo64);
     const PagedSeq sl = b0 == 0 ? s0 : read(b0 + lane);
-    int w = b0 == 0 ? w0 : paged_weight(a, sl, UT) * a.Hkv;
-    if (w > 0 && pad != 0) w += pad * a.Hkv;  // only where a sequence has one unit a key head
+    int w = b0 == 0 ? w0 : paged_weight(a, sl, UT);
+    if (w > 0) w += pad;  // not 0 only where a sequence has one unit a key head
+    const int per_head = w;
+    w *= a.Hkv;
     int inc = w;  // inclusive prefix over the lanes
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -237,12 +255,12 @@ __device__ __forceinline__ PagedCursor paged_start(const PagedArgs& a, int UT, i
       s.n = __shfl_sync(0xffffffffu, sl.n, l);
       s.len = __shfl_sync(0xffffffffu, sl.len, l);
       s.off = __shfl_sync(0xffffffffu, sl.off, l);
-      const int per_head = __shfl_sync(0xffffffffu, w, l) / a.Hkv;
+      const int each_head = __shfl_sync(0xffffffffu, per_head, l);
       int r = lo - before - __shfl_sync(0xffffffffu, inc - w, l);
       c.left = min(chunk, W - lo);
       c.b = b0 + l;
-      c.h = r / per_head;
-      r -= c.h * per_head;
+      c.h = paged_div(r, each_head);
+      r -= c.h * each_head;
       int tiles;
       for (;;) {
         tiles = paged_tiles(a, s, c.t * UT, UT);
