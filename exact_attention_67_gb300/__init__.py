@@ -24,6 +24,7 @@ from ._lib import (EXPORTS, ExattnError, Strides, attn_bwd, attn_bwd_d_and_dq, a
 from .host import HostStep, fwd_bwd_from_host
 from .paged import (attn_cache_append, attn_cache_copy, attn_fwd_paged, attn_fwd_paged_workspace_size, attn_rotary,
                     forward_paged, rotary, rotary_backward, rotary_frequencies)
+from .cache import OutOfPages, PagedCache, Step
 
 __all__ = ["attn_fwd", "attn_bwd", "attn_bwd_workspace_size", "attn_bwd_preprocess", "attn_bwd_dkdv",
            "attn_bwd_dq", "attn_bwd_d_and_dq", "attn_fwd_ex", "attn_bwd_ex", "attn_fwd_o32", "attn_bwd_o32",
@@ -32,6 +33,7 @@ __all__ = ["attn_fwd", "attn_bwd", "attn_bwd_workspace_size", "attn_bwd_preproce
            "attn_fwd_bwd_host_workspace_size", "attention", "flash_attn_func", "device_error",
            "attn_rotary", "attn_cache_append", "attn_cache_copy", "attn_fwd_paged",
            "attn_fwd_paged_workspace_size", "forward_paged", "rotary", "rotary_backward", "rotary_frequencies",
+           "PagedCache", "OutOfPages", "Step",
            "watchdog_check", "watchdog_poll", "status_string", "version", "load", "library_path", "ExattnError",
            "EXPORTS"]
 

@@ -154,3 +154,238 @@ def test_wide_scores_and_scale():
         p = Problem(new, [2000, 700], 4, 2, d, 32, dtype, seed=3, sigma=4.0)
         p.k = [k * 1.0 for k in p.k]
         p.check(*p.run(scale=0.05), scale=0.05)
+
+
+def test_layouts_and_rows_left_alone():
+    """Q a slice of a wider projection, O with strides of its own; rows behind the
+    last sequence stay as they were; the same bits every time."""
+    import exact_attention_67_gb300 as ex
+    for new, Hq, Hk, d in (([1, 2, 0, 3], 6, 2, 128), ([70, 2, 0, 90], 6, 2, 64)):
+        p = Problem(new, [400, 77, 5, 1000], Hq, Hk, d, 16, torch.bfloat16, seed=9, pad=5)
+        total = sum(new) + 5
+        wide = torch.zeros(total, Hq + 2 * Hk, d, dtype=torch.bfloat16, device=DEV)
+        wide[:, :Hq] = p.q
+        o = torch.full((Hq, total, d), 3.0, dtype=torch.bfloat16, device=DEV).transpose(0, 1)
+        lse = torch.full((Hq, total), 3.0, device=DEV)
+        ws = torch.empty(ex.attn_fwd_paged_workspace_size(4, Hq, Hk, total, 90, 1000, d), dtype=torch.uint8, device=DEV)
+        runs = []
+        for _ in range(3):
+            ex.attn_fwd_paged(wide[:, :Hq], p.kc, p.vc, o, lse, p.table, p.seq, p.cu, 90, 1000, True, d ** -0.5, ws)
+            runs.append((o.clone(), lse.clone()))
+        p.check(o, lse)
+        assert torch.all(o[sum(new):] == 3.0) and torch.all(lse[:, sum(new):] == 3.0)
+        assert all(torch.equal(a, b) for r in runs[1:] for a, b in zip(r, runs[0]))
+
+
+def test_even_batches_need_no_offsets():
+    for new in (1, 3, 40):
+        p = Problem([new] * 4, [100, 900, new, 333], 8, 2, 64, 32, torch.float16, seed=new)
+        a, b = p.run(), p.run(cu=False)
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+        p.check(*b)
+        p.check(*p.run(cu=False, max_seqlen_q=None, max_seqlen_k=None))
+
+
+def test_capture_and_replay_with_other_lengths():
+    """A captured call reads the tables that are there at the replay."""
+    import exact_attention_67_gb300 as ex
+    for new, Hq in (([1, 1, 1], 8), ([40, 3, 60], 4)):
+        p = Problem(new, [1500, 700, 90], Hq, 2, 128, 16, torch.bfloat16, seed=21)
+        o, lse = torch.empty_like(p.q), torch.empty(Hq, p.q.shape[0], device=DEV)
+        ws = torch.empty(ex.attn_fwd_paged_workspace_size(3, Hq, 2, sum(new), max(new), 1500, 128), dtype=torch.uint8,
+                         device=DEV)
+        seq = p.seq.clone()
+
+        def call():
+            ex.attn_fwd_paged(p.q, p.kc, p.vc, o, lse, p.table, seq, p.cu, max(new), 1500, True, 128 ** -0.5, ws)
+
+        call()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call()
+            call()
+        for lens in ([1500, 700, 90], [1400, 64, 61], [1000, 3, 90]):
+            seq.copy_(torch.tensor(lens, dtype=torch.int32))
+            o.fill_(NAN)
+            graph.replay()
+            torch.cuda.synchronize()
+            p.lens, full = lens, (p.k, p.v)
+            p.k, p.v = [k[:n] for k, n in zip(p.k, lens)], [v[:n] for v, n in zip(p.v, lens)]
+            p.check(o, lse)
+            p.k, p.v = full
+
+
+def test_two_calls_at_once():
+    """Two streams, each with its own workspace and outputs, against the same calls
+    one after the other."""
+    import exact_attention_67_gb300 as ex
+    problems = [Problem([1] * 6, [4000, 300, 2500, 17, 900, 3333], 8, 2, 128, 16, torch.bfloat16, seed=1),
+                Problem([100, 7], [3000, 2000], 8, 2, 128, 32, torch.bfloat16, seed=2)]
+    want = [p.run() for p in problems]
+    streams = [torch.cuda.Stream() for _ in problems]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(10):
+        for p, s in zip(problems, streams):
+            with torch.cuda.stream(s):
+                got.append(ex.forward_paged(p.q, p.kc, p.vc, p.table, p.seq, p.cu, max(p.new), max(p.lens)))
+    torch.cuda.synchronize()
+    assert ex.device_error() == 0
+    for i, out in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(out, want[i % 2]))
+
+
+def test_wrong_tables_and_bounds():
+    """Page numbers outside the pool read as zeros, sequences beyond the given bounds
+    are cut off, offsets past the tensors leave rows alone: wrong or short results,
+    never an access out of bounds."""
+    import exact_attention_67_gb300 as ex
+    for new, Hq in (([2, 2], 4), ([50, 30], 4)):
+        p = Problem(new, [200, 300], Hq, 2, 64, 16, torch.float16, seed=31)
+        p.table[1, 3] = p.kc.shape[0] + 7       # keys 48..63 of sequence 1
+        p.table[1, 4] = -3
+        p.k[1][48:80] = 0.0
+        p.v[1][48:80] = 0.0
+        p.check(*p.run())
+        o, lse = p.run(max_seqlen_k=128)        # only keys 0..127 are seen
+        cut = Problem(new, [200, 300], Hq, 2, 64, 16, torch.float16, seed=31)
+        cut.k, cut.v = [k[:128] for k in p.k], [v[:128] for v in p.v]
+        cut.lens, cut.new = [128, 128], new
+        cut.check(o, lse, causal=False)         # all of them lie before the new tokens
+        p.cu = torch.tensor([0, 1 << 30, -5], dtype=torch.int32, device=DEV)
+        p.run()
+        p.seq = torch.tensor([1 << 30, -9], dtype=torch.int32, device=DEV)
+        p.run()
+
+
+def test_nan_stays_with_its_rows():
+    """A NaN in a visible key reaches the rows that see it and no others."""
+    for new, lens, Hq in (([1, 1], [500, 700], 8), ([80, 60], [500, 700], 4)):
+        p = Problem(new, lens, Hq, 2, 128, 16, torch.bfloat16, seed=41)
+        page = int(p.table[0, 5])
+        p.kc[page, 1, 3, 7] = NAN               # key 83 of sequence 0, key head 1
+        o, lse = p.run()
+        hit = torch.zeros(sum(new), Hq, dtype=torch.bool, device=DEV)
+        hit[: new[0], Hq // 2:] = True
+        assert torch.equal(torch.isnan(o).all(-1), hit) and torch.equal(torch.isnan(o).any(-1), hit)
+        assert torch.equal(torch.isnan(lse).t(), hit)
+
+
+def test_pools_past_32_bits():
+    """Pages whose elements lie past 2^31, and bytes past 2^32, from the pool's start:
+    append, copy and attention."""
+    import exact_attention_67_gb300 as ex
+    pages, ps, d = 140000, 128, 128
+    pool = torch.empty(2, pages, 1, ps, d, dtype=torch.bfloat16, device=DEV)
+    n = 300
+    k, v, q = (randn(n, 1, d, seed=s, dtype=torch.bfloat16) for s in (1, 2, 3))
+    table = torch.tensor([[pages - 1, 3, pages - 2]], dtype=torch.int32, device=DEV)
+    seq = torch.tensor([n], dtype=torch.int32, device=DEV)
+    ex.attn_cache_append(k, v, pool[0], pool[1], table, seq)
+    ex.attn_cache_copy(pool, [pages - 1, 3], [pages - 7, pages - 9])
+    p = Problem([n], [n], 1, 1, d, ps, torch.bfloat16)
+    p.q, p.k, p.v = q, [k.double()], [v.double()]
+    for first in ([pages - 1, 3, pages - 2], [pages - 7, pages - 9, pages - 2]):
+        p.kc, p.vc, p.table = pool[0], pool[1], torch.tensor([first], dtype=torch.int32, device=DEV)
+        p.check(*p.run())
+
+
+@pytest.mark.parametrize("Hq,Hk,d,ps,dtype,window", [(8, 2, 128, 16, torch.bfloat16, 0), (6, 2, 64, 8, torch.float16, 50)])
+def test_a_serving_run(Hq, Hk, d, ps, dtype, window):
+    """A PagedCache through a life: prompts in chunks, single tokens, forks that write
+    on, tokens taken back, sequences freed, the pool compacted -- attention at every
+    step and layer against the tokens' own K and V in 64 bits."""
+    import random
+
+    import exact_attention_67_gb300 as ex
+    from tests.test_rotary_gpu import turned
+    r, layers = random.Random(d), 2
+    cache = ex.PagedCache(150, ps, layers, Hk, d, dtype)
+    cache.pool.fill_(NAN)
+    freq, factor = ex.rotary_frequencies(d // 2, yarn=2.0)
+    kept = {}                                    # sequence -> per layer, its rounded K and V
+    seed = [0]
+
+    def turn(x, pos):                            # [n, H, d], turned and rounded as the cache holds it
+        y, _ = turned(x.double().cpu().numpy().transpose(1, 0, 2), pos, freq.cpu().numpy(), factor, False)
+        return torch.from_numpy(y.transpose(1, 0, 2))
+
+    def step(seqs, new):
+        at = [cache.length(s) for s in seqs]
+        new = [new] * len(seqs) if isinstance(new, int) else new
+        st = cache.extend(seqs, new if len(set(new)) > 1 else new[0])
+        total = sum(new)
+        for layer in range(layers):
+            seed[0] += 1
+            k, v, q = (randn(total, h, d, seed=3 * seed[0] + i, dtype=dtype) for i, h in enumerate((Hk, Hk, Hq)))
+            qo = torch.empty_like(q)
+            cache.append(layer, st, k, v, q, qo, freq, False, factor)
+            o, lse = cache.attend(layer, st, qo, window=window)
+            torch.cuda.synchronize()
+            t = 0
+            for s, n, a in zip(seqs, new, at):
+                rows = slice(t, t + n)
+                t += n
+                if n == 0:
+                    continue
+                pos = torch.arange(a, a + n).numpy()
+                # The cache's own K (checked against the definition to one step of its type).
+                pages = cache.pages(s)
+                mine = torch.stack([cache.k_cache(layer)[pages[i // ps], :, i % ps] for i in range(a, a + n)])
+                want = turn(k[rows], pos).to(DEV)
+                assert bool(((mine.double() - want).abs() <= 2 * HALF[dtype] * want.abs() + 2.0 ** -16).all())
+                got_k, got_v = kept[s][layer]
+                kept[s][layer] = (torch.cat([got_k, mine]), torch.cat([got_v, v[rows]]))
+                m = a + n
+                p = Problem.__new__(Problem)
+                p.new, p.lens, p.Hq, p.Hk, p.d, p.dtype, p.q = [n], [m], Hq, Hk, d, dtype, qo[rows]
+                p.k, p.v = [kept[s][layer][0].double()], [kept[s][layer][1].double()]
+                p.check(o[rows], lse[:, rows], True, window)
+        assert ex.device_error() == 0
+
+    def add():
+        s = cache.add()
+        kept[s] = [(torch.empty(0, Hk, d, dtype=dtype, device=DEV),) * 2 for _ in range(layers)]
+        return s
+
+    a, b, c = add(), add(), add()
+    step([a, b], [130, 7])
+    step([a, b, c], [1, 40, 1])
+    step([a, b, c], 1)
+    forks = cache.fork(a, 2)
+    for f in forks:
+        kept[f] = list(kept[a])
+    step([forks[0], b, forks[1], a], 1)          # three writers of one shared page
+    step([forks[0], a], 3)
+    cache.truncate(a, cache.length(a) - 2)
+    kept[a] = [(x[:-2], y[:-2]) for x, y in kept[a]]
+    step([a, c], [2, 0])
+    cache.free([b, forks[1]])
+    moved = cache.compact()
+    assert moved > 0
+    for _ in range(2):
+        step(r.sample([a, c, forks[0]], 3), 1)
+    d2 = add()
+    step([d2, a], [65, 1])
+
+
+def test_attention_refusals():
+    import exact_attention_67_gb300 as ex
+    p = Problem([1, 1], [20, 30], 4, 2, 64, 16, torch.bfloat16)
+    call = ex.forward_paged
+    with pytest.raises(TypeError):
+        call(p.q, p.kc, p.vc, p.table.long(), p.seq, p.cu)
+    with pytest.raises(TypeError):
+        call(p.q.float(), p.kc, p.vc, p.table, p.seq, p.cu)
+    for bad in (lambda: call(p.q, p.kc.half(), p.vc.half(), p.table, p.seq, p.cu), lambda: call(p.q, p.kc, p.vc[:-1], p.table, p.seq),
+                lambda: call(p.q, p.kc, p.vc, p.table, p.seq[:1]), lambda: call(p.q, p.kc, p.vc, p.table, p.seq, p.cu[:2]),
+                lambda: call(p.q[:1], p.kc, p.vc, p.table, p.seq), lambda: call(p.q, p.kc, p.vc, p.table.cpu(), p.seq, p.cu),
+                lambda: call(p.q, p.kc.transpose(2, 3), p.vc.transpose(2, 3), p.table, p.seq, p.cu)):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: call(p.q, p.kc, p.vc, p.table, p.seq, p.cu, window=-1), lambda: call(p.q, p.kc, p.vc, p.table, p.seq, scale=0.0),
+                lambda: call(p.q[:, :3], p.kc, p.vc, p.table, p.seq)):
+        with pytest.raises(ex.ExattnError):
+            bad()
+    o, lse = call(p.q[:0], p.kc, p.vc, p.table, p.seq, torch.zeros(3, dtype=torch.int32, device=DEV))
+    assert o.shape[0] == 0 and lse.shape[1] == 0
