@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(512, 1)
         const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;
         const float2 sc2 = make_float2(a.scale_log2, a.scale_log2), nm2 = make_float2(neg_m, neg_m);
         uint32_t pk[4][16];
-        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        float2 sum[4] = {};
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
 #pragma unroll
@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(512, 1)
             const float2 y = ffma2(make_float2(__uint_as_float(sr[c][2 * e]), __uint_as_float(sr[c][2 * e + 1])), sc2, nm2);
             const float2 p = make_float2(ex2(y.x), ex2(y.y));
             pk[c][e] = PE::pack(p.x, p.y);
-            sum[e & 1] = fadd2(sum[e & 1], p);
+            sum[e & 3] = fadd2(sum[e & 3], p);
           }
           if constexpr (!C::EARLY_S) tmem_st16(tP + c * 16, pk[c]);
         }
@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(512, 1)
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive_warp(&bars->p_full[t]);
-        const float2 s2 = fadd2(sum[0], sum[1]);
+        const float2 s2 = fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3]));
         le = le * alpha + (s2.x + s2.y);
         if constexpr (!kConvertV) {
           float2 rb[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
