@@ -843,4 +843,4 @@ extern "C" const char* exattn_last_cuda_error(void) {
   return t_fail_text;
 }
 
-extern "C" int exattn_version(void) { return 202; }  // 0.2.2: fp32-O calls, exattn_last_cuda_error
+extern "C" int exattn_version(void) { return 203; }  // 0.2.3: rotary, paged cache and attention over it

@@ -231,7 +231,7 @@ int rotary(PyObject* const* p) {
   on.also(f);
   const int il = truth(p[6]), inverse = truth(p[7]);
   const float factor = as_float(p[8]);
-  if (q.numel() == 0) return EXATTN_OK;
+  if (q.numel() == 0 && (Hk == 0 || B * N == 0)) return EXATTN_OK;
   void* stream = on.enter(p[9]);
   const WithoutGil threads;
   return attn_rotary(dtype_of(q), q.data_ptr(), strides(q), qo.data_ptr(), strides(qo), as_int(q.size(h), "Hq"), k, sk, ko,

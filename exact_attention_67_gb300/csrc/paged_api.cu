@@ -1,6 +1,6 @@
 // paged_api.cu -- the C ABI of the operators around a paged key/value cache
-// (declared in include/exattn.h): argument validation and launches.  No device
-// memory is allocated and nothing synchronises.
+// (declared in include/exattn.h): argument validation, plans, tensor maps and
+// launches.  No device memory is allocated and nothing synchronises.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -174,6 +174,8 @@ extern "C" int attn_cache_copy(void* pool, long long slab_stride, long long page
   if (!pool || (n > 0 && (!src || !dst))) return EXATTN_ERR_NULL;
   if (slabs < 1 || slabs > 65535 || num_pages < 1 || page_bytes < 16 || page_bytes > (1ll << 30))
     return EXATTN_ERR_SHAPE;
+  if (slabs == 1) slab_stride = 0;  // never used
+  if (num_pages == 1) page_stride = 0;
   if (!aligned(pool, 16) || ((slab_stride | page_stride | page_bytes) & 15)) return EXATTN_ERR_ALIGN;
   // Pages of a slab, and slabs, must not overlap (either may be the outer one).
   if ((num_pages > 1 && page_stride < page_bytes) || (slabs > 1 && slab_stride < page_bytes)) return EXATTN_ERR_SHAPE;
@@ -231,6 +233,9 @@ AttendPlan paged_plan(int B, int Hq, int Hkv, int total, int max_q, int max_k, i
   p.cols = need <= 4 ? 4 : need <= 8 ? 8 : need <= 16 ? 16 : need <= kPagedDecodeCols ? 32 : 0;
   p.rows = p.cols ? std::max(p.cols, 16) : kPagedRows;
   p.tile_tokens = (p.cols ? p.cols : 128) / G;
+  // A unit's fixed cost in key tiles, and the least worth a CTA.  Chunks of 3, 6 and
+  // 9 weights: one sequence of 777 keys, 8 key heads 10.9, 13.3, 12.1 us; of 2,000
+  // 11.0, 13.4, 15.6; unit costs of 2 to 8 change long chunks by 3 % at most.
   p.unit_cost = 2;
   p.min_chunk = 3;
   const int ut = p.cols ? p.tile_tokens : 2 * p.tile_tokens;

@@ -37,7 +37,7 @@ __global__ void __launch_bounds__(64 * WPR) paged_merge_kernel(const __grid_cons
   // Pieces: CTA g - 1 + i has the weights [i chunk - lead, (i + 1) chunk - lead)
   // of the unit, lead those of its chunk that lie before it.
   const int w = p.tiles + p.cost, lead = p.chunk - p.pos;
-  const int pieces = (w + lead + p.chunk - 1) / p.chunk;
+  const int pieces = min((w + lead + p.chunk - 1) / p.chunk, a.ctas - g + 1);
   auto tiles_before = [&](int x) { return max(0, min(w, x) - p.cost); };  // in the unit's first x weights
   auto from = [&](int i) { return tiles_before(i * p.chunk - lead); };
   // All its key tiles on one CTA: that CTA has written the rows itself.
@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(64 * WPR) paged_merge_kernel(const __grid_cons
 #pragma unroll
   for (int i = 0; i < WPR; ++i) m = fmaxf(m, red[warp - part + i]);
   float acc[V] = {}, sum = 0.f;
-  if (live && m != -INFINITY) {
+  if (live) {
     for (int i0 = part; i0 < pieces; i0 += BATCH * WPR) {
       float e[BATCH], x[BATCH][V];
 #pragma unroll
@@ -67,8 +67,7 @@ __global__ void __launch_bounds__(64 * WPR) paged_merge_kernel(const __grid_cons
         if (i >= pieces || from(i + 1) <= from(i)) continue;
         const long long r = at(i);
         const float l = a.part_lse[r];
-        if (l == -INFINITY) continue;  // a piece that this row saw no key of: its O is not written
-        e[u] = expf(l - m);
+        e[u] = l == -INFINITY ? 0.f : expf(l - m);
         const float* po = a.part_o + r * D + lane * V;
         if constexpr (V == 4) {
           const float4 y = *reinterpret_cast<const float4*>(po);
@@ -112,11 +111,13 @@ __global__ void __launch_bounds__(64 * WPR) paged_merge_kernel(const __grid_cons
 }
 
 // The forward kernel's rows: a block takes 32 of a query tile, a lane each (their
-// partial results lie side by side), a warp a quarter of the columns.
+// partial results lie side by side), and 32 columns, 8 a warp.  One pass with a
+// running maximum over the pieces, four at a time, their loads all at once: few
+// units of long sequences have as many pieces as CTAs (16 units of 10 pieces, 256
+// rows: 19 us with one piece at a time and 128 columns a block).
 template <typename T, int D>
 __global__ void __launch_bounds__(128) paged_merge_rows_kernel(const __grid_constant__ PagedArgs a) {
-  constexpr int C4 = D / 16;  // 4-column vectors a warp
-  // The next kernel of the stream may set itself up; this one waits for the pieces.
+  constexpr int C4 = 2, BATCH = 4;  // 4-column vectors a thread, pieces at once
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int g = static_cast<int>(blockIdx.x) + 1;
@@ -124,52 +125,67 @@ __global__ void __launch_bounds__(128) paged_merge_rows_kernel(const __grid_cons
   if (p.pos == 0 || p.pos > p.chunk) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t = static_cast<int>(blockIdx.y) >> 2, row = (static_cast<int>(blockIdx.y) & 3) * 32 + lane;
+  const int c0 = static_cast<int>(blockIdx.z) * 8 + warp * C4;  // first 4-column vector
   const int row_tok = row / a.G, tok = t * a.tile_tokens + row_tok;
   const int w = p.tiles + p.cost, lead = p.chunk - p.pos;
-  const int pieces = (w + lead + p.chunk - 1) / p.chunk;
+  const int pieces = min((w + lead + p.chunk - 1) / p.chunk, a.ctas - g + 1);
   auto tiles_before = [&](int x) { return max(0, min(w, x) - p.cost); };
   auto from = [&](int i) { return tiles_before(i * p.chunk - lead); };
   int used = 0;
   for (int i = 0; i < pieces && used < 2; ++i) used += from(i + 1) > from(i);
   if (used < 2) return;
-  auto part = [&](int i) { return (static_cast<long long>(g - 1 + i) * 2 + (from(i) == 0)) * 2 + t; };
-  const bool live = row_tok < a.tile_tokens && tok < p.ntok;
-  float m = -INFINITY;
-  for (int i = 0; i < pieces; ++i)
-    if (live && from(i + 1) > from(i)) m = fmaxf(m, a.part_lse[part(i) * 128 + row]);
+  if (row_tok >= a.tile_tokens || tok >= p.ntok) return;
   float4 acc[C4];
 #pragma unroll
   for (int c = 0; c < C4; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-  float sum = 0.f;
-  for (int i = 0; i < pieces; ++i) {
-    if (!live || from(i + 1) <= from(i)) continue;
-    const float l = a.part_lse[part(i) * 128 + row];
-    if (l == -INFINITY) continue;  // a piece that this row saw no key of: its O may not be written
-    const float e = expf(l - m);
-    sum += e;
-    const float4* po = reinterpret_cast<const float4*>(a.part_o + part(i) * 128 * D) + warp * C4 * 128 + row;
+  float m = -INFINITY, sum = 0.f;
+  for (int i0 = 0; i0 < pieces; i0 += BATCH) {
+    float l[BATCH];
+    float4 x[BATCH][C4];
 #pragma unroll
-    for (int c = 0; c < C4; ++c) {
-      const float4 x = po[c * 128];
-      acc[c] = make_float4(fmaf(e, x.x, acc[c].x), fmaf(e, x.y, acc[c].y), fmaf(e, x.z, acc[c].z), fmaf(e, x.w, acc[c].w));
+    for (int u = 0; u < BATCH; ++u) {
+      const int i = i0 + u;
+      l[u] = -INFINITY;
+      if (i >= pieces || from(i + 1) <= from(i)) continue;
+      const long long part = (static_cast<long long>(g - 1 + i) * 2 + (from(i) == 0)) * 2 + t;
+      l[u] = a.part_lse[part * 128 + row];
+      const float4* po = reinterpret_cast<const float4*>(a.part_o + part * 128 * D) + c0 * 128 + row;
+#pragma unroll
+      for (int c = 0; c < C4; ++c) x[u][c] = po[c * 128];
     }
+    float top = m;
+#pragma unroll
+    for (int u = 0; u < BATCH; ++u) top = fmaxf(top, l[u]);
+    const float keep = m == -INFINITY ? 0.f : expf(m - top);
+    sum *= keep;
+#pragma unroll
+    for (int c = 0; c < C4; ++c)
+      acc[c] = make_float4(acc[c].x * keep, acc[c].y * keep, acc[c].z * keep, acc[c].w * keep);
+#pragma unroll
+    for (int u = 0; u < BATCH; ++u) {
+      if (l[u] == -INFINITY) continue;  // a piece that this row saw no key of: its O may not be written
+      const float e = expf(l[u] - top);
+      sum += e;
+#pragma unroll
+      for (int c = 0; c < C4; ++c)
+        acc[c] = make_float4(fmaf(e, x[u][c].x, acc[c].x), fmaf(e, x[u][c].y, acc[c].y), fmaf(e, x[u][c].z, acc[c].z),
+                             fmaf(e, x[u][c].w, acc[c].w));
+    }
+    m = top;
   }
-  if (!live) return;
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   const int head = p.h * a.G + row % a.G, prow = p.row + tok;
-  uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(a.o) + prow * a.so.n + head * a.so.h + warp * C4 * 4);
-#pragma unroll
-  for (int c = 0; c < C4; c += 2)
-    out[c / 2] = make_uint4(Elem<T>::pack(acc[c].x * inv, acc[c].y * inv), Elem<T>::pack(acc[c].z * inv, acc[c].w * inv),
-                            Elem<T>::pack(acc[c + 1].x * inv, acc[c + 1].y * inv),
-                            Elem<T>::pack(acc[c + 1].z * inv, acc[c + 1].w * inv));
-  if (warp == 0) a.lse[static_cast<long long>(head) * a.nt.total + prow] = sum == 0.f ? -INFINITY : m + logf(sum);
+  T* out = static_cast<T*>(a.o) + prow * a.so.n + head * a.so.h + c0 * 4;
+  *reinterpret_cast<uint4*>(out) =
+      make_uint4(Elem<T>::pack(acc[0].x * inv, acc[0].y * inv), Elem<T>::pack(acc[0].z * inv, acc[0].w * inv),
+                 Elem<T>::pack(acc[1].x * inv, acc[1].y * inv), Elem<T>::pack(acc[1].z * inv, acc[1].w * inv));
+  if (c0 == 0) a.lse[static_cast<long long>(head) * a.nt.total + prow] = sum == 0.f ? -INFINITY : m + logf(sum);
 }
 
 template <typename T, int D>
 cudaError_t launch_t(const PagedArgs& a, cudaStream_t stream) {
   const bool few = a.cols > 0, deep = few && a.cols <= 8;
-  const dim3 grid(a.ctas - 1, few ? a.cols / 2 : 8), block(deep ? 512 : 128);
+  const dim3 grid(a.ctas - 1, few ? a.cols / 2 : 8, few ? 1 : D / 32), block(deep ? 512 : 128);
   const char* what = "paged merge kernel launch";
   return deep  ? launch_dependent(what, paged_merge_kernel<T, D, 8>, grid, block, 0, stream, a)
          : few ? launch_dependent(what, paged_merge_kernel<T, D, 2>, grid, block, 0, stream, a)

@@ -154,3 +154,51 @@ def test_copy_of_layouts_and_refusals():
     with pytest.raises(ex.ExattnError):
         ex.attn_cache_copy(wide[:1].expand(2, -1, -1, -1, -1), [1], [2])  # slabs on top of each other
     ex.attn_cache_copy(pool, [], [])
+
+
+def test_a_captured_step():
+    """Append and attention of one token a sequence, captured once and replayed as
+    the sequences grow: the lengths and tables are read at the replay."""
+    import exact_attention_67_gb300 as ex
+    B, Hq, Hk, d, ps, width = 3, 8, 2, 64, 16, 12
+    kc, vc = (torch.full((B * width, Hk, ps, d), float("nan"), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    table = torch.randperm(B * width, generator=torch.Generator().manual_seed(1)).to(torch.int32).view(B, width).to(DEV)
+    lens = torch.tensor([0, 50, 14], dtype=torch.int32, device=DEV)
+    first = lens.tolist()
+    past = [randn(n, 2 * Hk, d, seed=30 + n, dtype=torch.bfloat16) for n in first]
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(first)]), dtype=torch.int32, device=DEV)
+    both = torch.cat(past)
+    ex.attn_cache_append(both[:, :Hk], both[:, Hk:], kc, vc, table, lens, cu)
+    q, k, v = (torch.zeros(B, h, d, dtype=torch.bfloat16, device=DEV) for h in (Hq, Hk, Hk))
+    qo, o, lse = torch.empty_like(q), torch.empty_like(q), torch.empty(Hq, B, device=DEV)
+    freq, _ = ex.rotary_frequencies(d)
+    ws = torch.empty(ex.attn_fwd_paged_workspace_size(B, Hq, Hk, B, 1, width * ps, d), dtype=torch.uint8, device=DEV)
+
+    def step():
+        lens.add_(1)
+        ex.attn_cache_append(k, v, kc, vc, table, lens, None, q, qo, freq)
+        ex.attn_fwd_paged(qo, kc, vc, o, lse, table, lens, None, 1, width * ps, True, d ** -0.5, ws)
+
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    held = [(p[:, :Hk].double(), p[:, Hk:].double()) for p in past]
+    for i in range(40):
+        for x, s in ((q, 100), (k, 200), (v, 300)):
+            x.copy_(randn(*x.shape, seed=s + i, dtype=torch.bfloat16))
+        graph.replay()
+        torch.cuda.synchronize()
+        for b in range(B):
+            p = first[b] + i
+            mine = kc[table[b, p // ps], :, p % ps]
+            want, size = turned(f64(k[b]), np.array([p]), freq.cpu().numpy(), 1.0, False)
+            check(mine, want, size, torch.bfloat16)
+            K, V = held[b]
+            K, V = held[b] = torch.cat([K, mine[None].double()]), torch.cat([V, v[b][None].double()])
+            x = torch.einsum("hgd,jhd->hgj", qo[b].double().view(Hk, Hq // Hk, d), K) * d ** -0.5
+            w = torch.softmax(x, -1)
+            out = torch.einsum("hgj,jhd->hgd", w, V).reshape(Hq, d)
+            # The bound of test_paged_gpu.py.
+            mass = torch.einsum("hgj,jhd->hgd", w, V.abs()).reshape(Hq, d)
+            assert bool(((o[b].double() - out).abs() <= 2.0 ** -8 * out.abs() + (2.0 ** -10 + 2.0 ** -12) * mass + 2.0 ** -18).all())
+    assert ex.device_error() == 0

@@ -147,6 +147,33 @@ def test_capture_and_replay():
     check(ko, *turned(f64(k), 12345 + np.arange(300), freq.cpu().numpy(), 1.0, False), torch.bfloat16)
 
 
+def test_forward_and_backward_captured():
+    import exact_attention_67_gb300 as ex
+    q = inputs(2, 40, 3, 64, torch.bfloat16, "bhnd", 13).requires_grad_()
+    g = inputs(2, 40, 3, 64, torch.bfloat16, "bhnd", 14)
+    pos = torch.arange(40, dtype=torch.int32, device=DEV)
+    freq, _ = ex.rotary_frequencies(64)
+
+    def step():
+        y = ex.rotary(q, None, pos, freq)
+        return y, torch.autograd.grad(y, q, g)[0]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y, dq = step()
+    pos.add_(777)
+    graph.replay()
+    torch.cuda.synchronize()
+    p, fr = 777 + np.arange(40), freq.cpu().numpy()
+    check(y, *turned(f64(q), p, fr, 1.0, False), torch.bfloat16)
+    check(dq, *turned(f64(g), p, fr, 1.0, False, -1), torch.bfloat16)
+
+
 def test_then_attention():
     """Rotary then the framework's causal attention, forward and backward, as a
     training step runs them, against both in 64 bits."""
@@ -186,6 +213,8 @@ def test_refusals():
         ex.rotary(q, q[:, :, :4], pos, freq)
     with pytest.raises(ValueError):
         ex.rotary(q, None, pos.cpu(), freq)
+    with pytest.raises(ex.ExattnError):
+        ex.rotary(q[:, :0], q, pos, freq)      # no query head, but keys
     with pytest.raises(ex.ExattnError):
         ex.rotary(q, None, pos, freq, factor=0.0)
     with pytest.raises(ex.ExattnError):
