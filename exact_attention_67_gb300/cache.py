@@ -21,7 +21,7 @@ from dataclasses import dataclass
 
 import torch
 
-from .paged import attn_cache_append, attn_cache_copy, forward_paged
+from .paged import attn_cache_append, attn_cache_copy, forward_paged, on_stream
 
 
 class OutOfPages(RuntimeError):
@@ -170,7 +170,7 @@ class PagedCache:
                     pages[-1] = own[s]
                 pages.extend(next(fresh) for _ in range(g))
                 tables.append(pages)
-            step = self._step(seqs, new, tables)
+            step = self._step(seqs, new, tables, stream)
             if src:
                 self._copy(src, dst, stream)
         except BaseException:
@@ -186,7 +186,7 @@ class PagedCache:
             self._length[s] += n
         return step
 
-    def _step(self, seqs, new, tables) -> Step:
+    def _step(self, seqs, new, tables, stream) -> Step:
         B = len(seqs)
         lens = [self._length[s] + n for s, n in zip(seqs, new)]
         width = max(max(len(pages) for pages in tables), 1)
@@ -199,7 +199,8 @@ class PagedCache:
         host = torch.tensor(rows + lens + offsets, dtype=torch.int32)
         if self.pool.is_cuda:
             host = host.pin_memory()
-        dev = host.to(self.pool.device, non_blocking=True)
+        with on_stream(stream, self.pool.device):
+            dev = host.to(self.pool.device, non_blocking=True)
         return Step(tuple(seqs), tuple(new), dev[: B * width].view(B, width), dev[B * width: B * width + B],
                     None if even else dev[B * width + B:], max(max(new), 1), max(max(lens), 1))
 

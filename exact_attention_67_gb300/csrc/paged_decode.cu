@@ -22,9 +22,10 @@
 //     two boxes of 64 columns, one warp took 2,400 a tile, more than the tile's
 //     own time).  Pages past the last visible key are not read, whatever the
 //     table says there;
-//   * the stored rows behind a sequence's end may hold anything: scores there are
-//     replaced (not added to) by -inf, and V rows are zeroed in shared memory
-//     by the converting warps, so that 0 * NaN never meets an accumulator;
+//   * the stored rows behind a sequence's end, or before its window, may hold
+//     anything: scores there are replaced (not added to) by -inf, and V rows are
+//     zeroed in shared memory by the converting warps, so that 0 * NaN never meets
+//     an accumulator;
 //   * the logsumexp comes from a sum of the unrounded weights, and so does
 //     bf16's O (P's f16 rounding, 2^-11 of a weight, is far below the output's);
 //     f16's O is normalised by the sum of the rounded weights.
@@ -473,17 +474,17 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
   } else if (warp >= C::READY_WARP) {
     if constexpr (C::SPLIT_REGS) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     // ------------------------------------------------------------ V made ready
-    // bf16 tiles to f16 in place; rows at or past the last visible key to zero.
+    // bf16 tiles to f16 in place; rows that no query sees to zero.
     const int ct = threadIdx.x - 32 * C::READY_WARP;
     int st = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
       const PagedPiece* pc = ring.get(k, wc);
       if (!pc) break;
-      const int t_lo = pc->t_lo, t_hi = pc->t_hi, key_hi = pc->key_hi;
+      const int t_lo = pc->t_lo, t_hi = pc->t_hi, key_lo = pc->key_lo, key_hi = pc->key_hi;
       ring.release(k);
       for (int t = t_lo; t < t_hi; ++t, ++st) {
-        const int s = st % C::V_STAGES, rows = key_hi - t * BN;
+        const int s = st % C::V_STAGES, lo = key_lo - t * BN, hi = key_hi - t * BN;  // rows that a query sees
         if (!(ok = mbar_wait_warp(&bars->v_full[s], (st / C::V_STAGES) & 1, wc))) break;
         uint4* tile = reinterpret_cast<uint4*>(smem + C::OFF_V + s * C::KV_TILE);
         if constexpr (kConvertV) {
@@ -498,13 +499,15 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
                                                      pd_bf16x2_to_f16x2(x[u].z), pd_bf16x2_to_f16x2(x[u].w));
           }
         }
-        if (rows < BN) {
+        if (lo > 0 || hi < BN) {
           // Each thread zeroes vectors that it has itself written above.
 #pragma unroll 1
-          for (int i = ct; i < C::KV_TILE / 16; i += 128)  // 64 vectors an atom of 8 rows, 8 a row
-            if (i / (64 * C::NCHUNK) * 8 + (i >> 3 & 7) >= rows) tile[i] = make_uint4(0, 0, 0, 0);
+          for (int i = ct; i < C::KV_TILE / 16; i += 128) {  // 64 vectors an atom of 8 rows, 8 a row
+            const int row = i / (64 * C::NCHUNK) * 8 + (i >> 3 & 7);
+            if (row < lo || row >= hi) tile[i] = make_uint4(0, 0, 0, 0);
+          }
         }
-        if (kConvertV || rows < BN) fence_proxy_async_smem();
+        if (kConvertV || lo > 0 || hi < BN) fence_proxy_async_smem();
         mbar_arrive_warp(&bars->v_ready[s]);
       }
     }

@@ -13,9 +13,9 @@
 //     piece after piece;
 //   * a key tile is gathered page by page: one box a page, issued by one lane
 //     each, page numbers read one tile ahead;
-//   * stored rows behind the last visible key may hold anything: their scores are
-//     replaced by -inf, their V rows zeroed in shared memory by the converting
-//     warps (which run for f16 inputs too, to that end);
+//   * stored rows before the first and behind the last visible key may hold
+//     anything: their scores are replaced by -inf, their V rows zeroed in shared
+//     memory by the converting warps (which run for f16 inputs too, to that end);
 //   * the logsumexp is formed from the unrounded weights.  So is bf16's O: the
 //     f16 rounding of P (2^-12 of a weight at most) is far below the output's.
 //     f16's O is normalised by the sum of the rounded weights.
@@ -359,10 +359,10 @@ __global__ void __launch_bounds__(512, 1)
     for (int i = 0; ok; ++i) {
       const PagedPiece* pc = ring.get(i, wc);
       if (!pc) break;
-      const int n = max(pc->n[0], pc->n[1]), keys = pc->key_hi - pc->t_lo * C::BN;
+      const int n = max(pc->n[0], pc->n[1]), keys_lo = pc->key_lo - pc->t_lo * C::BN, keys = pc->key_hi - pc->t_lo * C::BN;
       ring.release(i);
       for (int j = 0; j < n; ++j, ++vt) {
-        const int s = vt % C::STAGES, rows = keys - j * C::BN;
+        const int s = vt % C::STAGES, lo = keys_lo - j * C::BN, hi = keys - j * C::BN;  // rows that a query sees
         if (!(ok = mbar_wait_warp(&bars->v_full[s], (vt / C::STAGES) & 1, wc))) break;
         uint4* tile = reinterpret_cast<uint4*>(smem + C::OFF_V + s * C::TILE_BYTES);
         if constexpr (kConvertV) {
@@ -377,13 +377,15 @@ __global__ void __launch_bounds__(512, 1)
                                                      pf_bf16x2_to_f16x2(x[u].z), pf_bf16x2_to_f16x2(x[u].w));
           }
         }
-        if (rows < C::BN) {
+        if (lo > 0 || hi < C::BN) {
           // Each thread zeroes vectors that it has itself written above.
 #pragma unroll 1
-          for (int i = ct; i < C::TILE_BYTES / 16; i += 128)  // 64 vectors an atom of 8 rows, 8 a row
-            if (i / (64 * C::NCHUNK) * 8 + (i >> 3 & 7) >= rows) tile[i] = make_uint4(0, 0, 0, 0);
+          for (int v = ct; v < C::TILE_BYTES / 16; v += 128) {  // 64 vectors an atom of 8 rows, 8 a row
+            const int row = v / (64 * C::NCHUNK) * 8 + (v >> 3 & 7);
+            if (row < lo || row >= hi) tile[v] = make_uint4(0, 0, 0, 0);
+          }
         }
-        if (kConvertV || rows < C::BN) fence_proxy_async_smem();
+        if (kConvertV || lo > 0 || hi < C::BN) fence_proxy_async_smem();
         mbar_arrive_warp(&bars->v_ready[s]);
       }
     }

@@ -58,7 +58,7 @@ struct alignas(16) PagedPiece {  // 64 bytes
   PagedSeq s;
   int b, h;
   int tok0, ntok;   // tokens of the unit
-  int key_hi;       // keys end
+  int key_lo, key_hi;  // keys that some token sees
   int t_lo, t_hi, k_lo, k_hi;
   int n[2];         // forward kernel: key tiles from t_lo on that each query tile takes part in
   __device__ bool whole() const { return t_lo == k_lo && t_hi == k_hi; }
@@ -133,6 +133,7 @@ struct PagedCursor {
       p->h = h;
       p->tok0 = t0;
       p->ntok = t1 - t0;
+      p->key_lo = lo;
       p->key_hi = hi;
       p->k_lo = k0;
       p->k_hi = k1;

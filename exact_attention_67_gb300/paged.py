@@ -12,6 +12,7 @@ total / B of them.
 """
 from __future__ import annotations
 
+import contextlib
 import importlib.machinery
 import importlib.util
 import math
@@ -39,6 +40,18 @@ def _native():
         loader.exec_module(module)
         _binding = module
     return _binding
+
+
+def on_stream(stream, device):
+    """What a helper allocates and computes for a call on ``stream`` belongs to it:
+    made on the current stream, it would not be ordered with the call, and its
+    memory could be given away while the call runs."""
+    if stream is None or device.type != "cuda":
+        return contextlib.nullcontext()
+    if isinstance(stream, int):
+        # The default stream's handle is 0, which ExternalStream takes for none.
+        stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
 
 
 # ---------------------------------------------------------------- rotary positions
@@ -83,9 +96,10 @@ def attn_rotary(q, q_out, k, k_out, positions, inv_freq, interleaved: bool = Fal
 
 
 def _rotary(q, k, positions, inv_freq, interleaved, inverse, factor, stream):
-    qo, ko = torch.empty_like(q), None if k is None else torch.empty_like(k)
-    if positions is None:
-        positions = torch.arange(q.shape[2] if q.dim() == 4 else q.shape[0], dtype=torch.int32, device=q.device)
+    with on_stream(stream, q.device):
+        qo, ko = torch.empty_like(q), None if k is None else torch.empty_like(k)
+        if positions is None:
+            positions = torch.arange(q.shape[2] if q.dim() == 4 else q.shape[0], dtype=torch.int32, device=q.device)
     status = _native().rotary(q, qo, k, ko, positions, inv_freq, interleaved, inverse, factor, stream)
     if status:
         _check(status)
@@ -123,7 +137,8 @@ def rotary(q, k=None, positions=None, inv_freq=None, interleaved: bool = False, 
     from ``rotary_frequencies`` (its defaults if not given).  The first
     2 * len(inv_freq) elements of a head are turned, the others copied."""
     if inv_freq is None:
-        inv_freq, _ = rotary_frequencies(q.shape[-1], device=q.device)
+        with on_stream(stream, q.device):
+            inv_freq, _ = rotary_frequencies(q.shape[-1], device=q.device)
     if torch.is_grad_enabled() and (q.requires_grad or (k is not None and k.requires_grad)):
         if stream is not None:
             raise ValueError("rotary under autograd runs on the current stream: use torch.cuda.stream(...)")
@@ -136,7 +151,8 @@ def rotary_backward(dq, dk=None, positions=None, inv_freq=None, interleaved: boo
     """The gradient of ``rotary`` with the same arguments: from the gradients of
     its outputs those of q and k."""
     if inv_freq is None:
-        inv_freq, _ = rotary_frequencies(dq.shape[-1], device=dq.device)
+        with on_stream(stream, dq.device):
+            inv_freq, _ = rotary_frequencies(dq.shape[-1], device=dq.device)
     return _rotary(dq, dk, positions, inv_freq, interleaved, True, factor, stream)
 
 
@@ -183,10 +199,11 @@ def forward_paged(q, k_cache, v_cache, page_table, seqlens, cu_seqlens=None, max
     if max_seqlen_k is None:
         max_seqlen_k = page_table.shape[1] * k_cache.shape[2]
     watchdog_check(q.device)
-    o = torch.empty_like(q)
-    lse = torch.empty((Hq, total), dtype=torch.float32, device=q.device)
     nbytes = attn_fwd_paged_workspace_size(B, Hq, k_cache.shape[1], total, max_seqlen_q, max_seqlen_k, d)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    with on_stream(stream, q.device):
+        o = torch.empty_like(q)
+        lse = torch.empty((Hq, total), dtype=torch.float32, device=q.device)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
     attn_fwd_paged(q, k_cache, v_cache, o, lse, page_table, seqlens, cu_seqlens, max_seqlen_q, max_seqlen_k, causal,
                    d ** -0.5 if scale is None else scale, ws, stream, window)
     watchdog_poll(q.device, stream)

@@ -391,8 +391,9 @@ int attn_rotary(int dtype, const void* q, exattn_strides q_strides, void* q_out,
  *     multiple of B, else EXATTN_ERR_SHAPE).
  * The tables are read on the device and every access is checked against the
  * sizes given here, so a wrong table gives wrong results but never an access
- * out of bounds.  Rows of the packed tensors that belong to no sequence
- * (at or past cu_seqlens[B]) are neither read nor written.
+ * out of bounds.  Rows of the packed tensors that belong to no sequence (before
+ * cu_seqlens[0], or at or past cu_seqlens[B]) are not written, nor read into
+ * any output.
  *
  * attn_cache_append -- writes the new tokens' K and V into their pages, K
  *   turned as by attn_rotary at each token's position (seqlens[b] minus the
@@ -428,8 +429,11 @@ int attn_cache_append(int dtype, const void* q, exattn_strides q_strides, void* 
  *   max_seqlen_q, max_seqlen_k : at least the largest count of new tokens and the
  *     largest length; a sequence beyond them is cut off (its further rows are
  *     not written, its further keys not seen).
- *   Whatever is stored behind a sequence's last row -- NaN included -- does not
- *   reach its output; a row on a page number outside the pool reads as zeros.
+ *   Whatever is stored in rows that none of a sequence's new tokens sees (behind
+ *   its last one, or before the window of its first new token) -- NaN included --
+ *   reaches no output; a NaN or infinity in a V row that some of them see may
+ *   reach the others, as in attn_fwd.  A row on a page number outside the pool
+ *   reads as zeros.  o and lse overlap no other operand.
  *   The keys of the whole batch are shared evenly between the SMs, whatever
  *   its lengths, and the sequences that fall on several of them are joined by
  *   a second kernel from the workspace (attn_fwd_paged_workspace_size bytes,

@@ -271,6 +271,18 @@ def test_nan_stays_with_its_rows():
         assert torch.equal(torch.isnan(lse).t(), hit)
 
 
+def test_nan_queries_of_sequences_on_many_sms():
+    """A query of NaN: its rows are NaN in every piece, and after the join."""
+    for new, Hq in (([2], 4), ([40], 4)):
+        p = Problem(new, [9000], Hq, 2, 64, 32, torch.float16, seed=43)
+        p.q[1, 2] = NAN
+        o, lse = p.run()
+        hit = torch.zeros(new[0], Hq, dtype=torch.bool, device=DEV)
+        hit[1, 2] = True
+        assert torch.equal(torch.isnan(o).all(-1), hit) and torch.equal(torch.isnan(o).any(-1), hit)
+        assert torch.equal(torch.isnan(lse).t(), hit)
+
+
 def test_pools_past_32_bits():
     """Pages whose elements lie past 2^31, and bytes past 2^32, from the pool's start:
     append, copy and attention."""
@@ -367,6 +379,59 @@ def test_a_serving_run(Hq, Hk, d, ps, dtype, window):
         step(r.sample([a, c, forks[0]], 3), 1)
     d2 = add()
     step([d2, a], [65, 1])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("new,lens,Hq,Hk,d,window,causal", [
+    ([1, 1, 1], [200, 777, 90], 8, 2, 128, 70, True),
+    ([3, 2], [700, 130], 8, 2, 64, 40, False),
+    ([90, 33], [600, 250], 4, 1, 128, 100, True),
+    ([150], [500], 2, 2, 64, 33, False)])
+def test_rows_before_the_window(new, lens, Hq, Hk, d, window, causal, dtype):
+    """Rows that the window has left behind hold NaN, pages that it has left behind
+    whole are gone from the table."""
+    p = Problem(new, lens, Hq, Hk, d, 16, dtype, seed=47)
+    for b, (n, m) in enumerate(zip(new, lens)):
+        for r in range(max(0, m - n - window + 1)):
+            page = int(p.table[b, r // 16])
+            p.kc[page, :, r % 16] = p.vc[page, :, r % 16] = NAN
+        gone = max(0, m - n - window + 1) // 16
+        p.table[b, : gone // 2] = -1
+    p.check(*p.run(causal=causal, window=window), causal=causal, window=window)
+
+
+def test_helpers_on_a_given_stream():
+    """What the helpers allocate and compute belongs to the stream that they are
+    given: the current one, held up here, has no part in it."""
+    import exact_attention_67_gb300 as ex
+    p = Problem([1, 40], [700, 300], 4, 2, 64, 16, torch.bfloat16, seed=53)
+    x = p.q[None].transpose(1, 2)                                   # [1, Hq, 41, 64]
+    want, turned = p.run(), ex.rotary(x)
+    cache = ex.PagedCache(8, 16, 1, 2, 64)
+    k, v, q = randn(20, 2, 64, seed=1, dtype=torch.bfloat16), randn(20, 2, 64, seed=2, dtype=torch.bfloat16), p.q[:20]
+    seq = cache.add()
+    step = cache.extend([seq], 20)
+    cache.append(0, step, k, v)
+    through = cache.attend(0, step, q)
+    other = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for given in (other, other.cuda_stream):
+        torch.cuda._sleep(400_000_000)
+        busy = torch.cuda.Event()
+        busy.record()
+        got = ex.forward_paged(p.q, p.kc, p.vc, p.table, p.seq, p.cu, max(p.new), max(p.lens), stream=given)
+        y = ex.rotary(x, stream=given)
+        cache.free(seq)
+        seq = cache.add()
+        step = cache.extend([seq], 20, stream=given)
+        cache.append(0, step, k, v, stream=given)
+        again = cache.attend(0, step, q, stream=given)
+        other.synchronize()
+        assert not busy.query()
+        with torch.cuda.stream(other):
+            assert all(torch.equal(a, b) for a, b in zip([*got, y, *again], [*want, turned, *through]))
+        torch.cuda.synchronize()
+    assert ex.device_error() == 0
 
 
 def test_attention_refusals():
