@@ -185,25 +185,28 @@ __global__ void __launch_bounds__(512, 1)
         if (!(ok = mbar_wait_warp(&bars->s_full[t], cs & 1, wc))) break;
         tc_fence_after();
         if (j >= high || j < low) {
-          // Hidden columns to -inf, in place and in a rolled loop: unrolled over the
-          // 128 registers, this code, that a chunk meets a few times, took some 4,000
-          // clocks to fetch.
+          // Hidden columns to -inf, in place and in a rolled loop, by a word of 32
+          // columns' bits: unrolled over the 128 registers, this code, that a chunk
+          // meets a few times, took some 4,000 clocks to fetch.  A vote that skips
+          // words without hidden columns costs more than it saves.
           int hi = pc->key_hi - (pc->t_lo + j) * C::BN, lo = 0;  // visible: columns [lo, hi)
           const int pos = pc->s.off + pc->tok0 + t * TT + row / G - (pc->t_lo + j) * C::BN;
           if (a.causal) hi = min(hi, pos + 1);
           else if (a.window > 0) hi = min(hi, pos + a.window);
           if (a.window > 0) lo = pos - a.window + 1;
 #pragma unroll 1
-          for (int c = 0; c < C::BN; c += 16) {
-            uint32_t x[16];
-            tmem_ld16(tS + c, x);
+          for (int c = 0; c < C::BN; c += 32) {
+            const int h = min(max(hi - c, 0), 32), l = min(max(lo - c, 0), 32);
+            const uint32_t seen = (h == 32 ? ~0u : (1u << h) - 1) & (l == 32 ? 0u : ~0u << l);
+            uint32_t x[32];
+            tmem_ld32(tS + c, x);
             tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
+            for (int e = 0; e < 32; ++e) {
               asm volatile("" : "+r"(x[e]));
-              if (c + e >= hi || c + e < lo) x[e] = __float_as_uint(-INFINITY);
+              if (!(seen & (1u << e))) x[e] = __float_as_uint(-INFINITY);
             }
-            tmem_st16(tS + c, x);
+            tmem_st32(tS + c, x);
           }
           tmem_wait_st();
         }

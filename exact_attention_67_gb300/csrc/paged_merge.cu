@@ -14,9 +14,11 @@ namespace exattn {
 
 namespace {
 
-// The decode kernel's rows: two a block, WPR warps each.  Eight where there are
-// so few rows that a row's chain of loads over the pieces, as many as there are
-// CTAs, would be the kernel; else two.
+// The decode kernel's rows: two a block, WPR warps each, so that a row of few
+// long sequences, with a piece on every CTA, is not one chain of loads: four with
+// at most 8 columns (48 sequences of 32 heads: 9.7 us for the smallest calls and
+// 140.9 us with four, 9.9 and 143.3 with eight, whose blocks take two waves),
+// else two.
 template <typename T, int D, int WPR>
 __global__ void __launch_bounds__(64 * WPR) paged_merge_kernel(const __grid_constant__ PagedArgs a) {
   constexpr int V = D / 32;      // columns a lane
@@ -112,12 +114,13 @@ __global__ void __launch_bounds__(64 * WPR) paged_merge_kernel(const __grid_cons
 
 // The forward kernel's rows: a block takes 32 of a query tile, a lane each (their
 // partial results lie side by side), and 32 columns, 8 a warp.  One pass with a
-// running maximum over the pieces, four at a time, their loads all at once: few
-// units of long sequences have as many pieces as CTAs (16 units of 10 pieces, 256
-// rows: 19 us with one piece at a time and 128 columns a block).
+// running maximum over the pieces, two at a time (most units have two or three;
+// four at a time take more registers and leave fewer blocks an SM: a windowed
+// batch of 6 chunks 34.2 us with them, 32.6 with two).  Reading and joining the
+// pieces, mostly in L2, is latency: 2 to 5 us a call, 2 % of a long chunk's time.
 template <typename T, int D>
 __global__ void __launch_bounds__(128) paged_merge_rows_kernel(const __grid_constant__ PagedArgs a) {
-  constexpr int C4 = 2, BATCH = 4;  // 4-column vectors a thread, pieces at once
+  constexpr int C4 = 2, BATCH = 2;  // 4-column vectors a thread, pieces at once
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int g = static_cast<int>(blockIdx.x) + 1;
@@ -185,9 +188,9 @@ __global__ void __launch_bounds__(128) paged_merge_rows_kernel(const __grid_cons
 template <typename T, int D>
 cudaError_t launch_t(const PagedArgs& a, cudaStream_t stream) {
   const bool few = a.cols > 0, deep = few && a.cols <= 8;
-  const dim3 grid(a.ctas - 1, few ? a.cols / 2 : 8, few ? 1 : D / 32), block(deep ? 512 : 128);
+  const dim3 grid(a.ctas - 1, few ? a.cols / 2 : 8, few ? 1 : D / 32), block(deep ? 256 : 128);
   const char* what = "paged merge kernel launch";
-  return deep  ? launch_dependent(what, paged_merge_kernel<T, D, 8>, grid, block, 0, stream, a)
+  return deep  ? launch_dependent(what, paged_merge_kernel<T, D, 4>, grid, block, 0, stream, a)
          : few ? launch_dependent(what, paged_merge_kernel<T, D, 2>, grid, block, 0, stream, a)
                : launch_dependent(what, paged_merge_rows_kernel<T, D>, grid, block, 0, stream, a);
 }
