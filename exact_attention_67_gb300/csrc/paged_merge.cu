@@ -15,15 +15,15 @@ namespace exattn {
 namespace {
 
 // The decode kernel's rows: two a block, WPR warps each, so that a row of few
-// long sequences, with a piece on every CTA, is not one chain of loads: four with
-// at most 8 columns (48 sequences of 32 heads: 9.7 us for the smallest calls and
-// 140.9 us with four, 9.9 and 143.3 with eight, whose blocks take two waves),
-// else two.
+// long sequences, with a piece on every CTA, is not one chain of loads.  Four
+// warps with at most 8 columns, else two.  Whole calls with 2, 4 and 8 warps: 8
+// units of 4 pieces 9.2, 9.5, 9.8 us; one unit of 147 pieces 21.1, 16.2, 14.4;
+// 192 units of 1 to 3 pieces 141.1, 140.8, 142.8.
 template <typename T, int D, int WPR>
 __global__ void __launch_bounds__(64 * WPR) paged_merge_kernel(const __grid_constant__ PagedArgs a) {
   constexpr int V = D / 32;      // columns a lane
   constexpr int BATCH = 4;       // pieces a warp loads at once
-  __shared__ float red[2 * WPR];
+  __shared__ float2 red[2 * WPR];  // maximum, sum
   __shared__ float acc_s[2 * WPR][D];
   // The next kernel of the stream may set itself up; this one waits for the pieces.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -46,62 +46,68 @@ __global__ void __launch_bounds__(64 * WPR) paged_merge_kernel(const __grid_cons
   int used = 0;
   for (int i = 0; i < pieces && used < 2; ++i) used += from(i + 1) > from(i);
   if (used < 2) return;
-  auto at = [&](int i) { return (static_cast<long long>(g - 1 + i) * 2 + (from(i) == 0)) * a.rows + row; };
-  float m = -INFINITY;
-  if (live)
-    for (int i = part * 32 + lane; i < pieces; i += 32 * WPR)
-      if (from(i + 1) > from(i)) m = fmaxf(m, a.part_lse[at(i)]);
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (lane == 0) red[warp] = m;
-  __syncthreads();
+  // One pass with a running maximum, a batch of pieces' loads all at once.
+  float m = -INFINITY, sum = 0.f, acc[V] = {};
+  for (int i0 = part; live && i0 < pieces; i0 += BATCH * WPR) {
+    float l[BATCH], x[BATCH][V];
 #pragma unroll
-  for (int i = 0; i < WPR; ++i) m = fmaxf(m, red[warp - part + i]);
-  float acc[V] = {}, sum = 0.f;
-  if (live) {
-    for (int i0 = part; i0 < pieces; i0 += BATCH * WPR) {
-      float e[BATCH], x[BATCH][V];
+    for (int u = 0; u < BATCH; ++u) {
+      const int i = i0 + u * WPR;
+      l[u] = -INFINITY;
 #pragma unroll
-      for (int u = 0; u < BATCH; ++u) {
-        const int i = i0 + u * WPR;
-        e[u] = 0.f;
-#pragma unroll
-        for (int c = 0; c < V; ++c) x[u][c] = 0.f;
-        if (i >= pieces || from(i + 1) <= from(i)) continue;
-        const long long r = at(i);
-        const float l = a.part_lse[r];
-        e[u] = l == -INFINITY ? 0.f : expf(l - m);
-        const float* po = a.part_o + r * D + lane * V;
-        if constexpr (V == 4) {
-          const float4 y = *reinterpret_cast<const float4*>(po);
-          x[u][0] = y.x;
-          x[u][1] = y.y;
-          x[u][2] = y.z;
-          x[u][3] = y.w;
-        } else {
-          const float2 y = *reinterpret_cast<const float2*>(po);
-          x[u][0] = y.x;
-          x[u][1] = y.y;
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < BATCH; ++u) {
-        sum += e[u];
-#pragma unroll
-        for (int c = 0; c < V; ++c) acc[c] = fmaf(e[u], x[u][c], acc[c]);
+      for (int c = 0; c < V; ++c) x[u][c] = 0.f;
+      if (i >= pieces || from(i + 1) <= from(i)) continue;
+      const long long r = (static_cast<long long>(g - 1 + i) * 2 + (from(i) == 0)) * a.rows + row;
+      l[u] = a.part_lse[r];
+      const float* po = a.part_o + r * D + lane * V;
+      if constexpr (V == 4) {
+        const float4 y = *reinterpret_cast<const float4*>(po);
+        x[u][0] = y.x;
+        x[u][1] = y.y;
+        x[u][2] = y.z;
+        x[u][3] = y.w;
+      } else {
+        const float2 y = *reinterpret_cast<const float2*>(po);
+        x[u][0] = y.x;
+        x[u][1] = y.y;
       }
     }
+    float top = m;
+#pragma unroll
+    for (int u = 0; u < BATCH; ++u) top = fmaxf(top, l[u]);
+    // (A NaN is in no maximum, but in the sums, and stays there.)
+    const float keep = m == -INFINITY ? 0.f : expf(m - top);
+    sum *= keep;
+#pragma unroll
+    for (int c = 0; c < V; ++c) acc[c] *= keep;
+#pragma unroll
+    for (int u = 0; u < BATCH; ++u) {
+      const float e = l[u] == -INFINITY ? 0.f : expf(l[u] - top);
+      sum += e;
+#pragma unroll
+      for (int c = 0; c < V; ++c) acc[c] = fmaf(e, x[u][c], acc[c]);
+    }
+    m = top;
   }
-  __syncthreads();
-  if (lane == 0) red[warp] = sum;
+  // The row's warps, in order.
+  if (lane == 0) red[warp] = make_float2(m, sum);
 #pragma unroll
   for (int c = 0; c < V; ++c) acc_s[warp][lane * V + c] = acc[c];
   __syncthreads();
   if (part != 0 || !live) return;
+  m = -INFINITY;
 #pragma unroll
-  for (int i = 1; i < WPR; ++i) {
-    sum += red[warp + i];
+  for (int i = 0; i < WPR; ++i) m = fmaxf(m, red[warp + i].x);
+  sum = 0.f;
 #pragma unroll
-    for (int c = 0; c < V; ++c) acc[c] += acc_s[warp + i][lane * V + c];
+  for (int c = 0; c < V; ++c) acc[c] = 0.f;
+#pragma unroll
+  for (int i = 0; i < WPR; ++i) {
+    const float2 w_i = red[warp + i];
+    const float e = w_i.x == -INFINITY ? 0.f : expf(w_i.x - m);
+    sum = fmaf(e, w_i.y, sum);
+#pragma unroll
+    for (int c = 0; c < V; ++c) acc[c] = fmaf(e, acc_s[warp + i][lane * V + c], acc[c]);
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   const int head = p.h * a.G + row % a.G, prow = p.row + tok;
