@@ -130,6 +130,28 @@ def test_autograd_matches_formula_and_differences():
     check(q.grad, *turned(np.ones(q.shape), p, fr, factor, True, -1), torch.float16)
 
 
+def test_unusual_frequencies():
+    """Zero, denormal, tiny, negative and large frequencies against rational
+    arithmetic: an angle is off by 2^-53 of itself (the double 1 / 2 pi and its
+    product) and 2^-33 turns, cos and sin of it by 2^-22 more in fp32."""
+    from fractions import Fraction
+    import exact_attention_67_gb300 as ex
+    pi = Fraction(31415926535897932384626433832795028841971693993751, 10 ** 49)
+    fs = [0.0, 5e-324, 1e-300, 1e-12, 1e-3, 0.5, -0.5, 1.0, 3.0, -7.5, 100.0, 2.0 ** 20 + 0.3]
+    ps = [0, 1, -1, 2, 77, 999]
+    freq = torch.tensor(fs, dtype=torch.float64, device=DEV)
+    q = torch.zeros(1, 1, len(ps), 64, dtype=torch.float16, device=DEV)
+    q[..., : len(fs)] = 1.0                                         # pairs (1, 0): the outputs are cos and sin
+    y = ex.rotary(q, None, torch.tensor(ps, dtype=torch.int32, device=DEV), freq)[0, 0].double().cpu().numpy()
+    for i, p in enumerate(ps):
+        for j, f in enumerate(fs):
+            turns = Fraction(f) * p / (2 * pi)
+            angle = 2 * np.pi * float(turns - round(turns))
+            off = 2 * np.pi * (abs(float(turns)) * 2.0 ** -53 + 2.0 ** -33) + 2.0 ** -22
+            for got, want in ((y[i, j], np.cos(angle)), (y[i, j + len(fs)], np.sin(angle))):
+                assert abs(got - want) <= 2.0 ** -11 * abs(want) + 2.0 ** -25 + off, (p, f, got, want)
+
+
 def test_capture_and_replay():
     import exact_attention_67_gb300 as ex
     q, k = inputs(1, 300, 4, 128, torch.bfloat16, "bhnd", 11), inputs(1, 300, 2, 128, torch.bfloat16, "bhnd", 12)
