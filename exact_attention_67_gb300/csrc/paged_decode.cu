@@ -29,6 +29,12 @@
 //   * the logsumexp comes from a sum of the unrounded weights, and so does
 //     bf16's O (P's f16 rounding, 2^-11 of a weight, is far below the output's);
 //     f16's O is normalised by the sum of the rounded weights.
+// Bound by HBM on long batches: 4 sequences of 32,768 keys, 32 key heads of 128, 297
+// us (7.2 TB/s; a plain copy runs at 6.7), 48 ragged ones of up to 16,384 keys, 32
+// heads on 4, 141 us (6.5 TB/s).  Short calls are a chain of latencies: one of 777
+// keys 9.5 us (finding the place in the line 1.5, the first page number and tile
+// 1.5, its products and softmax 1.5, the merge 2.9); 16 of up to 5,000 keys with 5
+// new tokens, d = 64, 26.8 us where the bytes take 13.4.
 // d = 64: V^T has 64 rows and the MMA takes 128, so the second half reads the
 // shared memory behind the tile; those accumulator rows are never read.
 #include "paged.cuh"
@@ -460,7 +466,8 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
           const int q = w * H + i;
           if (q >= cols) break;
           const Column c = coef[q];
-          const float val = (c.c0 != 0.f ? __uint_as_float(o0[i]) * c.c0 : 0.f) + (c.c1 != 0.f ? __uint_as_float(o1[i]) * c.c1 : 0.f);
+          const float val = (c.c0 != 0.f ? __uint_as_float(o0[i]) * c.c0 : 0.f) +
+                            (c.c1 != 0.f ? __uint_as_float(o1[i]) * c.c1 : 0.f);
           if (tid < D) {
             if (!whole) a.part_o[c.row + tid] = val;
             else if constexpr (E::kFmt == 1) static_cast<T*>(a.o)[c.row + tid] = __float2bfloat16_rn(val);
@@ -514,155 +521,155 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
   } else {
     if constexpr (C::SPLIT_REGS) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == C::S_WARP) {
-    // ------------------------------------------------------------ S^T = K Q^T
-    constexpr uint32_t idesc = idesc_f16kind(E::kFmt, 128, NQ, 0, 0);
-    const uint64_t q_desc = sdesc_sw128(smem_u32(smem + C::OFF_Q), 16, 1024);
-    const uint64_t k_desc = sdesc_sw128(smem_u32(smem + C::OFF_K), 16, C::GROUP);
-    auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_warp(bar, parity, wc); };
-    int st = 0, seg = 0;
-    bool ok = true;
-    for (int i = 0; ok; ++i) {
-      const PagedPiece* pc = ring.get(i, wc);
-      if (!pc) break;
-      const int n = pc->t_hi - pc->t_lo;
-      ring.release(i);
-      if (n == 0) continue;
-      const int qb = seg % C::QBUF;
-      if (!(ok = wait(&bars->q_full[qb], (seg / C::QBUF) & 1))) break;
-      const uint64_t qd = q_desc + ((qb * C::Q_TILE) >> 4);
-      for (int j = 0; j < n; ++j, ++st) {
-        const int s = st % C::K_STAGES, b = st & 3;
-        if (!(ok = wait(&bars->k_full[s], (st / C::K_STAGES) & 1))) break;
-        if (st >= 4 && !(ok = wait(&bars->s_free[b], ((st >> 2) - 1) & 1))) break;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint64_t kd = k_desc + ((s * C::KV_TILE) >> 4);
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_ss(tmem + C::TM_S + b * NQ, kd + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4),
-                   qd + (((kk >> 2) * C::Q_CHUNK + (kk & 3) * 32) >> 4), idesc, kk > 0);
-          mma_commit(&bars->s_full[b]);
-          mma_commit(&bars->k_empty[s]);
-          if (j == n - 1) mma_commit(&bars->q_empty[qb]);
-        }
-        __syncwarp();
-      }
-      ++seg;
-    }
-    // Nothing may still read shared memory or write TMEM once the CTA tears down.
-    if (elect_one()) mma_commit(&bars->done[0]);
-    __syncwarp();
-    if (lane == 0) mbar_wait_drain(&bars->done[0], 0, a.err);
-    __syncwarp();
-    } else if (warp == C::O_WARP) {
-    // ------------------------------------------------------------ O^T += V^T P^T
-    constexpr uint32_t idesc = idesc_f16kind(PE::kFmt, 128, NQ, 1, 0);
-    const uint64_t p_desc = sdesc_sw128(smem_u32(smem + C::OFF_P), 16, 1024);
-    // Its two runs of 64 rows (d) are a group's two atoms; at d = 64 the second
-    // run is the next group's.
-    const uint64_t v_desc = sdesc_sw128(smem_u32(smem + C::OFF_V), 1024, C::GROUP);
-    auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_warp(bar, parity, wc); };
-    int st = 0, seg = 0;
-    bool ok = true;
-    for (int i = 0; ok; ++i) {
-      const PagedPiece* pc = ring.get(i, wc);
-      if (!pc) break;
-      const int n = pc->t_hi - pc->t_lo, ob = seg & 1;
-      ring.release(i);
-      if (n == 0) continue;
-      for (int j = 0; j < n; ++j, ++st) {
-        const int s = st % C::V_STAGES, w = st & 1;
-        if (!(ok = wait(&bars->v_ready[s], (st / C::V_STAGES) & 1))) break;
-        // The unit two before has been read out of these accumulators.
-        if (j == 0 && seg >= 2 && !(ok = wait(&bars->o_free[ob], ((seg >> 1) - 1) & 1))) break;
-        if (!(ok = wait(&bars->p_full[w], (st >> 1) & 1))) break;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint64_t vd = v_desc + ((s * C::KV_TILE) >> 4), pd = p_desc + ((w * C::P_TILE) >> 4);
-#pragma unroll
-          for (int kk = 0; kk < BN / 16; ++kk)
-            mma_ss(tmem + C::TM_O + (ob * 2 + w) * NQ, vd + ((kk * 2 * C::GROUP) >> 4),
-                   pd + (((kk >> 2) * C::P_CHUNK + (kk & 3) * 32) >> 4), idesc, (j >= 2 || kk > 0) ? 1u : 0u);
-          mma_commit(&bars->p_free[w]);
-          mma_commit(&bars->v_empty[s]);
-          if (j == n - 1) mma_commit(&bars->o_full[ob]);
-        }
-        __syncwarp();
-      }
-      ++seg;
-    }
-    if (elect_one()) mma_commit(&bars->done[1]);
-    __syncwarp();
-    if (lane == 0) mbar_wait_drain(&bars->done[1], 0, a.err);
-    __syncwarp();
-    } else {
-    // ------------------------------------------------------------ TMA producers
-    const bool is_k = warp == C::K_WARP;
-    const CUtensorMap* tm = is_k ? &tm_k : &tm_v;
-    uint64_t* full = is_k ? bars->k_full : bars->v_full;
-    uint64_t* empty = is_k ? bars->k_empty : bars->v_empty;
-    uint8_t* tiles = smem + (is_k ? C::OFF_K : C::OFF_V);
-    const int stages = is_k ? C::K_STAGES : C::V_STAGES;  // a power of two
-    const uint64_t pol = l2_policy_evict_first();
-    const int shift = a.pv.page_shift, box = min(a.pv.page_size, BN), per_tile = BN / box;
-    const uint32_t q_bytes = static_cast<uint32_t>(UT * G) * 128 * C::NCHUNK;
-    int st = 0, seg = 0;
-    bool ok = true;
-    // Boxes of a tile that hold a visible key, and this lane's page of it.
-    auto boxes = [&](const PagedPiece& pc, int t) { return min(per_tile, (pc.key_hi - t * BN + box - 1) / box); };
-    auto page_of = [&](const PagedPiece& pc, int t) {
-      return lane < boxes(pc, t) ? a.pv.table[pc.b * a.pv.table_stride + (t * BN >> shift) + lane] : 0;
-    };
-    for (int i = 0; ok; ++i) {
-      PagedPiece pc;
-      int first_page = 0;
-      if (is_k) {
-        const bool more = cur.next(a, UT, seq, &pc);
-        if (more && pc.t_hi > pc.t_lo) first_page = page_of(pc, pc.t_lo);
-        if (!(ok = ring.put(i, more ? &pc : nullptr, lane, wc)) || !more) break;
-      } else {
-        const PagedPiece* p = ring.get(i, wc);
-        if (!p) break;
-        pc = *p;
+      // ------------------------------------------------------------ S^T = K Q^T
+      constexpr uint32_t idesc = idesc_f16kind(E::kFmt, 128, NQ, 0, 0);
+      const uint64_t q_desc = sdesc_sw128(smem_u32(smem + C::OFF_Q), 16, 1024);
+      const uint64_t k_desc = sdesc_sw128(smem_u32(smem + C::OFF_K), 16, C::GROUP);
+      auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_warp(bar, parity, wc); };
+      int st = 0, seg = 0;
+      bool ok = true;
+      for (int i = 0; ok; ++i) {
+        const PagedPiece* pc = ring.get(i, wc);
+        if (!pc) break;
+        const int n = pc->t_hi - pc->t_lo;
         ring.release(i);
-        if (pc.t_hi > pc.t_lo) first_page = page_of(pc, pc.t_lo);
-      }
-      if (pc.t_hi == pc.t_lo) continue;
-      int page = first_page;
-      if (is_k) {
+        if (n == 0) continue;
         const int qb = seg % C::QBUF;
-        if (seg >= C::QBUF && !(ok = mbar_wait_warp(&bars->q_empty[qb], (seg / C::QBUF - 1) & 1, wc))) break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&bars->q_full[qb], q_bytes);
-          for (int c = 0; c < C::NCHUNK; ++c)
-            tma_load_4d(&tm_q, &bars->q_full[qb], smem + C::OFF_Q + qb * C::Q_TILE + c * C::Q_CHUNK, c * 64, 0, pc.h,
-                        pc.s.row0 + pc.tok0, pol);
+        if (!(ok = wait(&bars->q_full[qb], (seg / C::QBUF) & 1))) break;
+        const uint64_t qd = q_desc + ((qb * C::Q_TILE) >> 4);
+        for (int j = 0; j < n; ++j, ++st) {
+          const int s = st % C::K_STAGES, b = st & 3;
+          if (!(ok = wait(&bars->k_full[s], (st / C::K_STAGES) & 1))) break;
+          if (st >= 4 && !(ok = wait(&bars->s_free[b], ((st >> 2) - 1) & 1))) break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t kd = k_desc + ((s * C::KV_TILE) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+              mma_ss(tmem + C::TM_S + b * NQ, kd + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4),
+                     qd + (((kk >> 2) * C::Q_CHUNK + (kk & 3) * 32) >> 4), idesc, kk > 0);
+            mma_commit(&bars->s_full[b]);
+            mma_commit(&bars->k_empty[s]);
+            if (j == n - 1) mma_commit(&bars->q_empty[qb]);
+          }
+          __syncwarp();
+        }
+        ++seg;
+      }
+      // Nothing may still read shared memory or write TMEM once the CTA tears down.
+      if (elect_one()) mma_commit(&bars->done[0]);
+      __syncwarp();
+      if (lane == 0) mbar_wait_drain(&bars->done[0], 0, a.err);
+      __syncwarp();
+    } else if (warp == C::O_WARP) {
+      // ------------------------------------------------------------ O^T += V^T P^T
+      constexpr uint32_t idesc = idesc_f16kind(PE::kFmt, 128, NQ, 1, 0);
+      const uint64_t p_desc = sdesc_sw128(smem_u32(smem + C::OFF_P), 16, 1024);
+      // Its two runs of 64 rows (d) are a group's two atoms; at d = 64 the second
+      // run is the next group's.
+      const uint64_t v_desc = sdesc_sw128(smem_u32(smem + C::OFF_V), 1024, C::GROUP);
+      auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_warp(bar, parity, wc); };
+      int st = 0, seg = 0;
+      bool ok = true;
+      for (int i = 0; ok; ++i) {
+        const PagedPiece* pc = ring.get(i, wc);
+        if (!pc) break;
+        const int n = pc->t_hi - pc->t_lo, ob = seg & 1;
+        ring.release(i);
+        if (n == 0) continue;
+        for (int j = 0; j < n; ++j, ++st) {
+          const int s = st % C::V_STAGES, w = st & 1;
+          if (!(ok = wait(&bars->v_ready[s], (st / C::V_STAGES) & 1))) break;
+          // The unit two before has been read out of these accumulators.
+          if (j == 0 && seg >= 2 && !(ok = wait(&bars->o_free[ob], ((seg >> 1) - 1) & 1))) break;
+          if (!(ok = wait(&bars->p_full[w], (st >> 1) & 1))) break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t vd = v_desc + ((s * C::KV_TILE) >> 4), pd = p_desc + ((w * C::P_TILE) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < BN / 16; ++kk)
+              mma_ss(tmem + C::TM_O + (ob * 2 + w) * NQ, vd + ((kk * 2 * C::GROUP) >> 4),
+                     pd + (((kk >> 2) * C::P_CHUNK + (kk & 3) * 32) >> 4), idesc, (j >= 2 || kk > 0) ? 1u : 0u);
+            mma_commit(&bars->p_free[w]);
+            mma_commit(&bars->v_empty[s]);
+            if (j == n - 1) mma_commit(&bars->o_full[ob]);
+          }
+          __syncwarp();
+        }
+        ++seg;
+      }
+      if (elect_one()) mma_commit(&bars->done[1]);
+      __syncwarp();
+      if (lane == 0) mbar_wait_drain(&bars->done[1], 0, a.err);
+      __syncwarp();
+    } else {
+      // ------------------------------------------------------------ TMA producers
+      const bool is_k = warp == C::K_WARP;
+      const CUtensorMap* tm = is_k ? &tm_k : &tm_v;
+      uint64_t* full = is_k ? bars->k_full : bars->v_full;
+      uint64_t* empty = is_k ? bars->k_empty : bars->v_empty;
+      uint8_t* tiles = smem + (is_k ? C::OFF_K : C::OFF_V);
+      const int stages = is_k ? C::K_STAGES : C::V_STAGES;  // a power of two
+      const uint64_t pol = l2_policy_evict_first();
+      const int shift = a.pv.page_shift, box = min(a.pv.page_size, BN), per_tile = BN / box;
+      const uint32_t q_bytes = static_cast<uint32_t>(UT * G) * 128 * C::NCHUNK;
+      int st = 0, seg = 0;
+      bool ok = true;
+      // Boxes of a tile that hold a visible key, and this lane's page of it.
+      auto boxes = [&](const PagedPiece& pc, int t) { return min(per_tile, (pc.key_hi - t * BN + box - 1) / box); };
+      auto page_of = [&](const PagedPiece& pc, int t) {
+        return lane < boxes(pc, t) ? a.pv.table[pc.b * a.pv.table_stride + (t * BN >> shift) + lane] : 0;
+      };
+      for (int i = 0; ok; ++i) {
+        PagedPiece pc;
+        int first_page = 0;
+        if (is_k) {
+          const bool more = cur.next(a, UT, seq, &pc);
+          if (more && pc.t_hi > pc.t_lo) first_page = page_of(pc, pc.t_lo);
+          if (!(ok = ring.put(i, more ? &pc : nullptr, lane, wc)) || !more) break;
+        } else {
+          const PagedPiece* p = ring.get(i, wc);
+          if (!p) break;
+          pc = *p;
+          ring.release(i);
+          if (pc.t_hi > pc.t_lo) first_page = page_of(pc, pc.t_lo);
+        }
+        if (pc.t_hi == pc.t_lo) continue;
+        int page = first_page;
+        if (is_k) {
+          const int qb = seg % C::QBUF;
+          if (seg >= C::QBUF && !(ok = mbar_wait_warp(&bars->q_empty[qb], (seg / C::QBUF - 1) & 1, wc))) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&bars->q_full[qb], q_bytes);
+            for (int c = 0; c < C::NCHUNK; ++c)
+              tma_load_4d(&tm_q, &bars->q_full[qb], smem + C::OFF_Q + qb * C::Q_TILE + c * C::Q_CHUNK, c * 64, 0, pc.h,
+                          pc.s.row0 + pc.tok0, pol);
+          }
+        }
+        ++seg;
+        for (int t = pc.t_lo; t < pc.t_hi; ++t, ++st) {
+          const int s = st & (stages - 1);
+          const int next_page = t + 1 < pc.t_hi ? page_of(pc, t + 1) : 0;
+          if (!(ok = mbar_wait_warp(&empty[s], (st & stages) ? 0 : 1, wc))) break;
+          const int nb = boxes(pc, t);
+          if (lane == 0) mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(nb * box) * 128 * C::NCHUNK);
+          __syncwarp();
+          if (lane < nb)
+            load_page(tm, &full[s], tiles + s * C::KV_TILE + lane * box * 128 * C::NCHUNK, a.pv,
+                      (t * BN & (a.pv.page_size - 1)) >> 3, page, pc.h, is_k, pol);
+          __syncwarp();
+          page = next_page;
         }
       }
-      ++seg;
-      for (int t = pc.t_lo; t < pc.t_hi; ++t, ++st) {
-        const int s = st & (stages - 1);
-        const int next_page = t + 1 < pc.t_hi ? page_of(pc, t + 1) : 0;
-        if (!(ok = mbar_wait_warp(&empty[s], (st & stages) ? 0 : 1, wc))) break;
-        const int nb = boxes(pc, t);
-        if (lane == 0) mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(nb * box) * 128 * C::NCHUNK);
-        __syncwarp();
-        if (lane < nb)
-          load_page(tm, &full[s], tiles + s * C::KV_TILE + lane * box * 128 * C::NCHUNK, a.pv,
-                    (t * BN & (a.pv.page_size - 1)) >> 3, page, pc.h, is_k, pol);
-        __syncwarp();
-        page = next_page;
+      __syncwarp();
+      if (lane == 0 && *reinterpret_cast<volatile int*>(&bars->abort)) {
+        // Never leave a copy in flight into shared memory this CTA is about to release.
+        for (int i = max(0, seg - C::QBUF); is_k && i < seg; ++i)
+          mbar_wait_drain(&bars->q_full[i % C::QBUF], (i / C::QBUF) & 1, a.err);
+        for (int j = max(0, st - stages); j < st; ++j)
+          mbar_wait_drain(&full[j & (stages - 1)], (j & stages) ? 1 : 0, a.err);
       }
-    }
-    __syncwarp();
-    if (lane == 0 && *reinterpret_cast<volatile int*>(&bars->abort)) {
-      // Never leave a copy in flight into shared memory this CTA is about to release.
-      for (int i = max(0, seg - C::QBUF); is_k && i < seg; ++i)
-        mbar_wait_drain(&bars->q_full[i % C::QBUF], (i / C::QBUF) & 1, a.err);
-      for (int j = max(0, st - stages); j < st; ++j)
-        mbar_wait_drain(&full[j & (stages - 1)], (j & stages) ? 1 : 0, a.err);
-    }
-    __syncwarp();
+      __syncwarp();
     }
   }
 

@@ -19,6 +19,14 @@
 //   * the logsumexp is formed from the unrounded weights.  So is bf16's O: the
 //     f16 rounding of P (2^-12 of a weight at most) is far below the output's.
 //     f16's O is normalised by the sum of the rounded weights.
+//
+// Bound at d = 128 by the tensor core and the shared memory that feeds it: 2,048
+// tokens at 32,768 keys, 32 heads on 8, 800 to 840 us with the box's clock (1,270 to
+// 1,340 TFLOP/s, 66 to 70 % of cuBLAS's burst), 754 without any of the softmax's
+// arithmetic.  At d = 64 by the hand-offs between a tile's products and its softmax:
+// chunks of 1,500 at 9,000 keys 787 TFLOP/s, 1,030 without the arithmetic.  Short
+// chunks are their start, masked steps and the merge: 6 chunks of up to 600 under a
+// window of 1,024, 20 heads on 4, d = 64, 33.5 us, of which the steps are some 16.
 #include "paged.cuh"
 #include "paged_sched.cuh"
 #include "ptx.cuh"
@@ -53,9 +61,9 @@ struct PfCfg {
   // can be computed while the softmax still works on this one.
   static constexpr bool EARLY_S = D == 64;
   // A warp takes some 650 clocks to issue a product and wait for its operands:
-  // both tiles' four a step were the bound at d = 64 (690 TFLOP/s on long chunks;
-  // 826 with a warp a tile).  At d = 128 the products themselves take that long,
-  // and two warps' run into one another (1,199 TFLOP/s; 1,306 from one warp).
+  // both tiles' four a step were the bound at d = 64 (690 TFLOP/s on chunks of 2,048
+  // at 32,768 keys; 826 with a warp a tile).  At d = 128 the products themselves take
+  // that long, and two warps' run into one another (1,199 TFLOP/s; 1,306 from one).
   static constexpr int ISSUERS = D == 64 ? 2 : 1;
   static constexpr uint32_t TM_COLS = 512;
   __host__ __device__ static constexpr uint32_t tm_s(int t) { return 128u * t; }
@@ -306,7 +314,8 @@ __global__ void __launch_bounds__(512, 1)
       // No visible key: 0 and -inf.  A NaN among the scores makes the sum NaN.
       const float inv_l = l == 0.f ? 0.f : 1.f / l;
       const float L = le == 0.f ? -INFINITY : (m_ref + log2f(le)) * 0.6931471805599453f;
-      const int row_tok = row / G, tok = t * TT + row_tok, prow = pc->s.row0 + pc->tok0 + tok, head = pc->h * G + row % G;
+      const int row_tok = row / G, tok = t * TT + row_tok;
+      const int prow = pc->s.row0 + pc->tok0 + tok, head = pc->h * G + row % G;
       const bool live = row_tok < TT && tok < pc->ntok, whole = pc->whole();
       // Partial results lie [d / 4][row][4]: a warp's rows side by side.
       const long long part = (static_cast<long long>(blockIdx.x) * 2 + pc->slot()) * 2 + t;
@@ -362,10 +371,11 @@ __global__ void __launch_bounds__(512, 1)
     for (int i = 0; ok; ++i) {
       const PagedPiece* pc = ring.get(i, wc);
       if (!pc) break;
-      const int n = max(pc->n[0], pc->n[1]), keys_lo = pc->key_lo - pc->t_lo * C::BN, keys = pc->key_hi - pc->t_lo * C::BN;
+      const int n = max(pc->n[0], pc->n[1]);
+      const int keys_lo = pc->key_lo - pc->t_lo * C::BN, keys_hi = pc->key_hi - pc->t_lo * C::BN;
       ring.release(i);
       for (int j = 0; j < n; ++j, ++vt) {
-        const int s = vt % C::STAGES, lo = keys_lo - j * C::BN, hi = keys - j * C::BN;  // rows that a query sees
+        const int s = vt % C::STAGES, lo = keys_lo - j * C::BN, hi = keys_hi - j * C::BN;  // rows that a query sees
         if (!(ok = mbar_wait_warp(&bars->v_full[s], (vt / C::STAGES) & 1, wc))) break;
         uint4* tile = reinterpret_cast<uint4*>(smem + C::OFF_V + s * C::TILE_BYTES);
         if constexpr (kConvertV) {
@@ -395,174 +405,174 @@ __global__ void __launch_bounds__(512, 1)
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     if (warp == C::K_WARP || warp == C::V_WARP) {
-    // ------------------------------------------------------------ TMA producers
-    const bool is_k = warp == C::K_WARP;
-    const CUtensorMap* tm = is_k ? &tm_k : &tm_v;
-    uint64_t* full = is_k ? bars->k_full : bars->v_full;
-    uint64_t* empty = is_k ? bars->k_empty : bars->v_empty;
-    uint8_t* tiles = smem + (is_k ? C::OFF_K : C::OFF_V);
-    const uint64_t pol_kv = l2_policy_evict_last();  // re-read by every unit of the (sequence, key head)
-    const uint64_t pol_q = l2_policy_evict_first();
-    const int shift = a.pv.page_shift, box = min(a.pv.page_size, C::BN), per_tile = C::BN / box;
-    const uint32_t q_bytes = static_cast<uint32_t>(TT * G) * 128 * C::NCHUNK;
-    int kt = 0, seg = 0;  // key tiles and Qs issued
-    bool ok = true;
-    // Boxes of a tile that hold a visible key, and this lane's page of it.
-    auto boxes = [&](const PagedPiece& pc, int t) { return min(per_tile, (pc.key_hi - t * C::BN + box - 1) / box); };
-    auto page_of = [&](const PagedPiece& pc, int t) {
-      return lane < boxes(pc, t) ? a.pv.table[pc.b * a.pv.table_stride + (t * C::BN >> shift) + lane] : 0;
-    };
-    for (int i = 0; ok; ++i) {
-      PagedPiece pc;
-      int first_page = 0;
-      if (is_k) {
-        const bool more = cur.next(a, UT, seq, &pc);
-        if (more && pc.t_hi > pc.t_lo) first_page = page_of(pc, pc.t_lo);
-        for (int t = 0; t < 2; ++t) pc.n[t] = more ? tiles_of(a, pc, t) : 0;
-        if (!(ok = ring.put(i, more ? &pc : nullptr, lane, wc)) || !more) break;
-      } else {
-        const PagedPiece* p = ring.get(i, wc);
-        if (!p) break;
-        pc = *p;
-        ring.release(i);
-        if (pc.t_hi > pc.t_lo) first_page = page_of(pc, pc.t_lo);
-      }
-      const int n0 = pc.n[0], n1 = pc.n[1], n = max(n0, n1);
-      if (n == 0) continue;
-      int page = first_page;
-      if (is_k) {
-        if (seg >= 1 && !(ok = mbar_wait_warp(&bars->q_empty, (seg - 1) & 1, wc))) break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&bars->q_full, q_bytes * ((n0 > 0) + (n1 > 0)));
-          for (int t = 0; t < 2; ++t)
-            if ((t == 0 ? n0 : n1) > 0)
-              for (int c = 0; c < C::NCHUNK; ++c)
-                tma_load_4d(&tm_q, &bars->q_full, smem + C::OFF_Q + t * C::TILE_BYTES + c * C::CHUNK_BYTES, c * 64, 0, pc.h,
-                            pc.s.row0 + pc.tok0 + t * TT, pol_q);
+      // ------------------------------------------------------------ TMA producers
+      const bool is_k = warp == C::K_WARP;
+      const CUtensorMap* tm = is_k ? &tm_k : &tm_v;
+      uint64_t* full = is_k ? bars->k_full : bars->v_full;
+      uint64_t* empty = is_k ? bars->k_empty : bars->v_empty;
+      uint8_t* tiles = smem + (is_k ? C::OFF_K : C::OFF_V);
+      const uint64_t pol_kv = l2_policy_evict_last();  // re-read by every unit of the (sequence, key head)
+      const uint64_t pol_q = l2_policy_evict_first();
+      const int shift = a.pv.page_shift, box = min(a.pv.page_size, C::BN), per_tile = C::BN / box;
+      const uint32_t q_bytes = static_cast<uint32_t>(TT * G) * 128 * C::NCHUNK;
+      int kt = 0, seg = 0;  // key tiles and Qs issued
+      bool ok = true;
+      // Boxes of a tile that hold a visible key, and this lane's page of it.
+      auto boxes = [&](const PagedPiece& pc, int t) { return min(per_tile, (pc.key_hi - t * C::BN + box - 1) / box); };
+      auto page_of = [&](const PagedPiece& pc, int t) {
+        return lane < boxes(pc, t) ? a.pv.table[pc.b * a.pv.table_stride + (t * C::BN >> shift) + lane] : 0;
+      };
+      for (int i = 0; ok; ++i) {
+        PagedPiece pc;
+        int first_page = 0;
+        if (is_k) {
+          const bool more = cur.next(a, UT, seq, &pc);
+          if (more && pc.t_hi > pc.t_lo) first_page = page_of(pc, pc.t_lo);
+          for (int t = 0; t < 2; ++t) pc.n[t] = more ? tiles_of(a, pc, t) : 0;
+          if (!(ok = ring.put(i, more ? &pc : nullptr, lane, wc)) || !more) break;
+        } else {
+          const PagedPiece* p = ring.get(i, wc);
+          if (!p) break;
+          pc = *p;
+          ring.release(i);
+          if (pc.t_hi > pc.t_lo) first_page = page_of(pc, pc.t_lo);
         }
-      }
-      ++seg;
-      for (int t = pc.t_lo; t < pc.t_lo + n; ++t, ++kt) {
-        const int s = kt % C::STAGES;
-        const int next_page = t + 1 < pc.t_lo + n ? page_of(pc, t + 1) : 0;
-        if (!(ok = mbar_wait_warp(&empty[s], ((kt / C::STAGES) & 1) ^ 1, wc))) break;
-        const int nb = boxes(pc, t);
-        if (lane == 0) mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(nb * box) * 128 * C::NCHUNK);
-        __syncwarp();
-        if (lane < nb)
-          load_page(tm, &full[s], tiles + s * C::TILE_BYTES + lane * box * 128 * C::NCHUNK, a.pv,
-                    (t * C::BN & (a.pv.page_size - 1)) >> 3, page, pc.h, is_k, pol_kv);
-        __syncwarp();
-        page = next_page;
-      }
-    }
-    __syncwarp();
-    if (lane == 0 && *reinterpret_cast<volatile int*>(&bars->abort)) {
-      // Never leave a copy in flight into shared memory this CTA is about to release.
-      if (is_k && seg > 0) mbar_wait_drain(&bars->q_full, (seg - 1) & 1, a.err);
-      for (int j = max(0, kt - C::STAGES); j < kt; ++j)
-        mbar_wait_drain(&full[j % C::STAGES], (j / C::STAGES) & 1, a.err);
-    }
-    __syncwarp();
-    } else if (warp == C::MMA_WARP || C::ISSUERS == 2) {
-    // ------------------------------------------------------------ MMA issuers
-    constexpr int NT = 2 / C::ISSUERS;  // query tiles of this warp, from t0 on
-    const int t0 = warp == C::MMA_WARP ? 0 : 1;
-    constexpr uint32_t idesc_s = idesc_f16kind(E::kFmt, 128, C::BN, 0, 0);
-    constexpr uint32_t idesc_o = idesc_f16kind(PE::kFmt, 128, D, 0, 1);
-    const uint64_t q_desc = sdesc_sw128(smem_u32(smem + C::OFF_Q + t0 * C::TILE_BYTES), 16, 1024);
-    const uint64_t k_desc = sdesc_sw128(smem_u32(smem + C::OFF_K), 16, C::GROUP);
-    const uint64_t v_desc = sdesc_sw128(smem_u32(smem + C::OFF_V), 1024, C::GROUP);
-    constexpr uint32_t kTileDesc = C::TILE_BYTES >> 4;
-    auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_warp(bar, parity, wc); };
-    int kt = 0, seg = 0;
-    int cs[NT] = {}, cp[NT] = {}, co[NT] = {};  // S issued, P consumed, pieces that the tile took part in
-    int nt[NT], n = 0;
-    bool ok = true;
-    auto issue_s = [&](int u, int j) {
-      if (C::EARLY_S && cs[u] >= 1 && !(ok = wait(&bars->s_free[t0 + u], (cs[u] - 1) & 1))) return;
-      tc_fence_after();
-      if (elect_one()) {
-        const uint64_t kd = k_desc + (kt + j) % C::STAGES * kTileDesc;
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          mma_ss(tmem + C::tm_s(t0 + u), q_desc + u * kTileDesc + (((kk >> 2) * C::CHUNK_BYTES + (kk & 3) * 32) >> 4),
-                 kd + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), idesc_s, kk > 0);
-        mma_commit(&bars->s_full[t0 + u]);
-      }
-      __syncwarp();
-      ++cs[u];
-    };
-    auto want_k = [&](int j) { return ok = wait(&bars->k_full[(kt + j) % C::STAGES], ((kt + j) / C::STAGES) & 1); };
-    // This warp is done with the K tile of step j (and Q after the last).
-    auto release_k = [&](int j) {
-      if (elect_one()) {
-        mma_commit(&bars->k_empty[(kt + j) % C::STAGES]);
-        if (j == n - 1) mma_commit(&bars->q_empty);
-      }
-      __syncwarp();
-    };
-    auto all_s = [&](int j) {
-      if (!want_k(j)) return;
-#pragma unroll
-      for (int u = 0; u < NT; ++u)
-        if (ok && j < nt[u]) issue_s(u, j);
-      if (ok) release_k(j);
-    };
-    for (int i = 0; ok; ++i) {
-      const PagedPiece* pc = ring.get(i, wc);
-      if (!pc) break;
-      n = max(pc->n[0], pc->n[1]);
-#pragma unroll
-      for (int u = 0; u < NT; ++u) nt[u] = pc->n[t0 + u];
-      ring.release(i);
-      if (n == 0) continue;
-      if (!(ok = wait(&bars->q_full, seg & 1))) break;
-      all_s(0);
-      for (int j = 0; ok && j < n; ++j) {
-        const int s = (kt + j) % C::STAGES;
-        if (C::EARLY_S && j + 1 < n) all_s(j + 1);
-        if (!ok || !(ok = wait(&bars->v_ready[s], ((kt + j) / C::STAGES) & 1))) break;
-        bool k_ready = false, v_released = false;
-#pragma unroll
-        for (int u = 0; u < NT; ++u) {
-          const int t = t0 + u;
-          if (!ok || j >= nt[u]) continue;
-          // The piece before has been read out of O.
-          if (j == 0 && co[u] >= 1 && !(ok = wait(&bars->o_free[t], (co[u] - 1) & 1))) continue;
-          if (!(ok = wait(&bars->p_full[t], cp[u] & 1))) continue;
-          ++cp[u];
-          const bool last = u + 1 == NT || j >= nt[NT - 1];
-          tc_fence_after();
-          if (elect_one()) {
-#pragma unroll
-            for (int kk = 0; kk < C::BN / 16; ++kk)
-              mma_ts(tmem + C::tm_o(t), tmem + C::tm_p(t) + kk * 8, v_desc + s * kTileDesc + ((kk * 2 * C::GROUP) >> 4),
-                     idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
-            if (C::EARLY_S) mma_commit(&bars->pv_done[t]);
-            if (last) mma_commit(&bars->v_empty[s]);
-            if (j + 1 == nt[u]) mma_commit(&bars->o_full[t]);
+        const int n0 = pc.n[0], n1 = pc.n[1], n = max(n0, n1);
+        if (n == 0) continue;
+        int page = first_page;
+        if (is_k) {
+          if (seg >= 1 && !(ok = mbar_wait_warp(&bars->q_empty, (seg - 1) & 1, wc))) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&bars->q_full, q_bytes * ((n0 > 0) + (n1 > 0)));
+            for (int t = 0; t < 2; ++t)
+              if ((t == 0 ? n0 : n1) > 0)
+                for (int c = 0; c < C::NCHUNK; ++c)
+                  tma_load_4d(&tm_q, &bars->q_full, smem + C::OFF_Q + t * C::TILE_BYTES + c * C::CHUNK_BYTES, c * 64, 0, pc.h,
+                              pc.s.row0 + pc.tok0 + t * TT, pol_q);
           }
-          __syncwarp();
-          v_released = last;
-          if (!C::EARLY_S && j + 1 < nt[u] && (k_ready || (k_ready = want_k(j + 1)))) issue_s(u, j + 1);
         }
-        if (ok && !v_released) {  // none of this warp's tiles takes part any more
-          if (elect_one()) mma_commit(&bars->v_empty[s]);
+        ++seg;
+        for (int t = pc.t_lo; t < pc.t_lo + n; ++t, ++kt) {
+          const int s = kt % C::STAGES;
+          const int next_page = t + 1 < pc.t_lo + n ? page_of(pc, t + 1) : 0;
+          if (!(ok = mbar_wait_warp(&empty[s], ((kt / C::STAGES) & 1) ^ 1, wc))) break;
+          const int nb = boxes(pc, t);
+          if (lane == 0) mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(nb * box) * 128 * C::NCHUNK);
           __syncwarp();
+          if (lane < nb)
+            load_page(tm, &full[s], tiles + s * C::TILE_BYTES + lane * box * 128 * C::NCHUNK, a.pv,
+                      (t * C::BN & (a.pv.page_size - 1)) >> 3, page, pc.h, is_k, pol_kv);
+          __syncwarp();
+          page = next_page;
         }
-        if (!C::EARLY_S && ok && j + 1 < n) release_k(j + 1);
       }
-      kt += n;
-      ++seg;
+      __syncwarp();
+      if (lane == 0 && *reinterpret_cast<volatile int*>(&bars->abort)) {
+        // Never leave a copy in flight into shared memory this CTA is about to release.
+        if (is_k && seg > 0) mbar_wait_drain(&bars->q_full, (seg - 1) & 1, a.err);
+        for (int j = max(0, kt - C::STAGES); j < kt; ++j)
+          mbar_wait_drain(&full[j % C::STAGES], (j / C::STAGES) & 1, a.err);
+      }
+      __syncwarp();
+    } else if (warp == C::MMA_WARP || C::ISSUERS == 2) {
+      // ------------------------------------------------------------ MMA issuers
+      constexpr int NT = 2 / C::ISSUERS;  // query tiles of this warp, from t0 on
+      const int t0 = warp == C::MMA_WARP ? 0 : 1;
+      constexpr uint32_t idesc_s = idesc_f16kind(E::kFmt, 128, C::BN, 0, 0);
+      constexpr uint32_t idesc_o = idesc_f16kind(PE::kFmt, 128, D, 0, 1);
+      const uint64_t q_desc = sdesc_sw128(smem_u32(smem + C::OFF_Q + t0 * C::TILE_BYTES), 16, 1024);
+      const uint64_t k_desc = sdesc_sw128(smem_u32(smem + C::OFF_K), 16, C::GROUP);
+      const uint64_t v_desc = sdesc_sw128(smem_u32(smem + C::OFF_V), 1024, C::GROUP);
+      constexpr uint32_t kTileDesc = C::TILE_BYTES >> 4;
+      auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_warp(bar, parity, wc); };
+      int kt = 0, seg = 0;
+      int cs[NT] = {}, cp[NT] = {}, co[NT] = {};  // S issued, P consumed, pieces that the tile took part in
+      int nt[NT], n = 0;
+      bool ok = true;
+      auto issue_s = [&](int u, int j) {
+        if (C::EARLY_S && cs[u] >= 1 && !(ok = wait(&bars->s_free[t0 + u], (cs[u] - 1) & 1))) return;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t kd = k_desc + (kt + j) % C::STAGES * kTileDesc;
 #pragma unroll
-      for (int u = 0; u < NT; ++u) co[u] += nt[u] > 0;
-    }
-    // Nothing may still read shared memory or write TMEM once the CTA tears down.
-    if (elect_one()) mma_commit(&bars->mma_done);
-    __syncwarp();
-    if (lane == 0) mbar_wait_drain(&bars->mma_done, 0, a.err);
-    __syncwarp();
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_ss(tmem + C::tm_s(t0 + u), q_desc + u * kTileDesc + (((kk >> 2) * C::CHUNK_BYTES + (kk & 3) * 32) >> 4),
+                   kd + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), idesc_s, kk > 0);
+          mma_commit(&bars->s_full[t0 + u]);
+        }
+        __syncwarp();
+        ++cs[u];
+      };
+      auto want_k = [&](int j) { return ok = wait(&bars->k_full[(kt + j) % C::STAGES], ((kt + j) / C::STAGES) & 1); };
+      // This warp is done with the K tile of step j (and Q after the last).
+      auto release_k = [&](int j) {
+        if (elect_one()) {
+          mma_commit(&bars->k_empty[(kt + j) % C::STAGES]);
+          if (j == n - 1) mma_commit(&bars->q_empty);
+        }
+        __syncwarp();
+      };
+      auto all_s = [&](int j) {
+        if (!want_k(j)) return;
+#pragma unroll
+        for (int u = 0; u < NT; ++u)
+          if (ok && j < nt[u]) issue_s(u, j);
+        if (ok) release_k(j);
+      };
+      for (int i = 0; ok; ++i) {
+        const PagedPiece* pc = ring.get(i, wc);
+        if (!pc) break;
+        n = max(pc->n[0], pc->n[1]);
+#pragma unroll
+        for (int u = 0; u < NT; ++u) nt[u] = pc->n[t0 + u];
+        ring.release(i);
+        if (n == 0) continue;
+        if (!(ok = wait(&bars->q_full, seg & 1))) break;
+        all_s(0);
+        for (int j = 0; ok && j < n; ++j) {
+          const int s = (kt + j) % C::STAGES;
+          if (C::EARLY_S && j + 1 < n) all_s(j + 1);
+          if (!ok || !(ok = wait(&bars->v_ready[s], ((kt + j) / C::STAGES) & 1))) break;
+          bool k_ready = false, v_released = false;
+#pragma unroll
+          for (int u = 0; u < NT; ++u) {
+            const int t = t0 + u;
+            if (!ok || j >= nt[u]) continue;
+            // The piece before has been read out of O.
+            if (j == 0 && co[u] >= 1 && !(ok = wait(&bars->o_free[t], (co[u] - 1) & 1))) continue;
+            if (!(ok = wait(&bars->p_full[t], cp[u] & 1))) continue;
+            ++cp[u];
+            const bool last = u + 1 == NT || j >= nt[NT - 1];
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+              for (int kk = 0; kk < C::BN / 16; ++kk)
+                mma_ts(tmem + C::tm_o(t), tmem + C::tm_p(t) + kk * 8, v_desc + s * kTileDesc + ((kk * 2 * C::GROUP) >> 4),
+                       idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
+              if (C::EARLY_S) mma_commit(&bars->pv_done[t]);
+              if (last) mma_commit(&bars->v_empty[s]);
+              if (j + 1 == nt[u]) mma_commit(&bars->o_full[t]);
+            }
+            __syncwarp();
+            v_released = last;
+            if (!C::EARLY_S && j + 1 < nt[u] && (k_ready || (k_ready = want_k(j + 1)))) issue_s(u, j + 1);
+          }
+          if (ok && !v_released) {  // none of this warp's tiles takes part any more
+            if (elect_one()) mma_commit(&bars->v_empty[s]);
+            __syncwarp();
+          }
+          if (!C::EARLY_S && ok && j + 1 < n) release_k(j + 1);
+        }
+        kt += n;
+        ++seg;
+#pragma unroll
+        for (int u = 0; u < NT; ++u) co[u] += nt[u] > 0;
+      }
+      // Nothing may still read shared memory or write TMEM once the CTA tears down.
+      if (elect_one()) mma_commit(&bars->mma_done);
+      __syncwarp();
+      if (lane == 0) mbar_wait_drain(&bars->mma_done, 0, a.err);
+      __syncwarp();
     }
   }
 

@@ -173,7 +173,7 @@ struct PagedPlan {
   int tiles;         // key tiles of the unit
   int cost;          // its fixed weight
   int row, ntok, h;  // its first packed row, tokens, key head
-  int unused;
+  int pad;           // 32 bytes
 };
 
 // x / y for x >= 0, y > 0, without the division's subroutine: it and the loads are

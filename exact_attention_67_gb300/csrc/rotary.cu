@@ -34,6 +34,8 @@
 
 #include <limits.h>
 
+#include <algorithm>
+
 namespace exattn {
 
 namespace {
@@ -156,9 +158,11 @@ __global__ void __launch_bounds__(kThreads, 5) rotary_kernel(const __grid_consta
   const int half = a.inv_freq ? a.rot >> 1 : 0;
   const int heads = a.Hq + a.Hk + (APPEND ? a.Hk : 0), HL = ROWS >> deal.tok_shift;
   const int slot = tid % S, r = tid / S;
-  const int t = deal.head_major ? r & ((1 << deal.tok_shift) - 1) : r / HL, hl = deal.head_major ? r >> deal.tok_shift : r & (HL - 1);
+  const int t = deal.head_major ? r & ((1 << deal.tok_shift) - 1) : r / HL;
+  const int hl = deal.head_major ? r >> deal.tok_shift : r & (HL - 1);
   const bool live = t < nt;
-  const unsigned row = t0 + (live ? t : 0), b = APPEND ? 0 : deal.length(row), n = APPEND ? row : row - b * deal.length.d;
+  const unsigned row = t0 + (live ? t : 0), b = APPEND ? 0 : deal.length(row);
+  const unsigned n = APPEND ? row : row - b * deal.length.d;
   auto at = [&](const Strides& st) { return (APPEND ? 0 : b * st.b) + n * st.n; };
   const int pairs0 = slot * V;
   const bool turned = pairs0 < half;
@@ -297,7 +301,8 @@ cudaError_t launch_t(const RotaryArgs& a, cudaStream_t stream) {
   constexpr int kRows = kThreads / (D / (2 * V));
   Deal deal{};
   deal.rows = a.append ? a.nt.total : static_cast<unsigned>(a.B) * a.N;
-  while ((1 << deal.tok_shift) < kMaxTok && (1 << deal.tok_shift) < kRows && deal.rows >> (deal.tok_shift + 1) >= 152 * 8) ++deal.tok_shift;
+  while ((1 << deal.tok_shift) < std::min(kMaxTok, kRows) && deal.rows >> (deal.tok_shift + 1) >= 152 * 8)
+    ++deal.tok_shift;
   deal.head_major = a.Hq > 0 ? a.sq.n < a.sq.h : a.sk.n < a.sk.h;
   deal.length = Divide(!a.append ? a.N : a.nt.each > 0 ? a.nt.each : 1);
   const unsigned grid = (deal.rows + (1u << deal.tok_shift) - 1) >> deal.tok_shift;
