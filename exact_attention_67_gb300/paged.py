@@ -96,11 +96,12 @@ def attn_rotary(q, q_out, k, k_out, positions, inv_freq, interleaved: bool = Fal
 
 
 def _rotary(q, k, positions, inv_freq, interleaved, inverse, factor, stream):
-    with on_stream(stream, q.device):
-        qo, ko = torch.empty_like(q), None if k is None else torch.empty_like(k)
-        if positions is None:
-            positions = torch.arange(q.shape[2] if q.dim() == 4 else q.shape[0], dtype=torch.int32, device=q.device)
-    status = _native().rotary(q, qo, k, ko, positions, inv_freq, interleaved, inverse, factor, stream)
+    if stream is not None:
+        with on_stream(stream, q.device):
+            return _rotary(q, k, positions, inv_freq, interleaved, inverse, factor, None)
+    if positions is None:
+        positions = torch.arange(q.shape[2] if q.dim() == 4 else q.shape[0], dtype=torch.int32, device=q.device)
+    status, qo, ko = _native().rotary_new(q, k, positions, inv_freq, interleaved, inverse, factor, None)
     if status:
         _check(status)
     return qo if k is None else (qo, ko)
@@ -198,15 +199,20 @@ def forward_paged(q, k_cache, v_cache, page_table, seqlens, cu_seqlens=None, max
         max_seqlen_q = total if cu_seqlens is not None else total // max(B, 1)
     if max_seqlen_k is None:
         max_seqlen_k = page_table.shape[1] * k_cache.shape[2]
-    watchdog_check(q.device)
     nbytes = attn_fwd_paged_workspace_size(B, Hq, k_cache.shape[1], total, max_seqlen_q, max_seqlen_k, d)
     with on_stream(stream, q.device):
+        # Polls and their events are for calls that run now: a captured one is
+        # watched by the next eager call or device_error().
+        watched = not (q.is_cuda and torch.cuda.is_current_stream_capturing())
+        if watched:
+            watchdog_check(q.device)
         o = torch.empty_like(q)
         lse = torch.empty((Hq, total), dtype=torch.float32, device=q.device)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-    attn_fwd_paged(q, k_cache, v_cache, o, lse, page_table, seqlens, cu_seqlens, max_seqlen_q, max_seqlen_k, causal,
-                   d ** -0.5 if scale is None else scale, ws, stream, window)
-    watchdog_poll(q.device, stream)
+        attn_fwd_paged(q, k_cache, v_cache, o, lse, page_table, seqlens, cu_seqlens, max_seqlen_q, max_seqlen_k, causal,
+                       d ** -0.5 if scale is None else scale, ws, None, window)
+        if watched:
+            watchdog_poll(q.device)
     return o, lse
 
 

@@ -434,6 +434,40 @@ def test_helpers_on_a_given_stream():
     assert ex.device_error() == 0
 
 
+def test_cache_steps_in_a_graph():
+    """PagedCache's append and attend captured, replayed on other tokens, with eager
+    calls before and after."""
+    import exact_attention_67_gb300 as ex
+    cache = ex.PagedCache(16, 16, 2, 2, 64)
+    seqs = [cache.add(), cache.add()]
+    freq, factor = ex.rotary_frequencies(64)
+    step = cache.extend(seqs, 30)
+    new = [randn(60, h, 64, seed=60 + h, dtype=torch.bfloat16) for h in (2, 3, 8)]
+    k, v, q = new[0], new[1][:, :2], new[2]
+
+    def run():
+        outs = []
+        for layer in range(2):
+            turned = torch.empty_like(q)
+            cache.append(layer, step, k, v, q=q, q_out=turned, inv_freq=freq, factor=factor)
+            outs.append(cache.attend(layer, step, turned))
+        return outs
+
+    run()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = run()
+    for i in range(2):
+        for x in (k, v, q):
+            x.copy_(randn(*x.shape, seed=70 + i, dtype=torch.bfloat16))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [[t.clone() for t in pair] for pair in outs]
+        for a, b in zip(got, run()):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    assert ex.device_error() == 0
+
+
 def test_attention_refusals():
     import exact_attention_67_gb300 as ex
     p = Problem([1, 1], [20, 30], 4, 2, 64, 16, torch.bfloat16)
