@@ -4,6 +4,7 @@ in the library's CUDA kernels; there is no other implementation to fall back
 to, and a missing library raises instead of degrading."""
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -541,7 +542,10 @@ class _Watch:
 
     def __init__(self, dev):
         self.word = torch.zeros(1, dtype=torch.int32, pin_memory=True)
+        self.at = self.word.data_ptr()
+        self.now = ctypes.c_uint.from_address(self.at)  # the word, read in a tenth of a tensor element's time
         self.event = None
+        self.mark = None  # the event, kept: recorded again by each poll of watchdog_step
 
 
 _watch: dict = {}
@@ -561,6 +565,29 @@ def watchdog_check(device) -> None:
             device_error()  # synchronises, clears the word
         raise ExattnError(8, "a kernel's bounded internal wait gave up; outputs of the calls since the last "
                              "check are invalid")
+
+
+def watchdog_step(device, launch) -> None:
+    """watchdog_check, ``launch()``, watchdog_poll on the current stream, for calls
+    made once a token: one poll in flight at a time (the word stays set until it is
+    read, so the next poll sees what this one would have), its event kept.  None
+    while the stream is being captured: an event recorded there cannot be asked, and
+    the next eager call or device_error() tells."""
+    w = _watch.get(device)
+    if w is None:
+        w = _watch[device] = _Watch(device)
+    with torch.cuda.device(device) if device.index != torch.cuda.current_device() else contextlib.nullcontext():
+        watched = not torch.cuda.is_current_stream_capturing() and (w.event is None or w.event.query())
+        if watched and w.now.value != 0:
+            watchdog_check(device)
+        launch()
+        if watched:
+            st = torch.cuda.current_stream(device)
+            _check(load().exattn_device_error_poll(w.at, st.cuda_stream))
+            if w.mark is None:
+                w.mark = torch.cuda.Event()
+            w.mark.record(st)
+            w.event = w.mark
 
 
 def watchdog_poll(device, stream=None) -> None:

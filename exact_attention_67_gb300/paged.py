@@ -21,7 +21,7 @@ import os
 import torch
 
 from . import build as _build
-from ._lib import _check, load, watchdog_check, watchdog_poll
+from ._lib import _check, load, watchdog_step
 
 _binding = None
 
@@ -201,18 +201,12 @@ def forward_paged(q, k_cache, v_cache, page_table, seqlens, cu_seqlens=None, max
         max_seqlen_k = page_table.shape[1] * k_cache.shape[2]
     nbytes = attn_fwd_paged_workspace_size(B, Hq, k_cache.shape[1], total, max_seqlen_q, max_seqlen_k, d)
     with on_stream(stream, q.device):
-        # Polls and their events are for calls that run now: a captured one is
-        # watched by the next eager call or device_error().
-        watched = not (q.is_cuda and torch.cuda.is_current_stream_capturing())
-        if watched:
-            watchdog_check(q.device)
         o = torch.empty_like(q)
         lse = torch.empty((Hq, total), dtype=torch.float32, device=q.device)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-        attn_fwd_paged(q, k_cache, v_cache, o, lse, page_table, seqlens, cu_seqlens, max_seqlen_q, max_seqlen_k, causal,
-                       d ** -0.5 if scale is None else scale, ws, None, window)
-        if watched:
-            watchdog_poll(q.device)
+        watchdog_step(q.device, lambda: attn_fwd_paged(
+            q, k_cache, v_cache, o, lse, page_table, seqlens, cu_seqlens, max_seqlen_q, max_seqlen_k, causal,
+            d ** -0.5 if scale is None else scale, ws, None, window))
     return o, lse
 
 

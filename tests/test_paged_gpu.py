@@ -434,6 +434,19 @@ def test_helpers_on_a_given_stream():
     assert ex.device_error() == 0
 
 
+def test_a_wait_that_gave_up_is_told():
+    """The watchdog's self-test, then a call: it raises, and the next one runs."""
+    import exact_attention_67_gb300 as ex
+    from exact_attention_67_gb300 import _lib
+    p = Problem([1, 1], [20, 30], 4, 2, 64, 16, torch.bfloat16)
+    p.run()
+    _lib.watchdog_selftest()
+    torch.cuda.synchronize()
+    with pytest.raises(ex.ExattnError):
+        p.run()
+    p.check(*p.run())
+
+
 def test_cache_steps_in_a_graph():
     """PagedCache's append and attend captured, replayed on other tokens, with eager
     calls before and after."""
