@@ -3,11 +3,12 @@
     python -m exact_attention_67_gb300.bench_rows [--iters 20]
 
 One JSON line per case: f16 inputs, the [B, N, H, d] layout, a sliding
-window, a packed variable-length batch and decode-shaped forwards.  Inputs are
+window, a packed variable-length batch, decode-shaped forwards, rotary
+positions and the paged cache (append, attention, page copies).  Inputs are
 seeded synthetic bf16/f16 N(0, 1), resident on the device; each figure is the
 mean device time of ``iters`` back-to-back calls between two CUDA events after
 three warm-up calls (the square cases move far more than L2 per call and are
-compute-bound); the decode cases run the C ABI call on preallocated buffers,
+compute-bound); the decode, rotary and paged cases run the C ABI call on preallocated buffers,
 ``iters`` calls captured once as a CUDA graph and replayed, so that the
 host's per-call work does not show in calls of a few microseconds.  FLOPs count
 only visible (query, key) pairs: 4 d per pair forward, 2.5x that backward.
@@ -20,7 +21,9 @@ import os
 
 import torch
 
-from . import attn_fwd_decode, attn_fwd_decode_workspace_size, backward, backward_varlen, forward, forward_varlen
+from . import (attn_cache_append, attn_cache_copy, attn_fwd_decode, attn_fwd_decode_workspace_size, attn_fwd_paged,
+               attn_fwd_paged_workspace_size, attn_rotary, backward, backward_varlen, forward, forward_varlen,
+               rotary_frequencies)
 from .synth import seeded_bf16
 
 DEV = torch.device("cuda:0")
@@ -132,6 +135,48 @@ def _decode(name, B, H, Nq, Nk, d, iters, hbm):
             "workspace_bytes": attn_fwd_decode_workspace_size(B, H, Nq, Nk, d)}
 
 
+def _rotary(name, B, N, Hq, Hk, d, iters, hbm):
+    q, k = (seeded_bf16((B, h, N, d), 41 + h, 1.0).to(DEV) for h in (Hq, Hk))
+    qo, ko = torch.empty_like(q), torch.empty_like(k)
+    pos = torch.arange(N, dtype=torch.int32, device=DEV)
+    freq, _ = rotary_frequencies(d)
+    t = _time_graph_ms(lambda: attn_rotary(q, qo, k, ko, pos, freq), iters)
+    nbytes = 4.0 * B * N * (Hq + Hk) * d  # read and written
+    return {"case": name, "B": B, "N": N, "Hq": Hq, "Hk": Hk, "d": d, "ms": t, "gbs": nbytes / t / 1e6,
+            "pct_hbm": nbytes / t / 1e6 / hbm * 100}
+
+
+def _paged(name, lens, new, Hq, Hk, d, ps, iters, peak, hbm):
+    """Append and attention of ``new`` tokens of sequences of the given lengths."""
+    B, width = len(lens), max(-(-n // ps) for n in lens)
+    pages = B * width
+    kc, vc = (seeded_bf16((pages, Hk, ps, d), 51 + t, 1.0).to(DEV) for t in range(2))
+    table = torch.randperm(pages, generator=torch.Generator().manual_seed(5)).to(torch.int32).view(B, width).to(DEV)
+    seq = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    total = B * new
+    q, k, v = (seeded_bf16((total, h, d), 53 + i, 1.0).to(DEV) for i, h in enumerate((Hq, Hk, Hk)))
+    qo, o, lse = torch.empty_like(q), torch.empty_like(q), torch.empty((Hq, total), dtype=torch.float32, device=DEV)
+    freq, _ = rotary_frequencies(d)
+    ws = torch.empty(attn_fwd_paged_workspace_size(B, Hq, Hk, total, new, max(lens), d), dtype=torch.uint8, device=DEV)
+    t_a = _time_graph_ms(lambda: attn_cache_append(k, v, kc, vc, table, seq, None, q, qo, freq), iters)
+    t = _time_graph_ms(lambda: attn_fwd_paged(qo, kc, vc, o, lse, table, seq, None, new, max(lens), True, d ** -0.5, ws), iters)
+    nbytes = 4.0 * sum(lens) * Hk * d + 4.0 * total * Hq * d
+    f = 4.0 * d * Hq * sum(_pairs(new, n, True, 0) for n in lens)
+    return {"case": name, "B": B, "new": new, "keys": sum(lens), "Hq": Hq, "Hk": Hk, "d": d, "page_size": ps, "append_ms": t_a,
+            "ms": t, "gbs": nbytes / t / 1e6, "pct_hbm": nbytes / t / 1e6 / hbm * 100, "tflops": f / t / 1e9,
+            "pct_peak": f / t / 1e9 / peak * 100}
+
+
+def _copy(name, slabs, pages, copies, page_bytes, iters, hbm):
+    pool = torch.zeros((slabs, pages, page_bytes), dtype=torch.uint8, device=DEV)
+    order = torch.randperm(pages, generator=torch.Generator().manual_seed(6)).to(torch.int32)
+    src, dst = order[:copies].clone(), order[copies: 2 * copies].clone()
+    t = _time_graph_ms(lambda: attn_cache_copy(pool, src, dst), iters)
+    nbytes = 2.0 * slabs * copies * page_bytes
+    return {"case": name, "slabs": slabs, "pages": pages, "copies": copies, "page_bytes": page_bytes, "ms": t,
+            "gbs": nbytes / t / 1e6, "pct_hbm": nbytes / t / 1e6 / hbm * 100}
+
+
 def main(argv=None):
     ap = argparse.ArgumentParser()
     ap.add_argument("--iters", type=int, default=20)
@@ -148,6 +193,12 @@ def main(argv=None):
         _decode("decode Nq=1", 4, 32, 1, 32768, 128, a.iters, hbm),
         _decode("decode Nq=1, one head", 1, 1, 1, 131072, 128, a.iters, hbm),
         _decode("decode Nq=16", 8, 16, 16, 16384, 128, a.iters, hbm),
+        _rotary("rotary", 1, 32768, 16, 16, 128, a.iters, hbm),
+        _paged("paged decode", [32768] * 4, 1, 32, 32, 128, 64, a.iters, peak, hbm),
+        _paged("paged decode, shared key heads, mixed lengths", [512 * (i + 1) for i in range(32)], 1, 32, 4, 128, 16,
+               a.iters, peak, hbm),
+        _paged("paged chunk", [32768], 2048, 32, 8, 128, 64, a.iters, peak, hbm),
+        _copy("page copies", 32, 4096, 1500, 32768, a.iters, hbm),
     ]
     for r in rows:
         r["peak_source"] = src
