@@ -18,10 +18,10 @@
 //   * the columns' count, rounded up, is a template argument: straight-line code;
 //   * a 128-key tile is gathered page by page: one TMA box a page for K and one
 //     for V, by two producer warps, issued by one lane each, the page numbers read
-//     one tile ahead (a box takes some 75 clocks to issue: at 16 rows a page and
-//     two boxes of 64 columns, one warp took 2,400 a tile, more than the tile's
-//     own time).  Pages past the last visible key are not read, whatever the
-//     table says there;
+//     32 boxes at a time (a box takes some 75 clocks to issue: at 16 rows a page
+//     and two boxes of 64 columns, one warp took 2,400 a tile, more than the
+//     tile's own time).  Pages past the last visible key are not read, whatever
+//     the table says there;
 //   * the stored rows behind a sequence's end, or before its window, may hold
 //     anything: scores there are replaced (not added to) by -inf, and V rows are
 //     zeroed in shared memory by the converting warps, so that 0 * NaN never meets
@@ -31,10 +31,10 @@
 //     f16's O is normalised by the sum of the rounded weights.
 // Bound by HBM on long batches: 4 sequences of 32,768 keys, 32 key heads of 128, 297
 // us (7.2 TB/s; a plain copy runs at 6.7), 48 ragged ones of up to 16,384 keys, 32
-// heads on 4, 141 us (6.5 TB/s).  Short calls are a chain of latencies: one of 777
-// keys 9.5 us (finding the place in the line 1.5, the first page number and tile
+// heads on 4, 140 us (6.6 TB/s).  Short calls are a chain of latencies: one of 777
+// keys 9.3 us (finding the place in the line 1.5, the first page number and tile
 // 1.5, its products and softmax 1.5, the merge 2.9); 16 of up to 5,000 keys with 5
-// new tokens, d = 64, 26.8 us where the bytes take 13.4.
+// new tokens, d = 64, 25.4 us where the bytes take 13.4.
 // d = 64: V^T has 64 rows and the MMA takes 128, so the second half reads the
 // shared memory behind the tile; those accumulator rows are never read.
 #include "paged.cuh"
@@ -339,34 +339,38 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
           named_bar_sync(1 + w, 128);
           if (ok) ok = done = product_done();
           if (ok) {
-            float alpha[NC];
-            bool rescale = false;
+            // A lane a column, handed round by shuffles.  This code runs a few times a
+            // unit, from a cold instruction cache, so its length is its time: written out
+            // a column it took 2,600 clocks of a unit's first tile with 16 columns.
+            const int c = lane & (NC - 1);
+            const float4 v = mx[c];
+            const float up = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
+            const bool first = (none >> c) & 1u, move = up > (first ? -INFINITY : kPdRescale), again = move && !first;
+            const float step = move ? up : 0.f, alpha = again ? ex2(-up) : 1.f;
+            none &= ~__ballot_sync(0xffffffffu, move);
+            const bool rescale = __any_sync(0xffffffffu, again);
 #pragma unroll
             for (int q = 0; q < NC; ++q) {
-              const float4 v = mx[q];
-              const float up = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
-              const bool first = (none >> q) & 1u;
-              const bool move = first ? up != -INFINITY : up > kPdRescale;
-              alpha[q] = 1.f;
-              if (move) {
-                if (!first) {
-                  alpha[q] = ex2(-up);
-                  l[q] *= alpha[q];
-                  if constexpr (kRounded) lr[q] *= alpha[q];
-                  rescale = true;
-                }
-                m[q] += up;
-                y[q] -= up;
-                none &= ~(1u << q);
-              }
+              const float d = __shfl_sync(0xffffffffu, step, q);
+              m[q] += d;
+              y[q] -= d;
             }
-            if (rescale && j >= 2) {
-              tc_fence_after();
-              uint32_t o[NC];
-              tmem_read<NC>(tO, o);
+            if (rescale) {
 #pragma unroll
-              for (int q = 0; q < NC; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * alpha[q]);
-              tmem_write<NC>(tO, o);
+              for (int q = 0; q < NC; ++q) {
+                const float x = __shfl_sync(0xffffffffu, alpha, q);
+                l[q] *= x;
+                if constexpr (kRounded) lr[q] *= x;
+              }
+              if (j >= 2) {
+                tc_fence_after();
+                uint32_t o[NC];
+                tmem_read<NC>(tO, o);
+#pragma unroll
+                for (int q = 0; q < NC; ++q)
+                  o[q] = __float_as_uint(__uint_as_float(o[q]) * __shfl_sync(0xffffffffu, alpha, q));
+                tmem_write<NC>(tO, o);
+              }
             }
           }
         }
@@ -461,17 +465,26 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
           tc_fence_before();
           mbar_arrive_warp(&bars->o_free[ob]);
         }
+        if (tid < D) {
+          auto value = [&](int i, const Column& c) {
+            return (c.c0 != 0.f ? __uint_as_float(o0[i]) * c.c0 : 0.f) + (c.c1 != 0.f ? __uint_as_float(o1[i]) * c.c1 : 0.f);
+          };
+          if (whole) {
 #pragma unroll
-        for (int i = 0; i < H; ++i) {
-          const int q = w * H + i;
-          if (q >= cols) break;
-          const Column c = coef[q];
-          const float val = (c.c0 != 0.f ? __uint_as_float(o0[i]) * c.c0 : 0.f) +
-                            (c.c1 != 0.f ? __uint_as_float(o1[i]) * c.c1 : 0.f);
-          if (tid < D) {
-            if (!whole) a.part_o[c.row + tid] = val;
-            else if constexpr (E::kFmt == 1) static_cast<T*>(a.o)[c.row + tid] = __float2bfloat16_rn(val);
-            else static_cast<T*>(a.o)[c.row + tid] = __float2half_rn(val);
+            for (int i = 0; i < H; ++i) {
+              const Column c = coef[w * H + i];
+              const float val = value(i, c);
+              if (w * H + i >= cols) continue;
+              if constexpr (E::kFmt == 1) static_cast<T*>(a.o)[c.row + tid] = __float2bfloat16_rn(val);
+              else static_cast<T*>(a.o)[c.row + tid] = __float2half_rn(val);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+              const Column c = coef[w * H + i];
+              const float val = value(i, c);
+              if (w * H + i < cols) a.part_o[c.row + tid] = val;
+            }
           }
         }
       }
@@ -611,31 +624,25 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
       uint8_t* tiles = smem + (is_k ? C::OFF_K : C::OFF_V);
       const int stages = is_k ? C::K_STAGES : C::V_STAGES;  // a power of two
       const uint64_t pol = l2_policy_evict_first();
-      const int shift = a.pv.page_shift, box = min(a.pv.page_size, BN), per_tile = BN / box;
+      const int box = min(a.pv.page_size, BN), per_tile = BN / box;
       const uint32_t q_bytes = static_cast<uint32_t>(UT * G) * 128 * C::NCHUNK;
       int st = 0, seg = 0;
       bool ok = true;
-      // Boxes of a tile that hold a visible key, and this lane's page of it.
-      auto boxes = [&](const PagedPiece& pc, int t) { return min(per_tile, (pc.key_hi - t * BN + box - 1) / box); };
-      auto page_of = [&](const PagedPiece& pc, int t) {
-        return lane < boxes(pc, t) ? a.pv.table[pc.b * a.pv.table_stride + (t * BN >> shift) + lane] : 0;
-      };
+      PageNumbers pages{31 - __clz(per_tile), 0, 0, 0};
       for (int i = 0; ok; ++i) {
         PagedPiece pc;
-        int first_page = 0;
         if (is_k) {
           const bool more = cur.next(a, UT, seq, &pc);
-          if (more && pc.t_hi > pc.t_lo) first_page = page_of(pc, pc.t_lo);
+          if (more && pc.t_hi > pc.t_lo) pages.start(a, pc, lane);
           if (!(ok = ring.put(i, more ? &pc : nullptr, lane, wc)) || !more) break;
         } else {
           const PagedPiece* p = ring.get(i, wc);
           if (!p) break;
           pc = *p;
           ring.release(i);
-          if (pc.t_hi > pc.t_lo) first_page = page_of(pc, pc.t_lo);
+          if (pc.t_hi > pc.t_lo) pages.start(a, pc, lane);
         }
         if (pc.t_hi == pc.t_lo) continue;
-        int page = first_page;
         if (is_k) {
           const int qb = seg % C::QBUF;
           if (seg >= C::QBUF && !(ok = mbar_wait_warp(&bars->q_empty[qb], (seg / C::QBUF - 1) & 1, wc))) break;
@@ -649,16 +656,15 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
         ++seg;
         for (int t = pc.t_lo; t < pc.t_hi; ++t, ++st) {
           const int s = st & (stages - 1);
-          const int next_page = t + 1 < pc.t_hi ? page_of(pc, t + 1) : 0;
+          const int page = pages.take(a, pc, t, lane);
           if (!(ok = mbar_wait_warp(&empty[s], (st & stages) ? 0 : 1, wc))) break;
-          const int nb = boxes(pc, t);
+          const int nb = pages.boxes(pc, t);
           if (lane == 0) mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(nb * box) * 128 * C::NCHUNK);
           __syncwarp();
           if (lane < nb)
             load_page(tm, &full[s], tiles + s * C::KV_TILE + lane * box * 128 * C::NCHUNK, a.pv,
                       (t * BN & (a.pv.page_size - 1)) >> 3, page, pc.h, is_k, pol);
           __syncwarp();
-          page = next_page;
         }
       }
       __syncwarp();

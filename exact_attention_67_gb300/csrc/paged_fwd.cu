@@ -12,7 +12,7 @@
 //   * one CTA an SM runs through its chunk of the batch's keys (paged_sched.cuh),
 //     piece after piece;
 //   * a key tile is gathered page by page: one box a page, issued by one lane
-//     each, page numbers read one tile ahead;
+//     each, page numbers read 32 boxes at a time;
 //   * stored rows before the first and behind the last visible key may hold
 //     anything: their scores are replaced by -inf, their V rows zeroed in shared
 //     memory by the converting warps (which run for f16 inputs too, to that end);
@@ -413,21 +413,16 @@ __global__ void __launch_bounds__(512, 1)
       uint8_t* tiles = smem + (is_k ? C::OFF_K : C::OFF_V);
       const uint64_t pol_kv = l2_policy_evict_last();  // re-read by every unit of the (sequence, key head)
       const uint64_t pol_q = l2_policy_evict_first();
-      const int shift = a.pv.page_shift, box = min(a.pv.page_size, C::BN), per_tile = C::BN / box;
+      const int box = min(a.pv.page_size, C::BN), per_tile = C::BN / box;
       const uint32_t q_bytes = static_cast<uint32_t>(TT * G) * 128 * C::NCHUNK;
       int kt = 0, seg = 0;  // key tiles and Qs issued
       bool ok = true;
-      // Boxes of a tile that hold a visible key, and this lane's page of it.
-      auto boxes = [&](const PagedPiece& pc, int t) { return min(per_tile, (pc.key_hi - t * C::BN + box - 1) / box); };
-      auto page_of = [&](const PagedPiece& pc, int t) {
-        return lane < boxes(pc, t) ? a.pv.table[pc.b * a.pv.table_stride + (t * C::BN >> shift) + lane] : 0;
-      };
+      PageNumbers pages{31 - __clz(per_tile), 0, 0, 0};
       for (int i = 0; ok; ++i) {
         PagedPiece pc;
-        int first_page = 0;
         if (is_k) {
           const bool more = cur.next(a, UT, seq, &pc);
-          if (more && pc.t_hi > pc.t_lo) first_page = page_of(pc, pc.t_lo);
+          if (more && pc.t_hi > pc.t_lo) pages.start(a, pc, lane);
           for (int t = 0; t < 2; ++t) pc.n[t] = more ? tiles_of(a, pc, t) : 0;
           if (!(ok = ring.put(i, more ? &pc : nullptr, lane, wc)) || !more) break;
         } else {
@@ -435,11 +430,10 @@ __global__ void __launch_bounds__(512, 1)
           if (!p) break;
           pc = *p;
           ring.release(i);
-          if (pc.t_hi > pc.t_lo) first_page = page_of(pc, pc.t_lo);
+          if (pc.t_hi > pc.t_lo) pages.start(a, pc, lane);
         }
         const int n0 = pc.n[0], n1 = pc.n[1], n = max(n0, n1);
         if (n == 0) continue;
-        int page = first_page;
         if (is_k) {
           if (seg >= 1 && !(ok = mbar_wait_warp(&bars->q_empty, (seg - 1) & 1, wc))) break;
           if (lane == 0) {
@@ -454,16 +448,15 @@ __global__ void __launch_bounds__(512, 1)
         ++seg;
         for (int t = pc.t_lo; t < pc.t_lo + n; ++t, ++kt) {
           const int s = kt % C::STAGES;
-          const int next_page = t + 1 < pc.t_lo + n ? page_of(pc, t + 1) : 0;
+          const int page = pages.take(a, pc, t, lane);
           if (!(ok = mbar_wait_warp(&empty[s], ((kt / C::STAGES) & 1) ^ 1, wc))) break;
-          const int nb = boxes(pc, t);
+          const int nb = pages.boxes(pc, t);
           if (lane == 0) mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(nb * box) * 128 * C::NCHUNK);
           __syncwarp();
           if (lane < nb)
             load_page(tm, &full[s], tiles + s * C::TILE_BYTES + lane * box * 128 * C::NCHUNK, a.pv,
                       (t * C::BN & (a.pv.page_size - 1)) >> 3, page, pc.h, is_k, pol_kv);
           __syncwarp();
-          page = next_page;
         }
       }
       __syncwarp();
