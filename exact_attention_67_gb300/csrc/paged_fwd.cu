@@ -21,7 +21,7 @@
 //     f16's O is normalised by the sum of the rounded weights.
 //
 // Bound at d = 128 by the tensor core and the shared memory that feeds it: 2,048
-// tokens at 32,768 keys, 32 heads on 8, 800 to 840 us with the box's clock (1,270 to
+// tokens at 32,768 keys, 32 heads on 8, 800 to 850 us, with the clock (1,270 to
 // 1,340 TFLOP/s, 66 to 70 % of cuBLAS's burst), 754 without any of the softmax's
 // arithmetic.  At d = 64 by the hand-offs between a tile's products and its softmax:
 // chunks of 1,500 at 9,000 keys 787 TFLOP/s, 1,030 without the arithmetic.  Short

@@ -352,8 +352,7 @@ int attn_fwd_bwd_host(int dtype, const void* q, const void* k, const void* v, co
  * the other elements are copied.  Pair i is elements (i, i + rot_dim / 2), or
  * with `interleaved` (2 i, 2 i + 1).  `inverse` turns by -a: the gradient of
  * the call with the same arguments (the map is factor times an orthogonal
- * one).  The operands of attention that the flash_attn_func example of
- * "提示词再优也救不了的性能黑洞…", 第一章, takes as given.
+ * one).
  *   q, q_out : [B, Hq, N, d] views (exattn_strides) of one 16-bit type;
  *     k, k_out : [B, Hk, N, d], or NULL with Hk = 0.  An output may be its
  *     own input (same address and strides); otherwise no output may overlap
