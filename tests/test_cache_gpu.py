@@ -32,6 +32,7 @@ CASES = [
     ([5, 3], [2, 3], 2, 1, 128, 8, 6, False, torch.bfloat16, False),   # more new tokens than length: positions below 0
     ([600, 500], [70000, 500], 4, 4, 128, 128, 20, True, torch.bfloat16, False),
     ([40, 40], [41, 99], 0, 2, 64, 64, 0, False, torch.float16, True),
+    ([4001, 3000, 1, 3002], [4001, 5000, 9, 3100], 3, 1, 64, 64, 64, False, torch.bfloat16, False),  # eight tokens a block
 ]
 
 

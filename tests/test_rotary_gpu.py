@@ -58,6 +58,9 @@ CASES = [
     (1, 50, 2, 1, 128, 24, True, torch.bfloat16, "bhnd", 2 ** 31 - 64),
     (1, 50, 7, 1, 128, 72, False, torch.float16, "bnhd", 3),
     (1, 5000, 6, 2, 128, 128, True, torch.bfloat16, "bhnd", 0),
+    # Eight tokens a block, blocks across batch entries and a part of one at the end.
+    (3, 3333, 5, 1, 64, 64, False, torch.bfloat16, "bhnd", 11),
+    (3, 3333, 2, 3, 64, 64, True, torch.float16, "bnhd", 11),
 ]
 
 
