@@ -104,6 +104,7 @@ struct PagedArgs {
   int rows;                 // rows of a piece's partial results
   int ctas;                 // grid; the work's split follows from it (paged_sched.cuh)
   int unit_cost, min_chunk;
+  int whole;                // no unit is cut: a CTA takes the units that begin in its chunk
   float* part_o;            // [ctas][2][rows][d]
   float* part_lse;          // [ctas][2][rows]
   struct PagedPlan* plan;   // [ctas]

@@ -216,13 +216,15 @@ extern "C" int attn_cache_copy(void* pool, long long slab_stride, long long page
 namespace {
 
 constexpr int kSMs = 152;
+// Key tiles of a unit that is not cut: of few units, of half the SMs' count on.
+constexpr int kWholeFew = 4, kWholeMany = 8;
 
 // How a paged attention is laid out on the GPU, from sizes alone.
 struct AttendPlan {
   int cols;  // of the decode kernel, 0: the forward kernel
   int tile_tokens, ctas, rows, unit_cost, min_chunk;
   size_t plan_bytes, lse_bytes, total_bytes;
-  double weights;  // of the line, at most
+  double units, weights;  // of the line, at most
 };
 
 AttendPlan paged_plan(int B, int Hq, int Hkv, int total, int max_q, int max_k, int d) {
@@ -240,9 +242,9 @@ AttendPlan paged_plan(int B, int Hq, int Hkv, int total, int max_q, int max_k, i
   p.min_chunk = 3;
   const int ut = p.cols ? p.tile_tokens : 2 * p.tile_tokens;
   // At most so many weights (paged_sched.cuh): units of full length.
-  const double units = static_cast<double>(Hkv) * std::min<double>(static_cast<double>(B) * ((max_q + ut - 1) / ut),
-                                                                   static_cast<double>(total) / ut + B);
-  p.weights = units * ((static_cast<double>(max_k) + 127) / 128 + p.unit_cost);
+  p.units = static_cast<double>(Hkv) * std::min<double>(static_cast<double>(B) * ((max_q + ut - 1) / ut),
+                                                        static_cast<double>(total) / ut + B);
+  p.weights = p.units * ((static_cast<double>(max_k) + 127) / 128 + p.unit_cost);
   p.ctas = static_cast<int>(std::min<double>(kSMs, std::max(1.0, std::ceil(p.weights / 2))));
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
   const size_t slots = static_cast<size_t>(p.ctas) * 2 * p.rows;
@@ -345,6 +347,17 @@ extern "C" int attn_fwd_paged(int dtype, const void* q, exattn_strides sq, const
   a.cols = plan.cols;
   a.rows = plan.rows;
   a.ctas = plan.ctas;
+  {
+    // A unit's key tiles at most.  Short units are not cut: the merge takes some 3 us, a
+    // tile 0.3 (decode) to 2.  Cut and whole: one next token at 500 keys, 8 key heads
+    // (4 tiles) 8.9 and 8.2 us, at 777 keys (7) 9.3 and 10.3; 16 sequences of 5 tokens
+    // at 1,000 keys, 128 units of 8 tiles, 15.3 and 13.0, of 12 17.9 and 16.6; prompts
+    // of 512 tokens, 32 heads on 8, 21.2 and 17.1, of 1,024 29.1 and 25.5, of 1,500 (12
+    // tiles) 40.4 and 42.3; 6 chunks under a window of 1,024 (10) 33.3 and 39.3.
+    const long long span = a.window == 0 ? a.max_k : (a.causal ? 1ll : 2ll) * a.window + 2 * plan.tile_tokens;
+    const long long tiles = std::min((a.max_k + 127ll) / 128, span / 128 + 2);
+    a.whole = tiles <= (2 * plan.units >= kSMs ? kWholeMany : kWholeFew);
+  }
   a.unit_cost = plan.unit_cost;
   a.min_chunk = plan.min_chunk;
   char* ws = static_cast<char*>(workspace);
@@ -355,5 +368,5 @@ extern "C" int attn_fwd_paged(int dtype, const void* q, exattn_strides sq, const
   a.device = dev;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if ((plan.cols ? launch_paged_decode(a, st) : launch_paged_fwd(a, st)) != cudaSuccess) return EXATTN_ERR_CUDA;
-  return launch_paged_merge(a, st) == cudaSuccess ? EXATTN_OK : EXATTN_ERR_CUDA;
+  return a.whole || launch_paged_merge(a, st) == cudaSuccess ? EXATTN_OK : EXATTN_ERR_CUDA;
 }

@@ -9,7 +9,8 @@
 // end leaves pieces: each CTA has at most one piece that continues a unit and
 // one that is continued, so two slots of partial results a CTA hold them all,
 // and the merge joins them.  The lengths stay on the device; every CTA derives the
-// line from them by itself.
+// line from them by itself.  Where the largest length allows only short units, none
+// is cut, and no merge runs.
 #pragma once
 #include "paged.cuh"
 #include "ptx.cuh"
@@ -127,7 +128,7 @@ struct PagedCursor {
       paged_keys(a, s, t0, t1, &lo, &hi);
       const int k0 = lo / kKeyTile, k1 = hi > lo ? (hi + kKeyTile - 1) / kKeyTile : k0;
       const int w = k1 - k0 + cost;
-      const int take = min(left, w - pos);
+      const int take = a.whole ? w : min(left, w - pos);
       p->s = s;
       p->b = b;
       p->h = h;
@@ -221,9 +222,9 @@ __device__ __forceinline__ PagedCursor paged_start(const PagedArgs& a, int UT, i
     // (joining pieces takes some 2 us, a tile 0.6).  Unless this leaves over a
     // quarter of the SMs out of long work.
     const int most_pieces = paged_div(a.ctas, units);
-    const int each = tiles_each <= 4 ? tiles_each : max(paged_div(tiles_each + most_pieces - 1, most_pieces), 2);
+    const int each = tiles_each <= 4 || a.whole ? tiles_each : max(paged_div(tiles_each + most_pieces - 1, most_pieces), 2);
     const int k = paged_div(tiles_each + each - 1, each);
-    if (4 * units * k >= 3 * a.ctas || each <= 4) {
+    if (4 * units * k >= 3 * a.ctas || each <= 4 || a.whole) {
       chunk = each;
       cost = k * chunk - tiles_each;  // less than a chunk: the first piece's tiles are fewer by it
       W = units * k * chunk;
@@ -271,6 +272,11 @@ __device__ __forceinline__ PagedCursor paged_start(const PagedArgs& a, int UT, i
       }
       c.pos = r;
       *seq = s;
+      if (a.whole && r > 0) {  // the CTA before has it
+        c.left -= tiles + cost - r;
+        c.pos = 0;
+        ++c.t;
+      }
       plan = PagedPlan{r, chunk, tiles, cost, s.row0 + c.t * UT, min(UT, s.n - c.t * UT), c.h, 0};
       break;
     }

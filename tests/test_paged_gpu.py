@@ -126,6 +126,12 @@ CASES = [
     ([1, 1], [300, 5000], 20, 1, 128, 64, torch.float16, True, 0),
     ([2, 2, 0], [256, 1025, 7], 30, 2, 64, 128, torch.bfloat16, True, 200),
     ([7, 2], [5, 1500], 4, 1, 128, 8, torch.bfloat16, True, 0),
+    # Units of few key tiles, that are not cut: more and fewer of them than SMs.
+    ([1] * 300, [(37 * i) % 500 for i in range(300)], 4, 2, 128, 16, torch.bfloat16, True, 0),
+    ([3] * 33, [1 + (91 * i) % 1020 for i in range(33)], 15, 5, 64, 32, torch.float16, True, 0),
+    ([1] * 90, [9000 + i for i in range(90)], 8, 2, 64, 64, torch.bfloat16, True, 300),
+    ([100, 1, 0, 333, 500], [100, 480, 12, 400, 500], 8, 2, 128, 64, torch.bfloat16, True, 0),
+    ([700] * 3, [700, 900, 1024], 8, 8, 64, 16, torch.float16, True, 0),
     # More rows: the forward kernel.
     ([17], [17], 1, 1, 64, 16, torch.bfloat16, True, 0),
     ([130, 1, 40], [400, 33, 40], 4, 1, 128, 16, torch.bfloat16, True, 0),
