@@ -32,9 +32,9 @@
 // Bound by HBM on long batches: 4 sequences of 32,768 keys, 32 key heads of 128, 297
 // us (7.2 TB/s; a plain copy runs at 6.7), 48 ragged ones of up to 16,384 keys, 32
 // heads on 4, 140 us (6.6 TB/s).  Short calls are a chain of latencies: one of 777
-// keys 9.3 us (finding the place in the line 1.5, the first page number and tile
+// keys 9.1 us (finding the place in the line 1.5, the first page number and tile
 // 1.5, its products and softmax 1.5, the merge 2.9); 16 of up to 5,000 keys with 5
-// new tokens, d = 64, 25.4 us where the bytes take 13.4.
+// new tokens, d = 64, 25.1 us where the bytes take 13.4.
 // d = 64: V^T has 64 rows and the MMA takes 128, so the second half reads the
 // shared memory behind the tile; those accumulator rows are never read.
 #include "paged.cuh"
@@ -443,8 +443,8 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
         const float le = l0 * c0 + l1 * c1;
         float lo = le;
         if constexpr (kRounded) lo = sum(2) * c0 + sum(3) * c1;
-        const float inv = lo == 0.f ? 0.f : 1.f / lo;
-        const float L = le == 0.f ? -INFINITY : (top + log2f(le)) * 0.6931471805599453f;
+        const float inv = lo == 0.f ? 0.f : sum_inverse(lo);
+        const float L = le == 0.f ? -INFINITY : (top + sum_log2(le)) * 0.6931471805599453f;
         const int t = static_cast<int>(q * gm >> 16), head = pc->h * G + q - t * G, prow = pc->s.row0 + pc->tok0 + t;
         const long long part = (static_cast<long long>(blockIdx.x) * 2 + pc->slot()) * NQ + q;
         coef[q] = Column{c0 * inv, c1 * inv, whole ? prow * a.so.n + head * a.so.h : part * D};

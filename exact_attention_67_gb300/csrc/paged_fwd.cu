@@ -312,8 +312,8 @@ __global__ void __launch_bounds__(512, 1)
       }
       const float l = kConvertV ? le : lb;
       // No visible key: 0 and -inf.  A NaN among the scores makes the sum NaN.
-      const float inv_l = l == 0.f ? 0.f : 1.f / l;
-      const float L = le == 0.f ? -INFINITY : (m_ref + log2f(le)) * 0.6931471805599453f;
+      const float inv_l = l == 0.f ? 0.f : sum_inverse(l);
+      const float L = le == 0.f ? -INFINITY : (m_ref + sum_log2(le)) * 0.6931471805599453f;
       const int row_tok = row / G, tok = t * TT + row_tok;
       const int prow = pc->s.row0 + pc->tok0 + tok, head = pc->h * G + row % G;
       const bool live = row_tok < TT && tok < pc->ntok, whole = pc->whole();

@@ -109,13 +109,13 @@ __global__ void __launch_bounds__(64 * WPR) paged_merge_kernel(const __grid_cons
 #pragma unroll
     for (int c = 0; c < V; ++c) acc[c] = fmaf(e, acc_s[warp + i][lane * V + c], acc[c]);
   }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const float inv = sum == 0.f ? 0.f : sum_inverse(sum);
   const int head = p.h * a.G + row % a.G, prow = p.row + tok;
   T* out = static_cast<T*>(a.o) + prow * a.so.n + head * a.so.h + lane * V;
 #pragma unroll
   for (int c = 0; c < V; c += 2)
     *reinterpret_cast<uint32_t*>(out + c) = Elem<T>::pack(acc[c] * inv, acc[c + 1] * inv);
-  if (lane == 0) a.lse[static_cast<long long>(head) * a.nt.total + prow] = sum == 0.f ? -INFINITY : m + logf(sum);
+  if (lane == 0) a.lse[static_cast<long long>(head) * a.nt.total + prow] = sum == 0.f ? -INFINITY : m + sum_log2(sum) * 0.6931471805599453f;
 }
 
 // The forward kernel's rows: a block takes 32 of a query tile, a lane each (their
@@ -182,13 +182,13 @@ __global__ void __launch_bounds__(128) paged_merge_rows_kernel(const __grid_cons
     }
     m = top;
   }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const float inv = sum == 0.f ? 0.f : sum_inverse(sum);
   const int head = p.h * a.G + row % a.G, prow = p.row + tok;
   T* out = static_cast<T*>(a.o) + prow * a.so.n + head * a.so.h + c0 * 4;
   *reinterpret_cast<uint4*>(out) =
       make_uint4(Elem<T>::pack(acc[0].x * inv, acc[0].y * inv), Elem<T>::pack(acc[0].z * inv, acc[0].w * inv),
                  Elem<T>::pack(acc[1].x * inv, acc[1].y * inv), Elem<T>::pack(acc[1].z * inv, acc[1].w * inv));
-  if (c0 == 0) a.lse[static_cast<long long>(head) * a.nt.total + prow] = sum == 0.f ? -INFINITY : m + logf(sum);
+  if (c0 == 0) a.lse[static_cast<long long>(head) * a.nt.total + prow] = sum == 0.f ? -INFINITY : m + sum_log2(sum) * 0.6931471805599453f;
 }
 
 template <typename T, int D>

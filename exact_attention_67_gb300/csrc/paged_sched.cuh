@@ -21,6 +21,12 @@ namespace exattn {
 
 constexpr int kKeyTile = 128;
 
+// 1 / x and log2 x of a sum of weights, to 2^-22: it is at least 1 (the weight that
+// set the reference) or NaN.  The full functions are a subroutine each at a unit's
+// end: one next token at 777 keys 9.3 us with them, 9.1 without.
+__device__ __forceinline__ float sum_inverse(float x) { return __fdividef(1.f, x); }
+__device__ __forceinline__ float sum_log2(float x) { return __log2f(x); }
+
 struct PagedSeq {
   int row0, n;  // first packed row, new tokens
   int len;      // keys
