@@ -193,6 +193,8 @@ def forward_paged(q, k_cache, v_cache, page_table, seqlens, cu_seqlens=None, max
     [Hq, total].  ``max_seqlen_q`` defaults to total / B without ``cu_seqlens`` and
     to total with them, ``max_seqlen_k`` to the table's capacity: give them where
     they are known, they size the work's split."""
+    if not q.is_cuda:
+        raise ValueError("all device operands must be CUDA tensors")
     total, Hq, d = q.shape
     B = page_table.shape[0]
     if max_seqlen_q is None:

@@ -237,3 +237,15 @@ def test_frequencies():
                 dict(slow_turns=3.0, fast_turns=3.0)):
         with pytest.raises(ValueError):
             rotary_frequencies(**{**dict(rot_dim=8, device="cpu"), **bad})
+
+
+def test_host_tensors_are_refused():
+    import exact_attention_67_gb300 as ex
+    q, kc = torch.zeros(2, 4, 64, dtype=torch.bfloat16), torch.zeros(3, 2, 16, 64, dtype=torch.bfloat16)
+    table, lens = torch.zeros(2, 1, dtype=torch.int32), torch.full((2,), 5, dtype=torch.int32)
+    freq, _ = rotary_frequencies(64, device="cpu")
+    for call in (lambda: ex.forward_paged(q, kc, kc, table, lens), lambda: ex.rotary(q, None, lens, freq),
+                 lambda: ex.attn_cache_append(q[:, :2], q[:, :2], kc, kc, table, lens),
+                 lambda: ex.attn_cache_copy(kc[None], [0], [1])):
+        with pytest.raises(ValueError):
+            call()
