@@ -34,7 +34,7 @@
 // heads on 4, 140 us (6.6 TB/s).  Short calls are a chain of latencies: one of 777
 // keys 9.1 us (finding the place in the line 1.5, the first page number and tile
 // 1.5, its products and softmax 1.5, the merge 2.9); 16 of up to 5,000 keys with 5
-// new tokens, d = 64, 25.1 us where the bytes take 13.4.
+// new tokens, d = 64, 24.7 us where the bytes take 13.4.
 // d = 64: V^T has 64 rows and the MMA takes 128, so the second half reads the
 // shared memory behind the tile; those accumulator rows are never read.
 #include "paged.cuh"
@@ -58,9 +58,12 @@ struct PdCfg {
   static constexpr int QBUF = NC == 32 ? 1 : 2;  // Q tiles in shared memory
   static constexpr int P_CHUNK = NQ * 128;
   static constexpr int P_TILE = 2 * P_CHUNK;
-  // 192 KB of K and V.  A V tile is held longer (converted, and until its weights
-  // are there): some 3,500 clocks from its load against 1,800.
-  static constexpr int K_STAGES = D == 128 ? 2 : 4, V_STAGES = 2 * K_STAGES;
+  // At d = 128 192 KB of K and V: a V tile is held longer (converted, and until its
+  // weights are there), some 3,500 clocks from its load against 1,800; four K and two
+  // V stages 312.7 us for 4 sequences of 32,768 keys, 32 heads, these 295.9.  At d = 64
+  // eight V stages are a little worse than four: 16 sequences of up to 5,000 keys 25.0
+  // us against 24.7, of up to 20,000 63.2 against 62.4.
+  static constexpr int K_STAGES = D == 128 ? 2 : 4, V_STAGES = 4;
   // V before K: the 128-row read of a 64-wide V tile stays inside the buffers.
   static constexpr int OFF_V = 0;
   static constexpr int OFF_K = OFF_V + V_STAGES * KV_TILE;
