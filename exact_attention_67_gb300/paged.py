@@ -108,53 +108,75 @@ def _rotary(q, k, positions, inv_freq, interleaved, inverse, factor, stream):
 
 
 class _Rotary(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, q, k, positions, inv_freq, interleaved, factor):
-        ctx.save_for_backward(positions, inv_freq)
-        ctx.how = (interleaved, factor)
-        return _rotary(q, k, positions, inv_freq, interleaved, False, factor, None)
+    """The rotation, and with ``inverse`` its gradient.  It is linear, so forward
+    mode is the same call on the tangents, reverse mode the other one on the
+    gradients, to any order."""
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
+    def forward(ctx, q, k, positions, inv_freq, interleaved, inverse, factor):
+        ctx.save_for_backward(positions, inv_freq)
+        ctx.save_for_forward(positions, inv_freq)
+        ctx.how = (interleaved, inverse, factor)
+        return _rotary(q, k, positions, inv_freq, interleaved, inverse, factor, None)
+
+    @staticmethod
+    def jvp(ctx, tq, tk, *_):
+        positions, inv_freq = ctx.saved_tensors
+        interleaved, inverse, factor = ctx.how
+        return _turn(_read(tq), _read(tk), positions, inv_freq, interleaved, inverse, factor, None)
+
+    @staticmethod
     def backward(ctx, dq, dk=None):
         positions, inv_freq = ctx.saved_tensors
-        # As for attention: gradients the library cannot read in place (expanded,
-        # oddly strided, misaligned) are made contiguous first.
-        dq, dk = (g if g is None or _readable(g) else g.contiguous() for g in (dq, dk))
-        got = _rotary(dq, dk, positions, inv_freq, ctx.how[0], True, ctx.how[1], None)
+        interleaved, inverse, factor = ctx.how
+        got = _turn(_read(dq), _read(dk), positions, inv_freq, interleaved, not inverse, factor, None)
         dq, dk = (got, None) if dk is None else got
-        return dq, dk, None, None, None, None
+        return dq, dk, None, None, None, None, None
+
+
+def _read(g):
+    """As for attention: gradients the library cannot read in place (expanded,
+    oddly strided, misaligned) are made contiguous first."""
+    return g if g is None or _readable(g) else g.contiguous()
 
 
 def _readable(g) -> bool:
     return g.stride(-1) == 1 and all(s and s % 8 == 0 for s in g.stride()[:-1]) and g.data_ptr() % 16 == 0
 
 
-def rotary(q, k=None, positions=None, inv_freq=None, interleaved: bool = False, factor: float = 1.0, stream=None):
-    """Q and K (or Q alone) with rotary positions applied, differentiable in
-    both: q [B, Hq, N, d] and k [B, Hk, N, d] bf16/f16 views (any layout with d
-    contiguous), or both packed [total, H, d].  ``positions``: int32 [N] or
-    [B, N] ([total] when packed), by default 0..N-1; ``inv_freq`` and ``factor``
-    from ``rotary_frequencies`` (its defaults if not given).  The first
-    2 * len(inv_freq) elements of a head are turned, the others copied."""
+def _differentiated(*tensors) -> bool:
+    """Whether automatic differentiation, in either mode, follows one of them."""
+    return any(t is not None and (t.requires_grad and torch.is_grad_enabled()
+                                  or torch.autograd.forward_ad.unpack_dual(t).tangent is not None) for t in tensors)
+
+
+def _turn(q, k, positions, inv_freq, interleaved, inverse, factor, stream):
     if inv_freq is None:
         with on_stream(stream, q.device):
             inv_freq, _ = rotary_frequencies(q.shape[-1], device=q.device)
-    if torch.is_grad_enabled() and (q.requires_grad or (k is not None and k.requires_grad)):
+    if _differentiated(q, k):
         if stream is not None:
             raise ValueError("rotary under autograd runs on the current stream: use torch.cuda.stream(...)")
-        return _Rotary.apply(q, k, positions, inv_freq, bool(interleaved), float(factor))
-    return _rotary(q, k, positions, inv_freq, interleaved, False, factor, stream)
+        return _Rotary.apply(q, k, positions, inv_freq, bool(interleaved), inverse, float(factor))
+    return _rotary(q, k, positions, inv_freq, interleaved, inverse, factor, stream)
+
+
+def rotary(q, k=None, positions=None, inv_freq=None, interleaved: bool = False, factor: float = 1.0, stream=None):
+    """Q and K (or Q alone) with rotary positions applied, differentiable in
+    both (in reverse and forward mode, to any order): q [B, Hq, N, d] and k [B, Hk, N, d]
+    bf16/f16 views (any layout with d contiguous), or both packed [total, H, d].
+    ``positions``: int32 [N] or [B, N] ([total] when packed), by default 0..N-1;
+    ``inv_freq`` and ``factor`` from ``rotary_frequencies`` (its defaults if not
+    given).  The first 2 * len(inv_freq) elements of a head are turned, the
+    others copied."""
+    return _turn(q, k, positions, inv_freq, interleaved, False, factor, stream)
 
 
 def rotary_backward(dq, dk=None, positions=None, inv_freq=None, interleaved: bool = False, factor: float = 1.0,
                     stream=None):
     """The gradient of ``rotary`` with the same arguments: from the gradients of
-    its outputs those of q and k."""
-    if inv_freq is None:
-        with on_stream(stream, dq.device):
-            inv_freq, _ = rotary_frequencies(dq.shape[-1], device=dq.device)
-    return _rotary(dq, dk, positions, inv_freq, interleaved, True, factor, stream)
+    its outputs those of q and k.  Differentiable like ``rotary``."""
+    return _turn(dq, dk, positions, inv_freq, interleaved, True, factor, stream)
 
 
 # ---------------------------------------------------------------- the cache

@@ -244,3 +244,28 @@ def test_refusals():
         ex.rotary(q, None, pos, freq, factor=0.0)
     with pytest.raises(ex.ExattnError):
         ex.rotary(q, None, pos, ex.rotary_frequencies(128)[0])  # more than a head
+
+
+@pytest.mark.parametrize("name,sign", [("rotary", 1), ("rotary_backward", -1)])
+def test_forward_mode_and_second_order(name, sign):
+    """Tangents are turned like the values, with the same bound; rotary_backward is
+    differentiable itself."""
+    import exact_attention_67_gb300 as ex
+    from torch.autograd import forward_ad
+    call = getattr(ex, name)
+    q, k, tq, tk = (inputs(2, 37, h, 64, torch.bfloat16, "bnhd", 30 + i) for i, h in enumerate((3, 1, 3, 1)))
+    freq, factor = ex.rotary_frequencies(64, yarn=2.0)
+    pos = torch.arange(37, dtype=torch.int32, device=DEV) + 9
+    fr, p = freq.cpu().numpy(), pos.cpu().numpy()
+    with forward_ad.dual_level():
+        out = call(forward_ad.make_dual(q, tq), forward_ad.make_dual(k, tk), pos, freq, True, factor)
+        for o, x, t in zip(out, (q, k), (tq, tk)):
+            got = forward_ad.unpack_dual(o)
+            check(got.primal, *turned(f64(x), p, fr, factor, True, sign), torch.bfloat16)
+            check(got.tangent, *turned(f64(t), p, fr, factor, True, sign), torch.bfloat16)
+    q.requires_grad_()
+    g = tq.clone().requires_grad_()
+    dq, = torch.autograd.grad(call(q, None, pos, freq, True, factor), q, g, create_graph=True)
+    check(dq, *turned(f64(tq), p, fr, factor, True, -sign), torch.bfloat16)
+    back, = torch.autograd.grad(dq, g, q.detach())
+    check(back, *turned(f64(q), p, fr, factor, True, sign), torch.bfloat16)
