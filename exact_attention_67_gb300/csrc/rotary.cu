@@ -108,7 +108,8 @@ struct Token {
 };
 
 // frac(f / 2 pi) in 64-bit fixed point, by integers alone: FP64 units are few.
-// f = m 2^e with m below 2^53; C is 1 / 2 pi in double precision, as an integer.
+// f = m 2^e, finite, with m below 2^53; C is 1 / 2 pi in double precision, as an
+// integer.
 __device__ __forceinline__ unsigned long long turns_of(double f) {
   constexpr unsigned long long C = static_cast<unsigned long long>(0.15915494309189535 * 73786976294838206464.0);  // 2^66
   const long long bits = __double_as_longlong(f);
@@ -142,6 +143,7 @@ __global__ void __launch_bounds__(kThreads, 5) rotary_kernel(const __grid_consta
   constexpr int Q = V < 4 ? V : 4;  // angles a vector load
   __shared__ alignas(16) float cos_s[kMaxTok * (D / 2)], sin_s[kMaxTok * (D / 2)];
   __shared__ unsigned long long turns_s[D / 2];
+  __shared__ float factor_s[D / 2];  // of a pair's cos and sin: NaN where its frequency is not finite
   __shared__ Token tk[kMaxTok];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -186,7 +188,11 @@ __global__ void __launch_bounds__(kThreads, 5) rotary_kernel(const __grid_consta
   I x;
   load(hl, x);
 
-  for (int f = tid; f < half; f += kThreads) turns_s[f] = turns_of(a.inv_freq[f]);
+  for (int f = tid; f < half; f += kThreads) {
+    const double freq = a.inv_freq[f];
+    turns_s[f] = turns_of(freq);
+    factor_s[f] = isfinite(freq) ? a.factor : __int_as_float(0x7fffffff);
+  }
   // Each token by one warp (kMaxTok <= warps).
   if (warp < nt) {
     const unsigned t = t0 + warp;
@@ -235,8 +241,8 @@ __global__ void __launch_bounds__(kThreads, 5) rotary_kernel(const __grid_consta
     // Runs of Q angles of neighbouring items side by side: the items' vector
     // loads below then meet no bank twice.
     const int at = tt * (D / 2) + f % V / Q * (S * Q) + f / V * Q + f % Q;
-    cos_s[at] = c * a.factor;
-    sin_s[at] = (a.inverse ? -s : s) * a.factor;
+    cos_s[at] = c * factor_s[f];
+    sin_s[at] = (a.inverse ? -s : s) * factor_s[f];
   }
   __syncthreads();
   if (!live) return;

@@ -362,6 +362,7 @@ int attn_fwd_bwd_host(int dtype, const void* q, const void* k, const void* v, co
  *     any int32, negative ones included.
  *   inv_freq  : device fp64 [rot_dim / 2], radians a token.  Angles are
  *     reduced exactly in fixed point, so far positions lose nothing.
+ *     The pairs of a frequency that is not finite become NaN.
  *   rot_dim   : even, 2..d; factor finite and positive.
  * Products in fp32, rounded once to the output's type.  B N < 2^31, 1 <= Hq,
  * Hk <= 65536; a rot_dim out of range returns EXATTN_ERR_UNSUPPORTED, a

@@ -269,3 +269,29 @@ def test_forward_mode_and_second_order(name, sign):
     check(dq, *turned(f64(tq), p, fr, factor, True, -sign), torch.bfloat16)
     back, = torch.autograd.grad(dq, g, q.detach())
     check(back, *turned(f64(q), p, fr, factor, True, sign), torch.bfloat16)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_frequencies_that_are_not_finite(interleaved):
+    """Their pairs are NaN, as by the formula, position 0 among them; the others are
+    what they are without them."""
+    import exact_attention_67_gb300 as ex
+    q = inputs(1, 40, 3, 64, torch.bfloat16, "bhnd", 41)
+    freq, _ = ex.rotary_frequencies(64)
+    pos = torch.arange(40, dtype=torch.int32, device=DEV)
+    want = ex.rotary(q, None, pos, freq, interleaved)
+    for at, bad in ((0, float("nan")), (7, float("inf")), (31, -float("inf"))):
+        f = freq.clone()
+        f[at] = bad
+        hit = torch.zeros(64, dtype=torch.bool, device=DEV)
+        hit[[2 * at, 2 * at + 1] if interleaved else [at, at + 32]] = True
+        for y in (ex.rotary(q, None, pos, f, interleaved), ex.rotary_backward(q, None, pos, f, interleaved)):
+            assert bool(torch.isnan(y[..., hit]).all()) and not bool(torch.isnan(y[..., ~hit]).any())
+        assert torch.equal(ex.rotary(q, None, pos, f, interleaved)[..., ~hit], want[..., ~hit])
+        pages = torch.zeros(2, 40, 1, 8, 64, dtype=torch.bfloat16, device=DEV)
+        table = torch.arange(5, dtype=torch.int32, device=DEV)[None]
+        k = q[0, :1].transpose(0, 1).contiguous()
+        ex.attn_cache_append(k, k, pages[0], pages[1], table, torch.tensor([40], dtype=torch.int32, device=DEV), inv_freq=f,
+                             interleaved=interleaved)
+        stored = pages[0, :5, 0].reshape(40, 64)
+        assert bool(torch.isnan(stored[:, hit]).all()) and torch.equal(stored[:, ~hit], want[0, 0][:, ~hit])
