@@ -27,8 +27,8 @@
 //     zeroed in shared memory by the converting warps, so that 0 * NaN never meets
 //     an accumulator;
 //   * the logsumexp comes from a sum of the unrounded weights, and so does
-//     bf16's O (P's f16 rounding, 2^-11 of a weight, is far below the output's);
-//     f16's O is normalised by the sum of the rounded weights.
+//     bf16's O (P's f16 rounding, 2^-11 of a weight or 2^-32 of the row's largest, is
+//     far below the output's); f16's O is normalised by the sum of the rounded weights.
 // Bound by HBM on long batches: 4 sequences of 32,768 keys, 32 key heads of 128, 297
 // us (7.2 TB/s; a plain copy runs at 6.7), 48 ragged ones of up to 16,384 keys, 32
 // heads on 4, 140 us (6.6 TB/s).  Short calls are a chain of latencies: one of 777
@@ -104,8 +104,6 @@ struct alignas(16) Column {
   float c0, c1;
   long long row;  // element offset
 };
-
-constexpr float kPdRescale = 8.0f;  // log2 units a column's maximum may outgrow its reference
 
 __device__ __forceinline__ uint32_t pd_bf16x2_to_f16x2(uint32_t w) {
   return pack_f16x2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
@@ -289,14 +287,14 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
       const uint32_t tO = tmem + lane_bits + C::TM_O + (ob * 2 + w) * NQ;
       const uint32_t all = cols < 32 ? (1u << cols) - 1 : ~0u;
       uint32_t none = all;  // columns that have seen no key: their reference is 0 so far
-      float m[NC], l[NC], lr[kRounded ? NC : 1];
+      float m[NC], l[NC], lr[kRounded ? NC : 1];  // references, kLift subtracted; sums of weights
 #pragma unroll
       for (int q = 0; q < NC; ++q) m[q] = l[q] = 0.f;
 #pragma unroll
       for (int q = 0; q < (kRounded ? NC : 1); ++q) lr[q] = 0.f;
       for (int j = (st ^ w) & 1; j < n; j += 2) {
         const int s = st + j;
-        float y[NC];  // scores above the column's reference, log2 units
+        float y[NC];  // scores above the column's reference, log2 units (kLift at the reference)
         bool need = none != 0;
         if (ok) ok = mbar_wait_warp(&bars->s_full[s & 3], (s >> 2) & 1, wc);
         if (ok) {
@@ -325,7 +323,7 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
               if (q < lo || q >= hi) y[q] = -INFINITY;
           }
 #pragma unroll
-          for (int q = 0; q < NC; ++q) need |= y[q] > kPdRescale;
+          for (int q = 0; q < NC; ++q) need |= y[q] > kRescale + kLift;
         } else {
           need = false;
         }
@@ -348,8 +346,8 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
             const int c = lane & (NC - 1);
             const float4 v = mx[c];
             const float up = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
-            const bool first = (none >> c) & 1u, move = up > (first ? -INFINITY : kPdRescale), again = move && !first;
-            const float step = move ? up : 0.f, alpha = again ? ex2(-up) : 1.f;
+            const bool first = (none >> c) & 1u, move = up > (first ? -INFINITY : kRescale + kLift), again = move && !first;
+            const float step = move ? up - kLift : 0.f, alpha = again ? ex2(-step) : 1.f;
             none &= ~__ballot_sync(0xffffffffu, move);
             const bool rescale = __any_sync(0xffffffffu, again);
 #pragma unroll

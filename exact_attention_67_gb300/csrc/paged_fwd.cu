@@ -17,8 +17,9 @@
 //     anything: their scores are replaced by -inf, their V rows zeroed in shared
 //     memory by the converting warps (which run for f16 inputs too, to that end);
 //   * the logsumexp is formed from the unrounded weights.  So is bf16's O: the
-//     f16 rounding of P (2^-12 of a weight at most) is far below the output's.
-//     f16's O is normalised by the sum of the rounded weights.
+//     f16 rounding of P (2^-11 of a weight, or 2^-32 of the row's largest, kLift in
+//     paged_sched.cuh) is far below the output's.  f16's O is normalised by the sum
+//     of the rounded weights.
 //
 // Bound at d = 128 by the tensor core and the shared memory that feeds it: 2,048
 // tokens at 32,768 keys, 32 heads on 8, 800 to 850 us, with the clock (1,270 to
@@ -83,8 +84,6 @@ struct PfBars {
   uint32_t tmem_base;
   int abort;
 };
-
-constexpr float kPfRescale = 8.0f;
 
 __device__ __forceinline__ uint32_t pf_bf16x2_to_f16x2(uint32_t w) {
   return pack_f16x2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
@@ -246,14 +245,14 @@ __global__ void __launch_bounds__(512, 1)
         if (j == 0) {
           m_ref = m_new;
         } else {
-          const bool need = m_new > m_ref + kPfRescale;
+          const bool need = m_new > m_ref + kRescale;
           rescale_warp = __any_sync(0xffffffffu, need);
           if (need) {
             alpha = ex2(m_ref - m_new);
             m_ref = m_new;
           }
         }
-        const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;
+        const float neg_m = m_ref == -INFINITY ? 0.f : kLift - m_ref;
         const float2 sc2 = make_float2(a.scale_log2, a.scale_log2), nm2 = make_float2(neg_m, neg_m);
         uint32_t pk[4][16];
         float2 sum[4] = {};
@@ -313,7 +312,7 @@ __global__ void __launch_bounds__(512, 1)
       const float l = kConvertV ? le : lb;
       // No visible key: 0 and -inf.  A NaN among the scores makes the sum NaN.
       const float inv_l = l == 0.f ? 0.f : sum_inverse(l);
-      const float L = le == 0.f ? -INFINITY : (m_ref + sum_log2(le)) * 0.6931471805599453f;
+      const float L = le == 0.f ? -INFINITY : ((m_ref - kLift) + sum_log2(le)) * 0.6931471805599453f;
       const int row_tok = row / G, tok = t * TT + row_tok;
       const int prow = pc->s.row0 + pc->tok0 + tok, head = pc->h * G + row % G;
       const bool live = row_tok < TT && tok < pc->ntok, whole = pc->whole();

@@ -27,6 +27,14 @@ constexpr int kKeyTile = 128;
 __device__ __forceinline__ float sum_inverse(float x) { return __fdividef(1.f, x); }
 __device__ __forceinline__ float sum_log2(float x) { return __log2f(x); }
 
+// Weights are f16 operands of the second product, and f16 drops what is below 2^-25.
+// A row's weights are 1 at its reference and, the reference being moved once the
+// maximum is 2^kRescale above it, at most 2^kRescale; taken 2^kLift times as large
+// they still stay below f16's 65,504, and a key is dropped only 2^-32 below the row's
+// largest weight instead of 2^-25 (one key 17.5 above 131,071 others: the others' 3 in
+// 1,000 of the mass).  Sums and O are scaled alike, the logsumexp takes it out.
+constexpr float kRescale = 8.f, kLift = 7.f;  // log2
+
 struct PagedSeq {
   int row0, n;  // first packed row, new tokens
   int len;      // keys

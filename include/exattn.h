@@ -440,7 +440,10 @@ int attn_cache_append(int dtype, const void* q, exattn_strides q_strides, void* 
  *   16-byte aligned; 0 for invalid sizes; its contents need not be kept, and
  *   calls that may run at the same time need one each).  Results do not vary
  *   from run to run.  Arithmetic as attn_fwd (V entries beyond +-65504 are not
- *   supported); lse is formed from the unrounded weights.
+ *   supported, below 2^-14 they lose bits); a key's weight is rounded to 2^-11 of
+ *   itself or 2^-32 of its row's largest, so beside one dominating key N others of
+ *   less than 2^-32 of its weight are lost to O: at most N 2^-32 max |V|.  lse is
+ *   formed from the unrounded weights.
  *   H total and the other sizes below 2^31, lengths below 2^30.
  */
 size_t attn_fwd_paged_workspace_size(int B, int Hq, int Hkv, int total, int max_seqlen_q, int max_seqlen_k, int d);

@@ -507,3 +507,32 @@ def test_attention_refusals():
             bad()
     o, lse = call(p.q[:0], p.kc, p.vc, p.table, p.seq, torch.zeros(3, dtype=torch.int32, device=DEV))
     assert o.shape[0] == 0 and lse.shape[1] == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new,G", [(1, 1), (2, 8), (40, 1)])
+@pytest.mark.parametrize("at", [0, 70000, 131071])
+def test_many_small_weights_beside_a_large_one(new, G, d, dtype, at):
+    """One key 17.5 above 131,071 others, whose weights of 2^-25.2 of the largest
+    together are 3 in 1,000 of the mass.  Its V is 0, theirs are 1: O is their mass A,
+    to the bound of this file's head with the weights' absolute rounding at 2^-32 of
+    the largest, in the product and in the sum that normalises it."""
+    import exact_attention_67_gb300 as ex
+    B, n, ps = 160, 131072, 64
+    kc, vc = torch.zeros(2, 1, ps, d, dtype=dtype, device=DEV), torch.ones(2, 1, ps, d, dtype=dtype, device=DEV)
+    kc[1, 0, at % ps, 3], vc[1, 0, at % ps] = 17.5, 0.0              # exact in both types
+    table = torch.zeros(B, n // ps, dtype=torch.int32, device=DEV)   # page 0, again and again
+    table[:, at // ps] = 1
+    q = torch.zeros(B * new, G, d, dtype=dtype, device=DEV)
+    q[..., 3] = 1.0
+    o, lse = ex.forward_paged(q, kc, vc, table, torch.full((B,), n, dtype=torch.int32, device=DEV), None, new, n, causal=False,
+                              scale=1.0)
+    torch.cuda.synchronize()
+    assert ex.device_error() == 0
+    mass = (n - 1) * np.exp(-17.5)
+    A = mass / (1 + mass)
+    bound = HALF[dtype] * A + (2.0 ** -10 + 2.0 ** -12) * A + 2 * 2.0 ** -32 * n
+    assert float((o.double() - A).abs().max()) <= bound
+    L = 17.5 + np.log1p(mass)
+    assert float((lse.double() - L).abs().max()) <= 2.0 ** -12 * (1 + L * 2.0 ** -10)
