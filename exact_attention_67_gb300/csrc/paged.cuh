@@ -106,7 +106,7 @@ struct PagedArgs {
   int unit_cost, min_chunk;
   int whole;                // no unit is cut: a CTA takes the units that begin in its chunk
   float* part_o;            // [ctas][2][rows][d]
-  float* part_lse;          // [ctas][2][rows]
+  float2* part_sum;         // [ctas][2][rows]: reference (log2 units) and sum of weights, mass = y 2^x
   struct PagedPlan* plan;   // [ctas]
   unsigned* err;
   int device;

@@ -223,7 +223,7 @@ constexpr int kWholeFew = 4, kWholeMany = 8;
 struct AttendPlan {
   int cols;  // of the decode kernel, 0: the forward kernel
   int tile_tokens, ctas, rows, unit_cost, min_chunk;
-  size_t plan_bytes, lse_bytes, total_bytes;
+  size_t plan_bytes, sum_bytes, total_bytes;
   double units, weights;  // of the line, at most
 };
 
@@ -249,8 +249,8 @@ AttendPlan paged_plan(int B, int Hq, int Hkv, int total, int max_q, int max_k, i
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
   const size_t slots = static_cast<size_t>(p.ctas) * 2 * p.rows;
   p.plan_bytes = up(static_cast<size_t>(p.ctas) * 32);  // a PagedPlan each
-  p.lse_bytes = up(slots * sizeof(float));
-  p.total_bytes = p.plan_bytes + p.lse_bytes + up(slots * d * sizeof(float));
+  p.sum_bytes = up(slots * sizeof(float2));
+  p.total_bytes = p.plan_bytes + p.sum_bytes + up(slots * d * sizeof(float));
   return p;
 }
 
@@ -362,8 +362,8 @@ extern "C" int attn_fwd_paged(int dtype, const void* q, exattn_strides sq, const
   a.min_chunk = plan.min_chunk;
   char* ws = static_cast<char*>(workspace);
   a.plan = reinterpret_cast<exattn::PagedPlan*>(ws);
-  a.part_lse = reinterpret_cast<float*>(ws + plan.plan_bytes);
-  a.part_o = reinterpret_cast<float*>(ws + plan.plan_bytes + plan.lse_bytes);
+  a.part_sum = reinterpret_cast<float2*>(ws + plan.plan_bytes);
+  a.part_o = reinterpret_cast<float*>(ws + plan.plan_bytes + plan.sum_bytes);
   a.err = err;
   a.device = dev;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -451,7 +451,7 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
         coef[q] = Column{c0 * inv, c1 * inv, whole ? prow * a.so.n + head * a.so.h : part * D};
         if (ok && q < cols) {
           if (whole) a.lse[static_cast<long long>(head) * a.nt.total + prow] = L;
-          else a.part_lse[part] = L;
+          else a.part_sum[part] = make_float2(le == 0.f ? -INFINITY : top, le);
         }
       }
       named_bar_sync(1 + w, 128);

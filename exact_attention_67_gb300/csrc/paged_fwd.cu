@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(512, 1)
       if (whole) {
         if (live) a.lse[static_cast<long long>(head) * a.nt.total + prow] = L;
       } else {
-        a.part_lse[part * 128 + row] = L;
+        a.part_sum[part * 128 + row] = make_float2(m_ref - kLift, le);
       }
     }
   } else if (warp >= C::READY_WARP) {

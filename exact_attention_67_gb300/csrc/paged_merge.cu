@@ -1,9 +1,11 @@
 // paged_merge.cu -- joins the pieces of the units of a paged attention whose
 // keys ended up on several CTAs (paged_sched.cuh), for sm_103a.
 //
-// With a piece's O_s (normalised within it) and logsumexp L_s, lse = log sum_s
-// exp(L_s) and O = sum_s exp(L_s - lse) O_s, the combination the online
-// softmax makes inside one CTA.  One block for each boundary between two
+// With a piece's O_s (normalised within it) and mass l_s 2^(m_s), m_s its reference,
+// the whole mass is M = sum_s l_s 2^(m_s) and O = sum_s l_s 2^(m_s) O_s / M, the
+// combination the online softmax makes inside one CTA.  (By the pieces' logsumexps,
+// rounded to 32 bits, a piece's weight was off by 2^-24 |lse|: 1 in 1,000 at scores of
+// 20,000.)  One block for each boundary between two
 // chunks and a few rows; the first boundary inside a unit joins that unit, any
 // other block returns at once.  Launched as a programmatic dependent of the
 // kernel that wrote the pieces.
@@ -23,7 +25,7 @@ template <typename T, int D, int WPR>
 __global__ void __launch_bounds__(64 * WPR) paged_merge_kernel(const __grid_constant__ PagedArgs a) {
   constexpr int V = D / 32;      // columns a lane
   constexpr int BATCH = 4;       // pieces a warp loads at once
-  __shared__ float2 red[2 * WPR];  // maximum, sum
+  __shared__ float2 red[2 * WPR];  // reference, mass
   __shared__ float acc_s[2 * WPR][D];
   // The next kernel of the stream may set itself up; this one waits for the pieces.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -49,16 +51,17 @@ __global__ void __launch_bounds__(64 * WPR) paged_merge_kernel(const __grid_cons
   // One pass with a running maximum, a batch of pieces' loads all at once.
   float m = -INFINITY, sum = 0.f, acc[V] = {};
   for (int i0 = part; live && i0 < pieces; i0 += BATCH * WPR) {
-    float l[BATCH], x[BATCH][V];
+    float2 l[BATCH];  // references and masses
+    float x[BATCH][V];
 #pragma unroll
     for (int u = 0; u < BATCH; ++u) {
       const int i = i0 + u * WPR;
-      l[u] = -INFINITY;
+      l[u] = make_float2(-INFINITY, 0.f);
 #pragma unroll
       for (int c = 0; c < V; ++c) x[u][c] = 0.f;
       if (i >= pieces || from(i + 1) <= from(i)) continue;
       const long long r = (static_cast<long long>(g - 1 + i) * 2 + (from(i) == 0)) * a.rows + row;
-      l[u] = a.part_lse[r];
+      l[u] = a.part_sum[r];
       const float* po = a.part_o + r * D + lane * V;
       if constexpr (V == 4) {
         const float4 y = *reinterpret_cast<const float4*>(po);
@@ -74,15 +77,15 @@ __global__ void __launch_bounds__(64 * WPR) paged_merge_kernel(const __grid_cons
     }
     float top = m;
 #pragma unroll
-    for (int u = 0; u < BATCH; ++u) top = fmaxf(top, l[u]);
+    for (int u = 0; u < BATCH; ++u) top = fmaxf(top, l[u].x);
     // (A NaN is in no maximum, but in the sums, and stays there.)
-    const float keep = m == -INFINITY ? 0.f : expf(m - top);
+    const float keep = m == -INFINITY ? 0.f : ex2(m - top);
     sum *= keep;
 #pragma unroll
     for (int c = 0; c < V; ++c) acc[c] *= keep;
 #pragma unroll
     for (int u = 0; u < BATCH; ++u) {
-      const float e = l[u] == -INFINITY ? 0.f : expf(l[u] - top);
+      const float e = l[u].y == 0.f ? 0.f : l[u].y * ex2(l[u].x - top);
       sum += e;
 #pragma unroll
       for (int c = 0; c < V; ++c) acc[c] = fmaf(e, x[u][c], acc[c]);
@@ -104,7 +107,7 @@ __global__ void __launch_bounds__(64 * WPR) paged_merge_kernel(const __grid_cons
 #pragma unroll
   for (int i = 0; i < WPR; ++i) {
     const float2 w_i = red[warp + i];
-    const float e = w_i.x == -INFINITY ? 0.f : expf(w_i.x - m);
+    const float e = w_i.x == -INFINITY ? 0.f : ex2(w_i.x - m);
     sum = fmaf(e, w_i.y, sum);
 #pragma unroll
     for (int c = 0; c < V; ++c) acc[c] = fmaf(e, acc_s[warp + i][lane * V + c], acc[c]);
@@ -115,7 +118,7 @@ __global__ void __launch_bounds__(64 * WPR) paged_merge_kernel(const __grid_cons
 #pragma unroll
   for (int c = 0; c < V; c += 2)
     *reinterpret_cast<uint32_t*>(out + c) = Elem<T>::pack(acc[c] * inv, acc[c + 1] * inv);
-  if (lane == 0) a.lse[static_cast<long long>(head) * a.nt.total + prow] = sum == 0.f ? -INFINITY : m + sum_log2(sum) * 0.6931471805599453f;
+  if (lane == 0) a.lse[static_cast<long long>(head) * a.nt.total + prow] = sum == 0.f ? -INFINITY : (m + sum_log2(sum)) * 0.6931471805599453f;
 }
 
 // The forward kernel's rows: a block takes 32 of a query tile, a lane each (their
@@ -149,31 +152,31 @@ __global__ void __launch_bounds__(128) paged_merge_rows_kernel(const __grid_cons
   for (int c = 0; c < C4; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
   float m = -INFINITY, sum = 0.f;
   for (int i0 = 0; i0 < pieces; i0 += BATCH) {
-    float l[BATCH];
+    float2 l[BATCH];
     float4 x[BATCH][C4];
 #pragma unroll
     for (int u = 0; u < BATCH; ++u) {
       const int i = i0 + u;
-      l[u] = -INFINITY;
+      l[u] = make_float2(-INFINITY, 0.f);
       if (i >= pieces || from(i + 1) <= from(i)) continue;
       const long long part = (static_cast<long long>(g - 1 + i) * 2 + (from(i) == 0)) * 2 + t;
-      l[u] = a.part_lse[part * 128 + row];
+      l[u] = a.part_sum[part * 128 + row];
       const float4* po = reinterpret_cast<const float4*>(a.part_o + part * 128 * D) + c0 * 128 + row;
 #pragma unroll
       for (int c = 0; c < C4; ++c) x[u][c] = po[c * 128];
     }
     float top = m;
 #pragma unroll
-    for (int u = 0; u < BATCH; ++u) top = fmaxf(top, l[u]);
-    const float keep = m == -INFINITY ? 0.f : expf(m - top);
+    for (int u = 0; u < BATCH; ++u) top = fmaxf(top, l[u].x);
+    const float keep = m == -INFINITY ? 0.f : ex2(m - top);
     sum *= keep;
 #pragma unroll
     for (int c = 0; c < C4; ++c)
       acc[c] = make_float4(acc[c].x * keep, acc[c].y * keep, acc[c].z * keep, acc[c].w * keep);
 #pragma unroll
     for (int u = 0; u < BATCH; ++u) {
-      if (l[u] == -INFINITY) continue;  // a piece that this row saw no key of: its O may not be written
-      const float e = expf(l[u] - top);
+      if (l[u].y == 0.f) continue;  // a piece that this row saw no key of: its O may not be written
+      const float e = l[u].y * ex2(l[u].x - top);
       sum += e;
 #pragma unroll
       for (int c = 0; c < C4; ++c)
@@ -188,7 +191,7 @@ __global__ void __launch_bounds__(128) paged_merge_rows_kernel(const __grid_cons
   *reinterpret_cast<uint4*>(out) =
       make_uint4(Elem<T>::pack(acc[0].x * inv, acc[0].y * inv), Elem<T>::pack(acc[0].z * inv, acc[0].w * inv),
                  Elem<T>::pack(acc[1].x * inv, acc[1].y * inv), Elem<T>::pack(acc[1].z * inv, acc[1].w * inv));
-  if (c0 == 0) a.lse[static_cast<long long>(head) * a.nt.total + prow] = sum == 0.f ? -INFINITY : m + sum_log2(sum) * 0.6931471805599453f;
+  if (c0 == 0) a.lse[static_cast<long long>(head) * a.nt.total + prow] = sum == 0.f ? -INFINITY : (m + sum_log2(sum)) * 0.6931471805599453f;
 }
 
 template <typename T, int D>

@@ -536,3 +536,36 @@ def test_many_small_weights_beside_a_large_one(new, G, d, dtype, at):
     assert float((o.double() - A).abs().max()) <= bound
     L = 17.5 + np.log1p(mass)
     assert float((lse.double() - L).abs().max()) <= 2.0 ** -12 * (1 + L * 2.0 ** -10)
+
+
+@pytest.mark.parametrize("new,G,n", [(1, 8, 1300), (1, 1, 3000), (4, 2, 2500), (3, 8, 1500), (40, 1, 5000), (130, 2, 3000)])
+@pytest.mark.parametrize("d,dtype", [(64, torch.float16), (128, torch.bfloat16)])
+@pytest.mark.parametrize("base", [4096, 5120, 6144, 7168])
+def test_pieces_joined_at_large_scores(new, G, n, d, dtype, base):
+    """A sequence on many SMs whose scores all lie near 64 base: exact in 32 bits, and
+    with scale = ln 2 their weights are powers of 2, exact too, so that nothing but the
+    roundings of this file's head is left -- as where no sequence is cut."""
+    import exact_attention_67_gb300 as ex
+    g = torch.Generator().manual_seed(n + base)
+    small = torch.randint(-3, 4, (n,), generator=g)
+    ps, Hk = 32, 2
+    pages = -(-n // ps)
+    kc, vc = (torch.zeros(pages, Hk, ps, d, dtype=dtype, device=DEV) for _ in range(2))
+    sign = torch.where(torch.arange(n) < n // 2, 1.0, -1.0)
+    for j0 in range(0, n, ps):
+        m = min(ps, n - j0)
+        kc[j0 // ps, :, :m, 0], kc[j0 // ps, :, :m, 1] = float(base), small[j0: j0 + m].to(dtype).to(DEV)
+        vc[j0 // ps, :, :m] = sign[j0: j0 + m, None].to(dtype).to(DEV)
+    q = torch.zeros(new, Hk * G, d, dtype=dtype, device=DEV)
+    q[..., 0], q[..., 1] = 64.0, 1.0
+    table, lens = torch.arange(pages, dtype=torch.int32, device=DEV)[None], torch.tensor([n], dtype=torch.int32, device=DEV)
+    scale = float(torch.tensor(np.log(2.0), dtype=torch.float32))
+    o, lse = ex.forward_paged(q, kc, vc, table, lens, None, new, n, causal=False, scale=scale)
+    torch.cuda.synchronize()
+    assert ex.device_error() == 0
+    w = 2.0 ** small.double()
+    want = float((w * sign).sum() / w.sum())
+    bound = HALF[dtype] * abs(want) + 2.0 ** -10 + 2.0 ** -12 + 2.0 ** -32 * n
+    assert float((o.double() - want).abs().max()) <= bound
+    L = (64.0 * base + np.log2(float(w.sum()))) * np.log(2.0)
+    assert float((lse.double() - L).abs().max()) <= 2.0 ** -23 * L + 2.0 ** -20
