@@ -11,7 +11,9 @@ The helpers (forward, backward, their varlen and decode forms, attention)
 also watch the kernels' watchdog without synchronising: each call queues a
 copy of the device's watchdog word into page-locked memory after its
 launches, and the next call raises ExattnError (EXATTN_ERR_TIMEOUT) if a
-completed copy shows that a bounded wait gave up.
+completed copy shows that a bounded wait gave up.  forward_paged, called once a
+token and layer, leaves the copy out while the stream's last one is still in
+flight, and in a captured call; :func:`watchdog_check` reads the word then.
 """
 from __future__ import annotations
 
@@ -20,7 +22,7 @@ import math
 from ._lib import (EXPORTS, ExattnError, Strides, attn_bwd, attn_bwd_d_and_dq, attn_bwd_dkdv, attn_bwd_dq, attn_bwd_ex,
                    attn_bwd_o32, attn_fwd_o32, attn_bwd_preprocess, attn_bwd_varlen, attn_bwd_workspace_size, attn_fwd, attn_fwd_decode, attn_fwd_bwd_host,
                    attn_fwd_bwd_host_workspace_size, attn_fwd_decode_workspace_size, attn_fwd_ex, attn_fwd_varlen,
-                   device_error, library_path, load, status_string, version, watchdog_check, watchdog_poll)
+                   device_error, library_path, load, status_string, version, watchdog_check, watchdog_poll, watchdog_seen)
 from .host import HostStep, fwd_bwd_from_host
 from .paged import (attn_cache_append, attn_cache_copy, attn_fwd_paged, attn_fwd_paged_workspace_size, attn_rotary,
                     forward_paged, rotary, rotary_backward, rotary_frequencies)
@@ -57,7 +59,7 @@ def forward(q, k, v, causal: bool = False, scale: float | None = None, stream=No
     import torch
     B, H, N, d = q.shape
     s = _default_scale(d) if scale is None else scale
-    watchdog_check(q.device)
+    watchdog_seen(q.device)
     o = torch.empty_like(q)
     lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
     if fp32_o:
@@ -82,7 +84,7 @@ def backward(q, k, v, o, lse, dO, causal: bool = False, scale: float | None = No
     import torch
     B, H, N, d = q.shape
     s = _default_scale(d) if scale is None else scale
-    watchdog_check(q.device)
+    watchdog_seen(q.device)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     if workspace is None:
         nbytes = attn_bwd_workspace_size(B, H, N, d, causal)
@@ -104,7 +106,7 @@ def forward_varlen(q, k, v, cu_seqlens, max_seqlen: int, causal: bool = False, s
     import torch
     total, H, d = q.shape
     s = _default_scale(d) if scale is None else scale
-    watchdog_check(q.device)
+    watchdog_seen(q.device)
     o = torch.empty_like(q)
     lse = torch.empty((H, total), dtype=torch.float32, device=q.device)
     attn_fwd_varlen(q, k, v, o, lse, cu_seqlens, max_seqlen, causal, s, stream, window)
@@ -118,7 +120,7 @@ def backward_varlen(q, k, v, o, lse, dO, cu_seqlens, max_seqlen: int, causal: bo
     import torch
     total, H, d = q.shape
     s = _default_scale(d) if scale is None else scale
-    watchdog_check(q.device)
+    watchdog_seen(q.device)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     if workspace is None:
         workspace = torch.empty(attn_bwd_workspace_size(1, H, total, d, causal), dtype=torch.uint8, device=q.device)
@@ -136,7 +138,7 @@ def forward_decode(q, k, v, causal: bool = False, scale: float | None = None, st
     s = _default_scale(d) if scale is None else scale
     o = torch.empty_like(q)
     lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
-    watchdog_check(q.device)
+    watchdog_seen(q.device)
     nbytes = attn_fwd_decode_workspace_size(B, H, Nq, Nk, d)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
     attn_fwd_decode(q, k, v, o, lse, causal, s, ws, stream, window)

@@ -8,6 +8,7 @@ import contextlib
 import ctypes
 import os
 import threading
+import time
 
 import torch
 
@@ -531,72 +532,96 @@ def device_error() -> int:
     rc = int(load().exattn_device_error())
     w = _watch.get(torch.device("cuda", torch.cuda.current_device()))
     if w is not None:
-        w.word[0] = 0
-        w.event = None
+        w.now.value = 0
+        w.unpolled = False
     return rc
 
 
 class _Watch:
-    """Per device: a page-locked word that the last poll copies the
-    watchdog word into, and an event recorded after that copy."""
+    """Per device: a page-locked word that every poll copies the watchdog word
+    into.  The watchdog word stays set until device_error reads it, so a copy
+    that finds it set is never followed by one that does not."""
 
-    def __init__(self, dev):
+    def __init__(self):
         self.word = torch.zeros(1, dtype=torch.int32, pin_memory=True)
         self.at = self.word.data_ptr()
         self.now = ctypes.c_uint.from_address(self.at)  # the word, read in a tenth of a tensor element's time
-        self.event = None
-        self.mark = None  # the event, kept: recorded again by each poll of watchdog_step
+        self.polls = {}        # stream handle -> event behind the last poll of watchdog_step there
+        self.unpolled = False  # a call went without a poll of its own since device_error
+        self.aside = None      # stream of watchdog_check's polls
 
 
 _watch: dict = {}
 
 
-def watchdog_check(device) -> None:
-    """Raise ExattnError(EXATTN_ERR_TIMEOUT) if the last completed poll on
-    ``device`` saw a bounded wait give up (then read and clear the word).
-    Never waits: a poll still in flight is checked by a later call."""
+def _watch_of(device) -> _Watch:
     w = _watch.get(device)
-    if w is None or w.event is None or not w.event.query():
+    if w is None:
+        w = _watch[device] = _Watch()
+    return w
+
+
+def watchdog_seen(device) -> None:
+    """Raise ExattnError(EXATTN_ERR_TIMEOUT) if a completed poll on ``device`` saw
+    a bounded wait give up (then read and clear the word).  Never waits: a poll
+    still in flight is seen by a later call."""
+    w = _watch.get(device)
+    if w is None or w.now.value == 0:
         return
-    if int(w.word[0]) != 0:
-        w.word[0] = 0
-        w.event = None
+    with torch.cuda.device(device):
+        device_error()  # synchronises, clears the words
+    raise ExattnError(8, "a kernel's bounded internal wait gave up; outputs of the calls since the last "
+                         "check are invalid")
+
+
+def watchdog_check(device) -> None:
+    """Raise ExattnError(EXATTN_ERR_TIMEOUT) if a bounded wait is seen to have given
+    up on ``device`` (then read and clear the word): by a completed poll, or, where
+    calls went without one (watchdog_step, captured calls), by reading the word on
+    another stream.  It waits for that 4-byte copy, a millisecond at most, and for no
+    kernel: calls that are still running are seen by a later check."""
+    w = _watch.get(device)
+    if w is not None and w.unpolled:
         with torch.cuda.device(device):
-            device_error()  # synchronises, clears the word
-        raise ExattnError(8, "a kernel's bounded internal wait gave up; outputs of the calls since the last "
-                             "check are invalid")
+            if not torch.cuda.is_current_stream_capturing():
+                if w.aside is None:
+                    w.aside = torch.cuda.Stream(device)
+                _check(load().exattn_device_error_poll(w.at, w.aside.cuda_stream))
+                done, until = w.aside.record_event(), time.perf_counter() + 1e-3
+                while not done.query() and time.perf_counter() < until:
+                    pass
+    watchdog_seen(device)
 
 
 def watchdog_step(device, launch) -> None:
-    """watchdog_check, ``launch()``, watchdog_poll on the current stream, for calls
-    made once a token: one poll in flight at a time (the word stays set until it is
-    read, so the next poll sees what this one would have), its event kept.  None
-    while the stream is being captured: an event recorded there cannot be asked, and
-    the next eager call or device_error() tells."""
-    w = _watch.get(device)
-    if w is None:
-        w = _watch[device] = _Watch(device)
+    """watchdog_seen, ``launch()``, a poll on the current stream, for calls made once
+    a token and layer.  The copy holds up the stream (4 sequences of 32,768 keys 297
+    us a call, 307 with a poll behind each), so a stream has one poll in flight at a
+    time; none is made while it is being captured.  Calls that go without one are
+    seen by the next poll, or by watchdog_check."""
+    w = _watch_of(device)
     with torch.cuda.device(device) if device.index != torch.cuda.current_device() else contextlib.nullcontext():
-        watched = not torch.cuda.is_current_stream_capturing() and (w.event is None or w.event.query())
-        if watched and w.now.value != 0:
-            watchdog_check(device)
+        if torch.cuda.is_current_stream_capturing():
+            w.unpolled = True
+            return launch()
+        watchdog_seen(device)
         launch()
-        if watched:
-            st = torch.cuda.current_stream(device)
-            _check(load().exattn_device_error_poll(w.at, st.cuda_stream))
-            if w.mark is None:
-                w.mark = torch.cuda.Event()
-            w.mark.record(st)
-            w.event = w.mark
+        st = torch.cuda.current_stream(device)
+        event = w.polls.get(st.cuda_stream)
+        if event is None:
+            event = w.polls[st.cuda_stream] = torch.cuda.Event()
+        elif not event.query():
+            w.unpolled = True
+            return
+        _check(load().exattn_device_error_poll(w.at, st.cuda_stream))
+        event.record(st)
 
 
 def watchdog_poll(device, stream=None) -> None:
     """Queue a copy of the watchdog word into page-locked memory after the
     work on ``stream`` (default: the device's current stream); a later
-    watchdog_check reads it once it has landed.  No synchronisation."""
-    w = _watch.get(device)
-    if w is None:
-        w = _watch[device] = _Watch(device)
+    watchdog_check or call reads it once it has landed.  No synchronisation."""
+    w = _watch_of(device)
     with torch.cuda.device(device):
         if stream is None:
             st = torch.cuda.current_stream(device)
@@ -604,10 +629,7 @@ def watchdog_poll(device, stream=None) -> None:
             st = torch.cuda.ExternalStream(stream, device=device)
         else:
             st = stream
-        _check(load().exattn_device_error_poll(w.word.data_ptr(), st.cuda_stream))
-        ev = torch.cuda.Event()
-        ev.record(st)
-        w.event = ev
+        _check(load().exattn_device_error_poll(w.at, st.cuda_stream))
 
 
 def watchdog_selftest(timeout_us: int = 2000, stream=None) -> None:

@@ -569,3 +569,50 @@ def test_pieces_joined_at_large_scores(new, G, n, d, dtype, base):
     assert float((o.double() - want).abs().max()) <= bound
     L = (64.0 * base + np.log2(float(w.sum()))) * np.log(2.0)
     assert float((lse.double() - L).abs().max()) <= 2.0 ** -23 * L + 2.0 ** -20
+
+
+@pytest.mark.parametrize("streams", [1, 2])
+def test_a_wait_that_gave_up_behind_an_earlier_call_is_told(streams):
+    """The stream held up, a call, then a wait that gives up and another call, on the
+    same stream or on one that is not held up: once these are done the explicit check
+    raises, whatever polls were in flight."""
+    import exact_attention_67_gb300 as ex
+    from exact_attention_67_gb300 import _lib
+    p = Problem([1, 1], [20, 30], 4, 2, 64, 16, torch.bfloat16)
+    p.run()
+
+    def call():
+        return ex.forward_paged(p.q, p.kc, p.vc, p.table, p.seq, p.cu, 1, 30)
+
+    second = torch.cuda.Stream() if streams == 2 else torch.cuda.current_stream()
+    torch.cuda._sleep(400_000_000)
+    call()
+    with torch.cuda.stream(second):
+        assert _lib.load().exattn_watchdog_selftest(2000, second.cuda_stream) == 0
+        call()
+        call()
+    second.synchronize()
+    with pytest.raises(ex.ExattnError):
+        ex.watchdog_check(DEV)
+    ex.watchdog_check(DEV)
+    assert ex.device_error() == 0
+    p.check(*p.run())
+
+
+def test_a_wait_that_gave_up_in_a_graph_is_told():
+    """A captured call takes no poll; the explicit check tells of a replay's wait."""
+    import exact_attention_67_gb300 as ex
+    from exact_attention_67_gb300 import _lib
+    p = Problem([1, 1], [20, 30], 4, 2, 64, 16, torch.bfloat16)
+    p.run()
+    ex.watchdog_check(DEV)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ex.forward_paged(p.q, p.kc, p.vc, p.table, p.seq, p.cu, 1, 30)
+        assert _lib.load().exattn_watchdog_selftest(2000, torch.cuda.current_stream().cuda_stream) == 0
+    ex.watchdog_check(DEV)
+    graph.replay()
+    torch.cuda.synchronize()
+    with pytest.raises(ex.ExattnError):
+        ex.watchdog_check(DEV)
+    p.check(*p.run())
