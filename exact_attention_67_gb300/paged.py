@@ -136,8 +136,10 @@ class _Rotary(torch.autograd.Function):
 
 def _read(g):
     """As for attention: gradients the library cannot read in place (expanded,
-    oddly strided, misaligned) are made contiguous first."""
-    return g if g is None or _readable(g) else g.contiguous()
+    oddly strided, misaligned) are copied first.  (``contiguous()`` would give back
+    a contiguous tensor at a misaligned address, or with an odd stride along an axis
+    of one.)"""
+    return g if g is None or _readable(g) else g.clone(memory_format=torch.contiguous_format)
 
 
 def _readable(g) -> bool:

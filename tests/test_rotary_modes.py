@@ -104,3 +104,37 @@ def test_second_order(native, call, inverse):
         under, = torch.autograd.grad(ty, v, w * ty.detach())
     for got in (twice, over, under):
         assert got is not None and torch.allclose(got.double(), want.double(), rtol=2 ** -8, atol=2 ** -8)
+
+
+def offset(x, by=1):
+    """The same values, contiguous, in a buffer of their own from element `by` on."""
+    flat = torch.empty(x.numel() + by, dtype=x.dtype)
+    y = flat[by:].view(x.shape)
+    assert y.is_contiguous() and y.data_ptr() % 16
+    return y.copy_(x)
+
+
+def odd_stride(x):
+    """The same values with a stride of 5 along an axis of one."""
+    y = x.as_strided(x.shape, (x.stride(0), 5, x.stride(2), x.stride(3)))
+    assert x.shape[1] == 1 and y.is_contiguous()
+    return y
+
+
+@pytest.mark.parametrize("spoil", [offset, odd_stride, lambda x: x.transpose(2, 3).contiguous().transpose(2, 3),
+                                   lambda x: x[..., :1, :].expand_as(x)])
+def test_gradients_that_cannot_be_read_in_place(native, spoil):
+    """The native call gets them aligned, d contiguous, with strides of its kind."""
+    q, g = half(2, 1, 5, 64, seed=1).requires_grad_(), half(2, 1, 5, 64, seed=2)
+    bad = spoil(g)
+    y = ex.rotary(q, None, POS, FREQ, factor=1.5)
+    native.given.clear()
+    y.backward(bad)
+    got, = native.given
+    assert got.data_ptr() % 16 == 0 and got.stride(3) == 1 and all(s % 8 == 0 for s in got.stride()[:3])
+    assert torch.equal(q.grad, turn(bad, True))
+    with forward_ad.dual_level():
+        native.given.clear()
+        out = ex.rotary(forward_ad.make_dual(q.detach(), bad), None, POS, FREQ, factor=1.5)
+        assert torch.equal(forward_ad.unpack_dual(out).tangent, turn(bad))
+        assert native.given[-1].data_ptr() % 16 == 0 and all(s % 8 == 0 for s in native.given[-1].stride()[:3])
