@@ -33,11 +33,12 @@ class _Attention(torch.autograd.Function):
         # The library reads dO through its strides (d contiguous, other strides
         # multiples of 8 elements, nonzero) from a 16-byte-aligned address: an
         # expanded, oddly strided or offset gradient (e.g. from
-        # out.sum().backward(), or a slice of a larger buffer) is made
-        # contiguous first.
+        # out.sum().backward(), or a slice of a larger buffer) is copied
+        # first (contiguous() would give back a contiguous one at a misaligned
+        # address, or with an odd stride along an axis of one).
         if (do.stride(-1) != 1 or any(s == 0 or s % 8 for s in do.stride()[:-1]) or
                 do.data_ptr() % 16 != 0):
-            do = do.contiguous()
+            do = do.clone(memory_format=torch.contiguous_format)
         if ctx.fp32_o:
             dq, dk, dv = _backward(q, k, v, None, lse, do, ctx.causal, ctx.scale, window=ctx.window, o32=o_saved)
         else:
