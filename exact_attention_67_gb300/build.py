@@ -83,24 +83,26 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
 
     cxx = os.environ.get("CXX", "g++")
     binding_obj = os.path.join(OUT_DIR, "binding.o")
-    compile_flags, link_flags = _binding_flags()
 
     def compile_binding():
+        compile_flags, link_flags = _binding_flags()
         cmd = [cxx, *compile_flags, "-c", os.path.join(CSRC, "binding.cpp"), "-o", binding_obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"{cxx} failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
+        return link_flags
 
     with cf.ThreadPoolExecutor(len(SOURCES) + 1) as ex:
         bound = ex.submit(compile_binding)
         objs = list(ex.map(compile_one, SOURCES))
-        bound.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    # The library is in place for C callers whatever becomes of the Python side.
+    link_flags = bound.result()
     tmp = BINDING + f".tmp{os.getpid()}"
     r = subprocess.run([cxx, binding_obj, "-o", tmp, *link_flags], capture_output=True, text=True)
     if r.returncode != 0:
