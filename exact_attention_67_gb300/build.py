@@ -43,8 +43,25 @@ def _deps_mtime() -> float:
     return max(os.path.getmtime(f) for f in files if os.path.isfile(f))
 
 
+def _binding_for() -> str:
+    """What the Python module is compiled against; another Python or PyTorch may lay
+    its objects out otherwise."""
+    import torch
+    return f"{sys.implementation.cache_tag} torch {torch.__version__}"
+
+
+def binding_fits() -> bool:
+    """Whether the Python module was built for this Python and PyTorch (its note of
+    them lies beside it)."""
+    try:
+        with open(BINDING + ".for") as f:
+            return f.read() == _binding_for()
+    except OSError:
+        return False
+
+
 def up_to_date() -> bool:
-    return all(os.path.exists(f) and os.path.getmtime(f) >= _deps_mtime() for f in (LIB, BINDING))
+    return all(os.path.exists(f) and os.path.getmtime(f) >= _deps_mtime() for f in (LIB, BINDING)) and binding_fits()
 
 
 def _binding_flags():
@@ -108,6 +125,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link of the binding failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING)
+    with open(BINDING + ".for", "w") as f:
+        f.write(_binding_for())
     return LIB
 
 

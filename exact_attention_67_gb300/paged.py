@@ -34,6 +34,9 @@ def _native():
         load()
         if not os.path.exists(_build.BINDING):
             raise ImportError(f"{_build.BINDING} is missing: build it with `python -m exact_attention_67_gb300.build`")
+        if not _build.binding_fits():
+            raise ImportError(f"{_build.BINDING} was built for another Python or PyTorch: build it again with "
+                              "`python -m exact_attention_67_gb300.build`")
         loader = importlib.machinery.ExtensionFileLoader("_exattn_binding", _build.BINDING)
         spec = importlib.util.spec_from_file_location("_exattn_binding", _build.BINDING, loader=loader)
         module = importlib.util.module_from_spec(spec)

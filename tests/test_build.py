@@ -46,3 +46,20 @@ def test_the_library_is_built_where_the_binding_cannot_be(out, monkeypatch):
 def test_built_once(out):
     assert not b.up_to_date()
     assert b.build() == b.LIB and os.path.exists(b.BINDING) and b.up_to_date()
+
+
+def test_another_python_or_pytorch_builds_again(out, monkeypatch):
+    import torch
+
+    from exact_attention_67_gb300 import paged
+    b.build()
+    monkeypatch.setattr(torch, "__version__", "0.0.1")
+    assert not b.up_to_date()
+    monkeypatch.setattr(paged, "_binding", None)
+    monkeypatch.setattr(paged, "load", lambda: None)
+    with pytest.raises(ImportError, match="another"):
+        paged._native()
+    b.build()
+    assert b.up_to_date()
+    os.remove(b.BINDING + ".for")
+    assert not b.up_to_date()
