@@ -18,6 +18,7 @@ from __future__ import annotations
 
 import heapq
 from dataclasses import dataclass
+from functools import cached_property
 
 import torch
 
@@ -39,6 +40,11 @@ class Step:
     cu_seqlens: torch.Tensor | None     # int32 [B + 1]; None where all have as many
     max_seqlen_q: int
     max_seqlen_k: int
+
+    @cached_property
+    def tokens(self) -> int:
+        """Rows of the packed tensors."""
+        return sum(self.new)
 
 
 class PagedCache:
@@ -208,6 +214,7 @@ class PagedCache:
                factor: float = 1.0, stream=None) -> None:
         """Store the step's K and V of one layer, [tokens, kv_heads, head_dim], K and Q
         turned to their positions with ``inv_freq`` (``attn_cache_append``)."""
+        self._rows(step, k)
         attn_cache_append(k, v, self.k_cache(layer), self.v_cache(layer), step.page_table, step.seqlens, step.cu_seqlens,
                           q, q_out, inv_freq, interleaved, factor, stream)
 
@@ -215,8 +222,16 @@ class PagedCache:
                stream=None):
         """Attention of the step's Q, [tokens, Hq, head_dim], over one layer of the
         cache: O like q and the logsumexp [Hq, tokens] (``forward_paged``)."""
+        self._rows(step, q)
         return forward_paged(q, self.k_cache(layer), self.v_cache(layer), step.page_table, step.seqlens, step.cu_seqlens,
                              step.max_seqlen_q, step.max_seqlen_k, causal, scale, stream, window)
+
+    @staticmethod
+    def _rows(step, x) -> None:
+        # Without offsets the kernels take the rows to be divided evenly: twice the
+        # tokens would be taken for two a sequence, over the one before.
+        if x.dim() != 3 or x.shape[0] != step.tokens:
+            raise ValueError(f"the step has {step.tokens} new tokens, got {tuple(x.shape)}")
 
     # ------------------------------------------------------------ the pool
     def compact(self, stream=None) -> int:

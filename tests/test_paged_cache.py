@@ -249,3 +249,28 @@ def test_host_tensors_are_refused():
                  lambda: ex.attn_cache_copy(kc[None], [0], [1])):
         with pytest.raises(ValueError):
             call()
+
+
+@pytest.mark.parametrize("new", [1, [2, 3, 0]])
+def test_other_counts_of_tokens_are_refused(monkeypatch, new):
+    """append and attend take the rows that their step has made room for, no others."""
+    from exact_attention_67_gb300 import cache as module
+    made = []
+    monkeypatch.setattr(module, "attn_cache_append", lambda k, *a: made.append(k.shape[0]))
+    monkeypatch.setattr(module, "forward_paged", lambda q, *a: made.append(q.shape[0]))
+    cache = HostCache(16, 8, 1, 2, 64, device="cpu")
+    step = cache.extend([cache.add() for _ in range(3)], new)
+    n = step.tokens
+    assert n == (3 if new == 1 else 5)
+    rows = lambda count, heads=2: torch.zeros(count, heads, 64, dtype=torch.bfloat16)  # noqa: E731
+    for count in (2 * n, n + 1, n - 1, 0):
+        with pytest.raises(ValueError, match="new tokens"):
+            cache.append(0, step, rows(count), rows(count))
+        with pytest.raises(ValueError, match="new tokens"):
+            cache.attend(0, step, rows(count, 4))
+    with pytest.raises(ValueError, match="new tokens"):
+        cache.attend(0, step, rows(n, 4)[None])
+    assert made == []
+    cache.append(0, step, rows(n), rows(n))
+    cache.attend(0, step, rows(n, 4))
+    assert made == [n, n]
