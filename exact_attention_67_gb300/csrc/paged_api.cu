@@ -180,6 +180,7 @@ extern "C" int attn_cache_copy(void* pool, long long slab_stride, long long page
   // Pages of a slab, and slabs, must not overlap (either may be the outer one).
   if ((num_pages > 1 && page_stride < page_bytes) || (slabs > 1 && slab_stride < page_bytes)) return EXATTN_ERR_SHAPE;
   if (page_stride >= (1ll << 40) || slab_stride >= (1ll << 44)) return EXATTN_ERR_SHAPE;
+  if (page_stride > (1ll << 61) / num_pages) return EXATTN_ERR_SHAPE;  // a slab's extent below 2^62
   if (num_pages > 1 && slabs > 1 && slab_stride < page_stride * (num_pages - 1) + page_bytes &&
       page_stride < slab_stride * (slabs - 1) + page_bytes)
     return EXATTN_ERR_SHAPE;
@@ -316,10 +317,12 @@ extern "C" int attn_fwd_paged(int dtype, const void* q, exattn_strides sq, const
     const exattn_strides& s = i == 0 ? skc : svc;
     const long long sb = num_pages > 1 ? s.b_stride : 0, sh = Hkv > 1 ? s.h_stride : 0;
     const long long step = std::max(std::gcd(sb, sh), 8ll);
-    const long long places = (num_pages - 1) * (sb / step) + (Hkv - 1) * (sh / step) + 1;
+    const long long page_step = sb / step, head_step = sh / step;
+    if (page_step >= (1ll << 31) || head_step >= (1ll << 31)) return EXATTN_ERR_SHAPE;  // the sums below: 2^62 each
+    const long long places = (num_pages - 1) * page_step + (Hkv - 1) * head_step + 1;
     if (places >= (1ll << 31)) return EXATTN_ERR_SHAPE;
-    (i == 0 ? a.pv.k_page_step : a.pv.v_page_step) = static_cast<int>(sb / step);
-    (i == 0 ? a.pv.k_head_step : a.pv.v_head_step) = static_cast<int>(sh / step);
+    (i == 0 ? a.pv.k_page_step : a.pv.v_page_step) = static_cast<int>(page_step);
+    (i == 0 ? a.pv.k_head_step : a.pv.v_head_step) = static_cast<int>(head_step);
     const cuuint64_t dims[5] = {64, 8, static_cast<cuuint64_t>(d / 64), static_cast<cuuint64_t>(page_size / 8),
                                 static_cast<cuuint64_t>(places)};
     const cuuint64_t str[4] = {static_cast<cuuint64_t>(s.n_stride) * 2, 128, static_cast<cuuint64_t>(s.n_stride) * 16,

@@ -274,3 +274,10 @@ def test_other_counts_of_tokens_are_refused(monkeypatch, new):
     cache.append(0, step, rows(n), rows(n))
     cache.attend(0, step, rows(n, 4))
     assert made == [n, n]
+
+
+def test_pools_of_impossible_extent_are_refused(lib):
+    """Page counts and strides whose product passes 64 bits."""
+    one = (ctypes.c_int * 1)(1), (ctypes.c_int * 1)(2)
+    for pages, stride in ((2 ** 31 - 1, 1 << 34), (2 ** 31 - 1, 1 << 39), (1 << 30, (1 << 34) + 16)):
+        assert lib.attn_cache_copy(P[0], 1 << 43, stride, 4096, 4, pages, *one, 1, None) == 2
