@@ -1,6 +1,6 @@
 // paged.cuh -- launch interfaces of the operators around a paged key/value
-// cache (rotary.cu, pages.cu, paged.cu) and the set-up that paged_api.cu
-// shares with api.cu.
+// cache (rotary.cu, pages.cu, paged_decode.cu, paged_fwd.cu, paged_merge.cu) and the
+// set-up that paged_api.cu shares with api.cu.
 #pragma once
 #include "kernels.cuh"
 

@@ -105,10 +105,6 @@ struct alignas(16) Column {
   long long row;  // element offset
 };
 
-__device__ __forceinline__ uint32_t pd_bf16x2_to_f16x2(uint32_t w) {
-  return pack_f16x2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-}
-
 // N columns of TMEM for this lane, loaded and waited for (the empty statement
 // keeps every use of them behind the wait, as tmem_reg_fence).
 template <int N>
@@ -516,8 +512,8 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
             for (int u = 0; u < 8; ++u) x[u] = tile[(i0 + u) * 128 + ct];
 #pragma unroll
             for (int u = 0; u < 8; ++u)
-              tile[(i0 + u) * 128 + ct] = make_uint4(pd_bf16x2_to_f16x2(x[u].x), pd_bf16x2_to_f16x2(x[u].y),
-                                                     pd_bf16x2_to_f16x2(x[u].z), pd_bf16x2_to_f16x2(x[u].w));
+              tile[(i0 + u) * 128 + ct] = make_uint4(bf16x2_to_f16x2(x[u].x), bf16x2_to_f16x2(x[u].y),
+                                                     bf16x2_to_f16x2(x[u].z), bf16x2_to_f16x2(x[u].w));
           }
         }
         if (lo > 0 || hi < BN) {

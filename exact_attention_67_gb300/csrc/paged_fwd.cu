@@ -85,10 +85,6 @@ struct PfBars {
   int abort;
 };
 
-__device__ __forceinline__ uint32_t pf_bf16x2_to_f16x2(uint32_t w) {
-  return pack_f16x2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-}
-
 // Key tiles of piece p that query tile t (tokens [tok0 + t TT, ...)) takes part
 // in, counted from p.t_lo.
 __device__ __forceinline__ int tiles_of(const PagedArgs& a, const PagedPiece& p, int t) {
@@ -385,8 +381,8 @@ __global__ void __launch_bounds__(512, 1)
             for (int u = 0; u < BATCH; ++u) x[u] = tile[(b0 + u) * 128 + ct];
 #pragma unroll
             for (int u = 0; u < BATCH; ++u)
-              tile[(b0 + u) * 128 + ct] = make_uint4(pf_bf16x2_to_f16x2(x[u].x), pf_bf16x2_to_f16x2(x[u].y),
-                                                     pf_bf16x2_to_f16x2(x[u].z), pf_bf16x2_to_f16x2(x[u].w));
+              tile[(b0 + u) * 128 + ct] = make_uint4(bf16x2_to_f16x2(x[u].x), bf16x2_to_f16x2(x[u].y),
+                                                     bf16x2_to_f16x2(x[u].z), bf16x2_to_f16x2(x[u].w));
           }
         }
         if (lo > 0 || hi < C::BN) {

@@ -35,6 +35,11 @@ __device__ __forceinline__ float sum_log2(float x) { return __log2f(x); }
 // 1,000 of the mass).  Sums and O are scaled alike, the logsumexp takes it out.
 constexpr float kRescale = 8.f, kLift = 7.f;  // log2
 
+// V enters the second product in f16.
+__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w) {
+  return pack_f16x2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
 struct PagedSeq {
   int row0, n;  // first packed row, new tokens
   int len;      // keys

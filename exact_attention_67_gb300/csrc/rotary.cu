@@ -12,9 +12,12 @@
 // only its fraction of a turn matters.  Frequencies arrive in 64 bits and are
 // taken as turns a token in 64-bit fixed point, F = frac(f / 2 pi) 2^64; then
 // p F mod 2^64 is the angle's fraction of a turn, with no range reduction, from
-// one integer product (error below |p| 2^-54 turns from the 53 bits of f, and
-// 2^-33 from keeping the upper 32 bits), which sincospi takes in 32 bits.
-// The turned values are rounded once, to the output's type.
+// one integer product, whose upper 32 bits sincospi takes as an fp32 number of half
+// turns.  Errors: |p f| 2^-53 radians from 1 / 2 pi to 53 bits; in turns |p| 2^-64 from
+// F cut off at 64 bits, 2^-32 from keeping the upper half and 2^-26 from its conversion
+// to fp32: together below |p f| 2^-53 + 2^-23 radians.  (p f formed in 64-bit floating
+// point is off by |p f| 2^-53 too.)  The turned values are rounded once, to the
+// output's type.
 //
 // A block takes a few consecutive tokens: it forms cos and sin of their rot / 2
 // angles once, in shared memory, for all heads of Q and K; a thread turns one item

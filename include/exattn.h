@@ -361,7 +361,7 @@ int attn_fwd_bwd_host(int dtype, const void* q, const void* k, const void* v, co
  *     positions[b * pos_stride + n] (pos_stride 0: the same for every batch);
  *     any int32, negative ones included.
  *   inv_freq  : device fp64 [rot_dim / 2], radians a token.  Angles are
- *     reduced exactly in fixed point, so far positions lose nothing.
+ *     reduced in 64-bit fixed point: off by |p f_i| 2^-53 + 2^-23 radians at most.
  *     The pairs of a frequency that is not finite become NaN.
  *   rot_dim   : even, 2..d; factor finite and positive.
  * Products in fp32, rounded once to the output's type.  B N < 2^31, 1 <= Hq,
