@@ -29,12 +29,12 @@
 //   * the logsumexp comes from a sum of the unrounded weights, and so does
 //     bf16's O (P's f16 rounding, 2^-11 of a weight or 2^-32 of the row's largest, is
 //     far below the output's); f16's O is normalised by the sum of the rounded weights.
-// Bound by HBM on long batches: 4 sequences of 32,768 keys, 32 key heads of 128, 297
-// us (7.2 TB/s; a plain copy runs at 6.7), 48 ragged ones of up to 16,384 keys, 32
-// heads on 4, 140 us (6.6 TB/s).  Short calls are a chain of latencies: one of 777
-// keys 9.1 us (finding the place in the line 1.5, the first page number and tile
-// 1.5, its products and softmax 1.5, the merge 2.9); 16 of up to 5,000 keys with 5
-// new tokens, d = 64, 24.7 us where the bytes take 13.4.
+// Bound by HBM on long batches: 4 sequences of 32,768 keys, 32 key heads of 128, 292
+// to 296 us (7.3 TB/s; a plain copy runs at 6.7), 48 ragged ones of up to 16,384 keys,
+// 32 heads on 4, 138 to 140 us (6.6 TB/s).  Short calls are a chain of latencies: one
+// of 777 keys 9.4 us (finding the place in the line 1.5, the first page number and tile
+// 1.5, its products and softmax 1.5, the merge 2.7); 16 of up to 5,000 keys with 5
+// new tokens, d = 64, 24.8 us where the bytes take 13.4.
 // d = 64: V^T has 64 rows and the MMA takes 128, so the second half reads the
 // shared memory behind the tile; those accumulator rows are never read.
 #include "paged.cuh"

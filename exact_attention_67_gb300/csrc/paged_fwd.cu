@@ -22,12 +22,12 @@
 //     of the rounded weights.
 //
 // Bound at d = 128 by the tensor core and the shared memory that feeds it: 2,048
-// tokens at 32,768 keys, 32 heads on 8, 800 to 850 us, with the clock (1,270 to
-// 1,340 TFLOP/s, 66 to 70 % of cuBLAS's burst), 754 without any of the softmax's
+// tokens at 32,768 keys, 32 heads on 8, 839 to 852 us, with the clock (1,250 to
+// 1,270 TFLOP/s, 65 to 66 % of cuBLAS's burst), 754 without any of the softmax's
 // arithmetic.  At d = 64 by the hand-offs between a tile's products and its softmax:
 // chunks of 1,500 at 9,000 keys 787 TFLOP/s, 1,030 without the arithmetic.  Short
 // chunks are their start, masked steps and the merge: 6 chunks of up to 600 under a
-// window of 1,024, 20 heads on 4, d = 64, 33.5 us, of which the steps are some 16.
+// window of 1,024, 20 heads on 4, d = 64, 33.0 us, of which the steps are some 16.
 #include "paged.cuh"
 #include "paged_sched.cuh"
 #include "ptx.cuh"

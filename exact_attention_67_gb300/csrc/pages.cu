@@ -7,8 +7,9 @@
 // destination occurs twice or is a source, so the copies are independent.
 //
 // Bound by HBM: a block copies 16 KB, all of its loads before its stores, past the
-// caches' reuse.  1,500 pages of 32 KB in 32 slabs 457 us (6.9 TB/s), 7 pages in 64
-// slabs 5.2 us (5.7 TB/s).
+// caches' reuse.  1,500 pages of 32 KB in 32 slabs 458 us (6.9 TB/s), 7 pages in 64
+// slabs 5.2 us (5.7 TB/s).  A smaller page leaves threads idle: 1,000 pages of 8, 4
+// and 2 KB in 64 slabs 7.0, 6.4 and 4.0 TB/s.
 #include "paged.cuh"
 
 namespace exattn {

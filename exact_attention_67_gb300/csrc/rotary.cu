@@ -27,11 +27,13 @@
 // half of an item's run), so rot a multiple of 16 moves 16-byte vectors.
 //
 // Bound by memory traffic, every element read and written once, and near it by
-// instructions: 8,192 tokens of 16 + 16 heads of 128, head-major, 23.5 us (5.7
+// instructions: 8,192 tokens of 16 + 16 heads of 128, head-major, 23.8 us (5.6
 // TB/s; a plain elementwise map of these bytes 21.3 us), 16,380 tokens of 32 + 8
-// heads of 64 28.3 us (5.9 TB/s; 26.0), 9,838 appended tokens of 32 + 8 + 8 heads
-// of 128 42.2 us (5.7 TB/s; 36.4).  Before: angles by FP64, divisions and a
-// thread's angles kept in registers 26.5, 32.5 and 46.6 us.
+// heads of 64 28.8 us (5.8 TB/s; 26.0), 9,838 appended tokens of 32 + 8 + 8 heads
+// of 128 42.5 us (5.7 TB/s; 36.4).  Before: angles by FP64, divisions and a
+// thread's angles kept in registers 26.5, 32.5 and 46.6 us.  Narrower vectors move
+// the copied part of a head, and V, too: the first case with rot 24, 20 and 6 (8, 4
+// and 2 bytes) 25.4, 32.1 and 71.0 us, the append with rot 20 and 6 53.9 and 129.7.
 #include "paged.cuh"
 #include "ptx.cuh"
 
