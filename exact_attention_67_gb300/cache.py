@@ -213,7 +213,8 @@ class PagedCache:
     def append(self, layer: int, step: Step, k, v, q=None, q_out=None, inv_freq=None, interleaved: bool = False,
                factor: float = 1.0, stream=None) -> None:
         """Store the step's K and V of one layer, [tokens, kv_heads, head_dim], K and Q
-        turned to their positions with ``inv_freq`` (``attn_cache_append``)."""
+        turned to their positions with ``inv_freq`` (``attn_cache_append``).  A step
+        with offsets may be followed by rows of no sequence (padding)."""
         self._rows(step, k)
         attn_cache_append(k, v, self.k_cache(layer), self.v_cache(layer), step.page_table, step.seqlens, step.cu_seqlens,
                           q, q_out, inv_freq, interleaved, factor, stream)
@@ -221,7 +222,8 @@ class PagedCache:
     def attend(self, layer: int, step: Step, q, causal: bool = True, scale: float | None = None, window: int = 0,
                stream=None):
         """Attention of the step's Q, [tokens, Hq, head_dim], over one layer of the
-        cache: O like q and the logsumexp [Hq, tokens] (``forward_paged``)."""
+        cache: O like q and the logsumexp [Hq, tokens] (``forward_paged``), padding's
+        rows as they happen to be."""
         self._rows(step, q)
         return forward_paged(q, self.k_cache(layer), self.v_cache(layer), step.page_table, step.seqlens, step.cu_seqlens,
                              step.max_seqlen_q, step.max_seqlen_k, causal, scale, stream, window)
@@ -229,8 +231,9 @@ class PagedCache:
     @staticmethod
     def _rows(step, x) -> None:
         # Without offsets the kernels take the rows to be divided evenly: twice the
-        # tokens would be taken for two a sequence, over the one before.
-        if x.dim() != 3 or x.shape[0] != step.tokens:
+        # tokens would be taken for two a sequence, over the one before.  Rows behind
+        # the last offset are of no sequence.
+        if x.dim() != 3 or x.shape[0] < step.tokens or (x.shape[0] > step.tokens and step.cu_seqlens is None):
             raise ValueError(f"the step has {step.tokens} new tokens, got {tuple(x.shape)}")
 
     # ------------------------------------------------------------ the pool

@@ -219,7 +219,8 @@ def forward_paged(q, k_cache, v_cache, page_table, seqlens, cu_seqlens=None, max
     cache and tables as in the module's head; returns O (like q) and lse fp32
     [Hq, total].  ``max_seqlen_q`` defaults to total / B without ``cu_seqlens`` and
     to total with them, ``max_seqlen_k`` to the table's capacity: give them where
-    they are known, they size the work's split."""
+    they are known, they size the work's split.  Rows of no sequence, and new
+    tokens past ``max_seqlen_q``, are not written.  Not differentiable."""
     if not q.is_cuda:
         raise ValueError("all device operands must be CUDA tensors")
     total, Hq, d = q.shape

@@ -253,7 +253,8 @@ def test_host_tensors_are_refused():
 
 @pytest.mark.parametrize("new", [1, [2, 3, 0]])
 def test_other_counts_of_tokens_are_refused(monkeypatch, new):
-    """append and attend take the rows that their step has made room for, no others."""
+    """append and attend take the rows that their step has made room for, and with
+    offsets padding behind them."""
     from exact_attention_67_gb300 import cache as module
     made = []
     monkeypatch.setattr(module, "attn_cache_append", lambda k, *a: made.append(k.shape[0]))
@@ -263,7 +264,7 @@ def test_other_counts_of_tokens_are_refused(monkeypatch, new):
     n = step.tokens
     assert n == (3 if new == 1 else 5)
     rows = lambda count, heads=2: torch.zeros(count, heads, 64, dtype=torch.bfloat16)  # noqa: E731
-    for count in (2 * n, n + 1, n - 1, 0):
+    for count in (n - 1, 0) + ((2 * n, n + 1) if new == 1 else ()):
         with pytest.raises(ValueError, match="new tokens"):
             cache.append(0, step, rows(count), rows(count))
         with pytest.raises(ValueError, match="new tokens"):
@@ -274,6 +275,10 @@ def test_other_counts_of_tokens_are_refused(monkeypatch, new):
     cache.append(0, step, rows(n), rows(n))
     cache.attend(0, step, rows(n, 4))
     assert made == [n, n]
+    if new != 1:
+        cache.append(0, step, rows(n + 3), rows(n + 3))
+        cache.attend(0, step, rows(n + 3, 4))
+        assert made[2:] == [n + 3, n + 3]
 
 
 def test_pools_of_impossible_extent_are_refused(lib):
