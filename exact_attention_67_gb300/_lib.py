@@ -539,8 +539,8 @@ def device_error() -> int:
 
 class _Watch:
     """Per device: a page-locked word that every poll copies the watchdog word
-    into.  The watchdog word stays set until device_error reads it, so a copy
-    that finds it set is never followed by one that does not."""
+    into.  The watchdog word stays set until device_error reads it, so on a stream
+    a copy that finds it set is not followed by one that does not."""
 
     def __init__(self):
         self.word = torch.zeros(1, dtype=torch.int32, pin_memory=True)
