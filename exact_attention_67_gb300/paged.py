@@ -172,7 +172,7 @@ def rotary(q, k=None, positions=None, inv_freq=None, interleaved: bool = False, 
     bf16/f16 views (any layout with d contiguous), or both packed [total, H, d].
     ``positions``: int32 [N] or [B, N] ([total] when packed), by default 0..N-1;
     ``inv_freq`` and ``factor`` from ``rotary_frequencies`` (its defaults if not
-    given).  The first 2 * len(inv_freq) elements of a head are turned, the
+    given: they come from the host, so give them to a captured call).  The first 2 * len(inv_freq) elements of a head are turned, the
     others copied."""
     return _turn(q, k, positions, inv_freq, interleaved, False, factor, stream)
 

@@ -203,3 +203,32 @@ def test_a_captured_step():
             mass = torch.einsum("hgj,jhd->hgd", w, V.abs()).reshape(Hq, d)
             assert bool(((o[b].double() - out).abs() <= 2.0 ** -8 * out.abs() + (2.0 ** -10 + 2.0 ** -12) * mass + 2.0 ** -18).all())
     assert ex.device_error() == 0
+
+
+def test_append_in_place_and_rows_before_the_first_sequence():
+    """q_out may be q; rows before cu_seqlens[0] belong to no sequence, neither to the
+    append nor to the attention after it."""
+    import exact_attention_67_gb300 as ex
+    new, lens, Hq, Hk, d, ps = [3, 1, 5], [40, 7, 5], 6, 2, 64, 16
+    before, total = 4, 4 + 9
+    q, k, v = (randn(total, h, d, seed=60 + i, dtype=torch.bfloat16) for i, h in enumerate((Hq, Hk, Hk)))
+    pools = [randn(12, Hk, ps, d, seed=70 + i, dtype=torch.bfloat16) for i in range(2)]
+    table = torch.arange(12, dtype=torch.int32, device=DEV).view(3, 4)
+    seq = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    freq, _ = ex.rotary_frequencies(d)
+    offsets = np.concatenate([[0], np.cumsum(new)])
+    kc, vc = (x.clone() for x in pools)
+    qo = torch.empty_like(q[before:])
+    cu = torch.tensor(offsets, dtype=torch.int32, device=DEV)
+    ex.attn_cache_append(k[before:], v[before:], kc, vc, table, seq, cu, q[before:], qo, freq)
+    want = ex.forward_paged(qo, kc, vc, table, seq, cu, 5, 40)
+    kc2, vc2 = (x.clone() for x in pools)
+    q2, cu2 = q.clone(), cu + before
+    ex.attn_cache_append(k, v, kc2, vc2, table, seq, cu2, q2, q2, freq)
+    assert torch.equal(kc2, kc) and torch.equal(vc2, vc)
+    assert torch.equal(q2[before:], qo) and torch.equal(q2[:before], q[:before])
+    o, lse = torch.full_like(q2, 3.0), torch.full((Hq, total), 3.0, device=DEV)
+    ws = torch.empty(ex.attn_fwd_paged_workspace_size(3, Hq, Hk, total, 5, 40, d), dtype=torch.uint8, device=DEV)
+    ex.attn_fwd_paged(q2, kc2, vc2, o, lse, table, seq, cu2, 5, 40, True, d ** -0.5, ws)
+    assert torch.equal(o[before:], want[0]) and torch.equal(lse[:, before:], want[1])
+    assert torch.all(o[:before] == 3.0) and torch.all(lse[:, :before] == 3.0)
