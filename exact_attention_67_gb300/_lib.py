@@ -30,7 +30,8 @@ EXPORTS = ("attn_fwd", "attn_bwd", "attn_bwd_workspace_size", "attn_bwd_preproce
            "attn_bwd_varlen",
            "attn_fwd_decode_workspace_size", "attn_fwd_decode", "attn_bwd_noalloc",
            "attn_fwd_bwd_host_workspace_size", "attn_fwd_bwd_host",
-           "attn_rotary", "attn_cache_append", "attn_cache_copy", "attn_fwd_paged_workspace_size", "attn_fwd_paged",
+           "attn_rotary", "attn_norm_rotary", "attn_norm_rotary_backward_workspace_size", "attn_norm_rotary_backward",
+           "attn_cache_append", "attn_cache_append_norm", "attn_cache_copy", "attn_fwd_paged_workspace_size", "attn_fwd_paged",
            "exattn_status_string", "exattn_last_cuda_error",
            "exattn_device_error", "exattn_device_error_poll", "exattn_watchdog_selftest", "exattn_version")
 
@@ -118,6 +119,16 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
         lib.attn_cache_append.argtypes = [i, vp, S, vp, S, i, vp, S, vp, S, vp, S, vp, S, i, i, i, vp, ll, i, vp, vp, i, i,
                                           i, vp, i, i, f, vp]
         lib.attn_cache_append.restype = i
+        lib.attn_norm_rotary.argtypes = [i, vp, S, vp, S, i, vp, S, vp, S, i, vp, ll, vp, i, i, f, vp, vp, i, f, i, i, i, vp]
+        lib.attn_norm_rotary.restype = i
+        lib.attn_norm_rotary_backward_workspace_size.argtypes = [i, i, i]
+        lib.attn_norm_rotary_backward_workspace_size.restype = sz
+        lib.attn_norm_rotary_backward.argtypes = [i, vp, S, vp, S, vp, S, i, vp, S, vp, S, vp, S, i, vp, ll, vp, i, i, f, vp,
+                                                  vp, i, f, vp, vp, i, i, i, vp, sz, vp]
+        lib.attn_norm_rotary_backward.restype = i
+        lib.attn_cache_append_norm.argtypes = [i, vp, S, vp, S, i, vp, S, vp, S, vp, S, vp, S, i, i, i, vp, ll, i, vp, vp, i,
+                                               i, i, vp, i, i, f, vp, vp, i, f, vp]
+        lib.attn_cache_append_norm.restype = i
         lib.attn_cache_copy.argtypes = [vp, ll, ll, ll, i, i, vp, vp, i, vp]
         lib.attn_cache_copy.restype = i
         lib.attn_fwd_paged_workspace_size.argtypes = [i, i, i, i, i, i, i]

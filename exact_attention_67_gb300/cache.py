@@ -211,13 +211,14 @@ class PagedCache:
                     None if even else dev[B * width + B:], max(max(new), 1), max(max(lens), 1))
 
     def append(self, layer: int, step: Step, k, v, q=None, q_out=None, inv_freq=None, interleaved: bool = False,
-               factor: float = 1.0, stream=None) -> None:
+               factor: float = 1.0, stream=None, q_gain=None, k_gain=None, eps: float = 1e-6) -> None:
         """Store the step's K and V of one layer, [tokens, kv_heads, head_dim], K and Q
-        turned to their positions with ``inv_freq`` (``attn_cache_append``).  A step
-        with offsets may be followed by rows of no sequence (padding)."""
+        turned to their positions with ``inv_freq``, and before it normalised by head
+        with gains (``attn_cache_append``).  A step with offsets may be followed by rows
+        of no sequence (padding)."""
         self._rows(step, k)
         attn_cache_append(k, v, self.k_cache(layer), self.v_cache(layer), step.page_table, step.seqlens, step.cu_seqlens,
-                          q, q_out, inv_freq, interleaved, factor, stream)
+                          q, q_out, inv_freq, interleaved, factor, stream, q_gain, k_gain, eps)
 
     def attend(self, layer: int, step: Step, q, causal: bool = True, scale: float | None = None, window: int = 0,
                stream=None):

@@ -9,7 +9,9 @@
 // kept from call to call.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
+#include <ATen/ops/empty.h>
 #include <ATen/ops/empty_like.h>
+#include <ATen/ops/zeros.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -196,45 +198,117 @@ Tables tables(OnDevice& on, PyObject* page_table, PyObject* seqlens, PyObject* c
           static_cast<const int*>(t.data_ptr()), static_cast<const int*>(s.data_ptr()), cu};
 }
 
-// q and k (which may be missing) with their outputs; p: positions, inv_freq, interleaved, inverse, factor, stream.
-// [B, H, N, d] tensors with positions [N] or [B, N], or packed [total, H, d] ones with positions [total].
-int rotary_call(const at::Tensor& q, const at::Tensor& qo, const at::Tensor* kt, const at::Tensor* kot, PyObject* const* p) {
-  const bool packed = q.dim() == 3;
-  const int dims = packed ? 3 : 4, h = 1, n = packed ? 0 : 2;
-  auto strides = [&](const at::Tensor& t) { return packed ? strides3(t) : strides4(t); };
-  OnDevice on(q);
-  on.also(qo);
-  const int64_t B = packed ? 1 : q.size(0), N = q.size(n), d = q.size(dims - 1);
-  const void* k = nullptr;
-  void* ko = nullptr;
-  exattn_strides sk{}, sko{};
-  int Hk = 0;
-  if (kt) {
-    if ((!packed && kt->size(0) != B) || kt->size(n) != N || kt->size(dims - 1) != d)
-      bad_value("k must be laid out like q but for its heads, got " + shape_of(*kt));
-    on.also(*kt);
-    on.also(*kot);
-    k = kt->data_ptr();
-    ko = kot->data_ptr();
-    sk = strides(*kt);
-    sko = strides(*kot);
-    Hk = as_int(kt->size(h), "Hk");
+// What the calls that turn q and k (which may be missing) share.  [B, H, N, d] tensors with positions [N] or [B, N],
+// or packed [total, H, d] ones with positions [total].
+struct Turned {
+  bool packed, empty;
+  int64_t B, N, d, pos_stride;
+  int Hq, Hk, rot;
+  const int* pos;
+  const double* freq;
+  exattn_strides strides(const at::Tensor& t) const { return packed ? strides3(t) : strides4(t); }
+};
+Turned turned(OnDevice& on, const at::Tensor& q, const at::Tensor* k, PyObject* positions, PyObject* inv_freq) {
+  Turned t{};
+  t.packed = q.dim() == 3;
+  const int dims = t.packed ? 3 : 4, h = 1, n = t.packed ? 0 : 2;
+  t.B = t.packed ? 1 : q.size(0);
+  t.N = q.size(n);
+  t.d = q.size(dims - 1);
+  t.Hq = as_int(q.size(h), "Hq");
+  if (k) {
+    if ((!t.packed && k->size(0) != t.B) || k->size(n) != t.N || k->size(dims - 1) != t.d)
+      bad_value("k must be laid out like q but for its heads, got " + shape_of(*k));
+    on.also(*k);
+    t.Hk = as_int(k->size(h), "Hk");
   }
-  const bool shared = packed || tensor(p[0], "positions").dim() == 1;
-  const at::Tensor& pos = shared ? int32(p[0], "positions", {N}) : int32(p[0], "positions", {B, N});
-  const at::Tensor& f = tensor(p[1], "inv_freq");
-  const int rot = rotary_dim(f);
+  const bool shared = t.packed || tensor(positions, "positions").dim() == 1;
+  const at::Tensor& pos = shared ? int32(positions, "positions", {t.N}) : int32(positions, "positions", {t.B, t.N});
+  const at::Tensor& f = tensor(inv_freq, "inv_freq");
+  t.rot = rotary_dim(f);
   on.also(pos);
   on.also(f);
+  t.pos = static_cast<const int*>(pos.data_ptr());
+  t.pos_stride = shared || t.B <= 1 ? 0 : pos.stride(0);
+  t.freq = static_cast<const double*>(f.data_ptr());
+  t.empty = q.numel() == 0 && (t.Hk == 0 || t.B * t.N == 0);
+  return t;
+}
+
+// A tensor's place and strides; nothing where it is missing.
+struct Place {
+  void* at = nullptr;
+  exattn_strides s{};
+  Place(const Turned& t, const at::Tensor* x) {
+    if (!x) return;
+    at = x->data_ptr();
+    s = t.strides(*x);
+  }
+};
+
+// q and k (which may be missing) with their outputs; p: positions, inv_freq, interleaved, inverse, factor, stream.
+int rotary_call(const at::Tensor& q, const at::Tensor& qo, const at::Tensor* kt, const at::Tensor* kot, PyObject* const* p) {
+  OnDevice on(q);
+  on.also(qo);
+  if (kot) on.also(*kot);
+  const Turned t = turned(on, q, kt, p[0], p[1]);
   const int il = truth(p[2]), inverse = truth(p[3]);
   const float factor = as_float(p[4]);
-  if (q.numel() == 0 && (Hk == 0 || B * N == 0)) return EXATTN_OK;
+  if (t.empty) return EXATTN_OK;
+  const Place k(t, kt), ko(t, kot);
   void* stream = on.enter(p[5]);
   const WithoutGil threads;
-  return attn_rotary(dtype_of(q), q.data_ptr(), strides(q), qo.data_ptr(), strides(qo), as_int(q.size(h), "Hq"), k, sk, ko,
-                     sko, Hk, static_cast<const int*>(pos.data_ptr()), shared || B <= 1 ? 0 : pos.stride(0),
-                     static_cast<const double*>(f.data_ptr()), rot, il, inverse, factor, as_int(B, "B"), as_int(N, "N"),
-                     as_int(d, "d"), stream);
+  return attn_rotary(dtype_of(q), q.data_ptr(), t.strides(q), qo.data_ptr(), t.strides(qo), t.Hq, k.at, k.s, ko.at, ko.s, t.Hk,
+                     t.pos, t.pos_stride, t.freq, t.rot, il, inverse, factor, as_int(t.B, "B"), as_int(t.N, "N"),
+                     as_int(t.d, "d"), stream);
+}
+
+// Gains [d] of the norms, or nothing (all 1); of one type if both are given.
+struct Gains {
+  const void *q = nullptr, *k = nullptr;
+  at::ScalarType type = at::kFloat;
+  int dtype() const {
+    return type == at::kFloat ? EXATTN_DTYPE_F32 : type == at::kHalf ? EXATTN_DTYPE_F16 : EXATTN_DTYPE_BF16;
+  }
+};
+Gains gains(const OnDevice& on, PyObject* q, PyObject* k, int64_t d, const char* q_name = "q_gain",
+            const char* k_name = "k_gain") {
+  Gains g;
+  bool first = true;
+  auto one = [&](PyObject* o, const char* name) -> const void* {
+    if (o == Py_None) return nullptr;
+    const at::Tensor& t = tensor(o, name);
+    if (t.scalar_type() != at::kFloat && t.scalar_type() != at::kHalf && t.scalar_type() != at::kBFloat16)
+      bad_type(std::string(name) + " must be float32, bfloat16 or float16");
+    if (t.dim() != 1 || t.size(0) != d || !t.is_contiguous())
+      bad_value(std::string(name) + " must be a contiguous tensor [d], got " + shape_of(t));
+    on.also(t);
+    if (!first && t.scalar_type() != g.type) bad_value("the gains must be of one type");
+    first = false;
+    g.type = t.scalar_type();
+    return t.data_ptr();
+  };
+  g.q = one(q, q_name);
+  g.k = one(k, k_name);
+  return g;
+}
+
+// p: positions, inv_freq, q_gain, k_gain, interleaved, factor, eps, stream.
+int norm_call(const at::Tensor& q, const at::Tensor& qo, const at::Tensor* kt, const at::Tensor* kot, PyObject* const* p) {
+  OnDevice on(q);
+  on.also(qo);
+  if (kot) on.also(*kot);
+  const Turned t = turned(on, q, kt, p[0], p[1]);
+  const Gains g = gains(on, p[2], p[3], t.d);
+  const int il = truth(p[4]);
+  const float factor = as_float(p[5]), eps = as_float(p[6]);
+  if (t.empty) return EXATTN_OK;
+  const Place k(t, kt), ko(t, kot);
+  void* stream = on.enter(p[7]);
+  const WithoutGil threads;
+  return attn_norm_rotary(dtype_of(q), q.data_ptr(), t.strides(q), qo.data_ptr(), t.strides(qo), t.Hq, k.at, k.s, ko.at, ko.s,
+                          t.Hk, t.pos, t.pos_stride, t.freq, t.rot, il, factor, g.q, g.k, g.dtype(), eps, as_int(t.B, "B"),
+                          as_int(t.N, "N"), as_int(t.d, "d"), stream);
 }
 
 const at::Tensor& rotary_operand(PyObject* o, const char* name, const at::Tensor* q) {
@@ -242,34 +316,142 @@ const at::Tensor& rotary_operand(PyObject* o, const char* name, const at::Tensor
   return operand(o, name, dims, q);
 }
 
-// (q, q_out, k, k_out, positions, inv_freq, interleaved, inverse, factor, stream)
-PyObject* rotary(PyObject* const* p) {
+using TurnCall = int (*)(const at::Tensor&, const at::Tensor&, const at::Tensor*, const at::Tensor*, PyObject* const*);
+
+// (q, q_out, k, k_out, ...F's)
+template <TurnCall F>
+PyObject* turn_into(PyObject* const* p) {
   const at::Tensor& q = rotary_operand(p[0], "q", nullptr);
   const at::Tensor& qo = same(p[1], "q_out", q);
   if ((p[2] == Py_None) != (p[3] == Py_None)) bad_value("k and k_out go together");
-  if (p[2] == Py_None) return PyLong_FromLong(rotary_call(q, qo, nullptr, nullptr, p + 4));
+  if (p[2] == Py_None) return PyLong_FromLong(F(q, qo, nullptr, nullptr, p + 4));
   const at::Tensor& k = rotary_operand(p[2], "k", &q);
-  return PyLong_FromLong(rotary_call(q, qo, &k, &same(p[3], "k_out", k), p + 4));
+  return PyLong_FromLong(F(q, qo, &k, &same(p[3], "k_out", k), p + 4));
 }
 
-// (q, k or None, positions, inv_freq, interleaved, inverse, factor, stream) -> (status, q_out, k_out or None): the
-// outputs made here, which takes a third of the time that two calls from Python do.
-PyObject* rotary_new(PyObject* const* p) {
+PyObject* tensor_or_none(const at::Tensor& t) { return t.defined() ? THPVariable_Wrap(t) : Py_NewRef(Py_None); }
+
+// (status, tensors...), tensors that are not defined as None
+PyObject* answer(int status, std::initializer_list<at::Tensor> ts) {
+  PyObject* const out = PyTuple_New(static_cast<Py_ssize_t>(1 + ts.size()));
+  if (!out) throw Refused{nullptr, ""};
+  PyTuple_SET_ITEM(out, 0, PyLong_FromLong(status));
+  Py_ssize_t i = 1;
+  for (const at::Tensor& t : ts) PyTuple_SET_ITEM(out, i++, tensor_or_none(t));
+  return out;
+}
+
+// (q, k or None, ...F's) -> (status, q_out, k_out or None): the outputs made here, which takes a third of the time
+// that two calls from Python do.
+template <TurnCall F>
+PyObject* turn_new(PyObject* const* p) {
   const at::Tensor& q = rotary_operand(p[0], "q", nullptr);
   const at::Tensor* k = p[1] == Py_None ? nullptr : &rotary_operand(p[1], "k", &q);
   const at::Tensor qo = at::empty_like(q);
   at::Tensor ko;
   if (k) ko = at::empty_like(*k);
-  const int status = rotary_call(q, qo, k, k ? &ko : nullptr, p + 2);
-  PyObject* const out = PyTuple_New(3);
-  if (!out) throw Refused{nullptr, ""};
-  PyTuple_SET_ITEM(out, 0, PyLong_FromLong(status));
-  PyTuple_SET_ITEM(out, 1, THPVariable_Wrap(qo));
-  PyTuple_SET_ITEM(out, 2, k ? THPVariable_Wrap(ko) : Py_NewRef(Py_None));
-  return out;
+  const int status = F(q, qo, k, k ? &ko : nullptr, p + 2);
+  return answer(status, {qo, ko});
 }
 
-// (k, v, k_cache, v_cache, page_table, seqlens, cu_seqlens, q, q_out, inv_freq, interleaved, factor, stream)
+// The operands of the norms' gradient; dk, k, dk_out may be missing.
+struct NormGrad {
+  const at::Tensor &dq, &q, &dqo;
+  const at::Tensor *dk, *k, *dko;
+  void *dq_gain, *dk_gain, *ws;
+  size_t ws_bytes;
+};
+
+// p: interleaved, factor, eps, then `stream`.
+int norm_grad_call(OnDevice& on, const Turned& t, const Gains& g, const NormGrad& c, PyObject* const* p, PyObject* stream_of) {
+  const int il = truth(p[0]);
+  const float factor = as_float(p[1]), eps = as_float(p[2]);
+  if (t.empty) return EXATTN_OK;
+  const Place dk(t, c.dk), k(t, c.k), dko(t, c.dko);
+  void* stream = on.enter(stream_of);
+  const WithoutGil threads;
+  return attn_norm_rotary_backward(dtype_of(c.q), c.dq.data_ptr(), t.strides(c.dq), c.q.data_ptr(), t.strides(c.q),
+                                   c.dqo.data_ptr(), t.strides(c.dqo), t.Hq, dk.at, dk.s, k.at, k.s, dko.at, dko.s, t.Hk, t.pos,
+                                   t.pos_stride, t.freq, t.rot, il, factor, g.q, g.k, g.dtype(), eps, c.dq_gain, c.dk_gain,
+                                   as_int(t.B, "B"), as_int(t.N, "N"), as_int(t.d, "d"), c.ws, c.ws_bytes, stream);
+}
+
+struct Workspace {
+  void* at = nullptr;
+  size_t bytes = 0;
+  Workspace(const OnDevice& on, PyObject* o) {
+    if (o == Py_None) return;
+    const at::Tensor& w = tensor(o, "workspace");
+    on.also(w);
+    if (!w.is_contiguous()) bad_value("workspace must be contiguous");
+    at = w.data_ptr();
+    bytes = w.nbytes();
+  }
+};
+
+// (dq, q, dq_out, dk, k, dk_out, positions, inv_freq, q_gain, k_gain, dq_gain, dk_gain, interleaved, factor, eps,
+//  workspace, stream)
+int norm_grad(PyObject* const* p) {
+  const at::Tensor& q = rotary_operand(p[1], "q", nullptr);
+  OnDevice on(q);
+  const at::Tensor &dq = same(p[0], "dq", q), &dqo = same(p[2], "dq_out", q);
+  on.also(dq);
+  on.also(dqo);
+  if ((p[3] == Py_None) != (p[4] == Py_None) || (p[3] == Py_None) != (p[5] == Py_None))
+    bad_value("dk, k and dk_out go together");
+  const at::Tensor *dk = nullptr, *k = nullptr, *dko = nullptr;
+  if (p[4] != Py_None) {
+    k = &rotary_operand(p[4], "k", &q);
+    dk = &same(p[3], "dk", *k);
+    dko = &same(p[5], "dk_out", *k);
+    on.also(*dk);
+    on.also(*dko);
+  }
+  const Turned t = turned(on, q, k, p[6], p[7]);
+  Gains g = gains(on, p[8], p[9], t.d);
+  const Gains dg = gains(on, p[10], p[11], t.d, "dq_gain", "dk_gain");
+  if (!g.q && !g.k) g.type = dg.type;
+  if ((dg.q || dg.k) && dg.type != g.type) bad_value("the gains' gradients must be of the gains' type");
+  const Workspace ws(on, p[15]);
+  return norm_grad_call(on, t, g, {dq, q, dqo, dk, k, dko, const_cast<void*>(dg.q), const_cast<void*>(dg.k), ws.at, ws.bytes},
+                        p + 12, p[16]);
+}
+
+// (dq, dk or None, q, k or None, positions, inv_freq, q_gain, k_gain, want_q, want_k, interleaved, factor, eps, stream)
+// -> (status, gradients of q, k, q_gain and k_gain; None where missing or not wanted)
+PyObject* norm_grad_new(PyObject* const* p) {
+  const at::Tensor& q = rotary_operand(p[2], "q", nullptr);
+  OnDevice on(q);
+  const at::Tensor& dq = same(p[0], "dq", q);
+  on.also(dq);
+  if ((p[1] == Py_None) != (p[3] == Py_None)) bad_value("dk and k go together");
+  const at::Tensor *dk = nullptr, *k = nullptr;
+  if (p[3] != Py_None) {
+    k = &rotary_operand(p[3], "k", &q);
+    dk = &same(p[1], "dk", *k);
+    on.also(*dk);
+  }
+  const Turned t = turned(on, q, k, p[4], p[5]);
+  const Gains g = gains(on, p[6], p[7], t.d);
+  const at::Tensor dqo = at::empty_like(q);
+  at::Tensor dko, dqg, dkg;
+  if (k) dko = at::empty_like(*k);
+  const auto options = q.options().dtype(g.type);
+  auto fresh = [&]() { return t.empty ? at::zeros({t.d}, options) : at::empty({t.d}, options); };
+  if (g.q && truth(p[8])) dqg = fresh();
+  if (g.k && truth(p[9])) dkg = t.Hk ? fresh() : at::zeros({t.d}, options);
+  const size_t bytes = t.empty ? 0
+                               : attn_norm_rotary_backward_workspace_size(as_int(t.B, "B"), as_int(t.N, "N"), as_int(t.d, "d"));
+  const at::Tensor ws = at::empty({static_cast<int64_t>(bytes)}, q.options().dtype(at::kByte));
+  const int status = norm_grad_call(on, t, g,
+                                    {dq, q, dqo, dk, k, k ? &dko : nullptr, dqg.defined() ? dqg.data_ptr() : nullptr,
+                                     dkg.defined() ? dkg.data_ptr() : nullptr, ws.data_ptr(), bytes},
+                                    p + 10, p[13]);
+  return answer(status, {dqo, dko, dqg, dkg});
+}
+
+// (k, v, k_cache, v_cache, page_table, seqlens, cu_seqlens, q, q_out, inv_freq, interleaved, factor, stream, q_gain,
+//  k_gain, eps); with gains, normalised on the way
 int cache_append(PyObject* const* p) {
   const at::Tensor& k = operand(p[0], "k", 3);
   const at::Tensor& v = same(p[1], "v", k);
@@ -281,8 +463,11 @@ int cache_append(PyObject* const* p) {
   if (c.heads != k.size(1)) bad_value("k and v must have the cache's " + std::to_string(c.heads) + " heads");
   const int64_t total = k.size(0);
   const Tables t = tables(on, p[4], p[5], p[6], total);
-  if ((p[7] == Py_None) != (p[8] == Py_None) || (p[7] != Py_None && p[9] == Py_None))
+  const Gains g = gains(on, p[13], p[14], k.size(2));
+  const bool normed = g.q || g.k;
+  if ((p[7] == Py_None) != (p[8] == Py_None) || (p[7] != Py_None && p[9] == Py_None && !normed))
     bad_value("q, q_out and inv_freq go together");
+  if (normed && (!g.k || (p[7] == Py_None) != !g.q)) bad_value("gains are given for k, and for q where it is");
   const void* q = nullptr;
   void* qo = nullptr;
   exattn_strides sq{}, sqo{};
@@ -307,10 +492,15 @@ int cache_append(PyObject* const* p) {
     f = static_cast<const double*>(ft.data_ptr());
   }
   const int il = truth(p[10]);
-  const float factor = as_float(p[11]);
+  const float factor = as_float(p[11]), eps = as_float(p[15]);
   if (total == 0) return EXATTN_OK;
   void* stream = on.enter(p[12]);
   const WithoutGil threads;
+  if (normed)
+    return attn_cache_append_norm(dtype_of(k), q, sq, qo, sqo, Hq, k.data_ptr(), strides3(k), v.data_ptr(), strides3(v),
+                                  c.k.data_ptr(), strides4(c.k), c.v.data_ptr(), strides4(c.v), c.heads, c.pages, c.page_size,
+                                  t.table, t.row, t.pages, t.seqlens, t.cu, t.B, as_int(total, "total"),
+                                  as_int(k.size(2), "d"), f, rot, il, factor, g.q, g.k, g.dtype(), eps, stream);
   return attn_cache_append(dtype_of(k), q, sq, qo, sqo, Hq, k.data_ptr(), strides3(k), v.data_ptr(), strides3(v),
                            c.k.data_ptr(), strides4(c.k), c.v.data_ptr(), strides4(c.v), c.heads, c.pages, c.page_size,
                            t.table, t.row, t.pages, t.seqlens, t.cu, t.B, as_int(total, "total"), as_int(k.size(2), "d"), f,
@@ -333,15 +523,7 @@ int fwd_paged(PyObject* const* p) {
   on.also(o);
   on.also(lse);
   const Tables t = tables(on, p[5], p[6], p[7], total);
-  void* ws = nullptr;
-  size_t ws_bytes = 0;
-  if (p[12] != Py_None) {
-    const at::Tensor& w = tensor(p[12], "workspace");
-    on.also(w);
-    if (!w.is_contiguous()) bad_value("workspace must be contiguous");
-    ws = w.data_ptr();
-    ws_bytes = w.nbytes();
-  }
+  const Workspace ws(on, p[12]);
   const int mq = as_int(p[8], "max_seqlen_q"), mk = as_int(p[9], "max_seqlen_k"), causal = truth(p[10]);
   const float scale = as_float(p[11]);
   const int window = as_int(p[14], "window");
@@ -351,7 +533,7 @@ int fwd_paged(PyObject* const* p) {
   return attn_fwd_paged(dtype_of(q), q.data_ptr(), strides3(q), c.k.data_ptr(), strides4(c.k), c.v.data_ptr(),
                         strides4(c.v), o.data_ptr(), strides3(o), static_cast<float*>(lse.data_ptr()), c.pages,
                         c.page_size, t.table, t.row, t.pages, t.seqlens, t.cu, t.B, as_int(Hq, "Hq"), c.heads,
-                        as_int(total, "total"), mq, mk, as_int(q.size(2), "d"), causal, window, scale, ws, ws_bytes, stream);
+                        as_int(total, "total"), mq, mk, as_int(q.size(2), "d"), causal, window, scale, ws.at, ws.bytes, stream);
 }
 
 // Host page numbers: an int32 tensor, or any sequence of ints (into `own`).
@@ -432,15 +614,21 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return nullptr;
 }
 
+template <PyObject* (*F)(PyObject* const*), int ARGS>
+PyMethodDef method(const char* name) {
+  return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(call<F, ARGS>)), METH_FASTCALL, nullptr};
+}
+
 PyMethodDef kMethods[] = {
-    {"rotary", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(call<rotary, 10>)), METH_FASTCALL, nullptr},
-    {"rotary_new", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(call<rotary_new, 8>)), METH_FASTCALL, nullptr},
-    {"cache_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(call<status<cache_append>, 13>)),
-     METH_FASTCALL, nullptr},
-    {"fwd_paged", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(call<status<fwd_paged>, 15>)), METH_FASTCALL,
-     nullptr},
-    {"cache_copy", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(call<status<cache_copy>, 4>)), METH_FASTCALL,
-     nullptr},
+    method<turn_into<rotary_call>, 10>("rotary"),
+    method<turn_new<rotary_call>, 8>("rotary_new"),
+    method<turn_into<norm_call>, 12>("norm_rotary"),
+    method<turn_new<norm_call>, 10>("norm_rotary_new"),
+    method<status<norm_grad>, 17>("norm_rotary_grad"),
+    method<norm_grad_new, 14>("norm_rotary_grad_new"),
+    method<status<cache_append>, 16>("cache_append"),
+    method<status<fwd_paged>, 15>("fwd_paged"),
+    method<status<cache_copy>, 4>("cache_copy"),
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_exattn_binding", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};

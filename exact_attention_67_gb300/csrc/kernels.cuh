@@ -12,7 +12,7 @@ struct Strides {
 };
 
 // Element type of Q, K, V, O, dO, dQ, dK, dV (the C ABI's exattn_dtype).
-enum : int { kBF16 = 0, kF16 = 1 };
+enum : int { kBF16 = 0, kF16 = 1, kF32 = 2 };  // kF32: gains of the norms only
 
 // Where the rows of batch b live.  Fixed length (cu_seqlens == nullptr):
 // rows [0, N) of batch b, statistics (lse, D) at [b*H + h, N].  Packed

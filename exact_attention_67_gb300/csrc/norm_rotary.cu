@@ -1,0 +1,465 @@
+// norm_rotary.cu -- the norm of each head of queries and keys with the rotary turn in
+// one pass, its gradient, and the same on the way into a paged cache, for sm_103a.
+//
+// A row x (a token's head of d elements) becomes
+//     y = m R(p) (g x / s),   s = sqrt(mean x^2 + eps),
+// with the gains g of d elements (one vector for all heads of Q, one for K), the turn
+// R(p) of the first `rot` elements as in rotary.cu and the caller's factor m.
+// Gradient: with h = m R(p)^T dy, e = x / s and u = g h,
+//     dg = sum over rows of h e,      dx = (u - e mean(u e)) / s.
+// s is formed again from x, which the gradient reads anyway: nothing is kept between
+// the passes.  Sums, statistics and products are fp32, rounded once, to the output's
+// type.
+//
+// The lanes that hold a row's items (rotary.cuh: 2 V elements each) add its squares up
+// by exchanges; everything else stays in a thread.  The gradient's blocks run through
+// token groups, a thread summing h e of its places over the heads of Q in registers,
+// then of K, and at the end the block's threads in order; the blocks' sums go to the
+// workspace and a second kernel adds them up.  No atomics: results do not vary from
+// run to run.
+#include "rotary.cuh"
+
+#include <limits.h>
+
+#include <algorithm>
+
+namespace exattn {
+
+namespace {
+
+template <int D, int V>
+struct NormCfg {
+  static constexpr int S = D / (2 * V);          // items a head
+  static constexpr int K = S > 32 ? S / 32 : 1;  // of a thread: a head's lanes are of one warp
+  static constexpr int SL = S / K;               // lanes a head
+  static constexpr int ROWS = kRotaryThreads / SL;
+  static constexpr int W = Item<V>::W;
+};
+
+// Gains in shared memory by tensor and half of an item, each in the order of angle_at.
+template <int D>
+struct GainTable {
+  alignas(16) float g[2][2][D / 2];
+};
+
+// First elements of an item's two vectors (as in rotary.cu).
+template <int V, bool IL>
+__device__ __forceinline__ int first_of(int item, int half) {
+  return !IL && item * V < half ? item * V : 2 * item * V;
+}
+template <int V, bool IL>
+__device__ __forceinline__ int second_of(int item, int half) {
+  return !IL && item * V < half ? item * V + half : 2 * item * V + V;
+}
+
+__device__ __forceinline__ float gain_of(const void* g, int dtype, int i) {
+  if (!g) return 1.f;
+  if (dtype == kF32) return static_cast<const float*>(g)[i];
+  if (dtype == kF16) return __half2float(static_cast<const __half*>(g)[i]);
+  return __bfloat162float(static_cast<const __nv_bfloat16*>(g)[i]);
+}
+
+template <int D, int V, bool IL>
+__device__ __forceinline__ void read_gains(const NormArgs& a, int half, GainTable<D>& s) {
+  for (int i = threadIdx.x; i < 2 * D; i += kRotaryThreads) {
+    const int which = i / D, part = i / (D / 2) & 1, f = i % (D / 2), item = f / V;
+    const int e = (part ? second_of<V, IL>(item, half) : first_of<V, IL>(item, half)) + f % V;
+    s.g[which][part][angle_at<D, V>(f)] = gain_of(which ? a.k_gain : a.q_gain, a.gain_dtype, e);
+  }
+}
+
+// V values of a table as pairs (V = 1: the second of the pair 0).
+template <int D, int V>
+__device__ __forceinline__ void pairs_load(const float* table, int item, float2 (&out)[Item<V>::W]) {
+  float x[V];
+  angle_load<D, V>(table, item, x);
+#pragma unroll
+  for (int i = 0; i < Item<V>::W; ++i) out[i] = make_float2(x[V > 1 ? 2 * i : 0], V > 1 ? x[(2 * i + 1) % V] : 0.f);
+}
+
+// An item's values turned: pairs are (x1, x2) of the same place or, interleaved, the
+// two of a word.
+template <int D, int V, bool IL>
+__device__ __forceinline__ void turn(const float* cos, const float* sin, int item, float2 (&x1)[Item<V>::W],
+                                     float2 (&x2)[Item<V>::W]) {
+  constexpr int W = Item<V>::W;
+  if constexpr (!IL || V == 1) {
+    float2 c[W], s[W];
+    pairs_load<D, V>(cos, item, c);
+    pairs_load<D, V>(sin, item, s);
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const float2 y1 = ffma2(x2[i], make_float2(-s[i].x, -s[i].y), fmul2(x1[i], c[i]));
+      x2[i] = ffma2(x1[i], s[i], fmul2(x2[i], c[i]));
+      x1[i] = y1;
+    }
+  } else {
+    float c[V], s[V];
+    angle_load<D, V>(cos, item, c);
+    angle_load<D, V>(sin, item, s);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      float2& z = i < W ? x1[i] : x2[i - W];
+      z = ffma2(make_float2(z.y, z.x), make_float2(-s[i], s[i]), fmul2(z, make_float2(c[i], c[i])));
+    }
+  }
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void unpack_item(const Item<V>& x, float2 (&x1)[Item<V>::W], float2 (&x2)[Item<V>::W]) {
+#pragma unroll
+  for (int i = 0; i < Item<V>::W; ++i) {
+    x1[i] = Elem<T>::unpack(x.p1.w[i]);
+    x2[i] = Elem<T>::unpack(x.p2.w[i]);
+  }
+}
+
+// Sum over the SL lanes of a head, the same in each.
+template <int SL>
+__device__ __forceinline__ float head_sum(float x, unsigned mask) {
+#pragma unroll
+  for (int o = SL / 2; o > 0; o >>= 1) x += __shfl_xor_sync(mask, x, o);
+  return x;
+}
+
+// This thread's part of a block: items item(0..K-1) of the heads hl, hl + HL, ... of
+// token t of the group.  Of the tokens and heads of a block, neighbouring threads take
+// those that lie side by side.
+template <int D, int V>
+struct Part {
+  int slot, t, hl, HL;
+  unsigned mask;  // the head's lanes
+  __device__ explicit Part(const Deal& deal) {
+    using C = NormCfg<D, V>;
+    const int tid = threadIdx.x, lane = tid & 31, r = tid / C::SL;
+    HL = C::ROWS >> deal.tok_shift;
+    slot = tid % C::SL;
+    t = deal.head_major ? r & ((1 << deal.tok_shift) - 1) : r / HL;
+    hl = deal.head_major ? r >> deal.tok_shift : r & (HL - 1);
+    mask = C::SL == 32 ? ~0u : ((1u << C::SL) - 1) << (lane & ~(C::SL - 1));
+  }
+  __device__ int item(int k) const { return slot + k * NormCfg<D, V>::SL; }
+};
+
+template <typename T, int D, int V, bool IL, bool APPEND>
+__global__ void __launch_bounds__(kRotaryThreads) norm_rotary_kernel(const __grid_constant__ NormArgs na,
+                                                                    const __grid_constant__ Deal deal) {
+  using C = NormCfg<D, V>;
+  using VT = typename Vec<V>::type;
+  constexpr int K = C::K, W = C::W;
+  __shared__ AngleTable<D> angles;
+  __shared__ GainTable<D> gains;
+  __shared__ Token tk[kRotaryTokens];
+  const RotaryArgs& a = na.r;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const unsigned t0 = blockIdx.x << deal.tok_shift;
+  const int nt = static_cast<int>(min(1u << deal.tok_shift, deal.rows - t0));
+  const int half = a.inv_freq ? a.rot >> 1 : 0;
+  const int heads = a.Hq + a.Hk + (APPEND ? a.Hk : 0);
+  const Part<D, V> p(deal);
+  const int t = p.t;
+  const bool live = t < nt;
+  const unsigned row = t0 + (live ? t : 0), b = APPEND ? 0 : deal.length(row);
+  const unsigned n = APPEND ? row : row - b * deal.length.d;
+  auto at = [&](const Strides& st) { return (APPEND ? 0 : b * st.b) + n * st.n; };
+  const int hk = a.Hq, hv = APPEND ? a.Hq + a.Hk : INT_MAX;
+  auto load = [&](int h, Item<V> (&x)[K]) {
+    if (!live || h >= heads) return;
+    const T* src;
+    if (h < hk) src = static_cast<const T*>(a.q) + at(a.sq) + h * a.sq.h;
+    else if (h < hv) src = static_cast<const T*>(a.k) + at(a.sk) + (h - hk) * a.sk.h;
+    else src = static_cast<const T*>(a.v) + at(a.sv) + (h - hv) * a.sv.h;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      x[k].p1.v = *reinterpret_cast<const VT*>(src + first_of<V, IL>(p.item(k), half));
+      x[k].p2.v = *reinterpret_cast<const VT*>(src + second_of<V, IL>(p.item(k), half));
+    }
+  };
+  // The first items are on their way while the tokens are looked up and their angles
+  // formed.
+  Item<V> x[K];
+  load(p.hl, x);
+  read_frequencies<D>(a, half, angles);
+  read_gains<D, V, IL>(na, half, gains);
+  if (warp < nt) {
+    const Token k = find_token<APPEND>(a, deal, t0 + warp, lane);
+    if (lane == 0) tk[warp] = k;
+  }
+  __syncthreads();
+  form_angles<D, V>(a, half, nt, tk, angles);
+  __syncthreads();
+  if (!live) return;
+  const int flags = APPEND ? tk[t].flags : 3;
+  for (int h = p.hl; h < heads; h += p.HL) {
+    Item<V> y[K];
+    load(h + p.HL, y);
+    if (h < hv) {
+      float2 x1[K][W], x2[K][W], sum = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        unpack_item<T, V>(x[k], x1[k], x2[k]);
+#pragma unroll
+        for (int i = 0; i < W; ++i) sum = ffma2(x1[k][i], x1[k][i], ffma2(x2[k][i], x2[k][i], sum));
+      }
+      const float r = rsqrtf(fmaf(head_sum<C::SL>(sum.x + sum.y, p.mask), 1.f / D, na.eps));
+      const float2 rr = make_float2(r, r);
+      const float(*g)[D / 2] = gains.g[h < hk ? 0 : 1];
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const int item = p.item(k);
+        float2 w[W];
+        pairs_load<D, V>(g[0], item, w);
+#pragma unroll
+        for (int i = 0; i < W; ++i) x1[k][i] = fmul2(fmul2(x1[k][i], rr), w[i]);
+        pairs_load<D, V>(g[1], item, w);
+#pragma unroll
+        for (int i = 0; i < W; ++i) x2[k][i] = fmul2(fmul2(x2[k][i], rr), w[i]);
+        if (item * V < half) turn<D, V, IL>(angles.cos + t * (D / 2), angles.sin + t * (D / 2), item, x1[k], x2[k]);
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+          x[k].p1.w[i] = Elem<T>::pack(x1[k][i].x, x1[k][i].y);
+          x[k].p2.w[i] = Elem<T>::pack(x2[k][i].x, x2[k][i].y);
+        }
+      }
+    }
+    T* dst;
+    if (h < hk) dst = static_cast<T*>(a.q_out) + at(a.sqo) + h * a.sqo.h;
+    else if (!APPEND) dst = static_cast<T*>(a.k_out) + at(a.sko) + (h - hk) * a.sko.h;
+    else if (h < hv) dst = static_cast<T*>(a.k_out) + tk[t].k + (h - hk) * a.sko.h;
+    else dst = static_cast<T*>(a.v_out) + tk[t].v + (h - hv) * a.svo.h;
+    if (flags & (h < hk ? 1 : 2)) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        *reinterpret_cast<VT*>(dst + first_of<V, IL>(p.item(k), half)) = x[k].p1.v;
+        *reinterpret_cast<VT*>(dst + second_of<V, IL>(p.item(k), half)) = x[k].p2.v;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) x[k] = y[k];
+  }
+}
+
+// The gradient.  A block takes the token groups blockIdx.x, + gridDim.x, ...
+template <typename T, int D, int V, bool IL>
+__global__ void __launch_bounds__(kRotaryThreads, 2) norm_rotary_grad_kernel(const __grid_constant__ NormArgs na,
+                                                                            const __grid_constant__ Deal deal) {
+  using C = NormCfg<D, V>;
+  using VT = typename Vec<V>::type;
+  constexpr int K = C::K, W = C::W;
+  __shared__ AngleTable<D> angles;
+  __shared__ GainTable<D> gains;
+  __shared__ Token tk[kRotaryTokens];
+  __shared__ float sums[2][K][2][V][kRotaryThreads];  // h e by tensor, item, half, place and thread
+  const RotaryArgs& a = na.r;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int half = a.rot >> 1, heads = a.Hq + a.Hk, hk = a.Hq;
+  const Part<D, V> p(deal);
+  read_frequencies<D>(a, half, angles);
+  read_gains<D, V, IL>(na, half, gains);
+#pragma unroll
+  for (int i = 0; i < 4 * K * V; ++i) (&sums[0][0][0][0][0])[i * kRotaryThreads + tid] = 0.f;
+  for (unsigned t0 = blockIdx.x << deal.tok_shift; t0 < deal.rows; t0 += gridDim.x << deal.tok_shift) {
+    const int nt = static_cast<int>(min(1u << deal.tok_shift, deal.rows - t0)), t = p.t;
+    const bool live = t < nt;
+    const unsigned row = t0 + (live ? t : 0), b = deal.length(row), n = row - b * deal.length.d;
+    auto at = [&](const Strides& st) { return b * st.b + n * st.n; };
+    auto load = [&](int h, Item<V> (&x)[K], Item<V> (&g)[K]) {
+      if (!live || h >= heads) return;
+      const bool q = h < hk;
+      const T* xs = static_cast<const T*>(q ? a.q : a.k) + at(q ? a.sq : a.sk) + (q ? h * a.sq.h : (h - hk) * a.sk.h);
+      const T* gs = static_cast<const T*>(q ? na.dq : na.dk) + at(q ? na.sdq : na.sdk) + (q ? h * na.sdq.h : (h - hk) * na.sdk.h);
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const int e1 = first_of<V, IL>(p.item(k), half), e2 = second_of<V, IL>(p.item(k), half);
+        x[k].p1.v = *reinterpret_cast<const VT*>(xs + e1);
+        x[k].p2.v = *reinterpret_cast<const VT*>(xs + e2);
+        g[k].p1.v = *reinterpret_cast<const VT*>(gs + e1);
+        g[k].p2.v = *reinterpret_cast<const VT*>(gs + e2);
+      }
+    };
+    Item<V> x[K], g[K];
+    load(p.hl, x, g);
+    if (warp < nt) {
+      const Token k = find_token<false>(a, deal, t0 + warp, lane);
+      if (lane == 0) tk[warp] = k;
+    }
+    __syncthreads();
+    form_angles<D, V>(a, half, nt, tk, angles);
+    __syncthreads();
+    if (live) {
+      float2 s1[K][W], s2[K][W];  // this thread's sums of h e for one tensor
+      int which = p.hl < hk ? 0 : 1;
+      auto clear = [&]() {
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+          for (int i = 0; i < W; ++i) s1[k][i] = s2[k][i] = make_float2(0.f, 0.f);
+      };
+      auto flush = [&]() {
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            sums[which][k][0][i][tid] += i & 1 ? s1[k][i / 2].y : s1[k][i / 2].x;
+            sums[which][k][1][i][tid] += i & 1 ? s2[k][i / 2].y : s2[k][i / 2].x;
+          }
+      };
+      clear();
+      for (int h = p.hl; h < heads; h += p.HL) {
+        if (which == 0 && h >= hk) {
+          flush();
+          clear();
+          which = 1;
+        }
+        Item<V> xn[K], gn[K];
+        load(h + p.HL, xn, gn);
+        float2 x1[K][W], x2[K][W], h1[K][W], h2[K][W], sq = make_float2(0.f, 0.f), dot = make_float2(0.f, 0.f);
+        const float(*gain)[D / 2] = gains.g[which];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          const int item = p.item(k);
+          unpack_item<T, V>(x[k], x1[k], x2[k]);
+          unpack_item<T, V>(g[k], h1[k], h2[k]);
+          if (item * V < half) turn<D, V, IL>(angles.cos + t * (D / 2), angles.sin + t * (D / 2), item, h1[k], h2[k]);
+          float2 w[W];
+          // h to u = g h, and h x to this tensor's sums once the row's size is known.
+          pairs_load<D, V>(gain[0], item, w);
+#pragma unroll
+          for (int i = 0; i < W; ++i) {
+            sq = ffma2(x1[k][i], x1[k][i], sq);
+            dot = ffma2(fmul2(h1[k][i], w[i]), x1[k][i], dot);
+          }
+          pairs_load<D, V>(gain[1], item, w);
+#pragma unroll
+          for (int i = 0; i < W; ++i) {
+            sq = ffma2(x2[k][i], x2[k][i], sq);
+            dot = ffma2(fmul2(h2[k][i], w[i]), x2[k][i], dot);
+          }
+        }
+        const float r = rsqrtf(fmaf(head_sum<C::SL>(sq.x + sq.y, p.mask), 1.f / D, na.eps));
+        const float mean = head_sum<C::SL>(dot.x + dot.y, p.mask) * r * (1.f / D);  // of u e
+        const float2 rr = make_float2(r, r), mm = make_float2(-mean, -mean);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          float2 w[W];
+          pairs_load<D, V>(gain[0], p.item(k), w);
+#pragma unroll
+          for (int i = 0; i < W; ++i) {
+            const float2 e = fmul2(x1[k][i], rr);
+            s1[k][i] = ffma2(h1[k][i], e, s1[k][i]);
+            const float2 dx = fmul2(ffma2(e, mm, fmul2(h1[k][i], w[i])), rr);
+            x[k].p1.w[i] = Elem<T>::pack(dx.x, dx.y);
+          }
+          pairs_load<D, V>(gain[1], p.item(k), w);
+#pragma unroll
+          for (int i = 0; i < W; ++i) {
+            const float2 e = fmul2(x2[k][i], rr);
+            s2[k][i] = ffma2(h2[k][i], e, s2[k][i]);
+            const float2 dx = fmul2(ffma2(e, mm, fmul2(h2[k][i], w[i])), rr);
+            x[k].p2.w[i] = Elem<T>::pack(dx.x, dx.y);
+          }
+        }
+        T* dst = h < hk ? static_cast<T*>(a.q_out) + at(a.sqo) + h * a.sqo.h
+                        : static_cast<T*>(a.k_out) + at(a.sko) + (h - hk) * a.sko.h;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          *reinterpret_cast<VT*>(dst + first_of<V, IL>(p.item(k), half)) = x[k].p1.v;
+          *reinterpret_cast<VT*>(dst + second_of<V, IL>(p.item(k), half)) = x[k].p2.v;
+          x[k] = xn[k];
+          g[k] = gn[k];
+        }
+      }
+      flush();
+    }
+    __syncthreads();  // the angles are formed anew for the next group
+  }
+  __syncthreads();
+  // The block's sums, a value a thread, its rows in order.
+  for (int i = tid; i < 2 * D; i += kRotaryThreads) {
+    const int which = i / D, part = i / (D / 2) & 1, j = i % (D / 2) / C::S, item = i % C::S;
+    const float* s = sums[which][item / C::SL][part][j] + item % C::SL;
+    float sum = 0.f;
+#pragma unroll 8
+    for (int r = 0; r < C::ROWS; ++r) sum += s[r * C::SL];
+    const int e = (part ? second_of<V, IL>(item, half) : first_of<V, IL>(item, half)) + j;
+    na.partial[static_cast<long long>(blockIdx.x) * 2 * D + which * D + e] = sum;
+  }
+}
+
+// Gains' gradients: the blocks' sums added up, 32 columns a block, 16 runs of rows,
+// then the runs in order.
+template <int D>
+__global__ void __launch_bounds__(512) norm_gains_kernel(const __grid_constant__ NormArgs a) {
+  __shared__ float s[16][32];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x & 31, run = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
+  float sum = 0.f;
+#pragma unroll 4
+  for (int r = run; r < a.parts; r += 16) sum += a.partial[static_cast<long long>(r) * 2 * D + col];
+  s[run][lane] = sum;
+  __syncthreads();
+  if (run) return;
+  sum = 0.f;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) sum += s[r][lane];
+  void* out = col < D ? a.q_dgain : a.k_dgain;
+  const int i = col % D;
+  if (!out) return;
+  if (a.gain_dtype == kF32) static_cast<float*>(out)[i] = sum;
+  else if (a.gain_dtype == kF16) static_cast<__half*>(out)[i] = __float2half_rn(sum);
+  else static_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(sum);
+}
+
+template <typename T, int D, int V, bool IL>
+cudaError_t launch_t(const NormArgs& na, cudaStream_t stream) {
+  const RotaryArgs& a = na.r;
+  using C = NormCfg<D, V>;
+  // Several tokens a block (a power of two) once that still leaves eight blocks an SM.
+  Deal deal{};
+  deal.rows = a.append ? a.nt.total : static_cast<unsigned>(a.B) * a.N;
+  while ((1 << deal.tok_shift) < std::min(kRotaryTokens, C::ROWS) && deal.rows >> (deal.tok_shift + 1) >= 152 * 8)
+    ++deal.tok_shift;
+  deal.head_major = a.Hq > 0 ? a.sq.n < a.sq.h : a.sk.n < a.sk.h;
+  deal.length = Divide(!a.append ? a.N : a.nt.each > 0 ? a.nt.each : 1);
+  const unsigned groups = (deal.rows + (1u << deal.tok_shift) - 1) >> deal.tok_shift;
+  if (!na.partial) {
+    auto kern = a.append ? norm_rotary_kernel<T, D, V, IL, true> : norm_rotary_kernel<T, D, V, IL, false>;
+    return launch_dependent("norm kernel launch", kern, groups, kRotaryThreads, 0, stream, na, deal);
+  }
+  NormArgs g = na;
+  g.parts = static_cast<int>(std::min<unsigned>(groups, kNormParts));
+  cudaError_t e = launch_dependent("norm gradient kernel launch", norm_rotary_grad_kernel<T, D, V, IL>, g.parts, kRotaryThreads,
+                                   0, stream, g, deal);
+  if (e != cudaSuccess || (!g.q_dgain && !g.k_dgain)) return e;
+  return launch_dependent("gains' gradient kernel launch", norm_gains_kernel<D>, 2 * D / 32, 512, 0, stream, g);
+}
+
+template <typename T, int D>
+cudaError_t launch_d(const NormArgs& a, cudaStream_t stream) {
+  const int rot = a.r.inv_freq ? a.r.rot : D;
+  const int v = rot % 16 == 0 ? 8 : rot % 8 == 0 ? 4 : rot % 4 == 0 ? 2 : 1;
+  if (a.r.interleaved) {
+    if (v == 8) return launch_t<T, D, 8, true>(a, stream);
+    if (v == 4) return launch_t<T, D, 4, true>(a, stream);
+    if (v == 2) return launch_t<T, D, 2, true>(a, stream);
+    return launch_t<T, D, 1, true>(a, stream);
+  }
+  if (v == 8) return launch_t<T, D, 8, false>(a, stream);
+  if (v == 4) return launch_t<T, D, 4, false>(a, stream);
+  if (v == 2) return launch_t<T, D, 2, false>(a, stream);
+  return launch_t<T, D, 1, false>(a, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_norm_rotary(const NormArgs& a, cudaStream_t stream) {
+  if (a.r.dtype == kF16) return a.r.d == 64 ? launch_d<__half, 64>(a, stream) : launch_d<__half, 128>(a, stream);
+  return a.r.d == 64 ? launch_d<__nv_bfloat16, 64>(a, stream) : launch_d<__nv_bfloat16, 128>(a, stream);
+}
+
+}  // namespace exattn

@@ -83,6 +83,26 @@ struct RotaryArgs {
 };
 cudaError_t launch_rotary(const RotaryArgs& a, cudaStream_t stream);
 
+// Norms of the heads with the turn (norm_rotary.cu).  r.q, r.k are the rows x; the
+// gradient (partial not null) turns dq, dk back (r.inverse) and writes r.q_out, r.k_out.
+struct NormArgs {
+  RotaryArgs r;
+  const void* q_gain;  // [d] or nullptr (all 1)
+  const void* k_gain;
+  int gain_dtype;      // kBF16, kF16 or kF32
+  float eps;
+  const void* dq;
+  Strides sdq;
+  const void* dk;
+  Strides sdk;
+  void* q_dgain;       // [d] or nullptr
+  void* k_dgain;
+  float* partial;      // [parts][2][d]: the blocks' sums for the gains of Q and K
+  int parts;
+};
+constexpr int kNormParts = 152 * 2;  // blocks of the gradient at most
+cudaError_t launch_norm_rotary(const NormArgs& a, cudaStream_t stream);
+
 // Attention of new tokens over a paged cache.  The query heads of a key head
 // (G of them) and consecutive new tokens share the rows (forward kernel) or
 // columns (decode kernel) of a unit: unit row r is token r / G, head r % G.

@@ -39,6 +39,17 @@ int check_rotary(const double* inv_freq, int rot_dim, int d, float factor) {
   return EXATTN_OK;
 }
 
+// Gains [d] of the norms (each may be missing), of a 16-bit type or fp32.
+int check_gains(const void* q_gain, const void* k_gain, int gain_dtype, float eps) {
+  if (!known_dtype(gain_dtype) && gain_dtype != EXATTN_DTYPE_F32) return EXATTN_ERR_UNSUPPORTED;
+  const uintptr_t size = gain_dtype == EXATTN_DTYPE_F32 ? 4 : 2;
+  if (!aligned(q_gain, size) || !aligned(k_gain, size)) return EXATTN_ERR_ALIGN;
+  if (!std::isfinite(eps) || eps < 0.f) return EXATTN_ERR_VALUE;
+  return EXATTN_OK;
+}
+
+int element_type(int dtype) { return dtype == EXATTN_DTYPE_F32 ? kF32 : dtype == EXATTN_DTYPE_F16 ? kF16 : kBF16; }
+
 // Shared checks of a cache and its page table; fills the view.
 int check_pages(PageView* pv, const int* page_table, long long table_stride, int max_pages, int num_pages,
                 int page_size, int B, int Hkv, const exattn_strides& sk, const exattn_strides& sv) {
@@ -72,10 +83,13 @@ int check_tokens(NewTokens* nt, const int* cu_seqlens, const int* seqlens, int B
 
 }  // namespace
 
-extern "C" int attn_rotary(int dtype, const void* q, exattn_strides sq, void* q_out, exattn_strides sqo, int Hq,
-                           const void* k, exattn_strides sk, void* k_out, exattn_strides sko, int Hk,
-                           const int* positions, long long pos_stride, const double* inv_freq, int rot_dim,
-                           int interleaved, int inverse, float factor, int B, int N, int d, void* stream) {
+namespace {
+
+// Checks of a call that turns [B, H, N, d] views, and its kernel's arguments.
+int rotary_args(RotaryArgs* out, int dtype, const void* q, exattn_strides sq, void* q_out, exattn_strides sqo, int Hq,
+                const void* k, exattn_strides sk, void* k_out, exattn_strides sko, int Hk, const int* positions,
+                long long pos_stride, const double* inv_freq, int rot_dim, int interleaved, int inverse, float factor, int B,
+                int N, int d) {
   if (!q || !q_out || !positions || !inv_freq || (Hk > 0 && (!k || !k_out))) return EXATTN_ERR_NULL;
   if (!known_dtype(dtype) || (d != 64 && d != 128)) return EXATTN_ERR_UNSUPPORTED;
   if (B < 1 || N < 1 || Hq < 1 || Hk < 0 || Hq > 65536 || Hk > 65536) return EXATTN_ERR_SHAPE;
@@ -88,10 +102,7 @@ extern "C" int attn_rotary(int dtype, const void* q, exattn_strides sq, void* q_
   if (Hk > 0 &&
       ((rc = check_strides(sk, B, Hk, N)) != EXATTN_OK || (rc = check_strides(sko, B, Hk, N)) != EXATTN_OK))
     return rc;
-  int dev = 0;
-  unsigned* err = nullptr;
-  if ((rc = setup_device(&dev, &err)) != EXATTN_OK) return rc;
-  RotaryArgs a{};
+  RotaryArgs& a = *out;
   a.q = q;
   a.sq = to_strides(sq);
   a.q_out = q_out;
@@ -105,7 +116,7 @@ extern "C" int attn_rotary(int dtype, const void* q, exattn_strides sq, void* q_
   a.B = B;
   a.N = N;
   a.d = d;
-  a.dtype = dtype == EXATTN_DTYPE_F16 ? kF16 : kBF16;
+  a.dtype = element_type(dtype);
   a.positions = positions;
   a.pos_stride = pos_stride;
   a.inv_freq = inv_freq;
@@ -113,20 +124,20 @@ extern "C" int attn_rotary(int dtype, const void* q, exattn_strides sq, void* q_
   a.interleaved = interleaved ? 1 : 0;
   a.inverse = inverse ? 1 : 0;
   a.factor = factor;
-  return launch_rotary(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? EXATTN_OK : EXATTN_ERR_CUDA;
+  return EXATTN_OK;
 }
 
-extern "C" int attn_cache_append(int dtype, const void* q, exattn_strides sq, void* q_out, exattn_strides sqo, int Hq,
-                                 const void* k, exattn_strides sk, const void* v, exattn_strides sv, void* k_cache,
-                                 exattn_strides skc, void* v_cache, exattn_strides svc, int Hkv, int num_pages,
-                                 int page_size, const int* page_table, long long table_stride, int max_pages,
-                                 const int* seqlens, const int* cu_seqlens, int B, int total, int d,
-                                 const double* inv_freq, int rot_dim, int interleaved, float factor, void* stream) {
+// The same of a call that appends to a cache; `normed`: q needs no frequencies.
+int append_args(RotaryArgs* out, bool normed, int dtype, const void* q, exattn_strides sq, void* q_out, exattn_strides sqo,
+                int Hq, const void* k, exattn_strides sk, const void* v, exattn_strides sv, void* k_cache, exattn_strides skc,
+                void* v_cache, exattn_strides svc, int Hkv, int num_pages, int page_size, const int* page_table,
+                long long table_stride, int max_pages, const int* seqlens, const int* cu_seqlens, int B, int total, int d,
+                const double* inv_freq, int rot_dim, int interleaved, float factor) {
   if (!k || !v || !k_cache || !v_cache || !page_table || !seqlens) return EXATTN_ERR_NULL;
-  if (Hq > 0 && (!q || !q_out || !inv_freq)) return EXATTN_ERR_NULL;
+  if (Hq > 0 && (!q || !q_out || (!inv_freq && !normed))) return EXATTN_ERR_NULL;
   if (!known_dtype(dtype) || (d != 64 && d != 128)) return EXATTN_ERR_UNSUPPORTED;
   if (Hq < 0 || Hq > 65536 || Hkv < 1 || Hkv > 65536) return EXATTN_ERR_SHAPE;
-  RotaryArgs a{};
+  RotaryArgs& a = *out;
   int rc = check_tokens(&a.nt, cu_seqlens, seqlens, B, total);
   if (rc != EXATTN_OK) return rc;
   if ((rc = check_pages(&a.pv, page_table, table_stride, max_pages, num_pages, page_size, B, Hkv, skc, svc)) !=
@@ -141,9 +152,6 @@ extern "C" int attn_cache_append(int dtype, const void* q, exattn_strides sq, vo
     return rc;
   if ((rc = check_strides(sk, 1, Hkv, total)) != EXATTN_OK || (rc = check_strides(sv, 1, Hkv, total)) != EXATTN_OK)
     return rc;
-  int dev = 0;
-  unsigned* err = nullptr;
-  if ((rc = setup_device(&dev, &err)) != EXATTN_OK) return rc;
   a.q = q;
   a.sq = to_strides(sq);
   a.q_out = q_out;
@@ -159,13 +167,125 @@ extern "C" int attn_cache_append(int dtype, const void* q, exattn_strides sq, vo
   a.Hq = Hq;
   a.Hk = Hkv;
   a.d = d;
-  a.dtype = dtype == EXATTN_DTYPE_F16 ? kF16 : kBF16;
+  a.dtype = element_type(dtype);
   a.inv_freq = inv_freq;
   a.rot = rot_dim;
   a.interleaved = interleaved ? 1 : 0;
   a.factor = factor;
   a.append = true;
-  return launch_rotary(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? EXATTN_OK : EXATTN_ERR_CUDA;
+  return EXATTN_OK;
+}
+
+// The current device's set-up; calls that do not use its watchdog word.
+int device_ready() {
+  int dev = 0;
+  unsigned* err = nullptr;
+  return setup_device(&dev, &err);
+}
+
+int status_of(cudaError_t e) { return e == cudaSuccess ? EXATTN_OK : EXATTN_ERR_CUDA; }
+
+}  // namespace
+
+extern "C" int attn_rotary(int dtype, const void* q, exattn_strides sq, void* q_out, exattn_strides sqo, int Hq,
+                           const void* k, exattn_strides sk, void* k_out, exattn_strides sko, int Hk,
+                           const int* positions, long long pos_stride, const double* inv_freq, int rot_dim,
+                           int interleaved, int inverse, float factor, int B, int N, int d, void* stream) {
+  RotaryArgs a{};
+  int rc = rotary_args(&a, dtype, q, sq, q_out, sqo, Hq, k, sk, k_out, sko, Hk, positions, pos_stride, inv_freq, rot_dim,
+                       interleaved, inverse, factor, B, N, d);
+  if (rc != EXATTN_OK || (rc = device_ready()) != EXATTN_OK) return rc;
+  return status_of(launch_rotary(a, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" int attn_norm_rotary(int dtype, const void* q, exattn_strides sq, void* q_out, exattn_strides sqo, int Hq,
+                                const void* k, exattn_strides sk, void* k_out, exattn_strides sko, int Hk,
+                                const int* positions, long long pos_stride, const double* inv_freq, int rot_dim,
+                                int interleaved, float factor, const void* q_gain, const void* k_gain, int gain_dtype,
+                                float eps, int B, int N, int d, void* stream) {
+  NormArgs a{};
+  int rc = rotary_args(&a.r, dtype, q, sq, q_out, sqo, Hq, k, sk, k_out, sko, Hk, positions, pos_stride, inv_freq, rot_dim,
+                       interleaved, 0, factor, B, N, d);
+  if (rc != EXATTN_OK || (rc = check_gains(q_gain, k_gain, gain_dtype, eps)) != EXATTN_OK) return rc;
+  if ((rc = device_ready()) != EXATTN_OK) return rc;
+  a.q_gain = q_gain;
+  a.k_gain = k_gain;
+  a.gain_dtype = element_type(gain_dtype);
+  a.eps = eps;
+  return status_of(launch_norm_rotary(a, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" size_t attn_norm_rotary_backward_workspace_size(int B, int N, int d) {
+  if (B < 1 || N < 1 || static_cast<long long>(B) * N >= (1ll << 31) || (d != 64 && d != 128)) return 0;
+  return std::min<size_t>(static_cast<size_t>(B) * N, kNormParts) * 2 * d * sizeof(float);
+}
+
+extern "C" int attn_norm_rotary_backward(int dtype, const void* dq, exattn_strides sdq, const void* q, exattn_strides sq,
+                                         void* dq_out, exattn_strides sqo, int Hq, const void* dk, exattn_strides sdk,
+                                         const void* k, exattn_strides sk, void* dk_out, exattn_strides sko, int Hk,
+                                         const int* positions, long long pos_stride, const double* inv_freq, int rot_dim,
+                                         int interleaved, float factor, const void* q_gain, const void* k_gain,
+                                         int gain_dtype, float eps, void* dq_gain, void* dk_gain, int B, int N, int d,
+                                         void* workspace, size_t workspace_bytes, void* stream) {
+  if (!dq || (Hk > 0 && !dk)) return EXATTN_ERR_NULL;
+  NormArgs a{};
+  int rc = rotary_args(&a.r, dtype, q, sq, dq_out, sqo, Hq, k, sk, dk_out, sko, Hk, positions, pos_stride, inv_freq, rot_dim,
+                       interleaved, 1, factor, B, N, d);
+  if (rc != EXATTN_OK || (rc = check_gains(q_gain, k_gain, gain_dtype, eps)) != EXATTN_OK ||
+      (rc = check_gains(dq_gain, dk_gain, gain_dtype, eps)) != EXATTN_OK)
+    return rc;
+  if (!aligned(dq, 16) || !aligned(dk, 16)) return EXATTN_ERR_ALIGN;
+  if ((rc = check_strides(sdq, B, Hq, N)) != EXATTN_OK || (Hk > 0 && (rc = check_strides(sdk, B, Hk, N)) != EXATTN_OK))
+    return rc;
+  if (!workspace || workspace_bytes < attn_norm_rotary_backward_workspace_size(B, N, d)) return EXATTN_ERR_WORKSPACE;
+  if (!aligned(workspace, 16)) return EXATTN_ERR_ALIGN;
+  if ((rc = device_ready()) != EXATTN_OK) return rc;
+  a.q_gain = q_gain;
+  a.k_gain = k_gain;
+  a.gain_dtype = element_type(gain_dtype);
+  a.eps = eps;
+  a.dq = dq;
+  a.sdq = to_strides(sdq);
+  a.dk = dk;
+  a.sdk = to_strides(sdk);
+  a.q_dgain = dq_gain;
+  a.k_dgain = dk_gain;
+  a.partial = static_cast<float*>(workspace);
+  return status_of(launch_norm_rotary(a, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" int attn_cache_append(int dtype, const void* q, exattn_strides sq, void* q_out, exattn_strides sqo, int Hq,
+                                 const void* k, exattn_strides sk, const void* v, exattn_strides sv, void* k_cache,
+                                 exattn_strides skc, void* v_cache, exattn_strides svc, int Hkv, int num_pages,
+                                 int page_size, const int* page_table, long long table_stride, int max_pages,
+                                 const int* seqlens, const int* cu_seqlens, int B, int total, int d,
+                                 const double* inv_freq, int rot_dim, int interleaved, float factor, void* stream) {
+  RotaryArgs a{};
+  int rc = append_args(&a, false, dtype, q, sq, q_out, sqo, Hq, k, sk, v, sv, k_cache, skc, v_cache, svc, Hkv, num_pages,
+                       page_size, page_table, table_stride, max_pages, seqlens, cu_seqlens, B, total, d, inv_freq, rot_dim,
+                       interleaved, factor);
+  if (rc != EXATTN_OK || (rc = device_ready()) != EXATTN_OK) return rc;
+  return status_of(launch_rotary(a, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" int attn_cache_append_norm(int dtype, const void* q, exattn_strides sq, void* q_out, exattn_strides sqo, int Hq,
+                                      const void* k, exattn_strides sk, const void* v, exattn_strides sv, void* k_cache,
+                                      exattn_strides skc, void* v_cache, exattn_strides svc, int Hkv, int num_pages,
+                                      int page_size, const int* page_table, long long table_stride, int max_pages,
+                                      const int* seqlens, const int* cu_seqlens, int B, int total, int d,
+                                      const double* inv_freq, int rot_dim, int interleaved, float factor,
+                                      const void* q_gain, const void* k_gain, int gain_dtype, float eps, void* stream) {
+  NormArgs a{};
+  int rc = append_args(&a.r, true, dtype, q, sq, q_out, sqo, Hq, k, sk, v, sv, k_cache, skc, v_cache, svc, Hkv, num_pages,
+                       page_size, page_table, table_stride, max_pages, seqlens, cu_seqlens, B, total, d, inv_freq, rot_dim,
+                       interleaved, factor);
+  if (rc != EXATTN_OK || (rc = check_gains(q_gain, k_gain, gain_dtype, eps)) != EXATTN_OK) return rc;
+  if ((rc = device_ready()) != EXATTN_OK) return rc;
+  a.q_gain = q_gain;
+  a.k_gain = k_gain;
+  a.gain_dtype = element_type(gain_dtype);
+  a.eps = eps;
+  return status_of(launch_norm_rotary(a, static_cast<cudaStream_t>(stream)));
 }
 
 extern "C" int attn_cache_copy(void* pool, long long slab_stride, long long page_stride, long long page_bytes,

@@ -34,8 +34,7 @@
 // thread's angles kept in registers 26.5, 32.5 and 46.6 us.  Narrower vectors move
 // the copied part of a head, and V, too: the first case with rot 24, 20 and 6 (8, 4
 // and 2 bytes) 25.4, 32.1 and 71.0 us, the append with rot 20 and 6 53.9 and 129.7.
-#include "paged.cuh"
-#include "ptx.cuh"
+#include "rotary.cuh"
 
 #include <limits.h>
 
@@ -45,111 +44,12 @@ namespace exattn {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kMaxTok = 8;  // tokens a block at most
-static_assert(kMaxTok <= kThreads / 32, "a warp looks up each token");
-
-template <int V>
-struct Vec;
-template <>
-struct Vec<8> { using type = uint4; };
-template <>
-struct Vec<4> { using type = uint2; };
-template <>
-struct Vec<2> { using type = uint32_t; };
-template <>
-struct Vec<1> { using type = uint16_t; };
-
-// One item: two vectors of V elements, as 32-bit words of two (V = 1: one
-// element in a word's low half).
-template <int V>
-struct Item {
-  static constexpr int W = V > 1 ? V / 2 : 1;
-  union Half {
-    typename Vec<V>::type v;
-    uint32_t w[W];
-    __device__ Half() : w{} {}
-  } p1, p2;
-};
-
-template <int Q>
-struct alignas(4 * Q) Angles {
-  float a[Q];
-};
-
-// x / d for x below 2^31 and 0 < d < 2^31 by a product: d in (2^(l-1), 2^l],
-// magic = ceil(2^(31 + l) / d), x magic >> (31 + l).  magic exceeds 2^(31 + l) / d by
-// less than 1, so the product x / d by less than x / 2^(31 + l) < 2^-l <= 1 / d: too
-// little to reach the next integer.
-struct Divide {
-  unsigned d = 1, magic = 1u << 31;
-  int shift = 31;
-
-  Divide() = default;
-  explicit Divide(unsigned by) : d(by) {
-    int l = 0;
-    while ((1u << l) < d) ++l;
-    shift = 31 + l;
-    magic = static_cast<unsigned>(((1ull << shift) + d - 1) / d);
-  }
-  __device__ unsigned operator()(unsigned x) const {
-    return static_cast<unsigned>(static_cast<unsigned long long>(x) * magic >> shift);
-  }
-};
-
-// How the work is dealt out.
-struct Deal {
-  unsigned rows;     // tokens
-  int tok_shift;     // log2 of the tokens a block
-  bool head_major;   // a head's tokens lie side by side
-  Divide length;     // rows of a batch entry or sequence
-};
-
-// Where a token goes, found once a block.
-struct Token {
-  long long k, v;  // append: element offsets of head 0 in the caches
-  int pos;
-  int flags;       // bit 0: a row of some sequence; bit 1: its cache row exists
-};
-
-// frac(f / 2 pi) in 64-bit fixed point, by integers alone: FP64 units are few.
-// f = m 2^e, finite, with m below 2^53; C is 1 / 2 pi in double precision, as an
-// integer.
-__device__ __forceinline__ unsigned long long turns_of(double f) {
-  constexpr unsigned long long C = static_cast<unsigned long long>(0.15915494309189535 * 73786976294838206464.0);  // 2^66
-  const long long bits = __double_as_longlong(f);
-  const int field = static_cast<int>(bits >> 52) & 2047;
-  const unsigned long long m = (bits & ((1ll << 52) - 1)) | (field ? 1ull << 52 : 0);
-  const unsigned long long hi = __umul64hi(m, C), lo = m * C;
-  const int s = 1077 - max(field, 1);  // F = m C 2^-s
-  const unsigned long long F = s >= 128  ? 0
-                               : s >= 64 ? hi >> (s - 64)
-                               : s > 0   ? lo >> s | hi << (64 - s)
-                               : s > -64 ? lo << -s
-                                         : 0;
-  return bits < 0 ? 0 - F : F;
-}
-
-// The sequence of packed row t: the first b with cu[b + 1] > t (B if none),
-// counted by a whole warp with independent loads.
-__device__ __forceinline__ int sequence_of(const int* cu, int B, int t, int lane) {
-  int n = 0;
-  for (int b0 = 0; b0 < B; b0 += 32) {
-    const int b = b0 + lane;
-    n += __popc(__ballot_sync(0xffffffffu, b < B && cu[b + 1] <= t));
-  }
-  return n;
-}
-
 template <typename T, int D, int V, bool IL, bool APPEND>
-__global__ void __launch_bounds__(kThreads, 5) rotary_kernel(const __grid_constant__ RotaryArgs a,
+__global__ void __launch_bounds__(kRotaryThreads, 5) rotary_kernel(const __grid_constant__ RotaryArgs a,
                                                           const __grid_constant__ Deal deal) {
   constexpr int S = D / (2 * V);  // items a head
-  constexpr int Q = V < 4 ? V : 4;  // angles a vector load
-  __shared__ alignas(16) float cos_s[kMaxTok * (D / 2)], sin_s[kMaxTok * (D / 2)];
-  __shared__ unsigned long long turns_s[D / 2];
-  __shared__ float factor_s[D / 2];  // of a pair's cos and sin: NaN where its frequency is not finite
-  __shared__ Token tk[kMaxTok];
+  __shared__ AngleTable<D> angles;
+  __shared__ Token tk[kRotaryTokens];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -161,7 +61,7 @@ __global__ void __launch_bounds__(kThreads, 5) rotary_kernel(const __grid_consta
   // that lie side by side.
   using VT = typename Vec<V>::type;
   using I = Item<V>;
-  constexpr int ROWS = kThreads / S;
+  constexpr int ROWS = kRotaryThreads / S;
   const int half = a.inv_freq ? a.rot >> 1 : 0;
   const int heads = a.Hq + a.Hk + (APPEND ? a.Hk : 0), HL = ROWS >> deal.tok_shift;
   const int slot = tid % S, r = tid / S;
@@ -193,62 +93,14 @@ __global__ void __launch_bounds__(kThreads, 5) rotary_kernel(const __grid_consta
   I x;
   load(hl, x);
 
-  for (int f = tid; f < half; f += kThreads) {
-    const double freq = a.inv_freq[f];
-    turns_s[f] = turns_of(freq);
-    factor_s[f] = isfinite(freq) ? a.factor : __int_as_float(0x7fffffff);
-  }
-  // Each token by one warp (kMaxTok <= warps).
+  read_frequencies<D>(a, half, angles);
+  // Each token by one warp (kRotaryTokens <= warps).
   if (warp < nt) {
-    const unsigned t = t0 + warp;
-    Token k{};
-    if constexpr (APPEND) {
-      int b, i, n;
-      if (a.nt.cu_seqlens) {
-        b = sequence_of(a.nt.cu_seqlens, a.nt.B, static_cast<int>(t), lane);
-        i = n = 0;
-        if (b < a.nt.B) {
-          const int c0 = a.nt.cu_seqlens[b];
-          i = static_cast<int>(t) - c0;
-          n = a.nt.cu_seqlens[b + 1] - c0;
-        }
-      } else {
-        b = static_cast<int>(deal.length(t));
-        n = a.nt.each;
-        i = static_cast<int>(t) - b * n;
-      }
-      if (b < a.nt.B && i >= 0) {  // a row of some sequence
-        k.flags = 1;
-        k.pos = a.nt.seqlens[b] - n + i;
-        const int slot = k.pos >> a.pv.page_shift;
-        if (k.pos >= 0 && slot < a.pv.max_pages) {
-          const int page = a.pv.table[b * a.pv.table_stride + slot];
-          if (page >= 0 && page < a.pv.num_pages) {
-            const int row = k.pos & (a.pv.page_size - 1);
-            k.k = page * a.sko.b + row * a.sko.n;
-            k.v = page * a.svo.b + row * a.svo.n;
-            k.flags = 3;
-          }
-        }
-      }
-    } else {
-      const unsigned b = deal.length(t);
-      k.pos = a.positions[b * a.pos_stride + (t - b * deal.length.d)];
-    }
+    const Token k = find_token<APPEND>(a, deal, t0 + warp, lane);
     if (lane == 0) tk[warp] = k;
   }
   __syncthreads();
-  for (int i = tid; i < nt * half; i += kThreads) {
-    const int tt = i / half, f = i - tt * half;
-    const unsigned long long angle = static_cast<unsigned long long>(static_cast<long long>(tk[tt].pos)) * turns_s[f];
-    float s, c;
-    sincospif(static_cast<float>(static_cast<int>(angle >> 32)) * 4.656612873077393e-10f, &s, &c);  // 2^-31: half turns
-    // Runs of Q angles of neighbouring items side by side: the items' vector
-    // loads below then meet no bank twice.
-    const int at = tt * (D / 2) + f % V / Q * (S * Q) + f / V * Q + f % Q;
-    cos_s[at] = c * factor_s[f];
-    sin_s[at] = (a.inverse ? -s : s) * factor_s[f];
-  }
+  form_angles<D, V>(a, half, nt, tk, angles);
   __syncthreads();
   if (!live) return;
   const int flags = APPEND ? tk[t].flags : 3;
@@ -258,17 +110,8 @@ __global__ void __launch_bounds__(kThreads, 5) rotary_kernel(const __grid_consta
     load(h + HL, y);
     if (turned && h < hv) {
       float c[V], s[V];
-#pragma unroll
-      for (int i = 0; i < V / Q; ++i) {
-        const int at = t * (D / 2) + i * (S * Q) + slot * Q;
-        const Angles<Q> cc = *reinterpret_cast<const Angles<Q>*>(&cos_s[at]);
-        const Angles<Q> ss = *reinterpret_cast<const Angles<Q>*>(&sin_s[at]);
-#pragma unroll
-        for (int j = 0; j < Q; ++j) {
-          c[i * Q + j] = cc.a[j];
-          s[i * Q + j] = ss.a[j];
-        }
-      }
+      angle_load<D, V>(angles.cos + t * (D / 2), slot, c);
+      angle_load<D, V>(angles.sin + t * (D / 2), slot, s);
       if constexpr (V == 1) {
         const float x1 = E::unpack(x.p1.w[0]).x, x2 = E::unpack(x.p2.w[0]).x;
         x.p1.w[0] = E::pack(x1 * c[0] - x2 * s[0], 0.f);
@@ -309,16 +152,16 @@ template <typename T, int D, int V, bool IL>
 cudaError_t launch_t(const RotaryArgs& a, cudaStream_t stream) {
   // Several tokens a block (a power of two) once that still leaves eight blocks an
   // SM: 8,192 tokens with four 23.5 us, two (sixteen blocks) 25.3, one 29.
-  constexpr int kRows = kThreads / (D / (2 * V));
+  constexpr int kRows = kRotaryThreads / (D / (2 * V));
   Deal deal{};
   deal.rows = a.append ? a.nt.total : static_cast<unsigned>(a.B) * a.N;
-  while ((1 << deal.tok_shift) < std::min(kMaxTok, kRows) && deal.rows >> (deal.tok_shift + 1) >= 152 * 8)
+  while ((1 << deal.tok_shift) < std::min(kRotaryTokens, kRows) && deal.rows >> (deal.tok_shift + 1) >= 152 * 8)
     ++deal.tok_shift;
   deal.head_major = a.Hq > 0 ? a.sq.n < a.sq.h : a.sk.n < a.sk.h;
   deal.length = Divide(!a.append ? a.N : a.nt.each > 0 ? a.nt.each : 1);
   const unsigned grid = (deal.rows + (1u << deal.tok_shift) - 1) >> deal.tok_shift;
   auto kern = a.append ? rotary_kernel<T, D, V, IL, true> : rotary_kernel<T, D, V, IL, false>;
-  return launch_dependent("rotary kernel launch", kern, grid, kThreads, 0, stream, a, deal);
+  return launch_dependent("rotary kernel launch", kern, grid, kRotaryThreads, 0, stream, a, deal);
 }
 
 template <typename T, int D>

@@ -184,14 +184,118 @@ def rotary_backward(dq, dk=None, positions=None, inv_freq=None, interleaved: boo
     return _turn(dq, dk, positions, inv_freq, interleaved, True, factor, stream)
 
 
+# ---------------------------------------------------------------- norms of the heads, with the turn
+def attn_norm_rotary(q, q_out, k, k_out, positions, inv_freq, q_gain=None, k_gain=None, interleaved: bool = False,
+                     factor: float = 1.0, eps: float = 1e-6, stream=None) -> None:
+    """C ``attn_norm_rotary``: operands as ``attn_rotary``; gains [d] of one type,
+    float32, bfloat16 or float16, or None (all 1)."""
+    status = _native().norm_rotary(q, q_out, k, k_out, positions, inv_freq, q_gain, k_gain, interleaved, factor, eps, stream)
+    if status:
+        _check(status)
+
+
+def attn_norm_rotary_backward_workspace_size(B: int, N: int, d: int) -> int:
+    """C ``attn_norm_rotary_backward_workspace_size`` (bytes; 0 for invalid sizes)."""
+    return int(load().attn_norm_rotary_backward_workspace_size(B, N, d))
+
+
+def attn_norm_rotary_backward(dq, q, dq_out, dk, k, dk_out, positions, inv_freq, q_gain, k_gain, dq_gain, dk_gain,
+                              interleaved: bool, factor: float, eps: float, workspace, stream=None) -> None:
+    """C ``attn_norm_rotary_backward``: dq, q, dq_out of one shape, dk, k, dk_out
+    likewise or all None; gains as ``attn_norm_rotary``, their gradients [d] of the
+    same type, or None where they are not wanted."""
+    if q.numel() == 0 and (k is None or k.numel() == 0):
+        with on_stream(stream, q.device):
+            for g in (dq_gain, dk_gain):
+                if g is not None:
+                    g.zero_()
+    status = _native().norm_rotary_grad(dq, q, dq_out, dk, k, dk_out, positions, inv_freq, q_gain, k_gain, dq_gain, dk_gain,
+                                        interleaved, factor, eps, workspace, stream)
+    if status:
+        _check(status)
+
+
+def _places(q, positions, inv_freq, stream):
+    """The defaults of positions and frequencies: 0..N-1, and ``rotary_frequencies``'."""
+    if positions is None or inv_freq is None:
+        with on_stream(stream, q.device):
+            if positions is None:
+                positions = torch.arange(q.shape[2] if q.dim() == 4 else q.shape[0], dtype=torch.int32, device=q.device)
+            if inv_freq is None:
+                inv_freq, _ = rotary_frequencies(q.shape[-1], device=q.device)
+    return positions, inv_freq
+
+
+class _NormRotary(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, q_gain, k_gain, positions, inv_freq, interleaved, factor, eps):
+        ctx.save_for_backward(q, k, q_gain, k_gain, positions, inv_freq)
+        ctx.how = (interleaved, factor, eps)
+        return _norm_rotary(q, k, q_gain, k_gain, positions, inv_freq, interleaved, factor, eps)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dq, dk=None):
+        q, k, q_gain, k_gain, positions, inv_freq = ctx.saved_tensors
+        got = _norm_rotary_grad(_read(dq), _read(dk), q, k, q_gain, k_gain, positions, inv_freq, *ctx.how,
+                                want=ctx.needs_input_grad[2:4])
+        return (*got, None, None, None, None, None)
+
+
+def _norm_rotary(q, k, q_gain, k_gain, positions, inv_freq, interleaved, factor, eps):
+    status, qo, ko = _native().norm_rotary_new(q, k, positions, inv_freq, q_gain, k_gain, interleaved, factor, eps, None)
+    if status:
+        _check(status)
+    return qo if k is None else (qo, ko)
+
+
+def _norm_rotary_grad(dq, dk, q, k, q_gain, k_gain, positions, inv_freq, interleaved, factor, eps, want=(True, True)):
+    status, *got = _native().norm_rotary_grad_new(dq, dk, q, k, positions, inv_freq, q_gain, k_gain, want[0], want[1],
+                                                  interleaved, factor, eps, None)
+    if status:
+        _check(status)
+    return tuple(got)
+
+
+def norm_rotary(q, k=None, q_gain=None, k_gain=None, positions=None, inv_freq=None, interleaved: bool = False,
+                factor: float = 1.0, eps: float = 1e-6, stream=None):
+    """Each head of Q and K (or of Q alone) divided by its root mean square, scaled by
+    the gains [d] and turned to its position, in one pass: ``rotary`` of
+    ``gain * x / sqrt(mean(x ** 2) + eps)``, without a rounding between.  Gains:
+    float32, bfloat16 or float16 tensors of one type, or None (all 1); the other
+    arguments as ``rotary``.  Differentiable in q, k and the gains (once, in reverse
+    mode)."""
+    if _differentiated(q, k, q_gain, k_gain):
+        if stream is not None:
+            raise ValueError("norm_rotary under autograd runs on the current stream: use torch.cuda.stream(...)")
+        positions, inv_freq = _places(q, positions, inv_freq, None)
+        return _NormRotary.apply(q, k, q_gain, k_gain, positions, inv_freq, bool(interleaved), float(factor), float(eps))
+    with on_stream(stream, q.device):
+        positions, inv_freq = _places(q, positions, inv_freq, None)
+        return _norm_rotary(q, k, q_gain, k_gain, positions, inv_freq, interleaved, factor, eps)
+
+
+def norm_rotary_backward(dq, dk, q, k, q_gain=None, k_gain=None, positions=None, inv_freq=None, interleaved: bool = False,
+                         factor: float = 1.0, eps: float = 1e-6, stream=None):
+    """The gradient of ``norm_rotary`` with the same arguments: from the gradients of
+    its outputs those of q, k, q_gain and k_gain (None for what was None).  Not
+    differentiable."""
+    with on_stream(stream, q.device):
+        positions, inv_freq = _places(q, positions, inv_freq, None)
+        return _norm_rotary_grad(dq, dk, q, k, q_gain, k_gain, positions, inv_freq, interleaved, factor, eps)
+
+
 # ---------------------------------------------------------------- the cache
 def attn_cache_append(k, v, k_cache, v_cache, page_table, seqlens, cu_seqlens=None, q=None, q_out=None, inv_freq=None,
-                      interleaved: bool = False, factor: float = 1.0, stream=None) -> None:
+                      interleaved: bool = False, factor: float = 1.0, stream=None, q_gain=None, k_gain=None,
+                      eps: float = 1e-6) -> None:
     """C ``attn_cache_append``: k, v packed [total, Hkv, d] into the pages of their
     sequences; with ``inv_freq`` K is turned to its position, and q into q_out
-    ([total, Hq, d], which may be q) if given."""
+    ([total, Hq, d], which may be q) if given.  With gains (of K, and of Q where it is
+    given) C ``attn_cache_append_norm``: each head of them normalised first, as by
+    ``norm_rotary``; ``inv_freq`` may then be None."""
     status = _native().cache_append(k, v, k_cache, v_cache, page_table, seqlens, cu_seqlens, q, q_out, inv_freq, interleaved,
-                                    factor, stream)
+                                    factor, stream, q_gain, k_gain, eps)
     if status:
         _check(status)
 

@@ -156,7 +156,11 @@ int attn_bwd_d_and_dq(const void* q, const void* k, const void* v, const void* o
  *   {H*N*d, N*d, d}; contiguous [B, N, H, d] is {N*H*d, d, H*d}.  Rows of an
  *   output that overlap give undefined results.
  */
-typedef enum { EXATTN_DTYPE_BF16 = 0, EXATTN_DTYPE_F16 = 1 } exattn_dtype;
+typedef enum {
+  EXATTN_DTYPE_BF16 = 0,
+  EXATTN_DTYPE_F16 = 1,
+  EXATTN_DTYPE_F32 = 2 /* gains of the norms only (attn_norm_rotary) */
+} exattn_dtype;
 
 typedef struct {
   long long b_stride;
@@ -374,6 +378,48 @@ int attn_rotary(int dtype, const void* q, exattn_strides q_strides, void* q_out,
                 int inverse, float factor, int B, int N, int d, void* stream);
 
 /*
+ * The norm of each head of Q and K and the rotary turn in one pass: a row x (a
+ * token's head) becomes
+ *     y = factor R(p) (g x / s),   s = sqrt(mean x^2 + eps),
+ * the mean over its d elements, R(p) the turn of attn_rotary at the row's position
+ * (the elements past rot_dim keep g x / s, without the factor, as there).
+ *   q_gain, k_gain : device [d], the gains g of all heads of Q and of K, of type
+ *     gain_dtype (EXATTN_DTYPE_BF16, _F16 or _F32; 2- or 4-byte aligned), or NULL:
+ *     all 1.
+ *   eps : finite, at least 0 (else EXATTN_ERR_VALUE).  Rows of zeros give zeros with
+ *     eps > 0 and NaN with eps = 0.
+ * The squares are summed in fp32: rows whose mean square passes its range (elements
+ * near 10^19 in bf16) give zeros.  Otherwise arguments, arithmetic and errors as
+ * attn_rotary; an output may be its own input.
+ *
+ * attn_norm_rotary_backward -- its gradient.  From dq, dk, the gradients of its
+ *   outputs, and its inputs q, k:
+ *     h = factor R(p)^T dy,  e = x / s,  dg = sum over rows of h e,
+ *     dx = (g h - e mean(g h e)) / s.
+ *   dq_out, dk_out : gradients of q and k; each may be its own dq / dk or q / k (same
+ *     address and strides), and overlaps no other operand otherwise.
+ *   dq_gain, dk_gain : device [d] of gain_dtype, written, or NULL (not wanted).  The
+ *     rows are summed in fp32 in an order that the sizes fix: results do not vary
+ *     from run to run.
+ *   workspace : device memory of attn_norm_rotary_backward_workspace_size bytes (0
+ *     for invalid sizes), 16-byte aligned; its contents need not be kept, and calls
+ *     that may run at the same time need one each.
+ */
+int attn_norm_rotary(int dtype, const void* q, exattn_strides q_strides, void* q_out, exattn_strides qo_strides, int Hq,
+                     const void* k, exattn_strides k_strides, void* k_out, exattn_strides ko_strides, int Hk,
+                     const int* positions, long long pos_stride, const double* inv_freq, int rot_dim, int interleaved,
+                     float factor, const void* q_gain, const void* k_gain, int gain_dtype, float eps, int B, int N, int d,
+                     void* stream);
+size_t attn_norm_rotary_backward_workspace_size(int B, int N, int d);
+int attn_norm_rotary_backward(int dtype, const void* dq, exattn_strides dq_strides, const void* q,
+                              exattn_strides q_strides, void* dq_out, exattn_strides dqo_strides, int Hq, const void* dk,
+                              exattn_strides dk_strides, const void* k, exattn_strides k_strides, void* dk_out,
+                              exattn_strides dko_strides, int Hk, const int* positions, long long pos_stride,
+                              const double* inv_freq, int rot_dim, int interleaved, float factor, const void* q_gain,
+                              const void* k_gain, int gain_dtype, float eps, void* dq_gain, void* dk_gain, int B, int N,
+                              int d, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * A paged key/value cache.  K and V live in pages of page_size rows, so that
  * sequences grow without being moved and share the pages of a common prefix.
  *   k_cache, v_cache : [num_pages, Hkv, page_size, d] views, described by
@@ -412,6 +458,20 @@ int attn_cache_append(int dtype, const void* q, exattn_strides q_strides, void* 
                       int num_pages, int page_size, const int* page_table, long long table_stride, int max_pages,
                       const int* seqlens, const int* cu_seqlens, int B, int total, int d, const double* inv_freq,
                       int rot_dim, int interleaved, float factor, void* stream);
+
+/*
+ * attn_cache_append_norm -- attn_cache_append with the norms of attn_norm_rotary on
+ *   the way: K (and Q) normalised and scaled by its gains, then turned; with
+ *   inv_freq NULL normalised only (q and q_out may then be given too).  V is stored
+ *   as it is.
+ */
+int attn_cache_append_norm(int dtype, const void* q, exattn_strides q_strides, void* q_out, exattn_strides qo_strides,
+                           int Hq, const void* k, exattn_strides k_strides, const void* v, exattn_strides v_strides,
+                           void* k_cache, exattn_strides kc_strides, void* v_cache, exattn_strides vc_strides, int Hkv,
+                           int num_pages, int page_size, const int* page_table, long long table_stride, int max_pages,
+                           const int* seqlens, const int* cu_seqlens, int B, int total, int d, const double* inv_freq,
+                           int rot_dim, int interleaved, float factor, const void* q_gain, const void* k_gain,
+                           int gain_dtype, float eps, void* stream);
 
 /*
  * attn_fwd_paged -- attention of new tokens over a paged cache: O = softmax(
