@@ -24,9 +24,10 @@ from ._lib import (EXPORTS, ExattnError, Strides, attn_bwd, attn_bwd_d_and_dq, a
                    attn_fwd_bwd_host_workspace_size, attn_fwd_decode_workspace_size, attn_fwd_ex, attn_fwd_varlen,
                    device_error, library_path, load, status_string, version, watchdog_check, watchdog_poll, watchdog_seen)
 from .host import HostStep, fwd_bwd_from_host
-from .paged import (attn_cache_append, attn_cache_copy, attn_fwd_paged, attn_fwd_paged_workspace_size, attn_norm_rotary,
+from .paged import (attn_cache_append, attn_cache_copy, attn_fwd_paged, attn_fwd_paged_shared,
+                    attn_fwd_paged_shared_workspace_size, attn_fwd_paged_workspace_size, attn_norm_rotary,
                     attn_norm_rotary_backward, attn_norm_rotary_backward_workspace_size, attn_rotary, forward_paged,
-                    norm_rotary, norm_rotary_backward, rotary, rotary_backward, rotary_frequencies)
+                    forward_paged_shared, norm_rotary, norm_rotary_backward, rotary, rotary_backward, rotary_frequencies)
 from .cache import OutOfPages, PagedCache, Step
 
 __all__ = ["attn_fwd", "attn_bwd", "attn_bwd_workspace_size", "attn_bwd_preprocess", "attn_bwd_dkdv",
@@ -37,7 +38,7 @@ __all__ = ["attn_fwd", "attn_bwd", "attn_bwd_workspace_size", "attn_bwd_preproce
            "attn_rotary", "attn_cache_append", "attn_cache_copy", "attn_fwd_paged",
            "attn_fwd_paged_workspace_size", "forward_paged", "rotary", "rotary_backward", "rotary_frequencies",
            "attn_norm_rotary", "attn_norm_rotary_backward", "attn_norm_rotary_backward_workspace_size", "norm_rotary",
-           "norm_rotary_backward",
+           "norm_rotary_backward", "attn_fwd_paged_shared", "attn_fwd_paged_shared_workspace_size", "forward_paged_shared",
            "PagedCache", "OutOfPages", "Step",
            "watchdog_check", "watchdog_poll", "status_string", "version", "load", "library_path", "ExattnError",
            "EXPORTS"]

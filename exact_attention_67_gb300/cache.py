@@ -8,21 +8,21 @@ on the host the page tables, lengths and reference counts of the sequences.
         cache.append(layer, step, k, v, q=q, q_out=q, inv_freq=freq, factor=factor)
         o, lse = cache.attend(layer, step, q)
     drafts = cache.fork(seq, 4)                          # share the prompt's pages
-    step = cache.extend(drafts, 1)                       # each gets its own last page
+    step = cache.extend(drafts, 1, shared=True)          # each gets its own last page; attend reads the prompt once
     cache.free(drafts[1:])
     cache.compact()
 
 Everything that moves or computes on the device runs in the library's kernels
-(attn_cache_append, attn_fwd_paged, attn_cache_copy)."""
+(attn_cache_append, attn_fwd_paged, attn_fwd_paged_shared, attn_cache_copy)."""
 from __future__ import annotations
 
 import heapq
-from dataclasses import dataclass
+from dataclasses import dataclass, replace
 from functools import cached_property
 
 import torch
 
-from .paged import attn_cache_append, attn_cache_copy, forward_paged, on_stream
+from .paged import attn_cache_append, attn_cache_copy, forward_paged, forward_paged_shared, on_stream
 
 
 class OutOfPages(RuntimeError):
@@ -40,11 +40,45 @@ class Step:
     cu_seqlens: torch.Tensor | None     # int32 [B + 1]; None where all have as many
     max_seqlen_q: int
     max_seqlen_k: int
+    cu_groups: torch.Tensor | None = None    # int32 [groups + 1]: neighbours that share rows; None: no groups
+    prefix_lens: torch.Tensor | None = None  # int32 [B]: rows that a sequence shares with its group
+    max_group_q: int = 0
 
     @cached_property
     def tokens(self) -> int:
         """Rows of the packed tensors."""
         return sum(self.new)
+
+
+def _shared_rows(a, b, page_size: int) -> int:
+    """Rows of the leading pages that two page lists have in common."""
+    lo, hi = 0, min(len(a), len(b))
+    while lo < hi:
+        mid = (lo + hi + 1) // 2
+        if a[lo:mid] == b[lo:mid]:
+            lo = mid
+        else:
+            hi = mid - 1
+    return lo * page_size
+
+
+def _groups(tables, before, page_size: int):
+    """Offsets of the groups of neighbours that share rows before their new tokens, and
+    each sequence's shared rows.  A group takes the next sequence in where that saves at
+    least as many reads: m sequences that share c rows save (m - 1) c.  The kernels share
+    whole tiles of 128 rows."""
+    offsets, shared = [0], []
+    common, count = before[0], 1
+    for i in range(1, len(tables)):
+        rows = min(common, before[i], _shared_rows(tables[offsets[-1]], tables[i], page_size)) // 128 * 128
+        if rows and count * rows >= (count - 1) * common:
+            common, count = rows, count + 1
+            continue
+        shared += [common if count > 1 else 0] * count
+        offsets.append(i)
+        common, count = before[i], 1
+    shared += [common if count > 1 else 0] * count
+    return offsets + [len(tables)], shared
 
 
 class PagedCache:
@@ -138,9 +172,11 @@ class PagedCache:
                 heapq.heappush(self._free, p)
 
     # ------------------------------------------------------------ a step
-    def extend(self, seqs, new, stream=None) -> Step:
+    def extend(self, seqs, new, stream=None, shared: bool = False) -> Step:
         """Room for ``new`` tokens (a number, or one a sequence) at the end of each
-        sequence.  A last page that is shared and will be written to is copied
+        sequence.  With ``shared`` neighbours in ``seqs`` that have their first pages in
+        common (``fork``) are taken as groups, whose shared rows ``attend`` streams once:
+        put such sequences side by side.  A last page that is shared and will be written to is copied
         first, for all sequences and layers in one launch.  Raises OutOfPages,
         changing nothing, if the pool is too small."""
         seqs = list(seqs)
@@ -176,7 +212,7 @@ class PagedCache:
                     pages[-1] = own[s]
                 pages.extend(next(fresh) for _ in range(g))
                 tables.append(pages)
-            step = self._step(seqs, new, tables, stream)
+            step = self._step(seqs, new, tables, stream, shared)
             if src:
                 self._copy(src, dst, stream)
         except BaseException:
@@ -192,7 +228,7 @@ class PagedCache:
             self._length[s] += n
         return step
 
-    def _step(self, seqs, new, tables, stream) -> Step:
+    def _step(self, seqs, new, tables, stream, shared) -> Step:
         B = len(seqs)
         lens = [self._length[s] + n for s, n in zip(seqs, new)]
         width = max(max(len(pages) for pages in tables), 1)
@@ -202,13 +238,21 @@ class PagedCache:
         offsets = [0]
         for n in new:
             offsets.append(offsets[-1] + n)
-        host = torch.tensor(rows + lens + offsets, dtype=torch.int32)
+        groups, prefix = _groups(tables, [self._length[s] for s in seqs], self.page_size) if shared else ([], [])
+        if not any(prefix):
+            groups, prefix = [], []
+        host = torch.tensor(rows + lens + offsets + prefix + groups, dtype=torch.int32)
         if self.pool.is_cuda:
             host = host.pin_memory()
         with on_stream(stream, self.pool.device):
             dev = host.to(self.pool.device, non_blocking=True)
-        return Step(tuple(seqs), tuple(new), dev[: B * width].view(B, width), dev[B * width: B * width + B],
-                    None if even else dev[B * width + B:], max(max(new), 1), max(max(lens), 1))
+        table, lens_d, offsets_d, prefix_d, groups_d = dev.split([B * width, B, B + 1, len(prefix), len(groups)])
+        step = Step(tuple(seqs), tuple(new), table.view(B, width), lens_d, None if even else offsets_d, max(max(new), 1),
+                    max(max(lens), 1))
+        if groups:
+            step = replace(step, cu_groups=groups_d, prefix_lens=prefix_d,
+                           max_group_q=max(1, *(offsets[j] - offsets[i] for i, j in zip(groups, groups[1:]))))
+        return step
 
     def append(self, layer: int, step: Step, k, v, q=None, q_out=None, inv_freq=None, interleaved: bool = False,
                factor: float = 1.0, stream=None, q_gain=None, k_gain=None, eps: float = 1e-6) -> None:
@@ -223,9 +267,14 @@ class PagedCache:
     def attend(self, layer: int, step: Step, q, causal: bool = True, scale: float | None = None, window: int = 0,
                stream=None):
         """Attention of the step's Q, [tokens, Hq, head_dim], over one layer of the
-        cache: O like q and the logsumexp [Hq, tokens] (``forward_paged``), padding's
+        cache: O like q and the logsumexp [Hq, tokens] (``forward_paged``; over a step
+        made with ``shared`` and without a window ``forward_paged_shared``), padding's
         rows as they happen to be."""
         self._rows(step, q)
+        if step.cu_groups is not None and window == 0:
+            return forward_paged_shared(q, self.k_cache(layer), self.v_cache(layer), step.page_table, step.seqlens,
+                                        step.cu_groups, step.prefix_lens, step.cu_seqlens, step.max_seqlen_q,
+                                        step.max_seqlen_k, step.max_group_q, causal, scale, stream)
         return forward_paged(q, self.k_cache(layer), self.v_cache(layer), step.page_table, step.seqlens, step.cu_seqlens,
                              step.max_seqlen_q, step.max_seqlen_k, causal, scale, stream, window)
 

@@ -507,33 +507,69 @@ int cache_append(PyObject* const* p) {
                            rot, il, factor, stream);
 }
 
+// The operands of an attention over pages.
+struct Attend {
+  const at::Tensor& q;
+  OnDevice on;
+  const Cache c;
+  const at::Tensor &o, &lse;
+  int64_t total, Hq;
+  Tables t;
+  // p: q, k_cache, v_cache, o, lse, page_table, seqlens, cu_seqlens
+  explicit Attend(PyObject* const* p)
+      : q(operand(p[0], "q", 3)), on(q), c(cache(p[1], p[2], q)), o(same(p[3], "o", q)), lse(tensor(p[4], "lse")),
+        total(q.size(0)), Hq(q.size(1)), t{} {
+    if (lse.scalar_type() != at::kFloat || lse.sizes() != at::IntArrayRef({Hq, total}) || !lse.is_contiguous())
+      bad_value("lse must be contiguous float32 [Hq, total]");
+    on.also(c.k);
+    on.also(c.v);
+    on.also(o);
+    on.also(lse);
+    t = tables(on, p[5], p[6], p[7], total);
+  }
+};
+
 // (q, k_cache, v_cache, o, lse, page_table, seqlens, cu_seqlens, max_seqlen_q, max_seqlen_k, causal, scale, workspace,
 //  stream, window)
 int fwd_paged(PyObject* const* p) {
-  const at::Tensor& q = operand(p[0], "q", 3);
-  OnDevice on(q);
-  const Cache c = cache(p[1], p[2], q);
-  const at::Tensor& o = same(p[3], "o", q);
-  const at::Tensor& lse = tensor(p[4], "lse");
-  const int64_t total = q.size(0), Hq = q.size(1);
-  if (lse.scalar_type() != at::kFloat || lse.sizes() != at::IntArrayRef({Hq, total}) || !lse.is_contiguous())
-    bad_value("lse must be contiguous float32 [Hq, total]");
-  on.also(c.k);
-  on.also(c.v);
-  on.also(o);
-  on.also(lse);
-  const Tables t = tables(on, p[5], p[6], p[7], total);
-  const Workspace ws(on, p[12]);
+  Attend a(p);
+  const Workspace ws(a.on, p[12]);
   const int mq = as_int(p[8], "max_seqlen_q"), mk = as_int(p[9], "max_seqlen_k"), causal = truth(p[10]);
   const float scale = as_float(p[11]);
   const int window = as_int(p[14], "window");
-  if (total == 0) return EXATTN_OK;
-  void* stream = on.enter(p[13]);
+  if (a.total == 0) return EXATTN_OK;
+  void* stream = a.on.enter(p[13]);
+  const Tables& t = a.t;
   const WithoutGil threads;
-  return attn_fwd_paged(dtype_of(q), q.data_ptr(), strides3(q), c.k.data_ptr(), strides4(c.k), c.v.data_ptr(),
-                        strides4(c.v), o.data_ptr(), strides3(o), static_cast<float*>(lse.data_ptr()), c.pages,
-                        c.page_size, t.table, t.row, t.pages, t.seqlens, t.cu, t.B, as_int(Hq, "Hq"), c.heads,
-                        as_int(total, "total"), mq, mk, as_int(q.size(2), "d"), causal, window, scale, ws.at, ws.bytes, stream);
+  return attn_fwd_paged(dtype_of(a.q), a.q.data_ptr(), strides3(a.q), a.c.k.data_ptr(), strides4(a.c.k), a.c.v.data_ptr(),
+                        strides4(a.c.v), a.o.data_ptr(), strides3(a.o), static_cast<float*>(a.lse.data_ptr()), a.c.pages,
+                        a.c.page_size, t.table, t.row, t.pages, t.seqlens, t.cu, t.B, as_int(a.Hq, "Hq"), a.c.heads,
+                        as_int(a.total, "total"), mq, mk, as_int(a.q.size(2), "d"), causal, window, scale, ws.at, ws.bytes,
+                        stream);
+}
+
+// (q, k_cache, v_cache, o, lse, page_table, seqlens, cu_seqlens, cu_groups, prefix_lens, max_seqlen_q, max_seqlen_k,
+//  max_group_q, causal, scale, workspace, stream)
+int fwd_paged_shared(PyObject* const* p) {
+  Attend a(p);
+  const Tables& t = a.t;
+  const int64_t groups = tensor(p[8], "cu_groups").numel() - 1;
+  const at::Tensor &cg = int32(p[8], "cu_groups", {groups + 1}), &pl = int32(p[9], "prefix_lens", {t.B});
+  a.on.also(cg);
+  a.on.also(pl);
+  const Workspace ws(a.on, p[15]);
+  const int mq = as_int(p[10], "max_seqlen_q"), mk = as_int(p[11], "max_seqlen_k"), mg = as_int(p[12], "max_group_q");
+  const int causal = truth(p[13]);
+  const float scale = as_float(p[14]);
+  if (a.total == 0) return EXATTN_OK;
+  void* stream = a.on.enter(p[16]);
+  const WithoutGil threads;
+  return attn_fwd_paged_shared(
+      dtype_of(a.q), a.q.data_ptr(), strides3(a.q), a.c.k.data_ptr(), strides4(a.c.k), a.c.v.data_ptr(), strides4(a.c.v),
+      a.o.data_ptr(), strides3(a.o), static_cast<float*>(a.lse.data_ptr()), a.c.pages, a.c.page_size, t.table, t.row, t.pages,
+      t.seqlens, t.cu, static_cast<const int*>(cg.data_ptr()), static_cast<const int*>(pl.data_ptr()), t.B,
+      static_cast<int>(std::max<int64_t>(groups, 0)), as_int(a.Hq, "Hq"), a.c.heads, as_int(a.total, "total"), mq, mk, mg,
+      as_int(a.q.size(2), "d"), causal, scale, ws.at, ws.bytes, stream);
 }
 
 // Host page numbers: an int32 tensor, or any sequence of ints (into `own`).
@@ -628,6 +664,7 @@ PyMethodDef kMethods[] = {
     method<norm_grad_new, 14>("norm_rotary_grad_new"),
     method<status<cache_append>, 16>("cache_append"),
     method<status<fwd_paged>, 15>("fwd_paged"),
+    method<status<fwd_paged_shared>, 17>("fwd_paged_shared"),
     method<status<cache_copy>, 4>("cache_copy"),
     {nullptr, nullptr, 0, nullptr}};
 

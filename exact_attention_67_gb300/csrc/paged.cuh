@@ -103,6 +103,32 @@ struct NormArgs {
 constexpr int kNormParts = 152 * 2;  // blocks of the gradient at most
 cudaError_t launch_norm_rotary(const NormArgs& a, cudaStream_t stream);
 
+// Attention over rows that several sequences share (attn_fwd_paged_shared): two lines of
+// units, one over the groups' shared rows, one over the sequences' own, each run by a
+// launch of its own, side by side on the GPU's SMs; then a join of every row's parts.
+enum : int { kNoLine = 0, kSharedLine = 1, kOwnLine = 2 };
+
+// Where a row's part of one line is.
+struct alignas(16) PagedRecord {
+  float ref, mass;  // rest = 0: of the result in the row buffer
+  int part;         // rest > 0: slot of its first piece; the next CTAs' follow
+  int rest;         // key tiles after the first piece
+};
+
+struct PagedShare {
+  int line;                // of this launch
+  const int* cu_groups;    // device [groups + 1]: sequences [cu_groups[g], cu_groups[g + 1]) share rows
+  const int* prefix;       // device [B]: rows that a sequence shares with its group
+  int groups;
+  bool causal;             // of the own line (the shared one needs no mask)
+  int sms;                 // that the two lines divide between them
+  int ctas[2];             // the two launches' grids
+  int unit_tokens[2];
+  int tile_time[2];        // relative time of a key tile in a line's kernel
+  PagedRecord* rec;        // this line's [total, Hq]
+  long long rows_at;       // this line's row buffer [total, Hq, d], floats from part_o on
+};
+
 // Attention of new tokens over a paged cache.  The query heads of a key head
 // (G of them) and consecutive new tokens share the rows (forward kernel) or
 // columns (decode kernel) of a unit: unit row r is token r / G, head r % G.
@@ -130,13 +156,17 @@ struct PagedArgs {
   struct PagedPlan* plan;   // [ctas]
   unsigned* err;
   int device;
+  PagedShare share;         // share.line = kNoLine: attn_fwd_paged
 };
 constexpr int kPagedDecodeCols = 32;  // query columns of the decode kernel at most
 constexpr int kPagedRows = 256;       // unit rows of the forward kernel: two query tiles
 cudaError_t launch_paged_decode(const PagedArgs& a, cudaStream_t stream);
+cudaError_t launch_paged_decode_shared(const PagedArgs& a, cudaStream_t stream);  // a line of a.share
 cudaError_t launch_paged_fwd(const PagedArgs& a, cudaStream_t stream);
 // Joins the pieces of the units that ended up on several CTAs.
 cudaError_t launch_paged_merge(const PagedArgs& a, cudaStream_t stream);
+// Joins every row's parts of the two lines (paged_join.cu).
+cudaError_t launch_paged_join(const PagedArgs& shared, const PagedArgs& own, cudaStream_t stream);
 
 struct CopyArgs {
   char* pool;

@@ -393,17 +393,65 @@ extern "C" size_t attn_fwd_paged_workspace_size(int B, int Hq, int Hkv, int tota
   return p.weights < 2e9 ? p.total_bytes : 0;
 }
 
-extern "C" int attn_fwd_paged(int dtype, const void* q, exattn_strides sq, const void* k_cache, exattn_strides skc,
-                              const void* v_cache, exattn_strides svc, void* o, exattn_strides so, float* lse,
-                              int num_pages, int page_size, const int* page_table, long long table_stride,
-                              int max_pages, const int* seqlens, const int* cu_seqlens, int B, int Hq, int Hkv,
-                              int total, int max_seqlen_q, int max_seqlen_k, int d, int causal, int window,
-                              float scale, void* workspace, size_t workspace_bytes, void* stream) {
+namespace {
+
+// The tensor map of packed queries, tiles of `tokens` tokens of one key head.
+bool query_map(CUtensorMap* m, int dt, const void* q, const exattn_strides& sq, int Hkv, int G, int total, int d, int tokens) {
+  // A stride along an axis of extent 1 is never used; the encoder gets a legal one.
+  auto bytes = [&](int extent, long long stride) { return static_cast<cuuint64_t>(extent > 1 ? stride : d) * 2; };
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(G), static_cast<cuuint64_t>(Hkv),
+                              static_cast<cuuint64_t>(total)};
+  const cuuint64_t str[3] = {bytes(G, sq.h_stride), bytes(Hkv, G * sq.h_stride), bytes(total, sq.n_stride)};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(G), 1, static_cast<cuuint32_t>(tokens)};
+  return encode_map(m, dt, 4, q, dims, str, box);
+}
+
+// The maps of a cache's K (i = 0) or V, and its steps in the view.
+int cache_map(CUtensorMap* m, PageView* pv, int i, int dt, const void* base, const exattn_strides& s, int num_pages, int Hkv,
+              int page_size, int d) {
+  // Pages and heads as one axis: places a common divisor of both strides apart.
+  const long long sb = num_pages > 1 ? s.b_stride : 0, sh = Hkv > 1 ? s.h_stride : 0;
+  const long long step = std::max(std::gcd(sb, sh), 8ll);
+  const long long page_step = sb / step, head_step = sh / step;
+  if (page_step >= (1ll << 31) || head_step >= (1ll << 31)) return EXATTN_ERR_SHAPE;  // the sums below: 2^62 each
+  const long long places = (num_pages - 1) * page_step + (Hkv - 1) * head_step + 1;
+  if (places >= (1ll << 31)) return EXATTN_ERR_SHAPE;
+  (i == 0 ? pv->k_page_step : pv->v_page_step) = static_cast<int>(page_step);
+  (i == 0 ? pv->k_head_step : pv->v_head_step) = static_cast<int>(head_step);
+  const cuuint64_t dims[5] = {64, 8, static_cast<cuuint64_t>(d / 64), static_cast<cuuint64_t>(page_size / 8),
+                              static_cast<cuuint64_t>(places)};
+  const cuuint64_t str[4] = {static_cast<cuuint64_t>(s.n_stride) * 2, 128, static_cast<cuuint64_t>(s.n_stride) * 16,
+                             static_cast<cuuint64_t>(step) * 2};
+  const cuuint32_t box[5] = {64, 8, static_cast<cuuint32_t>(d / 64), static_cast<cuuint32_t>(std::min(page_size, 128) / 8), 1};
+  return encode_map(m, dt, 5, base, dims, str, box) ? EXATTN_OK : EXATTN_ERR_CUDA;
+}
+
+// What a launch of an attention over pages has from its plan and its place in the
+// workspace.
+void plan_args(PagedArgs* a, const AttendPlan& plan, char* ws) {
+  a->tile_tokens = plan.tile_tokens;
+  a->cols = plan.cols;
+  a->rows = plan.rows;
+  a->ctas = plan.ctas;
+  a->unit_cost = plan.unit_cost;
+  a->min_chunk = plan.min_chunk;
+  a->plan = reinterpret_cast<exattn::PagedPlan*>(ws);
+  a->part_sum = reinterpret_cast<float2*>(ws + plan.plan_bytes);
+  a->part_o = reinterpret_cast<float*>(ws + plan.plan_bytes + plan.sum_bytes);
+}
+
+// Checks of an attention over pages that hold whatever its masks, and what its launches
+// have in common.
+int attend_args(PagedArgs* out, int dtype, const void* q, const exattn_strides& sq, const void* k_cache,
+                const exattn_strides& skc, const void* v_cache, const exattn_strides& svc, void* o, const exattn_strides& so,
+                float* lse, int num_pages, int page_size, const int* page_table, long long table_stride, int max_pages,
+                const int* seqlens, const int* cu_seqlens, int B, int Hq, int Hkv, int total, int max_seqlen_q,
+                int max_seqlen_k, int d, int causal, int window, float scale) {
   if (!q || !k_cache || !v_cache || !o || !lse || !page_table || !seqlens) return EXATTN_ERR_NULL;
   if (!known_dtype(dtype)) return EXATTN_ERR_UNSUPPORTED;
   int rc = check_paged(B, Hq, Hkv, total, max_seqlen_q, max_seqlen_k, d);
   if (rc != EXATTN_OK) return rc;
-  PagedArgs a{};
+  PagedArgs& a = *out;
   if ((rc = check_tokens(&a.nt, cu_seqlens, seqlens, B, total)) != EXATTN_OK) return rc;
   if ((rc = check_pages(&a.pv, page_table, table_stride, max_pages, num_pages, page_size, B, Hkv, skc, svc)) !=
       EXATTN_OK)
@@ -413,63 +461,51 @@ extern "C" int attn_fwd_paged(int dtype, const void* q, exattn_strides sq, const
     return EXATTN_ERR_ALIGN;
   if ((rc = check_strides(sq, 1, Hq, total)) != EXATTN_OK || (rc = check_strides(so, 1, Hq, total)) != EXATTN_OK)
     return rc;
-  const AttendPlan plan = paged_plan(B, Hq, Hkv, total, max_seqlen_q, max_seqlen_k, d);
-  if (plan.weights >= 2e9) return EXATTN_ERR_SHAPE;
-  if (!workspace || workspace_bytes < plan.total_bytes) return EXATTN_ERR_WORKSPACE;
-  if (!aligned(workspace, 16)) return EXATTN_ERR_ALIGN;
-  int dev = 0;
-  unsigned* err = nullptr;
-  if ((rc = setup_device(&dev, &err)) != EXATTN_OK) return rc;
-
-  const int dt = dtype == EXATTN_DTYPE_F16 ? kF16 : kBF16, G = Hq / Hkv;
-  CUtensorMap mq, mk, mv;
-  // A stride along an axis of extent 1 is never used; the encoder gets a legal one.
-  auto bytes = [&](int extent, long long stride) { return static_cast<cuuint64_t>(extent > 1 ? stride : d) * 2; };
-  {
-    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(G), static_cast<cuuint64_t>(Hkv),
-                                static_cast<cuuint64_t>(total)};
-    const cuuint64_t str[3] = {bytes(G, sq.h_stride), bytes(Hkv, G * sq.h_stride), bytes(total, sq.n_stride)};
-    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(G), 1, static_cast<cuuint32_t>(plan.tile_tokens)};
-    if (!encode_map(&mq, dt, 4, q, dims, str, box)) return EXATTN_ERR_CUDA;
-  }
-  for (int i = 0; i < 2; ++i) {
-    // Pages and heads as one axis: places a common divisor of both strides apart.
-    const exattn_strides& s = i == 0 ? skc : svc;
-    const long long sb = num_pages > 1 ? s.b_stride : 0, sh = Hkv > 1 ? s.h_stride : 0;
-    const long long step = std::max(std::gcd(sb, sh), 8ll);
-    const long long page_step = sb / step, head_step = sh / step;
-    if (page_step >= (1ll << 31) || head_step >= (1ll << 31)) return EXATTN_ERR_SHAPE;  // the sums below: 2^62 each
-    const long long places = (num_pages - 1) * page_step + (Hkv - 1) * head_step + 1;
-    if (places >= (1ll << 31)) return EXATTN_ERR_SHAPE;
-    (i == 0 ? a.pv.k_page_step : a.pv.v_page_step) = static_cast<int>(page_step);
-    (i == 0 ? a.pv.k_head_step : a.pv.v_head_step) = static_cast<int>(head_step);
-    const cuuint64_t dims[5] = {64, 8, static_cast<cuuint64_t>(d / 64), static_cast<cuuint64_t>(page_size / 8),
-                                static_cast<cuuint64_t>(places)};
-    const cuuint64_t str[4] = {static_cast<cuuint64_t>(s.n_stride) * 2, 128, static_cast<cuuint64_t>(s.n_stride) * 16,
-                               static_cast<cuuint64_t>(step) * 2};
-    const cuuint32_t box[5] = {64, 8, static_cast<cuuint32_t>(d / 64),
-                               static_cast<cuuint32_t>(std::min(page_size, 128) / 8), 1};
-    if (!encode_map(i == 0 ? &mk : &mv, dt, 5, i == 0 ? k_cache : v_cache, dims, str, box)) return EXATTN_ERR_CUDA;
-  }
-  a.tm_q = &mq;
-  a.tm_k = &mk;
-  a.tm_v = &mv;
   a.o = o;
   a.so = to_strides(so);
   a.lse = lse;
   a.Hkv = Hkv;
-  a.G = G;
+  a.G = Hq / Hkv;
   a.d = d;
-  a.dtype = dt;
+  a.dtype = element_type(dtype);
   a.max_q = max_seqlen_q;
   a.max_k = static_cast<int>(std::min<long long>(max_seqlen_k, static_cast<long long>(max_pages) * page_size));
   a.causal = causal ? 1 : 0;
   a.window = std::min(window, 1 << 30);
   a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
-  a.tile_tokens = plan.tile_tokens;
-  a.cols = plan.cols;
-  a.rows = plan.rows;
-  a.ctas = plan.ctas;
+  return EXATTN_OK;
+}
+
+cudaError_t launch_line(const PagedArgs& a, cudaStream_t stream) {
+  return a.cols ? launch_paged_decode(a, stream) : launch_paged_fwd(a, stream);
+}
+
+}  // namespace
+
+extern "C" int attn_fwd_paged(int dtype, const void* q, exattn_strides sq, const void* k_cache, exattn_strides skc,
+                              const void* v_cache, exattn_strides svc, void* o, exattn_strides so, float* lse,
+                              int num_pages, int page_size, const int* page_table, long long table_stride,
+                              int max_pages, const int* seqlens, const int* cu_seqlens, int B, int Hq, int Hkv,
+                              int total, int max_seqlen_q, int max_seqlen_k, int d, int causal, int window,
+                              float scale, void* workspace, size_t workspace_bytes, void* stream) {
+  PagedArgs a{};
+  int rc = attend_args(&a, dtype, q, sq, k_cache, skc, v_cache, svc, o, so, lse, num_pages, page_size, page_table, table_stride,
+                       max_pages, seqlens, cu_seqlens, B, Hq, Hkv, total, max_seqlen_q, max_seqlen_k, d, causal, window, scale);
+  if (rc != EXATTN_OK) return rc;
+  const AttendPlan plan = paged_plan(B, Hq, Hkv, total, max_seqlen_q, max_seqlen_k, d);
+  if (plan.weights >= 2e9) return EXATTN_ERR_SHAPE;
+  if (!workspace || workspace_bytes < plan.total_bytes) return EXATTN_ERR_WORKSPACE;
+  if (!aligned(workspace, 16)) return EXATTN_ERR_ALIGN;
+  if ((rc = setup_device(&a.device, &a.err)) != EXATTN_OK) return rc;
+  CUtensorMap mq, mk, mv;
+  if (!query_map(&mq, a.dtype, q, sq, Hkv, a.G, total, d, plan.tile_tokens)) return EXATTN_ERR_CUDA;
+  if ((rc = cache_map(&mk, &a.pv, 0, a.dtype, k_cache, skc, num_pages, Hkv, page_size, d)) != EXATTN_OK ||
+      (rc = cache_map(&mv, &a.pv, 1, a.dtype, v_cache, svc, num_pages, Hkv, page_size, d)) != EXATTN_OK)
+    return rc;
+  a.tm_q = &mq;
+  a.tm_k = &mk;
+  a.tm_v = &mv;
+  plan_args(&a, plan, static_cast<char*>(workspace));
   {
     // A unit's key tiles at most.  Short units are not cut: the merge takes some 3 us, a
     // tile 0.3 (decode) to 2.  Cut and whole: one next token at 500 keys, 8 key heads
@@ -481,15 +517,109 @@ extern "C" int attn_fwd_paged(int dtype, const void* q, exattn_strides sq, const
     const long long tiles = std::min((a.max_k + 127ll) / 128, span / 128 + 2);
     a.whole = tiles <= (2 * plan.units >= kSMs ? kWholeMany : kWholeFew);
   }
-  a.unit_cost = plan.unit_cost;
-  a.min_chunk = plan.min_chunk;
-  char* ws = static_cast<char*>(workspace);
-  a.plan = reinterpret_cast<exattn::PagedPlan*>(ws);
-  a.part_sum = reinterpret_cast<float2*>(ws + plan.plan_bytes);
-  a.part_o = reinterpret_cast<float*>(ws + plan.plan_bytes + plan.sum_bytes);
-  a.err = err;
-  a.device = dev;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if ((plan.cols ? launch_paged_decode(a, st) : launch_paged_fwd(a, st)) != cudaSuccess) return EXATTN_ERR_CUDA;
+  if (launch_line(a, st) != cudaSuccess) return EXATTN_ERR_CUDA;
   return a.whole || launch_paged_merge(a, st) == cudaSuccess ? EXATTN_OK : EXATTN_ERR_CUDA;
+}
+
+namespace {
+
+// How an attention behind shared rows is laid out: each line's plan, and its part of the
+// workspace (what attn_fwd_paged's has, then the row buffer and the records).
+struct SharedPlan {
+  AttendPlan line[2];
+  size_t at[2], rec_at[2], total_bytes;
+  bool fits;  // the lines' weights in 31 bits
+};
+
+SharedPlan shared_plan(int B, int groups, int Hq, int Hkv, int total, int max_q, int max_k, int max_group_q, int d) {
+  SharedPlan p{};
+  p.line[0] = paged_plan(groups, Hq, Hkv, total, max_group_q, max_k, d);
+  p.line[1] = paged_plan(B, Hq, Hkv, total, max_q, max_k, d);
+  // max_group_q chooses the kernel and sizes the grid; a larger group is only slower.
+  const int ut = (p.line[0].cols ? 1 : 2) * p.line[0].tile_tokens;
+  const double most = Hkv * (static_cast<double>(total) / ut + groups) *
+                      ((static_cast<double>(max_k) + 127) / 128 + p.line[0].unit_cost);
+  p.fits = most < 2e9 && p.line[1].weights < 2e9;
+  auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+  const size_t rows = static_cast<size_t>(total) * Hq;
+  for (int i = 0; i < 2; ++i) {
+    p.at[i] = p.total_bytes;
+    p.rec_at[i] = p.at[i] + p.line[i].total_bytes + up(rows * d * sizeof(float));
+    p.total_bytes = p.rec_at[i] + up(rows * sizeof(PagedRecord));
+  }
+  return p;
+}
+
+int check_shared(int groups, int max_group_q) {
+  return groups < 1 || groups >= (1 << 24) || max_group_q < 1 ? EXATTN_ERR_SHAPE : EXATTN_OK;
+}
+
+}  // namespace
+
+extern "C" size_t attn_fwd_paged_shared_workspace_size(int B, int groups, int Hq, int Hkv, int total, int max_seqlen_q,
+                                                       int max_seqlen_k, int max_group_q, int d) {
+  if (check_paged(B, Hq, Hkv, total, max_seqlen_q, max_seqlen_k, d) != EXATTN_OK ||
+      check_shared(groups, max_group_q) != EXATTN_OK)
+    return 0;
+  const SharedPlan p = shared_plan(B, groups, Hq, Hkv, total, max_seqlen_q, max_seqlen_k, max_group_q, d);
+  return p.fits ? p.total_bytes : 0;
+}
+
+extern "C" int attn_fwd_paged_shared(int dtype, const void* q, exattn_strides sq, const void* k_cache, exattn_strides skc,
+                                     const void* v_cache, exattn_strides svc, void* o, exattn_strides so, float* lse,
+                                     int num_pages, int page_size, const int* page_table, long long table_stride,
+                                     int max_pages, const int* seqlens, const int* cu_seqlens, const int* cu_groups,
+                                     const int* prefix_lens, int B, int groups, int Hq, int Hkv, int total,
+                                     int max_seqlen_q, int max_seqlen_k, int max_group_q, int d, int causal, float scale,
+                                     void* workspace, size_t workspace_bytes, void* stream) {
+  if (!cu_groups || !prefix_lens) return EXATTN_ERR_NULL;
+  PagedArgs a{};
+  int rc = attend_args(&a, dtype, q, sq, k_cache, skc, v_cache, svc, o, so, lse, num_pages, page_size, page_table, table_stride,
+                       max_pages, seqlens, cu_seqlens, B, Hq, Hkv, total, max_seqlen_q, max_seqlen_k, d, causal, 0, scale);
+  if (rc != EXATTN_OK || (rc = check_shared(groups, max_group_q)) != EXATTN_OK) return rc;
+  if (!aligned(cu_groups, 4) || !aligned(prefix_lens, 4)) return EXATTN_ERR_ALIGN;
+  const SharedPlan plan = shared_plan(B, groups, Hq, Hkv, total, max_seqlen_q, max_seqlen_k, max_group_q, d);
+  if (!plan.fits) return EXATTN_ERR_SHAPE;
+  if (!workspace || workspace_bytes < plan.total_bytes) return EXATTN_ERR_WORKSPACE;
+  if (!aligned(workspace, 16)) return EXATTN_ERR_ALIGN;
+  if ((rc = setup_device(&a.device, &a.err)) != EXATTN_OK) return rc;
+  CUtensorMap mq[2], mk, mv;
+  for (int i = 0; i < 2; ++i)
+    if (!query_map(&mq[i], a.dtype, q, sq, Hkv, a.G, total, d, plan.line[i].tile_tokens)) return EXATTN_ERR_CUDA;
+  if ((rc = cache_map(&mk, &a.pv, 0, a.dtype, k_cache, skc, num_pages, Hkv, page_size, d)) != EXATTN_OK ||
+      (rc = cache_map(&mv, &a.pv, 1, a.dtype, v_cache, svc, num_pages, Hkv, page_size, d)) != EXATTN_OK)
+    return rc;
+  a.tm_k = &mk;
+  a.tm_v = &mv;
+  PagedShare& s = a.share;
+  s.cu_groups = cu_groups;
+  s.prefix = prefix_lens;
+  s.groups = groups;
+  s.causal = a.causal;
+  s.sms = kSMs;
+  for (int i = 0; i < 2; ++i) {
+    const AttendPlan& l = plan.line[i];
+    s.ctas[i] = l.ctas;
+    s.unit_tokens[i] = (l.cols ? 1 : 2) * l.tile_tokens;
+    // Two query tiles of the forward kernel take half as long again as one, or as the
+    // decode kernel's columns.
+    const long long tokens = std::min(total, i == 0 ? max_group_q : max_seqlen_q);
+    s.tile_time[i] = !l.cols && tokens > l.tile_tokens ? 3 : 2;
+  }
+  PagedArgs lines[2] = {a, a};
+  for (int i = 0; i < 2; ++i) {
+    PagedArgs& l = lines[i];
+    const AttendPlan& p = plan.line[i];
+    char* ws = static_cast<char*>(workspace) + plan.at[i];
+    plan_args(&l, p, ws);
+    l.tm_q = &mq[i];
+    l.share.line = i == 0 ? kSharedLine : kOwnLine;
+    l.share.rec = reinterpret_cast<PagedRecord*>(static_cast<char*>(workspace) + plan.rec_at[i]);
+    l.share.rows_at = static_cast<long long>((p.total_bytes - p.plan_bytes - p.sum_bytes) / sizeof(float));
+    if (i == 0) l.causal = 0;
+  }
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (launch_line(lines[0], st) != cudaSuccess || launch_line(lines[1], st) != cudaSuccess) return EXATTN_ERR_CUDA;
+  return status_of(launch_paged_join(lines[0], lines[1], st));
 }

@@ -183,7 +183,7 @@ __device__ __forceinline__ float warp_columns(const float (&in)[NC], int lane, O
 
 }  // namespace
 
-template <typename T, int D, int NC>
+template <typename T, int D, int NC, bool SH>
 __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PagedArgs a) {
@@ -202,9 +202,9 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int UT = a.tile_tokens, G = a.G;
 
-  PagedCursor cur{};
+  PagedCursor<SH> cur{};
   PagedSeq seq{};
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (!SH || a.share.line == kOwnLine) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 32) {
     for (int b = 0; b < 2; ++b) {
       mbar_init(&bars->q_full[b], 1);
@@ -249,8 +249,8 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
   // Up to here this CTA may run beside the stream's last kernel.  The walking warp
   // finds its place in the line.
   if (warp == C::K_WARP) paged_touch(a);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (warp == C::K_WARP) cur = paged_start(a, UT, lane, &seq);
+  paged_wait<SH>(a);
+  if (warp == C::K_WARP) cur = paged_start<SH>(a, UT, lane, &seq);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -444,9 +444,11 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
         const float L = le == 0.f ? -INFINITY : (top + sum_log2(le)) * 0.6931471805599453f;
         const int t = static_cast<int>(q * gm >> 16), head = pc->h * G + q - t * G, prow = pc->s.row0 + pc->tok0 + t;
         const long long part = (static_cast<long long>(blockIdx.x) * 2 + pc->slot()) * NQ + q;
-        coef[q] = Column{c0 * inv, c1 * inv, whole ? prow * a.so.n + head * a.so.h : part * D};
+        const long long out = static_cast<long long>(prow) * (a.Hkv * G) + head;  // shared: row of the row buffer
+        coef[q] = Column{c0 * inv, c1 * inv, !whole ? part * D : SH ? a.share.rows_at + out * D : prow * a.so.n + head * a.so.h};
         if (ok && q < cols) {
-          if (whole) a.lse[static_cast<long long>(head) * a.nt.total + prow] = L;
+          if (SH) paged_record(a, *pc, out, part, le == 0.f ? -INFINITY : top, le);
+          else if (whole) a.lse[static_cast<long long>(head) * a.nt.total + prow] = L;
           else a.part_sum[part] = make_float2(le == 0.f ? -INFINITY : top, le);
         }
       }
@@ -466,7 +468,7 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
           auto value = [&](int i, const Column& c) {
             return (c.c0 != 0.f ? __uint_as_float(o0[i]) * c.c0 : 0.f) + (c.c1 != 0.f ? __uint_as_float(o1[i]) * c.c1 : 0.f);
           };
-          if (whole) {
+          if (whole && !SH) {
 #pragma unroll
             for (int i = 0; i < H; ++i) {
               const Column c = coef[w * H + i];
@@ -680,36 +682,46 @@ __global__ void __launch_bounds__(PdCfg<D, NC>::THREADS, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == C::S_WARP) tmem_dealloc(tmem, C::TM_COLS);
+  paged_end<SH>(a);
 }
 
 namespace {
 
-template <typename T, int D, int NC>
+template <typename T, int D, int NC, bool SH>
 cudaError_t launch_n(const PagedArgs& a, cudaStream_t stream) {
   using C = PdCfg<D, NC>;
-  auto kern = paged_decode_kernel<T, D, NC>;
+  auto kern = paged_decode_kernel<T, D, NC, SH>;
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), C::SMEM_BYTES, a.device);
   if (e != cudaSuccess) return e;
   return launch_dependent("paged decode kernel launch", kern, a.ctas, C::THREADS, C::SMEM_BYTES, stream, *a.tm_q, *a.tm_k,
                           *a.tm_v, a);
 }
 
-template <typename T, int D>
+template <typename T, int D, bool SH>
 cudaError_t launch_t(const PagedArgs& a, cudaStream_t stream) {
   switch (a.cols) {
-    case 4: return launch_n<T, D, 4>(a, stream);
-    case 8: return launch_n<T, D, 8>(a, stream);
-    case 16: return launch_n<T, D, 16>(a, stream);
-    case 32: return launch_n<T, D, 32>(a, stream);
+    case 4: return launch_n<T, D, 4, SH>(a, stream);
+    case 8: return launch_n<T, D, 8, SH>(a, stream);
+    case 16: return launch_n<T, D, 16, SH>(a, stream);
+    case 32: return launch_n<T, D, 32, SH>(a, stream);
     default: return note_cuda(cudaErrorInvalidValue, "paged decode kernel (columns)");
   }
 }
 
+template <bool SH>
+cudaError_t launch_s(const PagedArgs& a, cudaStream_t stream) {
+  if (a.dtype == kF16) return a.d == 64 ? launch_t<__half, 64, SH>(a, stream) : launch_t<__half, 128, SH>(a, stream);
+  return a.d == 64 ? launch_t<__nv_bfloat16, 64, SH>(a, stream) : launch_t<__nv_bfloat16, 128, SH>(a, stream);
+}
+
 }  // namespace
 
+#ifdef EXATTN_PAGED_SHARED
+cudaError_t launch_paged_decode_shared(const PagedArgs& a, cudaStream_t stream) { return launch_s<true>(a, stream); }
+#else
 cudaError_t launch_paged_decode(const PagedArgs& a, cudaStream_t stream) {
-  if (a.dtype == kF16) return a.d == 64 ? launch_t<__half, 64>(a, stream) : launch_t<__half, 128>(a, stream);
-  return a.d == 64 ? launch_t<__nv_bfloat16, 64>(a, stream) : launch_t<__nv_bfloat16, 128>(a, stream);
+  return a.share.line ? launch_paged_decode_shared(a, stream) : launch_s<false>(a, stream);
 }
+#endif
 
 }  // namespace exattn

@@ -87,18 +87,18 @@ struct PfBars {
 
 // Key tiles of piece p that query tile t (tokens [tok0 + t TT, ...)) takes part
 // in, counted from p.t_lo.
-__device__ __forceinline__ int tiles_of(const PagedArgs& a, const PagedPiece& p, int t) {
+__device__ __forceinline__ int tiles_of(const PagedArgs& a, const PagedPiece& p, int t, int key0) {
   const int t0 = p.tok0 + t * a.tile_tokens, t1 = min(p.tok0 + p.ntok, t0 + a.tile_tokens);
   if (t0 >= t1) return 0;
   int lo, hi;
-  paged_keys(a, p.s, t0, t1, &lo, &hi);
+  paged_keys(a, p.s, t0, t1, &lo, &hi, key0, a.causal);
   if (hi <= lo) return 0;
   return max(0, min((hi + kKeyTile - 1) / kKeyTile, p.t_hi) - p.t_lo);
 }
 
 }  // namespace
 
-template <typename T, int D>
+template <typename T, int D, bool SH>
 __global__ void __launch_bounds__(512, 1)
     paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PagedArgs a) {
@@ -114,9 +114,9 @@ __global__ void __launch_bounds__(512, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int TT = a.tile_tokens, UT = 2 * TT, G = a.G;
 
-  PagedCursor cur{};
+  PagedCursor<SH> cur{};
   PagedSeq seq{};
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (!SH || a.share.line == kOwnLine) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 32) {
     mbar_init(&bars->q_full, 1);
     mbar_init(&bars->q_empty, C::ISSUERS);
@@ -147,8 +147,8 @@ __global__ void __launch_bounds__(512, 1)
   // Up to here this CTA may run beside the stream's last kernel.  The walking warp
   // finds its place in the line.
   if (warp == C::K_WARP) paged_touch(a);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (warp == C::K_WARP) cur = paged_start(a, UT, lane, &seq);
+  paged_wait<SH>(a);
+  if (warp == C::K_WARP) cur = paged_start<SH>(a, UT, lane, &seq);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -316,6 +316,10 @@ __global__ void __launch_bounds__(512, 1)
       const long long part = (static_cast<long long>(blockIdx.x) * 2 + pc->slot()) * 2 + t;
       float4* po = reinterpret_cast<float4*>(a.part_o + part * 128 * D) + row;
       T* orow = static_cast<T*>(a.o) + prow * a.so.n + head * a.so.h;
+      // Shared: row by row, a lane's 16 columns side by side.
+      const long long out = static_cast<long long>(prow) * (a.Hkv * G) + head;
+      float* prow_o = SH ? a.part_o + (whole ? a.share.rows_at + out * D : (part * 128 + row) * D) : nullptr;
+      if (SH && live) paged_record(a, *pc, out, part * 128 + row, m_ref - kLift, le);
       ring.release(i);
 #pragma unroll 1
       for (int c = 0; c < D; c += 16) {
@@ -330,7 +334,13 @@ __global__ void __launch_bounds__(512, 1)
           asm volatile("" : "+r"(o_r[e]));
           v[e] = l == 0.f || n == 0 ? 0.f : __uint_as_float(o_r[e]) * inv_l;
         }
-        if (!whole) {
+        if constexpr (SH) {
+          if (live && n > 0) {
+#pragma unroll
+            for (int v4 = 0; v4 < 4; ++v4)
+              reinterpret_cast<float4*>(prow_o + c)[v4] = make_float4(v[4 * v4], v[4 * v4 + 1], v[4 * v4 + 2], v[4 * v4 + 3]);
+          }
+        } else if (!whole) {
           if (n > 0) {
 #pragma unroll
             for (int v4 = 0; v4 < 4; ++v4)
@@ -349,7 +359,8 @@ __global__ void __launch_bounds__(512, 1)
         tc_fence_before();
         mbar_arrive_warp(&bars->o_free[t]);
       }
-      if (whole) {
+      if constexpr (SH) {
+      } else if (whole) {
         if (live) a.lse[static_cast<long long>(head) * a.nt.total + prow] = L;
       } else {
         a.part_sum[part * 128 + row] = make_float2(m_ref - kLift, le);
@@ -418,7 +429,7 @@ __global__ void __launch_bounds__(512, 1)
         if (is_k) {
           const bool more = cur.next(a, UT, seq, &pc);
           if (more && pc.t_hi > pc.t_lo) pages.start(a, pc, lane);
-          for (int t = 0; t < 2; ++t) pc.n[t] = more ? tiles_of(a, pc, t) : 0;
+          for (int t = 0; t < 2; ++t) pc.n[t] = more ? tiles_of(a, pc, t, SH ? cur.key0 : 0) : 0;
           if (!(ok = ring.put(i, more ? &pc : nullptr, lane, wc)) || !more) break;
         } else {
           const PagedPiece* p = ring.get(i, wc);
@@ -568,25 +579,31 @@ __global__ void __launch_bounds__(512, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == C::MMA_WARP) tmem_dealloc(tmem, C::TM_COLS);
+  paged_end<SH>(a);
 }
 
 namespace {
 
-template <typename T, int D>
+template <typename T, int D, bool SH>
 cudaError_t launch_t(const PagedArgs& a, cudaStream_t stream) {
   using C = PfCfg<D>;
-  auto kern = paged_fwd_kernel<T, D>;
+  auto kern = paged_fwd_kernel<T, D, SH>;
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), C::SMEM_BYTES, a.device);
   if (e != cudaSuccess) return e;
   return launch_dependent("paged forward kernel launch", kern, a.ctas, C::THREADS, C::SMEM_BYTES, stream, *a.tm_q, *a.tm_k,
                           *a.tm_v, a);
 }
 
+template <bool SH>
+cudaError_t launch_s(const PagedArgs& a, cudaStream_t stream) {
+  if (a.dtype == kF16) return a.d == 64 ? launch_t<__half, 64, SH>(a, stream) : launch_t<__half, 128, SH>(a, stream);
+  return a.d == 64 ? launch_t<__nv_bfloat16, 64, SH>(a, stream) : launch_t<__nv_bfloat16, 128, SH>(a, stream);
+}
+
 }  // namespace
 
 cudaError_t launch_paged_fwd(const PagedArgs& a, cudaStream_t stream) {
-  if (a.dtype == kF16) return a.d == 64 ? launch_t<__half, 64>(a, stream) : launch_t<__half, 128>(a, stream);
-  return a.d == 64 ? launch_t<__nv_bfloat16, 64>(a, stream) : launch_t<__nv_bfloat16, 128>(a, stream);
+  return a.share.line ? launch_s<true>(a, stream) : launch_s<false>(a, stream);
 }
 
 }  // namespace exattn

@@ -64,11 +64,41 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedArgs& a, int b) {
   return s;
 }
 
+// A line of units over shared rows (PagedShare): item b of the launch's line and its
+// first key, a tile's first.  Rows that fill a shared tile in part count as a sequence's
+// own.  The shared line's items are groups: `off`, which no mask of theirs needs, is the
+// sequence whose pages they read.
+__device__ __forceinline__ int shared_rows(const PagedArgs& a, int b) {
+  return min(max(a.share.prefix[b], 0), a.max_k) & ~(kKeyTile - 1);
+}
+__device__ __forceinline__ int line_items(const PagedArgs& a, int line) {
+  return line == kSharedLine ? a.share.groups : a.nt.B;
+}
+__device__ __forceinline__ PagedSeq line_seq(const PagedArgs& a, int line, int b, int* key0) {
+  if (line != kSharedLine) {
+    *key0 = line == kOwnLine ? shared_rows(a, b) : 0;
+    return paged_seq(a, b);
+  }
+  *key0 = 0;
+  const int f = min(max(a.share.cu_groups[b], 0), a.nt.B), e = min(max(a.share.cu_groups[b + 1], f), a.nt.B);
+  PagedSeq s{0, 0, 0, f};
+  if (e > f) {
+    int c0 = f * a.nt.each, c1 = e * a.nt.each;
+    if (a.nt.cu_seqlens) {
+      c0 = min(max(a.nt.cu_seqlens[f], 0), a.nt.total);
+      c1 = min(max(a.nt.cu_seqlens[e], c0), a.nt.total);
+    }
+    s = PagedSeq{c0, c1 - c0, shared_rows(a, f), f};
+  }
+  return s;
+}
+
 // Keys that some of the tokens [t0, t1) of a sequence see: [lo, hi).
-__device__ __forceinline__ void paged_keys(const PagedArgs& a, const PagedSeq& s, int t0, int t1, int* lo, int* hi) {
-  *lo = a.window > 0 ? max(0, s.off + t0 - a.window + 1) : 0;
+__device__ __forceinline__ void paged_keys(const PagedArgs& a, const PagedSeq& s, int t0, int t1, int* lo, int* hi, int key0,
+                                           bool causal) {
+  *lo = a.window > 0 ? max(0, s.off + t0 - a.window + 1) : key0;
   int e = s.len;
-  if (a.causal) e = min(e, s.off + t1);
+  if (causal) e = min(e, s.off + t1);
   else if (a.window > 0) e = min(e, s.off + t1 - 1 + a.window);
   *hi = max(e, *lo);
 }
@@ -120,12 +150,15 @@ struct PagedRing {
   __device__ void release(int i) { mbar_arrive_warp(&empty[i % kRing]); }
 };
 
-// A place in the line and the way through it.  UT: tokens a unit.
+// A place in the line and the way through it.  UT: tokens a unit.  SH: a line over
+// shared rows, or of what follows them.
+template <bool SH>
 struct PagedCursor {
   int b, h, t;
   int pos;    // weights of unit t already passed
   int cost;   // fixed weight of a unit
   int left;   // weights left of this CTA's chunk
+  int key0;   // first key of sequence b
 
   // The next piece with anything to do (an empty unit has its zeros to
   // write); false at the chunk's end.
@@ -135,21 +168,22 @@ struct PagedCursor {
         t = 0;
         if (++h >= a.Hkv || s.n <= 0) {
           h = 0;
-          if (++b >= a.nt.B) {
+          if (++b >= (SH ? line_items(a, a.share.line) : a.nt.B)) {
             left = 0;
             return false;
           }
-          s = paged_seq(a, b);
+          if constexpr (SH) s = line_seq(a, a.share.line, b, &key0);
+          else s = paged_seq(a, b);
         }
       }
       const int t0 = t * UT, t1 = min(s.n, t0 + UT);
       int lo, hi;
-      paged_keys(a, s, t0, t1, &lo, &hi);
+      paged_keys(a, s, t0, t1, &lo, &hi, SH ? key0 : 0, a.causal);
       const int k0 = lo / kKeyTile, k1 = hi > lo ? (hi + kKeyTile - 1) / kKeyTile : k0;
       const int w = k1 - k0 + cost;
       const int take = a.whole ? w : min(left, w - pos);
       p->s = s;
-      p->b = b;
+      p->b = SH && a.share.line == kSharedLine ? s.off : b;
       p->h = h;
       p->tok0 = t0;
       p->ntok = t1 - t0;
@@ -173,17 +207,43 @@ struct PagedCursor {
 };
 
 // Key tiles of the unit of tokens [t0, t0 + UT).
-__device__ __forceinline__ int paged_tiles(const PagedArgs& a, const PagedSeq& s, int t0, int UT) {
+__device__ __forceinline__ int paged_tiles(const PagedArgs& a, const PagedSeq& s, int t0, int UT, int key0, bool causal) {
   int lo, hi;
-  paged_keys(a, s, t0, min(s.n, t0 + UT), &lo, &hi);
+  paged_keys(a, s, t0, min(s.n, t0 + UT), &lo, &hi, key0, causal);
   return hi > lo ? (hi + kKeyTile - 1) / kKeyTile - lo / kKeyTile : 0;
 }
 
 // Weight of a sequence's units with one key head.
-__device__ __forceinline__ int paged_weight(const PagedArgs& a, const PagedSeq& s, int UT) {
+__device__ __forceinline__ int paged_weight(const PagedArgs& a, const PagedSeq& s, int UT, int key0, bool causal) {
   int w = 0;
-  for (int t0 = 0; t0 < s.n; t0 += UT) w += paged_tiles(a, s, t0, UT) + a.unit_cost;
+  for (int t0 = 0; t0 < s.n; t0 += UT) w += paged_tiles(a, s, t0, UT, key0, causal) + a.unit_cost;
   return w;
+}
+
+// The same on either line, and the whole line's, by a warp.  (Groups' tokens all see the
+// same keys: no loop over runs, and no mask.)
+__device__ __forceinline__ int line_weight(const PagedArgs& a, int line, const PagedSeq& s, int UT, int key0) {
+  if (line == kSharedLine) return (s.n + UT - 1) / UT * (s.len / kKeyTile + a.unit_cost);
+  return paged_weight(a, s, UT, key0, a.share.causal);
+}
+__device__ __forceinline__ int line_total(const PagedArgs& a, int line, int lane) {
+  int sum = 0;
+  for (int b = lane; b < line_items(a, line); b += 32) {
+    int key0;
+    const PagedSeq s = line_seq(a, line, b, &key0);
+    sum += line_weight(a, line, s, a.share.unit_tokens[line - 1], key0);
+  }
+  return __reduce_add_sync(0xffffffffu, sum) * a.Hkv;
+}
+
+// CTAs that work on `line` when the two weigh w[0] and w[1]: as many of the SMs as its
+// share of the time, the same numbers in both launches.
+__device__ __forceinline__ int line_ctas(const PagedArgs& a, int line, int w_shared, int w_own) {
+  const PagedShare& s = a.share;
+  const float t1 = static_cast<float>(w_shared) * static_cast<float>(s.tile_time[0]);
+  const float t2 = static_cast<float>(w_own) * static_cast<float>(s.tile_time[1]);
+  const int first = min(min(max(static_cast<int>(rintf(s.sms * (t1 / (t1 + t2)))), 1), s.sms - 1), s.ctas[0]);
+  return line == kSharedLine ? first : min(s.sms - first, s.ctas[1]);
 }
 
 // What the merge needs of the boundary before a CTA's chunk.
@@ -216,15 +276,29 @@ __device__ __forceinline__ void paged_touch(const PagedArgs& a) {
 // Start of this CTA's chunk, found by one warp; the same in every lane.  Leaves
 // the merge its PagedPlan.  The line's weights fit 31 bits (checked on the host
 // against the largest that the sizes allow).
-__device__ __forceinline__ PagedCursor paged_start(const PagedArgs& a, int UT, int lane, PagedSeq* seq) {
-  const int B = a.nt.B, cta = static_cast<int>(blockIdx.x);
-  auto read = [&](int b) { return b < B ? paged_seq(a, b) : PagedSeq{0, 0, 0, 0}; };
-  const PagedSeq s0 = read(lane);
-  const int w0 = paged_weight(a, s0, UT);  // kept: most batches have at most 32 sequences
-  int sum = w0, most = w0, least = w0 > 0 ? w0 : INT_MAX, count = w0 > 0;
+template <bool SH>
+__device__ __forceinline__ PagedCursor<SH> paged_start(const PagedArgs& a, int UT, int lane, PagedSeq* seq) {
+  const int line = SH ? a.share.line : kNoLine, B = SH ? line_items(a, line) : a.nt.B, cta = static_cast<int>(blockIdx.x);
+  auto read = [&](int b, int* key0) {
+    *key0 = 0;
+    if (b >= B) return PagedSeq{0, 0, 0, 0};
+    if constexpr (SH) return line_seq(a, line, b, key0);
+    else return paged_seq(a, b);
+  };
+  auto weight = [&](const PagedSeq& s, int key0) {
+    if constexpr (SH) return line_weight(a, line, s, UT, key0);
+    else return paged_weight(a, s, UT, 0, a.causal);
+  };
+  int k0;
+  const PagedSeq s0 = read(lane, &k0);
+  const int w0 = weight(s0, k0);  // kept: most batches have at most 32 sequences
+  int sum = w0, most = w0, least = w0 > 0 ? w0 : INT_MAX, count = w0 > 0, longest = s0.n;
   for (int b = 32 + lane; b < B; b += 32) {
-    const int w = paged_weight(a, paged_seq(a, b), UT);
+    int kb;
+    const PagedSeq s = read(b, &kb);
+    const int w = weight(s, kb);
     sum += w;
+    longest = max(longest, s.n);
     most = max(most, w);
     least = min(least, w > 0 ? w : INT_MAX);
     count += w > 0;
@@ -234,16 +308,23 @@ __device__ __forceinline__ PagedCursor paged_start(const PagedArgs& a, int UT, i
   least = __reduce_min_sync(0xffffffffu, least);
   const int units = __reduce_add_sync(0xffffffffu, count) * a.Hkv, tiles_each = most - a.unit_cost;
   int W = sum * a.Hkv, cost = a.unit_cost;
-  int chunk = max(paged_div(W + a.ctas - 1, a.ctas), a.min_chunk);
+  int ctas = a.ctas;
+  bool single = true;  // a unit is a (sequence, key head)
+  if constexpr (SH) {
+    const int other = line_total(a, kSharedLine + kOwnLine - line, lane);
+    ctas = line == kSharedLine ? line_ctas(a, line, W, other) : line_ctas(a, line, other, W);
+    single = __reduce_max_sync(0xffffffffu, longest) <= UT;
+  }
+  int chunk = max(paged_div(W + ctas - 1, ctas), a.min_chunk);
   // The decode kernel, where a unit is a (sequence, key head), and all weigh the same.
-  if (a.cols > 0 && most == least && tiles_each > 0 && units <= a.ctas) {
+  if (a.cols > 0 && single && most == least && tiles_each > 0 && units <= ctas) {
     // As many pieces a unit as CTAs, of two tiles at least; none of four or fewer
     // (joining pieces takes some 2 us, a tile 0.6).  Unless this leaves over a
     // quarter of the SMs out of long work.
-    const int most_pieces = paged_div(a.ctas, units);
+    const int most_pieces = paged_div(ctas, units);
     const int each = tiles_each <= 4 || a.whole ? tiles_each : max(paged_div(tiles_each + most_pieces - 1, most_pieces), 2);
     const int k = paged_div(tiles_each + each - 1, each);
-    if (4 * units * k >= 3 * a.ctas || each <= 4 || a.whole) {
+    if (4 * units * k >= 3 * ctas || each <= 4 || a.whole) {
       chunk = each;
       cost = k * chunk - tiles_each;  // less than a chunk: the first piece's tiles are fewer by it
       W = units * k * chunk;
@@ -251,14 +332,15 @@ __device__ __forceinline__ PagedCursor paged_start(const PagedArgs& a, int UT, i
   }
   const long long lo64 = static_cast<long long>(cta) * chunk;
   const int pad = cost - a.unit_cost;  // of every unit's weight
-  PagedCursor c{0, 0, 0, 0, cost, 0};
+  PagedCursor<SH> c{0, 0, 0, 0, cost, 0, 0};
   PagedPlan plan{0, chunk, 0, cost, 0, 0, 0, 0};
   *seq = PagedSeq{0, 0, 0, 0};
   int before = 0;
   for (int b0 = 0; b0 < B && lo64 < W; b0 += 32) {
     const int lo = static_cast<int>(lo64);
-    const PagedSeq sl = b0 == 0 ? s0 : read(b0 + lane);
-    int w = b0 == 0 ? w0 : paged_weight(a, sl, UT);
+    int kl = k0;
+    const PagedSeq sl = b0 == 0 ? s0 : read(b0 + lane, &kl);
+    int w = b0 == 0 ? w0 : weight(sl, kl);
     if (w > 0) w += pad;  // not 0 only where a sequence has one unit a key head
     const int per_head = w;
     w *= a.Hkv;
@@ -276,6 +358,7 @@ __device__ __forceinline__ PagedCursor paged_start(const PagedArgs& a, int UT, i
       s.n = __shfl_sync(0xffffffffu, sl.n, l);
       s.len = __shfl_sync(0xffffffffu, sl.len, l);
       s.off = __shfl_sync(0xffffffffu, sl.off, l);
+      if constexpr (SH) c.key0 = __shfl_sync(0xffffffffu, kl, l);
       const int each_head = __shfl_sync(0xffffffffu, per_head, l);
       int r = lo - before - __shfl_sync(0xffffffffu, inc - w, l);
       c.left = min(chunk, W - lo);
@@ -284,7 +367,7 @@ __device__ __forceinline__ PagedCursor paged_start(const PagedArgs& a, int UT, i
       r -= c.h * each_head;
       int tiles;
       for (;;) {
-        tiles = paged_tiles(a, s, c.t * UT, UT);
+        tiles = paged_tiles(a, s, c.t * UT, UT, SH ? c.key0 : 0, a.causal);
         if (r < tiles + cost) break;
         r -= tiles + cost;
         ++c.t;
@@ -303,6 +386,32 @@ __device__ __forceinline__ PagedCursor paged_start(const PagedArgs& a, int UT, i
   }
   if (lane == 0) a.plan[cta] = plan;
   return c;
+}
+
+// The shared line's launch waits for the stream before it lets the own line's begin, so
+// that one may read its operands at once; that one waits at its end, so that what
+// follows it follows both.
+template <bool SH>
+__device__ __forceinline__ void paged_wait(const PagedArgs& a) {
+  if (SH && a.share.line == kOwnLine) return;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (SH) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+template <bool SH>
+__device__ __forceinline__ void paged_end(const PagedArgs& a) {
+  if (SH && a.share.line == kOwnLine) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// Leaves the join a row's part of a piece: `out` its row of the row buffer, `part` its
+// slot.  A unit's first piece says where the others are.
+__device__ __forceinline__ void paged_record(const PagedArgs& a, const PagedPiece& p, long long out, long long part, float ref,
+                                             float mass) {
+  if (p.whole()) {
+    a.share.rec[out] = PagedRecord{ref, mass, 0, 0};
+    return;
+  }
+  a.part_sum[part] = make_float2(ref, mass);
+  if (p.t_lo == p.k_lo) a.share.rec[out] = PagedRecord{0.f, 0.f, static_cast<int>(part), p.k_hi - p.t_hi};
 }
 
 // The page numbers of a piece's tiles, read 32 boxes at a time and as many ahead (one

@@ -344,6 +344,57 @@ def forward_paged(q, k_cache, v_cache, page_table, seqlens, cu_seqlens=None, max
     return o, lse
 
 
+def attn_fwd_paged_shared_workspace_size(B: int, groups: int, Hq: int, Hkv: int, total: int, max_seqlen_q: int,
+                                         max_seqlen_k: int, max_group_q: int, d: int) -> int:
+    """C ``attn_fwd_paged_shared_workspace_size`` (bytes; 0 for invalid sizes)."""
+    return int(load().attn_fwd_paged_shared_workspace_size(B, groups, Hq, Hkv, total, max_seqlen_q, max_seqlen_k, max_group_q,
+                                                           d))
+
+
+def attn_fwd_paged_shared(q, k_cache, v_cache, o, lse, page_table, seqlens, cu_seqlens, cu_groups, prefix_lens,
+                          max_seqlen_q: int, max_seqlen_k: int, max_group_q: int, causal: bool, scale: float, workspace,
+                          stream=None) -> None:
+    """C ``attn_fwd_paged_shared``: ``attn_fwd_paged`` where the sequences of a group
+    (offsets cu_groups int32 [groups + 1]) have their first prefix_lens (int32 [B]) rows
+    on the same pages, which are streamed once for the group."""
+    status = _native().fwd_paged_shared(q, k_cache, v_cache, o, lse, page_table, seqlens, cu_seqlens, cu_groups, prefix_lens,
+                                        max_seqlen_q, max_seqlen_k, max_group_q, causal, scale, workspace, stream)
+    if status:
+        _check(status)
+
+
+def forward_paged_shared(q, k_cache, v_cache, page_table, seqlens, cu_groups, prefix_lens, cu_seqlens=None,
+                         max_seqlen_q: int | None = None, max_seqlen_k: int | None = None, max_group_q: int | None = None,
+                         causal: bool = True, scale: float | None = None, stream=None):
+    """``forward_paged`` for a batch whose sequences share their first pages: group g is
+    the sequences [cu_groups[g], cu_groups[g + 1]) (int32 [groups + 1] on the device),
+    whose first prefix_lens[b] rows (int32 [B], the same within a group, all new tokens
+    behind them; 0 for none) are on the same pages.  These are streamed once for the
+    group's new tokens.  ``max_group_q``, the largest count of a group's new tokens,
+    defaults to total: give it where it is known.  The rest, and what is returned, as
+    ``forward_paged``.  Not differentiable."""
+    if not q.is_cuda:
+        raise ValueError("all device operands must be CUDA tensors")
+    total, Hq, d = q.shape
+    B, groups = page_table.shape[0], cu_groups.numel() - 1
+    if max_seqlen_q is None:
+        max_seqlen_q = total if cu_seqlens is not None else total // max(B, 1)
+    if max_seqlen_k is None:
+        max_seqlen_k = page_table.shape[1] * k_cache.shape[2]
+    if max_group_q is None:
+        max_group_q = total
+    nbytes = attn_fwd_paged_shared_workspace_size(B, groups, Hq, k_cache.shape[1], total, max_seqlen_q, max_seqlen_k,
+                                                  max_group_q, d)
+    with on_stream(stream, q.device):
+        o = torch.empty_like(q)
+        lse = torch.empty((Hq, total), dtype=torch.float32, device=q.device)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        watchdog_step(q.device, lambda: attn_fwd_paged_shared(
+            q, k_cache, v_cache, o, lse, page_table, seqlens, cu_seqlens, cu_groups, prefix_lens, max_seqlen_q, max_seqlen_k,
+            max_group_q, causal, d ** -0.5 if scale is None else scale, ws, None))
+    return o, lse
+
+
 def attn_cache_copy(pool, src, dst, stream=None) -> None:
     """C ``attn_cache_copy``: pool [slabs, num_pages, ...] (each page dense; slabs are
     layers' K and V; a single cache passes as ``x.unsqueeze(0)``), src and dst

@@ -515,6 +515,37 @@ int attn_fwd_paged(int dtype, const void* q, exattn_strides q_strides, const voi
                    size_t workspace_bytes, void* stream);
 
 /*
+ * attn_fwd_paged_shared -- attn_fwd_paged (without a window) for a batch whose
+ *   sequences share their first pages: samples of one prompt, chats behind one system
+ *   prompt.  The rows that a group of sequences shares are streamed once for the new
+ *   tokens of all of them, then joined with each sequence's own rows.
+ *   cu_groups   : device int32 [groups + 1], non-decreasing offsets of consecutive
+ *     sequences, cu_groups[0] = 0 and cu_groups[groups] = B: group g is sequences
+ *     [cu_groups[g], cu_groups[g + 1]).
+ *   prefix_lens : device int32 [B], the same within a group: its sequences have their
+ *     first prefix_lens[b] rows on the same pages, and all their new tokens behind
+ *     them (prefix_lens[b] <= seqlens[b] minus the new tokens of b).  0: nothing is
+ *     shared.  Rows that fill a tile of 128 only in part are taken as each sequence's
+ *     own.
+ *   max_group_q : the largest count of a group's new tokens; it chooses how the shared
+ *     rows are streamed, a larger group is only slower.
+ *   The group's first sequence names the shared pages.  Tables that break these rules
+ *   give wrong results but no access out of bounds.  Arguments, layout, arithmetic and
+ *   errors otherwise as attn_fwd_paged; workspace as there, of
+ *   attn_fwd_paged_shared_workspace_size bytes (it holds fp32 results of every row
+ *   twice, for the join).
+ */
+size_t attn_fwd_paged_shared_workspace_size(int B, int groups, int Hq, int Hkv, int total, int max_seqlen_q,
+                                            int max_seqlen_k, int max_group_q, int d);
+int attn_fwd_paged_shared(int dtype, const void* q, exattn_strides q_strides, const void* k_cache,
+                          exattn_strides kc_strides, const void* v_cache, exattn_strides vc_strides, void* o,
+                          exattn_strides o_strides, float* lse, int num_pages, int page_size, const int* page_table,
+                          long long table_stride, int max_pages, const int* seqlens, const int* cu_seqlens,
+                          const int* cu_groups, const int* prefix_lens, int B, int groups, int Hq, int Hkv, int total,
+                          int max_seqlen_q, int max_seqlen_k, int max_group_q, int d, int causal, float scale,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * attn_cache_copy -- page dst[i] of every slab becomes a copy of page src[i],
  *   for i in [0, n): the partly filled last page of a forked sequence, or the
  *   moves that compact a fragmented pool.

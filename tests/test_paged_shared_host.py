@@ -1,0 +1,131 @@
+"""Attention behind shared rows, without a GPU: what its C call refuses, its workspace,
+and how PagedCache finds the groups."""
+import pytest
+import torch
+
+P = [0x100000 + 0x100000 * i for i in range(16)]
+NULL, SHAPE, ALIGN, UNSUPPORTED, WORKSPACE, VALUE = 1, 2, 3, 4, 6, 9
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from exact_attention_67_gb300 import build as b
+    b.build()
+    from exact_attention_67_gb300 import _lib
+    return _lib.load()
+
+
+def call(lib, dtype=0, q=P[0], kc=P[1], vc=P[2], o=P[3], lse=P[4], table=P[5], lens=P[6], cu=None, groups_at=P[7], prefix=P[8], B=4, groups=2,
+         Hq=8, Hk=2, total=4, mq=1, mk=1000, mg=2, d=64, scale=0.125, ws=P[9], ws_bytes=1 << 30, ps=16, sq=None):
+    from exact_attention_67_gb300 import Strides
+    s = Strides(0, 64, 512)
+    c = Strides(2 * 16 * 64, 16 * 64, 64)
+    return lib.attn_fwd_paged_shared(dtype, q, sq or s, kc, c, vc, c, o, s, lse, 100, ps, table, 64, 64, lens, cu, groups_at, prefix, B, groups,
+                                     Hq, Hk, total, mq, mk, mg, d, 1, scale, ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("how,status", [
+    (dict(q=None), NULL), (dict(groups_at=None), NULL), (dict(prefix=None), NULL), (dict(table=None), NULL), (dict(lse=None), NULL),
+    (dict(dtype=2), UNSUPPORTED), (dict(d=96), UNSUPPORTED), (dict(ps=24), UNSUPPORTED), (dict(Hq=9), SHAPE), (dict(groups=0), SHAPE),
+    (dict(groups=-1), SHAPE), (dict(mg=0), SHAPE), (dict(mq=0), SHAPE), (dict(total=6), SHAPE), (dict(groups_at=P[7] + 2), ALIGN),
+    (dict(prefix=P[8] + 1), ALIGN), (dict(q=P[0] + 8), ALIGN), (dict(scale=0.0), VALUE), (dict(scale=float("nan")), VALUE),
+    (dict(ws=None), WORKSPACE), (dict(ws_bytes=1000), WORKSPACE), (dict(ws=P[9] + 8), ALIGN),
+    (dict(mk=(1 << 30) - 1, Hk=8, B=1 << 20, total=1 << 20), SHAPE)])
+def test_refusals(lib, how, status):
+    assert call(lib, **how) == status
+
+
+def test_workspace_size(lib):
+    def size(B=4, groups=2, Hq=8, Hk=2, total=4, mq=1, mk=1000, mg=2, d=64):
+        return lib.attn_fwd_paged_shared_workspace_size(B, groups, Hq, Hk, total, mq, mk, mg, d)
+    n = size()
+    assert n > 2 * 4 * 8 * (64 * 4 + 16) and call(lib, ws_bytes=n - 1) == WORKSPACE
+    assert size(total=4000, B=4000) > n and size(mg=1 << 30) > 0
+    for bad in (dict(groups=0), dict(mg=0), dict(B=0), dict(Hq=7), dict(d=32), dict(mk=0), dict(Hq=256, Hk=1)):
+        assert size(**bad) == 0
+
+
+def test_python_refusals():
+    import exact_attention_67_gb300 as ex
+    q = torch.zeros(2, 2, 64, dtype=torch.bfloat16)
+    c = torch.zeros(4, 1, 16, 64, dtype=torch.bfloat16)
+    i = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA"):
+        ex.forward_paged_shared(q, c, c, torch.zeros(2, 2, dtype=torch.int32), i, i, i)
+
+
+# ---------------------------------------------------------------- PagedCache
+def cache_of(pages=200, ps=16):
+    from exact_attention_67_gb300 import PagedCache
+    return PagedCache(pages, ps, 1, 1, 64, device="cpu")
+
+
+@pytest.fixture()
+def no_copies(monkeypatch):
+    from exact_attention_67_gb300 import cache
+    monkeypatch.setattr(cache, "attn_cache_copy", lambda *a: None)
+
+
+def groups(step):
+    return None if step.cu_groups is None else (step.cu_groups.tolist(), step.prefix_lens.tolist(), step.max_group_q)
+
+
+def test_groups_of_forks(no_copies):
+    c = cache_of()
+    a, b = c.add(), c.add()
+    c.extend([a, b], [300, 200])
+    fa, fb = c.fork(a, 3), c.fork(b, 2)
+    # 300 rows: 18 whole pages (and a part that each copies before it writes), 256 in whole tiles.
+    step = c.extend([*fa, b, *fb], 1, shared=True)
+    assert groups(step) == ([0, 3, 6], [256] * 3 + [128] * 3, 3)
+    assert c.extend([*fa, b, *fb], 0, shared=True).cu_groups.tolist() == [0, 3, 6]
+    # Order matters: only neighbours are taken together.
+    assert groups(c.extend([fa[0], fb[0], fa[1], fb[1]], 1, shared=True)) is None
+    assert groups(c.extend([fa[0], fa[1]], [5, 2], shared=True)) == ([0, 2], [256, 256], 7)
+    # Not asked for, and nothing shared.
+    assert groups(c.extend([fa[0], fa[1]], 1)) is None
+    d = c.add()
+    c.extend([d], 256)
+    assert groups(c.extend([a, d], 1, shared=True)) is None
+
+
+def test_groups_take_in_what_saves_reads(no_copies):
+    c = cache_of(2000)
+    root = c.add()
+    c.extend([root], 256)
+    deep = c.fork(root, 1)[0]
+    c.extend([deep], 1024 - 256)
+    same = c.fork(deep, 3)
+    # Four share 1024 rows; taking in the root's 256 would save 4 * 256 rows instead of 3 * 1024.
+    assert groups(c.extend([deep, *same, root], 1, shared=True)) == ([0, 4, 5], [1024] * 4 + [0], 4)
+    # One alone goes with whoever shares a tile.
+    assert groups(c.extend([root, deep], 1, shared=True)) == ([0, 2], [256] * 2, 2)
+
+
+def test_rows_that_new_tokens_stand_on_are_not_shared(no_copies):
+    """A fork of an empty or short sequence, and new tokens that begin inside the common
+    pages after a truncation: shared rows end before the first new token of each."""
+    c = cache_of()
+    a = c.add()
+    c.extend([a], 400)
+    f, g = c.fork(a, 2)
+    c.truncate(f, 200)
+    step = c.extend([f, g, a], 1, shared=True)
+    n, p, m = groups(step)
+    assert n == [0, 1, 3] and p == [0, 384, 384] or n == [0, 3] and p == [128] * 3
+    for s, rows in zip(step.ids, p):
+        assert rows <= c.length(s) - 1
+    e = c.add()
+    c.extend([e], 0)
+    assert groups(c.extend([e, c.fork(e)[0]], 3, shared=True)) is None
+
+
+def test_out_of_pages_leaves_the_cache(no_copies):
+    from exact_attention_67_gb300 import OutOfPages
+    c = cache_of(20)
+    a = c.add()
+    c.extend([a], 300)
+    forks = c.fork(a, 2)
+    with pytest.raises(OutOfPages):
+        c.extend(forks, 16, shared=True)
+    assert c.free_pages == 1 and [c.length(s) for s in forks] == [300, 300]
