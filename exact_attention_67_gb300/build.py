@@ -24,8 +24,9 @@ OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libexattn.so")
 BINDING = os.path.join(OUT_DIR, "_exattn_binding.so")
 SOURCES = ["api.cu", "fwd.cu", "merge.cu", "bwd.cu", "dq.cu", "decode.cu", "noalloc.cu", "host.cu",
-           "paged_api.cu", "rotary.cu", "norm_rotary.cu", "pages.cu", "paged_decode.cu", "paged_decode_shared.cu", "paged_fwd.cu",
-           "paged_merge.cu", "paged_join.cu"]
+           "paged_api.cu", "rotary.cu", "norm_rotary.cu", "pages.cu", "paged_decode.cu", "paged_fwd.cu", "paged_merge.cu",
+           "paged_shared_bf16_64.cu", "paged_shared_bf16_128.cu", "paged_shared_f16_64.cu", "paged_shared_f16_128.cu",
+           "paged_join.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr",
          "-I", INCLUDE, "-I", CSRC]

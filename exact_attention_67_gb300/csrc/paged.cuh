@@ -104,8 +104,8 @@ constexpr int kNormParts = 152 * 2;  // blocks of the gradient at most
 cudaError_t launch_norm_rotary(const NormArgs& a, cudaStream_t stream);
 
 // Attention over rows that several sequences share (attn_fwd_paged_shared): two lines of
-// units, one over the groups' shared rows, one over the sequences' own, each run by a
-// launch of its own, side by side on the GPU's SMs; then a join of every row's parts.
+// units, one over the groups' shared rows, one over the sequences' own, side by side on
+// the GPU's SMs in one launch; then a join of every row's parts.
 enum : int { kNoLine = 0, kSharedLine = 1, kOwnLine = 2 };
 
 // Where a row's part of one line is.
@@ -116,13 +116,12 @@ struct alignas(16) PagedRecord {
 };
 
 struct PagedShare {
-  int line;                // of this launch
+  int line;                // of these arguments
   const int* cu_groups;    // device [groups + 1]: sequences [cu_groups[g], cu_groups[g + 1]) share rows
   const int* prefix;       // device [B]: rows that a sequence shares with its group
   int groups;
-  bool causal;             // of the own line (the shared one needs no mask)
   int sms;                 // that the two lines divide between them
-  int ctas[2];             // the two launches' grids
+  int ctas[2];             // that each has room for at most
   int unit_tokens[2];
   int tile_time[2];        // relative time of a key tile in a line's kernel
   PagedRecord* rec;        // this line's [total, Hq]
@@ -161,11 +160,18 @@ struct PagedArgs {
 constexpr int kPagedDecodeCols = 32;  // query columns of the decode kernel at most
 constexpr int kPagedRows = 256;       // unit rows of the forward kernel: two query tiles
 cudaError_t launch_paged_decode(const PagedArgs& a, cudaStream_t stream);
-cudaError_t launch_paged_decode_shared(const PagedArgs& a, cudaStream_t stream);  // a line of a.share
 cudaError_t launch_paged_fwd(const PagedArgs& a, cudaStream_t stream);
 // Joins the pieces of the units that ended up on several CTAs.
 cudaError_t launch_paged_merge(const PagedArgs& a, cudaStream_t stream);
-// Joins every row's parts of the two lines (paged_join.cu).
+// The two lines behind shared rows (paged_shared.cuh), arguments by line, then the join of
+// every row's parts (paged_join.cu).
+struct PagedLines {
+  PagedArgs line[2];
+};
+cudaError_t launch_paged_shared_bf16_64(const PagedLines& a, cudaStream_t stream);
+cudaError_t launch_paged_shared_bf16_128(const PagedLines& a, cudaStream_t stream);
+cudaError_t launch_paged_shared_f16_64(const PagedLines& a, cudaStream_t stream);
+cudaError_t launch_paged_shared_f16_128(const PagedLines& a, cudaStream_t stream);
 cudaError_t launch_paged_join(const PagedArgs& shared, const PagedArgs& own, cudaStream_t stream);
 
 struct CopyArgs {

@@ -348,12 +348,13 @@ struct AttendPlan {
   double units, weights;  // of the line, at most
 };
 
-AttendPlan paged_plan(int B, int Hq, int Hkv, int total, int max_q, int max_k, int d) {
+// shared: the line over shared rows, whose decode kernel has 8 or 32 columns.
+AttendPlan paged_plan(int B, int Hq, int Hkv, int total, int max_q, int max_k, int d, bool shared = false) {
   AttendPlan p{};
   const int G = Hq / Hkv;
   max_q = std::min(max_q, total);
   const long long need = static_cast<long long>(max_q) * G;
-  p.cols = need <= 4 ? 4 : need <= 8 ? 8 : need <= 16 ? 16 : need <= kPagedDecodeCols ? 32 : 0;
+  p.cols = shared && need <= kPagedDecodeCols ? (need <= 8 ? 8 : 32) : need <= 4 ? 4 : need <= 8 ? 8 : need <= 16 ? 16 : need <= kPagedDecodeCols ? 32 : 0;
   p.rows = p.cols ? std::max(p.cols, 16) : kPagedRows;
   p.tile_tokens = (p.cols ? p.cols : 128) / G;
   // A unit's fixed cost in key tiles, and the least worth a CTA.  Chunks of 3, 6 and
@@ -476,10 +477,6 @@ int attend_args(PagedArgs* out, int dtype, const void* q, const exattn_strides& 
   return EXATTN_OK;
 }
 
-cudaError_t launch_line(const PagedArgs& a, cudaStream_t stream) {
-  return a.cols ? launch_paged_decode(a, stream) : launch_paged_fwd(a, stream);
-}
-
 }  // namespace
 
 extern "C" int attn_fwd_paged(int dtype, const void* q, exattn_strides sq, const void* k_cache, exattn_strides skc,
@@ -518,7 +515,7 @@ extern "C" int attn_fwd_paged(int dtype, const void* q, exattn_strides sq, const
     a.whole = tiles <= (2 * plan.units >= kSMs ? kWholeMany : kWholeFew);
   }
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (launch_line(a, st) != cudaSuccess) return EXATTN_ERR_CUDA;
+  if ((plan.cols ? launch_paged_decode(a, st) : launch_paged_fwd(a, st)) != cudaSuccess) return EXATTN_ERR_CUDA;
   return a.whole || launch_paged_merge(a, st) == cudaSuccess ? EXATTN_OK : EXATTN_ERR_CUDA;
 }
 
@@ -532,15 +529,18 @@ struct SharedPlan {
   bool fits;  // the lines' weights in 31 bits
 };
 
+constexpr int kRowsUnitCost = 4;
+
 SharedPlan shared_plan(int B, int groups, int Hq, int Hkv, int total, int max_q, int max_k, int max_group_q, int d) {
   SharedPlan p{};
-  p.line[0] = paged_plan(groups, Hq, Hkv, total, max_group_q, max_k, d);
+  // A group has as many new tokens as its sequences, whatever the hint says.
+  p.line[0] = paged_plan(groups, Hq, Hkv, total, std::max(max_group_q, max_q), max_k, d, true);
   p.line[1] = paged_plan(B, Hq, Hkv, total, max_q, max_k, d);
   // max_group_q chooses the kernel and sizes the grid; a larger group is only slower.
   const int ut = (p.line[0].cols ? 1 : 2) * p.line[0].tile_tokens;
   const double most = Hkv * (static_cast<double>(total) / ut + groups) *
-                      ((static_cast<double>(max_k) + 127) / 128 + p.line[0].unit_cost);
-  p.fits = most < 2e9 && p.line[1].weights < 2e9;
+                      ((static_cast<double>(max_k) + 127) / 128 + kRowsUnitCost);
+  p.fits = most < 2e9 && 2 * p.line[1].weights < 2e9;
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
   const size_t rows = static_cast<size_t>(total) * Hq;
   for (int i = 0; i < 2; ++i) {
@@ -596,20 +596,21 @@ extern "C" int attn_fwd_paged_shared(int dtype, const void* q, exattn_strides sq
   s.cu_groups = cu_groups;
   s.prefix = prefix_lens;
   s.groups = groups;
-  s.causal = a.causal;
-  s.sms = kSMs;
+  s.sms = std::min(kSMs, std::max(2, plan.line[0].ctas + plan.line[1].ctas));
   for (int i = 0; i < 2; ++i) {
     const AttendPlan& l = plan.line[i];
     s.ctas[i] = l.ctas;
     s.unit_tokens[i] = (l.cols ? 1 : 2) * l.tile_tokens;
-    // Two query tiles of the forward kernel take half as long again as one, or as the
-    // decode kernel's columns.
-    const long long tokens = std::min(total, i == 0 ? max_group_q : max_seqlen_q);
-    s.tile_time[i] = !l.cols && tokens > l.tile_tokens ? 3 : 2;
   }
-  PagedArgs lines[2] = {a, a};
+  // A key tile of the forward kernel beside decode CTAs, which have more loads in flight,
+  // takes two (one query tile) to three times theirs: 4 groups of 8 to 256 rows behind
+  // 16,384 86.7 us at 3, 93 at 2.5, 90 at 4; 32 of 5 tokens (d = 64) 45.8 at 2, 49.5 at 1.5.
+  const bool two = std::min(total, max_group_q) > plan.line[0].tile_tokens;
+  s.tile_time[0] = plan.line[0].cols || !plan.line[1].cols ? 2 : two ? 6 : 4;
+  s.tile_time[1] = 2;
+  PagedLines both{{a, a}};
   for (int i = 0; i < 2; ++i) {
-    PagedArgs& l = lines[i];
+    PagedArgs& l = both.line[i];
     const AttendPlan& p = plan.line[i];
     char* ws = static_cast<char*>(workspace) + plan.at[i];
     plan_args(&l, p, ws);
@@ -617,9 +618,14 @@ extern "C" int attn_fwd_paged_shared(int dtype, const void* q, exattn_strides sq
     l.share.line = i == 0 ? kSharedLine : kOwnLine;
     l.share.rec = reinterpret_cast<PagedRecord*>(static_cast<char*>(workspace) + plan.rec_at[i]);
     l.share.rows_at = static_cast<long long>((p.total_bytes - p.plan_bytes - p.sum_bytes) / sizeof(float));
-    if (i == 0) l.causal = 0;
+    if (i == 0) l.causal = 0;  // all of a group's tokens stand behind its shared rows
+    // A unit of the forward kernel that ends in the row buffer, mostly of a few masked
+    // tiles: six of some 320 tokens behind a document 9.2 us a unit, a tile 1.6.
+    if (!p.cols) l.unit_cost = kRowsUnitCost;
   }
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (launch_line(lines[0], st) != cudaSuccess || launch_line(lines[1], st) != cudaSuccess) return EXATTN_ERR_CUDA;
-  return status_of(launch_paged_join(lines[0], lines[1], st));
+  auto launch = a.dtype == kF16 ? (d == 64 ? launch_paged_shared_f16_64 : launch_paged_shared_f16_128)
+                                : (d == 64 ? launch_paged_shared_bf16_64 : launch_paged_shared_bf16_128);
+  if (launch(both, st) != cudaSuccess) return EXATTN_ERR_CUDA;
+  return status_of(launch_paged_join(both.line[0], both.line[1], st));
 }

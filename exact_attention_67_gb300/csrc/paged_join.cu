@@ -8,8 +8,9 @@
 // this library's own, but rows that the tables leave out of every group have none: what
 // lies there instead is checked before it is used as a place.
 //
-// One warp a row and head, or WPR of them where there are few rows, each taking every
-// WPR-th piece; a lane has d / 32 columns.  Latency: three loads deep.
+// LPR lanes a row and head: a whole warp, and four of them that share its pieces out
+// where there are few rows, or eight lanes, four rows a warp, where there are many.  A
+// chain of three loads (record, mass, O), so what counts is how many rows are in flight.
 #include "paged.cuh"
 #include "paged_sched.cuh"
 
@@ -52,15 +53,18 @@ __device__ __forceinline__ JoinPieces pieces_of(const JoinLine& l, const PagedRe
   return p;
 }
 
-template <typename T, int D, int WPR>
+// WPR warps a row, or (WPR = 1) LPR lanes.
+template <typename T, int D, int LPR, int WPR>
 __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ JoinArgs a) {
-  constexpr int V = D / 32, BATCH = 4;
+  static_assert(WPR == 1 || LPR == 32, "several warps, or a part of one");
+  constexpr int V = D / LPR, V4 = V / 4 > 0 ? V / 4 : 1, BATCH = V > 4 ? 2 : 4;  // columns a lane; pieces at once
+  constexpr int HEADS = 256 / LPR / WPR;                                          // of a block
   __shared__ float2 red[8];  // reference, mass
   __shared__ float acc_s[WPR > 1 ? 8 : 1][D];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp % WPR;
-  const int row = blockIdx.x, head = static_cast<int>(blockIdx.y) * (8 / WPR) + warp / WPR;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = threadIdx.x % LPR, part = WPR > 1 ? warp % WPR : 0;
+  const int row = blockIdx.x, head = static_cast<int>(blockIdx.y) * HEADS + static_cast<int>(threadIdx.x) / (LPR * WPR);
   bool live = head < a.Hq;
   const long long at = static_cast<long long>(row) * a.Hq + (live ? head : 0);
   // Records, chunks and the row's place among its sequence's tokens.
@@ -100,17 +104,20 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
       } else {
         l[u] = p.whole;
       }
-      const float* po = ln.part_o + from + lane * V;
-      if constexpr (V == 4) {
-        const float4 y = *reinterpret_cast<const float4*>(po);
+      if constexpr (V == 2) {
+        const float2 y = *reinterpret_cast<const float2*>(ln.part_o + from + sub * V);
         x[u][0] = y.x;
         x[u][1] = y.y;
-        x[u][2] = y.z;
-        x[u][3] = y.w;
       } else {
-        const float2 y = *reinterpret_cast<const float2*>(po);
-        x[u][0] = y.x;
-        x[u][1] = y.y;
+        const float4* po = reinterpret_cast<const float4*>(ln.part_o + from) + sub;  // vectors LPR apart
+#pragma unroll
+        for (int c = 0; c < V4; ++c) {
+          const float4 y = po[c * LPR];
+          x[u][4 * c] = y.x;
+          x[u][4 * c + 1] = y.y;
+          x[u][4 * c + 2] = y.z;
+          x[u][4 * c + 3] = y.w;
+        }
       }
     }
     float top = m;
@@ -155,20 +162,26 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
   }
   if (!live) return;
   const float inv = sum == 0.f ? 0.f : sum_inverse(sum);
-  T* out = static_cast<T*>(a.o) + row * a.so.n + head * a.so.h + lane * V;
+  T* out = static_cast<T*>(a.o) + row * a.so.n + head * a.so.h;
+  if constexpr (V == 2) {
+    reinterpret_cast<uint32_t*>(out)[sub] = Elem<T>::pack(acc[0] * inv, acc[1] * inv);
+  } else {
 #pragma unroll
-  for (int c = 0; c < V; c += 2) *reinterpret_cast<uint32_t*>(out + c) = Elem<T>::pack(acc[c] * inv, acc[c + 1] * inv);
-  if (lane == 0)
+    for (int c = 0; c < V4; ++c)
+      reinterpret_cast<uint2*>(out)[sub + c * LPR] = make_uint2(Elem<T>::pack(acc[4 * c] * inv, acc[4 * c + 1] * inv),
+                                                                Elem<T>::pack(acc[4 * c + 2] * inv, acc[4 * c + 3] * inv));
+  }
+  if (sub == 0)
     a.lse[static_cast<long long>(head) * a.nt.total + row] = sum == 0.f ? -INFINITY : (m + sum_log2(sum)) * 0.6931471805599453f;
 }
 
 template <typename T, int D>
 cudaError_t launch_t(const JoinArgs& a, cudaStream_t stream) {
-  // Few rows have many pieces each.
-  const bool deep = static_cast<long long>(a.nt.total) * a.Hq <= 1024;
-  const int heads = deep ? 2 : 8;
+  // Few rows have many pieces each; many have few.
+  const long long rows = static_cast<long long>(a.nt.total) * a.Hq;
+  const int heads = rows <= 1024 ? 2 : rows <= 8192 ? 8 : 32;
   const dim3 grid(a.nt.total, (a.Hq + heads - 1) / heads);
-  auto kern = deep ? paged_join_kernel<T, D, 4> : paged_join_kernel<T, D, 1>;
+  auto kern = heads == 2 ? paged_join_kernel<T, D, 32, 4> : heads == 8 ? paged_join_kernel<T, D, 32, 1> : paged_join_kernel<T, D, 8, 1>;
   return launch_dependent("paged join kernel launch", kern, grid, 256, 0, stream, a);
 }
 

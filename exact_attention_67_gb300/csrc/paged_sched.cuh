@@ -220,30 +220,19 @@ __device__ __forceinline__ int paged_weight(const PagedArgs& a, const PagedSeq& 
   return w;
 }
 
-// The same on either line, and the whole line's, by a warp.  (Groups' tokens all see the
-// same keys: no loop over runs, and no mask.)
+// The same on either line.  (Groups' tokens all see the same keys: no loop over runs, and
+// no mask.)
 __device__ __forceinline__ int line_weight(const PagedArgs& a, int line, const PagedSeq& s, int UT, int key0) {
   if (line == kSharedLine) return (s.n + UT - 1) / UT * (s.len / kKeyTile + a.unit_cost);
-  return paged_weight(a, s, UT, key0, a.share.causal);
+  return paged_weight(a, s, UT, key0, a.causal);
 }
-__device__ __forceinline__ int line_total(const PagedArgs& a, int line, int lane) {
-  int sum = 0;
-  for (int b = lane; b < line_items(a, line); b += 32) {
-    int key0;
-    const PagedSeq s = line_seq(a, line, b, &key0);
-    sum += line_weight(a, line, s, a.share.unit_tokens[line - 1], key0);
-  }
-  return __reduce_add_sync(0xffffffffu, sum) * a.Hkv;
-}
-
-// CTAs that work on `line` when the two weigh w[0] and w[1]: as many of the SMs as its
-// share of the time, the same numbers in both launches.
-__device__ __forceinline__ int line_ctas(const PagedArgs& a, int line, int w_shared, int w_own) {
-  const PagedShare& s = a.share;
-  const float t1 = static_cast<float>(w_shared) * static_cast<float>(s.tile_time[0]);
-  const float t2 = static_cast<float>(w_own) * static_cast<float>(s.tile_time[1]);
-  const int first = min(min(max(static_cast<int>(rintf(s.sms * (t1 / (t1 + t2)))), 1), s.sms - 1), s.ctas[0]);
-  return line == kSharedLine ? first : min(s.sms - first, s.ctas[1]);
+// CTAs that work on the shared line when the two weigh w0 and w1, of a.share.sms for both:
+// as many as its share of the time, the line with less of it rounded up.
+__device__ __forceinline__ int shared_ctas(const PagedShare& s, int w0, int w1) {
+  const float t0 = static_cast<float>(w0) * static_cast<float>(s.tile_time[0]);
+  const float t1 = static_cast<float>(w1) * static_cast<float>(s.tile_time[1]);
+  const float n = static_cast<float>(s.sms) * (t0 / (t0 + t1));
+  return min(min(max(static_cast<int>(t0 < t1 ? ceilf(n) : floorf(n)), 1), s.sms - 1), s.ctas[0]);
 }
 
 // What the merge needs of the boundary before a CTA's chunk.
@@ -273,30 +262,40 @@ __device__ __forceinline__ void paged_touch(const PagedArgs& a) {
                "l"(a.plan), "l"(a.err));
 }
 
-// Start of this CTA's chunk, found by one warp; the same in every lane.  Leaves
-// the merge its PagedPlan.  The line's weights fit 31 bits (checked on the host
-// against the largest that the sizes allow).
+// The line as one warp has read it: its sequences' weights, and a lane's sequence of the
+// first 32 (most batches have no more).
 template <bool SH>
-__device__ __forceinline__ PagedCursor<SH> paged_start(const PagedArgs& a, int UT, int lane, PagedSeq* seq) {
-  const int line = SH ? a.share.line : kNoLine, B = SH ? line_items(a, line) : a.nt.B, cta = static_cast<int>(blockIdx.x);
-  auto read = [&](int b, int* key0) {
+struct PagedLine {
+  PagedSeq s0;
+  int k0, w0;
+  int W, units, most, least;  // the line's weights, units; the largest and smallest sequence's weight
+  bool single;                // a unit is a (sequence, key head)
+
+  __device__ __forceinline__ static int items(const PagedArgs& a) { return SH ? line_items(a, a.share.line) : a.nt.B; }
+  __device__ __forceinline__ static PagedSeq read(const PagedArgs& a, int b, int* key0) {
     *key0 = 0;
-    if (b >= B) return PagedSeq{0, 0, 0, 0};
-    if constexpr (SH) return line_seq(a, line, b, key0);
+    if (b >= items(a)) return PagedSeq{0, 0, 0, 0};
+    if constexpr (SH) return line_seq(a, a.share.line, b, key0);
     else return paged_seq(a, b);
-  };
-  auto weight = [&](const PagedSeq& s, int key0) {
-    if constexpr (SH) return line_weight(a, line, s, UT, key0);
+  }
+  __device__ __forceinline__ static int weight(const PagedArgs& a, const PagedSeq& s, int UT, int key0) {
+    if constexpr (SH) return line_weight(a, a.share.line, s, UT, key0);
     else return paged_weight(a, s, UT, 0, a.causal);
-  };
+  }
+};
+
+template <bool SH>
+__device__ __forceinline__ PagedLine<SH> paged_line(const PagedArgs& a, int UT, int lane) {
+  using L = PagedLine<SH>;
+  const int B = L::items(a);
   int k0;
-  const PagedSeq s0 = read(lane, &k0);
-  const int w0 = weight(s0, k0);  // kept: most batches have at most 32 sequences
+  const PagedSeq s0 = L::read(a, lane, &k0);
+  const int w0 = L::weight(a, s0, UT, k0);
   int sum = w0, most = w0, least = w0 > 0 ? w0 : INT_MAX, count = w0 > 0, longest = s0.n;
   for (int b = 32 + lane; b < B; b += 32) {
     int kb;
-    const PagedSeq s = read(b, &kb);
-    const int w = weight(s, kb);
+    const PagedSeq s = L::read(a, b, &kb);
+    const int w = L::weight(a, s, UT, kb);
     sum += w;
     longest = max(longest, s.n);
     most = max(most, w);
@@ -306,25 +305,32 @@ __device__ __forceinline__ PagedCursor<SH> paged_start(const PagedArgs& a, int U
   sum = __reduce_add_sync(0xffffffffu, sum);
   most = __reduce_max_sync(0xffffffffu, most);
   least = __reduce_min_sync(0xffffffffu, least);
-  const int units = __reduce_add_sync(0xffffffffu, count) * a.Hkv, tiles_each = most - a.unit_cost;
-  int W = sum * a.Hkv, cost = a.unit_cost;
-  int ctas = a.ctas;
-  bool single = true;  // a unit is a (sequence, key head)
-  if constexpr (SH) {
-    const int other = line_total(a, kSharedLine + kOwnLine - line, lane);
-    ctas = line == kSharedLine ? line_ctas(a, line, W, other) : line_ctas(a, line, other, W);
-    single = __reduce_max_sync(0xffffffffu, longest) <= UT;
-  }
+  const int units = __reduce_add_sync(0xffffffffu, count) * a.Hkv;
+  const bool single = !SH || __reduce_max_sync(0xffffffffu, longest) <= UT;
+  return PagedLine<SH>{s0, k0, w0, sum * a.Hkv, units, most, least, single};
+}
+
+// Start of the chunk of CTA `cta` of `ctas`, found by the warp that has read the line; the
+// same in every lane.  Leaves the merge its PagedPlan.  The line's weights fit 31 bits
+// (checked on the host against the largest that the sizes allow).
+template <bool SH>
+__device__ __forceinline__ PagedCursor<SH> paged_place(const PagedArgs& a, int UT, int lane, int cta, int ctas,
+                                                       const PagedLine<SH>& line, PagedSeq* seq) {
+  using L = PagedLine<SH>;
+  const int B = L::items(a), units = line.units, tiles_each = line.most - a.unit_cost;
+  int W = line.W, cost = a.unit_cost;
   int chunk = max(paged_div(W + ctas - 1, ctas), a.min_chunk);
   // The decode kernel, where a unit is a (sequence, key head), and all weigh the same.
-  if (a.cols > 0 && single && most == least && tiles_each > 0 && units <= ctas) {
+  if (a.cols > 0 && line.single && line.most == line.least && tiles_each > 0 && units <= ctas) {
     // As many pieces a unit as CTAs, of two tiles at least; none of four or fewer
     // (joining pieces takes some 2 us, a tile 0.6).  Unless this leaves over a
-    // quarter of the SMs out of long work.
+    // quarter of the SMs out of long work.  (Behind shared rows the pieces are joined
+    // anyway.)
     const int most_pieces = paged_div(ctas, units);
-    const int each = tiles_each <= 4 || a.whole ? tiles_each : max(paged_div(tiles_each + most_pieces - 1, most_pieces), 2);
+    const int few = SH ? 1 : 4;
+    const int each = tiles_each <= few || a.whole ? tiles_each : max(paged_div(tiles_each + most_pieces - 1, most_pieces), SH ? 1 : 2);
     const int k = paged_div(tiles_each + each - 1, each);
-    if (4 * units * k >= 3 * ctas || each <= 4 || a.whole) {
+    if (4 * units * k >= 3 * ctas || each <= few || a.whole) {
       chunk = each;
       cost = k * chunk - tiles_each;  // less than a chunk: the first piece's tiles are fewer by it
       W = units * k * chunk;
@@ -338,9 +344,9 @@ __device__ __forceinline__ PagedCursor<SH> paged_start(const PagedArgs& a, int U
   int before = 0;
   for (int b0 = 0; b0 < B && lo64 < W; b0 += 32) {
     const int lo = static_cast<int>(lo64);
-    int kl = k0;
-    const PagedSeq sl = b0 == 0 ? s0 : read(b0 + lane, &kl);
-    int w = b0 == 0 ? w0 : weight(sl, kl);
+    int kl = line.k0;
+    const PagedSeq sl = b0 == 0 ? line.s0 : L::read(a, b0 + lane, &kl);
+    int w = b0 == 0 ? line.w0 : L::weight(a, sl, UT, kl);
     if (w > 0) w += pad;  // not 0 only where a sequence has one unit a key head
     const int per_head = w;
     w *= a.Hkv;
@@ -388,18 +394,9 @@ __device__ __forceinline__ PagedCursor<SH> paged_start(const PagedArgs& a, int U
   return c;
 }
 
-// The shared line's launch waits for the stream before it lets the own line's begin, so
-// that one may read its operands at once; that one waits at its end, so that what
-// follows it follows both.
-template <bool SH>
-__device__ __forceinline__ void paged_wait(const PagedArgs& a) {
-  if (SH && a.share.line == kOwnLine) return;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (SH) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-template <bool SH>
-__device__ __forceinline__ void paged_end(const PagedArgs& a) {
-  if (SH && a.share.line == kOwnLine) asm volatile("griddepcontrol.wait;" ::: "memory");
+// Both, of attn_fwd_paged.
+__device__ __forceinline__ PagedCursor<false> paged_start(const PagedArgs& a, int UT, int lane, PagedSeq* seq) {
+  return paged_place<false>(a, UT, lane, static_cast<int>(blockIdx.x), a.ctas, paged_line<false>(a, UT, lane), seq);
 }
 
 // Leaves the join a row's part of a piece: `out` its row of the row buffer, `part` its
