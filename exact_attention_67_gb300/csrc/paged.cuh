@@ -99,6 +99,7 @@ struct NormArgs {
   void* k_dgain;
   float* partial;      // [parts][2][d]: the blocks' sums for the gains of Q and K
   int parts;
+  int device;
 };
 constexpr int kNormParts = 152 * 2;  // blocks of the gradient at most
 cudaError_t launch_norm_rotary(const NormArgs& a, cudaStream_t stream);

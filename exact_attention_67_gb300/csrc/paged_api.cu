@@ -177,10 +177,10 @@ int append_args(RotaryArgs* out, bool normed, int dtype, const void* q, exattn_s
 }
 
 // The current device's set-up; calls that do not use its watchdog word.
-int device_ready() {
-  int dev = 0;
+int device_ready(int* dev = nullptr) {
+  int own = 0;
   unsigned* err = nullptr;
-  return setup_device(&dev, &err);
+  return setup_device(dev ? dev : &own, &err);
 }
 
 int status_of(cudaError_t e) { return e == cudaSuccess ? EXATTN_OK : EXATTN_ERR_CUDA; }
@@ -239,7 +239,7 @@ extern "C" int attn_norm_rotary_backward(int dtype, const void* dq, exattn_strid
     return rc;
   if (!workspace || workspace_bytes < attn_norm_rotary_backward_workspace_size(B, N, d)) return EXATTN_ERR_WORKSPACE;
   if (!aligned(workspace, 16)) return EXATTN_ERR_ALIGN;
-  if ((rc = device_ready()) != EXATTN_OK) return rc;
+  if ((rc = device_ready(&a.device)) != EXATTN_OK) return rc;
   a.q_gain = q_gain;
   a.k_gain = k_gain;
   a.gain_dtype = element_type(gain_dtype);

@@ -185,8 +185,9 @@ __device__ __forceinline__ void read_frequencies(const RotaryArgs& a, int half, 
 // cos and sin of nt tokens' angles, by the whole block.
 template <int D, int V>
 __device__ __forceinline__ void form_angles(const RotaryArgs& a, int half, int nt, const Token* tk, AngleTable<D>& s) {
-  for (int i = threadIdx.x; i < nt * half; i += kRotaryThreads) {
-    const int tt = i / half, f = i - tt * half;
+  for (int i = threadIdx.x; i < nt * (D / 2); i += kRotaryThreads) {
+    const int tt = i / (D / 2), f = i % (D / 2);  // idle threads cost less than a division
+    if (f >= half) continue;
     const unsigned long long angle = static_cast<unsigned long long>(static_cast<long long>(tk[tt].pos)) * s.turns[f];
     float sn, c;
     sincospif(static_cast<float>(static_cast<int>(angle >> 32)) * 4.656612873077393e-10f, &sn, &c);  // 2^-31: half turns

@@ -19,6 +19,7 @@ import math
 import os
 
 import torch
+from torch.autograd import forward_ad
 
 from . import build as _build
 from ._lib import _check, load, watchdog_step
@@ -151,8 +152,10 @@ def _readable(g) -> bool:
 
 def _differentiated(*tensors) -> bool:
     """Whether automatic differentiation, in either mode, follows one of them."""
-    return any(t is not None and (t.requires_grad and torch.is_grad_enabled()
-                                  or torch.autograd.forward_ad.unpack_dual(t).tangent is not None) for t in tensors)
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        return True
+    # Outside a dual level, as nearly always, asking each tensor would take a microsecond.
+    return forward_ad._current_level >= 0 and any(t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors)
 
 
 def _turn(q, k, positions, inv_freq, interleaved, inverse, factor, stream):
@@ -215,14 +218,12 @@ def attn_norm_rotary_backward(dq, q, dq_out, dk, k, dk_out, positions, inv_freq,
         _check(status)
 
 
-def _places(q, positions, inv_freq, stream):
+def _places(q, positions, inv_freq):
     """The defaults of positions and frequencies: 0..N-1, and ``rotary_frequencies``'."""
-    if positions is None or inv_freq is None:
-        with on_stream(stream, q.device):
-            if positions is None:
-                positions = torch.arange(q.shape[2] if q.dim() == 4 else q.shape[0], dtype=torch.int32, device=q.device)
-            if inv_freq is None:
-                inv_freq, _ = rotary_frequencies(q.shape[-1], device=q.device)
+    if positions is None:
+        positions = torch.arange(q.shape[2] if q.dim() == 4 else q.shape[0], dtype=torch.int32, device=q.device)
+    if inv_freq is None:
+        inv_freq, _ = rotary_frequencies(q.shape[-1], device=q.device)
     return positions, inv_freq
 
 
@@ -265,14 +266,15 @@ def norm_rotary(q, k=None, q_gain=None, k_gain=None, positions=None, inv_freq=No
     float32, bfloat16 or float16 tensors of one type, or None (all 1); the other
     arguments as ``rotary``.  Differentiable in q, k and the gains (once, in reverse
     mode)."""
-    if _differentiated(q, k, q_gain, k_gain):
-        if stream is not None:
+    if stream is not None:
+        if _differentiated(q, k, q_gain, k_gain):
             raise ValueError("norm_rotary under autograd runs on the current stream: use torch.cuda.stream(...)")
-        positions, inv_freq = _places(q, positions, inv_freq, None)
+        with on_stream(stream, q.device):
+            return norm_rotary(q, k, q_gain, k_gain, positions, inv_freq, interleaved, factor, eps)
+    positions, inv_freq = _places(q, positions, inv_freq)
+    if _differentiated(q, k, q_gain, k_gain):
         return _NormRotary.apply(q, k, q_gain, k_gain, positions, inv_freq, bool(interleaved), float(factor), float(eps))
-    with on_stream(stream, q.device):
-        positions, inv_freq = _places(q, positions, inv_freq, None)
-        return _norm_rotary(q, k, q_gain, k_gain, positions, inv_freq, interleaved, factor, eps)
+    return _norm_rotary(q, k, q_gain, k_gain, positions, inv_freq, interleaved, factor, eps)
 
 
 def norm_rotary_backward(dq, dk, q, k, q_gain=None, k_gain=None, positions=None, inv_freq=None, interleaved: bool = False,
@@ -280,9 +282,11 @@ def norm_rotary_backward(dq, dk, q, k, q_gain=None, k_gain=None, positions=None,
     """The gradient of ``norm_rotary`` with the same arguments: from the gradients of
     its outputs those of q, k, q_gain and k_gain (None for what was None).  Not
     differentiable."""
-    with on_stream(stream, q.device):
-        positions, inv_freq = _places(q, positions, inv_freq, None)
-        return _norm_rotary_grad(dq, dk, q, k, q_gain, k_gain, positions, inv_freq, interleaved, factor, eps)
+    if stream is not None:
+        with on_stream(stream, q.device):
+            return norm_rotary_backward(dq, dk, q, k, q_gain, k_gain, positions, inv_freq, interleaved, factor, eps)
+    positions, inv_freq = _places(q, positions, inv_freq)
+    return _norm_rotary_grad(dq, dk, q, k, q_gain, k_gain, positions, inv_freq, interleaved, factor, eps)
 
 
 # ---------------------------------------------------------------- the cache
