@@ -86,17 +86,24 @@ class PagedCache:
     head_dim], and the sequences that hold them.  Not thread-safe; the device work
     of a call runs on the current stream (or ``stream``), so calls on several
     streams are for the caller to order.  Contents start uninitialised: rows that
-    no sequence has written reach no output."""
+    no sequence has written reach no output.
+
+    ``share_from``: bytes of K and V of a layer whose repeated reads a step has to save
+    before ``extend(shared=True)`` makes it one of groups.  Reading shared pages again, mostly
+    from L2, costs less than a second line of units and a join: next tokens are even
+    at 60 to 130 MB (16 of them behind 4,096 rows, 8 key heads of 128, 126 MB: 19.4 us
+    with groups, 25.4 without; behind 1,024 17.9 and 12.6), five tokens a sequence at 250,
+    so steps of more than one token take twice as many."""
 
     def __init__(self, num_pages: int, page_size: int, layers: int, kv_heads: int, head_dim: int,
-                 dtype=torch.bfloat16, device="cuda"):
+                 dtype=torch.bfloat16, device="cuda", share_from: int = 128 << 20):
         if num_pages < 1 or layers < 1 or kv_heads < 1:
             raise ValueError("num_pages, layers and kv_heads must be positive")
         if page_size < 8 or page_size > 1024 or page_size & (page_size - 1):
             raise ValueError(f"page_size must be a power of two, 8 to 1024, got {page_size}")
         if head_dim not in (64, 128) or dtype not in (torch.bfloat16, torch.float16):
             raise ValueError("head_dim must be 64 or 128, dtype bfloat16 or float16")
-        self.page_size, self.num_pages, self.layers = page_size, num_pages, layers
+        self.page_size, self.num_pages, self.layers, self.share_from = page_size, num_pages, layers, share_from
         self.pool = torch.empty((2 * layers, num_pages, kv_heads, page_size, head_dim), dtype=dtype, device=device)
         self._free = list(range(num_pages))  # a heap: the lowest first
         self._refs = [0] * num_pages
@@ -175,8 +182,8 @@ class PagedCache:
     def extend(self, seqs, new, stream=None, shared: bool = False) -> Step:
         """Room for ``new`` tokens (a number, or one a sequence) at the end of each
         sequence.  With ``shared`` neighbours in ``seqs`` that have their first pages in
-        common (``fork``) are taken as groups, whose shared rows ``attend`` streams once:
-        put such sequences side by side.  A last page that is shared and will be written to is copied
+        common (``fork``) are taken as groups, whose shared rows ``attend`` streams once,
+        where that pays (``share_from``): put such sequences side by side.  A last page that is shared and will be written to is copied
         first, for all sequences and layers in one launch.  Raises OutOfPages,
         changing nothing, if the pool is too small."""
         seqs = list(seqs)
@@ -239,7 +246,9 @@ class PagedCache:
         for n in new:
             offsets.append(offsets[-1] + n)
         groups, prefix = _groups(tables, [self._length[s] for s in seqs], self.page_size) if shared else ([], [])
-        if not any(prefix):
+        # What the first of a group reads, the others need not.
+        saved = sum(prefix) - sum(prefix[i] for i in groups[:-1])
+        if saved * self.pool.shape[2] * self.pool.shape[4] * 4 < max(1, self.share_from * (1 if max(new) <= 1 else 2)):
             groups, prefix = [], []
         host = torch.tensor(rows + lens + offsets + prefix + groups, dtype=torch.int32)
         if self.pool.is_cuda:

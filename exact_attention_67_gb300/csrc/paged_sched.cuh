@@ -320,8 +320,9 @@ __device__ __forceinline__ PagedCursor<SH> paged_place(const PagedArgs& a, int U
   const int B = L::items(a), units = line.units, tiles_each = line.most - a.unit_cost;
   int W = line.W, cost = a.unit_cost;
   int chunk = max(paged_div(W + ctas - 1, ctas), a.min_chunk);
-  // The decode kernel, where a unit is a (sequence, key head), and all weigh the same.
-  if (a.cols > 0 && line.single && line.most == line.least && tiles_each > 0 && units <= ctas) {
+  // The decode kernel (behind shared rows either), where a unit is a (sequence, key head),
+  // and all weigh the same.
+  if ((a.cols > 0 || SH) && line.single && line.most == line.least && tiles_each > 0 && units <= ctas) {
     // As many pieces a unit as CTAs, of two tiles at least; none of four or fewer
     // (joining pieces takes some 2 us, a tile 0.6).  Unless this leaves over a
     // quarter of the SMs out of long work.  (Behind shared rows the pieces are joined

@@ -274,7 +274,7 @@ def test_prompt_forks_and_next_tokens(d, Hq, Hk, ps, dtype):
     cache holds."""
     import exact_attention_67_gb300 as ex
     layers, prompt = 2, 300
-    cache = ex.PagedCache(200, ps, layers, Hk, d, dtype=dtype)
+    cache = ex.PagedCache(200, ps, layers, Hk, d, dtype=dtype, share_from=0)
     freq, factor = ex.rotary_frequencies(d)
     qg, kg = (1 + 0.2 * randn(d, seed=i, dtype=torch.float32) for i in (1, 2))
     root = cache.add()

@@ -55,9 +55,9 @@ def test_python_refusals():
 
 
 # ---------------------------------------------------------------- PagedCache
-def cache_of(pages=200, ps=16):
+def cache_of(pages=200, ps=16, share_from=0):
     from exact_attention_67_gb300 import PagedCache
-    return PagedCache(pages, ps, 1, 1, 64, device="cpu")
+    return PagedCache(pages, ps, 1, 1, 64, device="cpu", share_from=share_from)
 
 
 @pytest.fixture()
@@ -129,3 +129,16 @@ def test_out_of_pages_leaves_the_cache(no_copies):
     with pytest.raises(OutOfPages):
         c.extend(forks, 16, shared=True)
     assert c.free_pages == 1 and [c.length(s) for s in forks] == [300, 300]
+
+
+@pytest.mark.parametrize("new,times", [(1, 1), (5, 2)])
+def test_groups_where_enough_reads_are_saved(no_copies, new, times):
+    c = cache_of()
+    a = c.add()
+    c.extend([a], 300)
+    forks = c.fork(a, 3)
+    saved = 2 * 256 * 64 * 4  # two of the three need not read 256 rows of K and V, one head of 64
+    c.share_from = saved // times
+    assert groups(c.extend(forks, new, shared=True)) == ([0, 3], [256] * 3, 3 * new)
+    c.share_from = saved // times + 1
+    assert groups(c.extend(forks, new, shared=True)) is None
