@@ -348,13 +348,13 @@ struct AttendPlan {
   double units, weights;  // of the line, at most
 };
 
-// shared: the line over shared rows, whose decode kernel has 8 or 32 columns.
+// shared: the line over shared rows, whose decode kernel has 8, 16 or 32 columns.
 AttendPlan paged_plan(int B, int Hq, int Hkv, int total, int max_q, int max_k, int d, bool shared = false) {
   AttendPlan p{};
   const int G = Hq / Hkv;
   max_q = std::min(max_q, total);
   const long long need = static_cast<long long>(max_q) * G;
-  p.cols = shared && need <= kPagedDecodeCols ? (need <= 8 ? 8 : 32) : need <= 4 ? 4 : need <= 8 ? 8 : need <= 16 ? 16 : need <= kPagedDecodeCols ? 32 : 0;
+  p.cols = shared && need <= kPagedDecodeCols ? (need <= 8 ? 8 : need <= 16 ? 16 : 32) : need <= 4 ? 4 : need <= 8 ? 8 : need <= 16 ? 16 : need <= kPagedDecodeCols ? 32 : 0;
   p.rows = p.cols ? std::max(p.cols, 16) : kPagedRows;
   p.tile_tokens = (p.cols ? p.cols : 128) / G;
   // A unit's fixed cost in key tiles, and the least worth a CTA.  Chunks of 3, 6 and

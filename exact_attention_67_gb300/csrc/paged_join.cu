@@ -33,7 +33,8 @@ struct JoinArgs {
   Strides so;
   float* lse;
   NewTokens nt;
-  int Hq, max_q;
+  const int* prefix;  // shared rows of a sequence, as the lines take them
+  int Hq, max_q, max_k;
 };
 
 // Where piece i of a line's row is.
@@ -70,16 +71,21 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
   // Records, chunks and the row's place among its sequence's tokens.
   const PagedRecord r0 = a.line[0].rec[at], r1 = a.line[1].rec[at];
   const int chunk0 = a.line[0].plan->chunk, chunk1 = a.line[1].plan->chunk;
+  int b = 0;
   if (a.nt.cu_seqlens) {
-    int b = 0;
     for (int b0 = 0; b0 < a.nt.B; b0 += 32)
       b += __popc(__ballot_sync(0xffffffffu, b0 + lane < a.nt.B && a.nt.cu_seqlens[b0 + lane + 1] <= row));
     const int i = b < a.nt.B ? row - a.nt.cu_seqlens[b] : -1;
     live = live && i >= 0 && i < a.max_q;
   } else {
-    live = live && row % a.nt.each < a.max_q;
+    b = row / a.nt.each;
+    live = live && row - b * a.nt.each < a.max_q;
   }
-  const JoinPieces p0 = pieces_of(a.line[0], r0, chunk0), p1 = pieces_of(a.line[1], r1, chunk1);
+  // (Rows of a group that shares nothing have no record in the shared line.)
+  const bool shares = live && min(a.prefix[b], a.max_k) >= kKeyTile;
+  JoinPieces p0 = pieces_of(a.line[0], r0, chunk0);
+  const JoinPieces p1 = pieces_of(a.line[1], r1, chunk1);
+  if (!shares) p0.count = 0;
   const int count = live ? p0.count + p1.count : 0;
   float m = -INFINITY, sum = 0.f, acc[V] = {};
   for (int i0 = part; i0 < count; i0 += BATCH * WPR) {
@@ -200,6 +206,8 @@ cudaError_t launch_paged_join(const PagedArgs& shared, const PagedArgs& own, cud
   a.nt = own.nt;
   a.Hq = own.Hkv * own.G;
   a.max_q = own.max_q;
+  a.max_k = own.max_k;
+  a.prefix = own.share.prefix;
   if (own.dtype == kF16) return own.d == 64 ? launch_t<__half, 64>(a, stream) : launch_t<__half, 128>(a, stream);
   return own.d == 64 ? launch_t<__nv_bfloat16, 64>(a, stream) : launch_t<__nv_bfloat16, 128>(a, stream);
 }

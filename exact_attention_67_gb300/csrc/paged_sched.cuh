@@ -82,13 +82,14 @@ __device__ __forceinline__ PagedSeq line_seq(const PagedArgs& a, int line, int b
   *key0 = 0;
   const int f = min(max(a.share.cu_groups[b], 0), a.nt.B), e = min(max(a.share.cu_groups[b + 1], f), a.nt.B);
   PagedSeq s{0, 0, 0, f};
-  if (e > f) {
+  const int rows = e > f ? shared_rows(a, f) : 0;
+  if (rows > 0) {  // a group that shares nothing has no units
     int c0 = f * a.nt.each, c1 = e * a.nt.each;
     if (a.nt.cu_seqlens) {
       c0 = min(max(a.nt.cu_seqlens[f], 0), a.nt.total);
       c1 = min(max(a.nt.cu_seqlens[e], c0), a.nt.total);
     }
-    s = PagedSeq{c0, c1 - c0, shared_rows(a, f), f};
+    s = PagedSeq{c0, c1 - c0, rows, f};
   }
   return s;
 }

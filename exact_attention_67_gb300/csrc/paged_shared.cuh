@@ -12,7 +12,7 @@
 // second one's CTAs had to wait for those of the first that had nothing to do: they began
 // 7 us in, and its last ones ended 4 us after its work.)  The lines' kernels are those of
 // attn_fwd_paged: groups of more than 32 query rows take the forward kernel
-// (paged_fwd.cuh), smaller ones the decode kernel with 8 or 32 columns; own rows the one
+// (paged_fwd.cuh), smaller ones the decode kernel with 8, 16 or 32 columns; own rows the one
 // that their count of new tokens asks for.  What does not depend on the line is done
 // before the CTA knows it, beside the stream's last kernel: both lines' barriers, TMEM.
 #pragma once
@@ -137,6 +137,10 @@ template <typename T, int D>
 cudaError_t launch_paged_lines(const PagedLines& a, cudaStream_t stream) {
   if (a.line[0].cols == 8)
     return a.line[1].cols == 4 ? launch_lines<T, D, 8, 4>(a, stream) : launch_lines<T, D, 8, 8>(a, stream);
+  if (a.line[0].cols == 16)
+    return a.line[1].cols == 4   ? launch_lines<T, D, 16, 4>(a, stream)
+           : a.line[1].cols == 8 ? launch_lines<T, D, 16, 8>(a, stream)
+                                 : launch_lines<T, D, 16, 16>(a, stream);
   if (a.line[0].cols) return launch_own<T, D, 32>(a, stream);
   return a.line[1].cols ? launch_own<T, D, 0>(a, stream) : launch_lines<T, D, 0, 0>(a, stream);
 }
