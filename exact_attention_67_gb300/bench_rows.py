@@ -4,7 +4,8 @@
 
 One JSON line per case: f16 inputs, the [B, N, H, d] layout, a sliding
 window, a packed variable-length batch, decode-shaped forwards, rotary
-positions and the paged cache (append, attention, page copies).  Inputs are
+positions, head norms with them, and the paged cache (append, attention, attention
+behind shared rows, page copies).  Inputs are
 seeded synthetic bf16/f16 N(0, 1), resident on the device; each figure is the
 mean device time of ``iters`` back-to-back calls between two CUDA events after
 three warm-up calls (the square cases move far more than L2 per call and are
@@ -22,8 +23,9 @@ import os
 import torch
 
 from . import (attn_cache_append, attn_cache_copy, attn_fwd_decode, attn_fwd_decode_workspace_size, attn_fwd_paged,
-               attn_fwd_paged_workspace_size, attn_rotary, backward, backward_varlen, forward, forward_varlen,
-               rotary_frequencies)
+               attn_fwd_paged_shared, attn_fwd_paged_shared_workspace_size, attn_fwd_paged_workspace_size, attn_norm_rotary,
+               attn_norm_rotary_backward, attn_norm_rotary_backward_workspace_size, attn_rotary, backward,
+               backward_varlen, forward, forward_varlen, rotary_frequencies)
 from .synth import seeded_bf16
 
 DEV = torch.device("cuda:0")
@@ -146,6 +148,46 @@ def _rotary(name, B, N, Hq, Hk, d, iters, hbm):
             "pct_hbm": nbytes / t / 1e6 / hbm * 100}
 
 
+def _norm_rotary(name, B, N, Hq, Hk, d, iters, hbm):
+    """The norms with the turn, and their gradient."""
+    q, k, dq, dk = (seeded_bf16((B, h, N, d), 61 + i, 1.0).to(DEV) for i, h in enumerate((Hq, Hk, Hq, Hk)))
+    qo, ko = torch.empty_like(q), torch.empty_like(k)
+    gains = [torch.ones(d, dtype=torch.bfloat16, device=DEV) for _ in range(4)]
+    pos = torch.arange(N, dtype=torch.int32, device=DEV)
+    freq, _ = rotary_frequencies(d)
+    ws = torch.empty(attn_norm_rotary_backward_workspace_size(B, N, d), dtype=torch.uint8, device=DEV)
+    t_f = _time_graph_ms(lambda: attn_norm_rotary(q, qo, k, ko, pos, freq, *gains[:2]), iters)
+    t_b = _time_graph_ms(lambda: attn_norm_rotary_backward(dq, q, qo, dk, k, ko, pos, freq, *gains, False, 1.0, 1e-6, ws), iters)
+    nbytes = 4.0 * B * N * (Hq + Hk) * d  # read and written; the gradient reads twice that
+    return {"case": name, "B": B, "N": N, "Hq": Hq, "Hk": Hk, "d": d, "ms": t_f, "bwd_ms": t_b, "gbs": nbytes / t_f / 1e6,
+            "pct_hbm": nbytes / t_f / 1e6 / hbm * 100, "bwd_gbs": 1.5 * nbytes / t_b / 1e6,
+            "bwd_pct_hbm": 1.5 * nbytes / t_b / 1e6 / hbm * 100}
+
+
+def _shared(name, prefix, own, Hq, Hk, d, ps, iters, hbm):
+    """Next tokens of sequences whose first ``prefix`` rows are on the same pages, with
+    ``own`` rows each behind them; and the same without sharing the reads."""
+    B, lens = len(own), [prefix + n for n in own]
+    first, width = prefix // ps, max(-(-n // ps) for n in lens)
+    pages = first + B * (width - first)
+    kc, vc = (seeded_bf16((pages, Hk, ps, d), 71 + t, 1.0).to(DEV) for t in range(2))
+    order = torch.randperm(pages, generator=torch.Generator().manual_seed(5)).to(torch.int32)
+    table = torch.cat((order[:first].expand(B, first), order[first:].view(B, width - first)), 1).contiguous().to(DEV)
+    seq = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    groups = torch.tensor([0, B], dtype=torch.int32, device=DEV)
+    shared = torch.full((B,), prefix, dtype=torch.int32, device=DEV)
+    q = seeded_bf16((B, Hq, d), 73, 1.0).to(DEV)
+    o, lse = torch.empty_like(q), torch.empty((Hq, B), dtype=torch.float32, device=DEV)
+    ws = torch.empty(attn_fwd_paged_shared_workspace_size(B, 1, Hq, Hk, B, 1, max(lens), B, d), dtype=torch.uint8, device=DEV)
+    t = _time_graph_ms(lambda: attn_fwd_paged_shared(q, kc, vc, o, lse, table, seq, None, groups, shared, 1, max(lens), B, True,
+                                                     d ** -0.5, ws), iters)
+    plain = torch.empty(attn_fwd_paged_workspace_size(B, Hq, Hk, B, 1, max(lens), d), dtype=torch.uint8, device=DEV)
+    t_p = _time_graph_ms(lambda: attn_fwd_paged(q, kc, vc, o, lse, table, seq, None, 1, max(lens), True, d ** -0.5, plain), iters)
+    nbytes = 4.0 * (prefix + sum(own)) * Hk * d + 4.0 * B * Hq * d
+    return {"case": name, "B": B, "prefix": prefix, "keys": prefix + sum(own), "Hq": Hq, "Hk": Hk, "d": d, "page_size": ps, "ms": t,
+            "unshared_ms": t_p, "gbs": nbytes / t / 1e6, "pct_hbm": nbytes / t / 1e6 / hbm * 100}
+
+
 def _paged(name, lens, new, Hq, Hk, d, ps, iters, peak, hbm):
     """Append and attention of ``new`` tokens of sequences of the given lengths."""
     B, width = len(lens), max(-(-n // ps) for n in lens)
@@ -194,6 +236,8 @@ def main(argv=None):
         _decode("decode Nq=1, one head", 1, 1, 1, 131072, 128, a.iters, hbm),
         _decode("decode Nq=16", 8, 16, 16, 16384, 128, a.iters, hbm),
         _rotary("rotary", 1, 32768, 16, 16, 128, a.iters, hbm),
+        _norm_rotary("head norms with rotary", 1, 32768, 16, 16, 128, a.iters, hbm),
+        _shared("paged decode behind shared rows", 16384, [64 * (i + 1) for i in range(32)], 32, 8, 128, 16, a.iters, hbm),
         _paged("paged decode", [32768] * 4, 1, 32, 32, 128, 64, a.iters, peak, hbm),
         _paged("paged decode, shared key heads, mixed lengths", [512 * (i + 1) for i in range(32)], 1, 32, 4, 128, 16,
                a.iters, peak, hbm),

@@ -12,11 +12,23 @@
 // type.
 //
 // The lanes that hold a row's items (rotary.cuh: 2 V elements each) add its squares up
-// by exchanges; everything else stays in a thread.  The gradient's blocks run through
-// token groups, a thread summing h e of its places over the heads of Q in registers,
-// then of K, and at the end the block's threads in order; the blocks' sums go to the
-// workspace and a second kernel adds them up.  No atomics: results do not vary from
-// run to run.
+// by exchanges; everything else stays in a thread.  Items arrive by asynchronous copies
+// into shared memory (Feed), asked for before the block looks up its tokens and forms
+// their angles; 1 / s, the last thing to be known, is applied behind the turn.  The
+// gradient's blocks run through token groups, a thread summing h e of its places over the
+// heads of Q in registers, then of K, and at the end the block's threads in order; the
+// blocks' sums go to the workspace and a second kernel adds them up.  No atomics: results
+// do not vary from run to run.
+//
+// Bound by memory traffic and, nearly as much, by instructions (67 % of the issue slots
+// in the forward, 55 in the gradient): 8,192 tokens of 32 + 8 heads of 128, head-major, bf16,
+// 29.7 us (5.6 TB/s), the gradient 50.9 (4.9 TB/s); 16,380 tokens of 32 + 8 heads of 64,
+// token-major, f16, half turned in pairs, 30.5 and 50.2; 9,837 tokens of 32 + 4 + 4 heads of 64
+// into the cache 22.6 (4.5 TB/s).  A token of each of 64 sequences into the cache, a launch
+// and a chain of loads, 3.9.  With items in registers, one ahead, these were 34.7, 67.3,
+// 34.2, 67.3 and 27.7; three to five items on their way instead of two 30.2 to 33.5; four or
+// six blocks an SM instead of five 29.7 and 33.5; blocks that run through groups in the
+// forward too 38.5.
 #include "rotary.cuh"
 
 #include <limits.h>
@@ -303,7 +315,7 @@ __global__ void __launch_bounds__(kRotaryThreads, kNormGradBlocks) norm_rotary_g
   using C = NormCfg<D, V>;
   using VT = typename Vec<V>::type;
   constexpr int K = C::K, W = C::W, DEPTH = kNormGradDepth;
-  extern __shared__ uint8_t smem_raw[];
+  extern __shared__ __align__(16) uint8_t smem_raw[];
   NormGradShared<D, V>& sm = *reinterpret_cast<NormGradShared<D, V>*>(smem_raw);
   auto& feed = sm.feed;
   const RotaryArgs& a = na.r;

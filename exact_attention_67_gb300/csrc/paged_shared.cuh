@@ -15,6 +15,16 @@
 // (paged_fwd.cuh), smaller ones the decode kernel with 8, 16 or 32 columns; own rows the one
 // that their count of new tokens asks for.  What does not depend on the line is done
 // before the CTA knows it, beside the stream's last kernel: both lines' barriers, TMEM.
+//
+// 71 chats behind four prompts of up to 16,384 rows, 32 heads on 4 of 128, 87 us where
+// attn_fwd_paged takes 231 (429 MB of keys and values: 62.9 at the copy's rate): the own
+// rows' CTAs stream some 46 GB/s each, 192 KB in flight, whatever the others do, so the
+// SMs on the shared rows, bound by their products, are bandwidth lost.  16 samples behind
+// 8,192 rows, 32 heads on 8, 28 us (48): tables and place 2, the first tile 5, a CTA's six tiles
+// of 1.9 (a query tile alone is a chain of product, softmax, product), its end 2, stragglers
+// 3, the join and its launch 6.  Two behind 512 rows 12 us (9): not worth sharing.  Chunks of
+// prompts, bound by products either way, gain nothing: six of 264 tokens behind 16,384 rows 346 us
+// (350).
 #pragma once
 #include "paged_decode.cuh"
 #include "paged_fwd.cuh"

@@ -152,10 +152,13 @@ def _readable(g) -> bool:
 
 def _differentiated(*tensors) -> bool:
     """Whether automatic differentiation, in either mode, follows one of them."""
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
-        return True
-    # Outside a dual level, as nearly always, asking each tensor would take a microsecond.
-    return forward_ad._current_level >= 0 and any(t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors)
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                return True
+    if forward_ad._current_level < 0:  # no dual level, as nearly always: asking each tensor takes a microsecond
+        return False
+    return any(t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors)
 
 
 def _turn(q, k, positions, inv_freq, interleaved, inverse, factor, stream):

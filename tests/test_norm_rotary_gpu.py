@@ -349,3 +349,31 @@ def test_append_in_place_and_without_q():
     # The same numbers as the norm alone, at the positions of the step.
     pos = torch.tensor([*range(20), *range(3)], dtype=torch.int32, device=DEV)
     assert torch.equal(cache.k_cache(0)[p, :, :16].transpose(0, 1), ex.norm_rotary(k, None, g, None, pos, freq, eps=EPS)[:16])
+
+
+def test_refusals():
+    import exact_attention_67_gb300 as ex
+    from exact_attention_67_gb300 import ExattnError
+    x, g = rows(1, 8, 2, 64, torch.bfloat16, "bhnd", 1), gain_of(64, torch.float32, 1)
+    pos, freq = torch.arange(8, dtype=torch.int32, device=DEV), ex.rotary_frequencies(64)[0]
+    for bad in (g[:32], g.view(1, 64), g.repeat(2)[::2], g.cpu()):
+        with pytest.raises(ValueError):
+            ex.norm_rotary(x, None, bad, None, pos, freq)
+    with pytest.raises(TypeError):
+        ex.norm_rotary(x, None, g.double(), None, pos, freq)
+    with pytest.raises(ValueError, match="one type"):
+        ex.norm_rotary(x, x, g, g.half(), pos, freq)
+    with pytest.raises(ExattnError, match="VALUE"):
+        ex.norm_rotary(x, None, g, None, pos, freq, eps=-1.0)
+    with pytest.raises(ExattnError, match="ALIGN"):
+        ex.norm_rotary(torch.empty(1032, dtype=torch.bfloat16, device=DEV)[4:1028].view(1, 2, 8, 64), None, g, None, pos, freq)
+    with pytest.raises(ValueError):
+        ex.norm_rotary_backward(x, None, x, x, g, g, pos, freq)
+    with pytest.raises(ValueError):
+        ex.norm_rotary_backward(x[:, :1], None, x, None, g, None, pos, freq)
+    k = x[0].transpose(0, 1)
+    kc = torch.zeros(2, 2, 8, 64, dtype=torch.bfloat16, device=DEV)
+    tables = torch.zeros(1, 2, dtype=torch.int32, device=DEV), torch.full((1,), 8, dtype=torch.int32, device=DEV)
+    for how in (dict(q_gain=g), dict(k_gain=g, q_gain=g), dict(q=k, q_out=k, k_gain=g), dict(q=k, q_out=k, q_gain=g), dict(q=k, q_out=k)):
+        with pytest.raises(ValueError):
+            ex.attn_cache_append(k, k, kc, kc.clone(), *tables, **how)

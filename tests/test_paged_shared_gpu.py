@@ -105,6 +105,8 @@ CASES = {
     "not causal": ([(1024, [(4, 60), (2, 9)]), (256, [(1, 0), (1, 300)])], 8, 8, 128, 32, bf, False),
     "chunks, not causal": ([(512, [(90, 60), (70, 0)])], 12, 4, 64, 32, bf, False),
     "forty groups": ([(128 * (i % 4), [(1, 20 * i), (1, 7)]) for i in range(40)], 8, 1, 64, 64, hf, True),
+    "sixteen rows": ([(512, [(1, 40)] * 4), (1024, [(1, 3), (1, 200), (1, 77)]), (0, [(1, 9)])], 16, 4, 128, 16, bf, True),
+    "sixteen rows of drafts": ([(640, [(2, 40), (2, 0)]), (384, [(1, 300), (2, 1)])], 16, 4, 64, 32, hf, True),
     "odd heads": ([(768, [(1, 5), (1, 250), (3, 0)])], 21, 3, 128, 16, bf, True),
     "a hundred heads a key head": ([(256, [(1, 5), (2, 130)])], 100, 1, 64, 16, hf, True),
     "pages of 1024": ([(1024, [(1, 1100), (1, 3)])], 4, 2, 128, 1024, bf, True),
@@ -121,7 +123,7 @@ def test_shared_rows(name):
     assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
 
 
-@pytest.mark.parametrize("name", ["two answers", "drafts", "chunks"])
+@pytest.mark.parametrize("name", ["two answers", "drafts", "chunks", "sixteen rows of drafts"])
 def test_shared_rows_of_one_and_wide_scores(name):
     families, Hq, Hk, d, ps, dtype, causal = CASES[name]
     p = Family([(q, ms[:1]) for q, ms in families], Hq, Hk, d, ps, dtype, alone_shares=True, sigma=3.0)
@@ -140,7 +142,7 @@ def test_even_steps_without_offsets():
     assert torch.equal(o, with_cu[0]) and torch.equal(lse, with_cu[1])
 
 
-@pytest.mark.parametrize("name", ["two answers", "alone and together", "no new tokens", "chunks", "drafts"])
+@pytest.mark.parametrize("name", ["two answers", "alone and together", "no new tokens", "chunks", "drafts", "sixteen rows"])
 @pytest.mark.parametrize("fill", [0xFF, 0x7F, 0x00, 0x05])
 def test_whatever_the_workspace_holds(name, fill):
     families, Hq, Hk, d, ps, dtype, _ = CASES[name]
