@@ -182,19 +182,24 @@ __device__ __forceinline__ void read_frequencies(const RotaryArgs& a, int half, 
   }
 }
 
-// cos and sin of nt tokens' angles, by the whole block.
-template <int D, int V>
-__device__ __forceinline__ void form_angles(const RotaryArgs& a, int half, int nt, const Token* tk, AngleTable<D>& s) {
+// cos and sin of nt tokens' angles, by the whole block, value f of token t to place(t, f).
+template <int D, typename Place>
+__device__ __forceinline__ void form_angles(const RotaryArgs& a, int half, int nt, const Token* tk, AngleTable<D>& s,
+                                            const Place& place) {
   for (int i = threadIdx.x; i < nt * (D / 2); i += kRotaryThreads) {
-    const int tt = i / (D / 2), f = i % (D / 2);  // idle threads cost less than a division
+    const int t = i / (D / 2), f = i % (D / 2);  // idle threads cost less than a division
     if (f >= half) continue;
-    const unsigned long long angle = static_cast<unsigned long long>(static_cast<long long>(tk[tt].pos)) * s.turns[f];
+    const unsigned long long angle = static_cast<unsigned long long>(static_cast<long long>(tk[t].pos)) * s.turns[f];
     float sn, c;
     sincospif(static_cast<float>(static_cast<int>(angle >> 32)) * 4.656612873077393e-10f, &sn, &c);  // 2^-31: half turns
-    const int at = tt * (D / 2) + angle_at<D, V>(f);
+    const int at = place(t, f);
     s.cos[at] = c * s.factor[f];
     s.sin[at] = (a.inverse ? -sn : sn) * s.factor[f];
   }
+}
+template <int D, int V>
+__device__ __forceinline__ void form_angles(const RotaryArgs& a, int half, int nt, const Token* tk, AngleTable<D>& s) {
+  form_angles<D>(a, half, nt, tk, s, [](int t, int f) { return t * (D / 2) + angle_at<D, V>(f); });
 }
 
 }  // namespace exattn
