@@ -551,6 +551,37 @@ SharedPlan shared_plan(int B, int groups, int Hq, int Hkv, int total, int max_q,
   return p;
 }
 
+// Whether sharing can pay, were max_k rows shared: else the call runs as attn_fwd_paged,
+// which reads shared pages again mostly from L2.
+bool worth_sharing(int B, int groups, int Hq, int Hkv, int total, int max_q, int max_k, int d) {
+  const int G = Hq / Hkv;
+  const double tiles = max_k / 128;  // only whole tiles are shared
+  if (tiles < 1 || B <= groups) return false;
+  if (static_cast<long long>(std::min(max_q, total)) * G <= kPagedDecodeCols) {
+    // Saved reads, at some 15 TB/s, against the second line's units and the join.  Shared and
+    // not: one token of 2 sequences behind 512 rows, 8 key heads of 128, 11.6 and 9.3 us (2 MB),
+    // of 16 behind 2,048 21.5 and 19.6 (126 MB), behind 4,096 21.5 and 30.6; heads of 64, 63 MB
+    // 20.2 and 17.0, 126 MB 19.4 and 25.4.  Five tokens of 16 behind 4,096, heads of 64, 126 MB
+    // 38.2 and 34.9, 252 MB 53.5 and 57.5; of 32 in 4 groups behind 2,048, heads of 128, 235 MB 46.6
+    // and 46.7, 470 MB 62.8 and 78.9.
+    const double bytes = (B - static_cast<double>(groups)) * tiles * 128 * Hkv * d * 4;
+    return bytes >= (max_q == 1 ? 96e6 : 256e6);
+  }
+  // Chunks are bound by their products: units of 256 query rows (of up to 128 four fifths of the
+  // time) that fewer sequences fill better, 1.4 us a key tile and SM, against the join, 0.4 us
+  // for 1,000 rows and heads.  Ten tokens of 2 sequences behind 4,096 rows, 32 heads on 8 of 128, 17.3
+  // and 20.3 us, of 24 44.2 and 80.3; 30 of 8 behind 1,024 25.3 and 23.1, behind 16,384 73.3 and 98.7;
+  // 64 (256 rows each) of 24 behind 16,384 329.9 and 305.6; 150 of 8 behind 4,096 97.5 and 97.0,
+  // behind 16,384 266 and 300.
+  auto units = [](double rows) {
+    const double full = std::floor(rows / kPagedRows), rest = rows - full * kPagedRows;
+    return full + (rest <= 0 ? 0. : rest <= kPagedRows / 2 ? 0.8 : 1.);
+  };
+  const double rows = static_cast<double>(total) * G;
+  const double saved = (B * units(rows / B) - groups * units(rows / groups)) * tiles * Hkv;
+  return saved * 1.4 / kSMs >= 5 + 0.4e-3 * total * Hq;
+}
+
 int check_shared(int groups, int max_group_q) {
   return groups < 1 || groups >= (1 << 24) || max_group_q < 1 ? EXATTN_ERR_SHAPE : EXATTN_OK;
 }
@@ -562,6 +593,8 @@ extern "C" size_t attn_fwd_paged_shared_workspace_size(int B, int groups, int Hq
   if (check_paged(B, Hq, Hkv, total, max_seqlen_q, max_seqlen_k, d) != EXATTN_OK ||
       check_shared(groups, max_group_q) != EXATTN_OK)
     return 0;
+  if (!worth_sharing(B, groups, Hq, Hkv, total, max_seqlen_q, max_seqlen_k, d))
+    return attn_fwd_paged_workspace_size(B, Hq, Hkv, total, max_seqlen_q, max_seqlen_k, d);
   const SharedPlan p = shared_plan(B, groups, Hq, Hkv, total, max_seqlen_q, max_seqlen_k, max_group_q, d);
   return p.fits ? p.total_bytes : 0;
 }
@@ -579,6 +612,10 @@ extern "C" int attn_fwd_paged_shared(int dtype, const void* q, exattn_strides sq
                        max_pages, seqlens, cu_seqlens, B, Hq, Hkv, total, max_seqlen_q, max_seqlen_k, d, causal, 0, scale);
   if (rc != EXATTN_OK || (rc = check_shared(groups, max_group_q)) != EXATTN_OK) return rc;
   if (!aligned(cu_groups, 4) || !aligned(prefix_lens, 4)) return EXATTN_ERR_ALIGN;
+  if (!worth_sharing(B, groups, Hq, Hkv, total, max_seqlen_q, max_seqlen_k, d))
+    return attn_fwd_paged(dtype, q, sq, k_cache, skc, v_cache, svc, o, so, lse, num_pages, page_size, page_table, table_stride,
+                          max_pages, seqlens, cu_seqlens, B, Hq, Hkv, total, max_seqlen_q, max_seqlen_k, d, causal, 0, scale,
+                          workspace, workspace_bytes, stream);
   const SharedPlan plan = shared_plan(B, groups, Hq, Hkv, total, max_seqlen_q, max_seqlen_k, max_group_q, d);
   if (!plan.fits) return EXATTN_ERR_SHAPE;
   if (!workspace || workspace_bytes < plan.total_bytes) return EXATTN_ERR_WORKSPACE;

@@ -530,10 +530,12 @@ int attn_fwd_paged(int dtype, const void* q, exattn_strides q_strides, const voi
  *   max_group_q : the largest count of a group's new tokens; it chooses how the shared
  *     rows are streamed, a larger group is only slower.
  *   The group's first sequence names the shared pages.  Tables that break these rules
- *   give wrong results but no access out of bounds.  Arguments, layout, arithmetic and
- *   errors otherwise as attn_fwd_paged; workspace as there, of
- *   attn_fwd_paged_shared_workspace_size bytes (it holds fp32 results of every row
- *   twice, for the join).
+ *   give wrong results but no access out of bounds.  Where sharing cannot pay, were
+ *   max_seqlen_k rows shared (few sequences a group, few keys, chunks of many tokens), the
+ *   call runs as attn_fwd_paged: the sizes decide, so one of the same sizes always runs the
+ *   same way.  Arguments, layout, arithmetic and errors otherwise as attn_fwd_paged; workspace
+ *   as there, of attn_fwd_paged_shared_workspace_size bytes (it holds fp32 results of every
+ *   row twice, for the join).
  */
 size_t attn_fwd_paged_shared_workspace_size(int B, int groups, int Hq, int Hkv, int total, int max_seqlen_q,
                                             int max_seqlen_k, int max_group_q, int d);

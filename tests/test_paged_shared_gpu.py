@@ -1,6 +1,10 @@
 """Attention behind shared rows against the definition in 64 bits: the bounds, and the
 NaN in everything that no query may see, are those of test_paged_gpu.  (Joining pieces
-in fp32, by differences of references that are exact, adds less than 2^-20 of A.)"""
+in fp32, by differences of references that are exact, adds less than 2^-20 of A.)
+
+Calls whose sizes say that sharing cannot pay run as attn_fwd_paged.  The sizes here are
+small, so max_seqlen_k, a bound, is given as 2^20, which lets them share; that they do
+shows in their workspace."""
 import numpy as np
 import pytest
 import torch
@@ -58,7 +62,15 @@ class Family(Problem):
         self.seq = torch.tensor(self.lens, dtype=torch.int32, device=DEV)
 
     def sizes(self, **kw):
-        return {"max_seqlen_q": max(1, *self.new), "max_seqlen_k": max(1, *self.lens), "max_group_q": self.max_group} | kw
+        return {"max_seqlen_q": max(1, *self.new), "max_seqlen_k": 1 << 20, "max_group_q": self.max_group} | kw
+
+    def shares(self, **kw):
+        """Whether a call of these sizes streams shared rows once."""
+        import exact_attention_67_gb300 as ex
+        q, k, g = self.sizes(**kw).values()
+        B, total = len(self.new), self.q.shape[0]
+        return (ex.attn_fwd_paged_shared_workspace_size(B, self.groups.numel() - 1, self.Hq, self.Hk, total, q, k, g, self.d)
+                != ex.attn_fwd_paged_workspace_size(B, self.Hq, self.Hk, total, q, k, self.d))
 
     def run(self, causal=True, scale=None, cu=True, window=0, **kw):
         import exact_attention_67_gb300 as ex
@@ -101,9 +113,9 @@ CASES = {
     "drafts": ([(5000 // 32 * 32, [(5, 70), (5, 900)]), (640, [(3, 11), (5, 0), (1, 129)])], 24, 8, 64, 32, hf, True),
     "no new tokens": ([(256, [(0, 40), (1, 3), (0, 0)]), (128, [(0, 0), (0, 2)]), (384, [(2, 2), (1, 1)])], 8, 4, 64, 64, bf, True),
     "chunks": ([(2048, [(100, 0), (257, 5), (31, 700)])], 8, 2, 128, 64, bf, True),
-    "chunks, d 64": ([(640, [(300, 0), (17, 100)]), (256, [(130, 1), (200, 0)])], 6, 2, 64, 16, hf, True),
+    "chunks, d 64": ([(640, [(300, 0), (17, 100), (9, 3)]), (256, [(130, 1), (200, 0)])], 6, 2, 64, 16, hf, True),
     "not causal": ([(1024, [(4, 60), (2, 9)]), (256, [(1, 0), (1, 300)])], 8, 8, 128, 32, bf, False),
-    "chunks, not causal": ([(512, [(90, 60), (70, 0)])], 12, 4, 64, 32, bf, False),
+    "chunks, not causal": ([(512, [(90, 60), (70, 0), (14, 5)])], 12, 4, 64, 32, bf, False),
     "forty groups": ([(128 * (i % 4), [(1, 20 * i), (1, 7)]) for i in range(40)], 8, 1, 64, 64, hf, True),
     "sixteen rows": ([(512, [(1, 40)] * 4), (1024, [(1, 3), (1, 200), (1, 77)]), (0, [(1, 9)])], 16, 4, 128, 16, bf, True),
     "sixteen rows of drafts": ([(640, [(2, 40), (2, 0)]), (384, [(1, 300), (2, 1)])], 16, 4, 64, 32, hf, True),
@@ -116,17 +128,20 @@ CASES = {
 @pytest.mark.parametrize("name", CASES)
 def test_shared_rows(name):
     families, Hq, Hk, d, ps, dtype, causal = CASES[name]
-    p = Family(families, Hq, Hk, d, ps, dtype, seed=len(name))
+    p = Family(families, Hq, Hk, d, ps, dtype, seed=len(name), alone_shares=len(name) % 2 == 0)
+    assert p.shares()
     o, lse = p.run(causal)
     p.check(o, lse, causal)
+    # The same sizes as they are: some of these calls do not share.
+    p.check(*p.run(causal, max_seqlen_k=max(p.lens)), causal)
     again = p.run(causal)
     assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
 
 
 @pytest.mark.parametrize("name", ["two answers", "drafts", "chunks", "sixteen rows of drafts"])
-def test_shared_rows_of_one_and_wide_scores(name):
+def test_wide_scores_and_wrong_hints(name):
     families, Hq, Hk, d, ps, dtype, causal = CASES[name]
-    p = Family([(q, ms[:1]) for q, ms in families], Hq, Hk, d, ps, dtype, alone_shares=True, sigma=3.0)
+    p = Family(families, Hq, Hk, d, ps, dtype, sigma=3.0)
     p.check(*p.run(causal, scale=0.02), causal, scale=0.02)
     # The hint only chooses a kernel.
     p = Family(families, Hq, Hk, d, ps, dtype)
@@ -161,12 +176,6 @@ def test_cut_off_and_strided():
     full = p.run()
     # Both within 2^-8 |O| + (2^-10 + 2^-12) A of the same values, |O| and A below 6.
     assert (o[kept].double() - full[0][kept].double()).abs().max() <= 2.0 ** -4
-    # Keys past max_seqlen_k are not seen: like sequences that end there (not causal).
-    cut = p.run(causal=False, max_seqlen_k=600)
-    short = Family(families, 8, 2, 64, 32, bf)
-    short.lens = [min(m, 600) for m in p.lens]
-    short.k, short.v = [x[:600] for x in p.k], [x[:600] for x in p.v]
-    short.check(*cut, causal=False)
     # O and Q in a wider buffer.
     wide = torch.full((10, 8, 3, 64), 5.0, dtype=bf, device=DEV)
     q, out = wide[:, :, 0], wide[:, :, 2]
@@ -174,6 +183,30 @@ def test_cut_off_and_strided():
     p.q = q
     o, lse = p.into(0xFF, o=out)
     assert torch.equal(out, full[0]) and torch.equal(lse, full[1]) and (wide[:, :, 1] == 5.0).all()
+
+
+def test_keys_past_the_longest_are_not_seen():
+    """max_seqlen_k below the lengths, and below the shared rows of one group: like
+    sequences that end there (not causal)."""
+    families = [(512, [(1, 40 * i) for i in range(10)]), (768, [(1, 7), (1, 8), (1, 300), (1, 0)])]
+    p = Family(families, 32, 32, 128, 64, bf)
+    assert p.shares(max_seqlen_k=600)
+    cut = p.run(causal=False, max_seqlen_k=600)
+    p.lens = [min(m, 600) for m in p.lens]
+    p.k, p.v = [x[:600] for x in p.k], [x[:600] for x in p.v]
+    p.check(*cut, causal=False)
+
+
+def test_calls_that_cannot_pay_run_unshared():
+    import exact_attention_67_gb300 as ex
+    for name in ("two answers", "drafts", "chunks", "nothing shared"):
+        families, Hq, Hk, d, ps, dtype, causal = CASES[name]
+        p = Family(families, Hq, Hk, d, ps, dtype)
+        k = max(p.lens)
+        assert not p.shares(max_seqlen_k=k)
+        o, lse = p.run(causal, max_seqlen_k=k)
+        want = ex.forward_paged(p.q, p.kc, p.vc, p.table, p.seq, p.cu, max(p.new), k, causal=causal)
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
 
 
 def test_tables_that_break_the_rules_stay_in_bounds():
@@ -209,13 +242,13 @@ def test_captured_on_other_streams_and_replayed():
     import exact_attention_67_gb300 as ex
     a = Family([(512, [(1, 40), (1, 300)]), (256, [(1, 7), (1, 8)])], 8, 2, 64, 32, bf, seed=1)
     b = Family([(128, [(1, 500), (1, 20)]), (768, [(1, 1), (1, 200)])], 8, 2, 64, 32, bf, seed=2)
-    want = [p.run(cu=False, max_seqlen_k=2000, max_group_q=2) for p in (a, b)]
+    want = [p.run(cu=False, max_seqlen_k=1 << 20, max_group_q=2) for p in (a, b)]
     # Two streams at once, each with a workspace of its own.
     torch.cuda.synchronize()
     got = []
     for p in (a, b):
         side = torch.cuda.Stream()
-        got.append([ex.forward_paged_shared(p.q, p.kc, p.vc, p.table, p.seq, p.groups, p.prefix, None, 1, 2000, 2, stream=side)
+        got.append([ex.forward_paged_shared(p.q, p.kc, p.vc, p.table, p.seq, p.groups, p.prefix, None, 1, 1 << 20, 2, stream=side)
                     for _ in range(3)][-1])
     torch.cuda.synchronize()
     for g, w in zip(got, want):
@@ -229,7 +262,7 @@ def test_captured_on_other_streams_and_replayed():
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         out = ex.forward_paged_shared(hold["q"], hold["kc"], hold["vc"], hold["table"], hold["seq"], hold["groups"], hold["prefix"], None, 1,
-                                      2000, 2)
+                                      1 << 20, 2)
     for p, w in zip((a, b, a), (*want, want[0])):
         for n in ("q", "seq", "groups", "prefix"):
             hold[n].copy_(getattr(p, n))
@@ -270,11 +303,15 @@ def test_many_calls_in_a_row_and_among_others():
 
 # ---------------------------------------------------------------- together, as a server runs them
 @pytest.mark.parametrize("d,Hq,Hk,ps,dtype", [(128, 8, 2, 16, bf), (64, 6, 2, 32, hf)])
-def test_prompt_forks_and_next_tokens(d, Hq, Hk, ps, dtype):
+def test_prompt_forks_and_next_tokens(d, Hq, Hk, ps, dtype, monkeypatch):
     """A prompt, forks of it, next tokens with norms, rotation, the cache and attention
     behind the shared prompt, in two layers: against attention in 64 bits over what the
     cache holds."""
     import exact_attention_67_gb300 as ex
+    from exact_attention_67_gb300 import cache as cache_module
+    plain_call = cache_module.forward_paged_shared
+    monkeypatch.setattr(cache_module, "forward_paged_shared",
+                        lambda *a: plain_call(*a[:9], 1 << 20, *a[10:]))  # max_seqlen_k, so that these sizes share
     layers, prompt = 2, 300
     cache = ex.PagedCache(200, ps, layers, Hk, d, dtype=dtype, share_from=0)
     freq, factor = ex.rotary_frequencies(d)

@@ -131,14 +131,30 @@ def test_out_of_pages_leaves_the_cache(no_copies):
     assert c.free_pages == 1 and [c.length(s) for s in forks] == [300, 300]
 
 
-@pytest.mark.parametrize("new,times", [(1, 1), (5, 2)])
-def test_groups_where_enough_reads_are_saved(no_copies, new, times):
+@pytest.mark.parametrize("new", [1, 5])
+def test_groups_where_enough_reads_are_saved(no_copies, new):
     c = cache_of()
     a = c.add()
     c.extend([a], 300)
     forks = c.fork(a, 3)
-    saved = 2 * 256 * 64 * 4  # two of the three need not read 256 rows of K and V, one head of 64
-    c.share_from = saved // times
+    c.share_from = 2 * 256 * 64 * 4  # two of the three need not read 256 rows of K and V, one head of 64
     assert groups(c.extend(forks, new, shared=True)) == ([0, 3], [256] * 3, 3 * new)
-    c.share_from = saved // times + 1
+    c.share_from += 1
     assert groups(c.extend(forks, new, shared=True)) is None
+
+
+def test_sizes_that_cannot_pay_take_the_plain_workspace(lib):
+    def sizes(B=16, groups=1, Hq=32, Hk=8, total=16, mq=1, mk=8192, mg=16, d=128):
+        plain = lib.attn_fwd_paged_workspace_size(B, Hq, Hk, total, mq, mk, d)
+        return lib.attn_fwd_paged_shared_workspace_size(B, groups, Hq, Hk, total, mq, mk, mg, d), plain
+
+    shared, plain = sizes()
+    assert shared > plain
+    for how in (dict(mk=127), dict(groups=16), dict(mk=1024), dict(B=2, total=2), dict(Hk=1, mk=2048)):
+        shared, plain = sizes(**how)
+        assert shared == plain > 0
+    # Chunks: of few tokens, of as many as fill their tiles alone.
+    shared, plain = sizes(B=24, total=240, mq=10, mg=240, mk=4096)
+    assert shared > plain
+    shared, plain = sizes(B=24, total=24 * 64, mq=64, mg=24 * 64, mk=4096)
+    assert shared == plain
