@@ -9,6 +9,7 @@
 // kept from call to call.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
+#include <ATen/core/LegacyTypeDispatch.h>
 #include <ATen/ops/empty.h>
 #include <ATen/ops/empty_like.h>
 #include <ATen/ops/zeros.h>
@@ -347,9 +348,12 @@ template <TurnCall F>
 PyObject* turn_new(PyObject* const* p) {
   const at::Tensor& q = rotary_operand(p[0], "q", nullptr);
   const at::Tensor* k = p[1] == Py_None ? nullptr : &rotary_operand(p[1], "k", &q);
-  const at::Tensor qo = at::empty_like(q);
-  at::Tensor ko;
-  if (k) ko = at::empty_like(*k);
+  at::Tensor qo, ko;
+  {
+    const at::AutoDispatchBelowAutograd plain;  // new tensors: nothing for autograd to record
+    qo = at::empty_like(q);
+    if (k) ko = at::empty_like(*k);
+  }
   const int status = F(q, qo, k, k ? &ko : nullptr, p + 2);
   return answer(status, {qo, ko});
 }
@@ -433,6 +437,7 @@ PyObject* norm_grad_new(PyObject* const* p) {
   }
   const Turned t = turned(on, q, k, p[4], p[5]);
   const Gains g = gains(on, p[6], p[7], t.d);
+  const at::AutoDispatchBelowAutograd plain;  // new tensors: nothing for autograd to record
   const at::Tensor dqo = at::empty_like(q);
   at::Tensor dko, dqg, dkg;
   if (k) dko = at::empty_like(*k);

@@ -24,15 +24,15 @@
 //
 // Bound by memory traffic and, nearly as much, by instructions (67 % of the issue slots
 // in the forward, 55 in the gradient): 8,192 tokens of 32 + 8 heads of 128, head-major, bf16,
-// 29.7 us (5.6 TB/s), the gradient 50.8 (5.0 TB/s); interleaved, whatever part is turned, 35.7
-// and 55 (a lane's two vectors side by side); 20 or 6 of 128 elements turned as halves 42.0
-// and 40.0, 60.1 and 57.3.  16,380 tokens of 32 + 8 heads of 64, token-major, f16, half turned in
-// pairs, 32.4 and 50.9; 9,837 tokens of 32 + 4 + 4 heads of 64 into the cache 22.7 (4.5
+// 29.7 us (5.6 TB/s), the gradient 50.8 (5.0 TB/s); interleaved, whatever part is turned, 33.7
+// and 54 (a lane's two vectors side by side); 20 or 6 of 128 elements turned as halves 36.9
+// and 35.2, 60.0 and 57.4.  16,380 tokens of 32 + 8 heads of 64, token-major, f16, half turned in
+// pairs, 31.5 and 50.9; 9,837 tokens of 32 + 4 + 4 heads of 64 into the cache 22.7 (4.5
 // TB/s).  A token of each of 64 sequences into the cache, a launch and a chain of loads, 3.9.
 // With items in registers, one ahead, the first were 34.7 and 67.3; three to five items on
-// their way instead of two 30.2 to 33.5; four or six blocks an SM instead of five 29.7 and
-// 33.5; blocks that run through groups in the forward too 38.5; narrower vectors for other
-// turned parts (4 bytes for 20, 2 for 6) 45.4 and 69.3, their gradients 113.6 and 167.3.
+// their way instead of two 30.2 to 33.5; blocks that run through groups in the forward too
+// 38.5; narrower vectors for other turned parts (4 bytes for 20, 2 for 6) 45.4 and 69.3,
+// their gradients 113.6 and 167.3.
 #include "rotary.cuh"
 
 #include <limits.h>
@@ -43,8 +43,8 @@ namespace exattn {
 
 namespace {
 
-// Blocks an SM, and items of a thread on their way (Feed).
-constexpr int kNormBlocks = 5, kNormDepth = 2, kNormGradBlocks = kNormParts / 152, kNormGradDepth = 2;
+// Items of a thread on their way (Feed), and the gradient's blocks an SM.
+constexpr int kNormDepth = 2, kNormGradDepth = 2, kNormGradBlocks = kNormParts / 152;
 
 // Where a head's pairs are.
 enum Turn : int {
@@ -52,6 +52,11 @@ enum Turn : int {
   kPairs,     // (2 i, 2 i + 1)
   kAnywhere,  // (i, i + rot / 2): exchanged in shared memory
 };
+
+// The forward's blocks an SM: five where that spills next to nothing (four 30.8 us instead of
+// 29.7 for 8,192 tokens of 40 heads of 128), else four (five 35.6 and 42.0 instead of 33.7 and
+// 36.9, in pairs and with 20 elements turned).
+__host__ __device__ constexpr int norm_blocks(Turn m) { return m == kHalves ? 5 : 4; }
 
 constexpr int V = 8;  // elements a vector
 using Vector = typename Vec<V>::type;
@@ -269,8 +274,8 @@ struct NormGradShared {
 };
 
 template <typename T, int D, Turn M, bool APPEND>
-__global__ void __launch_bounds__(kRotaryThreads, kNormBlocks) norm_rotary_kernel(const __grid_constant__ NormArgs na,
-                                                                                 const __grid_constant__ Deal deal) {
+__global__ void __launch_bounds__(kRotaryThreads, norm_blocks(M))
+    norm_rotary_kernel(const __grid_constant__ NormArgs na, const __grid_constant__ Deal deal) {
   constexpr int DEPTH = kNormDepth;
   __shared__ AngleTable<D> angles;
   __shared__ GainTable<D> gains;
