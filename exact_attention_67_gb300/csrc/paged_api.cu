@@ -558,7 +558,7 @@ bool worth_sharing(int B, int groups, int Hq, int Hkv, int total, int max_q, int
   const double tiles = max_k / 128;  // only whole tiles are shared
   if (tiles < 1 || B <= groups) return false;
   if (static_cast<long long>(std::min(max_q, total)) * G <= kPagedDecodeCols) {
-    // Saved reads, at some 15 TB/s, against the second line's units and the join.  Shared and
+    // Saved reads, mostly of L2, against the second line's units and the join.  Shared and
     // not: one token of 2 sequences behind 512 rows, 8 key heads of 128, 11.6 and 9.3 us (2 MB),
     // of 16 behind 2,048 21.5 and 19.6 (126 MB), behind 4,096 21.5 and 30.6; heads of 64, 63 MB
     // 20.2 and 17.0, 126 MB 19.4 and 25.4.  Five tokens of 16 behind 4,096, heads of 64, 126 MB

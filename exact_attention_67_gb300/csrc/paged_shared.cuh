@@ -17,7 +17,7 @@
 // before the CTA knows it, beside the stream's last kernel: both lines' barriers, TMEM.
 //
 // 71 chats behind four prompts of up to 16,384 rows, 32 heads on 4 of 128, 87 us where
-// attn_fwd_paged takes 231 (429 MB of keys and values: 62.9 at the copy's rate): the own
+// attn_fwd_paged takes 231 (429 MB of keys and values: 62 at the copy's rate): the own
 // rows' CTAs stream some 46 GB/s each, 192 KB in flight, whatever the others do, so the
 // SMs on the shared rows, bound by their products, are bandwidth lost.  16 samples behind
 // 8,192 rows, 32 heads on 8, 28 us (48): tables and place 2, the first tile 5, a CTA's six tiles
