@@ -183,9 +183,10 @@ class PagedCache:
         """Room for ``new`` tokens (a number, or one a sequence) at the end of each
         sequence.  With ``shared`` neighbours in ``seqs`` that have their first pages in
         common (``fork``) are taken as groups, whose shared rows ``attend`` streams once,
-        where that pays (``share_from``): put such sequences side by side.  A last page that is shared and will be written to is copied
-        first, for all sequences and layers in one launch.  Raises OutOfPages,
-        changing nothing, if the pool is too small."""
+        where that pays (``share_from``): put such sequences side by side.  A last page
+        that is shared and will be written to is copied first, for all sequences and
+        layers in one launch.  Raises OutOfPages, changing nothing, if the pool is too
+        small."""
         seqs = list(seqs)
         new = [new] * len(seqs) if isinstance(new, int) else list(new)
         if not seqs or len(new) != len(seqs) or any(n < 0 for n in new):

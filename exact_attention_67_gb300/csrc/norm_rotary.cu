@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(kRotaryThreads, kNormGradBlocks) norm_rotary_g
                       : static_cast<T*>(a.k_out) + at(a.sko) + (h - hk) * a.sko.h;
       *reinterpret_cast<Vector*>(dst + e1) = x.p1.v;
       *reinterpret_cast<Vector*>(dst + e2) = x.p2.v;
-        ask(h + DEPTH * p.HL, s);
+      ask(h + DEPTH * p.HL, s);
       s = s + 1 == DEPTH ? 0 : s + 1;
     }
     flush();
