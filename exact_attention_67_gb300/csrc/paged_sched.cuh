@@ -285,6 +285,11 @@ struct PagedLine {
   }
 };
 
+// The host's limit on a line's weights, for offsets that ascend.  Others can name tokens more
+// than once: past the limit, where the sums below would wrap, such a line is taken as empty.
+// (The sum of the 32 lanes' 32nds, in 31 bits, is at most 32 below the lanes' sum by 32.)
+constexpr unsigned kMostWeights = 2000000000u;
+
 template <bool SH>
 __device__ __forceinline__ PagedLine<SH> paged_line(const PagedArgs& a, int UT, int lane) {
   using L = PagedLine<SH>;
@@ -292,23 +297,26 @@ __device__ __forceinline__ PagedLine<SH> paged_line(const PagedArgs& a, int UT, 
   int k0;
   const PagedSeq s0 = L::read(a, lane, &k0);
   const int w0 = L::weight(a, s0, UT, k0);
-  int sum = w0, most = w0, least = w0 > 0 ? w0 : INT_MAX, count = w0 > 0, longest = s0.n;
+  unsigned sum = w0;
+  int most = w0, least = w0 > 0 ? w0 : INT_MAX, count = w0 > 0, longest = s0.n;
   for (int b = 32 + lane; b < B; b += 32) {
     int kb;
     const PagedSeq s = L::read(a, b, &kb);
     const int w = L::weight(a, s, UT, kb);
-    sum += w;
+    sum = min(sum + w, kMostWeights);  // an item's weight alone is below it (host)
     longest = max(longest, s.n);
     most = max(most, w);
     least = min(least, w > 0 ? w : INT_MAX);
     count += w > 0;
   }
+  const bool broken = __reduce_add_sync(0xffffffffu, sum >> 5) > kMostWeights / 32 / static_cast<unsigned>(a.Hkv);
   sum = __reduce_add_sync(0xffffffffu, sum);
   most = __reduce_max_sync(0xffffffffu, most);
   least = __reduce_min_sync(0xffffffffu, least);
   const int units = __reduce_add_sync(0xffffffffu, count) * a.Hkv;
   const bool single = !SH || __reduce_max_sync(0xffffffffu, longest) <= UT;
-  return PagedLine<SH>{s0, k0, w0, sum * a.Hkv, units, most, least, single};
+  if (broken) return PagedLine<SH>{s0, k0, w0, 0, 0, 0, 0, false};
+  return PagedLine<SH>{s0, k0, w0, static_cast<int>(sum) * a.Hkv, units, most, least, single};
 }
 
 // Start of the chunk of CTA `cta` of `ctas`, found by the warp that has read the line; the

@@ -225,6 +225,33 @@ def test_tables_that_break_the_rules_stay_in_bounds():
     assert ex.device_error() == 0
 
 
+@pytest.mark.parametrize("shared", [True, False])
+def test_offsets_that_name_tokens_again_and_again(shared):
+    """Offsets that go back and forth: their units would weigh past 31 bits (3,000 groups,
+    every other one of 4,096 tokens, 514 a token; 2,048 times 16,384 tokens, 514 every
+    eight).  Such a line is empty, and the next call is right."""
+    import exact_attention_67_gb300 as ex
+    B, ps, k, d, Hq = 4096, 1024, 65536, 64, 32
+    total = B if shared else 16384
+    kc, vc = (torch.randn(64, 1, ps, d, device=DEV).to(bf) for _ in range(2))
+    q = torch.randn(total, Hq, d, device=DEV).to(bf)
+    table = torch.arange(64, dtype=torch.int32, device=DEV).repeat(B, 1)
+    seq = torch.full((B,), k, dtype=torch.int32, device=DEV)
+    back = torch.tensor([0, total], dtype=torch.int32, device=DEV).repeat(B)
+    if shared:
+        prefix = torch.full((B,), k - 128, dtype=torch.int32, device=DEV)
+        args = (q, kc, vc, table, seq, back[:3001].contiguous(), prefix, None, 1, k, 1)
+        assert ex.attn_fwd_paged_shared_workspace_size(B, 3000, Hq, 1, total, 1, k, 1, d) > ex.attn_fwd_paged_workspace_size(
+            B, Hq, 1, total, 1, k, d)
+        ex.forward_paged_shared(*args)
+    else:
+        ex.forward_paged(q, kc, vc, table, seq, back[:B + 1].contiguous(), total, k)
+    torch.cuda.synchronize()
+    assert ex.device_error() == 0
+    p = Family([(256, [(1, 40), (1, 300), (1, 3)])], 8, 2, 64, 32, bf)
+    p.check(*p.run())
+
+
 def test_nan_of_one_sequence_stays_there():
     p = Family([(256, [(1, 40), (1, 300), (1, 3)])], 8, 2, 64, 32, bf)
     want = p.run()
