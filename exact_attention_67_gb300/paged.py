@@ -268,7 +268,9 @@ def norm_rotary(q, k=None, q_gain=None, k_gain=None, positions=None, inv_freq=No
     ``gain * x / sqrt(mean(x ** 2) + eps)``, without a rounding between.  Gains:
     float32, bfloat16 or float16 tensors of one type, or None (all 1); the other
     arguments as ``rotary``.  Differentiable in q, k and the gains (once, in reverse
-    mode)."""
+    mode).  Before a backward pass is captured into a CUDA graph, drop eager graphs of the
+    same leaves (outputs or losses still held): a leaf's gradient is accumulated on the
+    stream of the graph that first named it, which is not the one being captured."""
     if stream is not None:
         if _differentiated(q, k, q_gain, k_gain):
             raise ValueError("norm_rotary under autograd runs on the current stream: use torch.cuda.stream(...)")
