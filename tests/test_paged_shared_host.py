@@ -158,3 +158,85 @@ def test_sizes_that_cannot_pay_take_the_plain_workspace(lib):
     assert shared > plain
     shared, plain = sizes(B=24, total=24 * 64, mq=64, mg=24 * 64, mk=4096)
     assert shared == plain
+
+
+# ---------------------------------------------------------------- which neighbours make a group
+def family(rows, count, base=(), first=0):
+    """Page lists of ``count`` sequences behind ``rows`` rows on common pages of 16, the first of them ``base``, and
+    one page of their own."""
+    common = list(base) + [first + i for i in range(rows // 16 - len(base))]
+    return [common + [first + 10 ** 6 + i] for i in range(count)]
+
+
+def saved_by(tables, before, ps=16):
+    from exact_attention_67_gb300.cache import _groups
+    offsets, shared = _groups(tables, before, ps)
+    assert offsets[0] == 0 and offsets[-1] == len(tables) and sorted(set(offsets)) == offsets
+    for i, j in zip(offsets, offsets[1:]):
+        rows = shared[i]
+        assert shared[i:j] == [rows] * (j - i) and rows % 128 == 0 and (j - i > 1 or rows == 0)
+        assert all(t[: rows // ps] == tables[i][: rows // ps] and rows <= n for t, n in zip(tables[i:j], before[i:j]))
+    return offsets, shared, sum(shared) - sum(shared[i] for i in offsets[:-1])
+
+
+def lengths(tables, ps=16):
+    return [len(t) * ps - 1 for t in tables]
+
+
+def test_a_shallow_sequence_does_not_pull_a_deep_group_down():
+    deep = family(16384, 31)
+    x = deep[0][:8] + [7 * 10 ** 6]  # 128 rows in common with them
+    for tables, at in (([x, *deep], [0, 1, 32]), ([*deep, x], [0, 31, 32]), ([*deep[:20], x, *deep[20:]], [0, 20, 21, 32])):
+        offsets, shared, saved = saved_by(tables, lengths(tables))
+        assert offsets == at and max(shared) == 16384
+        assert saved == sum(j - i - 1 for i, j in zip(at, at[1:])) * 16384
+    # Two deep groups behind one preamble, which the first sequence has alone.
+    other = family(16384, 31, base=deep[0][:8], first=10 ** 5)
+    tables = [x, *deep, *other]
+    assert saved_by(tables, lengths(tables)) == ([0, 1, 32, 63], [0] + [16384] * 62, 60 * 16384)
+
+
+def test_rows_under_a_truncation_end_the_group_there(no_copies):
+    """As test_rows_that_new_tokens_stand_on_are_not_shared: the split that saves most is the only one."""
+    c = cache_of()
+    a = c.add()
+    c.extend([a], 400)
+    f, g = c.fork(a, 2)
+    c.truncate(f, 200)
+    assert groups(c.extend([f, g, a], 1, shared=True)) == ([0, 1, 3], [0, 384, 384], 2)
+
+
+def test_groups_save_as_much_as_any_split():
+    """Against every split of neighbours, on random prompts that branch (pages as the path in a tree)."""
+    import random
+    rng = random.Random(5)
+    for _ in range(300):
+        n, path, tables = rng.randint(1, 9), [], []
+        for _ in range(n):
+            path = path[: rng.randint(0, len(path))]
+            path = path + [rng.randrange(10 ** 9) for _ in range(rng.choice((0, 1, 8, 16, 40)))]
+            tables.append(list(path))
+        before = [rng.randint(0, 16 * len(t)) if rng.random() < 0.3 else 16 * len(t) for t in tables]
+
+        def rows(i, j):
+            m = 0
+            while all(len(t) > m and t[m] == tables[i][m] for t in tables[i:j]):
+                m += 1
+            return min(16 * m, *before[i:j], 1 << 30) // 128 * 128
+
+        best = [0]
+        for j in range(1, n + 1):
+            best.append(max(best[i] + (j - i - 1) * rows(i, j) for i in range(j)))
+        assert saved_by(tables, before)[2] == best[n]
+
+
+def test_grouping_a_large_batch_is_quick():
+    """Its time is on the host at every step: forks of one prompt, and prompts that all branch at other rows."""
+    import time
+    forks = family(4096, 2048)
+    ladder = [list(range(8 * i)) + [10 ** 6 + i] for i in range(1, 300)]
+    tables = ladder + ladder[::-1]
+    for t in (forks, tables):
+        begin = time.perf_counter()
+        saved_by(t, lengths(t))
+        assert time.perf_counter() - begin < 2.0
