@@ -9,7 +9,9 @@
 //     dg = sum over rows of h e,      dx = (u - e mean(u e)) / s.
 // s is formed again from x, which the gradient reads anyway: nothing is kept between
 // the passes.  Sums, statistics and products are fp32, rounded once, to the output's
-// type.
+// type; a row whose squares would leave fp32's range is scaled by a power of two first
+// (scale_far: a branch that is not taken as a rule, gradient 52.3 -> 53.1 us, forward
+// 29.8 -> 30.0, into the cache 22.7 -> 22.4).
 //
 // A lane holds an item of a row, two vectors of 8 elements, whatever part of the head is
 // turned: its pairs' halves (`rot` a multiple of 16), or 16 consecutive elements, whose
@@ -24,10 +26,10 @@
 //
 // Bound by memory traffic and, nearly as much, by instructions (67 % of the issue slots
 // in the forward, 55 in the gradient): 8,192 tokens of 32 + 8 heads of 128, head-major, bf16,
-// 29.7 us (5.6 TB/s), the gradient 50.8 (5.0 TB/s); interleaved, whatever part is turned, 33.7
+// 30.0 us (5.6 TB/s), the gradient 53.1 (4.7 TB/s); interleaved, whatever part is turned, 33.7
 // and 54 (a lane's two vectors side by side); 20 or 6 of 128 elements turned as halves 36.9
 // and 35.2, 60.0 and 57.4.  16,380 tokens of 32 + 8 heads of 64, token-major, f16, half turned in
-// pairs, 31.5 and 50.9; 9,837 tokens of 32 + 4 + 4 heads of 64 into the cache 22.7 (4.5
+// pairs, 31.5 and 50.9; 9,837 tokens of 32 + 4 + 4 heads of 64 into the cache 22.4 (4.5
 // TB/s).  A token of each of 64 sequences into the cache, a launch and a chain of loads, 3.9.
 // With items in registers, one ahead, the first were 34.7 and 67.3; three to five items on
 // their way instead of two 30.2 to 33.5; blocks that run through groups in the forward too
@@ -214,6 +216,38 @@ __device__ __forceinline__ float head_sum(float x, unsigned mask) {
   return x;
 }
 
+// A row whose mean square (+ eps) t is outside this range is far: its squares may have left
+// fp32's, or its products with gains would.  (Of f16 rows only those of zeros could be.)
+template <typename T>
+__device__ __forceinline__ bool far_from_one(float t) {
+  return Elem<T>::kFmt != Elem<__half>::kFmt && !(t >= 0x1p-64f && t <= 0x1p64f);
+}
+
+// A far row by 2^k, exactly, so that the larger of its greatest element and sqrt(eps) is near 1:
+// g x / s stays what it is with eps by 2^2k, and 1 / s is 2^k times the scaled row's, which
+// together may be past fp32.  Gives the scaled mean square (+ eps).
+template <int D>
+__device__ __forceinline__ float scale_far(float2 (&x1)[W], float2 (&x2)[W], float eps, unsigned mask, float* scale) {
+  constexpr int S = NormCfg<D>::S;
+  float m = sqrtf(eps);
+#pragma unroll
+  for (int i = 0; i < W; ++i)
+    m = fmaxf(fmaxf(m, fmaxf(fabsf(x1[i].x), fabsf(x1[i].y))), fmaxf(fabsf(x2[i].x), fabsf(x2[i].y)));
+#pragma unroll
+  for (int o = S / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(mask, m, o));
+  const float k = __int_as_float(min(max(254 - (__float_as_int(m) >> 23), 1), 253) << 23);  // 2^-126 to 2^126
+  const float2 kk = make_float2(k, k);
+  float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    x1[i] = fmul2(x1[i], kk);
+    x2[i] = fmul2(x2[i], kk);
+    sum = ffma2(x1[i], x1[i], ffma2(x2[i], x2[i], sum));
+  }
+  *scale = k;
+  return fmaf(head_sum<S>(sum.x + sum.y, mask), 1.f / D, eps * k * k);
+}
+
 // This thread's part of a block: item `item` of the heads hl, hl + HL, ... of token t of
 // the group.  Of the tokens and heads of a block, neighbouring threads take those that lie
 // side by side.
@@ -331,7 +365,9 @@ __global__ void __launch_bounds__(kRotaryThreads, norm_blocks(M))
       unpack_item<T>(x, x1, x2);
 #pragma unroll
       for (int i = 0; i < W; ++i) sum = ffma2(x1[i], x1[i], ffma2(x2[i], x2[i], sum));
-      const float r = rsqrtf(fmaf(head_sum<NormCfg<D>::S>(sum.x + sum.y, p.mask), 1.f / D, na.eps));
+      float size = fmaf(head_sum<NormCfg<D>::S>(sum.x + sum.y, p.mask), 1.f / D, na.eps), scale;
+      if (far_from_one<T>(size)) size = scale_far<D>(x1, x2, na.eps, p.mask, &scale);
+      const float r = rsqrtf(size);
       const float(*g)[D / 2] = gains.g[h < hk ? 0 : 1];
       pairs_load<D>(g[0], p.item, w);
 #pragma unroll
@@ -460,24 +496,47 @@ __global__ void __launch_bounds__(kRotaryThreads, kNormGradBlocks) norm_rotary_g
         sq = ffma2(x2[i], x2[i], sq);
         dot = ffma2(fmul2(h2[i], w[i]), x2[i], dot);
       }
-      const float r = rsqrtf(fmaf(head_sum<C::S>(sq.x + sq.y, p.mask), 1.f / D, na.eps));
-      const float mean = head_sum<C::S>(dot.x + dot.y, p.mask) * r * (1.f / D);  // of g h e
+      float size = fmaf(head_sum<C::S>(sq.x + sq.y, p.mask), 1.f / D, na.eps);
+      float product = head_sum<C::S>(dot.x + dot.y, p.mask), scale;
+      const bool far = far_from_one<T>(size);
+      if (far) {
+        size = scale_far<D>(x1, x2, na.eps, p.mask, &scale);
+        dot = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < W; ++i) dot = ffma2(fmul2(h2[i], w[i]), x2[i], dot);
+        pairs_load<D>(gain[0], p.item, w);
+#pragma unroll
+        for (int i = 0; i < W; ++i) dot = ffma2(fmul2(h1[i], w[i]), x1[i], dot);
+        product = head_sum<C::S>(dot.x + dot.y, p.mask);
+      }
+      const float r = rsqrtf(size);
+      const float mean = product * r * (1.f / D);  // of g h e
       const float2 rr = make_float2(r, r), mm = make_float2(-mean, -mean);
       pairs_load<D>(gain[0], p.item, w);
 #pragma unroll
       for (int i = 0; i < W; ++i) {
         const float2 e = fmul2(x1[i], rr);
         s1[i] = ffma2(h1[i], e, s1[i]);
-        const float2 dx = fmul2(ffma2(e, mm, fmul2(h1[i], w[i])), rr);
-        x.p1.w[i] = Elem<T>::pack(dx.x, dx.y);
+        h1[i] = fmul2(ffma2(e, mm, fmul2(h1[i], w[i])), rr);  // dx from here on
       }
       pairs_load<D>(gain[1], p.item, w);
 #pragma unroll
       for (int i = 0; i < W; ++i) {
         const float2 e = fmul2(x2[i], rr);
         s2[i] = ffma2(h2[i], e, s2[i]);
-        const float2 dx = fmul2(ffma2(e, mm, fmul2(h2[i], w[i])), rr);
-        x.p2.w[i] = Elem<T>::pack(dx.x, dx.y);
+        h2[i] = fmul2(ffma2(e, mm, fmul2(h2[i], w[i])), rr);
+      }
+      if (far) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+          h1[i] = fmul2(h1[i], make_float2(scale, scale));
+          h2[i] = fmul2(h2[i], make_float2(scale, scale));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        x.p1.w[i] = Elem<T>::pack(h1[i].x, h1[i].y);
+        x.p2.w[i] = Elem<T>::pack(h2[i].x, h2[i].y);
       }
       T* dst = h < hk ? static_cast<T*>(a.q_out) + at(a.sqo) + h * a.sqo.h
                       : static_cast<T*>(a.k_out) + at(a.sko) + (h - hk) * a.sko.h;

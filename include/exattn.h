@@ -388,9 +388,10 @@ int attn_rotary(int dtype, const void* q, exattn_strides q_strides, void* q_out,
  *     all 1.
  *   eps : finite, at least 0 (else EXATTN_ERR_VALUE).  Rows of zeros give zeros with
  *     eps > 0 and NaN with eps = 0.
- * The squares are summed in fp32: rows whose mean square passes its range (elements
- * near 10^19 in bf16) give zeros.  Otherwise arguments, arithmetic and errors as
- * attn_rotary; an output may be its own input.
+ * The squares are summed in fp32; a row whose squares would leave its range (bf16
+ * elements near 10^19 or, with a small or no eps, near 10^-19) is scaled by a power of
+ * two first.  Otherwise arguments, arithmetic and errors as attn_rotary; an output may
+ * be its own input.
  *
  * attn_norm_rotary_backward -- its gradient.  From dq, dk, the gradients of its
  *   outputs, and its inputs q, k:

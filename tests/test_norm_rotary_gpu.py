@@ -377,3 +377,77 @@ def test_refusals():
     for how in (dict(q_gain=g), dict(k_gain=g, q_gain=g), dict(q=k, q_out=k, k_gain=g), dict(q=k, q_out=k, q_gain=g), dict(q=k, q_out=k)):
         with pytest.raises(ValueError):
             ex.attn_cache_append(k, k, kc, kc.clone(), *tables, **how)
+
+
+# ---------------------------------------------------------------- rows whose squares leave fp32
+def far_rows(H, N, d, exponents, dtype, seed):
+    """[1, H, N, d], row n of a size of 2^exponents[n % len]; the last row of every head has one large element."""
+    g = torch.Generator().manual_seed(seed)
+    at = torch.tensor([exponents[n % len(exponents)] for n in range(N)], dtype=torch.float64)
+    x = torch.randn(1, H, N, d, generator=g, dtype=torch.float64).clamp(-3.5, 3.5) * torch.exp2(at)[:, None]
+    x[:, :, -1, d // 3] = 2.0 ** max(exponents)
+    return x.to(dtype).to(DEV)
+
+
+def tight(got, want, size, dtype, unit):
+    """As check, down to half of the type's smallest step: scaling by powers of two is exact, so the bounds are the same."""
+    err, least = np.abs(f64(got) - want), 2.0 ** -134 if dtype == torch.bfloat16 else 2.0 ** -25
+    bound = HALF[dtype] * np.abs(want) + unit * size + least * (1 + 2.0 ** -10)
+    assert np.all(err <= bound), f"{np.argwhere(~(err <= bound))[:3]}: {f64(got)[~(err <= bound)][:3]} for {want[~(err <= bound)][:3]}"
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-30, EPS, 1e30])
+@pytest.mark.parametrize("d,rot,interleaved", [(128, 128, False), (64, 32, True), (64, 20, False), (128, 6, True)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_rows_whose_squares_leave_fp32(dtype, d, rot, interleaved, eps):
+    """The definition holds for every finite row of the type, with a small or no eps too."""
+    import exact_attention_67_gb300 as ex
+    exponents = [-131, -120, -70, -63, -31, 0, 31, 33, 62, 70, 126] if dtype == torch.bfloat16 else [-24, -14, 0, 12]
+    N, Hq, Hk = 3 * len(exponents) + 1, 3, 2
+    x = [far_rows(H, N, d, exponents, dtype, i) for i, H in enumerate((Hq, Hk))]
+    down = [-20 if e < -100 else -14 if dtype == torch.float16 else 0 for e in exponents]
+    dy = [far_rows(H, N, d, down, dtype, 7 + i) for i, H in enumerate((Hq, Hk))]
+    gain = [gain_of(d, torch.float32, 5 + i) for i in range(2)]
+    pos, (freq, factor) = torch.arange(N, dtype=torch.int32, device=DEV), ex.rotary_frequencies(rot, yarn=8.0)
+    args = (np.arange(N)[None, None], f64(freq), factor, interleaved, eps)
+    how = dict(positions=pos, inv_freq=freq, interleaved=interleaved, factor=factor, eps=eps)
+    for out, t, g in zip(ex.norm_rotary(*x, *gain, **how), x, gain):
+        tight(out, *normed(f64(t), f64(g), *args), dtype, 2.0 ** -18)
+    grads = ex.norm_rotary_backward(*dy, *x, *gain, **how)
+    for i in range(2):
+        dx, dx_size, dg, dg_size = normed_grad(f64(dy[i]), f64(x[i]), f64(gain[i]), *args)
+        if dtype == torch.bfloat16 or eps > 0:
+            tight(grads[i], dx, dx_size, dtype, 2.0 ** -16)
+        check(grads[2 + i], dg, dg_size, torch.float32, 2.0 ** -14 + 2.0 ** -18)
+
+
+def test_far_rows_into_the_cache():
+    import exact_attention_67_gb300 as ex
+    cache, exponents = ex.PagedCache(8, 16, 1, 2, 64), [-131, -70, 0, 70, 126]
+    seq = cache.add()
+    step = cache.extend([seq], 20)
+    q, k, v = (far_rows(H, 20, 64, exponents, torch.bfloat16, i)[0].transpose(0, 1).contiguous() for i, H in enumerate((4, 2, 2)))
+    g, freq = gain_of(64, torch.bfloat16, 1), ex.rotary_frequencies(64)[0]
+    cache.append(0, step, k, v, q, q_out := torch.empty_like(q), freq, q_gain=g, k_gain=g, eps=0.0)
+    args = (np.arange(20)[:, None], f64(freq), 1.0, False, 0.0)
+    tight(q_out, *normed(f64(q), f64(g), *args), torch.bfloat16, 2.0 ** -18)
+    stored = cache.k_cache(0)[list(cache.pages(seq))].transpose(1, 2).reshape(-1, 2, 64)[:20]
+    tight(stored, *normed(f64(k), f64(g), *args), torch.bfloat16, 2.0 ** -18)
+    assert torch.equal(cache.v_cache(0)[list(cache.pages(seq))].transpose(1, 2).reshape(-1, 2, 64)[:20], v)
+
+
+def test_far_rows_of_zeros_nan_and_infinities():
+    """Beside rows that need no scale: what is not finite stays in its row, and zeros are zeros with any eps above 0."""
+    import exact_attention_67_gb300 as ex
+    x = far_rows(1, 6, 128, [0], torch.bfloat16, 1)
+    x[0, 0, 0] = 0
+    x[0, 0, 1] *= 2.0 ** 70
+    x[0, 0, 1, 5] = float("nan")
+    x[0, 0, 2] *= 2.0 ** -70
+    x[0, 0, 2, 7] = float("inf")
+    for eps in (1e-40, 1e-30, 1e-6):
+        y = ex.norm_rotary(x, eps=eps)
+        assert not y[0, 0, 0].any() and y[0, 0, 1].isnan().all() and not y[0, 0, 3:].isnan().any()
+        assert y[0, 0, 2].isnan().sum() == 2  # the infinity's pair
+        dx = ex.norm_rotary_backward(x, None, x, None, None, None, eps=eps)[0]
+        assert not dx[0, 0, 0].any() and dx[0, 0, 1].isnan().all() and not dx[0, 0, 3:].isnan().any()
