@@ -114,14 +114,17 @@ class PagedCache:
     no sequence has written reach no output.
 
     ``share_from``: bytes of K and V of a layer whose repeated reads a step has to save
-    before ``extend(shared=True)`` makes it one of groups.  Reading shared pages again, mostly
-    from L2, costs less than a second line of units and a join: next tokens are even
-    at 60 to 130 MB (of 16 sequences behind 4,096 rows, 8 key heads of 64, 126 MB: 19.4 us
-    with groups, 25.4 without; behind 1,024, 31 MB, 17.9 and 12.6).  (``attn_fwd_paged_shared``
-    decides by its call's sizes once more, as if all of the longest sequence were shared.)"""
+    before ``extend(shared=True)`` makes it one of groups; None: 96 MiB where each sequence
+    takes one new token, 256 MB where some take more.  Reading shared pages again, mostly from
+    L2, costs less than a second line of units and a join: next tokens are even at 60 to 130 MB
+    (of 16 sequences behind 4,096 rows, 8 key heads of 64, 126 MB: 19.4 us with groups, 25.4
+    without; behind 1,024, 31 MB, 17.9 and 12.6), five at some 250 (126 MB 38.2 and 34.9, 252 MB
+    53.5 and 57.5).  (``attn_fwd_paged_shared`` decides by its call's sizes once more, as if all
+    of the longest sequence were shared.)  A call over groups has a workspace of 8 bytes an
+    element of O, for the join, beside what it has without."""
 
     def __init__(self, num_pages: int, page_size: int, layers: int, kv_heads: int, head_dim: int,
-                 dtype=torch.bfloat16, device="cuda", share_from: int = 96 << 20):
+                 dtype=torch.bfloat16, device="cuda", share_from: int | None = None):
         if num_pages < 1 or layers < 1 or kv_heads < 1:
             raise ValueError("num_pages, layers and kv_heads must be positive")
         if page_size < 8 or page_size > 1024 or page_size & (page_size - 1):
@@ -274,7 +277,8 @@ class PagedCache:
         groups, prefix = _groups(tables, [self._length[s] for s in seqs], self.page_size) if shared else ([], [])
         # What the first of a group reads, the others need not.
         saved = sum(prefix) - sum(prefix[i] for i in groups[:-1])
-        if saved * self.pool.shape[2] * self.pool.shape[4] * 4 < max(1, self.share_from):
+        least = self.share_from if self.share_from is not None else 96 << 20 if max(new) <= 1 else 256_000_000
+        if saved * self.pool.shape[2] * self.pool.shape[4] * 4 < max(1, least):
             groups, prefix = [], []
         host = torch.tensor(rows + lens + offsets + prefix + groups, dtype=torch.int32)
         if self.pool.is_cuda:

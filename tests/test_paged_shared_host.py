@@ -240,3 +240,21 @@ def test_grouping_a_large_batch_is_quick():
         begin = time.perf_counter()
         saved_by(t, lengths(t))
         assert time.perf_counter() - begin < 2.0
+
+
+def test_several_tokens_have_to_save_more(no_copies):
+    """What the reads saved have to make up for grows with the new tokens: at 126 MB one a sequence is even or gains
+    (heads of 128 21.5 and 19.6 us, of 64 19.4 and 25.4), five lose (31.0 and 26.3, 38.2 and 34.9)."""
+    from exact_attention_67_gb300 import PagedCache
+    c = PagedCache(400, 16, 1, 8, 128, device="cpu")
+    a = c.add()
+    c.extend([a], 2048)
+    forks = c.fork(a, 40)
+    some = forks[:16]  # fifteen of them need not read 2,048 rows of K and V of 8 heads of 128: 126 MB
+    assert groups(c.extend(some, 1, shared=True)) == ([0, 16], [2048] * 16, 16)
+    assert groups(c.extend(some, [1] * 15 + [2], shared=True)) is None
+    assert groups(c.extend(some, 5, shared=True)) is None
+    assert groups(c.extend(forks, 5, shared=True)) == ([0, 40], [2048] * 40, 200)  # 327 MB
+    assert groups(c.extend(some[:4], 1, shared=True)) is None
+    c.share_from = 1 << 20  # as given, whatever the count
+    assert groups(c.extend(some[:4], 5, shared=True)) == ([0, 4], [2048] * 4, 20)
