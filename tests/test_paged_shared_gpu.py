@@ -328,6 +328,51 @@ def test_many_calls_in_a_row_and_among_others():
         assert torch.equal(o, want[i % 6][0]) and torch.equal(lse, want[i % 6][1])
 
 
+def test_among_other_dependent_launches_on_one_workspace():
+    """Every kernel may be launched before the stream's last one has ended, and waits for it before it reads or
+    writes: this call's lines behind the join of the call before, on the same records and rows; attn_fwd_paged and the
+    norms' gradient on the same workspace; the norms into the cache whose rows are read next."""
+    import exact_attention_67_gb300 as ex
+    p = Family([(2048, [(1, 100 * i) for i in range(8)])], 32, 8, 128, 16, bf)
+    plain_sizes = (8, 32, 8, 8, 1, max(p.lens), 128)
+    n = max(ex.attn_fwd_paged_shared_workspace_size(8, 1, 32, 8, 8, *p.sizes().values(), 128),
+            ex.attn_fwd_paged_workspace_size(*plain_sizes), ex.attn_norm_rotary_backward_workspace_size(1, 8, 128))
+    ws = torch.full((n,), 0xFF, dtype=torch.uint8, device=DEV)
+    freq = ex.rotary_frequencies(128)[0]
+    pos = torch.tensor(p.lens, dtype=torch.int32, device=DEV) - 1
+    gain = 1 + 0.2 * randn(128, seed=1, dtype=torch.float32)
+    q, k, v = (torch.empty(8, H, 128, dtype=bf, device=DEV) for H in (32, 8, 8))
+
+    def step(seed):
+        q.copy_(randn(8, 32, 128, seed=seed, dtype=bf))
+        k.copy_(randn(8, 8, 128, seed=seed + 1, dtype=bf))
+        v.copy_(randn(8, 8, 128, seed=seed + 2, dtype=bf))
+        q_out, o, plain = (torch.empty_like(q) for _ in range(3))
+        lse, plain_lse = (torch.empty(32, 8, device=DEV) for _ in range(2))
+        dq, dg = torch.empty_like(q), torch.empty_like(gain)
+        ex.attn_cache_append(k, v, p.kc, p.vc, p.table, p.seq, None, q=q, q_out=q_out, inv_freq=freq, q_gain=gain, k_gain=gain)
+        for _ in range(2):
+            ex.attn_fwd_paged_shared(q_out, p.kc, p.vc, o, lse, p.table, p.seq, None, p.groups, p.prefix, *p.sizes().values(), True,
+                                     128 ** -0.5, ws)
+        ex.attn_norm_rotary_backward(o, q, dq, None, None, None, pos, freq, gain, None, dg, None, False, 1.0, 1e-6, ws)
+        ex.attn_fwd_paged(q_out, p.kc, p.vc, plain, plain_lse, p.table, p.seq, None, 1, max(p.lens), True, 128 ** -0.5, ws)
+        ex.attn_fwd_paged_shared(dq, p.kc, p.vc, q_out, lse, p.table, p.seq, None, p.groups, p.prefix, *p.sizes().values(), True,
+                                 128 ** -0.5, ws)
+        return q_out, o, lse, plain, plain_lse, dq, dg
+
+    want = []
+    for i in range(4):
+        want.append(step(10 * i))
+        torch.cuda.synchronize()
+    got = [step(10 * (i % 4)) for i in range(16)]
+    torch.cuda.synchronize()
+    assert ex.device_error() == 0
+    for i, outs in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(outs, want[i % 4]))
+    # Behind shared rows and not: within 2^-8 |O| + (2^-10 + 2^-12) A of the same values, |O| and A below 6.
+    assert all((w[1].double() - w[3].double()).abs().max() <= 2.0 ** -4 for w in want)
+
+
 # ---------------------------------------------------------------- together, as a server runs them
 @pytest.mark.parametrize("d,Hq,Hk,ps,dtype", [(128, 8, 2, 16, bf), (64, 6, 2, 32, hf)])
 def test_prompt_forks_and_next_tokens(d, Hq, Hk, ps, dtype, monkeypatch):
