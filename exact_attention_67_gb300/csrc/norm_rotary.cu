@@ -10,8 +10,7 @@
 // s is formed again from x, which the gradient reads anyway: nothing is kept between
 // the passes.  Sums, statistics and products are fp32, rounded once, to the output's
 // type; a row whose squares would leave fp32's range is scaled by a power of two first
-// (scale_far: a branch that is not taken as a rule, gradient 52.3 -> 53.1 us, forward
-// 29.8 -> 30.0, into the cache 22.7 -> 22.4).
+// (scale_far: a branch that is not taken as a rule).
 //
 // A lane holds an item of a row, two vectors of 8 elements, whatever part of the head is
 // turned: its pairs' halves (`rot` a multiple of 16), or 16 consecutive elements, whose
@@ -24,13 +23,16 @@
 // blocks' sums go to the workspace and a second kernel adds them up.  No atomics: results
 // do not vary from run to run.
 //
-// Bound by memory traffic and, nearly as much, by instructions (67 % of the issue slots
-// in the forward, 55 in the gradient): 8,192 tokens of 32 + 8 heads of 128, head-major, bf16,
-// 30.0 us (5.6 TB/s), the gradient 53.1 (4.7 TB/s); interleaved, whatever part is turned, 33.7
-// and 54 (a lane's two vectors side by side); 20 or 6 of 128 elements turned as halves 36.9
-// and 35.2, 60.0 and 57.4.  16,380 tokens of 32 + 8 heads of 64, token-major, f16, half turned in
-// pairs, 31.5 and 50.9; 9,837 tokens of 32 + 4 + 4 heads of 64 into the cache 22.4 (4.5
-// TB/s).  A token of each of 64 sequences into the cache, a launch and a chain of loads, 3.9.
+// Bound by memory traffic and, nearly as much, by instructions (71 % of the issue slots
+// in the forward, 56 in the gradient, whose blocks also take their token groups in rounds,
+// the last one filled in part, and let their items run out at each group's end): 8,192 tokens of 32 + 8 heads of 128, head-major, bf16,
+// 29.9 us (5.6 TB/s), the gradient 51.6 (4.9 TB/s); interleaved, whatever part is turned, 34.5
+// and 54.5 to 57 (a lane's two vectors side by side); 20 or 6 of 128 elements turned as halves
+// 37.9 and 36.0, 62.7 and 58.8.  16,380 tokens of 32 + 8 heads of 64, token-major, f16, half
+// turned in pairs, 31.3 and 50.9; 9,837 tokens of 32 + 4 + 4 heads of 64 into the cache 22.4 (4.5
+// TB/s; without a turn 21.6, the turn without the norms 21.4): 1,230 blocks on 760 places, whose
+// second round is thin.  A token of each of 64 sequences into the cache, a launch and a chain of
+// loads, 3.8.
 // With items in registers, one ahead, the first were 34.7 and 67.3; three to five items on
 // their way instead of two 30.2 to 33.5; blocks that run through groups in the forward too
 // 38.5; narrower vectors for other turned parts (4 bytes for 20, 2 for 6) 45.4 and 69.3,
@@ -226,6 +228,9 @@ __device__ __forceinline__ bool far_from_one(float t) {
 // A far row by 2^k, exactly, so that the larger of its greatest element and sqrt(eps) is near 1:
 // g x / s stays what it is with eps by 2^2k, and 1 / s is 2^k times the scaled row's, which
 // together may be past fp32.  Gives the scaled mean square (+ eps).
+// (Rows that are not far pay for the branch: the forward of 8,192 tokens of 40 heads of 128 0.1 us,
+// in pairs and by a row in shared memory 0.7 to 1.2, the gradient 0.7 to 2.5.  Forming y of a far
+// row once more behind the loop's own 36.9 instead of 30.7, in a function of its own 31.9.)
 template <int D>
 __device__ __forceinline__ float scale_far(float2 (&x1)[W], float2 (&x2)[W], float eps, unsigned mask, float* scale) {
   constexpr int S = NormCfg<D>::S;

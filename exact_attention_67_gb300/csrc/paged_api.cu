@@ -552,7 +552,12 @@ SharedPlan shared_plan(int B, int groups, int Hq, int Hkv, int total, int max_q,
 }
 
 // Whether sharing can pay, were max_k rows shared: else the call runs as attn_fwd_paged,
-// which reads shared pages again mostly from L2.
+// which reads shared pages again mostly from L2.  (The shared rows are known on the device only:
+// few of them before many of their own, or under a wide max_k, are shared at a loss.  Behind 512 rows
+// with 200 of their own, shared and not, five tokens of 4 groups of 32, 8 key heads of 128, 81.9 and
+// 63.7 us, one with 32 key heads 190.6 and 157.2; one of 4 groups of 8 with 2,000 of their own behind
+// 512 and 1,024 60.0 and 51.1, 63.7 and 54.9; one of 16 with one key head behind 16,384 22.7 and 20.0:
+// of 120 sizes the largest losses, and three more of 5 %.)
 bool worth_sharing(int B, int groups, int Hq, int Hkv, int total, int max_q, int max_k, int d) {
   const int G = Hq / Hkv;
   const double tiles = max_k / 128;  // only whole tiles are shared
@@ -570,7 +575,7 @@ bool worth_sharing(int B, int groups, int Hq, int Hkv, int total, int max_q, int
   // Chunks are bound by their products: units of 256 query rows (of up to 128 four fifths of the
   // time) that fewer sequences fill better, 1.4 us a key tile and SM, against the join, 0.4 us
   // for 1,000 rows and heads.  Ten tokens of 2 sequences behind 4,096 rows, 32 heads on 8 of 128, 17.3
-  // and 20.3 us, of 24 44.2 and 80.3; 30 of 8 behind 1,024 25.3 and 23.1, behind 16,384 73.3 and 98.7;
+  // and 20.3 us (too few units to count so: not shared), of 24 44.2 and 80.3; 30 of 8 behind 1,024 25.3 and 23.1, behind 16,384 73.3 and 98.7;
   // 64 (256 rows each) of 24 behind 16,384 329.9 and 305.6; 150 of 8 behind 4,096 97.5 and 97.0,
   // behind 16,384 266 and 300.
   auto units = [](double rows) {

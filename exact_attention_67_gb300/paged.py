@@ -380,8 +380,10 @@ def forward_paged_shared(q, k_cache, v_cache, page_table, seqlens, cu_groups, pr
     whose first prefix_lens[b] rows (int32 [B], the same within a group, all new tokens
     behind them; 0 for none) are on the same pages.  These are streamed once for the
     group's new tokens.  ``max_group_q``, the largest count of a group's new tokens,
-    defaults to total: give it where it is known.  The rest, and what is returned, as
-    ``forward_paged``.  Not differentiable."""
+    defaults to total: give it where it is known, and ``max_seqlen_k``, by which the call
+    decides whether sharing pays (by default it does, wherever the table is wide).  The
+    workspace, made for each call, holds 8 bytes an element of O.  The rest, and what is
+    returned, as ``forward_paged``.  Not differentiable."""
     if not q.is_cuda:
         raise ValueError("all device operands must be CUDA tensors")
     total, Hq, d = q.shape

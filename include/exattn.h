@@ -534,7 +534,8 @@ int attn_fwd_paged(int dtype, const void* q, exattn_strides q_strides, const voi
  *   give wrong results but no access out of bounds.  Where sharing cannot pay, were
  *   max_seqlen_k rows shared (few sequences a group, few keys, chunks of many tokens), the
  *   call runs as attn_fwd_paged: the sizes decide, so one of the same sizes always runs the
- *   same way.  Arguments, layout, arithmetic and errors otherwise as attn_fwd_paged; workspace
+ *   same way.  Few shared rows under a large max_seqlen_k may be shared at a loss (up to 30 %):
+ *   where the host knows that little is shared, call attn_fwd_paged.  Arguments, layout, arithmetic and errors otherwise as attn_fwd_paged; workspace
  *   as there, of attn_fwd_paged_shared_workspace_size bytes (it holds fp32 results of every
  *   row twice, for the join).
  */
